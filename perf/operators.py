@@ -452,7 +452,7 @@ def own_rope(s):
 def own_append(s):
     import online_softmax_05_gb300 as fa
     c = s["case"]
-    fa.kv4_append(s["pool"], s["k"], s["v"], s["block_table"], s["lengths"], s["cu_new"], max_new=c["new"],
+    fa.kv4_append(s["pool"], s["k"], s["v"], s["block_table"], s["lengths"], s["cu_new"],
                   rotary=s["table"])
     return list(fa.kv4_read(s["pool"], s["block_table"], s["lengths"], start=s["start"], count=c["new"]))
 
