@@ -63,7 +63,8 @@ typedef enum fa_status {
     FA_ERR_ARCH = -9,            /* current device is not compute capability 10.3 (sm_103a) */
     FA_ERR_SCRATCH = -10,        /* fa_bwd_noalloc: problem needs more than its fixed scratch buffer */
     FA_ERR_SEQLEN = -11,         /* recorded by a kernel: a cu_seqlens length is negative or above max_seqlen */
-    FA_ERR_DEBUG_CHECK = -12     /* debug library only: a kernel's run-time index failed its bounds check */
+    FA_ERR_DEBUG_CHECK = -12,    /* debug library only: a kernel's run-time index failed its bounds check */
+    FA_ERR_PAGE = -13            /* recorded by a kernel: a block table names no page of the pool where a token lies */
 } fa_status;
 
 /*
@@ -221,13 +222,166 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
 int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
               int B, int H, int Tq, int Tk, int D, float scale, void* stream);
 
+/*
+ * Rotary positions: turns pairs of channels of queries and keys by an angle
+ * that grows with the position, before attention or before a cache.
+ *   y1 = amplitude (x1 cos a - x2 sin a),  y2 = amplitude (x2 cos a + x1 sin a),
+ * a = position * f_i for pair i, x1 and x2 the channels i and i + rotary/2, or
+ * 2i and 2i + 1 when interleaved.  Channels from `rotary` on are copied.
+ * inverse = 1 turns back (-sin) and is the gradient of the map.
+ *   tensors      : n_tensors (1 or 2, e.g. queries and keys) (B, T, heads, D)
+ *                  tensors, each with its own heads and its strides in
+ *                  elements (channels are contiguous); in-place (out == in with
+ *                  the same strides) is allowed, any other overlap is not.
+ *                  Two in-place views of one buffer must not share elements.
+ *   positions  in: DEVICE int32 (or int64 if positions_64) [B][T] with batch
+ *                  stride positions_b (0: shared); NULL means 0 .. T-1.  May be
+ *                  negative.
+ *   freq       in: DEVICE uint64[rotary / 2], turns per position in units of
+ *                  2^-64 (so the angle is exact modulo a turn at any position)
+ *   rotary       : even, 2 .. D;  D: 2 .. FA_ROPE_MAX_D
+ *   dtype        : FA_BF16, FA_FP16 or FA_FP32, of every tensor; the rotation
+ *                  is computed in float32 and rounded once
+ * FA_ERR_UNSUPPORTED for rotary or dtype, FA_ERR_ARG for overlaps, negative
+ * strides or an output whose rows share elements.  No workspace.
+ */
+#define FA_BF16 0
+#define FA_FP16 1
+#define FA_FP32 2
+#define FA_ROPE_MAX_D 1024
+typedef struct fa_rope_tensor {
+    const void* in;
+    void* out;
+    long long heads;
+    long long in_b, in_t, in_h;    /* strides in elements */
+    long long out_b, out_t, out_h;
+} fa_rope_tensor;
+int fa_rope(const fa_rope_tensor* tensors, int n_tensors, const void* positions, int positions_64,
+            long long positions_b, const void* freq, int B, int T, int D, int rotary, int interleaved,
+            float amplitude, int inverse, int dtype, void* stream);
+
+/*
+ * Key/value cache held in 4 bits, in pages.  A group of `group` channels of a
+ * token and head is stored as m = min, s = bf16((max - min) / 15) (both bf16)
+ * and the codes round((x - m) / s), ties to even, 0..15; it stands for
+ * s * code + m.  s < 2^-100 is stored as 0.  A group that holds a NaN, or whose
+ * range is not finite in float32, reads back as NaN.
+ *   pool         : DEVICE bytes, num_pages * Hkv * page_size * (D + 8 D/group),
+ *                  16-byte aligned: (num_pages, Hkv, page_size / 16) blocks of
+ *                  16 tokens, each block key codes (16 rows of D/2 bytes), key
+ *                  scales (16 rows of D/group pairs s, m), value codes, value
+ *                  scales.  Key channel 32 g + 8 j + i is nibble i of the row's
+ *                  32-bit word j D/32 + g; value channel 32 g + 4 r + i is
+ *                  nibble i of its 16-bit half-word r D/32 + g.
+ *   block_table in: DEVICE int32[B][width]: slot t of sequence b lies in page
+ *                  block_table[b][t / page_size].  Entries behind the length
+ *                  are not read.
+ *   lengths    in: DEVICE int32[B], tokens held by each sequence (may be 0)
+ *   D: 64 or 128; group: 32 or 64; page_size: a multiple of 16;
+ *   B * Hkv <= 65535; width * page_size slots at most per sequence.
+ * A length the table cannot hold (or negative) is recorded as FA_ERR_SEQLEN and
+ * that sequence counts as empty; a table entry outside the pool, where a token
+ * lies, is recorded as FA_ERR_PAGE and those tokens are left out (read with
+ * fa_get_device_status; the outputs concerned are invalid).
+ */
+typedef struct fa_kv4_cache {
+    void* pool;
+    const int* block_table;
+    const int* lengths;
+    int B, Hkv, D, group, page_size, num_pages, width;
+} fa_kv4_cache;
+
+/*
+ * Writes new tokens to the cache: rotates the keys if `freq` is given, rounds
+ * them to bf16 as fa_rope does, quantises and stores.  cache->lengths counts
+ * the new tokens already: sequence b's n = cu_new[b+1] - cu_new[b] tokens go to
+ * slots lengths[b] - n .. lengths[b] - 1.
+ *   k, v       in: packed (total, Hkv, D) bf16 with strides k_t, k_h, v_t, v_h
+ *                  (elements, multiples of 8; bases 16-byte aligned)
+ *   cu_new     in: DEVICE int32[B + 1], non-decreasing; rows of k and v before
+ *                  cu_new[0] and from cu_new[B] on are not used (n may be 0)
+ *   positions  in: DEVICE int32 / int64 [total], NULL: the slot
+ *   freq, rotary, interleaved, amplitude: as in fa_rope; freq NULL: no rotation
+ *   weights   out: float32 [B][Hkv][slots] or NULL: 0 at the new slots
+ *   slot_positions out: int32 [B][Hkv][slots] or NULL: the new slots' positions
+ * A sequence without room for its tokens in the table (or in `slots`), or whose
+ * length is below n, is recorded as FA_ERR_SEQLEN; those tokens are not stored.
+ */
+int fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, long long k_t, long long k_h,
+                  long long v_t, long long v_h, const int* cu_new, int total, const void* positions,
+                  int positions_64, const void* freq, int rotary, int interleaved, float amplitude,
+                  float* weights, int* slot_positions, long long slots, void* stream);
+
+/*
+ * Reads `count` slots of every sequence back, from start[b] (NULL: 0) on.
+ *   k, v out: (B, Hkv, count, D) bf16, zeros for slots at or behind the length
+ * A negative start is recorded as FA_ERR_SEQLEN and reads zeros.
+ */
+int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k, void* v, void* stream);
+
+/*
+ * Decoding over the 4-bit cache, grouped heads (query head h reads key/value
+ * head h / (Hq / Hkv)), split over the tokens.
+ *   q       in: (B, Hq, Tq, D) bf16, 1 <= Tq <= 8, Hq / Hkv * Tq <= 1024
+ *   o      out: (B, Hq, Tq, D) bf16
+ *   lse    out: (B, Hq, Tq) float32, natural-log log-sum-exp of the scaled scores
+ *   causal    : 1 = the queries are the last Tq tokens of the sequence, query i
+ *               sees the slots below length - (Tq - 1 - i); 0 = all of them.
+ *               A row that sees nothing gives o = 0 and lse = -infinity.
+ *   weights in: float32 [B][Hkv][slots] or NULL (zeros); weights_out the same
+ *               or NULL: weights_out = weights + each slot's attention weight,
+ *               summed over the Hq / Hkv * Tq query rows that read the head.
+ *               Slots at and behind the length are not written.  weights_out
+ *               may be weights (added to in place).
+ *   workspace : fa_kv4_decode_workspace(B, Hq, Hkv, Tq, D, width * page_size,
+ *               weights_out != NULL) bytes, 16-byte aligned, used until the call's work
+ *               on `stream` is done; or NULL: taken with cudaMallocAsync.
+ *               FA_ERR_SCRATCH if workspace_bytes is too small.
+ * A non-finite query row gives NaN in its o and lse.
+ */
+long long fa_kv4_decode_workspace(int B, int Hq, int Hkv, int Tq, int D, int slots, int weights);
+int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse, int Hq, int Tq, float scale,
+                  int causal, const float* weights, float* weights_out, long long slots, void* workspace,
+                  long long workspace_bytes, void* stream);
+
+/*
+ * Evicts down to `budget` tokens per sequence, for each key/value head by
+ * itself.  Kept are the `recent` newest tokens (positions above the newest
+ * minus recent) and the ones with the largest weights, ties to the lowest slot;
+ * a NaN weight counts as the least.  A sequence of at most `budget` tokens
+ * stays as it is.  Kept tokens below the new length stay in their slots; those
+ * behind it move, in order, to the slots that fall free, so only what has to
+ * move is moved (attention does not depend on the order of the slots).
+ *   weights, slot_positions in: [B][Hkv][slots] float32 / int32
+ *   weights_out, positions_out out: the same after the eviction, 0 / -1 behind
+ *                  the new length; buffers of their own
+ *   lengths_out out: int32[B], min(length, budget)
+ *   source     out: int32 [B][Hkv][budget]: the slot each kept token came from,
+ *                  -1 behind the new length
+ *   recent       : 0 .. budget (FA_ERR_ARG)
+ *   workspace    : fa_kv4_evict_workspace(B, Hkv, budget) bytes, or NULL
+ * cache->lengths is not changed: use lengths_out from then on.
+ */
+long long fa_kv4_evict_workspace(int B, int Hkv, int budget);
+int fa_kv4_evict(const fa_kv4_cache* cache, const float* weights, const int* slot_positions, long long slots,
+                 int budget, int recent, float* weights_out, int* positions_out, int* lengths_out, int* source,
+                 void* workspace, long long workspace_bytes, void* stream);
+
+/*
+ * Host-only query (no GPU needed): the byte offset in the pool of the block
+ * that holds `slot` of sequence b, head h, as the kernels look it up in a block
+ * table, here a HOST int32[>= b + 1][width]; FA_ERR_PAGE where they refuse it.
+ */
+long long fa_kv4_block_offset(const int* block_table, int width, int Hkv, int D, int group, int page_size,
+                              int num_pages, int b, int h, int slot);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* fa_strerror(int status);
 
 /*
  * Synchronises `stream`, returns the device status word recorded by the
  * library's kernels on the current device since the last call (FA_OK,
- * FA_ERR_DEVICE_TIMEOUT or FA_ERR_SEQLEN), and clears it.  Returns FA_ERR_CUDA if the
+ * FA_ERR_DEVICE_TIMEOUT, FA_ERR_SEQLEN or FA_ERR_PAGE), and clears it.  Returns FA_ERR_CUDA if the
  * synchronisation itself fails.
  */
 int fa_get_device_status(void* stream);

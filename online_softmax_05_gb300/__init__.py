@@ -14,7 +14,8 @@ import threading
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_varlen", "attention_forward_varlen", "fa_bwd_varlen", "attention_backward_varlen", "fa_decode", "attention_decode", "fa_bwd_noalloc", "fa_strerror", "fa_get_device_status", "fa_version",
            "attention_forward", "attention_backward", "FAError", "library_path", "load_library",
-           "FlashAttention", "flash_attention"]
+           "FlashAttention", "flash_attention", "rope", "rotary_frequencies", "rotary_amplitude", "kv4_pool", "kv4_append",
+           "kv4_read", "attention_decode_kv4", "kv4_evict"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -25,7 +26,7 @@ FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", -1: "FA_ERR_NULL", -2: "FA_ERR_SHAPE", -3: "FA_ERR_UNSUPPORTED", -4: "FA_ERR_ALIGN",
                 -5: "FA_ERR_CUDA", -6: "FA_ERR_NOMEM", -7: "FA_ERR_DEVICE_TIMEOUT", -8: "FA_ERR_ARG",
                 -9: "FA_ERR_ARCH", -10: "FA_ERR_SCRATCH", -11: "FA_ERR_SEQLEN",
-                -12: "FA_ERR_DEBUG_CHECK"}
+                -12: "FA_ERR_DEBUG_CHECK", -13: "FA_ERR_PAGE"}
 
 
 class FAError(RuntimeError):
@@ -41,6 +42,8 @@ def library_path() -> str:
 def load_library():
     """Load libfa.so (built in-tree by ``online_softmax_05_gb300.build``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -88,6 +91,23 @@ def load_library():
         lib.fa_set_deterministic.restype = i
         lib.fa_set_timing_events.argtypes = [vp, vp, vp, vp, vp]
         lib.fa_set_timing_events.restype = i
+        ll, blob = ctypes.c_longlong, ctypes.c_char_p  # blob: a packed C struct
+        lib.fa_rope.argtypes = [blob, i, vp, i, ll, vp, i, i, i, i, i, f, i, i, vp]
+        lib.fa_rope.restype = i
+        lib.fa_kv4_append.argtypes = [blob, vp, vp, ll, ll, ll, ll, vp, i, vp, i, vp, i, i, f, vp, vp, ll, vp]
+        lib.fa_kv4_append.restype = i
+        lib.fa_kv4_read.argtypes = [blob, vp, i, vp, vp, vp]
+        lib.fa_kv4_read.restype = i
+        lib.fa_kv4_decode_workspace.argtypes = [i] * 7
+        lib.fa_kv4_decode_workspace.restype = ll
+        lib.fa_kv4_decode.argtypes = [blob, vp, vp, vp, i, i, f, i, vp, vp, ll, vp, ll, vp]
+        lib.fa_kv4_decode.restype = i
+        lib.fa_kv4_block_offset.argtypes = [ctypes.POINTER(i)] + [i] * 9
+        lib.fa_kv4_block_offset.restype = ll
+        lib.fa_kv4_evict_workspace.argtypes = [i, i, i]
+        lib.fa_kv4_evict_workspace.restype = ll
+        lib.fa_kv4_evict.argtypes = [blob, vp, vp, ll, i, i, vp, vp, vp, vp, vp, ll, vp]
+        lib.fa_kv4_evict.restype = i
         _lib = lib
         return lib
 
@@ -107,6 +127,30 @@ def _stream(s) -> int | None:
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _raw_stream(device: int) -> int:
+    """The current stream of a device, as the C ABI takes it."""
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch_on(tensor, stream, fn, *args):
+    """fn(*args) with the tensor's device and the given stream (default: the device's
+    current one) current, so that what fn allocates belongs to the stream that uses it."""
+    import torch
+    if not tensor.is_cuda:
+        raise ValueError("CUDA tensors are required; there is no CPU fallback")
+    dev = tensor.get_device()
+    if stream is None and dev == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        if stream is None:
+            return fn(*args)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        with torch.cuda.stream(stream):
+            return fn(*args)
 
 
 def fa_fwd(q, k, v, o, lse, B: int, H: int, T: int, D: int, scale: float, causal: int, stream=None) -> int:
@@ -345,6 +389,20 @@ def __getattr__(name):
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
-def flash_attention(q, k, v, causal: bool = False, scale: float | None = None):
-    """O = softmax(q k^T * scale) v, differentiable (see FlashAttention)."""
+def flash_attention(q, k, v, causal: bool = False, scale: float | None = None, rotary=None, positions=None,
+                    interleaved: bool = False, amplitude: float = 1.0):
+    """O = softmax(q k^T * scale) v, differentiable (see FlashAttention).
+
+    With ``rotary`` (a table from rotary_frequencies) q and k are rotated first,
+    at ``positions`` (see rope); the gradients go through the rotation."""
+    if rotary is not None:
+        if q.dim() == 3:
+            q, k = rope(q.unsqueeze(1), k.unsqueeze(1), rotary, positions, interleaved, amplitude)
+            q, k = q.squeeze(1), k.squeeze(1)
+        else:
+            q, k = rope(q, k, rotary, positions, interleaved, amplitude)
     return __getattr__("FlashAttention").apply(q, k, v, causal, scale)
+
+
+from .rotary import rope, rotary_amplitude, rotary_frequencies  # noqa: E402
+from .kv4 import attention_decode_kv4, kv4_append, kv4_evict, kv4_pool, kv4_read  # noqa: E402

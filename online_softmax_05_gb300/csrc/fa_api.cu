@@ -12,6 +12,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_kv4.cuh"
 #include "fa_sched.h"
 
 namespace {
@@ -88,10 +89,11 @@ const char* fa_strerror(int status) {
         case FA_ERR_CUDA: return "a CUDA runtime or driver call failed";
         case FA_ERR_NOMEM: return "stream-ordered workspace allocation failed";
         case FA_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out (pipeline stall); outputs are invalid";
-        case FA_ERR_ARG: return "causal must be 0 or 1, scale finite, and outputs must not overlap other buffers";
+        case FA_ERR_ARG: return "causal must be 0 or 1, scale finite, and outputs must not overlap other buffers (or another argument is out of its range)";
         case FA_ERR_ARCH: return "the current device is not compute capability 10.3 (sm_103a)";
         case FA_ERR_SEQLEN: return "a cu_seqlens length is negative or above max_seqlen (recorded by the kernel)";
         case FA_ERR_SCRATCH: return "fa_bwd_noalloc: the problem needs more than the fixed 64 MiB scratch buffer";
+        case FA_ERR_PAGE: return "a block table names no page of the pool where a token lies (recorded by the kernel)";
         case FA_ERR_DEBUG_CHECK: return "debug library: a kernel's run-time index failed its bounds check (access skipped)";
         default: return "unknown fa_status";
     }
@@ -286,8 +288,294 @@ int fa_get_device_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
     int a = fa::fwd_take_status();
     int b = fa::bwd_take_status();
-    if (a == -5 || b == -5) return FA_ERR_CUDA;
-    return a != 0 ? a : b;
+    int c = fa::kv4_cache_take_status();
+    int d = fa::kv4_decode_take_status();
+    if (a == -5 || b == -5 || c == -5 || d == -5) return FA_ERR_CUDA;
+    return a != 0 ? a : b != 0 ? b : c != 0 ? c : d;
+}
+
+int fa_rope(const fa_rope_tensor* tensors, int n_tensors, const void* positions, int positions_64, long long positions_b,
+            const void* freq, int B, int T, int D, int rotary, int interleaved, float amplitude, int inverse, int dtype,
+            void* stream) {
+    if (!tensors || !freq) return FA_ERR_NULL;
+    if (n_tensors < 1 || n_tensors > 2) return FA_ERR_ARG;
+    if (B < 1 || T < 1 || D < 2 || D > FA_ROPE_MAX_D) return FA_ERR_SHAPE;
+    if (static_cast<long long>(B) * T > INT_MAX) return FA_ERR_SHAPE;
+    if (rotary < 2 || rotary > D || rotary % 2 != 0) return FA_ERR_UNSUPPORTED;
+    if (dtype < FA_BF16 || dtype > FA_FP32) return FA_ERR_UNSUPPORTED;
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1) ||
+        (positions_64 != 0 && positions_64 != 1) || !std::isfinite(amplitude))
+        return FA_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(freq) & 7u) ||
+        (reinterpret_cast<uintptr_t>(positions) & (positions_64 ? 7u : 3u)))
+        return FA_ERR_ALIGN;
+    const int size = dtype == FA_FP32 ? 4 : 2;
+    Range in[2], out[2];
+    bool in_place[2];
+    fa::RopeTensor x[2];
+    for (int i = 0; i < n_tensors; ++i) {
+        const fa_rope_tensor& t = tensors[i];
+        if (!t.in || !t.out) return FA_ERR_NULL;
+        if (t.heads < 1 || t.heads > (1 << 20)) return FA_ERR_SHAPE;
+        if ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & (size - 1)) return FA_ERR_ALIGN;
+        if (t.in_b < 0 || t.in_t < 0 || t.in_h < 0 || t.out_b < 0 || t.out_t < 0 || t.out_h < 0) return FA_ERR_ARG;
+        // an output element is written once: no two rows of it may share one
+        if ((B > 1 && t.out_b < D) || (T > 1 && t.out_t < D) || (t.heads > 1 && t.out_h < D)) return FA_ERR_ARG;
+        in[i] = range_of(t.in, ((B - 1) * static_cast<size_t>(t.in_b) + (T - 1) * static_cast<size_t>(t.in_t) +
+                                (t.heads - 1) * static_cast<size_t>(t.in_h) + D) * size);
+        out[i] = range_of(t.out, ((B - 1) * static_cast<size_t>(t.out_b) + (T - 1) * static_cast<size_t>(t.out_t) +
+                                  (t.heads - 1) * static_cast<size_t>(t.out_h) + D) * size);
+        in_place[i] = t.in == t.out && t.in_b == t.out_b && t.in_t == t.out_t && t.in_h == t.out_h;
+        if (!in_place[i] && overlap(in[i], out[i])) return FA_ERR_ARG;
+        x[i] = {t.in, t.out, t.heads, t.in_b, t.in_t, t.in_h, t.out_b, t.out_t, t.out_h};
+    }
+    if (n_tensors == 2) {
+        // two views of one projection interleave, which only rotating both in place keeps apart
+        const bool views = in_place[0] && in_place[1] && tensors[0].in != tensors[1].in;
+        if (!views && (overlap(out[0], out[1]) || overlap(out[0], in[1]) || overlap(out[1], in[0]))) return FA_ERR_ARG;
+    }
+    int dev = 0, sms = 0;
+    const int rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return fa::launch_rope(x, n_tensors, positions, positions_64, positions_b, freq, B, T, D, rotary, interleaved,
+                           amplitude, inverse, dtype, static_cast<cudaStream_t>(stream), sms);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_kv4(const fa_kv4_cache* c) {
+    if (!c) return FA_ERR_NULL;
+    if (!c->pool || !c->block_table || !c->lengths) return FA_ERR_NULL;
+    if (c->B < 1 || c->Hkv < 1 || c->num_pages < 1 || c->width < 1 || c->page_size < 16) return FA_ERR_SHAPE;
+    if (static_cast<long long>(c->B) * c->Hkv > 65535) return FA_ERR_SHAPE;
+    if (static_cast<long long>(c->width) * c->page_size > INT_MAX - 65536) return FA_ERR_SHAPE;
+    if (static_cast<long long>(c->B) * c->width > INT_MAX) return FA_ERR_SHAPE;
+    if (c->D != 64 && c->D != 128) return FA_ERR_UNSUPPORTED;
+    if ((c->group != 32 && c->group != 64) || c->page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(c->pool) || (reinterpret_cast<uintptr_t>(c->block_table) & 3u) ||
+        (reinterpret_cast<uintptr_t>(c->lengths) & 3u))
+        return FA_ERR_ALIGN;
+    return FA_OK;
+}
+fa::Kv4Shape kv4_shape(const fa_kv4_cache* c) {
+    return {c->B, c->Hkv, c->D, c->group, c->page_size, c->num_pages, c->width};
+}
+Range kv4_pool_range(const fa_kv4_cache* c) {
+    return range_of(c->pool, static_cast<size_t>(c->num_pages) * c->Hkv * c->page_size * (c->D + 8 * c->D / c->group));
+}
+// Ranges of what a call only reads besides its own inputs.
+Range kv4_table_range(const fa_kv4_cache* c) {
+    return range_of(c->block_table, static_cast<size_t>(c->B) * c->width * 4);
+}
+Range kv4_lengths_range(const fa_kv4_cache* c) { return range_of(c->lengths, static_cast<size_t>(c->B) * 4); }
+bool overlaps_any(Range a, const Range* r, int n) {
+    for (int i = 0; i < n; ++i)
+        if (overlap(a, r[i])) return true;
+    return false;
+}
+
+// The caller's workspace, or one taken stream-ordered for the call.
+struct Workspace {
+    void* ptr = nullptr;
+    bool mine = false;
+    cudaStream_t stream;
+    int take(void* given, size_t given_bytes, size_t need, cudaStream_t st) {
+        stream = st;
+        if (given != nullptr) {
+            if (given_bytes < need) return FA_ERR_SCRATCH;
+            if (!aligned16(given)) return FA_ERR_ALIGN;
+            ptr = given;
+            return FA_OK;
+        }
+        if (cudaMallocAsync(&ptr, need, st) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_NOMEM;
+        }
+        mine = true;
+        return FA_OK;
+    }
+    int release(int rc) {
+        if (mine && cudaFreeAsync(ptr, stream) != cudaSuccess && rc == FA_OK) return FA_ERR_CUDA;
+        return rc;
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, long long k_t, long long k_h, long long v_t,
+                  long long v_h, const int* cu_new, int total, const void* positions, int positions_64,
+                  const void* freq, int rotary, int interleaved, float amplitude, float* weights, int* slot_positions,
+                  long long slots, void* stream) {
+    int rc = check_kv4(cache);
+    if (rc != FA_OK) return rc;
+    if (!k || !v || !cu_new) return FA_ERR_NULL;
+    if (total < 1 || static_cast<long long>(total) * cache->Hkv > INT_MAX) return FA_ERR_SHAPE;
+    if (k_t < 0 || k_h < 0 || v_t < 0 || v_h < 0) return FA_ERR_ARG;
+    if (freq && (rotary < 2 || rotary > cache->D || rotary % 2 != 0)) return FA_ERR_UNSUPPORTED;
+    if (freq && ((interleaved != 0 && interleaved != 1) || !std::isfinite(amplitude))) return FA_ERR_ARG;
+    if (positions_64 != 0 && positions_64 != 1) return FA_ERR_ARG;
+    if ((weights || slot_positions) && slots < 1) return FA_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || k_t % 8 || k_h % 8 || v_t % 8 || v_h % 8 ||
+        (reinterpret_cast<uintptr_t>(cu_new) & 3u) || (reinterpret_cast<uintptr_t>(freq) & 7u) ||
+        (reinterpret_cast<uintptr_t>(positions) & (positions_64 ? 7u : 3u)) ||
+        (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(slot_positions) & 3u))
+        return FA_ERR_ALIGN;
+    const int D = cache->D, H = cache->Hkv;
+    const size_t n_slots = static_cast<size_t>(cache->B) * H * (slots > 0 ? slots : 0) * 4;
+    const Range ins[6] = {
+        range_of(k, ((total - 1) * static_cast<size_t>(k_t) + (H - 1) * static_cast<size_t>(k_h) + D) * 2),
+        range_of(v, ((total - 1) * static_cast<size_t>(v_t) + (H - 1) * static_cast<size_t>(v_h) + D) * 2),
+        kv4_table_range(cache), kv4_lengths_range(cache), range_of(cu_new, (cache->B + 1) * static_cast<size_t>(4)),
+        range_of(positions, positions ? static_cast<size_t>(total) * (positions_64 ? 8 : 4) : 0)};
+    const Range pool = kv4_pool_range(cache), rw = range_of(weights, weights ? n_slots : 0),
+                rp = range_of(slot_positions, slot_positions ? n_slots : 0);
+    if (overlaps_any(pool, ins, 6) || overlaps_any(rw, ins, 6) || overlaps_any(rp, ins, 6) || overlap(pool, rw) ||
+        overlap(pool, rp) || overlap(rw, rp))
+        return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return fa::launch_kv4_append(kv4_shape(cache), cache->pool, cache->block_table, k, v, k_t, k_h, v_t, v_h,
+                                 cache->lengths, cu_new, total, positions, positions_64, freq, rotary, interleaved,
+                                 amplitude, weights, slot_positions, (weights || slot_positions) ? slots : 0,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k, void* v, void* stream) {
+    int rc = check_kv4(cache);
+    if (rc != FA_OK) return rc;
+    if (!k || !v) return FA_ERR_NULL;
+    if (count < 1 || static_cast<long long>(cache->B) * cache->Hkv * count > INT_MAX) return FA_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(start) & 3u)) return FA_ERR_ALIGN;
+    const size_t n = static_cast<size_t>(cache->B) * cache->Hkv * count * cache->D * 2;
+    const Range rk = range_of(k, n), rv = range_of(v, n);
+    const Range ins[4] = {kv4_pool_range(cache), kv4_table_range(cache), kv4_lengths_range(cache),
+                          range_of(start, start ? cache->B * static_cast<size_t>(4) : 0)};
+    if (overlap(rk, rv) || overlaps_any(rk, ins, 4) || overlaps_any(rv, ins, 4)) return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return fa::launch_kv4_read(kv4_shape(cache), cache->pool, cache->block_table, cache->lengths, start, count, k, v,
+                               static_cast<cudaStream_t>(stream));
+}
+
+long long fa_kv4_decode_workspace(int B, int Hq, int Hkv, int Tq, int D, int slots, int weights) {
+    if (B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Tq < 1 || slots < 16 || slots % 16 != 0) return FA_ERR_SHAPE;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    const int rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    const fa::Kv4Shape c{B, Hkv, D, 64, 16, 1, slots / 16};
+    return static_cast<long long>(fa::kv4_decode_workspace(c, Hq, Tq, weights != 0, sms));
+}
+
+int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse, int Hq, int Tq, float scale,
+                  int causal, const float* weights, float* weights_out, long long slots, void* workspace,
+                  long long workspace_bytes, void* stream) {
+    int rc = check_kv4(cache);
+    if (rc != FA_OK) return rc;
+    if (!q || !o || !lse || (weights && !weights_out)) return FA_ERR_NULL;
+    if (Hq < 1 || Hq % cache->Hkv != 0 || Tq < 1) return FA_ERR_SHAPE;
+    if (static_cast<long long>(cache->B) * Hq * Tq > INT_MAX) return FA_ERR_SHAPE;
+    if (Tq > 8) return FA_ERR_UNSUPPORTED;
+    if (Hq / cache->Hkv * Tq > 1024) return FA_ERR_UNSUPPORTED;
+    if (causal != 0 && causal != 1) return FA_ERR_ARG;
+    if (!std::isfinite(scale)) return FA_ERR_ARG;
+    if (weights_out && slots < 1) return FA_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+        (reinterpret_cast<uintptr_t>(weights_out) & 3u))
+        return FA_ERR_ALIGN;
+    const size_t nq = static_cast<size_t>(cache->B) * Hq * Tq * cache->D * 2;
+    const size_t nl = static_cast<size_t>(cache->B) * Hq * Tq * 4;
+    const size_t nw = weights_out ? static_cast<size_t>(cache->B) * cache->Hkv * slots * 4 : 0;
+    const fa::Kv4Shape shape = kv4_shape(cache);
+    // the weights may be added to in place; nothing else is shared
+    const Range ins[5] = {range_of(q, nq), kv4_pool_range(cache), kv4_table_range(cache), kv4_lengths_range(cache),
+                          range_of(weights, weights && weights != weights_out ? nw : 0)};
+    const Range outs[3] = {range_of(o, nq), range_of(lse, nl), range_of(weights_out, nw)};
+    for (int i = 0; i < 3; ++i) {
+        if (overlaps_any(outs[i], ins, 5)) return FA_ERR_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(outs[i], outs[j])) return FA_ERR_ARG;
+    }
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    const size_t need = fa::kv4_decode_workspace(shape, Hq, Tq, weights_out != nullptr, sms);
+    if (workspace) {
+        const Range ws = range_of(workspace, need);
+        if (overlaps_any(ws, ins, 5) || overlaps_any(ws, outs, 3)) return FA_ERR_ARG;
+    }
+    Workspace ws;
+    rc = ws.take(workspace, static_cast<size_t>(workspace_bytes > 0 ? workspace_bytes : 0), need,
+                 static_cast<cudaStream_t>(stream));
+    if (rc != FA_OK) return rc;
+    rc = fa::launch_kv4_decode(shape, cache->pool, cache->block_table, cache->lengths, q, o, lse, Hq, Tq, scale,
+                               causal != 0, weights, weights_out, slots, ws.ptr, static_cast<cudaStream_t>(stream),
+                               sms);
+    return ws.release(rc);
+}
+
+long long fa_kv4_evict_workspace(int B, int Hkv, int budget) {
+    if (B < 1 || Hkv < 1 || budget < 1) return FA_ERR_SHAPE;
+    return static_cast<long long>(fa::kv4_evict_workspace(B, Hkv, budget));
+}
+
+int fa_kv4_evict(const fa_kv4_cache* cache, const float* weights, const int* slot_positions, long long slots,
+                 int budget, int recent, float* weights_out, int* positions_out, int* lengths_out, int* source,
+                 void* workspace, long long workspace_bytes, void* stream) {
+    int rc = check_kv4(cache);
+    if (rc != FA_OK) return rc;
+    if (!weights || !slot_positions || !weights_out || !positions_out || !lengths_out || !source) return FA_ERR_NULL;
+    if (slots < 1 || slots > INT_MAX - 65536 || budget < 1 || budget > (1 << 30)) return FA_ERR_SHAPE;
+    if (recent < 0 || recent > budget) return FA_ERR_ARG;
+    const void* words[6] = {weights, slot_positions, weights_out, positions_out, lengths_out, source};
+    for (const void* w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return FA_ERR_ALIGN;
+    const size_t heads = static_cast<size_t>(cache->B) * cache->Hkv, n = heads * slots * 4;
+    const size_t need = fa::kv4_evict_workspace(cache->B, cache->Hkv, budget);
+    const Range ins[4] = {range_of(weights, n), range_of(slot_positions, n), kv4_table_range(cache),
+                          kv4_lengths_range(cache)};
+    const Range outs[6] = {kv4_pool_range(cache),       range_of(weights_out, n),
+                           range_of(positions_out, n),  range_of(lengths_out, cache->B * static_cast<size_t>(4)),
+                           range_of(source, heads * budget * 4), range_of(workspace, workspace ? need : 0)};
+    for (int i = 0; i < 6; ++i) {
+        if (overlaps_any(outs[i], ins, 4)) return FA_ERR_ARG;
+        for (int j = i + 1; j < 6; ++j)
+            if (overlap(outs[i], outs[j])) return FA_ERR_ARG;
+    }
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    Workspace ws;
+    rc = ws.take(workspace, static_cast<size_t>(workspace_bytes > 0 ? workspace_bytes : 0), need,
+                 static_cast<cudaStream_t>(stream));
+    if (rc != FA_OK) return rc;
+    rc = fa::launch_kv4_evict(kv4_shape(cache), cache->pool, cache->block_table, cache->lengths, weights,
+                              slot_positions, slots, budget, recent, weights_out, positions_out, lengths_out, source,
+                              ws.ptr, static_cast<cudaStream_t>(stream), sms);
+    return ws.release(rc);
+}
+
+long long fa_kv4_block_offset(const int* block_table, int width, int Hkv, int D, int group, int page_size,
+                              int num_pages, int b, int h, int slot) {
+    if (!block_table) return FA_ERR_NULL;
+    if (width < 1 || Hkv < 1 || num_pages < 1 || page_size < 16 || b < 0 || h < 0 || h >= Hkv || slot < 0)
+        return FA_ERR_SHAPE;
+    if ((D != 64 && D != 128) || (group != 32 && group != 64) || page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+    fa::Kv4Pages p{};
+    p.table = block_table;
+    p.width = width;
+    p.num_pages = num_pages;
+    p.heads = Hkv;
+    p.blocks_page = page_size / 16;
+    p.block_bytes = 16LL * (D + 8 * D / group);
+    const long long at = p.block_of(b, slot / 16);
+    return at < 0 ? static_cast<long long>(FA_ERR_PAGE) : at + h * p.head_bytes();
 }
 
 int fa_sched_tile_rows(int D, int* bm_fwd, int* bn, int* bm_bwd) {

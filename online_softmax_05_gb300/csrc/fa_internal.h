@@ -17,6 +17,7 @@ constexpr int kStatusTimeout = -7;
 constexpr int kStatusBadSeqlen = -11;
 constexpr int kStatusSmemAlign = -4;  // a kernel's dynamic shared-memory window was not 1024-byte aligned
 constexpr int kStatusDebugCheck = -12;  // debug build: a run-time index failed its bounds check
+constexpr int kStatusBadPage = -13;     // a page table names no page of the pool where a token lies
 
 // Launchers: arguments already validated by the C-ABI layer.
 // Hq query heads share Hkv key/value heads (Hq % Hkv == 0; Hkv == Hq is plain attention).
@@ -49,6 +50,38 @@ bool bwd_fuses_host(int B, int Hkv, int T, int D, int num_sms, bool deterministi
 int launch_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse,
                        void* dq, void* dk, void* dv, int B, int H, int T, int D, float scale, bool causal,
                        cudaStream_t stream, const DebugKnobs& dbg, int num_sms);
+
+// Rotary positions (fa_rope.cu).  One tensor (B, T, heads, D) by its strides in elements.
+struct RopeTensor {
+    const void* in;
+    void* out;
+    long long heads, in_b, in_t, in_h, out_b, out_t, out_h;
+};
+int launch_rope(const RopeTensor* tensors, int n_tensors, const void* positions, int pos64, long long pos_b,
+                const void* freq, int B, int T, int D, int R, int interleaved, float amplitude, int inverse,
+                int dtype, cudaStream_t stream, int num_sms);
+
+// 4-bit paged key/value cache (fa_kv4_cache.cu, fa_kv4_decode.cu; layout in fa_kv4.cuh).
+struct Kv4Shape {
+    int B, Hkv, D, group, page_size, num_pages, width;
+};
+int launch_kv4_append(const Kv4Shape& c, void* pool, const int* table, const void* k, const void* v, long long k_t,
+                      long long k_h, long long v_t, long long v_h, const int* lengths, const int* cu_new, int total,
+                      const void* positions, int pos64, const void* freq, int R, int interleaved, float amplitude,
+                      float* weights, int* slot_positions, long long slots, cudaStream_t stream);
+int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* start,
+                    int count, void* k, void* v, cudaStream_t stream);
+size_t kv4_evict_workspace(int B, int Hkv, int budget);
+int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int* lengths, const float* weights,
+                     const int* slot_positions, long long slots, int budget, int recent, float* weights_out,
+                     int* positions_out, int* lengths_out, int* source, void* workspace, cudaStream_t stream,
+                     int num_sms);
+size_t kv4_decode_workspace(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms);
+int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
+                      void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
+                      float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms);
+int kv4_cache_take_status();
+int kv4_decode_take_status();
 
 // Read and clear the device status word of each translation unit on the
 // current device (caller synchronises first).  Return 0 or a negative code.

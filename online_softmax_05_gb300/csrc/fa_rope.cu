@@ -1,0 +1,197 @@
+// fa_rope.cu -- rotary positions of queries and keys, and the gradient.
+//
+// Pair i of a row at position p turns by the angle p f_i:
+//   y1 = a (x1 cos - x2 sin),  y2 = a (x2 cos + x1 sin),
+// with x1, x2 the channels (i, i + R/2) (half layout) or (2i, 2i + 1)
+// (interleaved), R the rotated channels; the others are copied.  The gradient
+// is the same map with -sin.
+//
+// Angles.  f_i comes as a whole number of 2^-64 turns per position, so p f_i
+// modulo one turn is a wrapping 64-bit product: exact for every position,
+// however far (a product in fp32 is off by 0.06 rad at position 10^6).  Its
+// top 32 bits, read as a signed fraction of a turn, go to sincospif.
+//
+// One thread takes the same pairs of one token in several heads, so that an
+// angle is computed once for all of them.  Bound: HBM, each element read and
+// written once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeParams {
+    RopeTensor t[2];
+    int n_tensors;
+    const void* positions;  // [B or 1][T], or null: 0 .. T-1
+    long long pos_b;        // batch stride of positions (0: shared)
+    int pos64;
+    const unsigned long long* freq;
+    int T, D, R;
+    int units;         // vector units of one row
+    int heads_thread;  // heads per thread
+    long long items;   // B * T * units
+    float amp;
+    int inverse;
+};
+
+template <typename E>
+__device__ __forceinline__ float to_f(E x);
+template <>
+__device__ __forceinline__ float to_f(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <typename E>
+__device__ __forceinline__ E from_f(float x);
+template <>
+__device__ __forceinline__ float from_f(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+
+template <typename E, int V>
+struct alignas(sizeof(E) * V) Vec {
+    E e[V];
+};
+
+// A unit of a row: V pairs, or 2 V channels behind the rotated ones.
+template <typename E, int V, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
+    const long long item = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+    if (item >= p.items) return;
+    const int u = static_cast<int>(item % p.units);
+    const long long row = item / p.units;
+    const int t = static_cast<int>(row % p.T);
+    const long long b = row / p.T;
+    const int half = p.R >> 1;
+    const int pair0 = u * V;
+    const bool turned = pair0 < half;
+    // the unit's two vectors of V channels
+    int c0, c1;
+    if (turned) {
+        c0 = INTER ? 2 * pair0 : pair0;
+        c1 = INTER ? c0 + V : c0 + half;
+    } else {
+        c0 = p.R + 2 * (pair0 - half);
+        c1 = c0 + V;
+    }
+    float cs[V], sn[V];
+    if (turned) {
+        long long pos = t;
+        if (p.positions != nullptr) {
+            const long long at = b * p.pos_b + t;
+            pos = p.pos64 ? static_cast<const long long*>(p.positions)[at]
+                          : static_cast<long long>(static_cast<const int*>(p.positions)[at]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[pair0 + i];
+            const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
+            sincospif(x, &sn[i], &cs[i]);
+            cs[i] *= p.amp;
+            sn[i] *= p.inverse ? -p.amp : p.amp;
+        }
+    }
+    const bool tail = V > 1 || c1 < p.D;  // an odd head has a lone last channel
+    int h = blockIdx.y * p.heads_thread;
+    const int h_end = h + p.heads_thread;
+    for (int k = 0, h_base = 0; k < p.n_tensors; h_base += static_cast<int>(p.t[k].heads), ++k) {
+        const RopeTensor& x = p.t[k];
+        const int heads = static_cast<int>(x.heads);
+        const E* in = static_cast<const E*>(x.in) + b * x.in_b + static_cast<long long>(t) * x.in_t;
+        E* out = static_cast<E*>(x.out) + b * x.out_b + static_cast<long long>(t) * x.out_t;
+        const int last = min(h_end, h_base + heads);
+#pragma unroll 4
+        for (; h < last; ++h) {
+            const E* src = in + static_cast<long long>(h - h_base) * x.in_h;
+            E* dst = out + static_cast<long long>(h - h_base) * x.out_h;
+            Vec<E, V> a = *reinterpret_cast<const Vec<E, V>*>(src + c0), c;
+            if (tail) c = *reinterpret_cast<const Vec<E, V>*>(src + c1);
+            if (turned) {
+                E in2[2 * V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    in2[i] = a.e[i];
+                    in2[V + i] = c.e[i];
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int j1 = INTER ? 2 * i : i, j2 = INTER ? 2 * i + 1 : V + i;
+                    const float x1 = to_f(in2[j1]), x2 = to_f(in2[j2]);
+                    in2[j1] = from_f<E>(x1 * cs[i] - x2 * sn[i]);
+                    in2[j2] = from_f<E>(x2 * cs[i] + x1 * sn[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    a.e[i] = in2[i];
+                    c.e[i] = in2[V + i];
+                }
+            }
+            *reinterpret_cast<Vec<E, V>*>(dst + c0) = a;
+            if (tail) *reinterpret_cast<Vec<E, V>*>(dst + c1) = c;
+        }
+    }
+}
+
+template <typename E, int V>
+int launch(const RopeParams& p, int inter, dim3 grid, cudaStream_t st) {
+    if (inter)
+        fa_rope_kernel<E, V, true><<<grid, kRopeThreads, 0, st>>>(p);
+    else
+        fa_rope_kernel<E, V, false><<<grid, kRopeThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+}  // namespace
+
+int launch_rope(const RopeTensor* tensors, int n_tensors, const void* positions, int pos64, long long pos_b,
+                const void* freq, int B, int T, int D, int R, int interleaved, float amplitude, int inverse,
+                int dtype, cudaStream_t stream, int num_sms) {
+    const int size = dtype == 2 ? 4 : 2, wide = 16 / size;
+    // 16-byte vectors where every row starts on one and the unit borders fall on them
+    bool vec = (R / 2) % wide == 0 && (D - R) % (2 * wide) == 0;
+    RopeParams p{};
+    long long heads = 0;
+    for (int k = 0; k < n_tensors; ++k) {
+        const RopeTensor& x = tensors[k];
+        p.t[k] = x;
+        heads += x.heads;
+        vec = vec && ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out)) & 15u) == 0;
+        for (long long s : {x.in_b, x.in_t, x.in_h, x.out_b, x.out_t, x.out_h}) vec = vec && s % wide == 0;
+    }
+    const int V = vec ? wide : 1;
+    p.n_tensors = n_tensors;
+    p.positions = positions;
+    p.pos64 = pos64;
+    p.pos_b = pos_b;
+    p.freq = static_cast<const unsigned long long*>(freq);
+    p.T = T;
+    p.D = D;
+    p.R = R;
+    p.units = R / 2 / V + (D - R + 2 * V - 1) / (2 * V);
+    p.items = static_cast<long long>(B) * T * p.units;
+    p.amp = amplitude;
+    p.inverse = inverse;
+    // a thread takes up to 8 heads, fewer while the grid would leave SMs without work
+    int per = 8;
+    while (per > 1 && p.items * ((heads + per - 1) / per) < static_cast<long long>(num_sms) * 1024) per >>= 1;
+    p.heads_thread = per;
+    const long long blocks = (p.items + kRopeThreads - 1) / kRopeThreads, ny = (heads + per - 1) / per;
+    if (blocks > 0x7fffffffLL || ny > 65535) return -2;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ny));
+    if (dtype == 0) return vec ? launch<__nv_bfloat16, 8>(p, interleaved, grid, stream) : launch<__nv_bfloat16, 1>(p, interleaved, grid, stream);
+    if (dtype == 1) return vec ? launch<__half, 8>(p, interleaved, grid, stream) : launch<__half, 1>(p, interleaved, grid, stream);
+    return vec ? launch<float, 4>(p, interleaved, grid, stream) : launch<float, 1>(p, interleaved, grid, stream);
+}
+
+}  // namespace fa
