@@ -516,7 +516,7 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
     if (rc != FA_OK) return rc;
     rc = fa::launch_kv4_decode(shape, cache->pool, cache->block_table, cache->lengths, q, o, lse, Hq, Tq, scale,
                                causal != 0, weights, weights_out, slots, ws.ptr, static_cast<cudaStream_t>(stream),
-                               sms);
+                               knobs(), sms);
     return ws.release(rc);
 }
 

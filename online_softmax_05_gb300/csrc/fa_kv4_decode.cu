@@ -2,11 +2,34 @@
 //
 // With k = s n + m and v = s n + m per group g of channels (fa_kv4.cuh),
 //   S_t = scale sum_g ( s_tg (q_g . n_tg) + m_tg sum(q_g) ),  P = softmax(S),
-//   O_c = sum_t P_t (s_tg n_tc + m_tg).
-// The tokens of each sequence are split over CTAs, each keeping a running
-// maximum and sum, and a second kernel joins the parts, as in fa_decode.cu.
-// With weights, the scores are kept as well and a third kernel adds every
-// slot's attention weight, summed over the query rows, to its account.
+//   O_c = sum_t P_t s_tg n_tc + sum_t P_t m_tg.
+// The scales never meet the matrix operands' elements: the codes go to the
+// tensor cores as they are, K's scale multiplies the 16 x 8 tile of q . n, V's
+// scale multiplies P before the second product, and the minima are fp32 sums.
+//
+// Codes as fp16.  A nibble masked into the low bits of a 16-bit half is the
+// fp16 subnormal n 2^-24 (bits 0-3) or n 2^-20 (bits 4-7), which the matrix
+// instructions take exactly: one AND makes two operand elements, a shift by 8
+// the other four of a word.  (Converting through exponent tricks costs a
+// subtraction more per pair.)  q is scaled per row by a power of two into
+// fp16's range (bf16 values stay exact down to 2^-28 of the row's largest), and
+// the power goes into the row's score factor.
+//
+// Both products put the tokens or channels on the 16-row side and the query
+// rows on the 8-column side (m16n8k16), which suits 1 to 8 rows per key/value
+// head: S^T = K q^T, O^T = V^T P^T.  The channel order inside a row of codes is
+// the fragments' own, so there is no shuffle on K; a pair of tokens of V meets
+// with one byte permute, and P^T turns from accumulator to operand by movmatrix.
+// tcgen05 would need the operands dequantised into shared memory (a write and
+// a read of 4 times the cache's bytes) and uses 8 of its 128 rows.
+//
+// Bound: HBM, the cache's bytes once.  Each warp streams units of 32 or 64
+// tokens through its own ring of shared memory with bulk copies (16 tokens of a
+// head are contiguous), 8 warps per CTA and 2 CTAs per SM.  The units of all
+// sequences and heads form one line that is cut evenly over the CTAs, so ragged
+// lengths balance without the host knowing them; a head cut between CTAs is
+// joined by a second kernel.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "fa_internal.h"
@@ -18,212 +41,815 @@ namespace {
 
 __device__ int g_status_kv4_decode = 0;
 
+__device__ __forceinline__ void report(int code) { atomicCAS(&g_status_kv4_decode, 0, code); }
+
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kWarps = 4;
-constexpr int kRows = 8;  // query rows of one CTA
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 2;
 
 struct DecParams {
     const __nv_bfloat16* q;
     Kv4Pages pages;
     const int* lengths;
-    float* part_m;    // [B Hkv][n_split][R]
-    float* part_l;
-    float* part_acc;  // [B Hkv][n_split][R][D]
-    float* scores;    // [B Hkv][R][cap] in log2 units, or null
+    float2* part_o;   // [slot][NT][D/8][32] unnormalised output pairs, in the lanes' order
+    float* part_ml;   // [slot][NT][2][8] running maximum (log2 units) and sum
+    float* scores;    // [B Hkv][cap][RB NT 8] in log2 units, or null
     __nv_bfloat16* o;
     float* lse;
     const float* weights;
     float* weights_out;
     long long slots, cap;
-    int R, Tq, causal, n_split;
+    unsigned long long timeout_ns;
+    int B, R, RB, Tq, causal, n_cta;
     float sl2;  // scale log2(e)
+};
+
+template <int D_, int G_, int NT_>
+struct Cfg : Kv4<D_, G_> {
+    using L = Kv4<D_, G_>;
+    static constexpr int UB = D_ == 128 ? 2 : 4;    // blocks of 16 tokens in a unit
+    static constexpr int kTokens = UB * 16;
+    static constexpr int kUnitBytes = UB * L::kBlock;
+    static constexpr int kWords = D_ / 32;          // 32-channel slices
+    static constexpr int kPairs = D_ / 8;           // pairs of accumulators of a lane and row tile
+    static constexpr int kRing = kWarps * kStages * kUnitBytes;
+    static constexpr int kMergeO = kWarps * kPairs * 32 * 8;
+    static constexpr int kMergeML = kWarps * 2 * 8 * 4;
+    static constexpr int kSmem = kRing + kMergeO + kMergeML + kWarps * kStages * 8;
 };
 
 // Length of sequence b, 0 (and a status) if the table or the accounts cannot hold it.
 __device__ __forceinline__ int length_of(const DecParams& p, int b) {
     const int len = p.lengths[b];
     if (len < 0 || len > p.pages.capacity() || (p.weights_out != nullptr && len > p.slots)) {
-        atomicCAS(&g_status_kv4_decode, 0, kStatusBadSeqlen);
+        report(kStatusBadSeqlen);
         return 0;
     }
     return len;
 }
-// Tokens that query row r sees.
-__device__ __forceinline__ int seen_by(const DecParams& p, int r, int len) {
-    return p.causal ? max(0, len - (p.Tq - 1 - r % p.Tq)) : len;
-}
 
-__device__ __forceinline__ float warp_sum(float x) {
+__device__ __forceinline__ long long warp_sum_ll(long long x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// Code of channel c in a row of key or value codes.
-template <int D>
-__device__ __forceinline__ float key_code(const unsigned char* row, int c) {
-    const int n = 8 * ((c % 32) / 8 * (D / 32) + c / 32) + c % 8;
-    return static_cast<float>(row[n >> 1] >> (4 * (n & 1)) & 15);
+// Units of all sequences, and of those before sequence `upto`; per warp.
+template <int TOKENS>
+__device__ __forceinline__ void count_units(const DecParams& p, int lane, int upto, long long& all, long long& before) {
+    all = before = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int n = (length_of(p, b) + TOKENS - 1) / TOKENS;
+        all += n;
+        if (b < upto) before += n;
+    }
+    all = warp_sum_ll(all);
+    before = warp_sum_ll(before);
 }
-template <int D>
-__device__ __forceinline__ float value_code(const unsigned char* row, int c) {
-    const int n = 4 * ((c % 32) / 4 * (D / 32) + c / 32) + c % 4;
-    return static_cast<float>(row[n >> 1] >> (4 * (n & 1)) & 15);
+// Units of one CTA: an even share, and at least one for each of its warps.
+__device__ __forceinline__ long long share_of(const DecParams& p, long long all_units, int heads_rows) {
+    const long long total = all_units * heads_rows;
+    const long long even = (total + p.n_cta - 1) / p.n_cta;
+    return even > kWarps ? even : kWarps;
 }
 
-// One warp takes one token at a time, lane = D/32 channels.
-template <int D, int G>
-__global__ void __launch_bounds__(kWarps * 32) fa_kv4_decode_kernel(DecParams p) {
-    using L = Kv4<D, G>;
-    constexpr int E = D / 32;
-    const int split = blockIdx.x, bh = blockIdx.y, r0 = blockIdx.z * kRows;
-    const int b = bh / p.pages.heads, h = bh % p.pages.heads;
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// N 32-bit words from shared memory in one load.
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&x)[N]) {
+    static_assert(N == 1 || N == 2 || N == 4);
+    if constexpr (N == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[0]) : "r"(addr));
+    if constexpr (N == 2) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(addr));
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(addr));
+}
+
+// A stretch of units of one (sequence, head, row block) inside a CTA's share.
+struct Segment {
+    int b, hr;     // hr = head * RB + row block
+    int u0, u1;    // units of the sequence
+    int n, len;    // units and tokens of the sequence
+};
+
+// Token of row r (0..7) of a fragment: any order serves, as K and V agree; this
+// one puts neighbouring rows of K and the four rows of one V load on different
+// halves of the banks.
+__device__ __forceinline__ int token_of(int r) { return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1; }
+
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kernel(DecParams p) {
+    using C = Cfg<D, G, NT>;
+    extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = min(kRows, p.R - r0);
-    const int len = length_of(p, b);
-    const int chunk = (len + p.n_split - 1) / p.n_split;
-    const int t0 = split * chunk, t1 = min(len, t0 + chunk);
-    float q[kRows][E], m[kRows], l[kRows], acc[kRows][E];
+    const int g4 = lane >> 2, j = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * C::kUnitBytes;
+    float2* sm_o = reinterpret_cast<float2*>(smem + C::kRing);
+    float* sm_ml = reinterpret_cast<float*>(smem + C::kRing + C::kMergeO);
+    const uint32_t bars = smem_u32(smem + C::kRing + C::kMergeO + C::kMergeML) + warp * kStages * 8;
+    const int HR = p.pages.heads * p.RB;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (lane == 0) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            q[r][e] = r < rows ? __bfloat162float(p.q[(static_cast<long long>(bh) * p.R + r0 + r) * D + e * 32 + lane]) : 0.f;
-            acc[r][e] = 0.f;
-        }
+        for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+        fence_mbar_init();
     }
-    for (int t = t0 + warp; t < t1; t += kWarps) {
-        const long long at = p.pages.block_of(b, t >> 4);
-        if (at < 0) {
-            if (lane == 0) atomicCAS(&g_status_kv4_decode, 0, kStatusBadPage);
-            if (p.scores != nullptr && lane < rows)
-                p.scores[(static_cast<long long>(bh) * p.R + r0 + lane) * p.cap + t] = -INFINITY;
-            continue;
+    __syncwarp();
+
+    // this CTA's share of the line of units, found by one warp for all: every
+    // warp walks the same segments whatever else happens to the lengths
+    __shared__ Segment s_seg[2];
+    __shared__ long long s_left;
+    if (warp == 0) {
+        Segment seg{0, 0, 0, 0, 0, 0};
+        long long all, unused;
+        count_units<C::kTokens>(p, lane, 0, all, unused);
+        const long long share = share_of(p, all, HR), total = all * HR;
+        const long long first = blockIdx.x * share;
+        long long left = min(share, total - first);
+        long long base = 0;     // units before the chunk of sequences
+        bool found = false;
+        for (int b0 = 0; b0 < p.B && left > 0; b0 += 32) {
+            const int b = b0 + lane;
+            const int len = b < p.B ? length_of(p, b) : 0;
+            const int n = (len + C::kTokens - 1) / C::kTokens;
+            long long sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, (base + sum) * HR > first);
+            if (hit != 0) {
+                const int src = __ffs(hit) - 1;
+                seg.b = b0 + src;
+                seg.len = __shfl_sync(0xffffffffu, len, src);
+                seg.n = __shfl_sync(0xffffffffu, n, src);
+                const long long rem = first - (base + __shfl_sync(0xffffffffu, sum, src) - seg.n) * HR;
+                seg.hr = static_cast<int>(rem / seg.n);
+                seg.u0 = static_cast<int>(rem % seg.n);
+                seg.u1 = static_cast<int>(min(static_cast<long long>(seg.n), seg.u0 + left));
+                found = true;
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        const unsigned char* block = p.pages.pool + at + h * p.pages.head_bytes();
-        const int i = t & 15;
-        float kf[E], vf[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int c = e * 32 + lane, g = c / G;
-            const float2 ks = kv4_scale(reinterpret_cast<const uint32_t*>(block + L::kKeyScales + i * L::kScaleRow)[g]);
-            const float2 vs = kv4_scale(reinterpret_cast<const uint32_t*>(block + L::kValueScales + i * L::kScaleRow)[g]);
-            kf[e] = fmaf(key_code<D>(block + L::kKeyCodes + i * L::kRow, c), ks.x, ks.y);
-            vf[e] = fmaf(value_code<D>(block + L::kValueCodes + i * L::kRow, c), vs.x, vs.y);
-        }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (r >= rows) break;
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s = fmaf(q[r][e], kf[e], s);
-            s = warp_sum(s) * p.sl2;
-            if (t >= seen_by(p, r0 + r, len)) s = -INFINITY;
-            if (p.scores != nullptr && lane == 0)
-                p.scores[(static_cast<long long>(bh) * p.R + r0 + r) * p.cap + t] = s;
-            if (s == -INFINITY) continue;
-            const float m_new = fmaxf(m[r], s);
-            const float alpha = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - m_new);
-            const float w = ex2_approx(s - m_new);
-            l[r] = l[r] * alpha + w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[r][e] = fmaf(acc[r][e], alpha, w * vf[e]);
-            m[r] = m_new;
-        }
-    }
-    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-    __shared__ float sm_acc[kWarps][kRows][D];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
         if (lane == 0) {
-            sm_m[warp][r] = m[r];
-            sm_l[warp][r] = l[r];
+            s_seg[0] = seg;
+            s_left = found ? left : 0;
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) sm_acc[warp][r][e * 32 + lane] = acc[r][e];
     }
     __syncthreads();
-    for (int r = warp; r < rows; r += kWarps) {
-        float mm = -INFINITY, ll = 0.f, f[kWarps];
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][r]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            f[w] = sm_l[w][r] == 0.f ? 0.f : ex2_approx(sm_m[w][r] - mm);
-            ll = fmaf(f[w], sm_l[w][r], ll);
+    Segment seg = s_seg[0];
+    long long left = s_left;
+    if (left <= 0) return;  // whole CTA
+
+    // copies of one unit into a stage of this warp's ring; returns the blocks that have a page
+    const uint64_t policy = l2_policy_evict_first();
+    auto issue = [&](const Segment& s, int u, int stage) -> uint32_t {
+        long long at = -1;
+        const int blk = u * C::UB + lane;
+        if (lane < C::UB && blk * 16 < s.len) {
+            at = p.pages.block_of(s.b, blk);
+            if (at < 0) report(kStatusBadPage);
         }
-        const long long at = (static_cast<long long>(bh) * p.n_split + split) * p.R + r0 + r;
-        for (int d = lane; d < D; d += 32) {
-            float a = 0.f;
+        const uint32_t valid = __ballot_sync(0xffffffffu, at >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, __popc(valid) * C::kBlock);
+        __syncwarp();
+        if (at >= 0) {
+            const unsigned char* src = p.pages.pool + at + static_cast<long long>(s.hr / p.RB) * p.pages.head_bytes();
+            const uint32_t dst = ring + stage * C::kUnitBytes + lane * C::kBlock;
+            if (p.RB == 1)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+                    "l"(src), "r"(C::kBlock), "r"(bars + 8 * stage), "l"(policy)
+                    : "memory");
+            else
+                bulk_load_1d(dst, src, C::kBlock, bars + 8 * stage);
+        }
+        return valid;
+    };
+    uint32_t masks = 0;  // 8 bits of each stage: its blocks with a page
+    int issued = 0, taken = 0;
+    bool dead = false;   // a copy did not arrive in time
+    auto prologue = [&](const Segment& s) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) a = fmaf(f[w], sm_acc[w][r][d], a);
-            p.part_acc[at * D + d] = a;
+        for (int i = 0; i < kStages; ++i) {
+            const int u = s.u0 + warp + i * kWarps;
+            if (u < s.u1 && !dead) {
+                const int stage = issued % kStages;
+                masks = (masks & ~(0xffu << (8 * stage))) | issue(s, u, stage) << (8 * stage);
+                ++issued;
+            }
         }
-        if (lane == 0) {
-            p.part_m[at] = mm;
-            p.part_l[at] = ll;
+    };
+    auto wait = [&](int stage, uint32_t phase) -> bool {
+        if (mbar_try_wait(bars + 8 * stage, phase)) return true;
+        const uint64_t begin = globaltimer_ns();
+        while (!mbar_try_wait_sleep(bars + 8 * stage, phase, 20000)) {
+            if (globaltimer_ns() - begin > p.timeout_ns) return false;
         }
+        return true;
+    };
+    prologue(seg);
+
+    const int tokA = token_of(g4), tokB = 8 + tokA;
+    int parity = 0;
+    for (;;) {
+        left -= seg.u1 - seg.u0;
+        const int head = seg.hr / p.RB, rb = seg.hr % p.RB;
+        const int bh = seg.b * p.pages.heads + head;
+        const int row0 = rb * NT * 8;
+
+        // ---- queries: operand fragments, group sums and score factors
+        uint32_t qf[NT][C::kWords][4];
+        float qs[NT][C::kGroups][2], factor[NT][2];
+        int seen[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row0 + nt * 8 + g4;
+            uint4 raw[C::kWords];
+            float top = 0.f;
+            bool finite = true;
+#pragma unroll
+            for (int w = 0; w < C::kWords; ++w) {
+                raw[w] = make_uint4(0, 0, 0, 0);
+                if (row < p.R)
+                    raw[w] = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(bh) * p.R + row) * D +
+                                                             32 * w + 8 * j);
+                const uint32_t word[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = __uint_as_float(word[e] << 16), b = __uint_as_float(word[e] & 0xffff0000u);
+                    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+                    finite = finite && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                finite = __shfl_xor_sync(0xffffffffu, finite, o) && finite;
+            }
+            // 2^e <= top < 2^(e+1) goes to 2^14; two exact steps, as 2^(14-e) alone may leave fp32
+            const int e = top > 0.f && finite ? ilogbf(top) : 0;
+            const float up1 = exp2f(static_cast<float>((14 - e) / 2)), up2 = exp2f(static_cast<float>(14 - e - (14 - e) / 2));
+            float group[C::kGroups];
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) group[g] = 0.f;
+#pragma unroll
+            for (int w = 0; w < C::kWords; ++w) {
+                const uint32_t word[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = __uint_as_float(word[i] << 16) * up1 * up2;
+                    x[2 * i + 1] = __uint_as_float(word[i] & 0xffff0000u) * up1 * up2;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) group[w * 32 / G] += x[i];
+                qf[nt][w][0] = pack_f16(x[0], x[4]);
+                qf[nt][w][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+                qf[nt][w][2] = pack_f16(x[2], x[6]);
+                qf[nt][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+            }
+            const float back = finite ? p.sl2 * exp2f(static_cast<float>((10 + e) / 2)) *
+                                            exp2f(static_cast<float>(10 + e - (10 + e) / 2))
+                                      : NAN;
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) {
+                float s = group[g];
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                s *= 5.9604644775390625e-8f;  // 2^-24, the codes' unit
+                qs[nt][g][0] = __shfl_sync(0xffffffffu, s, 8 * j);
+                qs[nt][g][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
+            }
+            factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * j);
+            factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * j + 4);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = row0 + nt * 8 + 2 * j + c;
+                seen[nt][c] = p.causal ? seg.len - (p.Tq - 1 - r % p.Tq) : seg.len;
+            }
+        }
+        const int all_see = p.causal ? seg.len - (p.Tq - 1) : seg.len;  // tokens every row sees
+
+        float acc[NT][C::kWords][2][4];     // O^T: channels 32 w + 4 r + {0,1}, {2,3}
+        float om[NT][C::kGroups][2], l[NT][2], ref[NT][2];
+        float cap = 0.f, inv_cap = 0.f;     // power of two at or above every value scale so far
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int w = 0; w < C::kWords; ++w)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) acc[nt][w][x >> 2][x & 3] = 0.f;
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) om[nt][g][0] = om[nt][g][1] = 0.f;
+            l[nt][0] = l[nt][1] = 0.f;
+            ref[nt][0] = ref[nt][1] = -INFINITY;
+        }
+
+        for (int u = seg.u0 + warp; u < seg.u1; u += kWarps) {
+            const int stage = taken % kStages;
+            if (!dead && !__all_sync(0xffffffffu, wait(stage, (taken / kStages) & 1))) {
+                report(kStatusTimeout);
+                dead = true;
+            }
+            if (dead) break;
+            ++taken;
+            const uint32_t unit = ring + stage * C::kUnitBytes;
+            const uint32_t valid = masks >> (8 * stage) & 0xffu;
+            const int t0 = u * C::kTokens;
+            // some token of the unit is not there or not seen by every row
+            const bool edge = t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1;
+
+            // ---- S^T = K q^T
+            float s[C::UB][NT][4];
+#pragma unroll
+            for (int ub = 0; ub < C::UB; ++ub) {
+                const uint32_t blk = unit + ub * C::kBlock;
+                uint32_t xa[C::kWords], xb[C::kWords], pa[C::kGroups], pb[C::kGroups];
+                lds(blk + C::kKeyCodes + tokA * C::kRow + j * (C::kWords * 4), xa);
+                lds(blk + C::kKeyCodes + tokB * C::kRow + j * (C::kWords * 4), xb);
+                lds(blk + C::kKeyScales + tokA * C::kScaleRow, pa);
+                lds(blk + C::kKeyScales + tokB * C::kScaleRow, pb);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[ub][nt][c] = 0.f;
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) {
+                    float d[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) d[nt][c] = 0.f;
+#pragma unroll
+                    for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
+                        const uint32_t ya = xa[w] >> 8, yb = xb[w] >> 8;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(d[nt], xa[w] & 0x000f000fu, xb[w] & 0x000f000fu, xa[w] & 0x00f000f0u,
+                                    xb[w] & 0x00f000f0u, qf[nt][w][0], qf[nt][w][1]);
+                            mma_f16(d[nt], ya & 0x000f000fu, yb & 0x000f000fu, ya & 0x00f000f0u, yb & 0x00f000f0u,
+                                    qf[nt][w][2], qf[nt][w][3]);
+                        }
+                    }
+                    const float2 sa = kv4_scale(pa[g]), sb = kv4_scale(pb[g]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        s[ub][nt][0] = fmaf(sa.x, d[nt][0], fmaf(sa.y, qs[nt][g][0], s[ub][nt][0]));
+                        s[ub][nt][1] = fmaf(sa.x, d[nt][1], fmaf(sa.y, qs[nt][g][1], s[ub][nt][1]));
+                        s[ub][nt][2] = fmaf(sb.x, d[nt][2], fmaf(sb.y, qs[nt][g][0], s[ub][nt][2]));
+                        s[ub][nt][3] = fmaf(sb.x, d[nt][3], fmaf(sb.y, qs[nt][g][1], s[ub][nt][3]));
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[ub][nt][c] *= factor[nt][c & 1];
+                if (edge) {
+                    const bool here = valid >> ub & 1;
+                    const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (!here || (c < 2 ? ta : tb) >= seen[nt][c & 1]) s[ub][nt][c] = -INFINITY;
+                }
+                if (p.scores != nullptr) {
+                    const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+                    const int width = p.RB * NT * 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float* to = p.scores + (static_cast<long long>(bh) * p.cap + ta) * width + row0 + nt * 8 + 2 * j;
+                        if (ta < seg.len) *reinterpret_cast<float2*>(to) = make_float2(s[ub][nt][0], s[ub][nt][1]);
+                        if (tb < seg.len)
+                            *reinterpret_cast<float2*>(to + 8LL * width) = make_float2(s[ub][nt][2], s[ub][nt][3]);
+                    }
+                }
+            }
+
+            // ---- value scales, running maxima
+            float2 va[C::UB][C::kGroups], vb[C::UB][C::kGroups];
+            float vtop = 0.f;
+#pragma unroll
+            for (int ub = 0; ub < C::UB; ++ub) {
+                const uint32_t blk = unit + ub * C::kBlock;
+                uint32_t pa[C::kGroups], pb[C::kGroups];
+                lds(blk + C::kValueScales + tokA * C::kScaleRow, pa);
+                lds(blk + C::kValueScales + tokB * C::kScaleRow, pb);
+                const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) {
+                    if (edge && (!(valid >> ub & 1) || ta >= seg.len)) pa[g] = 0;
+                    if (edge && (!(valid >> ub & 1) || tb >= seg.len)) pb[g] = 0;
+                    va[ub][g] = kv4_scale(pa[g]);
+                    vb[ub][g] = kv4_scale(pb[g]);
+                    vtop = fmaxf(vtop, fmaxf(va[ub][g].x, vb[ub][g].x));
+                }
+            }
+            float mx[NT][2];
+            bool more = vtop > cap;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    mx[nt][c] = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+#pragma unroll
+                    for (int ub = 1; ub < C::UB; ++ub)
+                        mx[nt][c] = fmaxf(mx[nt][c], fmaxf(s[ub][nt][c], s[ub][nt][c + 2]));
+                    more = more || mx[nt][c] > ref[nt][c];
+                }
+            if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+                float shrink = 1.f;
+                if (vtop > cap) {
+                    // the power of two at or above it; 2^-100 is the format's least scale
+                    const float up = fmaxf(__uint_as_float((__float_as_uint(vtop) + 0x007fffffu) & 0x7f800000u),
+                                           7.888609052210118e-31f);
+                    shrink = cap / up;
+                    cap = up;
+                    inv_cap = 16384.f / cap;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float alpha[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1)
+                            mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], o));
+                        const float now = fmaxf(ref[nt][c], mx[nt][c]);
+                        alpha[c] = ref[nt][c] == -INFINITY ? 0.f : ex2_approx(ref[nt][c] - now);
+                        // nothing seen so far leaves NaN sums (a NaN score) as they are
+                        if (now == -INFINITY) alpha[c] = 1.f;
+                        ref[nt][c] = now;
+                        l[nt][c] *= alpha[c];
+                    }
+#pragma unroll
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        om[nt][g][0] *= alpha[0];
+                        om[nt][g][1] *= alpha[1];
+                    }
+                    alpha[0] *= shrink;
+                    alpha[1] *= shrink;
+#pragma unroll
+                    for (int w = 0; w < C::kWords; ++w)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) acc[nt][w][x >> 2][x & 3] *= alpha[x & 1];
+                }
+            }
+
+            // ---- P, and O^T += V^T P^T
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float r0 = ref[nt][0] == -INFINITY ? 0.f : ref[nt][0];
+                const float r1 = ref[nt][1] == -INFINITY ? 0.f : ref[nt][1];
+#pragma unroll
+                for (int ub = 0; ub < C::UB; ++ub) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[ub][nt][c] = ex2_approx(s[ub][nt][c] - (c & 1 ? r1 : r0));
+                    l[nt][0] += s[ub][nt][0] + s[ub][nt][2];
+                    l[nt][1] += s[ub][nt][1] + s[ub][nt][3];
+                }
+            }
+#pragma unroll
+            for (int ub = 0; ub < C::UB; ++ub) {
+                const uint32_t blk = unit + ub * C::kBlock + C::kValueCodes + g4 * (C::kWords * 2);
+                uint32_t x0[C::kWords / 2], x1[C::kWords / 2], x2[C::kWords / 2], x3[C::kWords / 2];
+                lds(blk + token_of(2 * j) * C::kRow, x0);
+                lds(blk + token_of(2 * j + 1) * C::kRow, x1);
+                lds(blk + (8 + token_of(2 * j)) * C::kRow, x2);
+                lds(blk + (8 + token_of(2 * j + 1)) * C::kRow, x3);
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) {
+                    uint32_t b0[NT], b1[NT];
+                    const float ka = va[ub][g].x * inv_cap, kb = vb[ub][g].x * inv_cap;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float* q = s[ub][nt];
+                        float w0 = q[0] * ka, w1 = q[1] * ka, w2 = q[2] * kb, w3 = q[3] * kb;
+                        float m0 = q[0] * va[ub][g].y, m1 = q[1] * va[ub][g].y;
+                        float m2 = q[2] * vb[ub][g].y, m3 = q[3] * vb[ub][g].y;
+                        if (edge) {
+                            // a token hidden from a row adds nothing to it, whatever its scale holds
+                            const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+                            if (ta >= seen[nt][0]) w0 = m0 = 0.f;
+                            if (ta >= seen[nt][1]) w1 = m1 = 0.f;
+                            if (tb >= seen[nt][0]) w2 = m2 = 0.f;
+                            if (tb >= seen[nt][1]) w3 = m3 = 0.f;
+                        }
+                        om[nt][g][0] += m0 + m2;
+                        om[nt][g][1] += m1 + m3;
+                        b0[nt] = transpose8(pack_f16(w0, w1));
+                        b1[nt] = transpose8(pack_f16(w2, w3));
+                    }
+#pragma unroll
+                    for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
+                        const uint32_t sel = w & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t z0 = __byte_perm(x0[w / 2], x1[w / 2], sel);
+                        const uint32_t z1 = __byte_perm(x2[w / 2], x3[w / 2], sel);
+                        const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(acc[nt][w][0], z0 & 0x000f000fu, z0 & 0x00f000f0u, z1 & 0x000f000fu,
+                                    z1 & 0x00f000f0u, b0[nt], b1[nt]);
+                            mma_f16(acc[nt][w][1], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu,
+                                    y1 & 0x00f000f0u, b0[nt], b1[nt]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read the stage
+            const int ahead = u + kStages * kWarps;
+            if (ahead < seg.u1) {
+                masks = (masks & ~(0xffu << (8 * stage))) | issue(seg, ahead, stage) << (8 * stage);
+                ++issued;
+            }
+        }
+
+        // ---- the next segment's first copies run while this one is joined
+        parity ^= 1;
+        if (warp == 0) {
+            Segment next = seg;
+            next.u0 = 0;
+            if (left > 0 && ++next.hr == HR) {
+                next.hr = 0;
+                do {
+                    ++next.b;
+                    next.len = next.b < p.B ? length_of(p, next.b) : 1;
+                    next.n = (next.len + C::kTokens - 1) / C::kTokens;
+                } while (next.n == 0);
+            }
+            next.u1 = static_cast<int>(min(static_cast<long long>(next.n), left));
+            if (next.b >= p.B) next.u1 = 0;
+            if (lane == 0) s_seg[parity] = next;
+        }
+        __syncthreads();
+        const Segment next = s_seg[parity];
+        const bool more_segments = next.u1 > 0;
+        if (more_segments) prologue(next);
+
+        // ---- join the warps: running maxima and sums, then outputs
+        const bool whole = seg.u0 == 0 && seg.u1 == seg.n;
+        const long long slot = blockIdx.x + static_cast<long long>(seg.b) * HR + seg.hr;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g)
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) om[nt][g][c] += __shfl_xor_sync(0xffffffffu, om[nt][g][c], o);
+            }
+            const float unit_o = cap * 1024.f;  // 2^24 of the codes over the 2^14 of P
+#pragma unroll
+            for (int w = 0; w < C::kWords; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float k = i & 1 ? unit_o * 0.0625f : unit_o;
+                    sm_o[(warp * C::kPairs + w * 4 + i) * 32 + lane] =
+                        make_float2(fmaf(acc[nt][w][i >> 1][2 * (i & 1)], k, om[nt][w * 32 / G][0]),
+                                    fmaf(acc[nt][w][i >> 1][2 * (i & 1) + 1], k, om[nt][w * 32 / G][1]));
+                }
+            if (g4 == 0) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    sm_ml[warp * 16 + 2 * j + c] = ref[nt][c];
+                    sm_ml[warp * 16 + 8 + 2 * j + c] = l[nt][c];
+                }
+            }
+            __syncthreads();
+            float f[kWarps][2], top[2], sum[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                top[c] = -INFINITY;
+                sum[c] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top[c] = fmaxf(top[c], sm_ml[w * 16 + 2 * j + c]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float lw = sm_ml[w * 16 + 8 + 2 * j + c];
+                    f[w][c] = lw == 0.f ? 0.f : ex2_approx(sm_ml[w * 16 + 2 * j + c] - top[c]);
+                    sum[c] = fmaf(f[w][c], lw, sum[c]);
+                }
+            }
+            const int row = row0 + nt * 8 + 2 * j;
+            for (int i = warp; i < C::kPairs; i += kWarps) {
+                float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 x = sm_o[(w * C::kPairs + i) * 32 + lane];
+                    if (f[w][0] != 0.f) o.x = fmaf(f[w][0], x.x, o.x);
+                    if (f[w][1] != 0.f) o.y = fmaf(f[w][1], x.y, o.y);
+                }
+                if (whole) {
+                    const int ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
+                    __nv_bfloat16* to = p.o + (static_cast<long long>(bh) * p.R + row) * D + ch;
+                    if (row < p.R) to[0] = __float2bfloat16_rn(sum[0] == 0.f ? 0.f : o.x / sum[0]);
+                    if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum[1] == 0.f ? 0.f : o.y / sum[1]);
+                } else {
+                    p.part_o[((slot * NT + nt) * C::kPairs + i) * 32 + lane] = o;
+                }
+            }
+            if (warp == 0 && g4 == 0) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (!whole) {
+                        p.part_ml[(slot * NT + nt) * 16 + 2 * j + c] = top[c];
+                        p.part_ml[(slot * NT + nt) * 16 + 8 + 2 * j + c] = sum[c];
+                    } else if (row + c < p.R) {
+                        p.lse[static_cast<long long>(bh) * p.R + row + c] =
+                            sum[c] == 0.f ? -INFINITY : (top[c] + __log2f(sum[c])) * kLn2;
+                    }
+                }
+            }
+            __syncthreads();  // the buffers are free again
+        }
+        if (!more_segments) break;
+        seg = next;
     }
+    // a copy that was late still writes to this CTA's memory: give it the same time again
+    if (dead)
+        while (taken < issued && __all_sync(0xffffffffu, wait(taken % kStages, (taken / kStages) & 1))) ++taken;
 }
 
-// One warp per query row: join the parts.
-template <int D>
-__global__ void __launch_bounds__(128) fa_kv4_merge_kernel(DecParams p, int n_rows) {
-    const int row = (blockIdx.x * 128 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    if (row >= n_rows) return;
-    const int bh = row / p.R, r = row % p.R;
-    auto at = [&](int s) { return (static_cast<long long>(bh) * p.n_split + s) * p.R + r; };
-    float mm = -INFINITY, ll = 0.f;
-    for (int s = 0; s < p.n_split; ++s) mm = fmaxf(mm, p.part_m[at(s)]);
-    for (int s = 0; s < p.n_split; ++s)
-        if (p.part_l[at(s)] != 0.f) ll = fmaf(ex2_approx(p.part_m[at(s)] - mm), p.part_l[at(s)], ll);
-    for (int d = lane; d < D; d += 32) {
-        float a = 0.f;
-        for (int s = 0; s < p.n_split; ++s)
-            if (p.part_l[at(s)] != 0.f) a = fmaf(ex2_approx(p.part_m[at(s)] - mm), p.part_acc[at(s) * D + d], a);
-        p.o[static_cast<long long>(row) * D + d] = __float2bfloat16_rn(ll == 0.f ? 0.f : a / ll);
+// Joins the parts of the heads that are cut between CTAs, and writes those that
+// have no tokens.  One CTA takes two pairs of accumulators (of kPairs NT) of one
+// (sequence, head, row block), its warps in twos a quarter of the parts each.
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
+    using C = Cfg<D, G, NT>;
+    __shared__ float2 sm_o[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g4 = lane >> 2, j = lane & 3;
+    const int HR = p.pages.heads * p.RB;
+    const int b = blockIdx.x / HR, hr = blockIdx.x % HR;
+    const int head = hr / p.RB, bh = b * p.pages.heads + head;
+    const int pair = blockIdx.y * 2 + (warp & 1), nt = pair / C::kPairs, i = pair % C::kPairs;
+    const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
+    long long all, before;
+    count_units<C::kTokens>(p, lane, b, all, before);
+    const int n = (length_of(p, b) + C::kTokens - 1) / C::kTokens;
+    const long long share = share_of(p, all, HR), first = before * HR + static_cast<long long>(hr) * n;
+    const long long c0 = first / share, c1 = n == 0 ? c0 : (first + n - 1) / share;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n > 0 && c0 == c1) return;  // written by its CTA
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    float2 o = make_float2(0.f, 0.f);
+    if (n > 0) {
+        const long long slot0 = static_cast<long long>(b) * HR + hr;
+        for (long long c = c0 + (warp >> 1); c <= c1; c += 4) {
+            const float* ml = p.part_ml + ((slot0 + c) * NT + nt) * 16;
+            const float2 m = *reinterpret_cast<const float2*>(ml + 2 * j), lw = *reinterpret_cast<const float2*>(ml + 8 + 2 * j);
+            const float2 x = p.part_o[(((slot0 + c) * NT + nt) * C::kPairs + i) * 32 + lane];
+            const float ms[2] = {m.x, m.y}, ls[2] = {lw.x, lw.y}, xs[2] = {x.x, x.y};
+            float* os[2] = {&o.x, &o.y};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (ls[e] == 0.f) continue;
+                const float now = fmaxf(top[e], ms[e]);
+                const float base = now == -INFINITY ? 0.f : now;
+                const float a = sum[e] == 0.f ? 0.f : ex2_approx(top[e] - base), f = ex2_approx(ms[e] - base);
+                sum[e] = sum[e] * a + ls[e] * f;
+                *os[e] = *os[e] * a + xs[e] * f;
+                top[e] = now;
+            }
+        }
     }
-    if (lane == 0) p.lse[row] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * kLn2;
+    __shared__ float2 sm_m[8][32], sm_l[8][32];
+    sm_o[warp][lane] = o;
+    sm_m[warp][lane] = make_float2(top[0], top[1]);
+    sm_l[warp][lane] = make_float2(sum[0], sum[1]);
+    __syncthreads();
+    if (warp >= 2) return;
+    float res[2], lse[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float m = -INFINITY, ll = 0.f, oo = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, e ? sm_m[warp + 2 * w][lane].y : sm_m[warp + 2 * w][lane].x);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 mw = sm_m[warp + 2 * w][lane], lw = sm_l[warp + 2 * w][lane], ow = sm_o[warp + 2 * w][lane];
+            const float le = e ? lw.y : lw.x;
+            if (le == 0.f) continue;
+            const float f = ex2_approx((e ? mw.y : mw.x) - (m == -INFINITY ? 0.f : m));
+            ll = fmaf(f, le, ll);
+            oo = fmaf(f, e ? ow.y : ow.x, oo);
+        }
+        res[e] = ll == 0.f ? 0.f : oo / ll;
+        lse[e] = ll == 0.f ? -INFINITY : (m + __log2f(ll)) * kLn2;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (row + e >= p.R) continue;
+        p.o[(static_cast<long long>(bh) * p.R + row + e) * D + ch] = __float2bfloat16_rn(res[e]);
+        if (i == 0 && g4 == 0) p.lse[static_cast<long long>(bh) * p.R + row + e] = lse[e];
+    }
 }
 
 // weights_out = weights + the sum over the rows of P, slot by slot.
-__global__ void __launch_bounds__(256) fa_kv4_weights_kernel(DecParams p) {
+__global__ void __launch_bounds__(256) fa_kv4_weights_kernel(DecParams p, int width) {
+    __shared__ float sm_lse[1024];
     const int bh = blockIdx.y, b = bh / p.pages.heads;
     const int len = length_of(p, b);
-    for (long long t = blockIdx.x * 256 + threadIdx.x; t < len; t += gridDim.x * 256) {
+    if (static_cast<long long>(blockIdx.x) * 256 >= len) return;
+    for (int r = threadIdx.x; r < p.R; r += 256) sm_lse[r] = p.lse[static_cast<long long>(bh) * p.R + r] * kLog2e;
+    __syncthreads();
+    for (long long t = blockIdx.x * 256LL + threadIdx.x; t < len; t += gridDim.x * 256LL) {
+        const float4* s = reinterpret_cast<const float4*>(p.scores + (bh * p.cap + t) * width);
         float sum = 0.f;
-        for (int r = 0; r < p.R; ++r) {
-            const float lse = p.lse[static_cast<long long>(bh) * p.R + r];
-            if (t < seen_by(p, r, len))
-                sum += ex2_approx(p.scores[(static_cast<long long>(bh) * p.R + r) * p.cap + t] - lse * kLog2e);
+        for (int r = 0; r < p.R; r += 4) {
+            const float4 x = s[r >> 2];
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e < p.R && xs[e] != -INFINITY) sum += ex2_approx(xs[e] - sm_lse[r + e]);
         }
         const long long at = bh * p.slots + t;
         p.weights_out[at] = (p.weights != nullptr ? p.weights[at] : 0.f) + sum;
     }
 }
 
-int splits_of(const Kv4Shape& c, int num_sms) {
-    const long long bh = static_cast<long long>(c.B) * c.Hkv, cap = static_cast<long long>(c.width) * c.page_size;
-    long long n = (16LL * num_sms + bh - 1) / bh;
-    const long long most = (cap + 255) / 256;
-    if (n > most) n = most;
-    return n < 1 ? 1 : static_cast<int>(n);
+// Row tiles of a CTA: one for up to 8 query rows, two above.
+int tiles_of(int R) { return R <= 8 ? 1 : 2; }
+int ctas_of(int nt, int num_sms) { return nt == 1 ? 2 * num_sms : num_sms; }
+
+struct Sizes {
+    size_t part_o, part_ml, scores;
+};
+Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
+    const int R = Hq / c.Hkv * Tq, nt = tiles_of(R);
+    const size_t RB = (R + 8 * nt - 1) / (8 * nt), bh = static_cast<size_t>(c.B) * c.Hkv;
+    const size_t slots = ctas_of(nt, num_sms) + bh * RB;
+    return {slots * nt * c.D * 8 * 4, slots * nt * 16 * 4,
+            weights ? bh * c.width * c.page_size * RB * nt * 8 * 4 : 0};
+}
+
+template <int D, int G, int NT>
+int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) {
+    using C = Cfg<D, G, NT>;
+    static_assert(C::kSmem + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
+    if (cudaFuncSetAttribute(fa_kv4_decode_kernel<D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+        cudaSuccess)
+        return -5;
+    fa_kv4_decode_kernel<D, G, NT><<<p.n_cta, kThreads, C::kSmem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return -5;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(bh) * p.RB, C::kPairs * NT / 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fa_kv4_merge_kernel<D, G, NT>, p) != cudaSuccess) return -5;
+    if (weights) {
+        long long n = (p.cap + 255) / 256;
+        const long long most = (16LL * num_sms + bh - 1) / bh;
+        fa_kv4_weights_kernel<<<dim3(static_cast<unsigned>(n < most ? n : most), bh), 256, 0, stream>>>(p, p.RB * NT * 8);
+        if (cudaGetLastError() != cudaSuccess) return -5;
+    }
+    return 0;
 }
 
 }  // namespace
 
 size_t kv4_decode_workspace(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
-    const size_t rows = static_cast<size_t>(c.B) * Hq * Tq;
-    return rows * splits_of(c, num_sms) * (c.D + 2) * 4 +
-           (weights ? rows * static_cast<size_t>(c.width) * c.page_size * 4 : 0);
+    const Sizes s = sizes_of(c, Hq, Tq, weights, num_sms);
+    return s.part_o + s.part_ml + s.scores;
 }
 
 int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
                       void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
-                      float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms) {
+                      float* weights_out, long long slots, void* workspace, cudaStream_t stream,
+                      const DebugKnobs& dbg, int num_sms) {
     DecParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.pages.pool = static_cast<unsigned char*>(const_cast<void*>(pool));
@@ -234,43 +860,36 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
     p.pages.blocks_page = c.page_size / 16;
     p.pages.block_bytes = 16LL * (c.D + 8 * c.D / c.group);
     p.lengths = lengths;
+    p.B = c.B;
     p.R = Hq / c.Hkv * Tq;
+    const int nt = tiles_of(p.R);
+    p.RB = (p.R + 8 * nt - 1) / (8 * nt);
     p.Tq = Tq;
     p.causal = causal;
-    p.n_split = splits_of(c, num_sms);
+    p.n_cta = ctas_of(nt, num_sms);
     p.cap = static_cast<long long>(c.width) * c.page_size;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
     p.weights = weights;
     p.weights_out = weights_out;
     p.slots = slots;
+    p.timeout_ns = dbg.timeout_ns;
     p.sl2 = scale * kLog2e;
     const int bh = c.B * c.Hkv;
-    const size_t parts = static_cast<size_t>(bh) * p.n_split * p.R;
-    p.part_acc = static_cast<float*>(workspace);
-    p.part_m = p.part_acc + parts * c.D;
-    p.part_l = p.part_m + parts;
-    p.scores = weights_out != nullptr ? p.part_l + parts : nullptr;
-    const dim3 grid(p.n_split, bh, (p.R + kRows - 1) / kRows);
+    const bool w = weights_out != nullptr;
+    const Sizes s = sizes_of(c, Hq, Tq, w, num_sms);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    p.part_o = reinterpret_cast<float2*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + s.part_o);
+    p.scores = w ? reinterpret_cast<float*>(ws + s.part_o + s.part_ml) : nullptr;
     if (c.D == 64) {
-        if (c.group == 32) fa_kv4_decode_kernel<64, 32><<<grid, kWarps * 32, 0, stream>>>(p);
-        else fa_kv4_decode_kernel<64, 64><<<grid, kWarps * 32, 0, stream>>>(p);
-    } else {
-        if (c.group == 32) fa_kv4_decode_kernel<128, 32><<<grid, kWarps * 32, 0, stream>>>(p);
-        else fa_kv4_decode_kernel<128, 64><<<grid, kWarps * 32, 0, stream>>>(p);
+        if (c.group == 32)
+            return nt == 1 ? launch<64, 32, 1>(p, stream, num_sms, bh, w) : launch<64, 32, 2>(p, stream, num_sms, bh, w);
+        return nt == 1 ? launch<64, 64, 1>(p, stream, num_sms, bh, w) : launch<64, 64, 2>(p, stream, num_sms, bh, w);
     }
-    if (cudaGetLastError() != cudaSuccess) return -5;
-    const int rows = bh * p.R, blocks = (rows + 3) / 4;
-    if (c.D == 64) fa_kv4_merge_kernel<64><<<blocks, 128, 0, stream>>>(p, rows);
-    else fa_kv4_merge_kernel<128><<<blocks, 128, 0, stream>>>(p, rows);
-    if (cudaGetLastError() != cudaSuccess) return -5;
-    if (weights_out != nullptr) {
-        long long n = (p.cap + 255) / 256;
-        const long long most = (16LL * num_sms + bh - 1) / bh;
-        fa_kv4_weights_kernel<<<dim3(static_cast<unsigned>(n < most ? n : most), bh), 256, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return -5;
-    }
-    return 0;
+    if (c.group == 32)
+        return nt == 1 ? launch<128, 32, 1>(p, stream, num_sms, bh, w) : launch<128, 32, 2>(p, stream, num_sms, bh, w);
+    return nt == 1 ? launch<128, 64, 1>(p, stream, num_sms, bh, w) : launch<128, 64, 2>(p, stream, num_sms, bh, w);
 }
 
 int kv4_decode_take_status() {
