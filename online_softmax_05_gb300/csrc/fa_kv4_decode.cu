@@ -26,9 +26,13 @@
 // Bound: HBM, the cache's bytes once.  Each warp streams units of 32 or 64
 // tokens through its own ring of shared memory with bulk copies (16 tokens of a
 // head are contiguous), 8 warps per CTA and 2 CTAs per SM.  The units of all
-// sequences and heads form one line that is cut evenly over the CTAs, so ragged
-// lengths balance without the host knowing them; a head cut between CTAs is
-// joined by a second kernel.
+// sequences and heads form one line that is cut evenly over the warps, so ragged
+// lengths balance without the host knowing them.  A warp works alone: it writes
+// the heads that lie wholly in its stretch, and at the end the CTA joins the
+// pieces that its warps share, and a second kernel those that CTAs share.  (One
+// head at a time per CTA, its warps joined after each, took 85 us instead of
+// MIXED_US on 24 sequences of 1 to 8111 tokens, as a short head costs all
+// warps a barrier and the latency of its queries.)
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -74,10 +78,11 @@ struct Cfg : Kv4<D_, G_> {
     static constexpr int kUnitBytes = UB * L::kBlock;
     static constexpr int kWords = D_ / 32;          // 32-channel slices
     static constexpr int kPairs = D_ / 8;           // pairs of accumulators of a lane and row tile
-    static constexpr int kRing = kWarps * kStages * kUnitBytes;
-    static constexpr int kMergeO = kWarps * kPairs * 32 * 8;
-    static constexpr int kMergeML = kWarps * 2 * 8 * 4;
-    static constexpr int kSmem = kRing + kMergeO + kMergeML + kWarps * kStages * 8;
+    static constexpr int kRing = kStages * kUnitBytes;      // of a warp
+    static constexpr int kPieceO = NT_ * kPairs * 32 * 8;   // a warp's outputs of one head, and
+    static constexpr int kPiece = kPieceO + NT_ * 64;       // its running maxima and sums
+    static_assert(kPiece <= kRing, "the last piece goes where the ring was");
+    static constexpr int kSmem = kWarps * (kRing + kPiece + kStages * 8);
 };
 
 // Length of sequence b, 0 (and a status) if the table or the accounts cannot hold it.
@@ -96,23 +101,29 @@ __device__ __forceinline__ long long warp_sum_ll(long long x) {
     return x;
 }
 
-// Units of all sequences, and of those before sequence `upto`; per warp.
+// Places on the line that a head of sequence b takes.
 template <int TOKENS>
-__device__ __forceinline__ void count_units(const DecParams& p, int lane, int upto, long long& all, long long& before) {
+__device__ __forceinline__ int places_of(int len) {
+    return len > 0 ? (len + TOKENS - 1) / TOKENS + 1 : 0;
+}
+// Places of one head of all sequences, and of those before sequence `upto`; per warp.
+template <int TOKENS>
+__device__ __forceinline__ void count_places(const DecParams& p, int lane, int upto, long long& all, long long& before) {
     all = before = 0;
     for (int b = lane; b < p.B; b += 32) {
-        const int n = (length_of(p, b) + TOKENS - 1) / TOKENS;
+        const int n = places_of<TOKENS>(length_of(p, b));
         all += n;
         if (b < upto) before += n;
     }
     all = warp_sum_ll(all);
     before = warp_sum_ll(before);
 }
-// Units of one CTA: an even share, and at least one for each of its warps.
-__device__ __forceinline__ long long share_of(const DecParams& p, long long all_units, int heads_rows) {
-    const long long total = all_units * heads_rows;
-    const long long even = (total + p.n_cta - 1) / p.n_cta;
-    return even > kWarps ? even : kWarps;
+// The line: every (sequence, head, row block) of n > 0 units takes n + 1 places,
+// the first one for the cost of starting it.  A warp's share of the places.
+__device__ __forceinline__ long long share_of(const DecParams& p, long long places) {
+    const long long warps = static_cast<long long>(p.n_cta) * kWarps;
+    const long long even = (places + warps - 1) / warps;
+    return even > 1 ? even : 1;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -144,11 +155,16 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&x)[N]) {
                      : "r"(addr));
 }
 
-// A stretch of units of one (sequence, head, row block) inside a CTA's share.
+// A stretch of units of one (sequence, head, row block) inside a warp's share.
 struct Segment {
     int b, hr;     // hr = head * RB + row block
     int u0, u1;    // units of the sequence
     int n, len;    // units and tokens of the sequence
+};
+// What a warp leaves to be joined.
+struct Piece {
+    long long head;  // b * heads * RB + hr, or -1
+    int first, last; // whether it holds the head's first and last unit
 };
 
 // Token of row r (0..7) of a fragment: any order serves, as K and V agree; this
@@ -162,10 +178,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g4 = lane >> 2, j = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * kStages * C::kUnitBytes;
-    float2* sm_o = reinterpret_cast<float2*>(smem + C::kRing);
-    float* sm_ml = reinterpret_cast<float*>(smem + C::kRing + C::kMergeO);
-    const uint32_t bars = smem_u32(smem + C::kRing + C::kMergeO + C::kMergeML) + warp * kStages * 8;
+    const uint32_t ring = smem_u32(smem) + warp * C::kRing;
+    // where piece y (0: a warp's first, 1: its last) of warp w is left
+    auto piece_at = [&](int w, int y) -> unsigned char* {
+        return smem + (y ? w * C::kRing : kWarps * C::kRing + w * C::kPiece);
+    };
+    const uint32_t bars = smem_u32(smem) + kWarps * (C::kRing + C::kPiece) + warp * kStages * 8;
+    __shared__ Piece s_piece[kWarps][2];
     const int HR = p.pages.heads * p.RB;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -173,26 +192,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
         for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
         fence_mbar_init();
+        s_piece[warp][0].head = s_piece[warp][1].head = -1;
     }
     __syncwarp();
 
-    // this CTA's share of the line of units, found by one warp for all: every
-    // warp walks the same segments whatever else happens to the lengths
-    __shared__ Segment s_seg[2];
-    __shared__ long long s_left;
-    if (warp == 0) {
-        Segment seg{0, 0, 0, 0, 0, 0};
+    // this warp's share of the line; from place `skip` of its first head on
+    Segment seg{0, 0, 0, 0, 0, 0};
+    long long left = 0;
+    {
         long long all, unused;
-        count_units<C::kTokens>(p, lane, 0, all, unused);
-        const long long share = share_of(p, all, HR), total = all * HR;
-        const long long first = blockIdx.x * share;
-        long long left = min(share, total - first);
-        long long base = 0;     // units before the chunk of sequences
-        bool found = false;
-        for (int b0 = 0; b0 < p.B && left > 0; b0 += 32) {
+        count_places<C::kTokens>(p, lane, 0, all, unused);
+        const long long total = all * HR, share = share_of(p, total);
+        const long long first = (blockIdx.x * static_cast<long long>(kWarps) + warp) * share;
+        long long base = 0;  // places of one head before the chunk of sequences
+        for (int b0 = 0; b0 < p.B && first < total; b0 += 32) {
             const int b = b0 + lane;
             const int len = b < p.B ? length_of(p, b) : 0;
-            const int n = (len + C::kTokens - 1) / C::kTokens;
+            const int n = places_of<C::kTokens>(len);
             long long sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -202,27 +218,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             const unsigned hit = __ballot_sync(0xffffffffu, (base + sum) * HR > first);
             if (hit != 0) {
                 const int src = __ffs(hit) - 1;
+                const int places = __shfl_sync(0xffffffffu, n, src);
+                const long long rem = first - (base + __shfl_sync(0xffffffffu, sum, src) - places) * HR;
                 seg.b = b0 + src;
                 seg.len = __shfl_sync(0xffffffffu, len, src);
-                seg.n = __shfl_sync(0xffffffffu, n, src);
-                const long long rem = first - (base + __shfl_sync(0xffffffffu, sum, src) - seg.n) * HR;
-                seg.hr = static_cast<int>(rem / seg.n);
-                seg.u0 = static_cast<int>(rem % seg.n);
-                seg.u1 = static_cast<int>(min(static_cast<long long>(seg.n), seg.u0 + left));
-                found = true;
+                seg.n = places - 1;
+                seg.hr = static_cast<int>(rem / places);
+                const int place = static_cast<int>(rem % places);
+                left = min(share, total - first);
+                seg.u0 = max(place - 1, 0);
+                seg.u1 = static_cast<int>(min(static_cast<long long>(seg.n), place + left - 1));
+                left -= seg.u1 + 1 - place;
                 break;
             }
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (lane == 0) {
-            s_seg[0] = seg;
-            s_left = found ? left : 0;
-        }
     }
-    __syncthreads();
-    Segment seg = s_seg[0];
-    long long left = s_left;
-    if (left <= 0) return;  // whole CTA
+    // the head after `s` and its places in what is left of the share; false at the end
+    auto advance = [&](Segment& s) -> bool {
+        if (left <= 0) return false;
+        s.u0 = 0;
+        if (++s.hr == HR) {
+            s.hr = 0;
+            do {
+                if (++s.b >= p.B) return false;
+                s.len = length_of(p, s.b);
+                s.n = places_of<C::kTokens>(s.len) - 1;
+            } while (s.n < 0);
+        }
+        s.u1 = static_cast<int>(min(static_cast<long long>(s.n), left - 1));
+        left -= s.u1 + 1;
+        return s.u1 > 0;
+    };
+    // a share may begin with the place of a head's start alone
+    bool working = seg.u1 > seg.u0;
+    if (!working && left > 0) working = advance(seg);
 
     // copies of one unit into a stage of this warp's ring; returns the blocks that have a page
     const uint64_t policy = l2_policy_evict_first();
@@ -255,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     auto prologue = [&](const Segment& s) {
 #pragma unroll
         for (int i = 0; i < kStages; ++i) {
-            const int u = s.u0 + warp + i * kWarps;
+            const int u = s.u0 + i;
             if (u < s.u1 && !dead) {
                 const int stage = issued % kStages;
                 masks = (masks & ~(0xffu << (8 * stage))) | issue(s, u, stage) << (8 * stage);
@@ -271,12 +301,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         }
         return true;
     };
-    prologue(seg);
+    if (working) prologue(seg);
 
     const int tokA = token_of(g4), tokB = 8 + tokA;
-    int parity = 0;
-    for (;;) {
-        left -= seg.u1 - seg.u0;
+    while (working) {
         const int head = seg.hr / p.RB, rb = seg.hr % p.RB;
         const int bh = seg.b * p.pages.heads + head;
         const int row0 = rb * NT * 8;
@@ -369,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             ref[nt][0] = ref[nt][1] = -INFINITY;
         }
 
-        for (int u = seg.u0 + warp; u < seg.u1; u += kWarps) {
+        for (int u = seg.u0; u < seg.u1; ++u) {
             const int stage = taken % kStages;
             if (!dead && !__all_sync(0xffffffffu, wait(stage, (taken / kStages) & 1))) {
                 report(kStatusTimeout);
@@ -451,22 +479,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             }
 
             // ---- value scales, running maxima
-            float2 va[C::UB][C::kGroups], vb[C::UB][C::kGroups];
+            uint32_t va[C::UB][C::kGroups], vb[C::UB][C::kGroups];
             float vtop = 0.f;
 #pragma unroll
             for (int ub = 0; ub < C::UB; ++ub) {
                 const uint32_t blk = unit + ub * C::kBlock;
-                uint32_t pa[C::kGroups], pb[C::kGroups];
-                lds(blk + C::kValueScales + tokA * C::kScaleRow, pa);
-                lds(blk + C::kValueScales + tokB * C::kScaleRow, pb);
+                lds(blk + C::kValueScales + tokA * C::kScaleRow, va[ub]);
+                lds(blk + C::kValueScales + tokB * C::kScaleRow, vb[ub]);
                 const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
 #pragma unroll
                 for (int g = 0; g < C::kGroups; ++g) {
-                    if (edge && (!(valid >> ub & 1) || ta >= seg.len)) pa[g] = 0;
-                    if (edge && (!(valid >> ub & 1) || tb >= seg.len)) pb[g] = 0;
-                    va[ub][g] = kv4_scale(pa[g]);
-                    vb[ub][g] = kv4_scale(pb[g]);
-                    vtop = fmaxf(vtop, fmaxf(va[ub][g].x, vb[ub][g].x));
+                    if (edge && (!(valid >> ub & 1) || ta >= seg.len)) va[ub][g] = 0;
+                    if (edge && (!(valid >> ub & 1) || tb >= seg.len)) vb[ub][g] = 0;
+                    vtop = fmaxf(vtop, fmaxf(kv4_scale(va[ub][g]).x, kv4_scale(vb[ub][g]).x));
                 }
             }
             float mx[NT][2];
@@ -546,13 +571,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                 for (int g = 0; g < C::kGroups; ++g) {
                     uint32_t b0[NT], b1[NT];
-                    const float ka = va[ub][g].x * inv_cap, kb = vb[ub][g].x * inv_cap;
+                    const float2 wa = kv4_scale(va[ub][g]), wb = kv4_scale(vb[ub][g]);
+                    const float ka = wa.x * inv_cap, kb = wb.x * inv_cap;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* q = s[ub][nt];
                         float w0 = q[0] * ka, w1 = q[1] * ka, w2 = q[2] * kb, w3 = q[3] * kb;
-                        float m0 = q[0] * va[ub][g].y, m1 = q[1] * va[ub][g].y;
-                        float m2 = q[2] * vb[ub][g].y, m3 = q[3] * vb[ub][g].y;
+                        float m0 = q[0] * wa.y, m1 = q[1] * wa.y;
+                        float m2 = q[2] * wb.y, m3 = q[3] * wb.y;
                         if (edge) {
                             // a token hidden from a row adds nothing to it, whatever its scale holds
                             const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
@@ -583,38 +609,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 }
             }
             __syncwarp();  // every lane has read the stage
-            const int ahead = u + kStages * kWarps;
+            const int ahead = u + kStages;
             if (ahead < seg.u1) {
                 masks = (masks & ~(0xffu << (8 * stage))) | issue(seg, ahead, stage) << (8 * stage);
                 ++issued;
             }
         }
 
-        // ---- the next segment's first copies run while this one is joined
-        parity ^= 1;
-        if (warp == 0) {
-            Segment next = seg;
-            next.u0 = 0;
-            if (left > 0 && ++next.hr == HR) {
-                next.hr = 0;
-                do {
-                    ++next.b;
-                    next.len = next.b < p.B ? length_of(p, next.b) : 1;
-                    next.n = (next.len + C::kTokens - 1) / C::kTokens;
-                } while (next.n == 0);
-            }
-            next.u1 = static_cast<int>(min(static_cast<long long>(next.n), left));
-            if (next.b >= p.B) next.u1 = 0;
-            if (lane == 0) s_seg[parity] = next;
+        // ---- sums over the lanes; the next head's first copies run meanwhile
+        Segment next = seg;
+        working = advance(next);
+        if (working) prologue(next);
+        const bool first = seg.u0 == 0, last = seg.u1 == seg.n;
+        const float unit_o = cap * 1024.f;  // 2^24 of the codes over the 2^14 of P
+        // a head that ends here and began before, or goes on behind this warp's share
+        Piece* piece = &s_piece[warp][working ? 0 : 1];
+        float2* out = reinterpret_cast<float2*>(piece_at(warp, working ? 0 : 1));
+        float* ml = reinterpret_cast<float*>(piece_at(warp, working ? 0 : 1) + C::kPieceO);
+        if (!(first && last) && lane == 0) {
+            piece->head = static_cast<long long>(seg.b) * HR + seg.hr;
+            piece->first = first;
+            piece->last = last;
         }
-        __syncthreads();
-        const Segment next = s_seg[parity];
-        const bool more_segments = next.u1 > 0;
-        if (more_segments) prologue(next);
-
-        // ---- join the warps: running maxima and sums, then outputs
-        const bool whole = seg.u0 == 0 && seg.u1 == seg.n;
-        const long long slot = blockIdx.x + static_cast<long long>(seg.b) * HR + seg.hr;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -626,76 +642,110 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) om[nt][g][c] += __shfl_xor_sync(0xffffffffu, om[nt][g][c], o);
             }
-            const float unit_o = cap * 1024.f;  // 2^24 of the codes over the 2^14 of P
+            const int row = row0 + nt * 8 + 2 * j;
+            const float n0 = l[nt][0] == 0.f ? 0.f : 1.f / l[nt][0], n1 = l[nt][1] == 0.f ? 0.f : 1.f / l[nt][1];
 #pragma unroll
             for (int w = 0; w < C::kWords; ++w)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float k = i & 1 ? unit_o * 0.0625f : unit_o;
-                    sm_o[(warp * C::kPairs + w * 4 + i) * 32 + lane] =
-                        make_float2(fmaf(acc[nt][w][i >> 1][2 * (i & 1)], k, om[nt][w * 32 / G][0]),
-                                    fmaf(acc[nt][w][i >> 1][2 * (i & 1) + 1], k, om[nt][w * 32 / G][1]));
+                    const float x0 = fmaf(acc[nt][w][i >> 1][2 * (i & 1)], k, om[nt][w * 32 / G][0]);
+                    const float x1 = fmaf(acc[nt][w][i >> 1][2 * (i & 1) + 1], k, om[nt][w * 32 / G][1]);
+                    if (first && last) {
+                        __nv_bfloat16* to = p.o + (static_cast<long long>(bh) * p.R + row) * D + 32 * w + 4 * g4 + i;
+                        if (row < p.R) to[0] = __float2bfloat16_rn(x0 * n0);
+                        if (row + 1 < p.R) to[D] = __float2bfloat16_rn(x1 * n1);
+                    } else {
+                        out[(nt * C::kPairs + w * 4 + i) * 32 + lane] = make_float2(x0, x1);
+                    }
                 }
             if (g4 == 0) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    sm_ml[warp * 16 + 2 * j + c] = ref[nt][c];
-                    sm_ml[warp * 16 + 8 + 2 * j + c] = l[nt][c];
+                    if (!(first && last)) {
+                        ml[nt * 16 + 2 * j + c] = ref[nt][c];
+                        ml[nt * 16 + 8 + 2 * j + c] = l[nt][c];
+                    } else if (row + c < p.R) {
+                        p.lse[static_cast<long long>(bh) * p.R + row + c] =
+                            l[nt][c] == 0.f ? -INFINITY : (ref[nt][c] + __log2f(l[nt][c])) * kLn2;
+                    }
                 }
             }
-            __syncthreads();
-            float f[kWarps][2], top[2], sum[2];
+        }
+        seg = next;
+    }
+    // a copy that was late still writes to this CTA's memory: give it the same time again
+    if (dead)
+        while (taken < issued && __all_sync(0xffffffffu, wait(taken % kStages, (taken / kStages) & 1))) ++taken;
+
+    // ---- join the pieces that this CTA's warps share: they stand in the line's order
+    __syncthreads();
+    for (int i = 0; i < 2 * kWarps;) {
+        const long long at = s_piece[i >> 1][i & 1].head;
+        if (at < 0) {
+            ++i;
+            continue;
+        }
+        int end = i + 1;  // behind the last piece of this head
+        for (int x = end; x < 2 * kWarps; ++x) {
+            const long long y = s_piece[x >> 1][x & 1].head;
+            if (y >= 0 && y != at) break;
+            if (y == at) end = x + 1;
+        }
+        const bool whole = s_piece[i >> 1][i & 1].first && s_piece[(end - 1) >> 1][(end - 1) & 1].last;
+        const int hr = static_cast<int>(at % HR);
+        const long long bh = at / HR * p.pages.heads + hr / p.RB;
+        const long long slot = blockIdx.x + at;
+        for (int x = warp; x < NT * C::kPairs; x += kWarps) {
+            const int nt = x / C::kPairs, pr = x % C::kPairs;
+            const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j;
+            float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+            for (int y = i; y < end; ++y) {
+                if (s_piece[y >> 1][y & 1].head != at) continue;
+                const float* ml = reinterpret_cast<const float*>(piece_at(y >> 1, y & 1) + C::kPieceO) + nt * 16;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                top[c] = -INFINITY;
-                sum[c] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top[c] = fmaxf(top[c], sm_ml[w * 16 + 2 * j + c]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float lw = sm_ml[w * 16 + 8 + 2 * j + c];
-                    f[w][c] = lw == 0.f ? 0.f : ex2_approx(sm_ml[w * 16 + 2 * j + c] - top[c]);
-                    sum[c] = fmaf(f[w][c], lw, sum[c]);
+                for (int c = 0; c < 2; ++c) top[c] = fmaxf(top[c], ml[2 * j + c]);
+            }
+            float2 o = make_float2(0.f, 0.f);
+            for (int y = i; y < end; ++y) {
+                if (s_piece[y >> 1][y & 1].head != at) continue;
+                const unsigned char* from = piece_at(y >> 1, y & 1);
+                const float* ml = reinterpret_cast<const float*>(from + C::kPieceO) + nt * 16;
+                const float2 v = reinterpret_cast<const float2*>(from)[x * 32 + lane];
+                const float l0 = ml[8 + 2 * j], l1 = ml[8 + 2 * j + 1];
+                if (l0 != 0.f) {
+                    const float f = ex2_approx(ml[2 * j] - top[0]);
+                    sum[0] = fmaf(f, l0, sum[0]);
+                    o.x = fmaf(f, v.x, o.x);
+                }
+                if (l1 != 0.f) {
+                    const float f = ex2_approx(ml[2 * j + 1] - top[1]);
+                    sum[1] = fmaf(f, l1, sum[1]);
+                    o.y = fmaf(f, v.y, o.y);
                 }
             }
-            const int row = row0 + nt * 8 + 2 * j;
-            for (int i = warp; i < C::kPairs; i += kWarps) {
-                float2 o = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 x = sm_o[(w * C::kPairs + i) * 32 + lane];
-                    if (f[w][0] != 0.f) o.x = fmaf(f[w][0], x.x, o.x);
-                    if (f[w][1] != 0.f) o.y = fmaf(f[w][1], x.y, o.y);
-                }
-                if (whole) {
-                    const int ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
-                    __nv_bfloat16* to = p.o + (static_cast<long long>(bh) * p.R + row) * D + ch;
-                    if (row < p.R) to[0] = __float2bfloat16_rn(sum[0] == 0.f ? 0.f : o.x / sum[0]);
-                    if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum[1] == 0.f ? 0.f : o.y / sum[1]);
-                } else {
-                    p.part_o[((slot * NT + nt) * C::kPairs + i) * 32 + lane] = o;
-                }
+            if (!whole) {
+                p.part_o[(slot * NT * C::kPairs + x) * 32 + lane] = o;
+            } else {
+                const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
+                __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
+                if (row < p.R) to[0] = __float2bfloat16_rn(sum[0] == 0.f ? 0.f : o.x / sum[0]);
+                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum[1] == 0.f ? 0.f : o.y / sum[1]);
             }
-            if (warp == 0 && g4 == 0) {
+            if (pr == 0 && g4 == 0) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (!whole) {
                         p.part_ml[(slot * NT + nt) * 16 + 2 * j + c] = top[c];
                         p.part_ml[(slot * NT + nt) * 16 + 8 + 2 * j + c] = sum[c];
                     } else if (row + c < p.R) {
-                        p.lse[static_cast<long long>(bh) * p.R + row + c] =
-                            sum[c] == 0.f ? -INFINITY : (top[c] + __log2f(sum[c])) * kLn2;
+                        p.lse[bh * p.R + row + c] = sum[c] == 0.f ? -INFINITY : (top[c] + __log2f(sum[c])) * kLn2;
                     }
                 }
             }
-            __syncthreads();  // the buffers are free again
         }
-        if (!more_segments) break;
-        seg = next;
+        i = end;
     }
-    // a copy that was late still writes to this CTA's memory: give it the same time again
-    if (dead)
-        while (taken < issued && __all_sync(0xffffffffu, wait(taken % kStages, (taken / kStages) & 1))) ++taken;
 }
 
 // Joins the parts of the heads that are cut between CTAs, and writes those that
@@ -713,9 +763,10 @@ __global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
     const int pair = blockIdx.y * 2 + (warp & 1), nt = pair / C::kPairs, i = pair % C::kPairs;
     const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
     long long all, before;
-    count_units<C::kTokens>(p, lane, b, all, before);
-    const int n = (length_of(p, b) + C::kTokens - 1) / C::kTokens;
-    const long long share = share_of(p, all, HR), first = before * HR + static_cast<long long>(hr) * n;
+    count_places<C::kTokens>(p, lane, b, all, before);
+    const int n = max(places_of<C::kTokens>(length_of(p, b)) - 1, 0);
+    const long long share = share_of(p, all * HR) * kWarps;
+    const long long first = before * HR + static_cast<long long>(hr) * (n + 1) + 1;  // the first unit's place
     const long long c0 = first / share, c1 = n == 0 ? c0 : (first + n - 1) / share;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n > 0 && c0 == c1) return;  // written by its CTA
@@ -814,7 +865,7 @@ Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
 template <int D, int G, int NT>
 int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) {
     using C = Cfg<D, G, NT>;
-    static_assert(C::kSmem + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
+    static_assert(C::kSmem + 2 * kWarps * static_cast<int>(sizeof(Piece)) + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
     if (cudaFuncSetAttribute(fa_kv4_decode_kernel<D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
         cudaSuccess)
         return -5;
