@@ -277,7 +277,7 @@ int fa_rope(const fa_rope_tensor* tensors, int n_tensors, const void* positions,
  *                  block_table[b][t / page_size].  Entries behind the length
  *                  are not read.
  *   lengths    in: DEVICE int32[B], tokens held by each sequence (may be 0)
- *   D: 64 or 128; group: 32 or 64; page_size: a multiple of 16;
+ *   D: 64 or 128; group: 32 or 64; page_size: a multiple of 16 up to 65536;
  *   B * Hkv <= 65535; width * page_size slots at most per sequence.
  * A length the table cannot hold (or negative) is recorded as FA_ERR_SEQLEN and
  * that sequence counts as empty; a table entry outside the pool, where a token

@@ -353,7 +353,8 @@ int check_kv4(const fa_kv4_cache* c) {
     if (static_cast<long long>(c->width) * c->page_size > INT_MAX - 65536) return FA_ERR_SHAPE;
     if (static_cast<long long>(c->B) * c->width > INT_MAX) return FA_ERR_SHAPE;
     if (c->D != 64 && c->D != 128) return FA_ERR_UNSUPPORTED;
-    if ((c->group != 32 && c->group != 64) || c->page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+    if ((c->group != 32 && c->group != 64) || c->page_size % 16 != 0 || c->page_size > 65536)
+        return FA_ERR_UNSUPPORTED;
     if (!aligned16(c->pool) || (reinterpret_cast<uintptr_t>(c->block_table) & 3u) ||
         (reinterpret_cast<uintptr_t>(c->lengths) & 3u))
         return FA_ERR_ALIGN;
@@ -516,7 +517,7 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
     if (rc != FA_OK) return rc;
     rc = fa::launch_kv4_decode(shape, cache->pool, cache->block_table, cache->lengths, q, o, lse, Hq, Tq, scale,
                                causal != 0, weights, weights_out, slots, ws.ptr, static_cast<cudaStream_t>(stream),
-                               knobs(), sms);
+                               sms);
     return ws.release(rc);
 }
 

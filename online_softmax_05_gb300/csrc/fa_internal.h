@@ -79,8 +79,7 @@ int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int*
 size_t kv4_decode_workspace(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms);
 int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
                       void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
-                      float* weights_out, long long slots, void* workspace, cudaStream_t stream,
-                      const DebugKnobs& dbg, int num_sms);
+                      float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms);
 int kv4_cache_take_status();
 int kv4_decode_take_status();
 

@@ -24,8 +24,8 @@
 // a read of 4 times the cache's bytes) and uses 8 of its 128 rows.
 //
 // Bound: HBM, the cache's bytes once.  Each warp streams units of 32 or 64
-// tokens through its own ring of shared memory with bulk copies (16 tokens of a
-// head are contiguous), 8 warps per CTA and 2 CTAs per SM.  The units of all
+// tokens through its own ring of shared memory with asynchronous copies (16 tokens
+// of a head are contiguous), 8 warps per CTA and 2 CTAs per SM.  The units of all
 // sequences and heads form one line that is cut evenly over the warps, so ragged
 // lengths balance without the host knowing them.  A warp works alone: it writes
 // the heads that lie wholly in its stretch, and at the end the CTA joins the
@@ -52,6 +52,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
+// The exponent's reference is set this far above the largest score so far (log2
+// units), so that it seldom moves again.  P times a value scale goes to fp16 at
+// up to 2^14, so what is 2^-23 of the largest still has all of its bits.
+constexpr float kAhead = 4.f;
 
 struct DecParams {
     const __nv_bfloat16* q;
@@ -65,7 +69,6 @@ struct DecParams {
     const float* weights;
     float* weights_out;
     long long slots, cap;
-    unsigned long long timeout_ns;
     int B, R, RB, Tq, causal, n_cta;
     float sl2;  // scale log2(e)
 };
@@ -82,7 +85,7 @@ struct Cfg : Kv4<D_, G_> {
     static constexpr int kPieceO = NT_ * kPairs * 32 * 8;   // a warp's outputs of one head, and
     static constexpr int kPiece = kPieceO + NT_ * 64;       // its running maxima and sums
     static_assert(kPiece <= kRing, "the last piece goes where the ring was");
-    static constexpr int kSmem = kWarps * (kRing + kPiece + kStages * 8);
+    static constexpr int kSmem = kWarps * (kRing + kPiece);
 };
 
 // Length of sequence b, 0 (and a status) if the table or the accounts cannot hold it.
@@ -133,6 +136,27 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// C = A B for bf16 A (16 x 16) and B (16 x 8), and for A (16 x 8) and B (8 x 8).
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -141,6 +165,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16 bytes from global to shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A power of two: 2^k as the product of two fp32 numbers, |k| <= 250.
+__device__ __forceinline__ float2 pow2_parts(int k) {
+    const int a = k / 2;
+    return make_float2(__int_as_float((a + 127) << 23), __int_as_float((k - a + 127) << 23));
 }
 
 // N 32-bit words from shared memory in one load.
@@ -183,18 +224,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     auto piece_at = [&](int w, int y) -> unsigned char* {
         return smem + (y ? w * C::kRing : kWarps * C::kRing + w * C::kPiece);
     };
-    const uint32_t bars = smem_u32(smem) + kWarps * (C::kRing + C::kPiece) + warp * kStages * 8;
     __shared__ Piece s_piece[kWarps][2];
     const int HR = p.pages.heads * p.RB;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
-        fence_mbar_init();
-        s_piece[warp][0].head = s_piece[warp][1].head = -1;
-    }
-    __syncwarp();
+    if (lane == 0) s_piece[warp][0].head = s_piece[warp][1].head = -1;
 
     // this warp's share of the line; from place `skip` of its first head on
     Segment seg{0, 0, 0, 0, 0, 0};
@@ -254,52 +288,72 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     bool working = seg.u1 > seg.u0;
     if (!working && left > 0) working = advance(seg);
 
-    // copies of one unit into a stage of this warp's ring; returns the blocks that have a page
-    const uint64_t policy = l2_policy_evict_first();
-    auto issue = [&](const Segment& s, int u, int stage) -> uint32_t {
-        long long at = -1;
-        const int blk = u * C::UB + lane;
-        if (lane < C::UB && blk * 16 < s.len) {
-            at = p.pages.block_of(s.b, blk);
-            if (at < 0) report(kStatusBadPage);
+    // The next block to be copied, walked page by page, so that a table entry is
+    // read once a page.  (Bulk copies, one per block and with a barrier per
+    // stage, cost three times these instructions: their operands are uniform, so
+    // two lanes' copies are a loop.)
+    const int per_page = p.pages.blocks_page;
+    const uint64_t policy = p.RB == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    int walk_left = 0, walk_page = 0, walk_in = 0;  // blocks left; page of the table; block in the page
+    const unsigned char* walk_from = nullptr;       // that block of the head, this lane's 16 bytes; null: no page
+    const int* walk_table = nullptr;
+    long long walk_head = 0;
+    auto look_up = [&]() {
+        walk_from = nullptr;
+        if (walk_left > 0 && walk_page < p.pages.width) {
+            const int page = walk_table[walk_page];
+            if (page >= 0 && page < p.pages.num_pages)
+                walk_from = p.pages.pool + page * (p.pages.head_bytes() * p.pages.heads) + walk_head;
         }
-        const uint32_t valid = __ballot_sync(0xffffffffu, at >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, __popc(valid) * C::kBlock);
-        __syncwarp();
-        if (at >= 0) {
-            const unsigned char* src = p.pages.pool + at + static_cast<long long>(s.hr / p.RB) * p.pages.head_bytes();
-            const uint32_t dst = ring + stage * C::kUnitBytes + lane * C::kBlock;
-            if (p.RB == 1)
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-                    "l"(src), "r"(C::kBlock), "r"(bars + 8 * stage), "l"(policy)
-                    : "memory");
-            else
-                bulk_load_1d(dst, src, C::kBlock, bars + 8 * stage);
+    };
+    auto walk_to = [&](const Segment& s) {
+        const int block = s.u0 * C::UB;
+        walk_left = (s.len + 15) / 16 - block;
+        walk_page = block / per_page;
+        walk_in = block - walk_page * per_page;
+        walk_table = p.pages.table + static_cast<long long>(s.b) * p.pages.width;
+        walk_head = s.hr / p.RB * p.pages.head_bytes() + lane * 16;
+        look_up();
+        if (walk_from != nullptr) walk_from += walk_in * C::kBlock;
+    };
+    // copies a unit into a stage of this warp's ring; returns the blocks that have a page
+    auto issue = [&](int stage) -> uint32_t {
+        uint32_t valid = 0;
+        uint32_t dst = ring + stage * C::kUnitBytes + lane * 16;
+#pragma unroll
+        for (int ub = 0; ub < C::UB; ++ub, dst += C::kBlock) {
+            if (walk_left > 0) {
+                if (walk_from != nullptr) {
+                    valid |= 1u << ub;
+#pragma unroll
+                    for (int x = 0; x < C::kBlock; x += 512)
+                        if (x + 512 <= C::kBlock || lane * 16 < C::kBlock - x) copy16(dst + x, walk_from + x, policy);
+                    walk_from += C::kBlock;
+                } else if (lane == 0) {
+                    report(kStatusBadPage);
+                }
+                --walk_left;
+                if (++walk_in == per_page) {
+                    walk_in = 0;
+                    ++walk_page;
+                    look_up();
+                }
+            }
         }
         return valid;
     };
     uint32_t masks = 0;  // 8 bits of each stage: its blocks with a page
-    int issued = 0, taken = 0;
-    bool dead = false;   // a copy did not arrive in time
+    int stage = 0;       // of the next unit to be used
+    // the first units of a segment; one group of copies per stage, empty or not
     auto prologue = [&](const Segment& s) {
+        walk_to(s);
+        masks = 0;
+        stage = 0;
 #pragma unroll
         for (int i = 0; i < kStages; ++i) {
-            const int u = s.u0 + i;
-            if (u < s.u1 && !dead) {
-                const int stage = issued % kStages;
-                masks = (masks & ~(0xffu << (8 * stage))) | issue(s, u, stage) << (8 * stage);
-                ++issued;
-            }
+            if (s.u0 + i < s.u1) masks |= issue(i) << (8 * i);
+            copy_commit();
         }
-    };
-    auto wait = [&](int stage, uint32_t phase) -> bool {
-        if (mbar_try_wait(bars + 8 * stage, phase)) return true;
-        const uint64_t begin = globaltimer_ns();
-        while (!mbar_try_wait_sleep(bars + 8 * stage, phase, 20000)) {
-            if (globaltimer_ns() - begin > p.timeout_ns) return false;
-        }
-        return true;
     };
     if (working) prologue(seg);
 
@@ -311,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 
         // ---- queries: operand fragments, group sums and score factors
         uint32_t qf[NT][C::kWords][4];
-        float qs[NT][C::kGroups][2], factor[NT][2];
+        uint32_t qs[NT][(C::kGroups + 1) / 2];
+        float factor[NT][2];
         int seen[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -338,9 +393,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 finite = __shfl_xor_sync(0xffffffffu, finite, o) && finite;
             }
-            // 2^e <= top < 2^(e+1) goes to 2^14; two exact steps, as 2^(14-e) alone may leave fp32
+            // 2^e <= top < 2^(e+1) goes to 2^14, in two exact steps, as 2^(14-e) alone may leave fp32
             const int e = top > 0.f && finite ? ilogbf(top) : 0;
-            const float up1 = exp2f(static_cast<float>((14 - e) / 2)), up2 = exp2f(static_cast<float>(14 - e - (14 - e) / 2));
+            const float2 up = pow2_parts(14 - e), down = pow2_parts(10 + e);
+            const float sign = p.sl2 < 0.f ? -up.x : p.sl2 == 0.f ? 0.f : up.x;
             float group[C::kGroups];
 #pragma unroll
             for (int g = 0; g < C::kGroups; ++g) group[g] = 0.f;
@@ -350,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = __uint_as_float(word[i] << 16) * up1 * up2;
-                    x[2 * i + 1] = __uint_as_float(word[i] & 0xffff0000u) * up1 * up2;
+                    x[2 * i] = __uint_as_float(word[i] << 16) * sign * up.y;
+                    x[2 * i + 1] = __uint_as_float(word[i] & 0xffff0000u) * sign * up.y;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) group[w * 32 / G] += x[i];
@@ -360,18 +416,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 qf[nt][w][2] = pack_f16(x[2], x[6]);
                 qf[nt][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
             }
-            const float back = finite ? p.sl2 * exp2f(static_cast<float>((10 + e) / 2)) *
-                                            exp2f(static_cast<float>(10 + e - (10 + e) / 2))
-                                      : NAN;
+            // a positive factor: its sign went into q, and a scale of 0 made q zero
+            const float back = !finite ? NAN : p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * down.x * down.y;
 #pragma unroll
             for (int g = 0; g < C::kGroups; ++g) {
                 float s = group[g];
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
                 s *= 5.9604644775390625e-8f;  // 2^-24, the codes' unit
-                qs[nt][g][0] = __shfl_sync(0xffffffffu, s, 8 * j);
-                qs[nt][g][1] = __shfl_sync(0xffffffffu, s, 8 * j + 4);
+                // the lane's piece of it: three bf16 pieces hold all 24 bits, lane j = 0, 1, 2 one each
+                const float hi = __bfloat162float(__float2bfloat16_rn(s)), rest = s - hi;
+                const float mid = __bfloat162float(__float2bfloat16_rn(rest));
+                group[g] = j == 0 ? hi : j == 1 ? mid : j == 2 ? rest - mid : 0.f;
             }
+            if constexpr (C::kGroups == 1) qs[nt][0] = pack_bf16x2(group[0], 0.f);
+            else
+#pragma unroll
+                for (int g = 0; g < C::kGroups; g += 2) qs[nt][g / 2] = pack_bf16x2(group[g], group[g + 1]);
             factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * j);
             factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * j + 4);
 #pragma unroll
@@ -398,13 +459,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         }
 
         for (int u = seg.u0; u < seg.u1; ++u) {
-            const int stage = taken % kStages;
-            if (!dead && !__all_sync(0xffffffffu, wait(stage, (taken / kStages) & 1))) {
-                report(kStatusTimeout);
-                dead = true;
-            }
-            if (dead) break;
-            ++taken;
+            copy_wait<kStages - 1>();
+            __syncwarp();
             const uint32_t unit = ring + stage * C::kUnitBytes;
             const uint32_t valid = masks >> (8 * stage) & 0xffu;
             const int t0 = u * C::kTokens;
@@ -421,41 +477,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 lds(blk + C::kKeyCodes + tokB * C::kRow + j * (C::kWords * 4), xb);
                 lds(blk + C::kKeyScales + tokA * C::kScaleRow, pa);
                 lds(blk + C::kKeyScales + tokB * C::kScaleRow, pb);
+                // the minima: sum_g m_tg sum(q_g), slots of the product: lane j's piece of the sums
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[ub][nt][c] = 0.f;
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (C::kGroups == 1)
+                        mma_bf16_zero(s[ub][nt], pa[0] >> 16, pb[0] >> 16, qs[nt][0]);
+                    else if constexpr (C::kGroups == 2)
+                        mma_bf16_zero(s[ub][nt], __byte_perm(pa[0], pa[1], 0x7632), __byte_perm(pb[0], pb[1], 0x7632),
+                                      qs[nt][0]);
+                    else
+                        mma_bf16_zero(s[ub][nt], __byte_perm(pa[0], pa[1], 0x7632), __byte_perm(pb[0], pb[1], 0x7632),
+                                      __byte_perm(pa[2], pa[3], 0x7632), __byte_perm(pb[2], pb[3], 0x7632), qs[nt][0],
+                                      qs[nt][1]);
+                }
 #pragma unroll
                 for (int g = 0; g < C::kGroups; ++g) {
                     float d[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) d[nt][c] = 0.f;
 #pragma unroll
                     for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
                         const uint32_t ya = xa[w] >> 8, yb = xb[w] >> 8;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(d[nt], xa[w] & 0x000f000fu, xb[w] & 0x000f000fu, xa[w] & 0x00f000f0u,
-                                    xb[w] & 0x00f000f0u, qf[nt][w][0], qf[nt][w][1]);
+                            if (w == g * (G / 32))
+                                mma_f16_zero(d[nt], xa[w] & 0x000f000fu, xb[w] & 0x000f000fu, xa[w] & 0x00f000f0u,
+                                             xb[w] & 0x00f000f0u, qf[nt][w][0], qf[nt][w][1]);
+                            else
+                                mma_f16(d[nt], xa[w] & 0x000f000fu, xb[w] & 0x000f000fu, xa[w] & 0x00f000f0u,
+                                        xb[w] & 0x00f000f0u, qf[nt][w][0], qf[nt][w][1]);
                             mma_f16(d[nt], ya & 0x000f000fu, yb & 0x000f000fu, ya & 0x00f000f0u, yb & 0x00f000f0u,
                                     qf[nt][w][2], qf[nt][w][3]);
                         }
                     }
-                    const float2 sa = kv4_scale(pa[g]), sb = kv4_scale(pb[g]);
+                    const float sa = kv4_scale(pa[g]).x, sb = kv4_scale(pb[g]).x;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        s[ub][nt][0] = fmaf(sa.x, d[nt][0], fmaf(sa.y, qs[nt][g][0], s[ub][nt][0]));
-                        s[ub][nt][1] = fmaf(sa.x, d[nt][1], fmaf(sa.y, qs[nt][g][1], s[ub][nt][1]));
-                        s[ub][nt][2] = fmaf(sb.x, d[nt][2], fmaf(sb.y, qs[nt][g][0], s[ub][nt][2]));
-                        s[ub][nt][3] = fmaf(sb.x, d[nt][3], fmaf(sb.y, qs[nt][g][1], s[ub][nt][3]));
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[ub][nt][c] = fmaf(c < 2 ? sa : sb, d[nt][c], s[ub][nt][c]);
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[ub][nt][c] *= factor[nt][c & 1];
                 if (edge) {
                     const bool here = valid >> ub & 1;
                     const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
@@ -471,16 +529,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float* to = p.scores + (static_cast<long long>(bh) * p.cap + ta) * width + row0 + nt * 8 + 2 * j;
-                        if (ta < seg.len) *reinterpret_cast<float2*>(to) = make_float2(s[ub][nt][0], s[ub][nt][1]);
+                        if (ta < seg.len)
+                            *reinterpret_cast<float2*>(to) =
+                                make_float2(s[ub][nt][0] * factor[nt][0], s[ub][nt][1] * factor[nt][1]);
                         if (tb < seg.len)
-                            *reinterpret_cast<float2*>(to + 8LL * width) = make_float2(s[ub][nt][2], s[ub][nt][3]);
+                            *reinterpret_cast<float2*>(to + 8LL * width) =
+                                make_float2(s[ub][nt][2] * factor[nt][0], s[ub][nt][3] * factor[nt][1]);
                     }
                 }
             }
 
             // ---- value scales, running maxima
             uint32_t va[C::UB][C::kGroups], vb[C::UB][C::kGroups];
-            float vtop = 0.f;
+            __nv_bfloat162 vmax = __floats2bfloat162_rn(0.f, 0.f);  // of (s, m) pairs
 #pragma unroll
             for (int ub = 0; ub < C::UB; ++ub) {
                 const uint32_t blk = unit + ub * C::kBlock;
@@ -491,9 +552,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 for (int g = 0; g < C::kGroups; ++g) {
                     if (edge && (!(valid >> ub & 1) || ta >= seg.len)) va[ub][g] = 0;
                     if (edge && (!(valid >> ub & 1) || tb >= seg.len)) vb[ub][g] = 0;
-                    vtop = fmaxf(vtop, fmaxf(kv4_scale(va[ub][g]).x, kv4_scale(vb[ub][g]).x));
+                    vmax = __hmax2(vmax, __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&va[ub][g]),
+                                                 *reinterpret_cast<const __nv_bfloat162*>(&vb[ub][g])));
                 }
             }
+            float vtop = __low2float(vmax);
             float mx[NT][2];
             bool more = vtop > cap;
 #pragma unroll
@@ -504,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                     for (int ub = 1; ub < C::UB; ++ub)
                         mx[nt][c] = fmaxf(mx[nt][c], fmaxf(s[ub][nt][c], s[ub][nt][c + 2]));
+                    mx[nt][c] *= factor[nt][c];
                     more = more || mx[nt][c] > ref[nt][c];
                 }
             if (__any_sync(0xffffffffu, more)) {
@@ -511,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 for (int o = 16; o > 0; o >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
                 float shrink = 1.f;
                 if (vtop > cap) {
-                    // the power of two at or above it; 2^-100 is the format's least scale
-                    const float up = fmaxf(__uint_as_float((__float_as_uint(vtop) + 0x007fffffu) & 0x7f800000u),
+                    // twice the power of two at or above it; 2^-100 is the format's least scale
+                    const float up = fmaxf(2.f * __uint_as_float((__float_as_uint(vtop) + 0x007fffffu) & 0x7f800000u),
                                            7.888609052210118e-31f);
                     shrink = cap / up;
                     cap = up;
@@ -526,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1)
                             mx[nt][c] = fmaxf(mx[nt][c], __shfl_xor_sync(0xffffffffu, mx[nt][c], o));
-                        const float now = fmaxf(ref[nt][c], mx[nt][c]);
+                        const float now = mx[nt][c] > ref[nt][c] ? mx[nt][c] + kAhead : ref[nt][c];
                         alpha[c] = ref[nt][c] == -INFINITY ? 0.f : ex2_approx(ref[nt][c] - now);
                         // nothing seen so far leaves NaN sums (a NaN score) as they are
                         if (now == -INFINITY) alpha[c] = 1.f;
@@ -555,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                 for (int ub = 0; ub < C::UB; ++ub) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[ub][nt][c] = ex2_approx(s[ub][nt][c] - (c & 1 ? r1 : r0));
+                    for (int c = 0; c < 4; ++c)
+                        s[ub][nt][c] = ex2_approx(fmaf(s[ub][nt][c], factor[nt][c & 1], c & 1 ? -r1 : -r0));
                     l[nt][0] += s[ub][nt][0] + s[ub][nt][2];
                     l[nt][1] += s[ub][nt][1] + s[ub][nt][3];
                 }
@@ -577,18 +642,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* q = s[ub][nt];
                         float w0 = q[0] * ka, w1 = q[1] * ka, w2 = q[2] * kb, w3 = q[3] * kb;
-                        float m0 = q[0] * wa.y, m1 = q[1] * wa.y;
-                        float m2 = q[2] * wb.y, m3 = q[3] * wb.y;
-                        if (edge) {
-                            // a token hidden from a row adds nothing to it, whatever its scale holds
+                        if (!edge) {
+                            om[nt][g][0] = fmaf(q[0], wa.y, fmaf(q[2], wb.y, om[nt][g][0]));
+                            om[nt][g][1] = fmaf(q[1], wa.y, fmaf(q[3], wb.y, om[nt][g][1]));
+                        } else {
+                            // a token hidden from a row adds nothing to it, whatever its scales hold
                             const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
-                            if (ta >= seen[nt][0]) w0 = m0 = 0.f;
-                            if (ta >= seen[nt][1]) w1 = m1 = 0.f;
-                            if (tb >= seen[nt][0]) w2 = m2 = 0.f;
-                            if (tb >= seen[nt][1]) w3 = m3 = 0.f;
+                            if (ta >= seen[nt][0]) w0 = 0.f;
+                            else om[nt][g][0] = fmaf(q[0], wa.y, om[nt][g][0]);
+                            if (ta >= seen[nt][1]) w1 = 0.f;
+                            else om[nt][g][1] = fmaf(q[1], wa.y, om[nt][g][1]);
+                            if (tb >= seen[nt][0]) w2 = 0.f;
+                            else om[nt][g][0] = fmaf(q[2], wb.y, om[nt][g][0]);
+                            if (tb >= seen[nt][1]) w3 = 0.f;
+                            else om[nt][g][1] = fmaf(q[3], wb.y, om[nt][g][1]);
                         }
-                        om[nt][g][0] += m0 + m2;
-                        om[nt][g][1] += m1 + m3;
                         b0[nt] = transpose8(pack_f16(w0, w1));
                         b1[nt] = transpose8(pack_f16(w2, w3));
                     }
@@ -609,11 +677,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 }
             }
             __syncwarp();  // every lane has read the stage
-            const int ahead = u + kStages;
-            if (ahead < seg.u1) {
-                masks = (masks & ~(0xffu << (8 * stage))) | issue(seg, ahead, stage) << (8 * stage);
-                ++issued;
-            }
+            if (u + kStages < seg.u1) masks = (masks & ~(0xffu << (8 * stage))) | issue(stage) << (8 * stage);
+            copy_commit();
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
 
         // ---- sums over the lanes; the next head's first copies run meanwhile
@@ -674,10 +740,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         }
         seg = next;
     }
-    // a copy that was late still writes to this CTA's memory: give it the same time again
-    if (dead)
-        while (taken < issued && __all_sync(0xffffffffu, wait(taken % kStages, (taken / kStages) & 1))) ++taken;
-
     // ---- join the pieces that this CTA's warps share: they stand in the line's order
     __syncthreads();
     for (int i = 0; i < 2 * kWarps;) {
@@ -749,18 +811,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 }
 
 // Joins the parts of the heads that are cut between CTAs, and writes those that
-// have no tokens.  One CTA takes two pairs of accumulators (of kPairs NT) of one
-// (sequence, head, row block), its warps in twos a quarter of the parts each.
-template <int D, int G, int NT>
+// have no tokens.  A CTA takes 8 / SPLIT pairs of accumulators of one (sequence,
+// head, row block), SPLIT warps to a pair taking the parts in turn.
+template <int D, int G, int NT, int SPLIT>
 __global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
     using C = Cfg<D, G, NT>;
-    __shared__ float2 sm_o[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g4 = lane >> 2, j = lane & 3;
     const int HR = p.pages.heads * p.RB;
     const int b = blockIdx.x / HR, hr = blockIdx.x % HR;
-    const int head = hr / p.RB, bh = b * p.pages.heads + head;
-    const int pair = blockIdx.y * 2 + (warp & 1), nt = pair / C::kPairs, i = pair % C::kPairs;
+    const int head = hr / p.RB;
+    const long long bh = static_cast<long long>(b) * p.pages.heads + head;
+    const int pair = blockIdx.y * (8 / SPLIT) + warp / SPLIT, sub = warp % SPLIT;
+    const int nt = pair / C::kPairs, i = pair % C::kPairs;
     const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
     long long all, before;
     count_places<C::kTokens>(p, lane, b, all, before);
@@ -770,57 +833,44 @@ __global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
     const long long c0 = first / share, c1 = n == 0 ? c0 : (first + n - 1) / share;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n > 0 && c0 == c1) return;  // written by its CTA
-    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-    float2 o = make_float2(0.f, 0.f);
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
+    auto take = [&](float2 m, float2 l, float2 x) {
+        const float ms[2] = {m.x, m.y}, ls[2] = {l.x, l.y}, xs[2] = {x.x, x.y};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (ls[e] == 0.f) continue;
+            const float now = fmaxf(top[e], ms[e]);
+            const float base = now == -INFINITY ? 0.f : now;  // NaN sums of rows that saw only NaN
+            const float a = sum[e] == 0.f ? 0.f : ex2_approx(top[e] - base), f = ex2_approx(ms[e] - base);
+            sum[e] = sum[e] * a + ls[e] * f;
+            o[e] = o[e] * a + xs[e] * f;
+            top[e] = now;
+        }
+    };
     if (n > 0) {
         const long long slot0 = static_cast<long long>(b) * HR + hr;
-        for (long long c = c0 + (warp >> 1); c <= c1; c += 4) {
-            const float* ml = p.part_ml + ((slot0 + c) * NT + nt) * 16;
-            const float2 m = *reinterpret_cast<const float2*>(ml + 2 * j), lw = *reinterpret_cast<const float2*>(ml + 8 + 2 * j);
-            const float2 x = p.part_o[(((slot0 + c) * NT + nt) * C::kPairs + i) * 32 + lane];
-            const float ms[2] = {m.x, m.y}, ls[2] = {lw.x, lw.y}, xs[2] = {x.x, x.y};
-            float* os[2] = {&o.x, &o.y};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (ls[e] == 0.f) continue;
-                const float now = fmaxf(top[e], ms[e]);
-                const float base = now == -INFINITY ? 0.f : now;
-                const float a = sum[e] == 0.f ? 0.f : ex2_approx(top[e] - base), f = ex2_approx(ms[e] - base);
-                sum[e] = sum[e] * a + ls[e] * f;
-                *os[e] = *os[e] * a + xs[e] * f;
-                top[e] = now;
-            }
+#pragma unroll 4
+        for (long long c = c0 + sub; c <= c1; c += SPLIT) {
+            const float* ml = p.part_ml + ((slot0 + c) * NT + nt) * 16 + 2 * j;
+            take(*reinterpret_cast<const float2*>(ml), *reinterpret_cast<const float2*>(ml + 8),
+                 p.part_o[(((slot0 + c) * NT + nt) * C::kPairs + i) * 32 + lane]);
         }
     }
-    __shared__ float2 sm_m[8][32], sm_l[8][32];
-    sm_o[warp][lane] = o;
-    sm_m[warp][lane] = make_float2(top[0], top[1]);
-    sm_l[warp][lane] = make_float2(sum[0], sum[1]);
-    __syncthreads();
-    if (warp >= 2) return;
-    float res[2], lse[2];
+    if constexpr (SPLIT > 1) {
+        __shared__ float2 sm[3][8][32];
+        sm[0][warp][lane] = make_float2(top[0], top[1]);
+        sm[1][warp][lane] = make_float2(sum[0], sum[1]);
+        sm[2][warp][lane] = make_float2(o[0], o[1]);
+        __syncthreads();
+        if (sub != 0) return;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        float m = -INFINITY, ll = 0.f, oo = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) m = fmaxf(m, e ? sm_m[warp + 2 * w][lane].y : sm_m[warp + 2 * w][lane].x);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float2 mw = sm_m[warp + 2 * w][lane], lw = sm_l[warp + 2 * w][lane], ow = sm_o[warp + 2 * w][lane];
-            const float le = e ? lw.y : lw.x;
-            if (le == 0.f) continue;
-            const float f = ex2_approx((e ? mw.y : mw.x) - (m == -INFINITY ? 0.f : m));
-            ll = fmaf(f, le, ll);
-            oo = fmaf(f, e ? ow.y : ow.x, oo);
-        }
-        res[e] = ll == 0.f ? 0.f : oo / ll;
-        lse[e] = ll == 0.f ? -INFINITY : (m + __log2f(ll)) * kLn2;
+        for (int x = 1; x < SPLIT; ++x) take(sm[0][warp + x][lane], sm[1][warp + x][lane], sm[2][warp + x][lane]);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (row + e >= p.R) continue;
-        p.o[(static_cast<long long>(bh) * p.R + row + e) * D + ch] = __float2bfloat16_rn(res[e]);
-        if (i == 0 && g4 == 0) p.lse[static_cast<long long>(bh) * p.R + row + e] = lse[e];
+        p.o[(bh * p.R + row + e) * D + ch] = __float2bfloat16_rn(sum[e] == 0.f ? 0.f : o[e] / sum[e]);
+        if (i == 0 && g4 == 0) p.lse[bh * p.R + row + e] = sum[e] == 0.f ? -INFINITY : (top[e] + __log2f(sum[e])) * kLn2;
     }
 }
 
@@ -862,6 +912,20 @@ Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
             weights ? bh * c.width * c.page_size * RB * nt * 8 * 4 : 0};
 }
 
+template <int D, int G, int NT, int SPLIT>
+int launch_merge(const DecParams& p, cudaStream_t stream, int bh) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(bh) * p.RB, D / 8 * NT * SPLIT / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_kv4_merge_kernel<D, G, NT, SPLIT>, p) == cudaSuccess ? 0 : -5;
+}
+
 template <int D, int G, int NT>
 int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) {
     using C = Cfg<D, G, NT>;
@@ -871,16 +935,11 @@ int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) 
         return -5;
     fa_kv4_decode_kernel<D, G, NT><<<p.n_cta, kThreads, C::kSmem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -5;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(bh) * p.RB, C::kPairs * NT / 2);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fa_kv4_merge_kernel<D, G, NT>, p) != cudaSuccess) return -5;
+    // Warps to a pair: a head has about n_cta / heads parts, more if few of the heads are long.
+    const long long heads = static_cast<long long>(bh) * p.RB;
+    const int rc = heads * 2 >= p.n_cta ? launch_merge<D, G, NT, 1>(p, stream, bh)
+                                        : launch_merge<D, G, NT, 8>(p, stream, bh);
+    if (rc != 0) return rc;
     if (weights) {
         long long n = (p.cap + 255) / 256;
         const long long most = (16LL * num_sms + bh - 1) / bh;
@@ -899,8 +958,7 @@ size_t kv4_decode_workspace(const Kv4Shape& c, int Hq, int Tq, bool weights, int
 
 int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
                       void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
-                      float* weights_out, long long slots, void* workspace, cudaStream_t stream,
-                      const DebugKnobs& dbg, int num_sms) {
+                      float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms) {
     DecParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.pages.pool = static_cast<unsigned char*>(const_cast<void*>(pool));
@@ -924,7 +982,6 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
     p.weights = weights;
     p.weights_out = weights_out;
     p.slots = slots;
-    p.timeout_ns = dbg.timeout_ns;
     p.sl2 = scale * kLog2e;
     const int bh = c.B * c.Hkv;
     const bool w = weights_out != nullptr;

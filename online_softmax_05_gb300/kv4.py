@@ -28,8 +28,8 @@ def kv4_pool(num_pages: int, kv_heads: int, dim: int, page_size: int = 64, group
     import torch
     if dim not in (64, 128) or group not in (32, 64):
         raise ValueError("dim must be 64 or 128 and group 32 or 64")
-    if page_size < 16 or page_size % 16 or num_pages < 1 or kv_heads < 1:
-        raise ValueError("page_size must be a multiple of 16, num_pages and kv_heads at least 1")
+    if page_size < 16 or page_size > 65536 or page_size % 16 or num_pages < 1 or kv_heads < 1:
+        raise ValueError("page_size must be a multiple of 16 up to 65536, num_pages and kv_heads at least 1")
     return torch.zeros(num_pages, kv_heads, page_size // 16, 16 * (dim + 8 * dim // group), dtype=torch.uint8,
                        device=device)
 

@@ -59,7 +59,7 @@ def evict(c=None, **kw):
 @pytest.mark.parametrize("call", [append, read, decode, evict])
 def test_cache_descriptions_are_refused(call):
     for kw, code in ((dict(pool=0), -1), (dict(table=0), -1), (dict(lengths=0), -1), (dict(B=0), -2), (dict(Hkv=0), -2),
-                     (dict(width=0), -2), (dict(pages=0), -2), (dict(page=0), -2), (dict(page=24), -3), (dict(D=96), -3),
+                     (dict(width=0), -2), (dict(pages=0), -2), (dict(page=0), -2), (dict(page=24), -3), (dict(page=1 << 17, width=1), -3), (dict(D=96), -3),
                      (dict(group=128), -3), (dict(B=1 << 14, Hkv=8), -2), (dict(width=1 << 26), -2),
                      (dict(pool=BASE + 8), -4), (dict(table=2 * BASE + 2), -4), (dict(lengths=3 * BASE + 1), -4)):
         assert call(cache(**kw)) == code, kw
