@@ -36,6 +36,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_ptx.cuh"
@@ -213,7 +215,7 @@ struct Piece {
 // halves of the banks.
 __device__ __forceinline__ int token_of(int r) { return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1; }
 
-template <int D, int G, int NT>
+template <int D, int G, int NT, bool SCORES>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kernel(DecParams p) {
     using C = Cfg<D, G, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -458,15 +460,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             ref[nt][0] = ref[nt][1] = -INFINITY;
         }
 
-        for (int u = seg.u0; u < seg.u1; ++u) {
-            copy_wait<kStages - 1>();
-            __syncwarp();
-            const uint32_t unit = ring + stage * C::kUnitBytes;
-            const uint32_t valid = masks >> (8 * stage) & 0xffu;
-            const int t0 = u * C::kTokens;
-            // some token of the unit is not there or not seen by every row
-            const bool edge = t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1;
-
+        // One unit in the ring at `unit`.  some_hidden: a token of it is not there or not
+        // seen by every row; the other units have none of those tests.
+        auto use = [&](auto some_hidden, uint32_t unit, uint32_t valid, int t0) {
+            constexpr bool edge = decltype(some_hidden)::value;
             // ---- S^T = K q^T
             float s[C::UB][NT][4];
 #pragma unroll
@@ -514,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                         for (int c = 0; c < 4; ++c) s[ub][nt][c] = fmaf(c < 2 ? sa : sb, d[nt][c], s[ub][nt][c]);
                 }
-                if (edge) {
+                if constexpr (edge) {
                     const bool here = valid >> ub & 1;
                     const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
 #pragma unroll
@@ -523,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                         for (int c = 0; c < 4; ++c)
                             if (!here || (c < 2 ? ta : tb) >= seen[nt][c & 1]) s[ub][nt][c] = -INFINITY;
                 }
-                if (p.scores != nullptr) {
+                if constexpr (SCORES) {
                     const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
                     const int width = p.RB * NT * 8;
 #pragma unroll
@@ -642,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* q = s[ub][nt];
                         float w0 = q[0] * ka, w1 = q[1] * ka, w2 = q[2] * kb, w3 = q[3] * kb;
-                        if (!edge) {
+                        if constexpr (!edge) {
                             om[nt][g][0] = fmaf(q[0], wa.y, fmaf(q[2], wb.y, om[nt][g][0]));
                             om[nt][g][1] = fmaf(q[1], wa.y, fmaf(q[3], wb.y, om[nt][g][1]));
                         } else {
@@ -676,6 +673,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     }
                 }
             }
+        };
+        for (int u = seg.u0; u < seg.u1; ++u) {
+            copy_wait<kStages - 1>();
+            __syncwarp();
+            const uint32_t unit = ring + stage * C::kUnitBytes;
+            const uint32_t valid = masks >> (8 * stage) & 0xffu;
+            const int t0 = u * C::kTokens;
+            if (t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1) use(std::true_type{}, unit, valid, t0);
+            else use(std::false_type{}, unit, valid, t0);
             __syncwarp();  // every lane has read the stage
             if (u + kStages < seg.u1) masks = (masks & ~(0xffu << (8 * stage))) | issue(stage) << (8 * stage);
             copy_commit();
@@ -930,10 +936,9 @@ template <int D, int G, int NT>
 int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) {
     using C = Cfg<D, G, NT>;
     static_assert(C::kSmem + 2 * kWarps * static_cast<int>(sizeof(Piece)) + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
-    if (cudaFuncSetAttribute(fa_kv4_decode_kernel<D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
-        cudaSuccess)
-        return -5;
-    fa_kv4_decode_kernel<D, G, NT><<<p.n_cta, kThreads, C::kSmem, stream>>>(p);
+    const auto kernel = weights ? fa_kv4_decode_kernel<D, G, NT, true> : fa_kv4_decode_kernel<D, G, NT, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return -5;
+    kernel<<<p.n_cta, kThreads, C::kSmem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -5;
     // Warps to a pair: a head has about n_cta / heads parts, more if few of the heads are long.
     const long long heads = static_cast<long long>(bh) * p.RB;
