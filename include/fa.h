@@ -322,7 +322,9 @@ int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k,
 /*
  * Decoding over the 4-bit cache, grouped heads (query head h reads key/value
  * head h / (Hq / Hkv)), split over the tokens.
- *   q       in: (B, Hq, Tq, D) bf16, 1 <= Tq <= 8, Hq / Hkv * Tq <= 1024
+ *   q       in: (B, Hq, Tq, D) bf16, 1 <= Tq <= 8, Hq / Hkv * Tq <= 1024;
+ *               B * Hkv * ceil(rows / 8) * width * page_size / 32 below 2^31
+ *               (FA_ERR_SHAPE), with rows = Hq / Hkv * Tq
  *   o      out: (B, Hq, Tq, D) bf16
  *   lse    out: (B, Hq, Tq) float32, natural-log log-sum-exp of the scaled scores
  *   causal    : 1 = the queries are the last Tq tokens of the sequence, query i

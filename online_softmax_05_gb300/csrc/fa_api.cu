@@ -484,6 +484,7 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
     if (static_cast<long long>(cache->B) * Hq * Tq > INT_MAX) return FA_ERR_SHAPE;
     if (Tq > 8) return FA_ERR_UNSUPPORTED;
     if (Hq / cache->Hkv * Tq > 1024) return FA_ERR_UNSUPPORTED;
+    if (!fa::kv4_decode_fits(kv4_shape(cache), Hq, Tq)) return FA_ERR_SHAPE;
     if (causal != 0 && causal != 1) return FA_ERR_ARG;
     if (!std::isfinite(scale)) return FA_ERR_ARG;
     if (weights_out && slots < 1) return FA_ERR_SHAPE;

@@ -77,6 +77,7 @@ int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int*
                      int* positions_out, int* lengths_out, int* source, void* workspace, cudaStream_t stream,
                      int num_sms);
 size_t kv4_decode_workspace(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms);
+bool kv4_decode_fits(const Kv4Shape& c, int Hq, int Tq);  // whether the kernel's 32-bit line of units holds the shape
 int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
                       void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
                       float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms);

@@ -58,6 +58,12 @@ constexpr int kStages = 2;
 // units), so that it seldom moves again.  P times a value scale goes to fp16 at
 // up to 2^14, so what is 2^-23 of the largest still has all of its bits.
 constexpr float kAhead = 4.f;
+// Places on the line for a head's start, its queries' and first copies' latency
+// and its outputs, in units of 32 or 64 tokens.
+#ifndef KSTART
+#define KSTART 2
+#endif
+constexpr int kStart = KSTART;
 
 struct DecParams {
     const __nv_bfloat16* q;
@@ -100,35 +106,35 @@ __device__ __forceinline__ int length_of(const DecParams& p, int b) {
     return len;
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long x) {
+__device__ __forceinline__ int warp_sum(int x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// Places on the line that a head of sequence b takes.
+// Places on the line that a head of sequence b takes.  (The whole line has fewer
+// than 2^31: checked on the host for the table's capacity.)
 template <int TOKENS>
 __device__ __forceinline__ int places_of(int len) {
-    return len > 0 ? (len + TOKENS - 1) / TOKENS + 1 : 0;
+    return len > 0 ? (len + TOKENS - 1) / TOKENS + kStart : 0;
 }
 // Places of one head of all sequences, and of those before sequence `upto`; per warp.
 template <int TOKENS>
-__device__ __forceinline__ void count_places(const DecParams& p, int lane, int upto, long long& all, long long& before) {
+__device__ __forceinline__ void count_places(const DecParams& p, int lane, int upto, int& all, int& before) {
     all = before = 0;
     for (int b = lane; b < p.B; b += 32) {
         const int n = places_of<TOKENS>(length_of(p, b));
         all += n;
         if (b < upto) before += n;
     }
-    all = warp_sum_ll(all);
-    before = warp_sum_ll(before);
+    all = warp_sum(all);
+    before = warp_sum(before);
 }
-// The line: every (sequence, head, row block) of n > 0 units takes n + 1 places,
-// the first one for the cost of starting it.  A warp's share of the places.
-__device__ __forceinline__ long long share_of(const DecParams& p, long long places) {
-    const long long warps = static_cast<long long>(p.n_cta) * kWarps;
-    const long long even = (places + warps - 1) / warps;
-    return even > 1 ? even : 1;
+// The line: every (sequence, head, row block) of n > 0 units takes n + kStart
+// places, the first ones for the cost of starting it.  A warp's share of them.
+__device__ __forceinline__ int share_of(const DecParams& p, int places) {
+    const unsigned warps = static_cast<unsigned>(p.n_cta) * kWarps;
+    return static_cast<int>(max((static_cast<unsigned>(places) + warps - 1) / warps, 1u));
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -180,7 +186,7 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A power of two: 2^k as the product of two fp32 numbers, |k| <= 250.
+// 2^k as the product of two fp32 numbers, |k| <= 250.
 __device__ __forceinline__ float2 pow2_parts(int k) {
     const int a = k / 2;
     return make_float2(__int_as_float((a + 127) << 23), __int_as_float((k - a + 127) << 23));
@@ -206,7 +212,7 @@ struct Segment {
 };
 // What a warp leaves to be joined.
 struct Piece {
-    long long head;  // b * heads * RB + hr, or -1
+    int head;        // b * heads * RB + hr, or -1
     int first, last; // whether it holds the head's first and last unit
 };
 
@@ -234,37 +240,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 
     // this warp's share of the line; from place `skip` of its first head on
     Segment seg{0, 0, 0, 0, 0, 0};
-    long long left = 0;
+    int left = 0;
     {
-        long long all, unused;
+        int all, unused;
         count_places<C::kTokens>(p, lane, 0, all, unused);
-        const long long total = all * HR, share = share_of(p, total);
-        const long long first = (blockIdx.x * static_cast<long long>(kWarps) + warp) * share;
-        long long base = 0;  // places of one head before the chunk of sequences
+        const int total = all * HR, share = share_of(p, total);
+        const long long start = (blockIdx.x * static_cast<long long>(kWarps) + warp) * share;
+        const int first = static_cast<int>(min(start, static_cast<long long>(total)));
+        const int first_row = first / HR;  // the place's head ends behind this place of the one-head line
+        int base = 0;                      // places of one head before the chunk of sequences
         for (int b0 = 0; b0 < p.B && first < total; b0 += 32) {
             const int b = b0 + lane;
             const int len = b < p.B ? length_of(p, b) : 0;
             const int n = places_of<C::kTokens>(len);
-            long long sum = n;
+            int sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                const int y = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += y;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, (base + sum) * HR > first);
+            const unsigned hit = __ballot_sync(0xffffffffu, base + sum > first_row);
             if (hit != 0) {
                 const int src = __ffs(hit) - 1;
                 const int places = __shfl_sync(0xffffffffu, n, src);
-                const long long rem = first - (base + __shfl_sync(0xffffffffu, sum, src) - places) * HR;
+                const int rem = first - (base + __shfl_sync(0xffffffffu, sum, src) - places) * HR;
                 seg.b = b0 + src;
                 seg.len = __shfl_sync(0xffffffffu, len, src);
-                seg.n = places - 1;
-                seg.hr = static_cast<int>(rem / places);
-                const int place = static_cast<int>(rem % places);
+                seg.n = places - kStart;
+                seg.hr = rem / places;
+                const int place = rem - seg.hr * places;
                 left = min(share, total - first);
-                seg.u0 = max(place - 1, 0);
-                seg.u1 = static_cast<int>(min(static_cast<long long>(seg.n), place + left - 1));
-                left -= seg.u1 + 1 - place;
+                seg.u0 = max(place - kStart, 0);
+                seg.u1 = min(seg.n, place + left - kStart);
+                left -= min(left, places - place);
                 break;
             }
             base += __shfl_sync(0xffffffffu, sum, 31);
@@ -279,11 +287,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             do {
                 if (++s.b >= p.B) return false;
                 s.len = length_of(p, s.b);
-                s.n = places_of<C::kTokens>(s.len) - 1;
+                s.n = places_of<C::kTokens>(s.len) - kStart;
             } while (s.n < 0);
         }
-        s.u1 = static_cast<int>(min(static_cast<long long>(s.n), left - 1));
-        left -= s.u1 + 1;
+        s.u1 = min(s.n, left - kStart);
+        left -= min(left, s.n + kStart);
         return s.u1 > 0;
     };
     // a share may begin with the place of a head's start alone
@@ -357,59 +365,61 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             copy_commit();
         }
     };
-    if (working) prologue(seg);
-
     const int tokA = token_of(g4), tokB = 8 + tokA;
+    bool fresh = true;  // the first segment, whose copies are yet to be started
     while (working) {
         const int head = seg.hr / p.RB, rb = seg.hr % p.RB;
         const int bh = seg.b * p.pages.heads + head;
         const int row0 = rb * NT * 8;
 
         // ---- queries: operand fragments, group sums and score factors
+        uint4 raw[NT][C::kWords];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row0 + nt * 8 + g4;
+#pragma unroll
+            for (int w = 0; w < C::kWords; ++w) {
+                raw[nt][w] = make_uint4(0, 0, 0, 0);
+                if (row < p.R)
+                    raw[nt][w] = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(bh) * p.R + row) * D +
+                                                                 32 * w + 8 * j);
+            }
+        }
+        if (fresh) prologue(seg);  // while the queries are on their way
         uint32_t qf[NT][C::kWords][4];
         uint32_t qs[NT][(C::kGroups + 1) / 2];
         float factor[NT][2];
         int seen[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = row0 + nt * 8 + g4;
-            uint4 raw[C::kWords];
-            float top = 0.f;
-            bool finite = true;
+            __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < C::kWords; ++w) {
-                raw[w] = make_uint4(0, 0, 0, 0);
-                if (row < p.R)
-                    raw[w] = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(bh) * p.R + row) * D +
-                                                             32 * w + 8 * j);
-                const uint32_t word[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+                const uint32_t word[4] = {raw[nt][w].x, raw[nt][w].y, raw[nt][w].z, raw[nt][w].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = __uint_as_float(word[e] << 16), b = __uint_as_float(word[e] & 0xffff0000u);
-                    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
-                    finite = finite && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
-                }
+                for (int e = 0; e < 4; ++e)
+                    most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&word[e])));
             }
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                finite = __shfl_xor_sync(0xffffffffu, finite, o) && finite;
-            }
-            // 2^e <= top < 2^(e+1) goes to 2^14, in two exact steps, as 2^(14-e) alone may leave fp32
-            const int e = top > 0.f && finite ? ilogbf(top) : 0;
-            const float2 up = pow2_parts(14 - e), down = pow2_parts(10 + e);
-            const float sign = p.sl2 < 0.f ? -up.x : p.sl2 == 0.f ? 0.f : up.x;
+            for (int o = 1; o < 4; o <<= 1) most = __hmax2_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float top = fmaxf(__low2float(most), __high2float(most));
+            const bool finite = __low2float(most) < INFINITY && __high2float(most) < INFINITY;
+            // 2^e <= top < 2^(e+1) goes to 2^14 (rows below 2^-113, to less)
+            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            const int up_e = min(14 - e, 127);
+            const float2 down = pow2_parts(24 - up_e);
+            const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((up_e + 127) << 23), p.sl2);
             float group[C::kGroups];
 #pragma unroll
             for (int g = 0; g < C::kGroups; ++g) group[g] = 0.f;
 #pragma unroll
             for (int w = 0; w < C::kWords; ++w) {
-                const uint32_t word[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+                const uint32_t word[4] = {raw[nt][w].x, raw[nt][w].y, raw[nt][w].z, raw[nt][w].w};
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = __uint_as_float(word[i] << 16) * sign * up.y;
-                    x[2 * i + 1] = __uint_as_float(word[i] & 0xffff0000u) * sign * up.y;
+                    x[2 * i] = __uint_as_float(word[i] << 16) * up;
+                    x[2 * i + 1] = __uint_as_float(word[i] & 0xffff0000u) * up;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) group[w * 32 / G] += x[i];
@@ -699,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         float2* out = reinterpret_cast<float2*>(piece_at(warp, working ? 0 : 1));
         float* ml = reinterpret_cast<float*>(piece_at(warp, working ? 0 : 1) + C::kPieceO);
         if (!(first && last) && lane == 0) {
-            piece->head = static_cast<long long>(seg.b) * HR + seg.hr;
+            piece->head = seg.b * HR + seg.hr;
             piece->first = first;
             piece->last = last;
         }
@@ -745,74 +755,92 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             }
         }
         seg = next;
+        fresh = false;
     }
     // ---- join the pieces that this CTA's warps share: they stand in the line's order
     __syncthreads();
-    for (int i = 0; i < 2 * kWarps;) {
-        const long long at = s_piece[i >> 1][i & 1].head;
-        if (at < 0) {
-            ++i;
-            continue;
+    constexpr int kMost = 2 * kWarps;
+    static_assert(kMost <= 32, "a lane for every piece");
+    // the pieces of a head are neighbours; lane y looks at piece y
+    const Piece mine = s_piece[(lane % kMost) >> 1][lane & 1];
+    const unsigned have = __ballot_sync(0xffffffffu, lane < kMost && mine.head >= 0);
+    if (have == 0) return;
+    // each piece's factor 2^(m - max) for every query row: a warp takes a row of each
+    // tile, a lane a piece, the maxima and sums run over the lanes of the same head
+    const unsigned same = __match_any_sync(0xffffffffu, have >> lane & 1 ? mine.head : -1 - lane);
+    // per query row: the pieces' factors, maxima and sums, behind the last pieces in the rings
+    static_assert(C::kPiece + NT * 3 * kMost * 4 <= C::kRing, "room for the tables");
+    auto joined_at = [&](int row, int nt) -> float* {
+        return reinterpret_cast<float*>(smem + row * C::kRing + C::kPiece) + nt * 3 * kMost;
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        static_assert(kWarps == 8, "a warp for each row of a tile");
+        const float* ml = reinterpret_cast<const float*>(piece_at((lane % kMost) >> 1, lane & 1) + C::kPieceO) + nt * 16;
+        const bool in = have >> lane & 1;
+        const float m = in ? ml[warp] : -INFINITY, lw = in ? ml[8 + warp] : 0.f;
+        float top = m, sum = 0.f;
+#pragma unroll
+        for (int y = 0; y < kMost; ++y) {
+            const float my = __shfl_sync(0xffffffffu, m, y);
+            if (same >> y & 1) top = fmaxf(top, my);
         }
-        int end = i + 1;  // behind the last piece of this head
-        for (int x = end; x < 2 * kWarps; ++x) {
-            const long long y = s_piece[x >> 1][x & 1].head;
-            if (y >= 0 && y != at) break;
-            if (y == at) end = x + 1;
+        const float f = lw == 0.f ? 0.f : ex2_approx(m - top);
+        const float part = f == 0.f ? 0.f : f * lw;
+#pragma unroll
+        for (int y = 0; y < kMost; ++y) {
+            const float py = __shfl_sync(0xffffffffu, part, y);
+            if (same >> y & 1) sum += py;
         }
-        const bool whole = s_piece[i >> 1][i & 1].first && s_piece[(end - 1) >> 1][(end - 1) & 1].last;
-        const int hr = static_cast<int>(at % HR);
-        const long long bh = at / HR * p.pages.heads + hr / p.RB;
-        const long long slot = blockIdx.x + at;
+        if (lane < kMost) {
+            float* table = joined_at(warp, nt);
+            table[lane] = f;
+            table[kMost + lane] = top;
+            table[2 * kMost + lane] = sum;
+        }
+    }
+    __syncthreads();
+    for (unsigned open = have; open != 0;) {
+        const int y0 = __ffs(open) - 1;
+        const unsigned group = __shfl_sync(0xffffffffu, same, y0);
+        const int at = __shfl_sync(0xffffffffu, mine.head, y0), y1 = 31 - __clz(group);
+        const bool whole = __shfl_sync(0xffffffffu, mine.first, y0) && __shfl_sync(0xffffffffu, mine.last, y1);
+        open &= ~group;
+        const int hr = at % HR;
+        const long long bh = static_cast<long long>(at / HR) * p.pages.heads + hr / p.RB;
+        const long long slot = blockIdx.x + static_cast<long long>(at);
         for (int x = warp; x < NT * C::kPairs; x += kWarps) {
             const int nt = x / C::kPairs, pr = x % C::kPairs;
             const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j;
-            float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-            for (int y = i; y < end; ++y) {
-                if (s_piece[y >> 1][y & 1].head != at) continue;
-                const float* ml = reinterpret_cast<const float*>(piece_at(y >> 1, y & 1) + C::kPieceO) + nt * 16;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) top[c] = fmaxf(top[c], ml[2 * j + c]);
-            }
             float2 o = make_float2(0.f, 0.f);
-            for (int y = i; y < end; ++y) {
-                if (s_piece[y >> 1][y & 1].head != at) continue;
-                const unsigned char* from = piece_at(y >> 1, y & 1);
-                const float* ml = reinterpret_cast<const float*>(from + C::kPieceO) + nt * 16;
-                const float2 v = reinterpret_cast<const float2*>(from)[x * 32 + lane];
-                const float l0 = ml[8 + 2 * j], l1 = ml[8 + 2 * j + 1];
-                if (l0 != 0.f) {
-                    const float f = ex2_approx(ml[2 * j] - top[0]);
-                    sum[0] = fmaf(f, l0, sum[0]);
-                    o.x = fmaf(f, v.x, o.x);
-                }
-                if (l1 != 0.f) {
-                    const float f = ex2_approx(ml[2 * j + 1] - top[1]);
-                    sum[1] = fmaf(f, l1, sum[1]);
-                    o.y = fmaf(f, v.y, o.y);
-                }
+#pragma unroll 4
+            for (int y = y0; y <= y1; ++y) {
+                if (!(group >> y & 1)) continue;
+                const float2 f = make_float2(joined_at(2 * j, nt)[y], joined_at(2 * j + 1, nt)[y]);
+                const float2 v = reinterpret_cast<const float2*>(piece_at(y >> 1, y & 1))[x * 32 + lane];
+                if (f.x != 0.f) o.x = fmaf(f.x, v.x, o.x);
+                if (f.y != 0.f) o.y = fmaf(f.y, v.y, o.y);
             }
+            const float2 sum = make_float2(joined_at(2 * j, nt)[2 * kMost + y0], joined_at(2 * j + 1, nt)[2 * kMost + y0]);
             if (!whole) {
                 p.part_o[(slot * NT * C::kPairs + x) * 32 + lane] = o;
             } else {
                 const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
                 __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
-                if (row < p.R) to[0] = __float2bfloat16_rn(sum[0] == 0.f ? 0.f : o.x / sum[0]);
-                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum[1] == 0.f ? 0.f : o.y / sum[1]);
-            }
-            if (pr == 0 && g4 == 0) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!whole) {
-                        p.part_ml[(slot * NT + nt) * 16 + 2 * j + c] = top[c];
-                        p.part_ml[(slot * NT + nt) * 16 + 8 + 2 * j + c] = sum[c];
-                    } else if (row + c < p.R) {
-                        p.lse[bh * p.R + row + c] = sum[c] == 0.f ? -INFINITY : (top[c] + __log2f(sum[c])) * kLn2;
-                    }
-                }
+                if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x);
+                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y);
             }
         }
-        i = end;
+        if (warp == 0 && lane < 8 * NT) {
+            const int nt = lane / 8, c = lane % 8, row = (hr % p.RB) * NT * 8 + lane;
+            const float top = joined_at(c, nt)[kMost + y0], sum = joined_at(c, nt)[2 * kMost + y0];
+            if (!whole) {
+                p.part_ml[(slot * NT + nt) * 16 + c] = top;
+                p.part_ml[(slot * NT + nt) * 16 + 8 + c] = sum;
+            } else if (row < p.R) {
+                p.lse[bh * p.R + row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+            }
+        }
     }
 }
 
@@ -831,12 +859,12 @@ __global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
     const int pair = blockIdx.y * (8 / SPLIT) + warp / SPLIT, sub = warp % SPLIT;
     const int nt = pair / C::kPairs, i = pair % C::kPairs;
     const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
-    long long all, before;
+    int all, before;
     count_places<C::kTokens>(p, lane, b, all, before);
-    const int n = max(places_of<C::kTokens>(length_of(p, b)) - 1, 0);
-    const long long share = share_of(p, all * HR) * kWarps;
-    const long long first = before * HR + static_cast<long long>(hr) * (n + 1) + 1;  // the first unit's place
-    const long long c0 = first / share, c1 = n == 0 ? c0 : (first + n - 1) / share;
+    const int n = max(places_of<C::kTokens>(length_of(p, b)) - kStart, 0);
+    const unsigned share = static_cast<unsigned>(share_of(p, all * HR)) * kWarps;
+    const unsigned first = before * HR + hr * (n + kStart) + kStart;  // the first unit's place
+    const unsigned c0 = first / share, c1 = n == 0 ? c0 : (first + n - 1) / share;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n > 0 && c0 == c1) return;  // written by its CTA
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
@@ -856,7 +884,7 @@ __global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
     if (n > 0) {
         const long long slot0 = static_cast<long long>(b) * HR + hr;
 #pragma unroll 4
-        for (long long c = c0 + sub; c <= c1; c += SPLIT) {
+        for (unsigned c = c0 + sub; c <= c1; c += SPLIT) {
             const float* ml = p.part_ml + ((slot0 + c) * NT + nt) * 16 + 2 * j;
             take(*reinterpret_cast<const float2*>(ml), *reinterpret_cast<const float2*>(ml + 8),
                  p.part_o[(((slot0 + c) * NT + nt) * C::kPairs + i) * 32 + lane]);
@@ -959,6 +987,12 @@ int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) 
 size_t kv4_decode_workspace(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
     const Sizes s = sizes_of(c, Hq, Tq, weights, num_sms);
     return s.part_o + s.part_ml + s.scores;
+}
+
+bool kv4_decode_fits(const Kv4Shape& c, int Hq, int Tq) {
+    const int R = Hq / c.Hkv * Tq, nt = tiles_of(R);
+    const double places = (static_cast<double>(c.width) * c.page_size / 32 + 1 + kStart) * c.B * c.Hkv * ((R + 8 * nt - 1) / (8 * nt));
+    return places + 4096.0 * kWarps < 2147483647.0;
 }
 
 int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
