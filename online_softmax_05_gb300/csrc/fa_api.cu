@@ -443,7 +443,7 @@ int fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, long 
     return fa::launch_kv4_append(kv4_shape(cache), cache->pool, cache->block_table, k, v, k_t, k_h, v_t, v_h,
                                  cache->lengths, cu_new, total, positions, positions_64, freq, rotary, interleaved,
                                  amplitude, weights, slot_positions, (weights || slot_positions) ? slots : 0,
-                                 static_cast<cudaStream_t>(stream));
+                                 static_cast<cudaStream_t>(stream), sms);
 }
 
 int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k, void* v, void* stream) {
@@ -569,13 +569,7 @@ long long fa_kv4_block_offset(const int* block_table, int width, int Hkv, int D,
     if (width < 1 || Hkv < 1 || num_pages < 1 || page_size < 16 || b < 0 || h < 0 || h >= Hkv || slot < 0)
         return FA_ERR_SHAPE;
     if ((D != 64 && D != 128) || (group != 32 && group != 64) || page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
-    fa::Kv4Pages p{};
-    p.table = block_table;
-    p.width = width;
-    p.num_pages = num_pages;
-    p.heads = Hkv;
-    p.blocks_page = page_size / 16;
-    p.block_bytes = 16LL * (D + 8 * D / group);
+    const fa::Kv4Pages p = fa::kv4_pages(nullptr, block_table, width, num_pages, Hkv, page_size, D, group);
     const long long at = p.block_of(b, slot / 16);
     return at < 0 ? static_cast<long long>(FA_ERR_PAGE) : at + h * p.head_bytes();
 }

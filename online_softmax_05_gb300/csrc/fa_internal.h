@@ -68,7 +68,7 @@ struct Kv4Shape {
 int launch_kv4_append(const Kv4Shape& c, void* pool, const int* table, const void* k, const void* v, long long k_t,
                       long long k_h, long long v_t, long long v_h, const int* lengths, const int* cu_new, int total,
                       const void* positions, int pos64, const void* freq, int R, int interleaved, float amplitude,
-                      float* weights, int* slot_positions, long long slots, cudaStream_t stream);
+                      float* weights, int* slot_positions, long long slots, cudaStream_t stream, int num_sms);
 int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* start,
                     int count, void* k, void* v, cudaStream_t stream);
 size_t kv4_evict_workspace(int B, int Hkv, int budget);

@@ -44,22 +44,39 @@ struct Kv4Pages {
     int num_pages;
     int heads;           // Hkv
     int blocks_page;     // page_size / 16
+    int shift;           // its logarithm, or -1 if it is no power of two
     long long block_bytes;
 
     // Byte offset of head 0's block holding slots 16 n .. 16 n + 15 of sequence
     // b, or -1 if the table names no page of the pool there.
     __host__ __device__ __forceinline__ long long block_of(int b, int n) const {
-        const int at = n / blocks_page;
+        const int at = shift >= 0 ? n >> shift : n / blocks_page;
         if (at >= width) return -1;
         const int page = table[static_cast<long long>(b) * width + at];
         if (page < 0 || page >= num_pages) return -1;
-        return (static_cast<long long>(page) * heads * blocks_page + n % blocks_page) * block_bytes;
+        return (static_cast<long long>(page) * heads * blocks_page + (n - at * blocks_page)) * block_bytes;
     }
     __host__ __device__ __forceinline__ long long head_bytes() const { return blocks_page * block_bytes; }
     __host__ __device__ __forceinline__ long long capacity() const {
         return static_cast<long long>(width) * blocks_page * 16;
     }
 };
+
+inline Kv4Pages kv4_pages(unsigned char* pool, const int* table, int width, int num_pages, int heads, int page_size,
+                          int D, int group) {
+    Kv4Pages x;
+    x.pool = pool;
+    x.table = table;
+    x.width = width;
+    x.num_pages = num_pages;
+    x.heads = heads;
+    x.blocks_page = page_size / 16;
+    x.shift = -1;
+    for (int s = 0; s < 16; ++s)
+        if (x.blocks_page == 1 << s) x.shift = s;
+    x.block_bytes = 16LL * (D + 8 * D / group);
+    return x;
+}
 
 __device__ __forceinline__ float2 kv4_scale(uint32_t pair) {  // (s, m)
     return make_float2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u));

@@ -6,6 +6,7 @@
 
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
+#include "fa_rope.cuh"
 
 namespace fa {
 namespace {
@@ -33,9 +34,16 @@ struct AppendParams {
     int B, total;
 };
 
-// Sequence of packed row t: the last b with cu[b] <= t, or -1.
+// Sequence of packed row t: the last b with cu[b] <= t, or -1.  `t` may differ
+// between lanes; a few lookups in parallel for small batches, bisection above.
 __device__ __forceinline__ int sequence_of(const int* cu, int B, int t) {
     if (t < cu[0] || t >= cu[B]) return -1;
+    if (B <= 16) {
+        int b = 0;
+#pragma unroll
+        for (int i = 1; i < 16; ++i) b += i < B && cu[min(i, B)] <= t;
+        return b;
+    }
     int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -45,44 +53,127 @@ __device__ __forceinline__ int sequence_of(const int* cu, int B, int t) {
     return lo;
 }
 
-// Channel c of a key row at position `pos`, rotated and rounded to bf16.
-__device__ __forceinline__ float rotated(const AppendParams& p, const __nv_bfloat16* row, int c, long long pos) {
-    const float x = __bfloat162float(row[c]);
-    if (c >= p.R) return x;
-    const int half = p.R >> 1;
-    const int pair = p.interleaved ? c >> 1 : (c < half ? c : c - half);
-    const bool first = p.interleaved ? (c & 1) == 0 : c < half;
-    const int other = p.interleaved ? c ^ 1 : (first ? c + half : c - half);
-    const float y = __bfloat162float(row[other]);
-    const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[pair];
-    float s, co;
-    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &s, &co);  // 2^-31
-    s *= p.amp;
-    co *= p.amp;
-    return __bfloat162float(__float2bfloat16_rn(first ? x * co - y * s : x * co + y * s));
+// Where a channel's partner in the rotation lies.
+enum Rotation {
+    kNone,         // keys are stored as they come
+    kHalf,         // channels (i, i + R/2), R/2 a multiple of 8: the partners are another lane's
+    kInterleaved,  // channels (2i, 2i + 1), R a multiple of 8: the thread's own
+    kAny,          // any R: looked up one by one
+};
+
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// Smallest and largest of a group's channels, 8 of them in `x`; NaN if one is.
+template <int G>
+__device__ __forceinline__ float2 range_of_group(const uint32_t (&x)[4]) {
+    const __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(as_bf2(x[0]), as_bf2(x[1])), __hmin2_nan(as_bf2(x[2]), as_bf2(x[3])));
+    const __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(as_bf2(x[0]), as_bf2(x[1])), __hmax2_nan(as_bf2(x[2]), as_bf2(x[3])));
+    // (min, -max) in one word: one exchange a step serves both
+    __nv_bfloat162 r = __halves2bfloat162(__hmin_nan(__low2bfloat16(lo2), __high2bfloat16(lo2)),
+                                          __hneg(__hmax_nan(__low2bfloat16(hi2), __high2bfloat16(hi2))));
+#pragma unroll
+    for (int o = 1; o < G / 8; o <<= 1) r = __hmin2_nan(r, as_bf2(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
+    return make_float2(__low2float(r), -__high2float(r));
 }
 
-// One thread quantises 8 channels of one key or value row; the G/8 threads of
-// a group find its range with shuffles.
-template <int D, int G>
-__global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p) {
+// Two fp32 numbers in one register pair: one instruction works on both.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two(uint64_t x) : v(x) {}
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ float2 both() const {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Two unpack(uint32_t x) {
+    return Two(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack(Two x) {
+    const float2 f = x.both();
+    return as_u32(__floats2bfloat162_rn(f.x, f.y));
+}
+
+// Quotient d / y, y of at most 8 significant bits and r within an ulp of 1 / y,
+// rounded as the division rounds it: q = d r is off by an ulp or three,
+// e = d - q y is exact, and q + e r differs from d / y by 2^-45 of it before its
+// one rounding (Markstein's correction).  d / y is no midpoint of two fp32 numbers
+// (a midpoint times y has more than d's 24 bits) and no nearer to one than 2^-33,
+// so that rounding is the division's.  Ties of the codes rely on it: differences
+// of bf16 numbers meet half steps often.
+__device__ __forceinline__ Two quotient(Two d, Two minus_y, Two r) {
+    const Two q = d * r;
+    return fma2(fma2(q, minus_y, d), r, q);
+}
+
+// Codes of 8 channels, and the group's (s, m) pair.
+__device__ __forceinline__ uint32_t quantise8(const uint32_t (&x)[4], float2 range, uint32_t& pair) {
+    const float lo = range.x, span = __fsub_rn(range.y, lo);
+    float s = __bfloat162float(__float2bfloat16_rn(
+        quotient(Two(span, 0.f), Two(-15.f, -15.f), Two(1.f / 15.f, 1.f / 15.f)).both().x));
+    if (s < 7.888609052210118e-31f) s = 0.f;  // 2^-100
+    pair = as_u32(__floats2bfloat162_rn(s, lo));
+    uint32_t word = 0;
+    if (s > 0.f) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        const Two minus_lo(-lo, -lo), minus_s(-s, -s), rr(r, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // 1.5 2^23 more: the low bits are the nearest whole number, ties to even.
+            // It is at most 15: s is span / 15 to 2^-9, so the quotient is below 15.1.
+            const float2 c = (quotient(unpack(x[i]) + minus_lo, minus_s, rr) + Two(12582912.f, 12582912.f)).both();
+            word += (__float_as_uint(c.x) << (8 * i)) + (__float_as_uint(c.y) << (8 * i + 4));
+        }
+        word -= 0x3f400000u;  // the eight shifted 0x4b400000, modulo 2^32
+    }
+    if (!(span <= 3.402823466e38f)) {
+        pair = 0x7fff7fffu;  // NaN, NaN
+        word = 0;
+    }
+    return word;
+}
+
+// A thread takes 8 channels of one token's keys and values in up to `heads_thread`
+// heads: the angles are computed once for them, the G/8 threads of a group find
+// its range with shuffles.  Bound: HBM, k and v once and the records.
+template <int D, int G, int ROT>
+__global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int heads_thread) {
     using L = Kv4<D, G>;
     constexpr int kOct = D / 8;
-    const long long item = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    const int oct = static_cast<int>(item % kOct);
-    const int is_v = static_cast<int>(item / kOct) & 1;
-    const long long th = item / (2 * kOct);
-    const int h = static_cast<int>(th % p.pages.heads);
-    const long long t_long = th / p.pages.heads;
+    const int lane = threadIdx.x & 31;
+    const int oct = threadIdx.x % kOct;
+    const long long t_long = static_cast<long long>(blockIdx.x) * (256 / kOct) + threadIdx.x / kOct;
     const int t = static_cast<int>(t_long < p.total ? t_long : p.total - 1);
-    bool live = t_long < p.total;
     const int b = sequence_of(p.cu_new, p.B, t);
-    live = live && b >= 0;
+    bool live = t_long < p.total && b >= 0;
     long long slot = 0, pos = 0;
     unsigned char* block = nullptr;
     if (live) {
-        const int n = p.cu_new[b + 1] - p.cu_new[b];
-        slot = static_cast<long long>(p.lengths[b]) - n + (t - p.cu_new[b]);
+        const int begin = p.cu_new[b], n = p.cu_new[b + 1] - begin;
+        slot = static_cast<long long>(p.lengths[b]) - n + (t - begin);
+        if (p.positions != nullptr)
+            pos = p.pos64 ? static_cast<const long long*>(p.positions)[t]
+                          : static_cast<long long>(static_cast<const int*>(p.positions)[t]);
+        else
+            pos = slot;
         if (slot < 0 || slot >= p.pages.capacity() || (p.slots != 0 && slot >= p.slots)) {
             report(kStatusBadSeqlen);
             live = false;
@@ -91,66 +182,112 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p) {
             if (at < 0) {
                 report(kStatusBadPage);
                 live = false;
-            } else {
-                block = p.pages.pool + at + h * p.pages.head_bytes();
             }
-            pos = slot;
-            if (p.positions != nullptr)
-                pos = p.pos64 ? static_cast<const long long*>(p.positions)[t]
-                              : static_cast<long long>(static_cast<const int*>(p.positions)[t]);
+            block = p.pages.pool + at;
         }
     }
-    const __nv_bfloat16* row = is_v ? p.v + t * p.v_t + h * p.v_h : p.k + t * p.k_t + h * p.k_h;
-    float x[8];
+    // angles of this thread's channels: cos, and sin with the sign of the partner's term
+    float cs[ROT == kInterleaved ? 4 : 8], sn[ROT == kInterleaved ? 4 : 8];
+    const int half = p.R >> 1;
+    const bool turned = ROT != kNone && oct * 8 < p.R;
+    if constexpr (ROT != kNone) {
+        if (turned) {
+            constexpr int N = ROT == kInterleaved ? 4 : 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (!is_v && p.freq != nullptr) x[i] = rotated(p, row, oct * 8 + i, pos);
-        else x[i] = __bfloat162float(row[oct * 8 + i]);
-    }
-    float lo = x[0], hi = x[0];
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        nan = nan || isnan(x[i]);
-    }
-    if (nan) hi = INFINITY;  // makes the range infinite
-#pragma unroll
-    for (int o = 1; o < G / 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const float range = __fsub_rn(hi, lo);
-    float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.f)));
-    const bool bad = !(range <= 3.402823466e38f);
-    if (s < 7.888609052210118e-31f) s = 0.f;  // 2^-100
-    uint32_t word = 0;
-    if (!bad && s > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = fminf(rintf(__fdiv_rn(__fsub_rn(x[i], lo), s)), 15.f);
-            word |= static_cast<uint32_t>(c) << (4 * i);
+            for (int i = 0; i < N; ++i) {
+                const int c = oct * 8 + i;  // channel (the pair, where interleaved)
+                int pair = c < half ? c : c - half;
+                bool first = c < half;
+                if constexpr (ROT == kInterleaved) {
+                    pair = oct * 4 + i;
+                    first = true;
+                } else if (ROT == kAny && p.interleaved) {
+                    pair = c >> 1;
+                    first = (c & 1) == 0;
+                }
+                if (ROT == kAny && c >= p.R) continue;
+                rope_angle(pos, p.freq[pair], p.amp, cs[i], sn[i]);
+                if (!first) sn[i] = -sn[i];
+            }
         }
     }
-    if (!live) return;
     const int r = static_cast<int>(slot & 15), g = oct >> 2, j = oct & 3;
-    if (is_v) {
-        unsigned short* codes = reinterpret_cast<unsigned short*>(block + L::kValueCodes + r * L::kRow);
-        codes[(2 * j) * (D / 32) + g] = static_cast<unsigned short>(word);
-        codes[(2 * j + 1) * (D / 32) + g] = static_cast<unsigned short>(word >> 16);
-    } else {
-        reinterpret_cast<uint32_t*>(block + L::kKeyCodes + r * L::kRow)[j * (D / 32) + g] = word;
-    }
-    if (oct % (G / 8) == 0) {
-        const __nv_bfloat162 sm = bad ? __floats2bfloat162_rn(NAN, NAN) : __floats2bfloat162_rn(s, lo);
-        *reinterpret_cast<__nv_bfloat162*>(block + (is_v ? L::kValueScales : L::kKeyScales) + r * L::kScaleRow +
-                                           oct / (G / 8) * 4) = sm;
-    }
-    if (is_v == 0 && oct == 0) {
-        const long long at = (static_cast<long long>(b) * p.pages.heads + h) * p.slots + slot;
-        if (p.weights != nullptr) p.weights[at] = 0.f;
-        if (p.slot_positions != nullptr) p.slot_positions[at] = static_cast<int>(pos);
+    const int h1 = min(p.pages.heads, (static_cast<int>(blockIdx.y) + 1) * heads_thread);
+    const int h0 = blockIdx.y * heads_thread;
+    const __nv_bfloat16* krow = p.k + t * p.k_t + h0 * p.k_h;
+    const __nv_bfloat16* vrow = p.v + t * p.v_t + h0 * p.v_h + oct * 8;
+    block += h0 * p.pages.head_bytes() + r * L::kRow;
+    uint4 kraw = *reinterpret_cast<const uint4*>(krow + oct * 8), vraw = *reinterpret_cast<const uint4*>(vrow);
+    for (int h = h0; h < h1; ++h) {
+        // the next head's rows are on their way while this one's are quantised
+        uint4 knext = kraw, vnext = vraw;
+        if (h + 1 < h1) {
+            knext = *reinterpret_cast<const uint4*>(krow + p.k_h + oct * 8);
+            vnext = *reinterpret_cast<const uint4*>(vrow + p.v_h);
+        }
+        uint32_t kx[4] = {kraw.x, kraw.y, kraw.z, kraw.w};
+        const uint32_t vx[4] = {vraw.x, vraw.y, vraw.z, vraw.w};
+        if constexpr (ROT == kHalf) {
+            const int other = turned ? (oct * 8 < half ? oct + half / 8 : oct - half / 8) : oct;
+            uint32_t y[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) y[w] = __shfl_sync(0xffffffffu, kx[w], lane - lane % kOct + other);
+            if (turned) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w)  // rope_turn of two channels
+                    kx[w] = pack(fma2(unpack(kx[w]), Two(cs[2 * w], cs[2 * w + 1]),
+                                      unpack(y[w]) * Two(-sn[2 * w], -sn[2 * w + 1])));
+            }
+        } else if constexpr (ROT == kInterleaved) {
+            if (turned) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float a0 = __uint_as_float(kx[w] << 16), a1 = __uint_as_float(kx[w] & 0xffff0000u);
+                    kx[w] = as_u32(__floats2bfloat162_rn(rope_turn(a0, a1, cs[w], sn[w]), rope_turn(a1, a0, cs[w], -sn[w])));
+                }
+            }
+        } else if constexpr (ROT == kAny) {
+            if (turned) {
+                float z[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = oct * 8 + i;
+                    z[i] = __bfloat162float(krow[c]);
+                    if (c < p.R) {
+                        const int other = p.interleaved ? c ^ 1 : (c < half ? c + half : c - half);
+                        z[i] = rope_turn(z[i], __bfloat162float(krow[other]), cs[i], sn[i]);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) kx[w] = as_u32(__floats2bfloat162_rn(z[2 * w], z[2 * w + 1]));
+            }
+        }
+        uint32_t kpair, vpair;
+        const uint32_t kw = quantise8(kx, range_of_group<G>(kx), kpair);
+        uint32_t vw = quantise8(vx, range_of_group<G>(vx), vpair);
+        // a value's 4 channels go to half-word r D/32 + g: even and odd slices meet in a word
+        const uint32_t give = g & 1 ? vw & 0xffffu : vw >> 16;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
+        vw = g & 1 ? got | (vw & 0xffff0000u) : (vw & 0xffffu) | got << 16;
+        if (live) {
+            reinterpret_cast<uint32_t*>(block + L::kKeyCodes)[j * (D / 32) + g] = kw;
+            reinterpret_cast<uint32_t*>(block + L::kValueCodes)[((2 * j + (g & 1)) * (D / 32) + g) >> 1] = vw;
+            if (oct % (G / 8) == 0) {
+                unsigned char* to = block + r * (L::kScaleRow - L::kRow) + oct / (G / 8) * 4;
+                *reinterpret_cast<uint32_t*>(to + L::kKeyScales) = kpair;
+                *reinterpret_cast<uint32_t*>(to + L::kValueScales) = vpair;
+            }
+            if (oct == 0) {
+                const long long at = (static_cast<long long>(b) * p.pages.heads + h) * p.slots + slot;
+                if (p.weights != nullptr) p.weights[at] = 0.f;
+                if (p.slot_positions != nullptr) p.slot_positions[at] = static_cast<int>(pos);
+            }
+        }
+        krow += p.k_h;
+        vrow += p.v_h;
+        block += p.pages.head_bytes();
+        kraw = knext;
+        vraw = vnext;
     }
 }
 
@@ -162,58 +299,66 @@ struct ReadParams {
     __nv_bfloat16* k;
     __nv_bfloat16* v;
     int B, count;
-    long long items;
 };
 
-// One thread restores 8 channels of a token's key and value.
+// One thread restores 8 channels of the keys and values of kTokensThread tokens.
+// Bound: HBM, mostly the writes.
+constexpr int kTokensThread = 4;
 template <int D, int G>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(ReadParams p) {
     using L = Kv4<D, G>;
-    constexpr int kOct = D / 8;
-    const long long item = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    if (item >= p.items) return;
-    const int oct = static_cast<int>(item % kOct);
-    const long long row = item / kOct;
-    const int i = static_cast<int>(row % p.count);
-    const long long bh = row / p.count;
-    const int h = static_cast<int>(bh % p.pages.heads), b = static_cast<int>(bh / p.pages.heads);
-    const long long slot = (p.start != nullptr ? static_cast<long long>(p.start[b]) : 0) + i;
-    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot < p.lengths[b]) {
-        long long at = -1;
-        if (slot < 0 || slot >= p.pages.capacity()) {
-            report(kStatusBadSeqlen);
-        } else {
-            at = p.pages.block_of(b, static_cast<int>(slot >> 4));
-            if (at < 0) report(kStatusBadPage);
-        }
-        if (at >= 0) {
-            const unsigned char* block = p.pages.pool + at + h * p.pages.head_bytes();
-            const int r = static_cast<int>(slot & 15), g = oct >> 2, j = oct & 3;
-            const uint32_t kw = reinterpret_cast<const uint32_t*>(block + L::kKeyCodes + r * L::kRow)[j * (D / 32) + g];
-            const unsigned short* vc = reinterpret_cast<const unsigned short*>(block + L::kValueCodes + r * L::kRow);
-            const uint32_t vw = vc[2 * j * (D / 32) + g] | static_cast<uint32_t>(vc[(2 * j + 1) * (D / 32) + g]) << 16;
-            const int so = r * L::kScaleRow + oct / (G / 8) * 4;
-            const float2 ks = kv4_scale(*reinterpret_cast<const uint32_t*>(block + L::kKeyScales + so));
-            const float2 vs = kv4_scale(*reinterpret_cast<const uint32_t*>(block + L::kValueScales + so));
+    constexpr int kOct = D / 8, kRows = 256 / kOct;
+    const int oct = threadIdx.x % kOct, g = oct >> 2, j = oct & 3;
+    const int bh = blockIdx.y, b = bh / p.pages.heads, h = bh - b * p.pages.heads;
+    const int len = p.lengths[b], start = p.start != nullptr ? p.start[b] : 0;
+    const int i0 = blockIdx.x * (kRows * kTokensThread) + threadIdx.x / kOct;
+    const unsigned char* block[kTokensThread];
+    uint32_t kw[kTokensThread], vw[kTokensThread], ks[kTokensThread], vs[kTokensThread];
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t word = w ? vw : kw;
-                const float2 sm = w ? vs : ks;
-                uint32_t pk[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(
-                        fmaf(static_cast<float>(word >> (8 * e) & 15u), sm.x, sm.y),
-                        fmaf(static_cast<float>(word >> (8 * e + 4) & 15u), sm.x, sm.y));
-                    pk[e] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                out[w] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    for (int x = 0; x < kTokensThread; ++x) {
+        const long long slot = static_cast<long long>(start) + i0 + x * kRows;
+        block[x] = nullptr;
+        if (i0 + x * kRows < p.count && slot < len) {
+            if (slot < 0 || slot >= p.pages.capacity()) {
+                report(kStatusBadSeqlen);
+            } else {
+                const long long at = p.pages.block_of(b, static_cast<int>(slot >> 4));
+                if (at < 0) report(kStatusBadPage);
+                else block[x] = p.pages.pool + at + h * p.pages.head_bytes();
             }
         }
     }
-    reinterpret_cast<uint4*>(p.k)[item] = out[0];
-    reinterpret_cast<uint4*>(p.v)[item] = out[1];
+#pragma unroll
+    for (int x = 0; x < kTokensThread; ++x) {
+        const int r = (start + i0 + x * kRows) & 15, so = r * L::kScaleRow + oct / (G / 8) * 4;
+        kw[x] = vw[x] = ks[x] = vs[x] = 0;
+        if (block[x] != nullptr) {
+            kw[x] = reinterpret_cast<const uint32_t*>(block[x] + L::kKeyCodes + r * L::kRow)[j * (D / 32) + g];
+            vw[x] = reinterpret_cast<const uint32_t*>(block[x] + L::kValueCodes + r * L::kRow)[((2 * j + (g & 1)) * (D / 32) + g) >> 1];
+            ks[x] = *reinterpret_cast<const uint32_t*>(block[x] + L::kKeyScales + so);
+            vs[x] = *reinterpret_cast<const uint32_t*>(block[x] + L::kValueScales + so);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < kTokensThread; ++x) {
+        // the word holds half-words of two slices: the other one's goes to the neighbour
+        const uint32_t give = g & 1 ? vw[x] & 0xffffu : vw[x] >> 16;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
+        const uint32_t v = g & 1 ? got | (vw[x] & 0xffff0000u) : (vw[x] & 0xffffu) | got << 16;
+        if (i0 + x * kRows >= p.count) continue;
+        const long long out = (static_cast<long long>(bh) * p.count + i0 + x * kRows) * kOct + oct;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint32_t word = w ? v : kw[x];
+            const float2 sm = kv4_scale(w ? vs[x] : ks[x]);
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                pk[e] = as_u32(__floats2bfloat162_rn(fmaf(static_cast<float>(word >> (8 * e) & 15u), sm.x, sm.y),
+                                                     fmaf(static_cast<float>(word >> (8 * e + 4) & 15u), sm.x, sm.y)));
+            __stcs(reinterpret_cast<uint4*>(w ? p.v : p.k) + out, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        }
+    }
 }
 
 // ------------------------------------------------------------------ evict
@@ -397,25 +542,26 @@ __global__ void __launch_bounds__(256) fa_kv4_move_kernel(EvictParams p, int D, 
 }
 
 Kv4Pages pages_of(const Kv4Shape& c, void* pool, const int* table) {
-    Kv4Pages x;
-    x.pool = static_cast<unsigned char*>(pool);
-    x.table = table;
-    x.width = c.width;
-    x.num_pages = c.num_pages;
-    x.heads = c.Hkv;
-    x.blocks_page = c.page_size / 16;
-    x.block_bytes = 16LL * (c.D + 8 * c.D / c.group);
-    return x;
+    return kv4_pages(static_cast<unsigned char*>(pool), table, c.width, c.num_pages, c.Hkv, c.page_size, c.D, c.group);
 }
 
 int last_error() { return cudaGetLastError() == cudaSuccess ? 0 : -5; }
+
+template <int D, int G>
+int append(const AppendParams& p, int rot, dim3 grid, int per, cudaStream_t stream) {
+    if (rot == kNone) fa_kv4_append_kernel<D, G, kNone><<<grid, 256, 0, stream>>>(p, per);
+    else if (rot == kHalf) fa_kv4_append_kernel<D, G, kHalf><<<grid, 256, 0, stream>>>(p, per);
+    else if (rot == kInterleaved) fa_kv4_append_kernel<D, G, kInterleaved><<<grid, 256, 0, stream>>>(p, per);
+    else fa_kv4_append_kernel<D, G, kAny><<<grid, 256, 0, stream>>>(p, per);
+    return last_error();
+}
 
 }  // namespace
 
 int launch_kv4_append(const Kv4Shape& c, void* pool, const int* table, const void* k, const void* v, long long k_t,
                       long long k_h, long long v_t, long long v_h, const int* lengths, const int* cu_new, int total,
                       const void* positions, int pos64, const void* freq, int R, int interleaved, float amplitude,
-                      float* weights, int* slot_positions, long long slots, cudaStream_t stream) {
+                      float* weights, int* slot_positions, long long slots, cudaStream_t stream, int num_sms) {
     AppendParams p{};
     p.k = static_cast<const __nv_bfloat16*>(k);
     p.v = static_cast<const __nv_bfloat16*>(v);
@@ -437,16 +583,16 @@ int launch_kv4_append(const Kv4Shape& c, void* pool, const int* table, const voi
     p.slots = slots;
     p.B = c.B;
     p.total = total;
-    const long long items = static_cast<long long>(total) * c.Hkv * (c.D / 4);
-    const unsigned blocks = static_cast<unsigned>((items + 255) / 256);
-    if (c.D == 64) {
-        if (c.group == 32) fa_kv4_append_kernel<64, 32><<<blocks, 256, 0, stream>>>(p);
-        else fa_kv4_append_kernel<64, 64><<<blocks, 256, 0, stream>>>(p);
-    } else {
-        if (c.group == 32) fa_kv4_append_kernel<128, 32><<<blocks, 256, 0, stream>>>(p);
-        else fa_kv4_append_kernel<128, 64><<<blocks, 256, 0, stream>>>(p);
-    }
-    return last_error();
+    const int rot = freq == nullptr                            ? kNone
+                    : interleaved ? (R % 8 == 0 ? kInterleaved : kAny)
+                                  : (R % 16 == 0 ? kHalf : kAny);
+    // up to 8 heads a thread, fewer while that leaves SMs without work
+    const long long rows = (total + 256 / (c.D / 8) - 1) / (256 / (c.D / 8));
+    int per = 8;
+    while (per > 1 && rows * ((c.Hkv + per - 1) / per) < 4LL * num_sms) per >>= 1;
+    const dim3 grid(static_cast<unsigned>(rows), (c.Hkv + per - 1) / per);
+    if (c.D == 64) return c.group == 32 ? append<64, 32>(p, rot, grid, per, stream) : append<64, 64>(p, rot, grid, per, stream);
+    return c.group == 32 ? append<128, 32>(p, rot, grid, per, stream) : append<128, 64>(p, rot, grid, per, stream);
 }
 
 int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* start,
@@ -459,8 +605,8 @@ int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const
     p.v = static_cast<__nv_bfloat16*>(v);
     p.B = c.B;
     p.count = count;
-    p.items = static_cast<long long>(c.B) * c.Hkv * count * (c.D / 8);
-    const unsigned blocks = static_cast<unsigned>((p.items + 255) / 256);
+    const int rows = 256 / (c.D / 8) * kTokensThread;
+    const dim3 blocks((count + rows - 1) / rows, c.B * c.Hkv);
     if (c.D == 64) {
         if (c.group == 32) fa_kv4_read_kernel<64, 32><<<blocks, 256, 0, stream>>>(p);
         else fa_kv4_read_kernel<64, 64><<<blocks, 256, 0, stream>>>(p);

@@ -60,10 +60,7 @@ constexpr int kStages = 2;
 constexpr float kAhead = 4.f;
 // Places on the line for a head's start, its queries' and first copies' latency
 // and its outputs, in units of 32 or 64 tokens.
-#ifndef KSTART
-#define KSTART 2
-#endif
-constexpr int kStart = KSTART;
+constexpr int kStart = 2;
 
 struct DecParams {
     const __nv_bfloat16* q;
@@ -1000,13 +997,8 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
                       float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms) {
     DecParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
-    p.pages.pool = static_cast<unsigned char*>(const_cast<void*>(pool));
-    p.pages.table = table;
-    p.pages.width = c.width;
-    p.pages.num_pages = c.num_pages;
-    p.pages.heads = c.Hkv;
-    p.pages.blocks_page = c.page_size / 16;
-    p.pages.block_bytes = 16LL * (c.D + 8 * c.D / c.group);
+    p.pages = kv4_pages(static_cast<unsigned char*>(const_cast<void*>(pool)), table, c.width, c.num_pages, c.Hkv,
+                        c.page_size, c.D, c.group);
     p.lengths = lengths;
     p.B = c.B;
     p.R = Hq / c.Hkv * Tq;

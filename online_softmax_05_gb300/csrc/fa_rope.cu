@@ -6,10 +6,8 @@
 // (interleaved), R the rotated channels; the others are copied.  The gradient
 // is the same map with -sin.
 //
-// Angles.  f_i comes as a whole number of 2^-64 turns per position, so p f_i
-// modulo one turn is a wrapping 64-bit product: exact for every position,
-// however far (a product in fp32 is off by 0.06 rad at position 10^6).  Its
-// top 32 bits, read as a signed fraction of a turn, go to sincospif.
+// Angles are exact modulo a turn at every position (fa_rope.cuh); a product in
+// fp32 would be off by 0.06 rad at position 10^6.
 //
 // One thread takes the same pairs of one token in several heads, so that an
 // angle is computed once for all of them.  Bound: HBM, each element read and
@@ -21,6 +19,7 @@
 #include <cstdint>
 
 #include "fa_internal.h"
+#include "fa_rope.cuh"
 
 namespace fa {
 namespace {
@@ -95,11 +94,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freq[pair0 + i];
-            const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
-            sincospif(x, &sn[i], &cs[i]);
-            cs[i] *= p.amp;
-            sn[i] *= p.inverse ? -p.amp : p.amp;
+            rope_angle(pos, p.freq[pair0 + i], p.amp, cs[i], sn[i]);
+            if (p.inverse) sn[i] = -sn[i];
         }
     }
     const bool tail = V > 1 || c1 < p.D;  // an odd head has a lone last channel
@@ -128,8 +124,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
                 for (int i = 0; i < V; ++i) {
                     const int j1 = INTER ? 2 * i : i, j2 = INTER ? 2 * i + 1 : V + i;
                     const float x1 = to_f(in2[j1]), x2 = to_f(in2[j2]);
-                    in2[j1] = from_f<E>(x1 * cs[i] - x2 * sn[i]);
-                    in2[j2] = from_f<E>(x2 * cs[i] + x1 * sn[i]);
+                    in2[j1] = from_f<E>(rope_turn(x1, x2, cs[i], sn[i]));
+                    in2[j2] = from_f<E>(rope_turn(x2, x1, cs[i], -sn[i]));
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
