@@ -1,5 +1,6 @@
 // fa_kv4_cache.cu -- writing to the 4-bit paged key/value cache, reading it
 // back, and evicting from it (layout: fa_kv4.cuh).
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -7,6 +8,8 @@
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_rope.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace fa {
 namespace {
@@ -372,171 +375,333 @@ struct EvictParams {
     int* lengths_out;
     int* source;   // [B][Hkv][budget]
     int* holes;    // workspace: [B][Hkv][budget]
-    int* n_holes;  // workspace: [B][Hkv]
+    int2* moved;   // workspace: [B][Hkv][budget] (from, to)
     long long slots;
     int budget, recent;
+    int row, scale;   // bytes of a token's codes and scales
+    int slots_shared; // slots whose weights and positions fit into a CTA's shared memory
 };
 
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
+constexpr int kBins = 2 * kEvictThreads;
+static_assert(kEvictWarps == 32 && kBins == 1 << 11, "the block's sums are scanned by one warp");
+constexpr int kEvictCluster = 8;
+constexpr uint32_t kProtected = 0xffffffffu;
 
-// Rank of a slot: larger is kept first.  Recent tokens before all others, then
-// by weight; a NaN weight counts as the least.
-__device__ __forceinline__ uint32_t rank_of(float w, int pos, long long newest, int recent) {
-    if (static_cast<long long>(pos) > newest - recent) return 0xffffffffu;
+// Order of the weights as whole numbers; a NaN weight counts as the least.
+__device__ __forceinline__ uint32_t key_of(float w) {
     if (isnan(w)) return 0u;
     const uint32_t u = __float_as_uint(w + 0.f);  // -0 counts as 0
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ int warp_inclusive(int x, int lane) {
+__device__ __forceinline__ int2 warp_inclusive(int2 v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+        if (lane >= o) {
+            v.x += x;
+            v.y += y;
+        }
     }
-    return x;
+    return v;
 }
-
-// Inclusive prefix sum over the block; `total` gets the whole sum.
-__device__ __forceinline__ int block_inclusive(int x, int* warp_sums, int& total) {
+// Sums over the warps before this one of a pair that each warp holds, and over the block.
+__device__ __forceinline__ int2 warps_before(int2 v, int2* warp_sums, int2& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int in_warp = warp_inclusive(x, lane);
+    __syncthreads();  // the sums of the scan before are read
+    if (lane == 0) warp_sums[warp] = v;
     __syncthreads();
-    if (lane == 31) warp_sums[warp] = in_warp;
-    __syncthreads();
-    if (warp == 0) warp_sums[lane] = warp_inclusive(warp_sums[lane], lane);
-    __syncthreads();
-    total = warp_sums[kEvictThreads / 32 - 1];
-    return in_warp + (warp > 0 ? warp_sums[warp - 1] : 0);
+    const int2 in = warp_inclusive(warp_sums[lane], lane);
+    total = make_int2(__shfl_sync(0xffffffffu, in.x, 31), __shfl_sync(0xffffffffu, in.y, 31));
+    return make_int2(__shfl_sync(0xffffffffu, in.x, warp) - v.x, __shfl_sync(0xffffffffu, in.y, warp) - v.y);
 }
 
-// One CTA per (sequence, head): the rank of the budget-th token by a radix
-// select of 8 bits a pass, then the kept map.  Ties go to the lowest slot.
-__global__ void __launch_bounds__(kEvictThreads) fa_kv4_select_kernel(EvictParams p) {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[32];
-    __shared__ long long s_newest;
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
-    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+// One cluster per (sequence, head), each CTA a slice of the slots, whose weights
+// and positions stay in shared memory.  A slot's rank is its weight's order, and
+// above all others where it is protected; the rank of the budget-th token is found by a radix select over the
+// range that the keys span, 11 bits of it a pass, with the CTAs' histograms summed
+// through distributed shared memory; ties go to the lowest slots.  Every hole lies
+// below the new length and every mover at or above it, so the n-th mover takes the
+// n-th hole, no copy touches what another reads, and the moves run in any order.
+// Bound: latency of about ten dependent steps (passes, scans, cluster barriers).
+__global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams p) {
+    extern __shared__ int2 kept_here[];  // (weight's bits, position) of the slice
+    __shared__ int hist[2][kBins];
+    __shared__ int2 warp_sums[kEvictWarps];
+    __shared__ int s_share[8];  // what the other CTAs of the cluster read
+    __shared__ uint32_t s_lo, s_hi;
+    __shared__ int s_need, s_all;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int C = cluster.num_blocks(), rank = cluster.block_rank();
+    const int b = blockIdx.y, h = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31;
     const long long bh = static_cast<long long>(b) * p.pages.heads + h;
     const float* w = p.weights + bh * p.slots;
     const int* pos = p.slot_positions + bh * p.slots;
     float* w_out = p.weights_out + bh * p.slots;
     int* pos_out = p.positions_out + bh * p.slots;
     int* source = p.source + bh * p.budget;
+    int* holes = p.holes + bh * p.budget;
     int len = p.lengths[b];
     if (len < 0 || len > p.slots || len > p.pages.capacity()) {
         report(kStatusBadSeqlen);
         len = 0;
     }
-    const int left = min(len, p.budget);
-    if (h == 0 && tid == 0) p.lengths_out[b] = left;
-    for (long long i = left + tid; i < p.slots; i += kEvictThreads) {
+    const int left = min(len, p.budget), step = C * kEvictThreads, me = rank * kEvictThreads + tid;
+    if (h == 0 && me == 0) p.lengths_out[b] = left;
+    for (long long i = left + me; i < p.slots; i += step) {
         w_out[i] = 0.f;
         pos_out[i] = -1;
     }
-    for (int i = left + tid; i < p.budget; i += kEvictThreads) source[i] = -1;
+    for (int i = left + me; i < p.budget; i += step) source[i] = -1;
     if (len <= p.budget) {
-        for (int i = tid; i < left; i += kEvictThreads) {
+        for (int i = me; i < left; i += step) {
             w_out[i] = w[i];
             pos_out[i] = pos[i];
             source[i] = i;
         }
-        if (tid == 0) p.n_holes[bh] = 0;
-        return;
+        return;  // whole cluster
     }
-    // the newest position
-    long long newest = LLONG_MIN;
-    for (int i = tid; i < len; i += kEvictThreads) newest = max(newest, static_cast<long long>(pos[i]));
-    if (tid == 0) s_newest = LLONG_MIN;
+    const int slice = (len + C - 1) / C, s0 = min(rank * slice, len), n = min(len, s0 + slice) - s0;
+    const bool shared = slice <= p.slots_shared;
+    // sum or largest over the cluster's first CTAs of what each left in s_share[at]
+    auto over_cluster = [&](int at, bool largest, int upto) -> int {
+        const int mine = lane < upto ? cluster.map_shared_rank(s_share, lane)[at] : largest ? INT_MIN : 0;
+        return largest ? __reduce_max_sync(0xffffffffu, mine) : __reduce_add_sync(0xffffffffu, mine);
+    };
+    int2* moved = p.moved + bh * p.budget;
+    if (tid < 8) s_share[tid] = tid == 0 || tid >= 6 ? INT_MIN : 0;
     __syncthreads();
-    atomicMax(&s_newest, newest);
+    // ---- the slice, and the newest position
+    int newest = INT_MIN;
+#pragma unroll 8
+    for (int i = tid; i < n; i += kEvictThreads) {
+        const int2 x = make_int2(shared ? __float_as_int(w[s0 + i]) : 0, pos[s0 + i]);
+        newest = max(newest, x.y);
+        if (shared) kept_here[i] = x;
+    }
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) atomicMax(&s_share[0], newest);
+    cluster.sync();
+    // positions above it are protected
+    const long long border = p.recent > 0 ? static_cast<long long>(over_cluster(0, true, C)) - p.recent : LLONG_MAX;
+    auto slot_at = [&](int i) -> int2 {
+        return shared ? kept_here[i] : make_int2(__float_as_int(w[s0 + i]), pos[s0 + i]);
+    };
+    auto key_at = [&](int i) -> uint32_t {
+        const int2 x = slot_at(i);
+        return static_cast<long long>(x.y) > border ? kProtected : key_of(__int_as_float(x.x));
+    };
+    // ---- how many are protected, and the range of the others' keys
+    {
+        int count = 0;
+        uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll 4
+        for (int i = tid; i < n; i += kEvictThreads) {
+            const uint32_t k = key_at(i);
+            if (k == kProtected) {
+                ++count;
+            } else {
+                lo = min(lo, k);
+                hi = max(hi, k);
+            }
+        }
+        count = __reduce_add_sync(0xffffffffu, count);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            atomicAdd(&s_share[1], count);
+            // unsigned order as signed: the top bit flipped; the least as the largest of the complement
+            atomicMax(&s_share[6], static_cast<int>(~lo ^ 0x80000000u));
+            atomicMax(&s_share[7], static_cast<int>(hi ^ 0x80000000u));
+        }
+        cluster.sync();
+    }
+    uint32_t lo = ~(static_cast<uint32_t>(over_cluster(6, true, C)) ^ 0x80000000u);
+    uint32_t hi = static_cast<uint32_t>(over_cluster(7, true, C)) ^ 0x80000000u;
+    int need = p.budget - over_cluster(1, false, C);
+    // ---- the rank of the last token kept: `need` more are taken from [lo, hi]
+    uint32_t threshold = kProtected;
+    int ties = p.budget;  // kept among those of exactly that rank
+    bool take_all = false;  // every rank from it on is kept
+    for (int pass = 0; need > 0; ++pass) {
+        const int bits = 32 - __clz(hi - lo), shift = max(0, bits - 11);
+        int* bin = hist[pass & 1];
+        for (int i = tid; i < kBins; i += kEvictThreads) bin[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
+            const int i = i0 + tid;
+            const uint32_t k = i < n ? key_at(i) : kProtected;
+            const bool in = k != kProtected && k >= lo && k <= hi;
+            const int at = in ? static_cast<int>((k - lo) >> shift) : -1;
+            // equal weights come in stretches: one addition for a warp that agrees
+            if (__all_sync(0xffffffffu, at == __shfl_sync(0xffffffffu, at, 0))) {
+                if (lane == 0 && at >= 0) atomicAdd(&bin[at], 32);
+            } else if (in) {
+                atomicAdd(&bin[at], 1);
+            }
+        }
+        cluster.sync();
+        // bins from the top down, two a thread
+        const int top = kBins - 2 - 2 * tid;
+        int2 sum = make_int2(0, 0);
+#pragma unroll
+        for (int c = 0; c < kEvictCluster; ++c) {
+            if (c >= C) break;
+            const int2 x = *reinterpret_cast<const int2*>(cluster.map_shared_rank(bin, c) + top);
+            sum.x += x.x;
+            sum.y += x.y;
+        }
+        const int2 in = warp_inclusive(make_int2(sum.x + sum.y, 0), lane);
+        int2 all;
+        const int warp_sum = __shfl_sync(0xffffffffu, in.x, 31);
+        int above = warps_before(make_int2(warp_sum, 0), warp_sums, all).x + in.x - sum.x - sum.y;
+        const int part[2] = {sum.y, sum.x};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (above < need && need <= above + part[x]) {
+                const uint32_t at = lo + (static_cast<uint32_t>(top + 1 - x) << shift);
+                s_lo = at;
+                s_hi = min(hi, at + ((1u << shift) - 1u));
+                s_need = need - above;
+                s_all = need == above + part[x];
+            }
+            above += part[x];
+        }
+        __syncthreads();
+        lo = s_lo;
+        hi = s_hi;
+        need = s_need;
+        // done with a bin of one rank, and with one that is kept whole
+        if (shift == 0 || s_all) {
+            threshold = lo;
+            ties = shift == 0 ? need : INT_MAX;
+            take_all = s_all;
+            break;
+        }
+    }
+    // ---- what is kept: each warp walks a stretch of the slice, 32 slots a step, with
+    // running counts of ties, holes and movers before it
+    const int warp = tid >> 5;
+    const int stretch = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+    const int r0 = min(warp * stretch, n), r1 = min(r0 + stretch, n);
+    const unsigned before = (1u << lane) - 1u;
+    int2 sum;
+    int tie0 = 0;
+    if (!take_all) {
+        int mine = 0;
+        for (int i = r0; i < r1; i += 32)
+            mine += __popc(__ballot_sync(0xffffffffu, i + lane < r1 && key_at(i + lane) == threshold));
+        tie0 = warps_before(make_int2(mine, 0), warp_sums, sum).x;
+        if (tid == 0) s_share[2] = sum.x;
+        cluster.sync();
+        tie0 += over_cluster(2, false, rank);
+    }
+    // f(slot, whether there is one, whether it is kept) for the stretch, the warp together
+    auto walk = [&](auto f) {
+        int tie = tie0;
+        for (int i = r0; i < r1; i += 32) {
+            const bool in = i + lane < r1;
+            const uint32_t k = in ? key_at(i + lane) : 0u;
+            bool keep = in && k >= threshold;
+            if (!take_all) {
+                const bool eq = in && k == threshold;
+                const unsigned same = __ballot_sync(0xffffffffu, eq);
+                if (eq) keep = tie + __popc(same & before) < ties;
+                tie += __popc(same);
+            }
+            f(s0 + i + lane, in, keep);
+        }
+    };
+    int2 mine = make_int2(0, 0);  // holes, movers
+    walk([&](int slot, bool in, bool keep) {
+        mine.x += __popc(__ballot_sync(0xffffffffu, in && !keep && slot < left));
+        mine.y += __popc(__ballot_sync(0xffffffffu, keep && slot >= left));
+    });
+    int2 at = warps_before(mine, warp_sums, sum);
     if (tid == 0) {
-        s_prefix = 0;
-        s_need = p.budget;
+        s_share[3] = sum.x;
+        s_share[4] = sum.y;
     }
-    __syncthreads();
-    newest = s_newest;
-    // threshold: the largest rank with at least `need` slots at or above it
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        const uint32_t prefix = s_prefix;
-        for (int i = tid; i < len; i += kEvictThreads) {
-            const uint32_t r = rank_of(w[i], pos[i], newest, p.recent);
-            if (shift == 24 || (r >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[r >> shift & 255], 1);
+    cluster.sync();
+    at.x += over_cluster(3, false, rank);
+    at.y += over_cluster(4, false, rank);
+    const int moves = over_cluster(4, false, C);
+    walk([&](int slot, bool in, bool keep) {
+        const bool hole = in && !keep && slot < left;
+        const unsigned all = __ballot_sync(0xffffffffu, hole);
+        if (hole) holes[at.x + __popc(all & before)] = slot;
+        at.x += __popc(all);
+        if (keep && slot < left) {
+            const int2 x = slot_at(slot - s0);
+            w_out[slot] = __int_as_float(x.x);
+            pos_out[slot] = x.y;
+            source[slot] = slot;
         }
-        __syncthreads();
-        if (tid == 0) {
-            int need = s_need, d = 255;
-            while (d > 0 && hist[d] < need) need -= hist[d--];
-            s_need = need;
-            s_prefix = prefix | static_cast<uint32_t>(d) << shift;
+    });
+    cluster.sync();  // the holes are listed
+    walk([&](int slot, bool in, bool keep) {
+        const bool mover = keep && slot >= left;
+        const unsigned all = __ballot_sync(0xffffffffu, mover);
+        if (mover) {
+            const int m = at.y + __popc(all & before), to = holes[m];
+            const int2 x = slot_at(slot - s0);
+            moved[m] = make_int2(slot, to);
+            w_out[to] = __int_as_float(x.x);
+            pos_out[to] = x.y;
+            source[to] = slot;
         }
-        __syncthreads();
-    }
-    const uint32_t threshold = s_prefix;
-    const int ties = s_need;  // slots of exactly the threshold that are kept, the first ones
-    // one walk over the slots: every hole lies before the new length and every
-    // kept token to be moved behind it, so the list of holes is complete when
-    // the first mover takes its place from it
-    int* holes = p.holes + bh * p.budget;
-    int done_ties = 0, done_holes = 0, done_movers = 0;
-    for (int base = 0; base < len; base += kEvictThreads) {
-        const int i = base + tid;
-        const bool in = i < len;
-        const uint32_t r = in ? rank_of(w[i], pos[i], newest, p.recent) : 0u;
-        const bool tie = in && r == threshold;
-        int n_ties, n_holes, n_movers;
-        const int tie_rank = block_inclusive(tie, warp_sums, n_ties) + done_ties;
-        const bool kept = in && (r > threshold || (tie && tie_rank <= ties));
-        const bool hole = in && i < left && !kept, mover = kept && i >= left;
-        const int hole_at = block_inclusive(hole, warp_sums, n_holes) - 1 + done_holes;
-        const int mover_at = block_inclusive(mover, warp_sums, n_movers) - 1 + done_movers;
-        if (hole) holes[hole_at] = i;
-        __syncthreads();
-        if (kept) {
-            const int to = mover ? holes[mover_at] : i;
-            w_out[to] = w[i];
-            pos_out[to] = pos[i];
-            source[to] = i;
+        at.y += __popc(all);
+    });
+    cluster.sync();  // and so are the moves
+    // ---- move the records: a lane finds the places of one, then 10 lanes (6 at
+    // D = 64) copy one, 16 bytes each and a scale row, several records at a time
+    const int codes = p.row / 16, parts = 2 * (codes + 1), at_once = 32 / parts;
+    const int which = lane / parts, part = lane % parts;
+    const int is_v = part > codes, y = is_v ? part - codes - 1 : part;
+    const bool code = y < codes;
+    const int size = code ? 16 : p.scale, pitch = code ? p.row : p.scale;
+    unsigned char* pool = p.pages.pool + h * p.pages.head_bytes() + is_v * 16 * (p.row + p.scale) + (code ? y * 16 : 16 * p.row);
+    const int warps = C * kEvictWarps, share = min(32, (moves + warps - 1) / warps);
+    for (int m0 = (rank * kEvictWarps + warp) * share; m0 < moves; m0 += warps * share) {
+        long long src = -1, dst = -1;  // of the record's block, its row in the low bits
+        if (lane < share && m0 + lane < moves) {
+            const int2 x = moved[m0 + lane];
+            src = p.pages.block_of(b, x.x >> 4);
+            dst = p.pages.block_of(b, x.y >> 4);
+            if (src < 0 || dst < 0) {
+                report(kStatusBadPage);
+                src = -1;
+            } else {  // blocks are multiples of 128 bytes
+                src |= x.x & 15;
+                dst |= x.y & 15;
+            }
         }
-        done_ties += n_ties;
-        done_holes += n_holes;
-        done_movers += n_movers;
-    }
-    if (tid == 0) p.n_holes[bh] = done_holes;
-}
-
-// Moves the records (codes and scales of key and value) of the movers into the
-// holes.  All sources lie behind the new length and all holes before it, so no
-// copy touches what another one reads.  One warp per record, 4 bytes a lane.
-__global__ void __launch_bounds__(256) fa_kv4_move_kernel(EvictParams p, int D, int groups) {
-    const int bh = blockIdx.y, lane = threadIdx.x & 31;
-    const int b = bh / p.pages.heads, h = bh % p.pages.heads;
-    const int n = p.n_holes[bh];
-    const int row = D / 2, scale = groups * 4;
-    const int half = 16 * (row + scale);
-    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
-        const int to = p.holes[static_cast<long long>(bh) * p.budget + i];
-        const int from = p.source[static_cast<long long>(bh) * p.budget + to];
-        const long long at = p.pages.block_of(b, from >> 4), dt = p.pages.block_of(b, to >> 4);
-        if (at < 0 || dt < 0) {
-            if (lane == 0) report(kStatusBadPage);
-            continue;
-        }
-        const unsigned char* src = p.pages.pool + at + h * p.pages.head_bytes();
-        unsigned char* dst = p.pages.pool + dt + h * p.pages.head_bytes();
-        const int words = (row + scale) / 4;  // of the key; as many of the value
-        for (int x = lane; x < 2 * words; x += 32) {
-            const int is_v = x >= words, y = is_v ? x - words : x;
-            const int base = is_v * half;
-            const int so = y < row / 4 ? base + (from & 15) * row + y * 4
-                                       : base + 16 * row + (from & 15) * scale + (y - row / 4) * 4;
-            const int to_off = y < row / 4 ? base + (to & 15) * row + y * 4
-                                           : base + 16 * row + (to & 15) * scale + (y - row / 4) * 4;
-            *reinterpret_cast<uint32_t*>(dst + to_off) = *reinterpret_cast<const uint32_t*>(src + so);
+        constexpr int kFlight = 4;
+        for (int x0 = 0; x0 < share; x0 += kFlight * at_once) {
+            uint4 data[kFlight];
+            unsigned char* to[kFlight];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const int x = x0 + f * at_once + which;
+                const long long sx = __shfl_sync(0xffffffffu, src, x & 31), dx = __shfl_sync(0xffffffffu, dst, x & 31);
+                to[f] = nullptr;
+                if (which < at_once && x < share && sx >= 0) {
+                    const unsigned char* from = pool + (sx & ~15LL) + (sx & 15) * pitch;
+                    to[f] = pool + (dx & ~15LL) + (dx & 15) * pitch;
+                    if (size == 16) data[f] = *reinterpret_cast<const uint4*>(from);
+                    else if (size == 8) data[f].x = reinterpret_cast<const uint2*>(from)->x, data[f].y = reinterpret_cast<const uint2*>(from)->y;
+                    else data[f].x = *reinterpret_cast<const uint32_t*>(from);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                if (to[f] == nullptr) continue;
+                if (size == 16) *reinterpret_cast<uint4*>(to[f]) = data[f];
+                else if (size == 8) *reinterpret_cast<uint2*>(to[f]) = make_uint2(data[f].x, data[f].y);
+                else *reinterpret_cast<uint32_t*>(to[f]) = data[f].x;
+            }
         }
     }
 }
@@ -618,7 +783,7 @@ int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const
 }
 
 size_t kv4_evict_workspace(int B, int Hkv, int budget) {
-    return static_cast<size_t>(B) * Hkv * (static_cast<size_t>(budget) + 1) * 4;
+    return static_cast<size_t>(B) * Hkv * static_cast<size_t>(budget) * 12;
 }
 
 int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int* lengths, const float* weights,
@@ -637,18 +802,35 @@ int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int*
     p.slots = slots;
     p.budget = budget;
     p.recent = recent;
-    const long long bh = static_cast<long long>(c.B) * c.Hkv;
-    p.holes = static_cast<int*>(workspace);
-    p.n_holes = p.holes + bh * budget;
-    fa_kv4_select_kernel<<<dim3(c.Hkv, c.B), kEvictThreads, 0, stream>>>(p);
-    if (last_error() != 0) return -5;
-    // about 8 CTAs per SM over all heads
-    long long per = (8LL * num_sms + bh - 1) / bh;
-    const long long most = (budget + 7) / 8;
-    if (per > most) per = most;
-    fa_kv4_move_kernel<<<dim3(static_cast<unsigned>(per), static_cast<unsigned>(bh)), 256, 0, stream>>>(p, c.D,
-                                                                                                        c.D / c.group);
-    return last_error();
+    p.moved = static_cast<int2*>(workspace);
+    p.holes = reinterpret_cast<int*>(p.moved + static_cast<size_t>(c.B) * c.Hkv * budget);
+    p.row = c.D / 2;
+    p.scale = c.D / c.group * 4;
+    // CTAs of a head: as many as run at once, with two thousand slots or more each,
+    // and no fewer than hold the slots in shared memory.  (Clusters of 16 do not all
+    // find room at once: 8 heads of 60007 slots took 95 us against 44 us with 8.)
+    constexpr int kSlotsMost = 24 * 1024;  // 192 KB
+    const long long heads = static_cast<long long>(c.B) * c.Hkv;
+    int cluster = 1;
+    while (cluster < kEvictCluster && (2 * cluster * heads <= num_sms && slots > 2048LL * cluster)) cluster *= 2;
+    while (cluster < kEvictCluster && slots > static_cast<long long>(kSlotsMost) * cluster) cluster *= 2;
+    const long long slice = (slots + cluster - 1) / cluster;
+    p.slots_shared = static_cast<int>(slice <= kSlotsMost ? slice : 0);
+    const int smem = p.slots_shared * 8;
+    if (cudaFuncSetAttribute(fa_kv4_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotsMost * 8) != cudaSuccess)
+        return -5;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c.Hkv * cluster, c.B);
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_kv4_evict_kernel, p) == cudaSuccess ? 0 : -5;
 }
 
 int kv4_cache_take_status() {
