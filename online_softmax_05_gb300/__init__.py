@@ -132,16 +132,17 @@ def _stream(s) -> int | None:
 def _raw_stream(device: int) -> int:
     """The current stream of a device, as the C ABI takes it."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's microsecond
+    return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _launch_on(tensor, stream, fn, *args):
     """fn(*args) with the tensor's device and the given stream (default: the device's
     current one) current, so that what fn allocates belongs to the stream that uses it."""
     import torch
-    if not tensor.is_cuda:
-        raise ValueError("CUDA tensors are required; there is no CPU fallback")
     dev = tensor.get_device()
+    if dev < 0:
+        raise ValueError("CUDA tensors are required; there is no CPU fallback")
     if stream is None and dev == torch.cuda.current_device():
         return fn(*args)
     with torch.cuda.device(dev):

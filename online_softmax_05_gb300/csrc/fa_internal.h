@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace fa {
 
 struct DebugKnobs {
@@ -83,6 +85,18 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
                       float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms);
 int kv4_cache_take_status();
 int kv4_decode_take_status();
+
+// Allows a kernel its dynamic shared memory, once per device (a microsecond a call otherwise).
+template <typename Kernel>
+inline bool allow_shared_memory(Kernel kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // Read and clear the device status word of each translation unit on the
 // current device (caller synchronises first).  Return 0 or a negative code.

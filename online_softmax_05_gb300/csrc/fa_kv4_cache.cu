@@ -817,8 +817,8 @@ int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int*
     const long long slice = (slots + cluster - 1) / cluster;
     p.slots_shared = static_cast<int>(slice <= kSlotsMost ? slice : 0);
     const int smem = p.slots_shared * 8;
-    if (cudaFuncSetAttribute(fa_kv4_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotsMost * 8) != cudaSuccess)
-        return -5;
+    static std::atomic<unsigned long long> allowed;
+    if (!allow_shared_memory(fa_kv4_evict_kernel, kSlotsMost * 8, allowed)) return -5;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = cluster;

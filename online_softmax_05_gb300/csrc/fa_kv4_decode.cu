@@ -962,7 +962,8 @@ int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) 
     using C = Cfg<D, G, NT>;
     static_assert(C::kSmem + 2 * kWarps * static_cast<int>(sizeof(Piece)) + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
     const auto kernel = weights ? fa_kv4_decode_kernel<D, G, NT, true> : fa_kv4_decode_kernel<D, G, NT, false>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return -5;
+    static std::atomic<unsigned long long> allowed[2];
+    if (!allow_shared_memory(kernel, C::kSmem, allowed[weights])) return -5;
     kernel<<<p.n_cta, kThreads, C::kSmem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -5;
     // Warps to a pair: a head has about n_cta / heads parts, more if few of the heads are long.

@@ -37,20 +37,18 @@ def kv4_pool(num_pages: int, kv_heads: int, dim: int, page_size: int = 64, group
 def _cache(pool, block_table, lengths):
     """(packed fa_kv4_cache, B, Hkv, D, slots per sequence, device index)"""
     import torch
-    if not (pool.is_cuda and pool.dtype == torch.uint8 and pool.dim() == 4 and pool.is_contiguous()):
+    dev, shape, i32 = pool.get_device(), pool.shape, torch.int32
+    fmt = _FORMATS.get(shape[3]) if len(shape) == 4 else None
+    if fmt is None or dev < 0 or pool.dtype is not torch.uint8 or shape[2] < 1 or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous uint8 CUDA tensor from kv4_pool")
-    dev = pool.get_device()
-    num_pages, heads, blocks, size = pool.shape
-    fmt = _FORMATS.get(size)
-    if fmt is None or blocks < 1:
-        raise ValueError("pool must be a contiguous uint8 CUDA tensor from kv4_pool")
-    i32 = torch.int32
-    if not (block_table.dtype == i32 and block_table.dim() == 2 and block_table.is_contiguous()
+    table_shape = block_table.shape
+    if not (block_table.dtype is i32 and len(table_shape) == 2 and block_table.is_contiguous()
             and block_table.get_device() == dev):
         raise ValueError("block_table must be a contiguous int32 (B, pages) tensor on the pool's device")
-    B, width = block_table.shape
-    if not (lengths.dtype == i32 and lengths.shape == (B,) and lengths.is_contiguous() and lengths.get_device() == dev):
+    B, width = table_shape
+    if not (lengths.dtype is i32 and lengths.shape == (B,) and lengths.is_contiguous() and lengths.get_device() == dev):
         raise ValueError("lengths must be a contiguous int32 (B,) tensor on the pool's device")
+    num_pages, heads, blocks, _ = shape
     packed = _pack_cache(pool.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), B, heads, fmt[0], fmt[1],
                          blocks * 16, num_pages, width)
     return packed, B, heads, fmt[0], width * blocks * 16, dev
@@ -118,7 +116,7 @@ def _read(pool, block_table, lengths, start, count):
         raise ValueError("start must be a contiguous int32 (B,) tensor on the pool's device")
     if count is None:
         count = slots
-    k = torch.empty(B, heads, count, D, dtype=torch.bfloat16, device=pool.device)
+    k = torch.empty((B, heads, count, D), dtype=torch.bfloat16, device=pool.device)
     v = torch.empty_like(k)
     rc = load_library().fa_kv4_read(packed, None if start is None else start.data_ptr(), count, k.data_ptr(),
                                     v.data_ptr(), _raw_stream(dev))
@@ -137,10 +135,11 @@ def kv4_read(pool, block_table, lengths, start=None, count: int | None = None, s
 def _decode(q, pool, block_table, lengths, causal, scale, weights, weights_out, out, lse):
     import torch
     packed, B, heads, D, slots, dev = _cache(pool, block_table, lengths)
-    if not (q.dtype == torch.bfloat16 and q.dim() == 4 and q.is_contiguous() and q.get_device() == dev
-            and q.shape[0] == B and q.shape[3] == D):
+    shape = q.shape
+    if not (q.dtype is torch.bfloat16 and len(shape) == 4 and q.is_contiguous() and q.get_device() == dev
+            and shape[0] == B and shape[3] == D):
         raise ValueError("q must be a contiguous (B, H, T, D) bf16 tensor on the pool's device")
-    _, Hq, Tq, _ = q.shape
+    _, Hq, Tq, _ = shape
     if out is None:
         out = torch.empty_like(q)
     elif not (out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous() and out.get_device() == dev):
@@ -167,13 +166,14 @@ def _decode(q, pool, block_table, lengths, causal, scale, weights, weights_out, 
         need = lib.fa_kv4_decode_workspace(B, Hq, heads, Tq, D, slots, int(w_out is not None))
         if need < 0:
             raise FAError(need, "fa_kv4_decode_workspace")
+        need = max(16, need)
         if len(_decode_bytes) > 4096:
             _decode_bytes.clear()
         _decode_bytes[key] = need
-    workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     rc = lib.fa_kv4_decode(packed, q.data_ptr(), out.data_ptr(), lse.data_ptr(), Hq, Tq,
                            1.0 / math.sqrt(D) if scale is None else scale, causal, w_in, w_out, w_slots,
-                           workspace.data_ptr(), workspace.shape[0], _raw_stream(dev))
+                           workspace.data_ptr(), need, _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv4_decode")
     return (out, lse) if w_out is None else (out, lse, weights_out)

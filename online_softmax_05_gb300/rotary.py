@@ -69,22 +69,23 @@ def _positions(positions, batch, rows, dev):
     import torch
     if positions is None:
         return None, 0, 0
-    if positions.dtype not in (torch.int32, torch.int64) or positions.get_device() != dev:
+    dtype, shape, stride = positions.dtype, positions.shape, positions.stride()
+    if (dtype is not torch.int32 and dtype is not torch.int64) or positions.get_device() != dev:
         raise ValueError("positions must be an int32 or int64 tensor on the device of the others")
-    if positions.dim() == 1:
-        stride = 0
-    elif positions.dim() == 2 and positions.shape[0] in (1, batch):
-        stride = positions.stride(0) if positions.shape[0] > 1 else 0
+    if len(shape) == 2 and (shape[0] == batch or shape[0] == 1):
+        step = stride[0] if shape[0] > 1 else 0
+    elif len(shape) == 1:
+        step = 0
     else:
         raise ValueError("positions must be (T,) or (B, T)")
-    if positions.shape[-1] != rows or (rows > 1 and positions.stride(-1) != 1):
+    if shape[-1] != rows or (rows > 1 and stride[-1] != 1):
         raise ValueError("positions must hold T consecutive values per row")
-    return positions.data_ptr(), int(positions.dtype == torch.int64), stride
+    return positions.data_ptr(), int(dtype is torch.int64), step
 
 
 def _check_table(table, dim, dev):
     import torch
-    if table.dtype != torch.int64 or table.dim() != 1 or not table.is_contiguous() or table.get_device() != dev:
+    if table.dtype is not torch.int64 or table.dim() != 1 or not table.is_contiguous() or table.get_device() != dev:
         raise ValueError("the frequency table must be a contiguous 1-D int64 tensor on the device of the others")
     rotary = 2 * table.shape[0]
     if rotary < 2 or rotary > dim:
@@ -98,34 +99,37 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
     if not _DTYPES:
         _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     first = tensors[0]
-    dev, dtype = first.get_device(), first.dtype
-    if first.dim() != 4:
-        raise ValueError("rope takes (B, H, T, D) tensors")
-    B, _, T, D = first.shape
+    dev, dtype, shape = first.get_device(), first.dtype, first.shape
     code = _DTYPES.get(dtype)
-    packed, results = b"", []
+    if len(shape) != 4 or code is None or dev < 0:
+        raise ValueError("rope takes (B, H, T, D) CUDA tensors of one type: bf16, fp16 or fp32")
+    B, _, T, D = shape
+    packed, results, heads = b"", [], 1
     for i, t in enumerate(tensors):
-        if code is None or t.dtype != dtype or not t.is_cuda or t.get_device() != dev or t.dim() != 4:
-            raise ValueError("rope takes (B, H, T, D) CUDA tensors of one type: bf16, fp16 or fp32")
-        shape = t.shape
-        if shape[0] != B or shape[2] != T or shape[3] != D:
-            raise ValueError("rope's tensors may differ in their heads only")
+        if i:
+            shape = t.shape
+            if t.dtype is not dtype or t.get_device() != dev or len(shape) != 4:
+                raise ValueError("rope takes (B, H, T, D) CUDA tensors of one type: bf16, fp16 or fp32")
+            if shape[0] != B or shape[2] != T or shape[3] != D:
+                raise ValueError("rope's tensors may differ in their heads only")
         sb, sh, st, sc = t.stride()
         if sc != 1 and D > 1:
             raise ValueError("the channels of rope's tensors must be contiguous")
-        if outs is None or outs[i] is None:
+        H = shape[1]
+        heads *= H
+        if outs is None:
             o = torch.empty(shape, dtype=dtype, device=t.device)
-            ob, oh, ot = shape[1] * T * D, T * D, D
+            ob, oh, ot = H * T * D, T * D, D
         else:
             o = outs[i]
-            if o.shape != shape or o.dtype != dtype or o.get_device() != dev or (o.stride(3) != 1 and D > 1):
+            if o.shape != shape or o.dtype is not dtype or o.get_device() != dev or (o.stride(3) != 1 and D > 1):
                 raise ValueError("out must match rope's input in shape, type and device, with contiguous channels")
             ob, oh, ot, _ = o.stride()
         results.append(o)
-        packed += _pack_tensor(t.data_ptr(), o.data_ptr(), shape[1], sb, st, sh, ob, ot, oh)
+        packed += _pack_tensor(t.data_ptr(), o.data_ptr(), H, sb, st, sh, ob, ot, oh)
     rotary = _check_table(table, D, dev)
     pos, pos64, pos_b = _positions(positions, B, T, dev)
-    if B * T and all(t.shape[1] for t in tensors):
+    if B * T * heads:
         rc = load_library().fa_rope(packed, len(tensors), pos, pos64, pos_b, table.data_ptr(), B, T, D, rotary,
                                     interleaved, amplitude, inverse, code, _raw_stream(dev))
         if rc != FA_OK:
@@ -141,7 +145,7 @@ def _make_rope_class():
         def forward(ctx, q, k, table, positions, interleaved, amplitude, inverse):
             ctx.save_for_backward(table, positions)
             ctx.args = interleaved, amplitude, inverse
-            got = _rope([t for t in (q, k) if t is not None], table, positions, interleaved, amplitude, inverse, None)
+            got = _rope((q,) if k is None else (q, k), table, positions, interleaved, amplitude, inverse, None)
             return tuple(got) if k is not None else got[0]
 
         @staticmethod
@@ -164,8 +168,9 @@ def _make_rope_class():
 
 
 def _rope_any(tensors, table, positions, interleaved, amplitude, inverse):
+    """_rope, through autograd where a tensor wants it."""
     import torch
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+    if torch.is_grad_enabled() and (tensors[0].requires_grad or tensors[-1].requires_grad):
         global _rope_cls
         if _rope_cls is None:
             cls = _make_rope_class()
@@ -173,7 +178,7 @@ def _rope_any(tensors, table, positions, interleaved, amplitude, inverse):
                 _rope_cls = _rope_cls or cls
         k = tensors[1] if len(tensors) > 1 else None
         got = _rope_cls.apply(tensors[0], k, table, positions, interleaved, amplitude, inverse)
-        return list(got) if k is not None else [got]
+        return got if k is not None else (got,)
     return _rope(tensors, table, positions, interleaved, amplitude, inverse, None)
 
 
@@ -190,16 +195,17 @@ def rope(q, k, table, positions=None, interleaved: bool = False, amplitude: floa
     (i, i + R/2).  ``inverse`` turns back.  ``out``: tensors (a tuple if k is
     given) to write to, which may be the inputs; not under autograd.
     Differentiable in q and k."""
+    tensors = (q,) if k is None else (q, k)
+    if out is None:
+        got = _launch_on(q, stream, _rope_any, tensors, table, positions, 1 if interleaved else 0, amplitude,
+                         1 if inverse else 0)
+        return tuple(got) if k is not None else got[0]
     import torch
-    tensors = [q] if k is None else [q, k]
-    args = table, positions, int(bool(interleaved)), float(amplitude), int(bool(inverse))
-    if out is not None:
-        outs = [out] if k is None else list(out)
-        if len(outs) != len(tensors):
-            raise ValueError("out must hold a tensor for each input")
-        if torch.is_grad_enabled() and any(t.requires_grad for t in tensors + outs):
-            raise ValueError("out cannot be given under autograd")
-        got = _launch_on(q, stream, _rope, tensors, *args, outs)
-    else:
-        got = _launch_on(q, stream, _rope_any, tensors, *args)
-    return got[0] if k is None else tuple(got)
+    outs = [out] if k is None else list(out)
+    if len(outs) != len(tensors):
+        raise ValueError("out must hold a tensor for each input")
+    if torch.is_grad_enabled() and any(t.requires_grad for t in list(tensors) + outs):
+        raise ValueError("out cannot be given under autograd")
+    got = _launch_on(q, stream, _rope, tensors, table, positions, int(bool(interleaved)), amplitude, int(bool(inverse)),
+                     outs)
+    return tuple(got) if k is not None else got[0]
