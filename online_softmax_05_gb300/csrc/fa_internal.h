@@ -86,6 +86,33 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
 int kv4_cache_take_status();
 int kv4_decode_take_status();
 
+// Launches a kernel that may be scheduled while the one before it in the stream
+// still runs: it hides the launch, and the kernel's first act is
+// wait_for_stream(), which returns when that one is done and its writes are seen.
+template <typename... Params, typename... Args>
+inline int launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          Args... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -5;
+}
+#ifdef __CUDACC__
+// Every thread of a chained kernel calls this before it reads or writes anything
+// in global memory; the next chained kernel may be scheduled from here on.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // Allows a kernel its dynamic shared memory, once per device (a microsecond a call otherwise).
 template <typename Kernel>
 inline bool allow_shared_memory(Kernel kernel, int bytes, std::atomic<unsigned long long>& done) {

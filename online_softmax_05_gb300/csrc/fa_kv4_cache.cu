@@ -159,6 +159,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&x)[4], float2 ran
 // its range with shuffles.  Bound: HBM, k and v once and the records.
 template <int D, int G, int ROT>
 __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int heads_thread) {
+    wait_for_stream();
     using L = Kv4<D, G>;
     constexpr int kOct = D / 8;
     const int lane = threadIdx.x & 31;
@@ -309,6 +310,7 @@ struct ReadParams {
 constexpr int kTokensThread = 4;
 template <int D, int G>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(ReadParams p) {
+    wait_for_stream();
     using L = Kv4<D, G>;
     constexpr int kOct = D / 8, kRows = 256 / kOct;
     const int oct = threadIdx.x % kOct, g = oct >> 2, j = oct & 3;
@@ -426,6 +428,7 @@ __device__ __forceinline__ int2 warps_before(int2 v, int2* warp_sums, int2& tota
 // n-th hole, no copy touches what another reads, and the moves run in any order.
 // Bound: latency of about ten dependent steps (passes, scans, cluster barriers).
 __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams p) {
+    wait_for_stream();
     extern __shared__ int2 kept_here[];  // (weight's bits, position) of the slice
     __shared__ int hist[2][kBins];
     __shared__ int2 warp_sums[kEvictWarps];
@@ -710,15 +713,12 @@ Kv4Pages pages_of(const Kv4Shape& c, void* pool, const int* table) {
     return kv4_pages(static_cast<unsigned char*>(pool), table, c.width, c.num_pages, c.Hkv, c.page_size, c.D, c.group);
 }
 
-int last_error() { return cudaGetLastError() == cudaSuccess ? 0 : -5; }
-
 template <int D, int G>
 int append(const AppendParams& p, int rot, dim3 grid, int per, cudaStream_t stream) {
-    if (rot == kNone) fa_kv4_append_kernel<D, G, kNone><<<grid, 256, 0, stream>>>(p, per);
-    else if (rot == kHalf) fa_kv4_append_kernel<D, G, kHalf><<<grid, 256, 0, stream>>>(p, per);
-    else if (rot == kInterleaved) fa_kv4_append_kernel<D, G, kInterleaved><<<grid, 256, 0, stream>>>(p, per);
-    else fa_kv4_append_kernel<D, G, kAny><<<grid, 256, 0, stream>>>(p, per);
-    return last_error();
+    void (*const kernels[4])(AppendParams, int) = {fa_kv4_append_kernel<D, G, kNone>, fa_kv4_append_kernel<D, G, kHalf>,
+                                                   fa_kv4_append_kernel<D, G, kInterleaved>,
+                                                   fa_kv4_append_kernel<D, G, kAny>};
+    return launch_chained(kernels[rot], grid, 256, 0, stream, p, per);
 }
 
 }  // namespace
@@ -772,14 +772,9 @@ int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const
     p.count = count;
     const int rows = 256 / (c.D / 8) * kTokensThread;
     const dim3 blocks((count + rows - 1) / rows, c.B * c.Hkv);
-    if (c.D == 64) {
-        if (c.group == 32) fa_kv4_read_kernel<64, 32><<<blocks, 256, 0, stream>>>(p);
-        else fa_kv4_read_kernel<64, 64><<<blocks, 256, 0, stream>>>(p);
-    } else {
-        if (c.group == 32) fa_kv4_read_kernel<128, 32><<<blocks, 256, 0, stream>>>(p);
-        else fa_kv4_read_kernel<128, 64><<<blocks, 256, 0, stream>>>(p);
-    }
-    return last_error();
+    const auto kernel = c.D == 64 ? (c.group == 32 ? fa_kv4_read_kernel<64, 32> : fa_kv4_read_kernel<64, 64>)
+                                  : (c.group == 32 ? fa_kv4_read_kernel<128, 32> : fa_kv4_read_kernel<128, 64>);
+    return launch_chained(kernel, blocks, 256, 0, stream, p);
 }
 
 size_t kv4_evict_workspace(int B, int Hkv, int budget) {
@@ -819,17 +814,19 @@ int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int*
     const int smem = p.slots_shared * 8;
     static std::atomic<unsigned long long> allowed;
     if (!allow_shared_memory(fa_kv4_evict_kernel, kSlotsMost * 8, allowed)) return -5;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(c.Hkv * cluster, c.B);
     cfg.blockDim = dim3(kEvictThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fa_kv4_evict_kernel, p) == cudaSuccess ? 0 : -5;
 }
 

@@ -61,6 +61,10 @@ constexpr float kAhead = 4.f;
 // Places on the line for a head's start, its queries' and first copies' latency
 // and its outputs, in units of 32 or 64 tokens.
 constexpr int kStart = 2;
+// Up to this many units a warp, a CTA takes a head by itself: it need not find its
+// place on the line, and nothing is left to a second kernel (2 heads of 117 tokens:
+// 8.4 us instead of 10.4; above, the line's finer cut is worth its joining).
+constexpr int kByHead = 2;
 
 struct DecParams {
     const __nv_bfloat16* q;
@@ -75,6 +79,7 @@ struct DecParams {
     float* weights_out;
     long long slots, cap;
     int B, R, RB, Tq, causal, n_cta;
+    int by_head;  // a CTA takes one (sequence, head, row block) alone: nothing to join between CTAs
     float sl2;  // scale log2(e)
 };
 
@@ -232,13 +237,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     __shared__ Piece s_piece[kWarps][2];
     const int HR = p.pages.heads * p.RB;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_stream();
     if (lane == 0) s_piece[warp][0].head = s_piece[warp][1].head = -1;
 
     // this warp's share of the line; from place `skip` of its first head on
     Segment seg{0, 0, 0, 0, 0, 0};
     int left = 0;
-    {
+    if (p.by_head) {
+        seg.b = blockIdx.x / HR;
+        seg.hr = blockIdx.x - seg.b * HR;
+        seg.len = length_of(p, seg.b);
+        seg.n = (seg.len + C::kTokens - 1) / C::kTokens;
+        const int share = (seg.n + kWarps - 1) / kWarps;
+        seg.u0 = min(seg.n, warp * share);
+        seg.u1 = min(seg.n, seg.u0 + share);
+        if (seg.n == 0) {  // no tokens
+            const long long row = (static_cast<long long>(seg.b) * p.pages.heads + seg.hr / p.RB) * p.R + seg.hr % p.RB * NT * 8;
+            const int rows = min(NT * 8, p.R - seg.hr % p.RB * NT * 8);
+            for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads)
+                reinterpret_cast<uint32_t*>(p.o + row * D)[i] = 0;
+            if (threadIdx.x < rows) p.lse[row + threadIdx.x] = -INFINITY;
+        }
+    } else {
         int all, unused;
         count_places<C::kTokens>(p, lane, 0, all, unused);
         const int total = all * HR, share = share_of(p, total);
@@ -841,31 +861,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     }
 }
 
-// Joins the parts of the heads that are cut between CTAs, and writes those that
-// have no tokens.  A CTA takes 8 / SPLIT pairs of accumulators of one (sequence,
-// head, row block), SPLIT warps to a pair taking the parts in turn.
-template <int D, int G, int NT, int SPLIT>
-__global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
-    using C = Cfg<D, G, NT>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g4 = lane >> 2, j = lane & 3;
+// Which parts a head was cut into: CTAs c0 .. c1 hold some of its n units.
+template <class C>
+__device__ __forceinline__ void parts_of(const DecParams& p, int lane, int b, int hr, int& n, unsigned& c0, unsigned& c1) {
     const int HR = p.pages.heads * p.RB;
-    const int b = blockIdx.x / HR, hr = blockIdx.x % HR;
-    const int head = hr / p.RB;
-    const long long bh = static_cast<long long>(b) * p.pages.heads + head;
-    const int pair = blockIdx.y * (8 / SPLIT) + warp / SPLIT, sub = warp % SPLIT;
-    const int nt = pair / C::kPairs, i = pair % C::kPairs;
-    const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
+    if (p.by_head) {
+        n = (length_of(p, b) + C::kTokens - 1) / C::kTokens;
+        c0 = c1 = 0;
+        return;
+    }
     int all, before;
     count_places<C::kTokens>(p, lane, b, all, before);
-    const int n = max(places_of<C::kTokens>(length_of(p, b)) - kStart, 0);
+    n = max(places_of<C::kTokens>(length_of(p, b)) - kStart, 0);
     const unsigned share = static_cast<unsigned>(share_of(p, all * HR)) * kWarps;
     const unsigned first = before * HR + hr * (n + kStart) + kStart;  // the first unit's place
-    const unsigned c0 = first / share, c1 = n == 0 ? c0 : (first + n - 1) / share;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (n > 0 && c0 == c1) return;  // written by its CTA
+    c0 = first / share;
+    c1 = n == 0 ? c0 : (first + n - 1) / share;
+}
+
+// A running maximum, sum and output pair, and more of the same head.
+struct Joined {
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
-    auto take = [&](float2 m, float2 l, float2 x) {
+    __device__ __forceinline__ void take(float2 m, float2 l, float2 x) {
         const float ms[2] = {m.x, m.y}, ls[2] = {l.x, l.y}, xs[2] = {x.x, x.y};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -877,54 +894,127 @@ __global__ void __launch_bounds__(256) fa_kv4_merge_kernel(DecParams p) {
             o[e] = o[e] * a + xs[e] * f;
             top[e] = now;
         }
-    };
+    }
+    __device__ __forceinline__ float lse2(int e) const { return sum[e] == 0.f ? -INFINITY : top[e] + __log2f(sum[e]); }
+};
+
+// Joins the parts of the heads that are cut between CTAs, and writes those that
+// have no tokens.  A CTA takes 8 / SPLIT pairs of accumulators of one (sequence,
+// head, row block), SPLIT warps to a pair taking the parts in turn.
+template <class C, int NT, int SPLIT>
+__device__ __forceinline__ void join_parts(const DecParams& p, int head_row, int y, float2 (&sm)[3][8][32]) {
+    constexpr int D = C::D;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g4 = lane >> 2, j = lane & 3;
+    const int HR = p.pages.heads * p.RB;
+    const int b = head_row / HR, hr = head_row % HR;
+    const long long bh = static_cast<long long>(b) * p.pages.heads + hr / p.RB;
+    const int pair = y * (8 / SPLIT) + warp / SPLIT, sub = warp % SPLIT;
+    const int nt = pair / C::kPairs, i = pair % C::kPairs;
+    const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
+    int n;
+    unsigned c0, c1;
+    parts_of<C>(p, lane, b, hr, n, c0, c1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (n > 0 && c0 == c1) return;  // written by its CTA
+    Joined all;
     if (n > 0) {
-        const long long slot0 = static_cast<long long>(b) * HR + hr;
 #pragma unroll 4
         for (unsigned c = c0 + sub; c <= c1; c += SPLIT) {
-            const float* ml = p.part_ml + ((slot0 + c) * NT + nt) * 16 + 2 * j;
-            take(*reinterpret_cast<const float2*>(ml), *reinterpret_cast<const float2*>(ml + 8),
-                 p.part_o[(((slot0 + c) * NT + nt) * C::kPairs + i) * 32 + lane]);
+            const long long slot = static_cast<long long>(head_row) + c;
+            const float* ml = p.part_ml + (slot * NT + nt) * 16 + 2 * j;
+            all.take(*reinterpret_cast<const float2*>(ml), *reinterpret_cast<const float2*>(ml + 8),
+                     p.part_o[((slot * NT + nt) * C::kPairs + i) * 32 + lane]);
         }
     }
     if constexpr (SPLIT > 1) {
-        __shared__ float2 sm[3][8][32];
-        sm[0][warp][lane] = make_float2(top[0], top[1]);
-        sm[1][warp][lane] = make_float2(sum[0], sum[1]);
-        sm[2][warp][lane] = make_float2(o[0], o[1]);
+        sm[0][warp][lane] = make_float2(all.top[0], all.top[1]);
+        sm[1][warp][lane] = make_float2(all.sum[0], all.sum[1]);
+        sm[2][warp][lane] = make_float2(all.o[0], all.o[1]);
         __syncthreads();
         if (sub != 0) return;
 #pragma unroll
-        for (int x = 1; x < SPLIT; ++x) take(sm[0][warp + x][lane], sm[1][warp + x][lane], sm[2][warp + x][lane]);
+        for (int x = 1; x < SPLIT; ++x) all.take(sm[0][warp + x][lane], sm[1][warp + x][lane], sm[2][warp + x][lane]);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (row + e >= p.R) continue;
-        p.o[(bh * p.R + row + e) * D + ch] = __float2bfloat16_rn(sum[e] == 0.f ? 0.f : o[e] / sum[e]);
-        if (i == 0 && g4 == 0) p.lse[bh * p.R + row + e] = sum[e] == 0.f ? -INFINITY : (top[e] + __log2f(sum[e])) * kLn2;
+        p.o[(bh * p.R + row + e) * D + ch] = __float2bfloat16_rn(all.sum[e] == 0.f ? 0.f : all.o[e] / all.sum[e]);
+        if (i == 0 && g4 == 0) p.lse[bh * p.R + row + e] = all.lse2(e) * kLn2;
     }
 }
 
-// weights_out = weights + the sum over the rows of P, slot by slot.
-__global__ void __launch_bounds__(256) fa_kv4_weights_kernel(DecParams p, int width) {
-    __shared__ float sm_lse[1024];
-    const int bh = blockIdx.y, b = bh / p.pages.heads;
+// weights_out = weights + the sum over the rows of P, slot by slot, for a head's
+// tokens from 256 x on, `step` apart.
+template <class C, int NT>
+__device__ __forceinline__ void add_weights(const DecParams& p, int bh, int x, int step, float* sm_lse) {
+    const int b = bh / p.pages.heads, head = bh % p.pages.heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = length_of(p, b);
-    if (static_cast<long long>(blockIdx.x) * 256 >= len) return;
-    for (int r = threadIdx.x; r < p.R; r += 256) sm_lse[r] = p.lse[static_cast<long long>(bh) * p.R + r] * kLog2e;
+    int n;
+    unsigned c0, c1;
+    parts_of<C>(p, lane, b, head * p.RB, n, c0, c1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (static_cast<long long>(x) * 256 >= len) return;
+    // the rows' log-sum-exp: from the head's CTA, or from the parts again, as nothing
+    // says that their join is done; a warp takes a pair of rows, its lanes the parts
+    const int width = p.RB * NT * 8;
+    for (int pr = warp; pr < width / 2; pr += 8) {
+        const int rb = pr / (NT * 4), nt = pr / 4 % NT, j = pr % 4;
+        if (rb > 0) parts_of<C>(p, lane, b, head * p.RB + rb, n, c0, c1);
+        if (c0 == c1) {
+            if (lane < 2 && 2 * pr + lane < p.R) sm_lse[2 * pr + lane] = p.lse[static_cast<long long>(bh) * p.R + 2 * pr + lane] * kLog2e;
+            continue;
+        }
+        Joined all;
+        for (unsigned c = c0 + lane; c <= c1; c += 32) {
+            const float* ml = p.part_ml + ((static_cast<long long>(bh) * p.RB + rb + c) * NT + nt) * 16 + 2 * j;
+            all.take(*reinterpret_cast<const float2*>(ml), *reinterpret_cast<const float2*>(ml + 8), make_float2(0.f, 0.f));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float2 m = make_float2(__shfl_xor_sync(0xffffffffu, all.top[0], o), __shfl_xor_sync(0xffffffffu, all.top[1], o));
+            const float2 l = make_float2(__shfl_xor_sync(0xffffffffu, all.sum[0], o), __shfl_xor_sync(0xffffffffu, all.sum[1], o));
+            all.take(m, l, make_float2(0.f, 0.f));
+        }
+        if (lane == 0) {
+            sm_lse[2 * pr] = all.lse2(0);
+            sm_lse[2 * pr + 1] = all.lse2(1);
+        }
+    }
     __syncthreads();
-    for (long long t = blockIdx.x * 256LL + threadIdx.x; t < len; t += gridDim.x * 256LL) {
+    for (long long t = x * 256LL + threadIdx.x; t < len; t += step * 256LL) {
         const float4* s = reinterpret_cast<const float4*>(p.scores + (bh * p.cap + t) * width);
         float sum = 0.f;
         for (int r = 0; r < p.R; r += 4) {
-            const float4 x = s[r >> 2];
-            const float xs[4] = {x.x, x.y, x.z, x.w};
+            const float4 v = s[r >> 2];
+            const float vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (r + e < p.R && xs[e] != -INFINITY) sum += ex2_approx(xs[e] - sm_lse[r + e]);
+                if (r + e < p.R && vs[e] != -INFINITY) sum += ex2_approx(vs[e] - sm_lse[r + e]);
         }
         const long long at = bh * p.slots + t;
         p.weights_out[at] = (p.weights != nullptr ? p.weights[at] : 0.f) + sum;
+    }
+}
+
+// What is left when the line is done: blocks below `joins` in y join parts, the
+// others add weights.
+template <int D, int G, int NT, int SPLIT, bool WEIGHTS>
+__global__ void __launch_bounds__(256) fa_kv4_finish_kernel(DecParams p, int joins) {
+    using C = Cfg<D, G, NT>;
+    __shared__ float2 sm[3][8][32];
+    static_assert(sizeof(sm) >= 1024 * sizeof(float), "the log-sum-exps of 1024 rows");
+    // the lengths may be read at once: they are older than the decoding kernel, which
+    // lets this one be scheduled when it has waited for what came before it
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int heads = p.B * p.pages.heads;
+    if (static_cast<int>(blockIdx.y) < joins) {
+        join_parts<C, NT, SPLIT>(p, blockIdx.x, blockIdx.y, sm);
+    } else if constexpr (WEIGHTS) {
+        // the x dimension counts row blocks too: they share the head's tokens
+        const int x = (blockIdx.y - joins) * p.RB + blockIdx.x / heads, step = (gridDim.y - joins) * p.RB;
+        add_weights<C, NT>(p, blockIdx.x % heads, x, step, reinterpret_cast<float*>(sm));
     }
 }
 
@@ -944,40 +1034,34 @@ Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
 }
 
 template <int D, int G, int NT, int SPLIT>
-int launch_merge(const DecParams& p, cudaStream_t stream, int bh) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(bh) * p.RB, D / 8 * NT * SPLIT / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_kv4_merge_kernel<D, G, NT, SPLIT>, p) == cudaSuccess ? 0 : -5;
+int launch_finish(const DecParams& p, cudaStream_t stream, int bh, int num_sms) {
+    const int joins = p.by_head ? 0 : D / 8 * NT * SPLIT / 8, heads = bh * p.RB;
+    int adds = 0;
+    if (p.weights_out != nullptr) {
+        const long long most = (p.cap + 256 * p.RB - 1) / (256 * p.RB), want = (8LL * num_sms + heads - 1) / heads;
+        adds = static_cast<int>(most < want ? most : want);
+    }
+    if (joins + adds == 0) return 0;
+    const dim3 grid(heads, joins + adds);
+    return launch_chained(adds > 0 ? fa_kv4_finish_kernel<D, G, NT, SPLIT, true> : fa_kv4_finish_kernel<D, G, NT, SPLIT, false>,
+                          grid, 256, 0, stream, p, joins);
 }
 
 template <int D, int G, int NT>
 int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) {
     using C = Cfg<D, G, NT>;
     static_assert(C::kSmem + 2 * kWarps * static_cast<int>(sizeof(Piece)) + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
+    p.by_head = p.cap <= static_cast<long long>(kByHead) * kWarps * C::kTokens;
+    if (p.by_head) p.n_cta = bh * p.RB;
     const auto kernel = weights ? fa_kv4_decode_kernel<D, G, NT, true> : fa_kv4_decode_kernel<D, G, NT, false>;
     static std::atomic<unsigned long long> allowed[2];
     if (!allow_shared_memory(kernel, C::kSmem, allowed[weights])) return -5;
-    kernel<<<p.n_cta, kThreads, C::kSmem, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return -5;
-    // Warps to a pair: a head has about n_cta / heads parts, more if few of the heads are long.
+    if (launch_chained(kernel, dim3(p.n_cta), kThreads, C::kSmem, stream, p) != 0) return -5;
+    // Warps to a pair: a head has about n_cta / heads parts, more if few of the heads
+    // are long.  (Eight warps to each of 64 heads with 2 to 4 parts: 45 us instead of 41.)
     const long long heads = static_cast<long long>(bh) * p.RB;
-    const int rc = heads * 2 >= p.n_cta ? launch_merge<D, G, NT, 1>(p, stream, bh)
-                                        : launch_merge<D, G, NT, 8>(p, stream, bh);
-    if (rc != 0) return rc;
-    if (weights) {
-        long long n = (p.cap + 255) / 256;
-        const long long most = (16LL * num_sms + bh - 1) / bh;
-        fa_kv4_weights_kernel<<<dim3(static_cast<unsigned>(n < most ? n : most), bh), 256, 0, stream>>>(p, p.RB * NT * 8);
-        if (cudaGetLastError() != cudaSuccess) return -5;
-    }
-    return 0;
+    return heads * 8 >= p.n_cta ? launch_finish<D, G, NT, 1>(p, stream, bh, num_sms)
+                                : launch_finish<D, G, NT, 8>(p, stream, bh, num_sms);
 }
 
 }  // namespace

@@ -69,6 +69,7 @@ struct alignas(sizeof(E) * V) Vec {
 // A unit of a row: V pairs, or 2 V channels behind the rotated ones.
 template <typename E, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
+    wait_for_stream();
     const long long item = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
     if (item >= p.items) return;
     const int u = static_cast<int>(item % p.units);
@@ -144,11 +145,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
 
 template <typename E, int V>
 int launch(const RopeParams& p, int inter, dim3 grid, cudaStream_t st) {
-    if (inter)
-        fa_rope_kernel<E, V, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else
-        fa_rope_kernel<E, V, false><<<grid, kRopeThreads, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+    return launch_chained(inter ? fa_rope_kernel<E, V, true> : fa_rope_kernel<E, V, false>, grid, kRopeThreads, 0, st, p);
 }
 
 }  // namespace

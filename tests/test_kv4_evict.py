@@ -270,3 +270,74 @@ def test_a_serving_run(dim, group, each):
                     sim[b][h] = [sim[b][h][i] for i in src]
                     shadow[b][h] = shadow[b][h][:, src]
             assert held.tolist() == [min(n, budget) for n in lengths]
+
+
+@pytest.mark.gpu
+def test_a_captured_step_between_other_work():
+    """One serving step captured with fills, copies and library kernels before and between
+    the operators, on a stream that waits for another: replays equal the eager step."""
+    B, heads, hq, dim, page = 3, 2, 8, 128, 16
+    c = ref.Batch([200, 33, 64], heads, dim, 64, page, seed=21, spare=2)
+    pool, table, held = c.on()
+    slots = table.shape[1] * page
+    used = set(c.table[c.table >= 0].tolist())
+    free = [i for i in range(c.pool.shape[0]) if i not in used]
+    for b in range(2):          # the two spare pages go to the sequences that need one for a new token
+        row = c.table[b]
+        row[np.argmax(row < 0)] = free[b]
+    c.lengths[2] = 60
+    table = torch.from_numpy(c.table).cuda()
+    held = torch.tensor(c.lengths, dtype=torch.int32).cuda()
+    freq = fa.rotary_frequencies(dim, device="cuda")
+    g = torch.Generator("cuda").manual_seed(3)
+    qkv = torch.randn(B, 1, hq + 2 * heads, dim, device="cuda", generator=g).to(torch.bfloat16)
+    weights = torch.rand(B, heads, slots, device="cuda", generator=g)
+    where = torch.arange(slots, dtype=torch.int32, device="cuda").expand(B, heads, slots).contiguous()
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+
+    def step(qkv, pool, held, weights, where):
+        lengths = torch.zeros_like(held)
+        lengths.copy_(held)
+        lengths += 1
+        x = qkv.transpose(1, 2)
+        pos = (lengths - 1)[:, None]
+        q = fa.rope(x[:, :hq], None, freq, pos)
+        fa.kv4_append(pool, qkv[:, 0, hq:hq + heads], qkv[:, 0, hq + heads:], table, lengths, cu, rotary=freq,
+                      positions=pos[:, 0].contiguous(), weights=weights, slot_positions=where)
+        o, lse, w = fa.attention_decode_kv4(q, pool, table, lengths, weights=weights)
+        o = o * 1.0
+        got = fa.kv4_evict(pool, table, lengths, w, where, 50, 8)
+        k, v = fa.kv4_read(pool, table, got[2], count=50)
+        return [o, lse, *got, k, v, pool.clone()]
+
+    base = [t.clone() for t in (qkv, pool, held, weights, where)]
+    want = step(*[t.clone() for t in base])
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == 0
+    static = [t.clone() for t in base]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*[t.clone() for t in base])        # what capture needs to have run once
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*static)
+    for _ in range(3):
+        for s, b in zip(static, base):
+            s.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fa.fa_get_device_status() == 0
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    # and eagerly on another stream, ordered by events alone
+    for _ in range(3):
+        fresh = [t.clone() for t in base]
+        fresh[0].mul_(1.0)
+        ev = torch.cuda.Event()
+        ev.record()
+        side.wait_event(ev)
+        with torch.cuda.stream(side):
+            got = step(*fresh)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
