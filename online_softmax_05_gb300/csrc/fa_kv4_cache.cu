@@ -194,7 +194,23 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
     float cs[ROT == kInterleaved ? 4 : 8], sn[ROT == kInterleaved ? 4 : 8];
     const int half = p.R >> 1;
     const bool turned = ROT != kNone && oct * 8 < p.R;
-    if constexpr (ROT != kNone) {
+    // the lane that holds this one's partner channels (half layout)
+    const int partner = lane - lane % kOct + (!turned ? oct : oct * 8 < half ? oct + half / 8 : oct - half / 8);
+    if constexpr (ROT == kHalf) {
+        // the two lanes of eight pairs take the angles of four each
+        const bool first = oct * 8 < half;
+        const int pair = (first ? oct : oct - half / 8) * 8 + (first ? 0 : 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float c = 0.f, s = 0.f;
+            if (turned) rope_angle(pos, p.freq[pair + i], p.amp, c, s);
+            const float oc = __shfl_sync(0xffffffffu, c, partner), os = __shfl_sync(0xffffffffu, s, partner);
+            cs[i] = first ? c : oc;
+            cs[4 + i] = first ? oc : c;
+            sn[i] = first ? s : -os;
+            sn[4 + i] = first ? os : -s;
+        }
+    } else if constexpr (ROT != kNone) {
         if (turned) {
             constexpr int N = ROT == kInterleaved ? 4 : 8;
 #pragma unroll
@@ -205,7 +221,7 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
                 if constexpr (ROT == kInterleaved) {
                     pair = oct * 4 + i;
                     first = true;
-                } else if (ROT == kAny && p.interleaved) {
+                } else if (p.interleaved) {
                     pair = c >> 1;
                     first = (c & 1) == 0;
                 }
@@ -232,10 +248,9 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
         uint32_t kx[4] = {kraw.x, kraw.y, kraw.z, kraw.w};
         const uint32_t vx[4] = {vraw.x, vraw.y, vraw.z, vraw.w};
         if constexpr (ROT == kHalf) {
-            const int other = turned ? (oct * 8 < half ? oct + half / 8 : oct - half / 8) : oct;
             uint32_t y[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) y[w] = __shfl_sync(0xffffffffu, kx[w], lane - lane % kOct + other);
+            for (int w = 0; w < 4; ++w) y[w] = __shfl_sync(0xffffffffu, kx[w], partner);
             if (turned) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w)  // rope_turn of two channels
@@ -550,11 +565,10 @@ __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams
         const int top = kBins - 2 - 2 * tid;
         int2 sum = make_int2(0, 0);
 #pragma unroll
-        for (int c = 0; c < kEvictCluster; ++c) {
-            if (c >= C) break;
-            const int2 x = *reinterpret_cast<const int2*>(cluster.map_shared_rank(bin, c) + top);
-            sum.x += x.x;
-            sum.y += x.y;
+        for (int c = 0; c < kEvictCluster; ++c) {  // all on their way together; past C, this CTA's again
+            const int2 x = *reinterpret_cast<const int2*>(cluster.map_shared_rank(bin, c < C ? c : rank) + top);
+            sum.x += c < C ? x.x : 0;
+            sum.y += c < C ? x.y : 0;
         }
         const int2 in = warp_inclusive(make_int2(sum.x + sum.y, 0), lane);
         int2 all;
