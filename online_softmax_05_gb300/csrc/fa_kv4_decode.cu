@@ -100,7 +100,7 @@ struct Cfg : Kv4<D_, G_> {
 
 // Length of sequence b, 0 (and a status) if the table or the accounts cannot hold it.
 __device__ __forceinline__ int length_of(const DecParams& p, int b) {
-    const int len = p.lengths[b];
+    const int len = __ldcg(p.lengths + b);  // from L2: the joining kernel reads it before it has waited
     if (len < 0 || len > p.pages.capacity() || (p.weights_out != nullptr && len > p.slots)) {
         report(kStatusBadSeqlen);
         return 0;
@@ -1005,8 +1005,8 @@ __global__ void __launch_bounds__(256) fa_kv4_finish_kernel(DecParams p, int joi
     using C = Cfg<D, G, NT>;
     __shared__ float2 sm[3][8][32];
     static_assert(sizeof(sm) >= 1024 * sizeof(float), "the log-sum-exps of 1024 rows");
-    // the lengths may be read at once: they are older than the decoding kernel, which
-    // lets this one be scheduled when it has waited for what came before it
+    // The lengths may be read at once: this kernel is scheduled when every CTA of the
+    // decoding kernel has waited for the kernels before it, so their writes are in L2.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int heads = p.B * p.pages.heads;
     if (static_cast<int>(blockIdx.y) < joins) {

@@ -349,3 +349,35 @@ def test_python_entries_refuse():
                 lambda: fa.kv4_read(pool, table, held, count=0)):
         with pytest.raises(fa.FAError):
             bad()
+
+
+@pytest.mark.gpu
+def test_pages_behind_the_first_four_gigabytes():
+    # a pool of 5 GB, the sequences' pages at its end: append, read, decode and evict there
+    heads, dim, group, page = 8, 128, 64, 64
+    pages = 5 * 2 ** 30 // (heads * page * 144)
+    pool = torch.empty(pages, heads, page // 16, 16 * 144, dtype=torch.uint8, device="cuda")
+    width = 12
+    rng = np.random.default_rng(0)
+    table = torch.from_numpy((pages - 1 - rng.permutation(2 * width)).reshape(2, width).astype(np.int32)).cuda()
+    assert int(table.min()) * heads * page * 144 > 2 ** 32
+    held = torch.tensor([700, 300], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 700, 1000], dtype=torch.int32).cuda()
+    g = torch.Generator("cuda").manual_seed(1)
+    k, v = (torch.randn(1000, heads, dim, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(2, heads, 1, dim, device="cuda", generator=g).to(torch.bfloat16)
+    w = torch.rand(2, heads, 768, device="cuda", generator=g)
+    p = torch.arange(768, dtype=torch.int32, device="cuda").expand(2, heads, 768).contiguous()
+
+    def steps(pool, table):
+        fa.kv4_append(pool, k, v, table, held, cu)
+        out = [*fa.kv4_read(pool, table, held), *fa.attention_decode_kv4(q, pool, table, held)]
+        got = fa.kv4_evict(pool, table, held, w, p, 200, 20)
+        return out + [*got, *fa.kv4_read(pool, table, got[2], count=200)]
+
+    small = fa.kv4_pool(2 * width, heads, dim, page_size=page, group=group)
+    want = steps(small, torch.arange(2 * width, dtype=torch.int32, device="cuda").view(2, width))
+    got = steps(pool, table)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -118,6 +118,32 @@ def test_many_sequences_of_every_length():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("each,tq", [(4, 1), (5, 3)])
+@pytest.mark.parametrize("count", [33, 100, 300])
+def test_many_sequences_beside_a_long_one(count, each, tq):
+    # the line of units over more sequences than a warp has lanes: several whole heads in one
+    # warp's stretch, heads cut between warps and between CTAs
+    c = ref.Batch([(i * 37) % 97 for i in range(count - 2)] + [3001, 700], 2, 128, 64, 32, seed=count)
+    run(c, 2 * each, tq, weights=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 4096])
+def test_one_token_steps_and_page_borders(page):
+    # lengths around the borders of units, pages and warps' stretches, one step at a time
+    for n in (1, 16, 31, 32, 33, 511, 512, 513, 1023, 1024, 1025, 4096):
+        run(ref.Batch([n], 1, 64, 32, page, seed=n), 3, 1)
+
+
+@pytest.mark.gpu
+def test_sequences_that_share_pages():
+    # a common prefix held once: both tables name the same pages
+    c = ref.Batch([200, 136], 2, 128, 64, 32, seed=17)
+    c.table[1, :4] = c.table[0, :4]
+    run(c, 8, 1, weights=True)
+
+
+@pytest.mark.gpu
 def test_one_long_sequence():
     c = ref.Batch([70001], 1, 128, 64, 64, seed=9)
     run(c, 8, 1, weights=True)
