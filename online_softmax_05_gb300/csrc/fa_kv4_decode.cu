@@ -95,7 +95,11 @@ struct Cfg : Kv4<D_, G_> {
     static constexpr int kPieceO = NT_ * kPairs * 32 * 8;   // a warp's outputs of one head, and
     static constexpr int kPiece = kPieceO + NT_ * 64;       // its running maxima and sums
     static_assert(kPiece <= kRing, "the last piece goes where the ring was");
-    static constexpr int kSmem = kWarps * (kRing + kPiece);
+    // the joining tables: [row tile][factor, maximum, sum][piece][query row], behind the
+    // last piece in the first ring where they fit
+    static constexpr int kTable = NT_ * 3 * 2 * kWarps * 8 * 4;
+    static constexpr int kTableAt = kPiece + kTable <= kRing ? kPiece : kWarps * (kRing + kPiece);
+    static constexpr int kSmem = kWarps * (kRing + kPiece) + (kTableAt == kPiece ? 0 : kTable);
 };
 
 // Length of sequence b, 0 (and a status) if the table or the accounts cannot hold it.
@@ -785,10 +789,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     // each piece's factor 2^(m - max) for every query row: a warp takes a row of each
     // tile, a lane a piece, the maxima and sums run over the lanes of the same head
     const unsigned same = __match_any_sync(0xffffffffu, have >> lane & 1 ? mine.head : -1 - lane);
-    // per query row: the pieces' factors, maxima and sums, behind the last pieces in the rings
-    static_assert(C::kPiece + NT * 3 * kMost * 4 <= C::kRing, "room for the tables");
-    auto joined_at = [&](int row, int nt) -> float* {
-        return reinterpret_cast<float*>(smem + row * C::kRing + C::kPiece) + nt * 3 * kMost;
+    // table `what` (0: the pieces' factors, 1: maxima, 2: sums) of row tile nt, [piece][query row]
+    auto table = [&](int nt, int what) -> float* {
+        return reinterpret_cast<float*>(smem + C::kTableAt) + (nt * 3 + what) * kMost * 8;
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -810,10 +813,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             if (same >> y & 1) sum += py;
         }
         if (lane < kMost) {
-            float* table = joined_at(warp, nt);
-            table[lane] = f;
-            table[kMost + lane] = top;
-            table[2 * kMost + lane] = sum;
+            table(nt, 0)[lane * 8 + warp] = f;
+            table(nt, 1)[lane * 8 + warp] = top;
+            table(nt, 2)[lane * 8 + warp] = sum;
         }
     }
     __syncthreads();
@@ -829,16 +831,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         for (int x = warp; x < NT * C::kPairs; x += kWarps) {
             const int nt = x / C::kPairs, pr = x % C::kPairs;
             const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j;
-            float2 o = make_float2(0.f, 0.f);
-#pragma unroll 4
-            for (int y = y0; y <= y1; ++y) {
-                if (!(group >> y & 1)) continue;
-                const float2 f = make_float2(joined_at(2 * j, nt)[y], joined_at(2 * j + 1, nt)[y]);
-                const float2 v = reinterpret_cast<const float2*>(piece_at(y >> 1, y & 1))[x * 32 + lane];
-                if (f.x != 0.f) o.x = fmaf(f.x, v.x, o.x);
-                if (f.y != 0.f) o.y = fmaf(f.y, v.y, o.y);
+            // A head has last pieces of neighbouring warps, and at most one first piece, its
+            // end.  All warps' last pieces are read, of this head or not, so that no load
+            // waits for another (a loop over the members took three times as long).
+            float2 f[kWarps + 1], v[kWarps + 1], o = make_float2(0.f, 0.f);
+            const int first_piece = (group & 0x55555555u) != 0 ? __ffs(group & 0x55555555u) - 1 : 0;
+#pragma unroll
+            for (int y = 0; y <= kWarps; ++y) {
+                const int at_piece = y < kWarps ? 2 * y + 1 : first_piece;
+                f[y] = *reinterpret_cast<const float2*>(table(nt, 0) + at_piece * 8 + 2 * j);
+                v[y] = reinterpret_cast<const float2*>(piece_at(at_piece >> 1, y < kWarps))[x * 32 + lane];
             }
-            const float2 sum = make_float2(joined_at(2 * j, nt)[2 * kMost + y0], joined_at(2 * j + 1, nt)[2 * kMost + y0]);
+#pragma unroll
+            for (int y = 0; y <= kWarps; ++y) {
+                const bool in = group >> (y < kWarps ? 2 * y + 1 : first_piece) & 1;
+                if (in && f[y].x != 0.f) o.x = fmaf(f[y].x, v[y].x, o.x);
+                if (in && f[y].y != 0.f) o.y = fmaf(f[y].y, v[y].y, o.y);
+            }
+            const float2 sum = *reinterpret_cast<const float2*>(table(nt, 2) + y0 * 8 + 2 * j);
             if (!whole) {
                 p.part_o[(slot * NT * C::kPairs + x) * 32 + lane] = o;
             } else {
@@ -850,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         }
         if (warp == 0 && lane < 8 * NT) {
             const int nt = lane / 8, c = lane % 8, row = (hr % p.RB) * NT * 8 + lane;
-            const float top = joined_at(c, nt)[kMost + y0], sum = joined_at(c, nt)[2 * kMost + y0];
+            const float top = table(nt, 1)[y0 * 8 + c], sum = table(nt, 2)[y0 * 8 + c];
             if (!whole) {
                 p.part_ml[(slot * NT + nt) * 16 + c] = top;
                 p.part_ml[(slot * NT + nt) * 16 + 8 + c] = sum;
