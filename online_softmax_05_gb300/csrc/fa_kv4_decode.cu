@@ -95,11 +95,7 @@ struct Cfg : Kv4<D_, G_> {
     static constexpr int kPieceO = NT_ * kPairs * 32 * 8;   // a warp's outputs of one head, and
     static constexpr int kPiece = kPieceO + NT_ * 64;       // its running maxima and sums
     static_assert(kPiece <= kRing, "the last piece goes where the ring was");
-    // the joining tables: [row tile][factor, maximum, sum][piece][query row], behind the
-    // last piece in the first ring where they fit
-    static constexpr int kTable = NT_ * 3 * 2 * kWarps * 8 * 4;
-    static constexpr int kTableAt = kPiece + kTable <= kRing ? kPiece : kWarps * (kRing + kPiece);
-    static constexpr int kSmem = kWarps * (kRing + kPiece) + (kTableAt == kPiece ? 0 : kTable);
+    static constexpr int kSmem = kWarps * (kRing + kPiece);
 };
 
 // Length of sequence b, 0 (and a status) if the table or the accounts cannot hold it.
@@ -784,88 +780,73 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     static_assert(kMost <= 32, "a lane for every piece");
     // the pieces of a head are neighbours; lane y looks at piece y
     const Piece mine = s_piece[(lane % kMost) >> 1][lane & 1];
-    const unsigned have = __ballot_sync(0xffffffffu, lane < kMost && mine.head >= 0);
-    if (have == 0) return;
-    // each piece's factor 2^(m - max) for every query row: a warp takes a row of each
-    // tile, a lane a piece, the maxima and sums run over the lanes of the same head
-    const unsigned same = __match_any_sync(0xffffffffu, have >> lane & 1 ? mine.head : -1 - lane);
-    // table `what` (0: the pieces' factors, 1: maxima, 2: sums) of row tile nt, [piece][query row]
-    auto table = [&](int nt, int what) -> float* {
-        return reinterpret_cast<float*>(smem + C::kTableAt) + (nt * 3 + what) * kMost * 8;
-    };
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        static_assert(kWarps == 8, "a warp for each row of a tile");
-        const float* ml = reinterpret_cast<const float*>(piece_at((lane % kMost) >> 1, lane & 1) + C::kPieceO) + nt * 16;
-        const bool in = have >> lane & 1;
-        const float m = in ? ml[warp] : -INFINITY, lw = in ? ml[8 + warp] : 0.f;
-        float top = m, sum = 0.f;
-#pragma unroll
-        for (int y = 0; y < kMost; ++y) {
-            const float my = __shfl_sync(0xffffffffu, m, y);
-            if (same >> y & 1) top = fmaxf(top, my);
-        }
-        const float f = lw == 0.f ? 0.f : ex2_approx(m - top);
-        const float part = f == 0.f ? 0.f : f * lw;
-#pragma unroll
-        for (int y = 0; y < kMost; ++y) {
-            const float py = __shfl_sync(0xffffffffu, part, y);
-            if (same >> y & 1) sum += py;
-        }
-        if (lane < kMost) {
-            table(nt, 0)[lane * 8 + warp] = f;
-            table(nt, 1)[lane * 8 + warp] = top;
-            table(nt, 2)[lane * 8 + warp] = sum;
-        }
-    }
-    __syncthreads();
-    for (unsigned open = have; open != 0;) {
+    unsigned open = __ballot_sync(0xffffffffu, lane < kMost && mine.head >= 0);
+    while (open != 0) {
         const int y0 = __ffs(open) - 1;
-        const unsigned group = __shfl_sync(0xffffffffu, same, y0);
-        const int at = __shfl_sync(0xffffffffu, mine.head, y0), y1 = 31 - __clz(group);
-        const bool whole = __shfl_sync(0xffffffffu, mine.first, y0) && __shfl_sync(0xffffffffu, mine.last, y1);
+        const int at = __shfl_sync(0xffffffffu, mine.head, y0);
+        const unsigned group = __ballot_sync(0xffffffffu, mine.head == at) & open;
+        const bool whole = __shfl_sync(0xffffffffu, mine.first, y0) && __shfl_sync(0xffffffffu, mine.last, 31 - __clz(group));
         open &= ~group;
         const int hr = at % HR;
         const long long bh = static_cast<long long>(at / HR) * p.pages.heads + hr / p.RB;
         const long long slot = blockIdx.x + static_cast<long long>(at);
-        for (int x = warp; x < NT * C::kPairs; x += kWarps) {
-            const int nt = x / C::kPairs, pr = x % C::kPairs;
+        // A head has last pieces of neighbouring warps, and at most one first piece, its
+        // end.  All warps' last pieces are read, of this head or not, and every warp
+        // computes all factors, so that no load waits for another and nothing is passed
+        // round (a loop over the members took three times as long, a table of factors
+        // and its barrier 1 us).
+        const int first_piece = (group & 0x55555555u) != 0 ? __ffs(group & 0x55555555u) - 1 : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j;
-            // A head has last pieces of neighbouring warps, and at most one first piece, its
-            // end.  All warps' last pieces are read, of this head or not, so that no load
-            // waits for another (a loop over the members took three times as long).
-            float2 f[kWarps + 1], v[kWarps + 1], o = make_float2(0.f, 0.f);
-            const int first_piece = (group & 0x55555555u) != 0 ? __ffs(group & 0x55555555u) - 1 : 0;
+            float2 f[kWarps + 1], lw[kWarps + 1], top = make_float2(-INFINITY, -INFINITY), sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int y = 0; y <= kWarps; ++y) {
-                const int at_piece = y < kWarps ? 2 * y + 1 : first_piece;
-                f[y] = *reinterpret_cast<const float2*>(table(nt, 0) + at_piece * 8 + 2 * j);
-                v[y] = reinterpret_cast<const float2*>(piece_at(at_piece >> 1, y < kWarps))[x * 32 + lane];
+                const float2* ml = reinterpret_cast<const float2*>(
+                    piece_at(y < kWarps ? y : first_piece >> 1, y < kWarps) + C::kPieceO) + nt * 8 + j;
+                f[y] = ml[0];
+                lw[y] = ml[4];
+                if (!(group >> (y < kWarps ? 2 * y + 1 : first_piece) & 1)) lw[y] = make_float2(0.f, 0.f);
+                if (lw[y].x != 0.f) top.x = fmaxf(top.x, f[y].x);
+                if (lw[y].y != 0.f) top.y = fmaxf(top.y, f[y].y);
             }
 #pragma unroll
             for (int y = 0; y <= kWarps; ++y) {
-                const bool in = group >> (y < kWarps ? 2 * y + 1 : first_piece) & 1;
-                if (in && f[y].x != 0.f) o.x = fmaf(f[y].x, v[y].x, o.x);
-                if (in && f[y].y != 0.f) o.y = fmaf(f[y].y, v[y].y, o.y);
+                f[y].x = lw[y].x == 0.f ? 0.f : ex2_approx(f[y].x - top.x);
+                f[y].y = lw[y].y == 0.f ? 0.f : ex2_approx(f[y].y - top.y);
+                if (lw[y].x != 0.f) sum.x = fmaf(f[y].x, lw[y].x, sum.x);
+                if (lw[y].y != 0.f) sum.y = fmaf(f[y].y, lw[y].y, sum.y);
             }
-            const float2 sum = *reinterpret_cast<const float2*>(table(nt, 2) + y0 * 8 + 2 * j);
-            if (!whole) {
-                p.part_o[(slot * NT * C::kPairs + x) * 32 + lane] = o;
-            } else {
-                const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
-                __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
-                if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x);
-                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y);
+#pragma unroll
+            for (int xi = 0; xi < C::kPairs / kWarps; ++xi) {
+                const int pr = xi * kWarps + warp;
+                float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y <= kWarps; ++y) {
+                    const float2 v = reinterpret_cast<const float2*>(
+                        piece_at(y < kWarps ? y : first_piece >> 1, y < kWarps))[(nt * C::kPairs + pr) * 32 + lane];
+                    // (a factor of 0 too: a NaN that the piece saw stays one)
+                    if (lw[y].x != 0.f) o.x = fmaf(f[y].x, v.x, o.x);
+                    if (lw[y].y != 0.f) o.y = fmaf(f[y].y, v.y, o.y);
+                }
+                if (!whole) {
+                    p.part_o[((slot * NT + nt) * C::kPairs + pr) * 32 + lane] = o;
+                } else {
+                    const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
+                    __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
+                    if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x);
+                    if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y);
+                }
             }
-        }
-        if (warp == 0 && lane < 8 * NT) {
-            const int nt = lane / 8, c = lane % 8, row = (hr % p.RB) * NT * 8 + lane;
-            const float top = table(nt, 1)[y0 * 8 + c], sum = table(nt, 2)[y0 * 8 + c];
-            if (!whole) {
-                p.part_ml[(slot * NT + nt) * 16 + c] = top;
-                p.part_ml[(slot * NT + nt) * 16 + 8 + c] = sum;
-            } else if (row < p.R) {
-                p.lse[bh * p.R + row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+            if (warp == 0 && g4 == 0) {
+                if (!whole) {
+                    float2* ml = reinterpret_cast<float2*>(p.part_ml + (slot * NT + nt) * 16) + j;
+                    ml[0] = top;
+                    ml[4] = sum;
+                } else {
+                    if (row < p.R) p.lse[bh * p.R + row] = sum.x == 0.f ? -INFINITY : (top.x + __log2f(sum.x)) * kLn2;
+                    if (row + 1 < p.R) p.lse[bh * p.R + row + 1] = sum.y == 0.f ? -INFINITY : (top.y + __log2f(sum.y)) * kLn2;
+                }
             }
         }
     }

@@ -168,6 +168,27 @@ def test_nan_in_a_masked_or_unused_place_stays_there():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("first,count", [(640, 64), (1000, 1), (0, 3000), (2999, 1)])
+@pytest.mark.parametrize("part", [1, 3])
+def test_a_nan_token_is_seen_however_little_it_weighs(first, count, part):
+    # whole stretches of a warp that are NaN, and single tokens, against rows whose other
+    # scores are far above: keys spoil every output, values those of their group
+    c = ref.Batch([3000], 1, 64, 32, 64, seed=18)
+    at, size = ref.sections(64, 32)[part]
+    for t in range(first, first + count):
+        page, block, r = c.table[0][t // 64], t % 64 // 16, t % 16
+        c.pool[page, 0, block, at + r * size:at + r * size + 4] = 255     # the first group's pair
+    q = (c.queries(4, 1).float() * 30).to(torch.bfloat16).cuda()
+    pool, table, held = c.on()
+    o, lse = fa.attention_decode_kv4(q, pool, table, held)
+    assert fa.fa_get_device_status() == 0
+    if part == 1:
+        assert torch.isnan(o).all() and torch.isnan(lse).all()
+    else:
+        assert torch.isnan(o[..., :32]).all() and torch.isfinite(o[..., 32:]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
 def test_a_bad_query_spoils_its_own_row():
     c = ref.Batch([100, 100], 2, 128, 64, 16, seed=11)
     q = c.queries(8, 1)
