@@ -104,7 +104,7 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
     if len(shape) != 4 or code is None or dev < 0:
         raise ValueError("rope takes (B, H, T, D) CUDA tensors of one type: bf16, fp16 or fp32")
     B, _, T, D = shape
-    packed, results, heads = b"", [], 1
+    packed, results, heads = b"", (), 1
     for i, t in enumerate(tensors):
         if i:
             shape = t.shape
@@ -125,7 +125,7 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
             if o.shape != shape or o.dtype is not dtype or o.get_device() != dev or (o.stride(3) != 1 and D > 1):
                 raise ValueError("out must match rope's input in shape, type and device, with contiguous channels")
             ob, oh, ot, _ = o.stride()
-        results.append(o)
+        results += (o,)
         packed += _pack_tensor(t.data_ptr(), o.data_ptr(), H, sb, st, sh, ob, ot, oh)
     rotary = _check_table(table, D, dev)
     pos, pos64, pos_b = _positions(positions, B, T, dev)
@@ -146,7 +146,7 @@ def _make_rope_class():
             ctx.save_for_backward(table, positions)
             ctx.args = interleaved, amplitude, inverse
             got = _rope((q,) if k is None else (q, k), table, positions, interleaved, amplitude, inverse, None)
-            return tuple(got) if k is not None else got[0]
+            return got if k is not None else got[0]
 
         @staticmethod
         def backward(ctx, *grads):
@@ -199,13 +199,13 @@ def rope(q, k, table, positions=None, interleaved: bool = False, amplitude: floa
     if out is None:
         got = _launch_on(q, stream, _rope_any, tensors, table, positions, 1 if interleaved else 0, amplitude,
                          1 if inverse else 0)
-        return tuple(got) if k is not None else got[0]
-    import torch
-    outs = [out] if k is None else list(out)
-    if len(outs) != len(tensors):
-        raise ValueError("out must hold a tensor for each input")
-    if torch.is_grad_enabled() and any(t.requires_grad for t in list(tensors) + outs):
-        raise ValueError("out cannot be given under autograd")
-    got = _launch_on(q, stream, _rope, tensors, table, positions, int(bool(interleaved)), amplitude, int(bool(inverse)),
-                     outs)
-    return tuple(got) if k is not None else got[0]
+    else:
+        outs = (out,) if k is None else tuple(out)
+        if len(outs) != len(tensors):
+            raise ValueError("out must hold a tensor for each input")
+        import torch
+        if torch.is_grad_enabled() and any(t.requires_grad for t in tensors + outs):
+            raise ValueError("out cannot be given under autograd")
+        got = _launch_on(q, stream, _rope, tensors, table, positions, 1 if interleaved else 0, amplitude,
+                         1 if inverse else 0, outs)
+    return got if k is not None else got[0]
