@@ -129,8 +129,8 @@ __device__ __forceinline__ Two quotient(Two d, Two minus_y, Two r) {
 // Codes of 8 channels, and the group's (s, m) pair.
 __device__ __forceinline__ uint32_t quantise8(const uint32_t (&x)[4], float2 range, uint32_t& pair) {
     const float lo = range.x, span = __fsub_rn(range.y, lo);
-    float s = __bfloat162float(__float2bfloat16_rn(
-        quotient(Two(span, 0.f), Two(-15.f, -15.f), Two(1.f / 15.f, 1.f / 15.f)).both().x));
+    const float q15 = __fmul_rn(span, 1.f / 15.f);  // span / 15, as quotient() has it
+    float s = __bfloat162float(__float2bfloat16_rn(__fmaf_rn(__fmaf_rn(-q15, 15.f, span), 1.f / 15.f, q15)));
     if (s < 7.888609052210118e-31f) s = 0.f;  // 2^-100
     pair = as_u32(__floats2bfloat162_rn(s, lo));
     uint32_t word = 0;
@@ -138,14 +138,19 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&x)[4], float2 ran
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
         const Two minus_lo(-lo, -lo), minus_s(-s, -s), rr(r, r);
+        uint32_t even[4], odd[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // 1.5 2^23 more: the low bits are the nearest whole number, ties to even.
+            // 1.5 2^23 more: the low byte is the nearest whole number, ties to even.
             // It is at most 15: s is span / 15 to 2^-9, so the quotient is below 15.1.
             const float2 c = (quotient(unpack(x[i]) + minus_lo, minus_s, rr) + Two(12582912.f, 12582912.f)).both();
-            word += (__float_as_uint(c.x) << (8 * i)) + (__float_as_uint(c.y) << (8 * i + 4));
+            even[i] = __float_as_uint(c.x);
+            odd[i] = __float_as_uint(c.y);
         }
-        word -= 0x3f400000u;  // the eight shifted 0x4b400000, modulo 2^32
+        auto bytes = [](const uint32_t (&n)[4]) {
+            return __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+        };
+        word = bytes(even) + (bytes(odd) << 4);
     }
     if (!(span <= 3.402823466e38f)) {
         pair = 0x7fff7fffu;  // NaN, NaN
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
         }
     }
     // angles of this thread's channels: cos, and sin with the sign of the partner's term
+    // in rope_turn (half layout: negated, as the product is added there)
     float cs[ROT == kInterleaved ? 4 : 8], sn[ROT == kInterleaved ? 4 : 8];
     const int half = p.R >> 1;
     const bool turned = ROT != kNone && oct * 8 < p.R;
@@ -207,8 +213,8 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
             const float oc = __shfl_sync(0xffffffffu, c, partner), os = __shfl_sync(0xffffffffu, s, partner);
             cs[i] = first ? c : oc;
             cs[4 + i] = first ? oc : c;
-            sn[i] = first ? s : -os;
-            sn[4 + i] = first ? os : -s;
+            sn[i] = first ? -s : os;
+            sn[4 + i] = first ? -os : s;
         }
     } else if constexpr (ROT != kNone) {
         if (turned) {
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
 #pragma unroll
                 for (int w = 0; w < 4; ++w)  // rope_turn of two channels
                     kx[w] = pack(fma2(unpack(kx[w]), Two(cs[2 * w], cs[2 * w + 1]),
-                                      unpack(y[w]) * Two(-sn[2 * w], -sn[2 * w + 1])));
+                                      unpack(y[w]) * Two(sn[2 * w], sn[2 * w + 1])));
             }
         } else if constexpr (ROT == kInterleaved) {
             if (turned) {
