@@ -314,7 +314,8 @@ int fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, long 
 
 /*
  * Reads `count` slots of every sequence back, from start[b] (NULL: 0) on.
- *   k, v out: (B, Hkv, count, D) bf16, zeros for slots at or behind the length
+ *   k, v out: (B, Hkv, count, D) bf16, s * code + m rounded once, zeros for slots
+ *             at or behind the length
  * A negative start is recorded as FA_ERR_SEQLEN and reads zeros.
  */
 int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k, void* v, void* stream);
