@@ -240,8 +240,9 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
  *   freq       in: DEVICE uint64[rotary / 2], turns per position in units of
  *                  2^-64 (so the angle is exact modulo a turn at any position)
  *   rotary       : even, 2 .. D;  D: 2 .. FA_ROPE_MAX_D
- *   dtype        : FA_BF16, FA_FP16 or FA_FP32, of every tensor; the rotation
- *                  is computed in float32 and rounded once
+ *   dtype        : FA_BF16, FA_FP16 or FA_FP32, of every tensor; cosine and
+ *                  sine, products and sums are float32, each rounded to nearest,
+ *                  the result rounded to the type
  * FA_ERR_UNSUPPORTED for rotary or dtype, FA_ERR_ARG for overlaps, negative
  * strides or an output whose rows share elements.  No workspace.
  */

@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
             if (turned) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w)  // rope_turn of two channels
-                    kx[w] = pack(fma2(unpack(kx[w]), Two(cs[2 * w], cs[2 * w + 1]),
-                                      unpack(y[w]) * Two(sn[2 * w], sn[2 * w + 1])));
+                    kx[w] = pack(unpack(kx[w]) * Two(cs[2 * w], cs[2 * w + 1]) +
+                                 unpack(y[w]) * Two(sn[2 * w], sn[2 * w + 1]));
             }
         } else if constexpr (ROT == kInterleaved) {
             if (turned) {

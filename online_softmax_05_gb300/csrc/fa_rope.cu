@@ -11,10 +11,10 @@
 //
 // One thread takes the same pairs of one token in several heads, so that an
 // angle is computed once for all of them.  Bound: HBM, each element read and
-// written once.  B=2 H=16+16 T=8192 D=128 bf16 (268 MB) takes 47.3 us with the
-// launch, 84 % of the measured copy rate; holding four heads' loads before the
-// first store took 72 us (118 registers, a quarter of the warps), 16 heads a thread
-// 50.4 us.
+// written once.  B=2 H=16+16 T=8192 D=128 bf16 (268 MB) takes 49.4 us with the
+// launch, 80 % of the measured copy rate (47.3 us with fp32's own sine and cosine);
+// holding four heads' loads before the first store took 72 us (118 registers, a
+// quarter of the warps), 16 heads a thread 50.4 us, against those 47.3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,7 +27,7 @@
 namespace fa {
 namespace {
 
-constexpr int kRopeThreads = 128;  // 256: 51.6 us instead of 47.3 in the case below, the last wave being coarser
+constexpr int kRopeThreads = 128;  // 256: 51.6 us instead of 47.3 in the case above, the last wave being coarser
 
 struct RopeParams {
     RopeTensor t[2];

@@ -2,9 +2,8 @@
 numbers, every element; gradients against the formula's and against differences.
 
 Tolerance of an element: half a step of its type, and for the fp32 arithmetic
-a (|x1| + |x2|) times 4.1e-7, bounded here by 2^-21: the angle is held in 24 bits of
-half a turn (9.5e-8 rad), sine and cosine are within 2 units of 2^-24, the amplitude,
-two products and a sum add 2^-24 each (3 together at most on each term)."""
+2^-22 a (|x1| + |x2|): cosine and sine are rounded to fp32 (2^-24), and so are their
+products with the amplitude, those with x1 and x2, and the sum."""
 import math
 
 import numpy as np
@@ -41,7 +40,7 @@ def turned(x, table, positions, interleaved, amplitude, inverse=False):
 
 def check(got, want, size, dtype):
     got = got.detach().cpu().double().numpy()
-    tol = HALF[dtype] * np.abs(want) + size * 2.0 ** -21 + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    tol = HALF[dtype] * np.abs(want) + size * 2.0 ** -22 + (2.0 ** -25 if dtype == torch.float16 else 0.0)
     assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) - tol).max())
 
 
