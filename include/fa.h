@@ -62,7 +62,8 @@ typedef enum fa_status {
     FA_ERR_ARG = -8,             /* causal not 0/1, or scale not finite */
     FA_ERR_ARCH = -9,            /* current device is not compute capability 10.3 (sm_103a) */
     FA_ERR_SCRATCH = -10,        /* fa_bwd_noalloc: problem needs more than its fixed scratch buffer */
-    FA_ERR_SEQLEN = -11,         /* recorded by a kernel: a cu_seqlens length is negative or above max_seqlen */
+    FA_ERR_SEQLEN = -11,         /* recorded by a kernel: a cu_seqlens length is negative or above max_seqlen,
+                                    or a cache's length or slot is outside its block table or accounts */
     FA_ERR_DEBUG_CHECK = -12,    /* debug library only: a kernel's run-time index failed its bounds check */
     FA_ERR_PAGE = -13            /* recorded by a kernel: a block table names no page of the pool where a token lies */
 } fa_status;
@@ -355,7 +356,9 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
  * a NaN weight counts as the least.  A sequence of at most `budget` tokens
  * stays as it is.  Kept tokens below the new length stay in their slots; those
  * behind it move, in order, to the slots that fall free, so only what has to
- * move is moved (attention does not depend on the order of the slots).
+ * move is moved (attention does not depend on the order of the slots).  The
+ * pages of a sequence that loses tokens must be its own: what moves would move
+ * under any other sequence whose table names them.
  *   weights, slot_positions in: [B][Hkv][slots] float32 / int32
  *   weights_out, positions_out out: the same after the eviction, 0 / -1 behind
  *                  the new length; buffers of their own

@@ -1016,10 +1016,15 @@ int ctas_of(int nt, int num_sms) { return nt == 1 ? 2 * num_sms : num_sms; }
 struct Sizes {
     size_t part_o, part_ml, scores;
 };
+// Whether a CTA takes a head by itself (kByHead).
+bool by_head(const Kv4Shape& c) {
+    const int tokens = c.D == 128 ? Cfg<128, 64, 1>::kTokens : Cfg<64, 64, 1>::kTokens;
+    return static_cast<long long>(c.width) * c.page_size <= static_cast<long long>(kByHead) * kWarps * tokens;
+}
 Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
     const int R = Hq / c.Hkv * Tq, nt = tiles_of(R);
     const size_t RB = (R + 8 * nt - 1) / (8 * nt), bh = static_cast<size_t>(c.B) * c.Hkv;
-    const size_t slots = ctas_of(nt, num_sms) + bh * RB;
+    const size_t slots = by_head(c) ? 0 : ctas_of(nt, num_sms) + bh * RB;
     return {slots * nt * c.D * 8 * 4, slots * nt * 16 * 4,
             weights ? bh * c.width * c.page_size * RB * nt * 8 * 4 : 0};
 }
@@ -1042,8 +1047,6 @@ template <int D, int G, int NT>
 int launch(DecParams p, cudaStream_t stream, int num_sms, int bh, bool weights) {
     using C = Cfg<D, G, NT>;
     static_assert(C::kSmem + 2 * kWarps * static_cast<int>(sizeof(Piece)) + 1024 <= (NT == 1 ? 233472 / 2 : 232448), "shared memory of the resident CTAs");
-    p.by_head = p.cap <= static_cast<long long>(kByHead) * kWarps * C::kTokens;
-    if (p.by_head) p.n_cta = bh * p.RB;
     const auto kernel = weights ? fa_kv4_decode_kernel<D, G, NT, true> : fa_kv4_decode_kernel<D, G, NT, false>;
     static std::atomic<unsigned long long> allowed[2];
     if (!allow_shared_memory(kernel, C::kSmem, allowed[weights])) return -5;
@@ -1082,7 +1085,8 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
     p.RB = (p.R + 8 * nt - 1) / (8 * nt);
     p.Tq = Tq;
     p.causal = causal;
-    p.n_cta = ctas_of(nt, num_sms);
+    p.by_head = by_head(c);
+    p.n_cta = p.by_head ? c.B * c.Hkv * p.RB : ctas_of(nt, num_sms);
     p.cap = static_cast<long long>(c.width) * c.page_size;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;

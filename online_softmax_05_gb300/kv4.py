@@ -166,14 +166,13 @@ def _decode(q, pool, block_table, lengths, causal, scale, weights, weights_out, 
         need = lib.fa_kv4_decode_workspace(B, Hq, heads, Tq, D, slots, int(w_out is not None))
         if need < 0:
             raise FAError(need, "fa_kv4_decode_workspace")
-        need = max(16, need)
         if len(_decode_bytes) > 4096:
             _decode_bytes.clear()
         _decode_bytes[key] = need
-    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     rc = lib.fa_kv4_decode(packed, q.data_ptr(), out.data_ptr(), lse.data_ptr(), Hq, Tq,
                            1.0 / math.sqrt(D) if scale is None else scale, causal, w_in, w_out, w_slots,
-                           workspace.data_ptr(), need, _raw_stream(dev))
+                           workspace.data_ptr() if need else None, need, _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv4_decode")
     return (out, lse) if w_out is None else (out, lse, weights_out)
@@ -217,7 +216,8 @@ def kv4_evict(pool, block_table, lengths, weights, slot_positions, budget: int, 
     """Evicts every sequence down to ``budget`` tokens, each kv head by itself: the
     ``recent`` newest stay, and the ones with the largest accumulated weights.
 
-    Moves what has to move inside the pool and returns (weights, slot_positions,
+    The pages must not be shared with other sequences (a common prefix, say).  Moves
+    what has to move inside the pool and returns (weights, slot_positions,
     lengths, source) to go on with: the accounts after the eviction (0 and -1 behind
     the new length), min(length, budget), and the slot each kept token came from,
     int32 (B, kv heads, budget)."""

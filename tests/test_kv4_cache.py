@@ -305,6 +305,13 @@ def test_lengths_and_pages_that_do_not_fit_are_reported():
         fa.kv4_append(pool, k, k, table, bad.int().cuda(), cu)
         assert fa.fa_get_device_status() == status
         assert fa.fa_get_device_status() == 0
+    pool.copy_(before)          # accounts shorter than a sequence: its tokens are not stored
+    fa.kv4_append(pool, k, k, table, held, cu, weights=torch.zeros(2, 2, 30, device="cuda"))
+    assert fa.fa_get_device_status() == -11
+    whole = before.clone()
+    fa.kv4_append(whole, k, k, table, held, cu)
+    at = table[0].tolist()[:2]
+    assert torch.equal(pool[at], whole[at]) and torch.equal(pool[table[1, :3].long()], before[table[1, :3].long()])
     broken = table.clone()
     broken[0, 1] = c.pool.shape[0]
     pool.copy_(before)

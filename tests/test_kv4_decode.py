@@ -76,7 +76,7 @@ def test_long_and_uneven_batches(dim, group, page):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("each,tq", [(1, 3), (4, 2), (6, 8), (16, 1), (40, 1)])
+@pytest.mark.parametrize("each,tq", [(1, 3), (4, 2), (6, 8), (16, 1), (40, 1), (128, 8)])
 def test_weights_and_masks(each, tq, causal):
     c = ref.Batch([5, 1, 613, 0, 128], 2, 128, 64, 64, seed=each + tq)
     run(c, 2 * each, tq, causal=causal, weights=True)
@@ -263,7 +263,7 @@ def test_same_call_same_bits_on_streams_and_in_graphs():
 @pytest.mark.gpu
 def test_c_entry_takes_its_own_workspace_or_refuses_a_small_one():
     import ctypes
-    c = ref.Batch([500, 20], 2, 64, 64, 16, seed=14)
+    c = ref.Batch([2500, 20], 2, 64, 64, 16, seed=14)
     pool, table, held = c.on()
     q = c.queries(4, 1).cuda()
     want = fa.attention_decode_kv4(q, pool, table, held)

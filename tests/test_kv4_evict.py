@@ -117,6 +117,15 @@ def test_long_sequences():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind,recent", [("low bits", 5000), ("ties", 0)])
+def test_slots_beyond_shared_memory(kind, recent):
+    # more slots than the CTAs of a cluster hold in shared memory: read again each pass
+    c = ref.Batch([200003], 1, 64, 64, 64, seed=6)
+    w, p = accounts(c, 200100, 7, kind)
+    check(c, w, p, 30000, recent)
+
+
+@pytest.mark.gpu
 def test_evicting_twice_is_evicting_once():
     # what moved comes from behind the new length, so the same call on the same accounts
     # finds the same pool behind it and repeats the same moves
