@@ -403,7 +403,7 @@ struct EvictParams {
     int* lengths_out;
     int* source;   // [B][Hkv][budget]
     int* holes;    // workspace: [B][Hkv][budget]
-    int2* moved;   // workspace: [B][Hkv][budget] (from, to)
+    int* movers;   // workspace: [B][Hkv][budget]
     long long slots;
     int budget, recent;
     int row, scale;   // bytes of a token's codes and scales
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams
         const int mine = lane < upto ? cluster.map_shared_rank(s_share, lane)[at] : largest ? INT_MIN : 0;
         return largest ? __reduce_max_sync(0xffffffffu, mine) : __reduce_add_sync(0xffffffffu, mine);
     };
-    int2* moved = p.moved + bh * p.budget;
+    int* movers = p.movers + bh * p.budget;
     if (tid < 8) s_share[tid] = tid == 0 || tid >= 6 ? INT_MIN : 0;
     __syncthreads();
     // ---- the slice, and the newest position
@@ -657,10 +657,12 @@ __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams
     at.y += over_cluster(4, false, rank);
     const int moves = over_cluster(4, false, C);
     walk([&](int slot, bool in, bool keep) {
-        const bool hole = in && !keep && slot < left;
-        const unsigned all = __ballot_sync(0xffffffffu, hole);
-        if (hole) holes[at.x + __popc(all & before)] = slot;
-        at.x += __popc(all);
+        const bool hole = in && !keep && slot < left, mover = keep && slot >= left;
+        const unsigned all_holes = __ballot_sync(0xffffffffu, hole), all_movers = __ballot_sync(0xffffffffu, mover);
+        if (hole) holes[at.x + __popc(all_holes & before)] = slot;
+        if (mover) movers[at.y + __popc(all_movers & before)] = slot;
+        at.x += __popc(all_holes);
+        at.y += __popc(all_movers);
         if (keep && slot < left) {
             const int2 x = slot_at(slot - s0);
             w_out[slot] = __int_as_float(x.x);
@@ -668,21 +670,7 @@ __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams
             source[slot] = slot;
         }
     });
-    cluster.sync();  // the holes are listed
-    walk([&](int slot, bool in, bool keep) {
-        const bool mover = keep && slot >= left;
-        const unsigned all = __ballot_sync(0xffffffffu, mover);
-        if (mover) {
-            const int m = at.y + __popc(all & before), to = holes[m];
-            const int2 x = slot_at(slot - s0);
-            moved[m] = make_int2(slot, to);
-            w_out[to] = __int_as_float(x.x);
-            pos_out[to] = x.y;
-            source[to] = slot;
-        }
-        at.y += __popc(all);
-    });
-    cluster.sync();  // and so are the moves
+    cluster.sync();  // holes and movers are listed
     // ---- move the records: a lane finds the places of one, then 10 lanes (6 at
     // D = 64) copy one, 16 bytes each and a scale row, several records at a time
     const int codes = p.row / 16, parts = 2 * (codes + 1), at_once = 32 / parts;
@@ -695,15 +683,18 @@ __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams
     for (int m0 = (rank * kEvictWarps + warp) * share; m0 < moves; m0 += warps * share) {
         long long src = -1, dst = -1;  // of the record's block, its row in the low bits
         if (lane < share && m0 + lane < moves) {
-            const int2 x = moved[m0 + lane];
-            src = p.pages.block_of(b, x.x >> 4);
-            dst = p.pages.block_of(b, x.y >> 4);
+            const int from = movers[m0 + lane], to = holes[m0 + lane];
+            w_out[to] = w[from];
+            pos_out[to] = pos[from];
+            source[to] = from;
+            src = p.pages.block_of(b, from >> 4);
+            dst = p.pages.block_of(b, to >> 4);
             if (src < 0 || dst < 0) {
                 report(kStatusBadPage);
                 src = -1;
             } else {  // blocks are multiples of 128 bytes
-                src |= x.x & 15;
-                dst |= x.y & 15;
+                src |= from & 15;
+                dst |= to & 15;
             }
         }
         constexpr int kFlight = 4;
@@ -803,7 +794,7 @@ int launch_kv4_read(const Kv4Shape& c, const void* pool, const int* table, const
 }
 
 size_t kv4_evict_workspace(int B, int Hkv, int budget) {
-    return static_cast<size_t>(B) * Hkv * static_cast<size_t>(budget) * 12;
+    return static_cast<size_t>(B) * Hkv * static_cast<size_t>(budget) * 8;
 }
 
 int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int* lengths, const float* weights,
@@ -822,8 +813,8 @@ int launch_kv4_evict(const Kv4Shape& c, void* pool, const int* table, const int*
     p.slots = slots;
     p.budget = budget;
     p.recent = recent;
-    p.moved = static_cast<int2*>(workspace);
-    p.holes = reinterpret_cast<int*>(p.moved + static_cast<size_t>(c.B) * c.Hkv * budget);
+    p.holes = static_cast<int*>(workspace);
+    p.movers = p.holes + static_cast<size_t>(c.B) * c.Hkv * budget;
     p.row = c.D / 2;
     p.scale = c.D / c.group * 4;
     // CTAs of a head: as many as run at once, with two thousand slots or more each,
