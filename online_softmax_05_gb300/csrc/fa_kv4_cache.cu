@@ -161,7 +161,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&x)[4], float2 ran
 
 // A thread takes 8 channels of one token's keys and values in up to `heads_thread`
 // heads: the angles are computed once for them, the G/8 threads of a group find
-// its range with shuffles.  Bound: HBM, k and v once and the records.
+// its range with shuffles.  Bound: its instructions (about 15 a channel) ahead of
+// HBM: 31 k tokens of 8 heads, D = 128 (164 MB) take 51 us, 3.2 TB/s, with the ALUs
+// 61 % busy and three of four issue slots used.  Angles for every head apart and
+// IEEE divisions took 298 us; one fp32 at a time instead of two 67 us.
 template <int D, int G, int ROT>
 __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int heads_thread) {
     wait_for_stream();
@@ -341,7 +344,7 @@ __device__ __forceinline__ uint4 restore8(uint32_t word, uint32_t pair) {
 }
 
 // One thread restores 8 channels of the keys and values of kTokensThread tokens.
-// Bound: HBM, mostly the writes.
+// Bound: HBM, mostly the writes: 201 MB out and 36 in take 38 us, 6.3 TB/s.
 constexpr int kTokensThread = 4;
 template <int D, int G>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(ReadParams p) {
@@ -452,7 +455,10 @@ __device__ __forceinline__ int2 warps_before(int2 v, int2* warp_sums, int2& tota
 // through distributed shared memory; ties go to the lowest slots.  Every hole lies
 // below the new length and every mover at or above it, so the n-th mover takes the
 // n-th hole, no copy touches what another reads, and the moves run in any order.
-// Bound: latency of about ten dependent steps (passes, scans, cluster barriers).
+// Bound: the latency of about ten dependent steps (passes, scans, cluster
+// barriers, 2 to 4 us each), then the moves.  128 heads of up to 8191 slots to 2048
+// take 36 us, 8 heads of 60007 to 8192 38 us; select and move as two kernels with
+// one CTA a head took 92 and 242 us.
 __global__ void __launch_bounds__(kEvictThreads) fa_kv4_evict_kernel(EvictParams p) {
     wait_for_stream();
     extern __shared__ int2 kept_here[];  // (weight's bits, position) of the slice
