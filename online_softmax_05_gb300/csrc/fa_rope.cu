@@ -37,7 +37,9 @@ struct RopeParams {
     int pos64;
     const unsigned long long* freq;
     int T, D, R;
-    int units;         // vector units of one row
+    int units;         // units of one row: of V pairs, of 2 V channels to copy, of 16 bytes to copy
+    int turns, copies; // how many of the first two
+    int wide;          // channel where the third begin
     int heads_thread;  // heads per thread
     long long items;   // B * T * units
     float amp;
@@ -66,10 +68,14 @@ struct alignas(sizeof(E) * V) Vec {
     E e[V];
 };
 
-// A unit of a row: V pairs, or 2 V channels behind the rotated ones.
-template <typename E, int V, bool INTER>
+// A unit of a row: V pairs (interleaved: 2 V channels, of which those behind the
+// rotated ones are copied), 2 V channels to copy, or 16 bytes of them.
+// PART: the last interleaved unit's pairs are not all rotated (registers that the
+// whole ones go without).
+template <typename E, int V, bool INTER, bool PART>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
     wait_for_stream();
+    constexpr int W = 16 / sizeof(E);
     const long long item = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
     if (item >= p.items) return;
     const int u = static_cast<int>(item % p.units);
@@ -78,14 +84,14 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
     const long long b = row / p.T;
     const int half = p.R >> 1;
     const int pair0 = u * V;
-    const bool turned = pair0 < half;
-    // the unit's two vectors of V channels
+    const bool turned = u < p.turns, wide = u >= p.turns + p.copies;
+    // the unit's two vectors of V channels, or its one of W
     int c0, c1;
     if (turned) {
         c0 = INTER ? 2 * pair0 : pair0;
         c1 = INTER ? c0 + V : c0 + half;
     } else {
-        c0 = p.R + 2 * (pair0 - half);
+        c0 = wide ? p.wide + W * (u - p.turns - p.copies) : (INTER ? 2 * V * p.turns : p.R) + 2 * V * (u - p.turns);
         c1 = c0 + V;
     }
     float cs[V], sn[V];
@@ -98,10 +104,11 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            rope_angle(pos, p.freq[pair0 + i], p.amp, cs[i], sn[i]);
+            rope_angle(pos, p.freq[PART ? min(pair0 + i, half - 1) : pair0 + i], p.amp, cs[i], sn[i]);
             if (p.inverse) sn[i] = -sn[i];
         }
     }
+    const int pairs = half - pair0;  // of an interleaved unit: V, or fewer in the last
     const bool tail = V > 1 || c1 < p.D;  // an odd head has a lone last channel
     int h = blockIdx.y * p.heads_thread;
     const int h_end = h + p.heads_thread;
@@ -111,6 +118,12 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
         const E* in = static_cast<const E*>(x.in) + b * x.in_b + static_cast<long long>(t) * x.in_t;
         E* out = static_cast<E*>(x.out) + b * x.out_b + static_cast<long long>(t) * x.out_t;
         const int last = min(h_end, h_base + heads);
+        if (V < W && wide) {
+            for (; h < last; ++h)
+                *reinterpret_cast<uint4*>(out + static_cast<long long>(h - h_base) * x.out_h + c0) =
+                    *reinterpret_cast<const uint4*>(in + static_cast<long long>(h - h_base) * x.in_h + c0);
+            continue;
+        }
 #pragma unroll 4
         for (; h < last; ++h) {
             const E* src = in + static_cast<long long>(h - h_base) * x.in_h;
@@ -128,8 +141,11 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
                 for (int i = 0; i < V; ++i) {
                     const int j1 = INTER ? 2 * i : i, j2 = INTER ? 2 * i + 1 : V + i;
                     const float x1 = to_f(in2[j1]), x2 = to_f(in2[j2]);
-                    in2[j1] = from_f<E>(rope_turn(x1, x2, cs[i], sn[i]));
-                    in2[j2] = from_f<E>(rope_turn(x2, x1, cs[i], -sn[i]));
+                    const E y1 = from_f<E>(rope_turn(x1, x2, cs[i], sn[i])), y2 = from_f<E>(rope_turn(x2, x1, cs[i], -sn[i]));
+                    if (!PART || i < pairs) {  // the others are copied
+                        in2[j1] = y1;
+                        in2[j2] = y2;
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -145,7 +161,15 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(RopeParams p) {
 
 template <typename E, int V>
 int launch(const RopeParams& p, int inter, dim3 grid, cudaStream_t st) {
-    return launch_chained(inter ? fa_rope_kernel<E, V, true> : fa_rope_kernel<E, V, false>, grid, kRopeThreads, 0, st, p);
+    return launch_chained(!inter ? fa_rope_kernel<E, V, false, false>
+                          : p.R / 2 % V ? fa_rope_kernel<E, V, true, (V > 1)>
+                                        : fa_rope_kernel<E, V, true, false>,
+                          grid, kRopeThreads, 0, st, p);
+}
+
+template <typename E>
+int launch16(const RopeParams& p, int V, int inter, dim3 grid, cudaStream_t st) {
+    return V == 8 ? launch<E, 8>(p, inter, grid, st) : V == 2 ? launch<E, 2>(p, inter, grid, st) : launch<E, 1>(p, inter, grid, st);
 }
 
 }  // namespace
@@ -153,19 +177,34 @@ int launch(const RopeParams& p, int inter, dim3 grid, cudaStream_t st) {
 int launch_rope(const RopeTensor* tensors, int n_tensors, const void* positions, int pos64, long long pos_b,
                 const void* freq, int B, int T, int D, int R, int interleaved, float amplitude, int inverse,
                 int dtype, cudaStream_t stream, int num_sms) {
-    const int size = dtype == 2 ? 4 : 2, wide = 16 / size;
-    // 16-byte vectors where every row starts on one and the unit borders fall on them
-    bool vec = (R / 2) % wide == 0 && (D - R) % (2 * wide) == 0;
+    // How far rows are aligned, in channels: to 16 bytes, to 4, or to one channel.
+    const int size = dtype == 2 ? 4 : 2, W = 16 / size;
     RopeParams p{};
     long long heads = 0;
+    uintptr_t grain = 16;
     for (int k = 0; k < n_tensors; ++k) {
         const RopeTensor& x = tensors[k];
         p.t[k] = x;
         heads += x.heads;
-        vec = vec && ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out)) & 15u) == 0;
-        for (long long s : {x.in_b, x.in_t, x.in_h, x.out_b, x.out_t, x.out_h}) vec = vec && s % wide == 0;
+        grain |= reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out);
+        for (long long s : {x.in_b, x.in_t, x.in_h, x.out_b, x.out_t, x.out_h}) grain |= static_cast<uintptr_t>(s) * size;
     }
-    const int V = vec ? wide : 1;
+    const bool by16 = (grain & 15u) == 0, by4 = (grain & 3u) == 0;
+    const int half = R / 2;
+    // Pairs to a unit: as many as make 16-byte vectors, else (16-bit types) 4-byte ones.
+    int V = 1;
+    if (interleaved) {
+        if (by16 && D % (2 * W) == 0) V = W;
+        else if (size == 2 && by4 && D % 4 == 0) V = 2;
+    } else {
+        if (by16 && half % W == 0 && (D - R) % (2 * W) == 0) V = W;
+        else if (size == 2 && by4 && half % 2 == 0 && (D - R) % 4 == 0) V = 2;
+    }
+    p.turns = interleaved ? (half + V - 1) / V : half / V;
+    const int behind = interleaved ? 2 * V * p.turns : R;  // the first channel that no turn covers
+    // narrow turns, wide copies: rows of 16-byte pieces from the next border on
+    p.wide = V < W && by16 && D % W == 0 ? (behind + W - 1) / W * W : D;
+    p.copies = (p.wide - behind + 2 * V - 1) / (2 * V);
     p.n_tensors = n_tensors;
     p.positions = positions;
     p.pos64 = pos64;
@@ -174,7 +213,7 @@ int launch_rope(const RopeTensor* tensors, int n_tensors, const void* positions,
     p.T = T;
     p.D = D;
     p.R = R;
-    p.units = R / 2 / V + (D - R + 2 * V - 1) / (2 * V);
+    p.units = p.turns + p.copies + (D - p.wide + W - 1) / W;
     p.items = static_cast<long long>(B) * T * p.units;
     p.amp = amplitude;
     p.inverse = inverse;
@@ -185,9 +224,8 @@ int launch_rope(const RopeTensor* tensors, int n_tensors, const void* positions,
     const long long blocks = (p.items + kRopeThreads - 1) / kRopeThreads, ny = (heads + per - 1) / per;
     if (blocks > 0x7fffffffLL || ny > 65535) return -2;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ny));
-    if (dtype == 0) return vec ? launch<__nv_bfloat16, 8>(p, interleaved, grid, stream) : launch<__nv_bfloat16, 1>(p, interleaved, grid, stream);
-    if (dtype == 1) return vec ? launch<__half, 8>(p, interleaved, grid, stream) : launch<__half, 1>(p, interleaved, grid, stream);
-    return vec ? launch<float, 4>(p, interleaved, grid, stream) : launch<float, 1>(p, interleaved, grid, stream);
+    if (dtype == 2) return V == 4 ? launch<float, 4>(p, interleaved, grid, stream) : launch<float, 1>(p, interleaved, grid, stream);
+    return dtype == 0 ? launch16<__nv_bfloat16>(p, V, interleaved, grid, stream) : launch16<__half>(p, V, interleaved, grid, stream);
 }
 
 }  // namespace fa

@@ -126,7 +126,9 @@ def test_c_entry_refuses():
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("B,T,Hq,Hkv,D,rotary", [
     (2, 5, 3, 1, 64, 64), (1, 1, 1, 1, 128, 128), (3, 17, 8, 2, 128, 64), (2, 33, 9, 3, 64, 20), (1, 7, 5, 5, 80, 62),
-    (2, 3, 2, 1, 33, 2), (1, 300, 12, 4, 96, 96), (2, 9, 40, 1, 256, 32), (1, 2, 2, 2, 2, 2)])
+    (2, 3, 2, 1, 33, 2), (1, 300, 12, 4, 96, 96), (2, 9, 40, 1, 256, 32), (1, 2, 2, 2, 2, 2),
+    (2, 19, 4, 2, 128, 126), (2, 19, 4, 2, 128, 20), (1, 5, 3, 3, 72, 22), (1, 5, 3, 3, 66, 12), (3, 4, 2, 2, 68, 44),
+    (1, 6, 2, 1, 1024, 1022)])
 def test_rope_matches_the_formula(B, T, Hq, Hkv, D, rotary, interleaved, dtype):
     q, k = fused(B, T, Hq, Hkv, D, dtype, seed=B * T + D)
     table = fa.rotary_frequencies(rotary, device="cuda")
