@@ -1029,15 +1029,19 @@ int ctas_of(int nt, int num_sms) { return nt == 1 ? 2 * num_sms : num_sms; }
 struct Sizes {
     size_t part_o, part_ml, scores;
 };
-// Whether a CTA takes a head by itself (kByHead).
-bool by_head(const Kv4Shape& c) {
+// Whether a CTA takes a head by itself (kByHead): short caches whose heads find room in
+// two rounds of CTAs.  The others are cut like long ones: 1408 heads of 16 rows on 152
+// CTAs take 31 us so and 56 with a CTA each; 512 heads on 304 take 19 and 15.
+bool by_head(const Kv4Shape& c, size_t heads, int n_cta) {
     const int tokens = c.D == 128 ? Cfg<128, 64, 1>::kTokens : Cfg<64, 64, 1>::kTokens;
-    return static_cast<long long>(c.width) * c.page_size <= static_cast<long long>(kByHead) * kWarps * tokens;
+    return heads <= 2 * static_cast<size_t>(n_cta) &&
+           static_cast<long long>(c.width) * c.page_size <= static_cast<long long>(kByHead) * kWarps * tokens;
 }
 Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
     const int R = Hq / c.Hkv * Tq, nt = tiles_of(R);
     const size_t RB = (R + 8 * nt - 1) / (8 * nt), bh = static_cast<size_t>(c.B) * c.Hkv;
-    const size_t slots = by_head(c) ? 0 : ctas_of(nt, num_sms) + bh * RB;
+    const int n_cta = ctas_of(nt, num_sms);
+    const size_t slots = by_head(c, bh * RB, n_cta) ? 0 : n_cta + bh * RB;
     return {slots * nt * c.D * 8 * 4, slots * nt * 16 * 4,
             weights ? bh * c.width * c.page_size * RB * nt * 8 * 4 : 0};
 }
@@ -1098,8 +1102,9 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
     p.RB = (p.R + 8 * nt - 1) / (8 * nt);
     p.Tq = Tq;
     p.causal = causal;
-    p.by_head = by_head(c);
-    p.n_cta = p.by_head ? c.B * c.Hkv * p.RB : ctas_of(nt, num_sms);
+    p.n_cta = ctas_of(nt, num_sms);
+    p.by_head = by_head(c, static_cast<size_t>(c.B) * c.Hkv * p.RB, p.n_cta);
+    if (p.by_head) p.n_cta = c.B * c.Hkv * p.RB;
     p.cap = static_cast<long long>(c.width) * c.page_size;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
