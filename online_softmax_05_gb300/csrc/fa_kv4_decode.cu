@@ -791,15 +791,77 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     // the pieces of a head are neighbours; lane y looks at piece y
     const Piece mine = s_piece[(lane % kMost) >> 1][lane & 1];
     unsigned open = __ballot_sync(0xffffffffu, lane < kMost && mine.head >= 0);
-    while (open != 0) {
+    const unsigned peers = __match_any_sync(0xffffffffu, mine.head) & open;
+    const int heads = __popc(__ballot_sync(0xffffffffu, (peers & ((2u << lane) - 1)) == 1u << lane));
+    // With many heads a warp joins one by itself, or two, from its own pieces alone; with
+    // few all warps join each, a part of the channels a warp.  (1920 heads of about 52
+    // tokens and 16 rows: 39 us for both kernels; 61 when all warps joined each of a
+    // CTA's 8 heads and the second kernel took a block a head.  The second path costs
+    // 8 long sequences 1 us of 217.)
+    const bool alone = heads > kWarps / 2;
+    for (int turn = 0; open != 0; ++turn) {
         const int y0 = __ffs(open) - 1;
         const int at = __shfl_sync(0xffffffffu, mine.head, y0);
         const unsigned group = __ballot_sync(0xffffffffu, mine.head == at) & open;
         const bool whole = __shfl_sync(0xffffffffu, mine.first, y0) && __shfl_sync(0xffffffffu, mine.last, 31 - __clz(group));
         open &= ~group;
+        if (alone && turn % kWarps != warp) continue;
         const int hr = at % HR;
         const long long bh = static_cast<long long>(at / HR) * p.pages.heads + hr / p.RB;
         const long long slot = blockIdx.x + static_cast<long long>(at);
+        auto put = [&](int nt, int pr, int row, float2 o, float2 sum) {
+            if (!whole) {
+                p.part_o[((slot * NT + nt) * C::kPairs + pr) * 32 + lane] = o;
+            } else {
+                const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
+                __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
+                if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x);
+                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y);
+            }
+        };
+        auto put_sums = [&](int nt, int row, float2 top, float2 sum) {
+            if (!whole) {
+                float2* ml = reinterpret_cast<float2*>(p.part_ml + (slot * NT + nt) * 16) + j;
+                ml[0] = top;
+                ml[4] = sum;
+            } else {
+                if (row < p.R) p.lse[bh * p.R + row] = sum.x == 0.f ? -INFINITY : (top.x + __log2f(sum.x)) * kLn2;
+                if (row + 1 < p.R) p.lse[bh * p.R + row + 1] = sum.y == 0.f ? -INFINITY : (top.y + __log2f(sum.y)) * kLn2;
+            }
+        };
+        if (__builtin_expect(alone, 0)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j;
+                float2 o[C::kPairs], top = make_float2(-INFINITY, -INFINITY), sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int pr = 0; pr < C::kPairs; ++pr) o[pr] = make_float2(0.f, 0.f);
+                for (unsigned m = group; m != 0; m &= m - 1) {
+                    const int y = __ffs(m) - 1;
+                    const float2* ml = reinterpret_cast<const float2*>(piece_at(y >> 1, y & 1) + C::kPieceO) + nt * 8 + j;
+                    if (ml[4].x != 0.f) top.x = fmaxf(top.x, ml[0].x);
+                    if (ml[4].y != 0.f) top.y = fmaxf(top.y, ml[0].y);
+                }
+                for (unsigned m = group; m != 0; m &= m - 1) {
+                    const int y = __ffs(m) - 1;
+                    const unsigned char* piece = piece_at(y >> 1, y & 1);
+                    const float2* ml = reinterpret_cast<const float2*>(piece + C::kPieceO) + nt * 8 + j;
+                    const float2 f = make_float2(ex2_approx(ml[0].x - top.x), ex2_approx(ml[0].y - top.y)), lw = ml[4];
+                    if (lw.x != 0.f) sum.x = fmaf(f.x, lw.x, sum.x);
+                    if (lw.y != 0.f) sum.y = fmaf(f.y, lw.y, sum.y);
+#pragma unroll
+                    for (int pr = 0; pr < C::kPairs; ++pr) {
+                        const float2 v = reinterpret_cast<const float2*>(piece)[(nt * C::kPairs + pr) * 32 + lane];
+                        if (lw.x != 0.f) o[pr].x = fmaf(f.x, v.x, o[pr].x);
+                        if (lw.y != 0.f) o[pr].y = fmaf(f.y, v.y, o[pr].y);
+                    }
+                }
+#pragma unroll
+                for (int pr = 0; pr < C::kPairs; ++pr) put(nt, pr, row, o[pr], sum);
+                if (g4 == 0) put_sums(nt, row, top, sum);
+            }
+            continue;
+        }
         // A head has last pieces of neighbouring warps, and at most one first piece, its
         // end.  All warps' last pieces are read, of this head or not, and every warp
         // computes all factors, so that no load waits for another and nothing is passed
@@ -839,30 +901,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     if (lw[y].x != 0.f) o.x = fmaf(f[y].x, v.x, o.x);
                     if (lw[y].y != 0.f) o.y = fmaf(f[y].y, v.y, o.y);
                 }
-                if (!whole) {
-                    p.part_o[((slot * NT + nt) * C::kPairs + pr) * 32 + lane] = o;
-                } else {
-                    const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
-                    __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
-                    if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x);
-                    if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y);
-                }
+                put(nt, pr, row, o, sum);
             }
-            if (warp == 0 && g4 == 0) {
-                if (!whole) {
-                    float2* ml = reinterpret_cast<float2*>(p.part_ml + (slot * NT + nt) * 16) + j;
-                    ml[0] = top;
-                    ml[4] = sum;
-                } else {
-                    if (row < p.R) p.lse[bh * p.R + row] = sum.x == 0.f ? -INFINITY : (top.x + __log2f(sum.x)) * kLn2;
-                    if (row + 1 < p.R) p.lse[bh * p.R + row + 1] = sum.y == 0.f ? -INFINITY : (top.y + __log2f(sum.y)) * kLn2;
-                }
-            }
+            if (warp == 0 && g4 == 0) put_sums(nt, row, top, sum);
         }
     }
 }
 
-// Which parts a head was cut into: CTAs c0 .. c1 hold some of its n units.
+// Which parts a head was cut into: CTAs c0 .. c1 hold some of its n units; `before` are
+// the places of one head before its sequence, `share` those of a CTA.
+__device__ __forceinline__ void cut_of(int before, int HR, int hr, int n, unsigned share, unsigned& c0, unsigned& c1) {
+    const unsigned first = before * HR + hr * (n + kStart) + kStart;  // the first unit's place
+    c0 = first / share;
+    c1 = n == 0 ? c0 : (first + n - 1) / share;
+}
 template <class C>
 __device__ __forceinline__ void parts_of(const DecParams& p, int lane, int b, int hr, int& n, unsigned& c0, unsigned& c1) {
     const int HR = p.pages.heads * p.RB;
@@ -874,10 +926,7 @@ __device__ __forceinline__ void parts_of(const DecParams& p, int lane, int b, in
     int all, before;
     count_places<C::kTokens>(p, lane, b, all, before);
     n = max(places_of<C::kTokens>(length_of(p, b)) - kStart, 0);
-    const unsigned share = static_cast<unsigned>(share_of(p, all * HR)) * kWarps;
-    const unsigned first = before * HR + hr * (n + kStart) + kStart;  // the first unit's place
-    c0 = first / share;
-    c1 = n == 0 ? c0 : (first + n - 1) / share;
+    cut_of(before, HR, hr, n, static_cast<unsigned>(share_of(p, all * HR)) * kWarps, c0, c1);
 }
 
 // A running maximum, sum and output pair, and more of the same head.
@@ -899,25 +948,18 @@ struct Joined {
     __device__ __forceinline__ float lse2(int e) const { return sum[e] == 0.f ? -INFINITY : top[e] + __log2f(sum[e]); }
 };
 
-// Joins the parts of the heads that are cut between CTAs, and writes those that
-// have no tokens.  A CTA takes 8 / SPLIT pairs of accumulators of one (sequence,
-// head, row block), SPLIT warps to a pair taking the parts in turn.
+// Joins the parts of a head, CTAs c0 .. c1's; n is its units, none of them a row of zeros.
 template <class C, int NT, int SPLIT>
-__device__ __forceinline__ void join_parts(const DecParams& p, int head_row, int y, float2 (&sm)[3][8][32]) {
+__device__ __forceinline__ void join_head(const DecParams& p, int b, int hr, int n, unsigned c0, unsigned c1, int y,
+                                          float2 (&sm)[3][8][32]) {
     constexpr int D = C::D;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g4 = lane >> 2, j = lane & 3;
-    const int HR = p.pages.heads * p.RB;
-    const int b = head_row / HR, hr = head_row % HR;
+    const int head_row = b * p.pages.heads * p.RB + hr;
     const long long bh = static_cast<long long>(b) * p.pages.heads + hr / p.RB;
     const int pair = y * (8 / SPLIT) + warp / SPLIT, sub = warp % SPLIT;
     const int nt = pair / C::kPairs, i = pair % C::kPairs;
     const int row = (hr % p.RB) * NT * 8 + nt * 8 + 2 * j, ch = 32 * (i >> 2) + 4 * g4 + (i & 3);
-    int n;
-    unsigned c0, c1;
-    parts_of<C>(p, lane, b, hr, n, c0, c1);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (n > 0 && c0 == c1) return;  // written by its CTA
     Joined all;
     if (n > 0) {
 #pragma unroll 4
@@ -942,6 +984,34 @@ __device__ __forceinline__ void join_parts(const DecParams& p, int head_row, int
         if (row + e >= p.R) continue;
         p.o[(bh * p.R + row + e) * D + ch] = __float2bfloat16_rn(all.sum[e] == 0.f ? 0.f : all.o[e] / all.sum[e]);
         if (i == 0 && g4 == 0) p.lse[bh * p.R + row + e] = all.lse2(e) * kLn2;
+    }
+}
+
+// Joins the parts of the heads that are cut between CTAs, and writes those that
+// have no tokens.  A CTA takes 8 / SPLIT pairs of accumulators of each of `each`
+// heads (sequence, head, row block) in a row, SPLIT warps to a pair taking the parts
+// in turn.  (A CTA a head: 38 us for 1920 heads, most of them whole.)
+template <class C, int NT, int SPLIT>
+__device__ __forceinline__ void join_parts(const DecParams& p, int x, int y, int each, float2 (&sm)[3][8][32]) {
+    const int lane = threadIdx.x & 31;
+    const int HR = p.pages.heads * p.RB, heads = p.B * HR;
+    int head_row = x * each;
+    int b = head_row / HR, hr = head_row - b * HR, all, before;
+    count_places<C::kTokens>(p, lane, b, all, before);
+    int n = max(places_of<C::kTokens>(length_of(p, b)) - kStart, 0);
+    const unsigned share = static_cast<unsigned>(share_of(p, all * HR)) * kWarps;
+    unsigned c0, c1;
+    cut_of(before, HR, hr, n, share, c0, c1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (const int end = min(head_row + each, heads);;) {
+        if (n == 0 || c0 != c1) join_head<C, NT, SPLIT>(p, b, hr, n, c0, c1, y, sm);
+        if (++head_row == end) break;
+        if (++hr == HR) {
+            hr = 0;
+            before += n == 0 ? 0 : n + kStart;
+            n = max(places_of<C::kTokens>(length_of(p, ++b)) - kStart, 0);
+        }
+        cut_of(before, HR, hr, n, share, c0, c1);
     }
 }
 
@@ -999,23 +1069,23 @@ __device__ __forceinline__ void add_weights(const DecParams& p, int bh, int x, i
     }
 }
 
-// What is left when the line is done: blocks below `joins` in y join parts, the
-// others add weights.
+// What is left when the line is done: the first `joins` blocks join parts, D / 8 NT
+// SPLIT / 8 of them in a row the same heads' channels, and the others add weights.
 template <int D, int G, int NT, int SPLIT, bool WEIGHTS>
-__global__ void __launch_bounds__(256) fa_kv4_finish_kernel(DecParams p, int joins) {
+__global__ void __launch_bounds__(256) fa_kv4_finish_kernel(DecParams p, int joins, int each) {
     using C = Cfg<D, G, NT>;
     __shared__ float2 sm[3][8][32];
     static_assert(sizeof(sm) >= 1024 * sizeof(float), "the log-sum-exps of 1024 rows");
     // The lengths may be read at once: this kernel is scheduled when every CTA of the
     // decoding kernel has waited for the kernels before it, so their writes are in L2.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int heads = p.B * p.pages.heads;
-    if (static_cast<int>(blockIdx.y) < joins) {
-        join_parts<C, NT, SPLIT>(p, blockIdx.x, blockIdx.y, sm);
+    constexpr int kY = D / 8 * NT * SPLIT / 8;
+    const int x = blockIdx.x;
+    if (x < joins) {
+        join_parts<C, NT, SPLIT>(p, x / kY, x % kY, each, sm);
     } else if constexpr (WEIGHTS) {
-        // the x dimension counts row blocks too: they share the head's tokens
-        const int x = (blockIdx.y - joins) * p.RB + blockIdx.x / heads, step = (gridDim.y - joins) * p.RB;
-        add_weights<C, NT>(p, blockIdx.x % heads, x, step, reinterpret_cast<float*>(sm));
+        const int heads = p.B * p.pages.heads;
+        add_weights<C, NT>(p, (x - joins) % heads, (x - joins) / heads, (gridDim.x - joins) / heads, reinterpret_cast<float*>(sm));
     }
 }
 
@@ -1031,7 +1101,7 @@ struct Sizes {
 };
 // Whether a CTA takes a head by itself (kByHead): short caches whose heads find room in
 // two rounds of CTAs.  The others are cut like long ones: 1408 heads of 16 rows on 152
-// CTAs take 31 us so and 56 with a CTA each; 512 heads on 304 take 19 and 15.
+// CTAs take 21 us so and 56 with a CTA each; 512 heads on 304 take 19 and 15.
 bool by_head(const Kv4Shape& c, size_t heads, int n_cta) {
     const int tokens = c.D == 128 ? Cfg<128, 64, 1>::kTokens : Cfg<64, 64, 1>::kTokens;
     return heads <= 2 * static_cast<size_t>(n_cta) &&
@@ -1046,18 +1116,24 @@ Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
             weights ? bh * c.width * c.page_size * RB * nt * 8 * 4 : 0};
 }
 
+// Ranges of heads that blocks of the second kernel take, when there are more heads:
+// with 4 blocks to a range, what is resident at once.
+constexpr int kJoiners = 304;
 template <int D, int G, int NT, int SPLIT>
 int launch_finish(const DecParams& p, cudaStream_t stream, int bh, int num_sms) {
-    const int joins = p.by_head ? 0 : D / 8 * NT * SPLIT / 8, heads = bh * p.RB;
-    int adds = 0;
+    // More heads than CTAs are joined several to a block: at most a head a CTA is cut.
+    constexpr int kY = D / 8 * NT * SPLIT / 8;
+    const int heads = bh * p.RB, each = SPLIT > 1 ? 1 : (heads + kJoiners - 1) / kJoiners;
+    const int joins = p.by_head ? 0 : (heads + each - 1) / each * kY;
+    long long adds = 0;  // blocks to a head, sharing its tokens
     if (p.weights_out != nullptr) {
-        const long long most = (p.cap + 256 * p.RB - 1) / (256 * p.RB), want = (8LL * num_sms + heads - 1) / heads;
-        adds = static_cast<int>(most < want ? most : want);
+        const long long most = (p.cap + 255) / 256, want = (8LL * num_sms + bh - 1) / bh;
+        adds = most < want ? most : want;
     }
     if (joins + adds == 0) return 0;
-    const dim3 grid(heads, joins + adds);
+    const dim3 grid(static_cast<unsigned>(joins + adds * bh));
     return launch_chained(adds > 0 ? fa_kv4_finish_kernel<D, G, NT, SPLIT, true> : fa_kv4_finish_kernel<D, G, NT, SPLIT, false>,
-                          grid, 256, 0, stream, p, joins);
+                          grid, 256, 0, stream, p, joins, each);
 }
 
 template <int D, int G, int NT>

@@ -118,6 +118,15 @@ def test_many_sequences_of_every_length():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", FORMATS)
+@pytest.mark.parametrize("each,tq,weights", [(3, 1, False), (4, 5, False), (4, 5, True)])
+def test_many_more_heads_than_ctas_on_short_caches(dim, group, each, tq, weights):
+    # several heads in one CTA, each with two warps' pieces or one; runs of empty sequences, at the end too
+    c = ref.Batch([(i * 37) % 101 if i % 7 else 0 for i in range(90)] + [1, 0, 0], 8, dim, group, 16, seed=dim + tq)
+    run(c, 8 * each, tq, weights=weights)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("each,tq", [(4, 1), (5, 3)])
 @pytest.mark.parametrize("count", [33, 100, 300])
 def test_many_sequences_beside_a_long_one(count, each, tq):
