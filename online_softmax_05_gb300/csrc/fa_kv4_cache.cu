@@ -31,6 +31,7 @@ struct AppendParams {
     const unsigned long long* freq;  // null: keys are stored as they come
     int R, interleaved;
     float amp;
+    float one;  // 1, from the host (see turn2)
     float* weights;       // [B][Hkv][slots] or null: zeroed at the new slots
     int* slot_positions;  // [B][Hkv][slots] or null: the tokens' positions
     long long slots;
@@ -113,6 +114,13 @@ __device__ __forceinline__ uint32_t pack(Two x) {
     const float2 f = x.both();
     return as_u32(__floats2bfloat162_rn(f.x, f.y));
 }
+
+// x c + y s, both products and the sum rounded.  The compiler makes one fused
+// instruction of a packed product and a packed sum, though each is written to round to
+// nearest: one in 70000 of the turned channels then became another bf16 number than the
+// formula's.  A product times a 1 that it cannot know leaves it nothing to fuse, and
+// takes as many instructions.
+__device__ __forceinline__ Two turn2(Two x, Two y, Two c, Two s, Two one) { return fma2(x * c, one, y * s); }
 
 // Quotient d / y, y of at most 8 significant bits and r within an ulp of 1 / y,
 // rounded as the division rounds it: q = d r is off by an ulp or three,
@@ -263,8 +271,8 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
             if (turned) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w)  // rope_turn of two channels
-                    kx[w] = pack(unpack(kx[w]) * Two(cs[2 * w], cs[2 * w + 1]) +
-                                 unpack(y[w]) * Two(sn[2 * w], sn[2 * w + 1]));
+                    kx[w] = pack(turn2(unpack(kx[w]), unpack(y[w]), Two(cs[2 * w], cs[2 * w + 1]),
+                                       Two(sn[2 * w], sn[2 * w + 1]), Two(p.one, p.one)));
             }
         } else if constexpr (ROT == kInterleaved) {
             if (turned) {
@@ -765,6 +773,7 @@ int launch_kv4_append(const Kv4Shape& c, void* pool, const int* table, const voi
     p.R = R;
     p.interleaved = interleaved;
     p.amp = amplitude;
+    p.one = 1.f;
     p.weights = weights;
     p.slot_positions = slot_positions;
     p.slots = slots;

@@ -68,7 +68,7 @@ __device__ __forceinline__ void rope_angle(long long pos, unsigned long long fre
     const float sn = fmaf(t * t2, fmaf(t2, 1.f / 120.f, -1.f / 6.f), t_lo);
     const float cm = t2 * fmaf(t2, 1.f / 24.f, -0.5f);
     const float4 e = kRopeTable.v[k & 255u];
-    const float st = e.z * t, ct = e.x * t;
+    const float st = __fmul_rn(e.z, t), ct = __fmul_rn(e.x, t);  // not fused into the sums: their rest is added below
     const float c_low = fmaf(e.x, cm, e.y) - (fmaf(e.z, t, -st) + fmaf(e.z, sn, e.w * t));
     const float s_low = fmaf(e.z, cm, e.w) + (fmaf(e.x, t, -ct) + fmaf(e.x, sn, e.y * t));
     // the tabled value is 0 or above the product: the sum's rounding is exact this way

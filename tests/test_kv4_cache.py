@@ -208,6 +208,43 @@ def test_append_rotates_as_rope_does(dim, rotary, interleaved, far):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+def test_append_rounds_both_products_of_a_turn(dim):
+    # pairs whose turned channel is a tie between two bf16 numbers when both products are rounded to
+    # 32 bits, and is not when one of them goes into the sum as it is; the smallest of its group, so
+    # that the cache holds it as the group's minimum, exactly
+    table = fa.rotary_frequencies(64, device="cpu")
+    to_bf16 = lambda x: ref.bf16(x).float().numpy()
+    rng, hits = np.random.default_rng(11), []
+    turns = table.numpy().view(np.uint64)
+    for _ in range(4):
+        n = 1 << 21
+        pos, i = rng.integers(0, 1000, n), rng.integers(0, 32, n)
+        a, b = (to_bf16(rng.standard_normal(n)) for _ in range(2))
+        angle = (pos.astype(np.uint64) * turns[i]).astype(np.float64) * (2 * np.pi / 2.0 ** 64)
+        c, s = np.cos(angle).astype(np.float32), np.sin(angle).astype(np.float32)
+        x, y = a * c, b * s
+        u = x - y
+        first = (a.astype(np.float64) * c - y).astype(np.float32)
+        second = (x - b.astype(np.float64) * s).astype(np.float32)
+        sign = np.where(u > 0, -1, 1).astype(np.float32)
+        hit = (to_bf16(u) != to_bf16(first)) | (to_bf16(u) != to_bf16(second))
+        hits += [z[hit] for z in (pos, i, a * sign, b * sign, to_bf16(u) * sign)]
+    pos, i, a, b, u = (np.concatenate(hits[z::5]) for z in range(5))
+    n = len(pos)
+    assert n > 40
+    k, at = torch.zeros(n, 1, dim), torch.arange(n)
+    k[at, 0, i], k[at, 0, i + 32] = torch.from_numpy(a), torch.from_numpy(b)
+    k = k.to(torch.bfloat16).cuda()
+    pool = fa.kv4_pool(n // 16 + 1, 1, dim, page_size=16, group=32)
+    pages = torch.arange(n // 16 + 1, dtype=torch.int32, device="cuda")[None]
+    held, cu = (torch.tensor(z, dtype=torch.int32, device="cuda") for z in ([n], [0, n]))
+    fa.kv4_append(pool, k, torch.zeros_like(k), pages, held, cu, rotary=table.cuda(), positions=torch.from_numpy(pos).cuda())
+    got = fa.kv4_read(pool, pages, held)[0][0, 0].float().cpu().numpy()
+    assert np.array_equal(got[np.arange(n), i], u)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("group", [32, 64])
 def test_append_of_hard_groups(group):
     # equal values, tiny and huge ranges, subnormals, infinities and NaN, ties on the grid
