@@ -1125,9 +1125,11 @@ int launch_finish(const DecParams& p, cudaStream_t stream, int bh, int num_sms) 
     constexpr int kY = D / 8 * NT * SPLIT / 8;
     const int heads = bh * p.RB, each = SPLIT > 1 ? 1 : (heads + kJoiners - 1) / kJoiners;
     const int joins = p.by_head ? 0 : (heads + each - 1) / each * kY;
-    long long adds = 0;  // blocks to a head, sharing its tokens
+    // Blocks to a head, sharing its tokens: what is resident at once (5 an SM).  (8 an SM, two
+    // rounds: 92 us instead of 89 for 2 sequences of 32768 tokens, 59 instead of 57.5 for 24 ragged ones.)
+    long long adds = 0;
     if (p.weights_out != nullptr) {
-        const long long most = (p.cap + 255) / 256, want = (8LL * num_sms + bh - 1) / bh;
+        const long long most = (p.cap + 255) / 256, want = (5LL * num_sms + bh - 1) / bh;
         adds = most < want ? most : want;
     }
     if (joins + adds == 0) return 0;
