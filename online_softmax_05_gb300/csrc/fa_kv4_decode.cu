@@ -63,9 +63,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;
 // The exponent's reference is set this far above the largest score so far (log2
-// units), so that it seldom moves again.  P times a value scale goes to fp16 at
-// up to 2^14, so what is 2^-23 of the largest still has all of its bits.
+// units), so that it seldom moves again.
 constexpr float kAhead = 4.f;
+// Outputs of a piece are sums of P v, P up to 1: held 2^-24 times, so that 2^24 tokens
+// of the largest bf16 values do not overflow.
+constexpr float kPieceUnit = 0x1p-24f;
 // Places on the line for a head's start, its queries' and first copies' latency
 // and its outputs, in units of 32 or 64 tokens.  (1, 2, 3, 4: 45.0, 42.9, 42.1,
 // 42.2 us on 24 ragged sequences, 47.4, 41.4, 41.1, 41.2 on 8 with 16 rows a head,
@@ -204,6 +206,13 @@ __device__ __forceinline__ float2 pow2_parts(int k) {
     return make_float2(__int_as_float((a + 127) << 23), __int_as_float((k - a + 127) << 23));
 }
 
+// The larger magnitude of each half; its sign means nothing.  A NaN gives way.
+__device__ __forceinline__ uint32_t larger_of(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
 // N 32-bit words from shared memory in one load.
 template <int N>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&x)[N]) {
@@ -331,25 +340,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     // two lanes' copies are a loop.)
     const int per_page = p.pages.blocks_page;
     const uint64_t policy = p.RB == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-    int walk_left = 0, walk_page = 0, walk_in = 0;  // blocks left; page of the table; block in the page
+    int walk_left = 0, walk_in = 0, walk_head = 0;  // blocks left; block in the page; key/value head
+    const int* walk_entry = nullptr;                // of that page; inside the sequence's row of the table while blocks are left
     const unsigned char* walk_from = nullptr;       // that block of the head, this lane's 16 bytes; null: no page
-    const int* walk_table = nullptr;
-    long long walk_head = 0;
     auto look_up = [&]() {
         walk_from = nullptr;
-        if (walk_left > 0 && walk_page < p.pages.width) {
-            const int page = walk_table[walk_page];
+        if (walk_left > 0) {
+            const int page = *walk_entry;
             if (page >= 0 && page < p.pages.num_pages)
-                walk_from = p.pages.pool + page * (p.pages.head_bytes() * p.pages.heads) + walk_head;
+                walk_from = p.pages.pool + (page * static_cast<long long>(p.pages.heads) + walk_head) * p.pages.head_bytes() + lane * 16;
         }
     };
     auto walk_to = [&](const Segment& s) {
-        const int block = s.u0 * C::UB;
+        const int block = s.u0 * C::UB, page = block / per_page;
         walk_left = (s.len + 15) / 16 - block;
-        walk_page = block / per_page;
-        walk_in = block - walk_page * per_page;
-        walk_table = p.pages.table + static_cast<long long>(s.b) * p.pages.width;
-        walk_head = s.hr / p.RB * p.pages.head_bytes() + lane * 16;
+        walk_in = block - page * per_page;
+        walk_entry = p.pages.table + static_cast<long long>(s.b) * p.pages.width + page;
+        walk_head = s.hr / p.RB;
         look_up();
         if (walk_from != nullptr) walk_from += walk_in * C::kBlock;
     };
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 --walk_left;
                 if (++walk_in == per_page) {
                     walk_in = 0;
-                    ++walk_page;
+                    ++walk_entry;
                     look_up();
                 }
             }
@@ -416,7 +423,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         uint32_t qf[NT][C::kWords][4];
         uint32_t qs[NT][(C::kGroups + 1) / 2];
         float factor[NT][2];
-        int seen[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
@@ -474,17 +480,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 for (int g = 0; g < C::kGroups; g += 2) qs[nt][g / 2] = pack_bf16x2(group[g], group[g + 1]);
             factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * j);
             factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * j + 4);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int r = row0 + nt * 8 + 2 * j + c;
-                seen[nt][c] = p.causal ? seg.len - (p.Tq - 1 - r % p.Tq) : seg.len;
-            }
         }
         const int all_see = p.causal ? seg.len - (p.Tq - 1) : seg.len;  // tokens every row sees
 
         float acc[NT][C::kWords][2][4];     // O^T: channels 32 w + 4 r + {0,1}, {2,3}
         float om[NT][C::kGroups][2], l[NT][2], ref[NT][2];
-        float cap = 0.f, inv_cap = 0.f;     // power of two at or above every value scale so far
+        // Outputs are held in units of 1 / inv, a power of two: 2^14 over one at or above
+        // every value scale and 2^-13 of every minimum so far (a group of two bf16 numbers
+        // or more has a step above 2^-13 of its minimum, so that the minima of flat groups
+        // alone take part).  P times a scale is then at most 2^14 and no sum overflows,
+        // whatever bf16 numbers the cache stands for.  At the start, the format's least scale's.
+        float inv = 0x1p114f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -501,6 +507,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         // seen by every row; the other units have none of those tests.
         auto use = [&](auto some_hidden, uint32_t unit, uint32_t valid, int t0) {
             constexpr bool edge = decltype(some_hidden)::value;
+            int seen[NT][2];  // tokens that a row sees
+            if constexpr (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = row0 + nt * 8 + 2 * j + c;
+                        seen[nt][c] = p.causal ? seg.len - (p.Tq - 1 - r % p.Tq) : seg.len;
+                    }
+            }
             // ---- S^T = K q^T
             float s[C::UB][NT][4];
 #pragma unroll
@@ -573,26 +589,47 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 }
             }
 
-            // ---- value scales, running maxima
-            uint32_t va[C::UB][C::kGroups], vb[C::UB][C::kGroups];
-            __nv_bfloat162 vmax = __floats2bfloat162_rn(0.f, 0.f);  // of (s, m) pairs
+            // ---- running maxima, of the value scales too
+            // the value scales of a block's two tokens of this lane, 0 where no token is
+            auto value_scales = [&](int ub, uint32_t (&va)[C::kGroups], uint32_t (&vb)[C::kGroups]) {
+                const uint32_t blk = unit + ub * C::kBlock + C::kValueScales;
+                lds(blk + tokA * C::kScaleRow, va);
+                lds(blk + tokB * C::kScaleRow, vb);
+                if constexpr (edge) {
+                    const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
 #pragma unroll
-            for (int ub = 0; ub < C::UB; ++ub) {
-                const uint32_t blk = unit + ub * C::kBlock;
-                lds(blk + C::kValueScales + tokA * C::kScaleRow, va[ub]);
-                lds(blk + C::kValueScales + tokB * C::kScaleRow, vb[ub]);
-                const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        if (!(valid >> ub & 1) || ta >= seg.len) va[g] = 0;
+                        if (!(valid >> ub & 1) || tb >= seg.len) vb[g] = 0;
+                    }
+                }
+            };
+            uint32_t vmax = 0;  // of (s, m) pairs
+            if constexpr (edge) {
 #pragma unroll
-                for (int g = 0; g < C::kGroups; ++g) {
-                    if (edge && (!(valid >> ub & 1) || ta >= seg.len)) va[ub][g] = 0;
-                    if (edge && (!(valid >> ub & 1) || tb >= seg.len)) vb[ub][g] = 0;
-                    vmax = __hmax2(vmax, __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&va[ub][g]),
-                                                 *reinterpret_cast<const __nv_bfloat162*>(&vb[ub][g])));
+                for (int ub = 0; ub < C::UB; ++ub) {
+                    uint32_t va[C::kGroups], vb[C::kGroups];
+                    value_scales(ub, va, vb);
+#pragma unroll
+                    for (int g = 0; g < C::kGroups; ++g) vmax = larger_of(vmax, larger_of(va[g], vb[g]));
+                }
+            } else {  // every token is there: the lanes share the unit's pairs
+                constexpr int kBlocks = C::kGroups == 1 ? 2 : 1;  // a load's
+                constexpr int kPairs = 16 * C::kGroups * kBlocks / 32;
+                const uint32_t at = unit + C::kValueScales +
+                                    (kBlocks == 2 ? (lane >> 4) * C::kBlock + (lane & 15) * 4 : lane * (4 * kPairs));
+#pragma unroll
+                for (int ub = 0; ub < C::UB; ub += kBlocks) {
+                    uint32_t pairs[kPairs];
+                    lds(at + ub * C::kBlock, pairs);
+#pragma unroll
+                    for (int x = 0; x < kPairs; ++x) vmax = larger_of(vmax, pairs[x]);
                 }
             }
-            float vtop = __low2float(vmax);
+            const float2 tops = kv4_scale(vmax);
+            float vtop = fmaxf(fabsf(tops.x), fabsf(tops.y) * 0x1p-13f);
             float mx[NT][2];
-            bool more = vtop > cap;
+            bool more = vtop * inv > 16384.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -608,13 +645,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
                 float shrink = 1.f;
-                if (vtop > cap) {
-                    // twice the power of two at or above it; 2^-100 is the format's least scale
-                    const float up = fmaxf(2.f * __uint_as_float((__float_as_uint(vtop) + 0x007fffffu) & 0x7f800000u),
-                                           7.888609052210118e-31f);
-                    shrink = cap / up;
-                    cap = up;
-                    inv_cap = 16384.f / cap;
+                if (vtop * inv > 16384.f) {
+                    // 2^13 over the power of two at or above it
+                    const int now = (267 << 23) - ((__float_as_int(vtop) + 0x007fffff) & 0x7f800000);
+                    shrink = __int_as_float(max(0x3f800000 + now - __float_as_int(inv), 0));
+                    inv = __int_as_float(now);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -632,12 +667,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                         l[nt][c] *= alpha[c];
                     }
 #pragma unroll
-                    for (int g = 0; g < C::kGroups; ++g) {
-                        om[nt][g][0] *= alpha[0];
-                        om[nt][g][1] *= alpha[1];
+                    for (int c = 0; c < 2; ++c) {
+                        alpha[c] *= shrink;
+#pragma unroll
+                        for (int g = 0; g < C::kGroups; ++g) om[nt][g][c] *= alpha[c];
                     }
-                    alpha[0] *= shrink;
-                    alpha[1] *= shrink;
 #pragma unroll
                     for (int w = 0; w < C::kWords; ++w)
 #pragma unroll
@@ -657,25 +691,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                         s[ub][nt][c] = ex2_approx(fmaf(s[ub][nt][c], factor[nt][c & 1], c & 1 ? -r1 : -r0));
                     l[nt][0] += s[ub][nt][0] + s[ub][nt][2];
                     l[nt][1] += s[ub][nt][1] + s[ub][nt][3];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[ub][nt][c] *= inv;
                 }
             }
 #pragma unroll
             for (int ub = 0; ub < C::UB; ++ub) {
                 const uint32_t blk = unit + ub * C::kBlock + C::kValueCodes + g4 * (C::kWords * 2);
-                uint32_t x0[C::kWords / 2], x1[C::kWords / 2], x2[C::kWords / 2], x3[C::kWords / 2];
-                lds(blk + token_of(2 * j) * C::kRow, x0);
-                lds(blk + token_of(2 * j + 1) * C::kRow, x1);
-                lds(blk + (8 + token_of(2 * j)) * C::kRow, x2);
-                lds(blk + (8 + token_of(2 * j + 1)) * C::kRow, x3);
+                uint32_t va[C::kGroups], vb[C::kGroups];
+                value_scales(ub, va, vb);
+                uint32_t b0[C::kGroups][NT], b1[C::kGroups][NT];
 #pragma unroll
                 for (int g = 0; g < C::kGroups; ++g) {
-                    uint32_t b0[NT], b1[NT];
-                    const float2 wa = kv4_scale(va[ub][g]), wb = kv4_scale(vb[ub][g]);
-                    const float ka = wa.x * inv_cap, kb = wb.x * inv_cap;
+                    const float2 wa = kv4_scale(va[g]), wb = kv4_scale(vb[g]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* q = s[ub][nt];
-                        float w0 = q[0] * ka, w1 = q[1] * ka, w2 = q[2] * kb, w3 = q[3] * kb;
+                        float w0 = q[0] * wa.x, w1 = q[1] * wa.x, w2 = q[2] * wb.x, w3 = q[3] * wb.x;
                         if constexpr (!edge) {
                             om[nt][g][0] = fmaf(q[0], wa.y, fmaf(q[2], wb.y, om[nt][g][0]));
                             om[nt][g][1] = fmaf(q[1], wa.y, fmaf(q[3], wb.y, om[nt][g][1]));
@@ -691,9 +723,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                             if (tb >= seen[nt][1]) w3 = 0.f;
                             else om[nt][g][1] = fmaf(q[3], wb.y, om[nt][g][1]);
                         }
-                        b0[nt] = transpose8(pack_f16(w0, w1));
-                        b1[nt] = transpose8(pack_f16(w2, w3));
+                        b0[g][nt] = transpose8(pack_f16(w0, w1));
+                        b1[g][nt] = transpose8(pack_f16(w2, w3));
                     }
+                }
+                uint32_t x0[C::kWords / 2], x1[C::kWords / 2], x2[C::kWords / 2], x3[C::kWords / 2];
+                lds(blk + token_of(2 * j) * C::kRow, x0);
+                lds(blk + token_of(2 * j + 1) * C::kRow, x1);
+                lds(blk + (8 + token_of(2 * j)) * C::kRow, x2);
+                lds(blk + (8 + token_of(2 * j + 1)) * C::kRow, x3);
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) {
 #pragma unroll
                     for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
                         const uint32_t sel = w & 1 ? 0x7632u : 0x5410u;
@@ -703,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_f16(acc[nt][w][0], z0 & 0x000f000fu, z0 & 0x00f000f0u, z1 & 0x000f000fu,
-                                    z1 & 0x00f000f0u, b0[nt], b1[nt]);
+                                    z1 & 0x00f000f0u, b0[g][nt], b1[g][nt]);
                             mma_f16(acc[nt][w][1], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu,
-                                    y1 & 0x00f000f0u, b0[nt], b1[nt]);
+                                    y1 & 0x00f000f0u, b0[g][nt], b1[g][nt]);
                         }
                     }
                 }
@@ -730,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         working = advance(next);
         if (working) prologue(next);
         const bool first = seg.u0 == 0, last = seg.u1 == seg.n;
-        const float unit_o = cap * 1024.f;  // 2^24 of the codes over the 2^14 of P
+        const float unit_o = __int_as_float((254 << 23) - __float_as_int(inv));  // 1 / inv
         // a head that ends here and began before, or goes on behind this warp's share
         Piece* piece = &s_piece[warp][working ? 0 : 1];
         float2* out = reinterpret_cast<float2*>(piece_at(warp, working ? 0 : 1));
@@ -757,15 +797,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             for (int w = 0; w < C::kWords; ++w)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float k = i & 1 ? unit_o * 0.0625f : unit_o;
+                    const float k = i & 1 ? 0x1p20f : 0x1p24f;  // the codes' unit
                     const float x0 = fmaf(acc[nt][w][i >> 1][2 * (i & 1)], k, om[nt][w * 32 / G][0]);
                     const float x1 = fmaf(acc[nt][w][i >> 1][2 * (i & 1) + 1], k, om[nt][w * 32 / G][1]);
                     if (first && last) {
                         __nv_bfloat16* to = p.o + (static_cast<long long>(bh) * p.R + row) * D + 32 * w + 4 * g4 + i;
-                        if (row < p.R) to[0] = __float2bfloat16_rn(x0 * n0);
-                        if (row + 1 < p.R) to[D] = __float2bfloat16_rn(x1 * n1);
+                        if (row < p.R) to[0] = __float2bfloat16_rn(x0 * n0 * unit_o);
+                        if (row + 1 < p.R) to[D] = __float2bfloat16_rn(x1 * n1 * unit_o);
                     } else {
-                        out[(nt * C::kPairs + w * 4 + i) * 32 + lane] = make_float2(x0, x1);
+                        out[(nt * C::kPairs + w * 4 + i) * 32 + lane] = make_float2(x0 * kPieceUnit * unit_o, x1 * kPieceUnit * unit_o);
                     }
                 }
             if (g4 == 0) {
@@ -815,8 +855,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             } else {
                 const int ch = 32 * (pr >> 2) + 4 * g4 + (pr & 3);
                 __nv_bfloat16* to = p.o + (bh * p.R + row) * D + ch;
-                if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x);
-                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y);
+                if (row < p.R) to[0] = __float2bfloat16_rn(sum.x == 0.f ? 0.f : o.x / sum.x * (1.f / kPieceUnit));
+                if (row + 1 < p.R) to[D] = __float2bfloat16_rn(sum.y == 0.f ? 0.f : o.y / sum.y * (1.f / kPieceUnit));
             }
         };
         auto put_sums = [&](int nt, int row, float2 top, float2 sum) {
@@ -982,7 +1022,8 @@ __device__ __forceinline__ void join_head(const DecParams& p, int b, int hr, int
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (row + e >= p.R) continue;
-        p.o[(bh * p.R + row + e) * D + ch] = __float2bfloat16_rn(all.sum[e] == 0.f ? 0.f : all.o[e] / all.sum[e]);
+        p.o[(bh * p.R + row + e) * D + ch] =
+            __float2bfloat16_rn(all.sum[e] == 0.f ? 0.f : all.o[e] / all.sum[e] * (1.f / kPieceUnit));
         if (i == 0 && g4 == 0) p.lse[bh * p.R + row + e] = all.lse2(e) * kLn2;
     }
 }

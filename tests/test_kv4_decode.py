@@ -330,3 +330,37 @@ def test_reading_back_and_decoding_in_bf16_agree():
         size = np.einsum("hid,htd->hit", np.abs(q64), np.abs(ks + km)).max() * 128 ** -0.5
         bound = (2.0 ** -7 + 2 * size * 2.0 ** -8) * np.abs(vs + vm).max()
         assert np.abs((o[b] - o2[b]).cpu().double().numpy()).max() <= bound
+
+
+def rescaled(c, part, factor=1.0, minima=None, steps=None):
+    """Multiplies the (s, m) pairs of the keys (part 1) or values (3) by `factor`, which broadcasts to
+    (pages, heads, blocks, 16, groups); `steps` and `minima` replace s and m first."""
+    at, size = ref.sections(c.dim, c.group)[part]
+    pairs = torch.from_numpy(c.pool[..., at:at + 16 * size].copy()).view(torch.bfloat16)
+    x = pairs.double().view(*pairs.shape[:-1], 16, -1, 2)
+    for i, given in ((0, steps), (1, minima)):
+        if given is not None:
+            x[..., i] = torch.where(x[..., i].isnan(), x[..., i], torch.as_tensor(given, dtype=torch.float64))
+    x = x * torch.as_tensor(factor, dtype=torch.float64)[..., None]
+    pairs = x.float().to(torch.bfloat16).view(pairs.shape)     # powers of two: exact
+    c.pool[..., at:at + 16 * size] = pairs.view(torch.uint8).numpy()
+
+
+def place(c, b, t):
+    """The pool's (page, block, row) of a token."""
+    return c.table[b][t // c.page], t % c.page // 16, t % 16
+
+
+# a head to a CTA; cut over CTAs; whole heads in a warp; several heads a CTA, joined by a warp each
+SHAPES = [([117, 40], 2, 4, 1), ([5000, 77], 2, 4, 2), ([30, 31, 900], 2, 16, 1), ([(i * 37) % 101 for i in range(90)], 8, 4, 5)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", FORMATS)
+@pytest.mark.parametrize("lengths,heads,each,tq", SHAPES)
+def test_values_near_the_largest_bf16_numbers_stay_finite(lengths, heads, each, tq, dim, group):
+    # groups that span 2^125 and minima of -2^123, as kv4_append stores them and kv4_read returns them
+    c = ref.Batch(lengths, heads, dim, group, 64, seed=21)
+    rescaled(c, 3, 2.0 ** 122)
+    got = run(c, heads * each, tq)
+    assert torch.isfinite(got[0]).all()
