@@ -485,12 +485,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 
         float acc[NT][C::kWords][2][4];     // O^T: channels 32 w + 4 r + {0,1}, {2,3}
         float om[NT][C::kGroups][2], l[NT][2], ref[NT][2];
-        // Outputs are held in units of 1 / inv, a power of two: 2^14 over one at or above
-        // every value scale and 2^-13 of every minimum so far (a group of two bf16 numbers
-        // or more has a step above 2^-13 of its minimum, so that the minima of flat groups
-        // alone take part).  P times a scale is then at most 2^14 and no sum overflows,
-        // whatever bf16 numbers the cache stands for.  At the start, the format's least scale's.
-        float inv = 0x1p114f;
+        // A row's outputs are held in units of 1 / inv, a power of two: 2^14 over one at or
+        // above every value scale and 2^-13 of every minimum that the row saw (a group of two
+        // bf16 numbers or more has a step above 2^-13 of its minimum, so that the minima of
+        // flat groups alone take part).  P times a scale is then at most 2^14 and no sum
+        // overflows, whatever bf16 numbers the cache stands for.  At the start, the format's
+        // least scale's.  Rows differ in the units with tokens that some do not see only.
+        float inv[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -501,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             for (int g = 0; g < C::kGroups; ++g) om[nt][g][0] = om[nt][g][1] = 0.f;
             l[nt][0] = l[nt][1] = 0.f;
             ref[nt][0] = ref[nt][1] = -INFINITY;
+            inv[nt][0] = inv[nt][1] = 0x1p114f;
         }
 
         // One unit in the ring at `unit`.  some_hidden: a token of it is not there or not
@@ -604,20 +606,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     }
                 }
             };
-            uint32_t vmax = 0;  // of (s, m) pairs
+            // what the outputs' unit goes by: the largest of a row's (s, 2^-13 m)
+            auto size_of = [](uint32_t pair) {
+                const float2 x = kv4_scale(pair);
+                return fmaxf(fabsf(x.x), fabsf(x.y) * 0x1p-13f);
+            };
+            float vtop[NT][2];
             if constexpr (edge) {
 #pragma unroll
+                for (int nt = 0; nt < NT; ++nt) vtop[nt][0] = vtop[nt][1] = 0.f;
+#pragma unroll
                 for (int ub = 0; ub < C::UB; ++ub) {
-                    uint32_t va[C::kGroups], vb[C::kGroups];
+                    uint32_t va[C::kGroups], vb[C::kGroups], ma = 0, mb = 0;
                     value_scales(ub, va, vb);
 #pragma unroll
-                    for (int g = 0; g < C::kGroups; ++g) vmax = larger_of(vmax, larger_of(va[g], vb[g]));
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        ma = larger_of(ma, va[g]);
+                        mb = larger_of(mb, vb[g]);
+                    }
+                    const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            if (ta < seen[nt][c]) vtop[nt][c] = fmaxf(vtop[nt][c], size_of(ma));
+                            if (tb < seen[nt][c]) vtop[nt][c] = fmaxf(vtop[nt][c], size_of(mb));
+                        }
                 }
-            } else {  // every token is there: the lanes share the unit's pairs
+            } else {  // every row sees every token: the lanes share the unit's pairs
                 constexpr int kBlocks = C::kGroups == 1 ? 2 : 1;  // a load's
                 constexpr int kPairs = 16 * C::kGroups * kBlocks / 32;
                 const uint32_t at = unit + C::kValueScales +
                                     (kBlocks == 2 ? (lane >> 4) * C::kBlock + (lane & 15) * 4 : lane * (4 * kPairs));
+                uint32_t vmax = 0;
 #pragma unroll
                 for (int ub = 0; ub < C::UB; ub += kBlocks) {
                     uint32_t pairs[kPairs];
@@ -625,11 +646,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                     for (int x = 0; x < kPairs; ++x) vmax = larger_of(vmax, pairs[x]);
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) vtop[nt][0] = vtop[nt][1] = size_of(vmax);
             }
-            const float2 tops = kv4_scale(vmax);
-            float vtop = fmaxf(fabsf(tops.x), fabsf(tops.y) * 0x1p-13f);
             float mx[NT][2];
-            bool more = vtop * inv > 16384.f;
+            bool more = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -639,17 +660,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     for (int ub = 1; ub < C::UB; ++ub)
                         mx[nt][c] = fmaxf(mx[nt][c], fmaxf(s[ub][nt][c], s[ub][nt][c + 2]));
                     mx[nt][c] *= factor[nt][c];
-                    more = more || mx[nt][c] > ref[nt][c];
+                    more = more || mx[nt][c] > ref[nt][c] || vtop[nt][c] * inv[nt][c] > 16384.f;
                 }
             if (__any_sync(0xffffffffu, more)) {
+                if constexpr (!edge) {  // the lanes of a row hold some of the unit's tokens only
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-                float shrink = 1.f;
-                if (vtop * inv > 16384.f) {
-                    // 2^13 over the power of two at or above it
-                    const int now = (267 << 23) - ((__float_as_int(vtop) + 0x007fffff) & 0x7f800000);
-                    shrink = __int_as_float(max(0x3f800000 + now - __float_as_int(inv), 0));
-                    inv = __int_as_float(now);
+                    for (int o = 1; o < 4; o <<= 1) vtop[0][0] = fmaxf(vtop[0][0], __shfl_xor_sync(0xffffffffu, vtop[0][0], o));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) vtop[nt][0] = vtop[nt][1] = vtop[0][0];
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -668,7 +686,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     }
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        alpha[c] *= shrink;
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1)
+                            vtop[nt][c] = fmaxf(vtop[nt][c], __shfl_xor_sync(0xffffffffu, vtop[nt][c], o));
+                        if (vtop[nt][c] * inv[nt][c] > 16384.f) {
+                            // 2^13 over the power of two at or above it
+                            const int now = (267 << 23) - ((__float_as_int(vtop[nt][c]) + 0x007fffff) & 0x7f800000);
+                            alpha[c] *= __int_as_float(max(0x3f800000 + now - __float_as_int(inv[nt][c]), 0));
+                            inv[nt][c] = __int_as_float(now);
+                        }
 #pragma unroll
                         for (int g = 0; g < C::kGroups; ++g) om[nt][g][c] *= alpha[c];
                     }
@@ -692,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     l[nt][0] += s[ub][nt][0] + s[ub][nt][2];
                     l[nt][1] += s[ub][nt][1] + s[ub][nt][3];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[ub][nt][c] *= inv;
+                    for (int c = 0; c < 4; ++c) s[ub][nt][c] *= inv[nt][c & 1];
                 }
             }
 #pragma unroll
@@ -770,7 +796,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         working = advance(next);
         if (working) prologue(next);
         const bool first = seg.u0 == 0, last = seg.u1 == seg.n;
-        const float unit_o = __int_as_float((254 << 23) - __float_as_int(inv));  // 1 / inv
         // a head that ends here and began before, or goes on behind this warp's share
         Piece* piece = &s_piece[warp][working ? 0 : 1];
         float2* out = reinterpret_cast<float2*>(piece_at(warp, working ? 0 : 1));
@@ -793,6 +818,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             }
             const int row = row0 + nt * 8 + 2 * j;
             const float n0 = l[nt][0] == 0.f ? 0.f : 1.f / l[nt][0], n1 = l[nt][1] == 0.f ? 0.f : 1.f / l[nt][1];
+            float unit_o[2];  // 1 / inv
+#pragma unroll
+            for (int c = 0; c < 2; ++c) unit_o[c] = __int_as_float((254 << 23) - __float_as_int(inv[nt][c]));
 #pragma unroll
             for (int w = 0; w < C::kWords; ++w)
 #pragma unroll
@@ -802,10 +830,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     const float x1 = fmaf(acc[nt][w][i >> 1][2 * (i & 1) + 1], k, om[nt][w * 32 / G][1]);
                     if (first && last) {
                         __nv_bfloat16* to = p.o + (static_cast<long long>(bh) * p.R + row) * D + 32 * w + 4 * g4 + i;
-                        if (row < p.R) to[0] = __float2bfloat16_rn(x0 * n0 * unit_o);
-                        if (row + 1 < p.R) to[D] = __float2bfloat16_rn(x1 * n1 * unit_o);
+                        if (row < p.R) to[0] = __float2bfloat16_rn(x0 * n0 * unit_o[0]);
+                        if (row + 1 < p.R) to[D] = __float2bfloat16_rn(x1 * n1 * unit_o[1]);
                     } else {
-                        out[(nt * C::kPairs + w * 4 + i) * 32 + lane] = make_float2(x0 * kPieceUnit * unit_o, x1 * kPieceUnit * unit_o);
+                        out[(nt * C::kPairs + w * 4 + i) * 32 + lane] =
+                            make_float2(x0 * kPieceUnit * unit_o[0], x1 * kPieceUnit * unit_o[1]);
                     }
                 }
             if (g4 == 0) {

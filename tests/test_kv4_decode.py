@@ -364,3 +364,19 @@ def test_values_near_the_largest_bf16_numbers_stay_finite(lengths, heads, each, 
     rescaled(c, 3, 2.0 ** 122)
     got = run(c, heads * each, tq)
     assert torch.isfinite(got[0]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("apart", [30, 118, -118])
+@pytest.mark.parametrize("each,tq", [(1, 2), (4, 4), (2, 8)])
+@pytest.mark.parametrize("length", [9, 33, 700, 5000])
+def test_a_token_that_a_row_does_not_see_does_not_touch_it(length, each, tq, apart):
+    # the last token's values 2^118 times the others', or all others 2^118 times its own: the rows
+    # before it do not see it
+    c = ref.Batch([length, 1], 2, 128, 64, 64, seed=25)
+    page, block, r = place(c, 0, length - 1)
+    factor = torch.full((*c.pool.shape[:3], 16, 2), 2.0 ** max(0, -apart), dtype=torch.float64)
+    factor[page, :, block, r] = 2.0 ** max(0, apart)
+    rescaled(c, 3, factor)
+    got = run(c, 2 * each, tq)
+    assert torch.isfinite(got[0]).all()
