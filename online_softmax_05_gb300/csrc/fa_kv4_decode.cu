@@ -8,7 +8,8 @@
 // scale multiplies P before the second product.  K's minima, bf16 numbers, are a
 // small product of their own with sum(q_g) in three bf16 pieces (24 bits); V's are
 // fp32 sums.  P times V's scale is rounded to fp16 (2^-11, where bf16 would lose
-// 2^-8 as much as the output's own rounding); everything else is fp32.
+// 2^-8 as much as the output's own rounding), in several bands of scales where they
+// lie more than 2^10 apart (kLeast); everything else is fp32.
 //
 // Codes as fp16.  A nibble masked into the low bits of a 16-bit half is the
 // fp16 subnormal n 2^-24 (bits 0-3) or n 2^-20 (bits 4-7), which the matrix
@@ -65,6 +66,15 @@ constexpr int kStages = 2;
 // The exponent's reference is set this far above the largest score so far (log2
 // units), so that it seldom moves again.
 constexpr float kAhead = 4.f;
+// P times a value scale goes to fp16 in units that put the largest scale at 2^12 or above and
+// the largest P at 2^-4 or above.  While every scale of a unit is kLeast or more there, 2^-10
+// of the largest or so, what weighs 2^-12 of the heaviest token or more keeps all of its bits.
+// From a smaller scale on, the values go through the products in bands: each P times a scale
+// in the first of them that brings it to kLeast, a further kBand (2^12) up each time, the
+// accumulators in units as much smaller meanwhile; the bands reach down to scales 2^-106 of
+// the largest.  (64 heads of 32768 tokens: 67.0 us without looking for such scales, 67.7
+// with it; 123, 153 and 245 where two groups lie 2^14, 2^30 and 2^60 apart.)
+constexpr float kLeast = 4.f, kBand = 4096.f, kLastBand = 0x1p96f;
 // Outputs of a piece are sums of P v, P up to 1: held 2^-24 times, so that 2^24 tokens
 // of the largest bf16 values do not overflow.
 constexpr float kPieceUnit = 0x1p-24f;
@@ -211,6 +221,17 @@ __device__ __forceinline__ uint32_t larger_of(uint32_t x, uint32_t y) {
     uint32_t r;
     asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+// (2^14 / inv, 2^27 / inv), inv a power of two of 2^-112 to 2^114; the second at most 2^127.
+__device__ __forceinline__ uint32_t range_of(float inv) {
+    const uint32_t most = (268u << 7) - (__float_as_uint(inv) >> 16);
+    return most | min(most + (13u << 7), 254u << 7) << 16;
+}
+__device__ __forceinline__ uint32_t smaller_of(uint32_t x, uint32_t y) {
+    const __nv_bfloat162 r = __hmin2(as_bf2(x), as_bf2(y));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // N 32-bit words from shared memory in one load.
@@ -492,6 +513,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         // overflows, whatever bf16 numbers the cache stands for.  At the start, the format's
         // least scale's.  Rows differ in the units with tokens that some do not see only.
         float inv[NT][2];
+        uint32_t range = range_of(0x1p114f);  // the scales and minima that inv is for, at most
+        uint32_t lowest = 0x7f807f80u;           // the least step but 0 so far of this lane's share of them, in the low half
+        float deepest = 1.f;  // the last band's factor; units take all bands from the first that needs another on
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -506,8 +530,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         }
 
         // One unit in the ring at `unit`.  some_hidden: a token of it is not there or not
-        // seen by every row; the other units have none of those tests.
-        auto use = [&](auto some_hidden, uint32_t unit, uint32_t valid, int t0) {
+        // seen by every row, or its scales take more than one band; the other units have none
+        // of those tests, and return true, with nothing added, where the scales do.
+        auto use = [&](auto some_hidden, uint32_t unit, uint32_t valid, int t0) -> bool {
             constexpr bool edge = decltype(some_hidden)::value;
             int seen[NT][2];  // tokens that a row sees
             if constexpr (edge) {
@@ -606,51 +631,68 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     }
                 }
             };
-            // what the outputs' unit goes by: the largest of a row's (s, 2^-13 m)
+            // what the outputs' unit goes by, the largest of a row's (s, 2^-13 m), and the least s
             auto size_of = [](uint32_t pair) {
                 const float2 x = kv4_scale(pair);
                 return fmaxf(fabsf(x.x), fabsf(x.y) * 0x1p-13f);
             };
+            auto step_of = [](uint32_t pair) {  // a step of 0 adds nothing (2^-100 is the format's least)
+                const float s = kv4_scale(pair).x;
+                return s >= 0x1p-101f ? s : INFINITY;
+            };
+            auto pair_of_step = [](float s) { return __float_as_uint(s) >> 16 | 0x7f800000u; };
             float vtop[NT][2];
+            uint32_t least = 0;
+            bool more = false;  // the scales leave the range that the outputs' unit is for
             if constexpr (edge) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) vtop[nt][0] = vtop[nt][1] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
+                    for (int c = 0; c < 2; ++c) vtop[nt][c] = 0.f;
+                float low = step_of(lowest);
+#pragma unroll 1
                 for (int ub = 0; ub < C::UB; ++ub) {
-                    uint32_t va[C::kGroups], vb[C::kGroups], ma = 0, mb = 0;
-                    value_scales(ub, va, vb);
+                    uint32_t v[2][C::kGroups];
+                    value_scales(ub, v[0], v[1]);
 #pragma unroll
-                    for (int g = 0; g < C::kGroups; ++g) {
-                        ma = larger_of(ma, va[g]);
-                        mb = larger_of(mb, vb[g]);
-                    }
-                    const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t most = 0;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            if (ta < seen[nt][c]) vtop[nt][c] = fmaxf(vtop[nt][c], size_of(ma));
-                            if (tb < seen[nt][c]) vtop[nt][c] = fmaxf(vtop[nt][c], size_of(mb));
+                        for (int g = 0; g < C::kGroups; ++g) {
+                            most = larger_of(most, v[x][g]);
+                            low = fminf(low, step_of(v[x][g]));
                         }
+                        const float top = size_of(most);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (t0 + ub * 16 + tokA + 8 * x < seen[nt][c]) vtop[nt][c] = fmaxf(vtop[nt][c], top);
+                    }
                 }
+                lowest = pair_of_step(low);
             } else {  // every row sees every token: the lanes share the unit's pairs
                 constexpr int kBlocks = C::kGroups == 1 ? 2 : 1;  // a load's
                 constexpr int kPairs = 16 * C::kGroups * kBlocks / 32;
                 const uint32_t at = unit + C::kValueScales +
                                     (kBlocks == 2 ? (lane >> 4) * C::kBlock + (lane & 15) * 4 : lane * (4 * kPairs));
-                uint32_t vmax = 0;
+                uint32_t most = 0;
+                least = lowest;  // and steps of 0
 #pragma unroll
                 for (int ub = 0; ub < C::UB; ub += kBlocks) {
                     uint32_t pairs[kPairs];
                     lds(at + ub * C::kBlock, pairs);
 #pragma unroll
-                    for (int x = 0; x < kPairs; ++x) vmax = larger_of(vmax, pairs[x]);
+                    for (int x = 0; x < kPairs; ++x) {
+                        most = larger_of(most, pairs[x]);
+                        least = smaller_of(least, pairs[x]);
+                    }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) vtop[nt][0] = vtop[nt][1] = size_of(vmax);
+                vtop[0][0] = size_of(most);
+                const uint32_t floor = (range - (12u << 7) & 0xffffu) | 0xff800000u;  // (kLeast / inv, -infinity)
+                more = !__hble2(as_bf2(most & 0x7fff7fffu), as_bf2(range)) || !__hbge2(as_bf2(least), as_bf2(floor));
             }
             float mx[NT][2];
-            bool more = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -660,10 +702,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     for (int ub = 1; ub < C::UB; ++ub)
                         mx[nt][c] = fmaxf(mx[nt][c], fmaxf(s[ub][nt][c], s[ub][nt][c + 2]));
                     mx[nt][c] *= factor[nt][c];
-                    more = more || mx[nt][c] > ref[nt][c] || vtop[nt][c] * inv[nt][c] > 16384.f;
+                    more = more || mx[nt][c] > ref[nt][c];
+                    if constexpr (edge)
+                        more = more || vtop[nt][c] * inv[nt][c] > 16384.f || step_of(lowest) * (inv[nt][c] * deepest) < kLeast;
                 }
             if (__any_sync(0xffffffffu, more)) {
-                if constexpr (!edge) {  // the lanes of a row hold some of the unit's tokens only
+                if constexpr (!edge) {
 #pragma unroll
                     for (int o = 1; o < 4; o <<= 1) vtop[0][0] = fmaxf(vtop[0][0], __shfl_xor_sync(0xffffffffu, vtop[0][0], o));
 #pragma unroll
@@ -703,7 +747,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
                         for (int x = 0; x < 8; ++x) acc[nt][w][x >> 2][x & 3] *= alpha[x & 1];
                 }
+                range = range_of(inv[0][0]);
+                if constexpr (edge) {
+                    float low = step_of(lowest);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+                    lowest = pair_of_step(low);
+                    for (; deepest < kLastBand; deepest *= kBand) {
+                        bool below = false;
+#pragma unroll
+                        for (int x = 0; x < 2 * NT; ++x) below = below || low * (inv[x >> 1][x & 1] * deepest) < kLeast;
+                        if (!__any_sync(0xffffffffu, below)) break;
+                    }
+                } else if (__any_sync(0xffffffffu, kv4_scale(least).x * inv[0][0] < kLeast)) {  // or steps of 0
+                    float low = step_of(lowest);
+                    for (int x = lane; x < C::UB * 16 * C::kGroups; x += 32) {
+                        uint32_t pair[1];
+                        lds(unit + x / (16 * C::kGroups) * C::kBlock + C::kValueScales + x % (16 * C::kGroups) * 4, pair);
+                        low = fminf(low, step_of(pair[0]));
+                    }
+                    lowest = least = pair_of_step(low);
+                    if (__any_sync(0xffffffffu, low * inv[0][0] < kLeast)) return true;
+                }
             }
+            if constexpr (!edge) lowest = least;
 
             // ---- P, and O^T += V^T P^T
 #pragma unroll
@@ -721,61 +788,89 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     for (int c = 0; c < 4; ++c) s[ub][nt][c] *= inv[nt][c & 1];
                 }
             }
+            float boost = 1.f;  // of the band
+            for (;;) {
 #pragma unroll
-            for (int ub = 0; ub < C::UB; ++ub) {
-                const uint32_t blk = unit + ub * C::kBlock + C::kValueCodes + g4 * (C::kWords * 2);
-                uint32_t va[C::kGroups], vb[C::kGroups];
-                value_scales(ub, va, vb);
-                uint32_t b0[C::kGroups][NT], b1[C::kGroups][NT];
+                for (int ub = 0; ub < C::UB; ++ub) {
+                    const uint32_t blk = unit + ub * C::kBlock + C::kValueCodes + g4 * (C::kWords * 2);
+                    uint32_t va[C::kGroups], vb[C::kGroups];
+                    value_scales(ub, va, vb);
+                    uint32_t b0[C::kGroups][NT], b1[C::kGroups][NT];
 #pragma unroll
-                for (int g = 0; g < C::kGroups; ++g) {
-                    const float2 wa = kv4_scale(va[g]), wb = kv4_scale(vb[g]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float* q = s[ub][nt];
-                        float w0 = q[0] * wa.x, w1 = q[1] * wa.x, w2 = q[2] * wb.x, w3 = q[3] * wb.x;
-                        if constexpr (!edge) {
-                            om[nt][g][0] = fmaf(q[0], wa.y, fmaf(q[2], wb.y, om[nt][g][0]));
-                            om[nt][g][1] = fmaf(q[1], wa.y, fmaf(q[3], wb.y, om[nt][g][1]));
-                        } else {
-                            // a token hidden from a row adds nothing to it, whatever its scales hold
-                            const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
-                            if (ta >= seen[nt][0]) w0 = 0.f;
-                            else om[nt][g][0] = fmaf(q[0], wa.y, om[nt][g][0]);
-                            if (ta >= seen[nt][1]) w1 = 0.f;
-                            else om[nt][g][1] = fmaf(q[1], wa.y, om[nt][g][1]);
-                            if (tb >= seen[nt][0]) w2 = 0.f;
-                            else om[nt][g][0] = fmaf(q[2], wb.y, om[nt][g][0]);
-                            if (tb >= seen[nt][1]) w3 = 0.f;
-                            else om[nt][g][1] = fmaf(q[3], wb.y, om[nt][g][1]);
-                        }
-                        b0[g][nt] = transpose8(pack_f16(w0, w1));
-                        b1[g][nt] = transpose8(pack_f16(w2, w3));
-                    }
-                }
-                uint32_t x0[C::kWords / 2], x1[C::kWords / 2], x2[C::kWords / 2], x3[C::kWords / 2];
-                lds(blk + token_of(2 * j) * C::kRow, x0);
-                lds(blk + token_of(2 * j + 1) * C::kRow, x1);
-                lds(blk + (8 + token_of(2 * j)) * C::kRow, x2);
-                lds(blk + (8 + token_of(2 * j + 1)) * C::kRow, x3);
-#pragma unroll
-                for (int g = 0; g < C::kGroups; ++g) {
-#pragma unroll
-                    for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
-                        const uint32_t sel = w & 1 ? 0x7632u : 0x5410u;
-                        const uint32_t z0 = __byte_perm(x0[w / 2], x1[w / 2], sel);
-                        const uint32_t z1 = __byte_perm(x2[w / 2], x3[w / 2], sel);
-                        const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        const float2 wa = kv4_scale(va[g]), wb = kv4_scale(vb[g]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(acc[nt][w][0], z0 & 0x000f000fu, z0 & 0x00f000f0u, z1 & 0x000f000fu,
-                                    z1 & 0x00f000f0u, b0[g][nt], b1[g][nt]);
-                            mma_f16(acc[nt][w][1], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu,
-                                    y1 & 0x00f000f0u, b0[g][nt], b1[g][nt]);
+                            const float* q = s[ub][nt];
+                            float w0 = q[0] * wa.x, w1 = q[1] * wa.x, w2 = q[2] * wb.x, w3 = q[3] * wb.x;
+                            if constexpr (!edge) {
+                                om[nt][g][0] = fmaf(q[0], wa.y, fmaf(q[2], wb.y, om[nt][g][0]));
+                                om[nt][g][1] = fmaf(q[1], wa.y, fmaf(q[3], wb.y, om[nt][g][1]));
+                            } else {
+                                // a token hidden from a row adds nothing to it, whatever its scales hold
+                                const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
+                                const auto add = [&](float& w, float q, float2 x, int at, int c) {
+                                    const bool sees = at < seen[nt][c];
+                                    w = sees ? q * x.x : 0.f;
+                                    if (sees && boost == 1.f) om[nt][g][c] = fmaf(q, x.y, om[nt][g][c]);
+                                    if (boost != deepest && w < kLeast) w = 0.f;                // a later band's
+                                    if (boost != 1.f && !(w < kLeast * kBand)) w = 0.f;  // an earlier one's
+                                };
+                                add(w0, q[0], wa, ta, 0);
+                                add(w1, q[1], wa, ta, 1);
+                                add(w2, q[2], wb, tb, 0);
+                                add(w3, q[3], wb, tb, 1);
+                            }
+                            b0[g][nt] = transpose8(pack_f16(w0, w1));
+                            b1[g][nt] = transpose8(pack_f16(w2, w3));
+                        }
+                    }
+                    uint32_t x0[C::kWords / 2], x1[C::kWords / 2], x2[C::kWords / 2], x3[C::kWords / 2];
+                    lds(blk + token_of(2 * j) * C::kRow, x0);
+                    lds(blk + token_of(2 * j + 1) * C::kRow, x1);
+                    lds(blk + (8 + token_of(2 * j)) * C::kRow, x2);
+                    lds(blk + (8 + token_of(2 * j + 1)) * C::kRow, x3);
+#pragma unroll
+                    for (int g = 0; g < C::kGroups; ++g) {
+#pragma unroll
+                        for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
+                            const uint32_t sel = w & 1 ? 0x7632u : 0x5410u;
+                            const uint32_t z0 = __byte_perm(x0[w / 2], x1[w / 2], sel);
+                            const uint32_t z1 = __byte_perm(x2[w / 2], x3[w / 2], sel);
+                            const uint32_t y0 = z0 >> 8, y1 = z1 >> 8;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_f16(acc[nt][w][0], z0 & 0x000f000fu, z0 & 0x00f000f0u, z1 & 0x000f000fu,
+                                        z1 & 0x00f000f0u, b0[g][nt], b1[g][nt]);
+                                mma_f16(acc[nt][w][1], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu,
+                                        y1 & 0x00f000f0u, b0[g][nt], b1[g][nt]);
+                            }
                         }
                     }
                 }
+                if (!edge || boost == deepest) break;
+                boost *= kBand;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int w = 0; w < C::kWords; ++w)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) acc[nt][w][x >> 2][x & 3] *= kBand;
+#pragma unroll
+                    for (int ub = 0; ub < C::UB; ++ub)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[ub][nt][c] *= kBand;
+                }
             }
+            if (edge && boost != 1.f) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int w = 0; w < C::kWords; ++w)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) acc[nt][w][x >> 2][x & 3] *= 1.f / boost;
+            }
+            return false;
         };
         for (int u = seg.u0; u < seg.u1; ++u) {
             copy_wait<kStages - 1>();
@@ -783,8 +878,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             const uint32_t unit = ring + stage * C::kUnitBytes;
             const uint32_t valid = masks >> (8 * stage) & 0xffu;
             const int t0 = u * C::kTokens;
-            if (t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1) use(std::true_type{}, unit, valid, t0);
-            else use(std::false_type{}, unit, valid, t0);
+            if (t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1 || deepest != 1.f ||
+                use(std::false_type{}, unit, valid, t0))
+                use(std::true_type{}, unit, valid, t0);
             __syncwarp();  // every lane has read the stage
             if (u + kStages < seg.u1) masks = (masks & ~(0xffu << (8 * stage))) | issue(stage) << (8 * stage);
             copy_commit();

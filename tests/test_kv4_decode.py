@@ -367,6 +367,79 @@ def test_values_near_the_largest_bf16_numbers_stay_finite(lengths, heads, each, 
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", FORMATS)
+@pytest.mark.parametrize("lengths,heads,each,tq", SHAPES)
+@pytest.mark.parametrize("apart", [20, 30, 100])
+def test_groups_whose_scales_lie_far_apart(lengths, heads, each, tq, dim, group, apart):
+    # one group's values 2^20 to 2^100 times the others'; D = G = 64 has one group: its heads instead
+    c = ref.Batch(lengths, heads, dim, group, 64, seed=22)
+    factor = torch.ones(heads, 1, 1, dim // group, dtype=torch.float64)
+    factor[(slice(None), 0, 0, 0) if dim > group else (0,)] = 2.0 ** apart
+    rescaled(c, 3, factor * 2.0 ** (-apart // 2))
+    run(c, heads * each, tq)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("lengths,heads,each,tq", SHAPES)
+@pytest.mark.parametrize("apart", [20, 30])
+def test_a_huge_value_of_little_weight_hides_no_other(lengths, heads, each, tq, dim, group, apart):
+    # the token that weighs least holds values 2^20 or 2^30 times the others'
+    c = ref.Batch(lengths, heads, dim, group, 64, seed=23)
+    pool, table, held = c.on()
+    q = c.queries(heads * each, tq, 3.0)
+    factor = torch.ones(*c.pool.shape[:3], 16, dim // group, dtype=torch.float64)
+    for b, n in enumerate(lengths):
+        if n < 2 * tq:
+            continue
+        p = ref.attend(q[b].double().numpy(), c.loaded(b), dim ** -0.5, True)[2]
+        for h, t in enumerate(p[:, :n - tq].argmin(-1)):
+            page, block, r = place(c, b, t)
+            factor[page, h, block, r] = 2.0 ** apart
+    rescaled(c, 3, factor)
+    pool = torch.from_numpy(c.pool).cuda()
+    o, lse = fa.attention_decode_kv4(q.cuda(), pool, table, held)
+    assert fa.fa_get_device_status() == 0
+    check(c, q, o, lse, dim ** -0.5, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", FORMATS)
+@pytest.mark.parametrize("first", [0, 320, 640])
+@pytest.mark.parametrize("apart", [30, 50])
+def test_a_stretch_of_huge_values_of_little_weight(apart, first, dim, group):
+    # 128 tokens whose scores are 0, far below the others' largest, with values 2^30 or 2^50 times the others'
+    c = ref.Batch([768, 700], 2, dim, group, 64, seed=29)
+    keys, values = (torch.ones(*c.pool.shape[:3], 16, dim // group, dtype=torch.float64) for _ in range(2))
+    for b in range(2):
+        for t in range(first, min(first + 128, c.lengths[b])):
+            page, block, r = place(c, b, t)
+            keys[page, :, block, r], values[page, :, block, r] = 0.0, 2.0 ** apart
+    rescaled(c, 1, keys)
+    rescaled(c, 3, values)
+    q = c.queries(8, 1, 6.0)
+    pool, table, held = c.on()
+    o, lse = fa.attention_decode_kv4(q.cuda(), pool, table, held)
+    assert fa.fa_get_device_status() == 0
+    check(c, q, o, lse, dim ** -0.5, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", [(128, 64), (128, 32), (64, 64)])
+@pytest.mark.parametrize("first", [0, 300, 699])
+def test_a_huge_scale_whose_codes_are_zero_adds_nothing(dim, group, first):
+    # all minima 0; one token's scale is 2^24 times the others', its codes 0: what is left is the others' sum
+    c = ref.Batch([700], 2, dim, group, 64, seed=24)
+    page, block, r = place(c, 0, first)
+    factor = torch.ones(*c.pool.shape[:3], 16, dim // group, dtype=torch.float64)
+    factor[page, :, block, r] = 2.0 ** 24
+    rescaled(c, 3, factor, minima=0.0)
+    at, size = ref.sections(dim, group)[2]
+    c.pool[page, :, block, at + r * size:at + (r + 1) * size] = 0
+    run(c, 8, 1)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("apart", [30, 118, -118])
 @pytest.mark.parametrize("each,tq", [(1, 2), (4, 4), (2, 8)])
 @pytest.mark.parametrize("length", [9, 33, 700, 5000])
