@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "fa_internal.h"
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         uint32_t qf[NT][C::kWords][4];
         uint32_t qs[NT][(C::kGroups + 1) / 2];
         float factor[NT][2];
+        uint32_t far = 0;  // rows whose scores take a further factor of 2^40: bit 4 row + tile
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
@@ -461,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             // 2^e <= top < 2^(e+1) goes to 2^14 (rows below 2^-113, to less)
             const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
             const int up_e = min(14 - e, 127);
-            const float2 down = pow2_parts(24 - up_e);
             const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((up_e + 127) << 23), p.sl2);
             float group[C::kGroups];
 #pragma unroll
@@ -483,7 +484,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 qf[nt][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
             }
             // a positive factor: its sign went into q, and a scale of 0 made q zero
-            const float back = !finite ? NAN : p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * down.x * down.y;
+            float2 down = pow2_parts(24 - up_e);
+            float back = !finite ? NAN : p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * down.x * down.y;
+            const bool big = back > 0x1p100f;  // the factor alone might overflow where the score does not
+            if (big) {
+                down = pow2_parts(24 - 40 - up_e);
+                back = fminf(fabsf(p.sl2) * down.x * down.y, FLT_MAX);
+            }
+            far |= (__ballot_sync(0xffffffffu, big) & 0x11111111u) << nt;
 #pragma unroll
             for (int g = 0; g < C::kGroups; ++g) {
                 float s = group[g];
@@ -514,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         // least scale's.  Rows differ in the units with tokens that some do not see only.
         float inv[NT][2];
         uint32_t range = range_of(0x1p114f);  // the scales and minima that inv is for, at most
-        uint32_t lowest = 0x7f807f80u;           // the least step but 0 so far of this lane's share of them, in the low half
+        uint32_t lowest = 0x7f807f80u;        // the least step but 0 so far of this lane's share of them, in the low half
         float deepest = 1.f;  // the last band's factor; units take all bands from the first that needs another on
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -530,8 +538,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
         }
 
         // One unit in the ring at `unit`.  some_hidden: a token of it is not there or not
-        // seen by every row, or its scales take more than one band; the other units have none
-        // of those tests, and return true, with nothing added, where the scales do.
+        // seen by every row, its scales take several bands or a row a further factor.  The
+        // other units have none of those tests, and return true, with nothing added, where
+        // the scales take several bands.
         auto use = [&](auto some_hidden, uint32_t unit, uint32_t valid, int t0) -> bool {
             constexpr bool edge = decltype(some_hidden)::value;
             int seen[NT][2];  // tokens that a row sees
@@ -592,6 +601,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                         for (int c = 0; c < 4; ++c) s[ub][nt][c] = fmaf(c < 2 ? sa : sb, d[nt][c], s[ub][nt][c]);
                 }
                 if constexpr (edge) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (far >> (8 * j + 4 * (c & 1) + nt) & 1) s[ub][nt][c] *= 0x1p40f;
                     const bool here = valid >> ub & 1;
                     const int ta = t0 + ub * 16 + tokA, tb = ta + 8;
 #pragma unroll
@@ -878,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
             const uint32_t unit = ring + stage * C::kUnitBytes;
             const uint32_t valid = masks >> (8 * stage) & 0xffu;
             const int t0 = u * C::kTokens;
-            if (t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1 || deepest != 1.f ||
+            if (t0 + C::kTokens > all_see || valid != (1u << C::UB) - 1 || deepest != 1.f || far != 0 ||
                 use(std::false_type{}, unit, valid, t0))
                 use(std::true_type{}, unit, valid, t0);
             __syncwarp();  // every lane has read the stage

@@ -453,3 +453,19 @@ def test_a_token_that_a_row_does_not_see_does_not_touch_it(length, each, tq, apa
     rescaled(c, 3, factor)
     got = run(c, 2 * each, tq)
     assert torch.isfinite(got[0]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", FORMATS)
+@pytest.mark.parametrize("each,tq", [(4, 1), (4, 4)])
+def test_finite_queries_of_any_size_give_finite_scores(dim, group, each, tq):
+    # queries up to 2^124 over keys of 2^-120 (flat groups: a step of 0), and ordinary queries beside them
+    c = ref.Batch([300, 40], 2, dim, group, 64, seed=26)
+    rescaled(c, 1, 2.0 ** -120, steps=0.0)
+    q = c.queries(2 * each, tq)
+    q[:, ::2] *= 2.0 ** 122
+    pool, table, held = c.on()
+    w = torch.zeros(2, 2, c.table.shape[1] * 64, device="cuda")
+    o, lse, w = fa.attention_decode_kv4(q.cuda(), pool, table, held, weights_out=w)
+    assert fa.fa_get_device_status() == 0
+    check(c, q, o, lse, dim ** -0.5, True, w)
