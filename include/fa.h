@@ -346,7 +346,8 @@ int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k,
  * fp16's 11 bits; a query's elements are exact down to 2^-28 of their row's largest,
  * what is smaller loses bits.  Within what a row sees, values whose s lies below 2^-106
  * of the largest s may count as their minimum.
- * A non-finite query row gives NaN in its o and lse.
+ * A non-finite query row that sees a token gives NaN in its o and lse, and in the
+ * accounts of the tokens that it sees.
  */
 long long fa_kv4_decode_workspace(int B, int Hq, int Hkv, int Tq, int D, int slots, int weights);
 int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse, int Hq, int Tq, float scale,

@@ -459,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) most = __hmax2_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
             const float top = fmaxf(__low2float(most), __high2float(most));
-            const bool finite = __low2float(most) < INFINITY && __high2float(most) < INFINITY;
             // 2^e <= top < 2^(e+1) goes to 2^14 (rows below 2^-113, to less)
             const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
             const int up_e = min(14 - e, 127);
@@ -483,9 +482,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                 qf[nt][w][2] = pack_f16(x[2], x[6]);
                 qf[nt][w][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
             }
-            // a positive factor: its sign went into q, and a scale of 0 made q zero
+            // A positive factor: its sign went into q, and a scale of 0 made q zero.  (A row that is
+            // not finite has a NaN among the pieces of its sums below, so that all of its scores
+            // are, but for the tokens that it does not see.)
             float2 down = pow2_parts(24 - up_e);
-            float back = !finite ? NAN : p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * down.x * down.y;
+            float back = p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * down.x * down.y;
             const bool big = back > 0x1p100f;  // the factor alone might overflow where the score does not
             if (big) {
                 down = pow2_parts(24 - 40 - up_e);

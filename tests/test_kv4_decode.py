@@ -469,3 +469,21 @@ def test_finite_queries_of_any_size_give_finite_scores(dim, group, each, tq):
     o, lse, w = fa.attention_decode_kv4(q.cuda(), pool, table, held, weights_out=w)
     assert fa.fa_get_device_status() == 0
     check(c, q, o, lse, dim ** -0.5, True, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("each", [2, 4])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_query_of_a_row_that_sees_nothing(bad, each):
+    # two tokens, four queries: the first two rows see nothing, whatever they hold; a bad row spoils the
+    # accounts of the tokens that it sees and of no other
+    c = ref.Batch([2, 40], 2, 64, 32, 16, seed=27)
+    q = c.queries(2 * each, 4)
+    q[0, 0, :2, 3], q[1, 0, 1, 3] = bad, bad
+    pool, table, held = c.on()
+    o, lse, w = fa.attention_decode_kv4(q.cuda(), pool, table, held, weights_out=torch.zeros(2, 2, 48, device="cuda"))
+    assert fa.fa_get_device_status() == 0
+    assert not o[0, :, :2].any() and torch.isneginf(lse[0, :, :2]).all()
+    assert torch.isfinite(o[0]).all() and torch.isfinite(w[0]).all() and torch.isfinite(lse[0, :, 2:]).all()
+    assert torch.isnan(o[1, 0, 1]).all() and torch.isnan(lse[1, 0, 1])
+    assert torch.isnan(w[1, 0, :38]).all() and torch.isfinite(w[1, 0, 38:]).all() and torch.isfinite(w[1, 1]).all()
