@@ -487,3 +487,26 @@ def test_a_bad_query_of_a_row_that_sees_nothing(bad, each):
     assert torch.isfinite(o[0]).all() and torch.isfinite(w[0]).all() and torch.isfinite(lse[0, :, 2:]).all()
     assert torch.isnan(o[1, 0, 1]).all() and torch.isnan(lse[1, 0, 1])
     assert torch.isnan(w[1, 0, :38]).all() and torch.isfinite(w[1, 0, 38:]).all() and torch.isfinite(w[1, 1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("lengths,each", [([2500, 20], 2), ([2500, 20], 12), ([100, 20], 2), ([9000] * 3 + [5] * 40, 3)])
+def test_a_workspace_of_exactly_the_size_asked_for(lengths, each, weights):
+    c = ref.Batch(lengths, 2, 128, 64, 64, seed=28)
+    pool, table, held = c.on()
+    q = c.queries(2 * each, 1).cuda()
+    slots = c.table.shape[1] * 64
+    account = lambda: torch.full((len(lengths), 2, slots), 3.0, device="cuda") if weights else None  # noqa: E731
+    want = fa.attention_decode_kv4(q, pool, table, held, weights_out=account())
+    from online_softmax_05_gb300.kv4 import _cache
+    lib, o, lse, w = fa.load_library(), torch.empty_like(q), torch.empty(q.shape[:3], device="cuda"), account()
+    need = lib.fa_kv4_decode_workspace(len(lengths), 2 * each, 2, 1, 128, slots, int(weights))
+    ws = torch.full((need + 4096,), 0xa5, dtype=torch.uint8, device="cuda")
+    rc = lib.fa_kv4_decode(_cache(pool, table, held)[0], q.data_ptr(), o.data_ptr(), lse.data_ptr(), 2 * each, 1,
+                           128 ** -0.5, 1, None, w.data_ptr() if weights else None, slots if weights else 0,
+                           ws.data_ptr() if need else None, need, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and fa.fa_get_device_status() == 0
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and (not weights or torch.equal(w, want[2]))
+    assert (ws[need:] == 0xa5).all()
