@@ -361,7 +361,12 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(ReadParams p) {
     constexpr int kOct = D / 8, kRows = 256 / kOct;
     const int oct = threadIdx.x % kOct, g = oct >> 2, j = oct & 3;
     const int bh = blockIdx.y, b = bh / p.pages.heads, h = bh - b * p.pages.heads;
-    const int len = p.lengths[b], start = p.start != nullptr ? p.start[b] : 0;
+    const int start = p.start != nullptr ? p.start[b] : 0;
+    int len = p.lengths[b];
+    if (len < 0 || len > p.pages.capacity() || start < 0) {  // the sequence counts as empty
+        report(kStatusBadSeqlen);
+        len = 0;
+    }
     const int i0 = blockIdx.x * (kRows * kTokensThread) + threadIdx.x / kOct;
     const unsigned char* block[kTokensThread];
     uint32_t kw[kTokensThread], vw[kTokensThread], ks[kTokensThread], vs[kTokensThread];
@@ -370,13 +375,9 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(ReadParams p) {
         const long long slot = static_cast<long long>(start) + i0 + x * kRows;
         block[x] = nullptr;
         if (i0 + x * kRows < p.count && slot < len) {
-            if (slot < 0 || slot >= p.pages.capacity()) {
-                report(kStatusBadSeqlen);
-            } else {
-                const long long at = p.pages.block_of(b, static_cast<int>(slot >> 4));
-                if (at < 0) report(kStatusBadPage);
-                else block[x] = p.pages.pool + at + h * p.pages.head_bytes();
-            }
+            const long long at = p.pages.block_of(b, static_cast<int>(slot >> 4));
+            if (at < 0) report(kStatusBadPage);
+            else block[x] = p.pages.pool + at + h * p.pages.head_bytes();
         }
     }
 #pragma unroll

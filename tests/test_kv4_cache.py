@@ -425,3 +425,22 @@ def test_pages_behind_the_first_four_gigabytes():
     torch.cuda.synchronize()
     assert fa.fa_get_device_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("start", [None, [0, 0], [-3, 10]])
+@pytest.mark.parametrize("bad", [49, -1, 20])
+def test_reading_a_sequence_that_cannot_be_counts_it_as_empty(bad, start):
+    # a length the table of 48 slots cannot hold, a negative one, a negative start: zeros, and a status
+    c = ref.Batch([20, 40], 2, 64, 64, 16, seed=30)
+    pool, table, held = c.on()
+    if bad == 20 and (start is None or start[0] >= 0):
+        return
+    want = fa.kv4_read(pool, table, held)
+    lengths = torch.tensor([bad, 40], dtype=torch.int32).cuda()
+    first = None if start is None else torch.tensor(start, dtype=torch.int32).cuda()
+    for x, y in zip(fa.kv4_read(pool, table, lengths, start=first, count=None if start is None else 30), want):
+        assert not x[0].any()
+        assert torch.equal(x[1], y[1] if start is None else y[1, :, start[1]:start[1] + 30])
+    assert fa.fa_get_device_status() == -11
+    assert fa.fa_get_device_status() == 0
