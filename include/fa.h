@@ -307,7 +307,7 @@ typedef struct fa_kv4_cache {
  *   weights   out: float32 [B][Hkv][slots] or NULL: 0 at the new slots
  *   slot_positions out: int32 [B][Hkv][slots] or NULL: the new slots' positions
  * A sequence without room for its tokens in the table (or in `slots`), or whose
- * length is below n, is recorded as FA_ERR_SEQLEN; those tokens are not stored.
+ * length is below n, is recorded as FA_ERR_SEQLEN; none of its tokens is stored.
  */
 int fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, long long k_t, long long k_h,
                   long long v_t, long long v_h, const int* cu_new, int total, const void* positions,

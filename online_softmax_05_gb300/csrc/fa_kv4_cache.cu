@@ -188,13 +188,15 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
     unsigned char* block = nullptr;
     if (live) {
         const int begin = p.cu_new[b], n = p.cu_new[b + 1] - begin;
-        slot = static_cast<long long>(p.lengths[b]) - n + (t - begin);
+        const long long len = p.lengths[b];
+        slot = len - n + (t - begin);
         if (p.positions != nullptr)
             pos = p.pos64 ? static_cast<const long long*>(p.positions)[t]
                           : static_cast<long long>(static_cast<const int*>(p.positions)[t]);
         else
             pos = slot;
-        if (slot < 0 || slot >= p.pages.capacity() || (p.slots != 0 && slot >= p.slots)) {
+        // a sequence without room for all of its tokens stores none
+        if (len < n || len > p.pages.capacity() || (p.slots != 0 && len > p.slots) || slot < 0 || slot >= len) {
             report(kStatusBadSeqlen);
             live = false;
         } else {

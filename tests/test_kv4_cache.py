@@ -444,3 +444,28 @@ def test_reading_a_sequence_that_cannot_be_counts_it_as_empty(bad, start):
         assert torch.equal(x[1], y[1] if start is None else y[1, :, start[1]:start[1] + 30])
     assert fa.fa_get_device_status() == -11
     assert fa.fa_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length,slots", [(2, None), (-1, None), (50, None), (2 ** 31 - 1, None), (32, 30)])
+def test_a_sequence_without_room_for_its_tokens_stores_none(length, slots):
+    # fewer tokens than new ones, more than the table's 48 slots or than the accounts', by less than
+    # the new tokens: the pool and the accounts stay as they are, the other sequence's tokens are stored
+    c = ref.Batch([20, 29], 2, 64, 64, 16, seed=31, spare=1)
+    c.table[0] = c.table[0][0], c.table[1][0], c.pool.shape[0] - 1       # three pages for each sequence
+    c.table[1] = [x for x in range(c.pool.shape[0]) if x not in c.table[0].tolist()][:3]
+    pool, table, _ = c.on()
+    before = pool.clone()
+    k = torch.randn(8, 2, 64, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 4, 8], dtype=torch.int32).cuda()
+    alone = torch.tensor([4, 4, 8], dtype=torch.int32).cuda()             # the second sequence's tokens only
+    new = lambda: (torch.full((2, 2, slots or 48), 7.0, device="cuda"),   # noqa: E731
+                   torch.full((2, 2, slots or 48), -5, dtype=torch.int32, device="cuda"))
+    held = torch.tensor([length, 29], dtype=torch.int32).cuda()
+    want, accounts = new(), new()
+    fa.kv4_append(pool, k, k, table, held, cu, weights=accounts[0], slot_positions=accounts[1])
+    assert fa.fa_get_device_status() == -11
+    fa.kv4_append(before, k, k, table, held, alone, weights=want[0], slot_positions=want[1])
+    assert fa.fa_get_device_status() == 0
+    assert torch.equal(pool, before) and torch.equal(accounts[0], want[0]) and torch.equal(accounts[1], want[1])
+    assert (want[0][1, :, 25:29] == 0).all()
