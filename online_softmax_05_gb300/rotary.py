@@ -104,7 +104,7 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
     if len(shape) != 4 or code is None or dev < 0:
         raise ValueError("rope takes (B, H, T, D) CUDA tensors of one type: bf16, fp16 or fp32")
     B, _, T, D = shape
-    packed, results, heads = b"", (), 1
+    packed, results, count = b"", (), 0
     for i, t in enumerate(tensors):
         if i:
             shape = t.shape
@@ -116,7 +116,6 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
         if sc != 1 and D > 1:
             raise ValueError("the channels of rope's tensors must be contiguous")
         H = shape[1]
-        heads *= H
         if outs is None:
             o = torch.empty(shape, dtype=dtype, device=t.device)
             ob, oh, ot = H * T * D, T * D, D
@@ -126,11 +125,13 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
                 raise ValueError("out must match rope's input in shape, type and device, with contiguous channels")
             ob, oh, ot, _ = o.stride()
         results += (o,)
-        packed += _pack_tensor(t.data_ptr(), o.data_ptr(), H, sb, st, sh, ob, ot, oh)
+        if H:
+            packed += _pack_tensor(t.data_ptr(), o.data_ptr(), H, sb, st, sh, ob, ot, oh)
+            count += 1
     rotary = _check_table(table, D, dev)
     pos, pos64, pos_b = _positions(positions, B, T, dev)
-    if B * T * heads:
-        rc = load_library().fa_rope(packed, len(tensors), pos, pos64, pos_b, table.data_ptr(), B, T, D, rotary,
+    if B * T * count:
+        rc = load_library().fa_rope(packed, count, pos, pos64, pos_b, table.data_ptr(), B, T, D, rotary,
                                     interleaved, amplitude, inverse, code, _raw_stream(dev))
         if rc != FA_OK:
             raise FAError(rc, "fa_rope")

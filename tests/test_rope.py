@@ -289,3 +289,23 @@ def test_streams_and_graph():
     torch.cuda.synchronize()
     want = fa.rope(q.flip(2), k.flip(2), table)
     assert torch.equal(cap[0], want[0]) and torch.equal(cap[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("empty", [0, 1])
+def test_a_tensor_without_heads_leaves_the_other(empty):
+    q, k = fused(2, 9, 3, 2, 64, torch.bfloat16, 12)
+    table = fa.rotary_frequencies(64, device="cuda")
+    x = [t.detach().contiguous() for t in (q, k)]
+    x[empty] = x[empty][:, :0]
+    full = x[1 - empty]
+    want = fa.rope(full, None, table)
+    torch.full((4, *full.shape), 9.0, dtype=full.dtype, device="cuda")      # what a result not written would hold
+    got = fa.rope(*x, table)
+    assert got[empty].shape == x[empty].shape and torch.equal(got[1 - empty], want)
+    leaves = [t.requires_grad_() for t in x]
+    out = fa.rope(*leaves, table)
+    torch.full((4, *full.shape), 9.0, dtype=full.dtype, device="cuda")
+    grads = torch.autograd.grad(out, leaves, [torch.ones_like(t) for t in out])
+    assert grads[empty].shape == x[empty].shape
+    assert torch.equal(grads[1 - empty], fa.rope(torch.ones_like(want), None, table, inverse=True))
