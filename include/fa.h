@@ -245,7 +245,8 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
  *                  sine, products and sums are float32, each rounded to nearest,
  *                  the result rounded to the type
  * FA_ERR_UNSUPPORTED for rotary or dtype, FA_ERR_ARG for overlaps, negative
- * strides or an output whose rows share elements.  No workspace.
+ * strides or an output whose rows may share elements (by rising stride, each of
+ * its dimensions must step over all that those before it span).  No workspace.
  */
 #define FA_BF16 0
 #define FA_FP16 1

@@ -4,6 +4,8 @@
 // nothing and needs no GPU.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <array>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -294,6 +296,30 @@ int fa_get_device_status(void* stream) {
     return a != 0 ? a : b != 0 ? b : c != 0 ? c : d;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Whether rows of D elements lie apart: by rising stride, each dimension's step clears what
+// the dimensions within it span.
+struct Dim {
+    long long size, stride;
+};
+bool rows_apart(std::array<Dim, 3> dims, int D) {
+    std::sort(dims.begin(), dims.end(), [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    long long span = D;
+    for (const Dim& d : dims) {
+        if (d.size == 1) continue;
+        if (d.stride < span || d.stride > (LLONG_MAX - span) / (d.size - 1)) return false;
+        span += (d.size - 1) * d.stride;
+    }
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
 int fa_rope(const fa_rope_tensor* tensors, int n_tensors, const void* positions, int positions_64, long long positions_b,
             const void* freq, int B, int T, int D, int rotary, int interleaved, float amplitude, int inverse, int dtype,
             void* stream) {
@@ -320,7 +346,7 @@ int fa_rope(const fa_rope_tensor* tensors, int n_tensors, const void* positions,
         if ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & (size - 1)) return FA_ERR_ALIGN;
         if (t.in_b < 0 || t.in_t < 0 || t.in_h < 0 || t.out_b < 0 || t.out_t < 0 || t.out_h < 0) return FA_ERR_ARG;
         // an output element is written once: no two rows of it may share one
-        if ((B > 1 && t.out_b < D) || (T > 1 && t.out_t < D) || (t.heads > 1 && t.out_h < D)) return FA_ERR_ARG;
+        if (!rows_apart({{{B, t.out_b}, {T, t.out_t}, {t.heads, t.out_h}}}, D)) return FA_ERR_ARG;
         in[i] = range_of(t.in, ((B - 1) * static_cast<size_t>(t.in_b) + (T - 1) * static_cast<size_t>(t.in_t) +
                                 (t.heads - 1) * static_cast<size_t>(t.in_h) + D) * size);
         out[i] = range_of(t.out, ((B - 1) * static_cast<size_t>(t.out_b) + (T - 1) * static_cast<size_t>(t.out_t) +

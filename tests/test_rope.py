@@ -309,3 +309,28 @@ def test_a_tensor_without_heads_leaves_the_other(empty):
     grads = torch.autograd.grad(out, leaves, [torch.ones_like(t) for t in out])
     assert grads[empty].shape == x[empty].shape
     assert torch.equal(grads[1 - empty], fa.rope(torch.ones_like(want), None, table, inverse=True))
+
+
+def test_outputs_whose_rows_share_elements_are_refused():
+    # each stride covers a row by itself, but batch 1 lies on rows 1 .. of batch 0, or rows on heads
+    assert c_rope(tensors=dict(heads=1, out_b=64, out_t=64)) == -8
+    assert c_rope(tensors=dict(out_t=64, out_h=64)) == -8
+    assert c_rope(tensors=dict(out_t=64, out_h=960)) == -8          # the last row on the next head's first
+    assert c_rope(tensors=dict(out_b=3072, out_t=64, out_h=1024)) == -8
+    assert c_rope(tensors=dict(out_t=256, out_h=64, out_b=16 * 256 - 1)) == -8
+    assert c_rope(tensors=dict(inp=BASE, out=BASE, in_t=64, in_h=64, out_t=64, out_h=64)) == -8      # in place
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (0, 2, 1, 3), (1, 0, 2, 3), (2, 1, 0, 3)])
+def test_outputs_of_any_order_of_dimensions(order):
+    q, k = fused(2, 9, 3, 2, 64, torch.bfloat16, 13)
+    table = fa.rotary_frequencies(64, device="cuda")
+    want = fa.rope(q, k, table)
+    back = [order.index(i) for i in range(4)]
+    out = tuple(torch.zeros([t.shape[i] for i in order], dtype=t.dtype, device="cuda").permute(back) for t in (q, k))
+    got = fa.rope(q, k, table, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # dimensions of one element take any stride
+    one = torch.zeros(1, 1, 9, 64, dtype=q.dtype, device="cuda").as_strided((1, 1, 9, 64), (1, 2, 64, 1))
+    assert torch.equal(fa.rope(q[:1, :1], None, table, out=one), want[0][:1, :1])
