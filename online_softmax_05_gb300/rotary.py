@@ -11,6 +11,7 @@ __all__ = ["rope", "rotary_frequencies", "rotary_amplitude"]
 
 _DTYPES: dict = {}
 _rope_cls = None
+_forward_ad = None
 _pack_tensor = struct.Struct("9q").pack
 
 
@@ -168,10 +169,20 @@ def _make_rope_class():
     return Rope
 
 
+def _has_tangent(tensors):
+    """Whether a tensor carries a forward-mode derivative."""
+    global _forward_ad
+    if _forward_ad is None:
+        from torch.autograd import forward_ad as _forward_ad
+    if getattr(_forward_ad, "_current_level", 0) < 0:  # no forward mode at all: a microsecond saved
+        return False
+    return any(_forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def _rope_any(tensors, table, positions, interleaved, amplitude, inverse):
-    """_rope, through autograd where a tensor wants it."""
+    """_rope, through autograd where a tensor wants it (which refuses forward mode)."""
     import torch
-    if torch.is_grad_enabled() and (tensors[0].requires_grad or tensors[-1].requires_grad):
+    if (torch.is_grad_enabled() and (tensors[0].requires_grad or tensors[-1].requires_grad)) or _has_tangent(tensors):
         global _rope_cls
         if _rope_cls is None:
             cls = _make_rope_class()
@@ -195,7 +206,7 @@ def rope(q, k, table, positions=None, interleaved: bool = False, amplitude: floa
     (B, T), 0 .. T-1 if None.  ``interleaved``: pairs (2i, 2i + 1) instead of
     (i, i + R/2).  ``inverse`` turns back.  ``out``: tensors (a tuple if k is
     given) to write to, which may be the inputs; not under autograd.
-    Differentiable in q and k."""
+    Differentiable in q and k, any number of times; forward-mode derivatives raise."""
     tensors = (q,) if k is None else (q, k)
     if out is None:
         got = _launch_on(q, stream, _rope_any, tensors, table, positions, 1 if interleaved else 0, amplitude,
@@ -205,7 +216,7 @@ def rope(q, k, table, positions=None, interleaved: bool = False, amplitude: floa
         if len(outs) != len(tensors):
             raise ValueError("out must hold a tensor for each input")
         import torch
-        if torch.is_grad_enabled() and any(t.requires_grad for t in tensors + outs):
+        if torch.is_grad_enabled() and any(t.requires_grad for t in tensors + outs) or _has_tangent(tensors + outs):
             raise ValueError("out cannot be given under autograd")
         got = _launch_on(q, stream, _rope, tensors, table, positions, 1 if interleaved else 0, amplitude,
                          1 if inverse else 0, outs)

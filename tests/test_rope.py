@@ -334,3 +334,24 @@ def test_outputs_of_any_order_of_dimensions(order):
     # dimensions of one element take any stride
     one = torch.zeros(1, 1, 9, 64, dtype=q.dtype, device="cuda").as_strided((1, 1, 9, 64), (1, 2, 64, 1))
     assert torch.equal(fa.rope(q[:1, :1], None, table, out=one), want[0][:1, :1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_derivatives_raise(grad):
+    # never a result without its tangent, which would be a derivative of zero
+    import torch.autograd.forward_ad as fwd
+    q, k = (t.detach().clone() for t in fused(1, 8, 2, 1, 64, torch.bfloat16, 14))
+    v = torch.zeros_like(q)
+    table = fa.rotary_frequencies(64, device="cuda")
+    with fwd.dual_level(), torch.set_grad_enabled(grad):
+        for x in ((fwd.make_dual(q, torch.ones_like(q)), k), (q, fwd.make_dual(k, torch.ones_like(k)))):
+            with pytest.raises(RuntimeError):
+                fa.rope(*x, table)
+            with pytest.raises(ValueError):
+                fa.rope(*x, table, out=(q.clone(), k.clone()))
+        with pytest.raises(RuntimeError):
+            fa.flash_attention(fwd.make_dual(q, torch.ones_like(q)), q, v, rotary=table)
+        assert fa.rope(q, k, table)[0].shape == q.shape
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda x: fa.rope(x, k, table)[0], (q,), (torch.ones_like(q),))
