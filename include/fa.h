@@ -63,7 +63,7 @@ typedef enum fa_status {
     FA_ERR_ARCH = -9,            /* current device is not compute capability 10.3 (sm_103a) */
     FA_ERR_SCRATCH = -10,        /* fa_bwd_noalloc: problem needs more than its fixed scratch buffer */
     FA_ERR_SEQLEN = -11,         /* recorded by a kernel: a cu_seqlens length is negative or above max_seqlen,
-                                    or a cache's length or slot is outside its block table or accounts */
+                                    or a cache's length, slot or position is outside its block table or accounts */
     FA_ERR_DEBUG_CHECK = -12,    /* debug library only: a kernel's run-time index failed its bounds check */
     FA_ERR_PAGE = -13            /* recorded by a kernel: a block table names no page of the pool where a token lies */
 } fa_status;
@@ -306,7 +306,9 @@ typedef struct fa_kv4_cache {
  *   positions  in: DEVICE int32 / int64 [total], NULL: the slot
  *   freq, rotary, interleaved, amplitude: as in fa_rope; freq NULL: no rotation
  *   weights   out: float32 [B][Hkv][slots] or NULL: 0 at the new slots
- *   slot_positions out: int32 [B][Hkv][slots] or NULL: the new slots' positions
+ *   slot_positions out: int32 [B][Hkv][slots] or NULL: the new slots' positions; one
+ *                  that int32 cannot hold is recorded as FA_ERR_SEQLEN and stored as
+ *                  the nearest that it can
  * A sequence without room for its tokens in the table (or in `slots`), or whose
  * length is below n, is recorded as FA_ERR_SEQLEN; none of its tokens is stored.
  */

@@ -93,7 +93,7 @@ const char* fa_strerror(int status) {
         case FA_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out (pipeline stall); outputs are invalid";
         case FA_ERR_ARG: return "causal must be 0 or 1, scale finite, and outputs must not overlap other buffers (or another argument is out of its range)";
         case FA_ERR_ARCH: return "the current device is not compute capability 10.3 (sm_103a)";
-        case FA_ERR_SEQLEN: return "a cu_seqlens length is negative or above max_seqlen, or a cache's length or slot is outside its block table or accounts (recorded by the kernel)";
+        case FA_ERR_SEQLEN: return "a cu_seqlens length is negative or above max_seqlen, or a cache's length, slot or position is outside its block table or accounts (recorded by the kernel)";
         case FA_ERR_SCRATCH: return "fa_bwd_noalloc: the problem needs more than the fixed 64 MiB scratch buffer";
         case FA_ERR_PAGE: return "a block table names no page of the pool where a token lies (recorded by the kernel)";
         case FA_ERR_DEBUG_CHECK: return "debug library: a kernel's run-time index failed its bounds check (access skipped)";

@@ -318,7 +318,11 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(AppendParams p, int 
             if (oct == 0) {
                 const long long at = (static_cast<long long>(b) * p.pages.heads + h) * p.slots + slot;
                 if (p.weights != nullptr) p.weights[at] = 0.f;
-                if (p.slot_positions != nullptr) p.slot_positions[at] = static_cast<int>(pos);
+                if (p.slot_positions != nullptr) {
+                    const long long near = max(min(pos, static_cast<long long>(INT_MAX)), static_cast<long long>(INT_MIN));
+                    if (near != pos) report(kStatusBadSeqlen);
+                    p.slot_positions[at] = static_cast<int>(near);
+                }
             }
         }
         krow += p.k_h;

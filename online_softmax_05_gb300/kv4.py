@@ -103,7 +103,7 @@ def kv4_append(pool, k, v, block_table, lengths, cu_new, rotary=None, positions=
     rotary_frequencies) the keys are rotated first, at ``positions`` (one per
     token; the slot if None), with the same result as ``rope`` before.
     ``weights`` and ``slot_positions`` (float32 / int32 (B, kv heads, slots)), kept
-    for kv4_evict, get 0 and the position at the new slots."""
+    for kv4_evict, get 0 and the position at the new slots (positions within int32)."""
     _launch_on(pool, stream, _append, pool, k, v, block_table, lengths, cu_new, rotary, positions,
                int(bool(interleaved)), float(amplitude), weights, slot_positions)
 

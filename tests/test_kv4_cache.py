@@ -469,3 +469,23 @@ def test_a_sequence_without_room_for_its_tokens_stores_none(length, slots):
     assert fa.fa_get_device_status() == 0
     assert torch.equal(pool, before) and torch.equal(accounts[0], want[0]) and torch.equal(accounts[1], want[1])
     assert (want[0][1, :, 25:29] == 0).all()
+
+
+@pytest.mark.gpu
+def test_accounts_of_positions_beyond_32_bits_are_reported():
+    # they would come back wrapped, the newest token as the oldest; the keys' own rotation takes them
+    c = ref.Batch([6], 1, 64, 64, 16, seed=32)
+    pool, table, held = c.on()
+    k = torch.randn(6, 1, 64, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 6], dtype=torch.int32).cuda()
+    positions = torch.tensor([0, 2 ** 31 - 1, 2 ** 31, 2 ** 40, -2 ** 31, -2 ** 31 - 1], device="cuda")
+    freq = fa.rotary_frequencies(64, device="cuda")
+    p = torch.zeros(1, 1, 16, dtype=torch.int32, device="cuda")
+    fa.kv4_append(pool, k, k, table, held, cu, rotary=freq, positions=positions)
+    assert fa.fa_get_device_status() == 0
+    want = pool.clone()
+    fa.kv4_append(pool, k, k, table, held, cu, rotary=freq, positions=positions, slot_positions=p)
+    assert fa.fa_get_device_status() == -11
+    assert p[0, 0, :6].tolist() == [0] + [2 ** 31 - 1] * 3 + [-2 ** 31] * 2 and torch.equal(pool, want)
+    fa.kv4_append(pool, k, k, table, held, cu, rotary=freq, positions=positions.clamp(-2 ** 31, 2 ** 31 - 1), slot_positions=p)
+    assert fa.fa_get_device_status() == 0
