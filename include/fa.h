@@ -300,7 +300,8 @@ typedef struct fa_kv4_cache {
  * the new tokens already: sequence b's n = cu_new[b+1] - cu_new[b] tokens go to
  * slots lengths[b] - n .. lengths[b] - 1.
  *   k, v       in: packed (total, Hkv, D) bf16 with strides k_t, k_h, v_t, v_h
- *                  (elements, multiples of 8; bases 16-byte aligned)
+ *                  (elements, multiples of 8 where there is more than one token
+ *                  or head; bases 16-byte aligned)
  *   cu_new     in: DEVICE int32[B + 1], non-decreasing; rows of k and v before
  *                  cu_new[0] and from cu_new[B] on are not used (n may be 0)
  *   positions  in: DEVICE int32 / int64 [total], NULL: the slot

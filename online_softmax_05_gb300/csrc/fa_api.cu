@@ -447,7 +447,8 @@ int fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, long 
     if (freq && ((interleaved != 0 && interleaved != 1) || !std::isfinite(amplitude))) return FA_ERR_ARG;
     if (positions_64 != 0 && positions_64 != 1) return FA_ERR_ARG;
     if ((weights || slot_positions) && slots < 1) return FA_ERR_SHAPE;
-    if (!aligned16(k) || !aligned16(v) || k_t % 8 || k_h % 8 || v_t % 8 || v_h % 8 ||
+    // a dimension of one element may have any stride
+    if (!aligned16(k) || !aligned16(v) || (total > 1 && (k_t % 8 || v_t % 8)) || (cache->Hkv > 1 && (k_h % 8 || v_h % 8)) ||
         (reinterpret_cast<uintptr_t>(cu_new) & 3u) || (reinterpret_cast<uintptr_t>(freq) & 7u) ||
         (reinterpret_cast<uintptr_t>(positions) & (positions_64 ? 7u : 3u)) ||
         (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(slot_positions) & 3u))

@@ -489,3 +489,20 @@ def test_accounts_of_positions_beyond_32_bits_are_reported():
     assert p[0, 0, :6].tolist() == [0] + [2 ** 31 - 1] * 3 + [-2 ** 31] * 2 and torch.equal(pool, want)
     fa.kv4_append(pool, k, k, table, held, cu, rotary=freq, positions=positions.clamp(-2 ** 31, 2 ** 31 - 1), slot_positions=p)
     assert fa.fa_get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("total,heads,strides", [(1, 2, (133, 64, 1)), (5, 1, (64, 3, 1)), (1, 1, (7, 13, 1))])
+def test_append_takes_any_stride_of_a_single_token_or_head(total, heads, strides):
+    g = torch.Generator().manual_seed(33)
+    flat = torch.randn(2 * total * heads * 64 + 256, generator=g).to(torch.bfloat16).cuda()
+    k, v = (flat[at:].as_strided((total, heads, 64), strides) for at in (0, 128))
+    held, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([total], [0, total]))
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    pools = [fa.kv4_pool(1, heads, 64, page_size=16, group=32) for _ in range(2)]
+    freq = fa.rotary_frequencies(20, device="cuda")
+    fa.kv4_append(pools[0], k, v, table, held, cu, rotary=freq)
+    fa.kv4_append(pools[1], k.contiguous().view(-1).view(total, heads, 64).clone(), v.clone(memory_format=torch.contiguous_format),
+                  table, held, cu, rotary=freq)
+    assert fa.fa_get_device_status() == 0
+    assert pools[0].any() and torch.equal(*pools)
