@@ -136,6 +136,13 @@ def _raw_stream(device: int) -> int:
     return get(device) if get is not None else torch.cuda.current_stream(device).cuda_stream
 
 
+def _c_int(n: int, name: str) -> int:
+    """n, if a C int holds it (ctypes would cut it to 32 bits)."""
+    if not -(1 << 31) <= n < 1 << 31:
+        raise ValueError(f"{name} is out of range")
+    return n
+
+
 def _launch_on(tensor, stream, fn, *args):
     """fn(*args) with the tensor's device and the given stream (default: the device's
     current one) current, so that what fn allocates belongs to the stream that uses it."""

@@ -8,7 +8,7 @@ from __future__ import annotations
 import math
 import struct
 
-from . import FA_OK, FAError, _launch_on, _raw_stream, load_library
+from . import FA_OK, FAError, _c_int, _launch_on, _raw_stream, load_library
 from .rotary import _check_table, _positions
 
 __all__ = ["kv4_pool", "kv4_append", "kv4_read", "attention_decode_kv4", "kv4_evict"]
@@ -72,7 +72,7 @@ def _append(pool, k, v, block_table, lengths, cu_new, rotary, positions, interle
     if not (cu_new.dtype == torch.int32 and cu_new.is_contiguous() and cu_new.shape == (B + 1,)
             and cu_new.get_device() == dev):
         raise ValueError("cu_new must be a contiguous int32 (B + 1,) tensor on the pool's device")
-    total = k.shape[0]
+    total = _c_int(k.shape[0], "the number of tokens")
     table = turned = None
     if rotary is not None:
         turned = _check_table(rotary, D, dev)
@@ -114,8 +114,7 @@ def _read(pool, block_table, lengths, start, count):
     if start is not None and not (start.dtype == torch.int32 and start.shape == (B,) and start.is_contiguous()
                                   and start.get_device() == dev):
         raise ValueError("start must be a contiguous int32 (B,) tensor on the pool's device")
-    if count is None:
-        count = slots
+    count = _c_int(slots if count is None else int(count), "count")
     k = torch.empty((B, heads, count, D), dtype=torch.bfloat16, device=pool.device)
     v = torch.empty_like(k)
     rc = load_library().fa_kv4_read(packed, None if start is None else start.data_ptr(), count, k.data_ptr(),
@@ -221,5 +220,5 @@ def kv4_evict(pool, block_table, lengths, weights, slot_positions, budget: int, 
     lengths, source) to go on with: the accounts after the eviction (0 and -1 behind
     the new length), min(length, budget), and the slot each kept token came from,
     int32 (B, kv heads, budget)."""
-    return _launch_on(pool, stream, _evict, pool, block_table, lengths, weights, slot_positions, int(budget),
-                      int(recent))
+    return _launch_on(pool, stream, _evict, pool, block_table, lengths, weights, slot_positions,
+                      _c_int(int(budget), "budget"), _c_int(int(recent), "recent"))

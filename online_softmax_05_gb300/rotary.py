@@ -5,7 +5,7 @@ from __future__ import annotations
 import math
 import struct
 
-from . import FA_OK, FAError, _launch_on, _lock, _raw_stream, load_library
+from . import FA_OK, FAError, _c_int, _launch_on, _lock, _raw_stream, load_library
 
 __all__ = ["rope", "rotary_frequencies", "rotary_amplitude"]
 
@@ -105,6 +105,7 @@ def _rope(tensors, table, positions, interleaved, amplitude, inverse, outs):
     if len(shape) != 4 or code is None or dev < 0:
         raise ValueError("rope takes (B, H, T, D) CUDA tensors of one type: bf16, fp16 or fp32")
     B, _, T, D = shape
+    _c_int(B * T, "the number of rows of a head")
     packed, results, count = b"", (), 0
     for i, t in enumerate(tensors):
         if i:

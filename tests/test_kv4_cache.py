@@ -506,3 +506,18 @@ def test_append_takes_any_stride_of_a_single_token_or_head(total, heads, strides
                   table, held, cu, rotary=freq)
     assert fa.fa_get_device_status() == 0
     assert pools[0].any() and torch.equal(*pools)
+
+
+@pytest.mark.gpu
+def test_numbers_beyond_32_bits_are_refused():
+    # a C int would hold their low 32 bits: recent = 2^32 would protect nothing
+    pool = fa.kv4_pool(4, 1, 64, page_size=16, group=32)
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    held, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([60], [0, 1]))
+    w, p = torch.rand(1, 1, 64, device="cuda"), torch.arange(64, dtype=torch.int32, device="cuda")[None, None]
+    k = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda").expand(2 ** 32 + 1, 1, 64)
+    for bad in (lambda: fa.kv4_evict(pool, table, held, w, p, 8, 2 ** 32), lambda: fa.kv4_evict(pool, table, held, w, p, 2 ** 32 + 8),
+                lambda: fa.kv4_evict(pool, table, held, w, p, 8, -2 ** 32), lambda: fa.kv4_read(pool, table, held, count=2 ** 32 + 8),
+                lambda: fa.kv4_append(pool, k, k, table, held, cu)):
+        with pytest.raises(ValueError):
+            bad()

@@ -355,3 +355,12 @@ def test_forward_mode_derivatives_raise(grad):
         assert fa.rope(q, k, table)[0].shape == q.shape
     with pytest.raises(RuntimeError):
         torch.func.jvp(lambda x: fa.rope(x, k, table)[0], (q,), (torch.ones_like(q),))
+
+
+@pytest.mark.gpu
+def test_more_rows_than_32_bits_count_are_refused():
+    q = torch.zeros(1, 1, 1, 2, dtype=torch.bfloat16, device="cuda")
+    table = fa.rotary_frequencies(2, device="cuda")
+    for shape in ((1, 1, 2 ** 32 + 1, 2), (2 ** 16, 1, 2 ** 16, 2)):
+        with pytest.raises(ValueError):
+            fa.rope(q.expand(shape), None, table)
