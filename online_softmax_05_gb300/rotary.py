@@ -221,4 +221,7 @@ def rope(q, k, table, positions=None, interleaved: bool = False, amplitude: floa
             raise ValueError("out cannot be given under autograd")
         got = _launch_on(q, stream, _rope, tensors, table, positions, 1 if interleaved else 0, amplitude,
                          1 if inverse else 0, outs)
+        for t in outs:  # as torch's own in-place operations: a gradient that saved the old values raises
+            if not t.is_inference():
+                torch.autograd.graph.increment_version(t)
     return got if k is not None else got[0]

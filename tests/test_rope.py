@@ -364,3 +364,17 @@ def test_more_rows_than_32_bits_count_are_refused():
     for shape in ((1, 1, 2 ** 32 + 1, 2), (2 ** 16, 1, 2 ** 16, 2)):
         with pytest.raises(ValueError):
             fa.rope(q.expand(shape), None, table)
+
+
+@pytest.mark.gpu
+def test_gradients_that_saved_what_is_rotated_in_place_raise():
+    q, k = (t.detach().contiguous() for t in fused(1, 8, 2, 1, 64, torch.float32, 15))
+    table = fa.rotary_frequencies(64, device="cuda")
+    x = torch.ones_like(q).requires_grad_()
+    y = x * q                       # saves q
+    fa.rope(q, k, table, out=(q, k))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        z = q.clone()
+        assert torch.equal(fa.rope(z, None, table, out=z), fa.rope(q, None, table))
