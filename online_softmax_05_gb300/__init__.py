@@ -409,6 +409,8 @@ def flash_attention(q, k, v, causal: bool = False, scale: float | None = None, r
             q, k = q.squeeze(1), k.squeeze(1)
         else:
             q, k = rope(q, k, rotary, positions, interleaved, amplitude)
+    elif positions is not None or interleaved or amplitude != 1.0:
+        raise ValueError("positions, interleaved and amplitude go with a rotary table")
     return __getattr__("FlashAttention").apply(q, k, v, causal, scale)
 
 

@@ -378,3 +378,10 @@ def test_gradients_that_saved_what_is_rotated_in_place_raise():
     with torch.inference_mode():
         z = q.clone()
         assert torch.equal(fa.rope(z, None, table, out=z), fa.rope(q, None, table))
+
+
+@pytest.mark.parametrize("kw", [dict(positions=torch.arange(4)), dict(interleaved=True), dict(amplitude=1.5)])
+def test_flash_attention_refuses_a_rotation_without_its_table(kw):
+    x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="rotary"):
+        fa.flash_attention(x, x, x, **kw)
