@@ -30,7 +30,7 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
                     fewer than low_turns divided by factor, more than high_turns
                     kept, a linear mix between; use rotary_amplitude(factor) with it
     ``frequencies`` (radians per position, rotary_dim / 2 of them) replaces the
-    formula."""
+    formula; "linear" and "parts" apply to it."""
     import torch
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and at least 2")
@@ -42,6 +42,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
         f = [float(x) for x in frequencies]
         if len(f) != rotary_dim // 2 or not all(math.isfinite(x) for x in f):
             raise ValueError("frequencies must be rotary_dim / 2 finite numbers")
+        if scaling == "base":
+            raise ValueError("scaling 'base' is for the formula, which frequencies replaces")
     else:
         if scaling == "base":
             if rotary_dim == 2:

@@ -385,3 +385,11 @@ def test_flash_attention_refuses_a_rotation_without_its_table(kw):
     x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="rotary"):
         fa.flash_attention(x, x, x, **kw)
+
+
+def test_own_frequencies_have_no_base_to_scale():
+    own = [0.5, 0.25]
+    with pytest.raises(ValueError, match="base"):
+        fa.rotary_frequencies(4, scaling="base", factor=2.0, frequencies=own, device="cpu")
+    half = fa.rotary_frequencies(4, scaling="linear", factor=2.0, frequencies=own, device="cpu")
+    assert torch.equal(half, fa.rotary_frequencies(4, frequencies=[0.25, 0.125], device="cpu"))
