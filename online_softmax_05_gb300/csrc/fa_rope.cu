@@ -220,9 +220,10 @@ int launch_rope(const RopeTensor* tensors, int n_tensors, const void* positions,
     // a thread takes up to 8 heads, fewer while the grid would leave SMs without work
     int per = 8;
     while (per > 1 && p.items * ((heads + per - 1) / per) < static_cast<long long>(num_sms) * 1024) per >>= 1;
+    while ((heads + per - 1) / per > 65535) per *= 2;  // a grid's second extent
     p.heads_thread = per;
     const long long blocks = (p.items + kRopeThreads - 1) / kRopeThreads, ny = (heads + per - 1) / per;
-    if (blocks > 0x7fffffffLL || ny > 65535) return -2;
+    if (blocks > 0x7fffffffLL) return -2;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ny));
     if (dtype == 2) return V == 4 ? launch<float, 4>(p, interleaved, grid, stream) : launch<float, 1>(p, interleaved, grid, stream);
     return dtype == 0 ? launch16<__nv_bfloat16>(p, V, interleaved, grid, stream) : launch16<__half>(p, V, interleaved, grid, stream);

@@ -393,3 +393,14 @@ def test_own_frequencies_have_no_base_to_scale():
         fa.rotary_frequencies(4, scaling="base", factor=2.0, frequencies=own, device="cpu")
     half = fa.rotary_frequencies(4, scaling="linear", factor=2.0, frequencies=own, device="cpu")
     assert torch.equal(half, fa.rotary_frequencies(4, frequencies=[0.25, 0.125], device="cpu"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv", [(160000, 0), (70001, 100001)])
+def test_more_heads_than_a_grid_has_rows(Hq, Hkv):
+    q, k = (torch.randn(1, h, 1, 2, generator=torch.Generator().manual_seed(16)).cuda() for h in (Hq, Hkv))
+    table = fa.rotary_frequencies(2, device="cuda")
+    where = torch.tensor([5], device="cuda")
+    got = fa.rope(q, k, table, where)
+    for x, y in zip((q, k), got):
+        assert torch.equal(y, torch.cat([fa.rope(part, None, table, where) for part in x.split(60000, 1)], 1))
