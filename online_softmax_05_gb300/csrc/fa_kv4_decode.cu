@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     // stage, cost three times these instructions: their operands are uniform, so
     // two lanes' copies are a loop.)
     const int per_page = p.pages.blocks_page;
-    const uint64_t policy = p.RB == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t policy = p.RB == 1 ? l2_policy_evict_first() : l2_policy_unchanged();
     int walk_left = 0, walk_in = 0, walk_head = 0;  // blocks left; block in the page; key/value head
     const int* walk_entry = nullptr;                // of that page; inside the sequence's row of the table while blocks are left
     const unsigned char* walk_from = nullptr;       // that block of the head, this lane's 16 bytes; null: no page
@@ -1297,14 +1297,12 @@ Sizes sizes_of(const Kv4Shape& c, int Hq, int Tq, bool weights, int num_sms) {
             weights ? bh * c.width * c.page_size * RB * nt * 8 * 4 : 0};
 }
 
-// Ranges of heads that blocks of the second kernel take, when there are more heads:
-// with 4 blocks to a range, what is resident at once.
-constexpr int kJoiners = 304;
 template <int D, int G, int NT, int SPLIT>
 int launch_finish(const DecParams& p, cudaStream_t stream, int bh, int num_sms) {
-    // More heads than CTAs are joined several to a block: at most a head a CTA is cut.
+    // More heads than CTAs are joined several to a block, in two ranges an SM (with 4 blocks
+    // to a range, what is resident at once): at most a head a CTA is cut.
     constexpr int kY = D / 8 * NT * SPLIT / 8;
-    const int heads = bh * p.RB, each = SPLIT > 1 ? 1 : (heads + kJoiners - 1) / kJoiners;
+    const int heads = bh * p.RB, each = SPLIT > 1 ? 1 : (heads + 2 * num_sms - 1) / (2 * num_sms);
     const int joins = p.by_head ? 0 : (heads + each - 1) / each * kY;
     // Blocks to a head, sharing its tokens: what is resident at once (5 an SM).  (8 an SM, two
     // rounds: 92 us instead of 89 for 2 sequences of 32768 tokens, 59 instead of 57.5 for 24 ragged ones.)

@@ -26,7 +26,7 @@ constexpr RopeTable rope_table() {
             else c += n % 4 == 0 ? term : -term;
         }
         const int q = (oct + 1) / 2;  // quarter turns that a is counted from
-        double cc = oct % 2 ? c : c, ss = oct % 2 ? -s : s;  // of +-a
+        double cc = c, ss = oct % 2 ? -s : s;  // of +-a
         for (int i = 0; i < q; ++i) {
             const double x = cc;
             cc = -ss;
