@@ -344,7 +344,9 @@ int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k,
  *               may be weights (added to in place).
  *   workspace : fa_kv4_decode_workspace(B, Hq, Hkv, Tq, D, width * page_size,
  *               weights_out != NULL) bytes, 16-byte aligned, used until the call's work
- *               on `stream` is done; or NULL: taken with cudaMallocAsync.
+ *               on `stream` is done (with weights the scores of every slot that the table
+ *               names, 4 bytes for each query row of a head, 8 or a multiple of 16 of
+ *               them, whatever the lengths are); or NULL: taken with cudaMallocAsync.
  *               FA_ERR_SCRATCH if workspace_bytes is too small.
  * Sums, maxima and the softmax are float32.  A weight times a value's s is rounded to
  * fp16's 11 bits; a query's elements are exact down to 2^-28 of their row's largest,

@@ -38,10 +38,11 @@
 // on 24 sequences of 1 to 8111 tokens, as a short head costs all warps a barrier
 // and the latency of its queries.)
 //
-// Measured, with the launches: B=8 H=32 T=32768 D=128 (1.21 GB) 215 us, 5.6 TB/s,
-// 83 % of the copy rate; the 24 sequences above with 8 heads of 4 query rows
-// (115 MB) 41 us, of which 14 are a start (three dependent loads: lengths, table,
-// tokens), the joins and the second kernel.  While it streams it moves 7 TB/s.
+// Measured, with the launches: B=8 H=32 T=32768 D=128 (1.21 GB) 221 us, 5.5 TB/s,
+// 81 % of the copy rate; the 24 sequences above with 8 heads of 4 query rows
+// (115 MB) 41.5 us, 2.8 TB/s, of which 14 are a start (three dependent loads: lengths,
+// table, tokens), the joins and the second kernel.  In D = 128, 8 rows and groups of 32
+// registers spill (236 bytes; 464 with weights).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -86,7 +87,7 @@ constexpr float kPieceUnit = 0x1p-24f;
 constexpr int kStart = 2;
 // Up to this many units a warp, a CTA takes a head by itself: it need not find its
 // place on the line, and nothing is left to a second kernel (2 heads of 117 tokens:
-// 8.4 us instead of 10.4; above, the line's finer cut is worth its joining).
+// 8.4 us instead of 12.4; above, the line's finer cut is worth its joining).
 constexpr int kByHead = 2;
 
 struct DecParams {
@@ -975,9 +976,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
     const int heads = __popc(__ballot_sync(0xffffffffu, (peers & ((2u << lane) - 1)) == 1u << lane));
     // With many heads a warp joins one by itself, or two, from its own pieces alone; with
     // few all warps join each, a part of the channels a warp.  (1920 heads of about 52
-    // tokens and 16 rows: 39 us for both kernels; 61 when all warps joined each of a
-    // CTA's 8 heads and the second kernel took a block a head.  The second path costs
-    // 8 long sequences 1 us of 217.)
+    // tokens and 16 rows take 41 us for both kernels; it was 39 against 61 with all warps
+    // at each of a CTA's 8 heads and a block a head in the second kernel.  The second path
+    // costs 8 long sequences 1 us of 221.)
     const bool alone = heads > kWarps / 2;
     for (int turn = 0; open != 0; ++turn) {
         const int y0 = __ffs(open) - 1;
@@ -1270,10 +1271,11 @@ __global__ void __launch_bounds__(256) fa_kv4_finish_kernel(DecParams p, int joi
     }
 }
 
-// Row tiles of a CTA: one for up to 8 query rows, two above.  Two tiles take 250
+// Row tiles of a CTA: one for up to 8 query rows, two above.  Two tiles take 255
 // registers, so one CTA of 8 warps an SM, but read and unpack the cache once for 16
-// rows: 59 us on 8 sequences of 16384 tokens with 16 rows a head, against 70 with
-// one tile twice (10 or 12 warps with 168 registers spill: 66 and 68).
+// rows: 57.5 us on 8 sequences of 16384 tokens with 16 rows a head, against 72 with
+// one tile twice.  (Before the bands, 10 or 12 warps with 168 registers spilled: 66 and 68
+// where two tiles took 59.)
 int tiles_of(int R) { return R <= 8 ? 1 : 2; }
 int ctas_of(int nt, int num_sms) { return nt == 1 ? 2 * num_sms : num_sms; }
 
@@ -1282,7 +1284,8 @@ struct Sizes {
 };
 // Whether a CTA takes a head by itself (kByHead): short caches whose heads find room in
 // two rounds of CTAs.  The others are cut like long ones: 1408 heads of 16 rows on 152
-// CTAs take 21 us so and 56 with a CTA each; 512 heads on 304 take 19 and 15.
+// CTAs take 23 us so and 62 with a CTA each, 1920 take 41 and 99; 512 heads on 304 take
+// 16.9 and 16.5.
 bool by_head(const Kv4Shape& c, size_t heads, int n_cta) {
     const int tokens = c.D == 128 ? Cfg<128, 64, 1>::kTokens : Cfg<64, 64, 1>::kTokens;
     return heads <= 2 * static_cast<size_t>(n_cta) &&
