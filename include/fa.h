@@ -350,7 +350,7 @@ int fa_kv4_read(const fa_kv4_cache* cache, const int* start, int count, void* k,
  *               FA_ERR_SCRATCH if workspace_bytes is too small.
  * Sums, maxima and the softmax are float32.  A weight times a value's s is rounded to
  * fp16's 11 bits; a query's elements are exact down to 2^-28 of their row's largest,
- * what is smaller loses bits.  Within what a row sees, values whose s lies below 2^-106
+ * what is smaller loses bits.  Within what a row sees, values whose s lies below 2^-110
  * of the largest s may count as their minimum.
  * A non-finite query row that sees a token gives NaN in its o and lse, and in the
  * accounts of the tokens that it sees.

@@ -9,7 +9,7 @@
 // small product of their own with sum(q_g) in three bf16 pieces (24 bits); V's are
 // fp32 sums.  P times V's scale is rounded to fp16 (2^-11, where bf16 would lose
 // 2^-8 as much as the output's own rounding), in several bands of scales where they
-// lie more than 2^10 apart (kLeast); everything else is fp32.
+// lie more than 2^14 apart (kLeast); everything else is fp32.
 //
 // Codes as fp16.  A nibble masked into the low bits of a 16-bit half is the
 // fp16 subnormal n 2^-24 (bits 0-3) or n 2^-20 (bits 4-7), which the matrix
@@ -69,14 +69,16 @@ constexpr int kStages = 2;
 // units), so that it seldom moves again.
 constexpr float kAhead = 4.f;
 // P times a value scale goes to fp16 in units that put the largest scale at 2^12 or above and
-// the largest P at 2^-4 or above.  While every scale of a unit is kLeast or more there, 2^-10
-// of the largest or so, what weighs 2^-12 of the heaviest token or more keeps all of its bits.
-// From a smaller scale on, the values go through the products in bands: each P times a scale
-// in the first of them that brings it to kLeast, a further kBand (2^12) up each time, the
-// accumulators in units as much smaller meanwhile; the bands reach down to scales 2^-106 of
-// the largest.  (64 heads of 32768 tokens: 67.0 us without looking for such scales, 67.7
-// with it; 123, 153 and 245 where two groups lie 2^14, 2^30 and 2^60 apart.)
-constexpr float kLeast = 4.f, kBand = 4096.f, kLastBand = 0x1p96f;
+// the largest P at 2^-4 or above.  While every scale so far is kLeast or more there, 2^-14
+// of the largest or so, what fp16 cannot hold of a product is 2^-25, against the 2^-6 or more
+// that the heaviest token adds to a row: 2^-11.5 for 32768 tokens, at random, as much as
+// their rounding.  From a smaller scale on, the values go through the products in bands: each
+// P times a scale in the first of them that brings it to kLeast, a further kBand (2^16) up
+// each time, the accumulators in units as much smaller meanwhile; the bands reach down to
+// scales 2^-110 of the largest.  (64 heads of 32768 tokens: 67.0 us without looking for such scales, 67.7
+// with it; 126, 156 and 188 where two groups lie 2^18, 2^30 and 2^60 apart, 75 where the
+// steps of one are all 0.)
+constexpr float kLeast = 0.25f, kBand = 65536.f, kLastBand = 0x1p96f;
 // Outputs of a piece are sums of P v, P up to 1: held 2^-24 times, so that 2^24 tokens
 // of the largest bf16 values do not overflow.
 constexpr float kPieceUnit = 0x1p-24f;
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fa_kv4_decode_kerne
                     }
                 }
                 vtop[0][0] = size_of(most);
-                const uint32_t floor = (range - (12u << 7) & 0xffffu) | 0xff800000u;  // (kLeast / inv, -infinity)
+                const uint32_t floor = (range - (16u << 7) & 0xffffu) | 0xff800000u;  // (kLeast / inv, -infinity)
                 more = !__hble2(as_bf2(most & 0x7fff7fffu), as_bf2(range)) || !__hbge2(as_bf2(least), as_bf2(floor));
             }
             float mx[NT][2];
