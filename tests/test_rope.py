@@ -316,7 +316,7 @@ def test_outputs_whose_rows_share_elements_are_refused():
     assert c_rope(tensors=dict(heads=1, out_b=64, out_t=64)) == -8
     assert c_rope(tensors=dict(out_t=64, out_h=64)) == -8
     assert c_rope(tensors=dict(out_t=64, out_h=960)) == -8          # the last row on the next head's first
-    assert c_rope(tensors=dict(out_b=3072, out_t=64, out_h=1024)) == -8
+    assert c_rope(tensors=dict(out_b=2048, out_t=64, out_h=1024)) == -8
     assert c_rope(tensors=dict(out_t=256, out_h=64, out_b=16 * 256 - 1)) == -8
     assert c_rope(tensors=dict(inp=BASE, out=BASE, in_t=64, in_h=64, out_t=64, out_h=64)) == -8      # in place
 
