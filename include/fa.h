@@ -55,7 +55,7 @@ typedef enum fa_status {
     FA_ERR_NULL = -1,            /* a required pointer is NULL */
     FA_ERR_SHAPE = -2,           /* B, H, T (Tq, Tk) out of range, or a size overflows the index types */
     FA_ERR_UNSUPPORTED = -3,     /* D is not 64 or 128 */
-    FA_ERR_ALIGN = -4,           /* a base pointer is not 16-byte aligned */
+    FA_ERR_ALIGN = -4,           /* a base pointer is not 16-byte aligned, or a stride no multiple of 8 elements */
     FA_ERR_CUDA = -5,            /* a CUDA runtime / driver call failed (launch, attribute, tensor map) */
     FA_ERR_NOMEM = -6,           /* stream-ordered workspace allocation failed */
     FA_ERR_DEVICE_TIMEOUT = -7,  /* a kernel's bounded wait ran out (pipeline stall); outputs invalid */
@@ -63,7 +63,7 @@ typedef enum fa_status {
     FA_ERR_ARCH = -9,            /* current device is not compute capability 10.3 (sm_103a) */
     FA_ERR_SCRATCH = -10,        /* fa_bwd_noalloc: problem needs more than its fixed scratch buffer */
     FA_ERR_SEQLEN = -11,         /* recorded by a kernel: a cu_seqlens length is negative or above max_seqlen,
-                                    or a cache's length, slot or position is outside its block table or accounts */
+                                    a key length is outside its tensor, or a cache's length, slot or position is outside its block table or accounts */
     FA_ERR_DEBUG_CHECK = -12,    /* debug library only: a kernel's run-time index failed its bounds check */
     FA_ERR_PAGE = -13            /* recorded by a kernel: a block table names no page of the pool where a token lies */
 } fa_status;
@@ -222,6 +222,54 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
  */
 int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
               int B, int H, int Tq, int Tk, int D, float scale, void* stream);
+
+/*
+ * Cross attention: Tq queries of a sequence over the Tk keys and values of another
+ * (an encoder's states), grouped heads as in fa_fwd_gqa, no causal mask.
+ *   S = Q K^T scale over the keys j < key_lengths[b], O = softmax(S) V,
+ *   LSE = log sum exp(S);  the backward is fa_bwd's over the same keys.
+ * A sequence without keys gives O = 0, LSE = -infinity and gradients of 0.
+ *   q, o, dO, dq    : (B, Hq, Tq, D) bf16;  k, v, dk, dv: (B, Hkv, Tk, D) bf16,
+ *                     each by its strides b, h, t in elements, positive
+ *                     multiples of 8 where the dimension is more than one, channels
+ *                     contiguous: heads may lie behind or before tokens, and
+ *                     tensors may be views of a fused projection
+ *   key_lengths  in : DEVICE int32[B], 0 .. Tk, or NULL: Tk everywhere.  Keys and
+ *                     values past the length are not used, whatever they hold
+ *                     (NaN and infinities too); dk and dv are 0 there.  Another length
+ *                     is recorded as FA_ERR_SEQLEN and counts as 0.
+ *   lse             : (B, Hq, Tq) float32, contiguous
+ *   o_rest          : (B, Hq, Tq, D) bf16, contiguous, or NULL: what rounding o to
+ *                     bf16 took off, written by the forward for the backward, whose
+ *                     rowsum(dO o O) is then of O to 16 bits.  Without it dq is less exact where
+ *                     keys have a mean.
+ *   workspace       : fa_cross_bwd: fa_cross_bwd_workspace(B, Hq, Hkv, Tq, Tk, D)
+ *                     bytes, 256-byte aligned, used until the call's work on `stream` is
+ *                     done; or NULL: taken with cudaMallocAsync.  FA_ERR_SCRATCH if
+ *                     workspace_bytes is too small.  The forward takes none.
+ * B * Hq * Tq and B * Hkv * Tk within int32.  FA_ERR_ALIGN for a base that is not
+ * 16-byte aligned or a stride that is no multiple of 8; FA_ERR_ARG for a stride
+ * below 1, an output whose rows may share elements, or one whose range of addresses
+ * meets another tensor's.  fa_set_deterministic holds as for fa_bwd: at D = 64, with
+ * at least one CTA per SM, dq's last bits may otherwise vary.
+ */
+typedef struct fa_cross_shape {
+    int B, Hq, Hkv, Tq, Tk, D;
+    const int* key_lengths;
+} fa_cross_shape;
+typedef struct fa_cross_tensor {
+    void* ptr;              /* not written through where the tensor is an input */
+    long long b, h, t;      /* strides in elements */
+} fa_cross_tensor;
+int fa_cross_fwd(const fa_cross_shape* shape, const fa_cross_tensor* q, const fa_cross_tensor* k,
+                 const fa_cross_tensor* v, const fa_cross_tensor* o, void* o_rest, float* lse, float scale,
+                 void* stream);
+long long fa_cross_bwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D);
+int fa_cross_bwd(const fa_cross_shape* shape, const fa_cross_tensor* q, const fa_cross_tensor* k,
+                 const fa_cross_tensor* v, const fa_cross_tensor* o, const void* o_rest,
+                 const fa_cross_tensor* dO, const float* lse,
+                 const fa_cross_tensor* dq, const fa_cross_tensor* dk, const fa_cross_tensor* dv, float scale,
+                 void* workspace, long long workspace_bytes, void* stream);
 
 /*
  * Rotary positions: turns pairs of channels of queries and keys by an angle

@@ -15,7 +15,8 @@ import threading
 __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_varlen", "attention_forward_varlen", "fa_bwd_varlen", "attention_backward_varlen", "fa_decode", "attention_decode", "fa_bwd_noalloc", "fa_strerror", "fa_get_device_status", "fa_version",
            "attention_forward", "attention_backward", "FAError", "library_path", "load_library",
            "FlashAttention", "flash_attention", "rope", "rotary_frequencies", "rotary_amplitude", "kv4_pool", "kv4_append",
-           "kv4_read", "attention_decode_kv4", "kv4_evict"]
+           "kv4_read", "attention_decode_kv4", "kv4_evict", "attention_forward_cross", "attention_backward_cross",
+           "cross_attention"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -108,6 +109,12 @@ def load_library():
         lib.fa_kv4_evict_workspace.restype = ll
         lib.fa_kv4_evict.argtypes = [blob, vp, vp, ll, i, i, vp, vp, vp, vp, vp, ll, vp]
         lib.fa_kv4_evict.restype = i
+        lib.fa_cross_fwd.argtypes = [blob] * 5 + [vp, vp, f, vp]
+        lib.fa_cross_fwd.restype = i
+        lib.fa_cross_bwd_workspace.argtypes = [i] * 6
+        lib.fa_cross_bwd_workspace.restype = ll
+        lib.fa_cross_bwd.argtypes = [blob] * 5 + [vp, blob, vp] + [blob] * 3 + [f, vp, ll, vp]
+        lib.fa_cross_bwd.restype = i
         _lib = lib
         return lib
 
@@ -416,3 +423,4 @@ def flash_attention(q, k, v, causal: bool = False, scale: float | None = None, r
 
 from .rotary import rope, rotary_amplitude, rotary_frequencies  # noqa: E402
 from .kv4 import attention_decode_kv4, kv4_append, kv4_evict, kv4_pool, kv4_read  # noqa: E402
+from .cross import attention_backward_cross, attention_forward_cross, cross_attention  # noqa: E402

@@ -87,13 +87,13 @@ const char* fa_strerror(int status) {
         case FA_ERR_NULL: return "a required pointer is NULL";
         case FA_ERR_SHAPE: return "B, H and T (Tq, Tk) must be >= 1 and B*H*T must fit in a 32-bit index";
         case FA_ERR_UNSUPPORTED: return "head dimension D must be 64 or 128 (and fa_decode takes at most 8 query rows)";
-        case FA_ERR_ALIGN: return "tensor base pointers must be 16-byte aligned";
+        case FA_ERR_ALIGN: return "tensor base pointers must be 16-byte aligned (and strides multiples of 8 elements)";
         case FA_ERR_CUDA: return "a CUDA runtime or driver call failed";
         case FA_ERR_NOMEM: return "stream-ordered workspace allocation failed";
         case FA_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out (pipeline stall); outputs are invalid";
         case FA_ERR_ARG: return "causal must be 0 or 1, scale finite, and outputs must not overlap other buffers (or another argument is out of its range)";
         case FA_ERR_ARCH: return "the current device is not compute capability 10.3 (sm_103a)";
-        case FA_ERR_SEQLEN: return "a cu_seqlens length is negative or above max_seqlen, or a cache's length, slot or position is outside its block table or accounts (recorded by the kernel)";
+        case FA_ERR_SEQLEN: return "a cu_seqlens length is negative or above max_seqlen, a key length is outside its tensor, or a cache's length, slot or position is outside its block table or accounts (recorded by the kernel)";
         case FA_ERR_SCRATCH: return "fa_bwd_noalloc: the problem needs more than the fixed 64 MiB scratch buffer";
         case FA_ERR_PAGE: return "a block table names no page of the pool where a token lies (recorded by the kernel)";
         case FA_ERR_DEBUG_CHECK: return "debug library: a kernel's run-time index failed its bounds check (access skipped)";
@@ -288,12 +288,14 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
 
 int fa_get_device_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
-    int a = fa::fwd_take_status();
-    int b = fa::bwd_take_status();
-    int c = fa::kv4_cache_take_status();
-    int d = fa::kv4_decode_take_status();
-    if (a == -5 || b == -5 || c == -5 || d == -5) return FA_ERR_CUDA;
-    return a != 0 ? a : b != 0 ? b : c != 0 ? c : d;
+    int first = FA_OK;
+    for (const auto take : {fa::fwd_take_status, fa::bwd_take_status, fa::kv4_cache_take_status,
+                            fa::kv4_decode_take_status}) {
+        const int status = take();
+        if (status == FA_ERR_CUDA) return FA_ERR_CUDA;
+        if (first == FA_OK) first = status;
+    }
+    return first;
 }
 
 }  // extern "C"
@@ -316,9 +318,149 @@ bool rows_apart(std::array<Dim, 3> dims, int D) {
     return true;
 }
 
+// The caller's workspace, or one taken stream-ordered for the call.
+struct Workspace {
+    void* ptr = nullptr;
+    bool mine = false;
+    cudaStream_t stream;
+    int take(void* given, size_t given_bytes, size_t need, cudaStream_t st, uintptr_t align = 16) {
+        stream = st;
+        if (need == 0) return FA_OK;
+        if (given != nullptr) {
+            if (given_bytes < need) return FA_ERR_SCRATCH;
+            if (reinterpret_cast<uintptr_t>(given) & (align - 1)) return FA_ERR_ALIGN;
+            ptr = given;
+            return FA_OK;
+        }
+        if (cudaMallocAsync(&ptr, need, st) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_NOMEM;
+        }
+        mine = true;
+        return FA_OK;
+    }
+    int release(int rc) {
+        if (mine && cudaFreeAsync(ptr, stream) != cudaSuccess && rc == FA_OK) return FA_ERR_CUDA;
+        return rc;
+    }
+};
+
+bool overlaps_any(Range a, const Range* r, int n) {
+    for (int i = 0; i < n; ++i)
+        if (overlap(a, r[i])) return true;
+    return false;
+}
+
+int check_cross(const fa_cross_shape* s, float scale) {
+    if (s->B < 1 || s->Hq < 1 || s->Hkv < 1 || s->Tq < 1 || s->Tk < 1 || s->Hq % s->Hkv != 0) return FA_ERR_SHAPE;
+    const long long heads_q = static_cast<long long>(s->B) * s->Hq, heads_k = static_cast<long long>(s->B) * s->Hkv;
+    if (heads_q > (1 << 30) || heads_q * s->Tq > INT_MAX || heads_k * s->Tk > INT_MAX) return FA_ERR_SHAPE;
+    if (s->D != 64 && s->D != 128) return FA_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return FA_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(s->key_lengths) & 3u) return FA_ERR_ALIGN;
+    return FA_OK;
+}
+// One tensor of (B, heads, T, D): its checks, its range of addresses, and the launchers' form.
+int check_cross_tensor(const fa_cross_tensor* x, int B, int heads, int T, int D, bool written, Range* range,
+                       fa::CrossTensor* out) {
+    if (!x || !x->ptr) return FA_ERR_NULL;
+    const Dim dims[3] = {{B, x->b}, {heads, x->h}, {T, x->t}};
+    size_t span = D;
+    for (const Dim& d : dims) {
+        if (d.size == 1) continue;
+        if (d.stride < 1) return FA_ERR_ARG;
+        if (d.stride >= 1LL << 38) return FA_ERR_SHAPE;  // a tensor map's strides end at 2^40 bytes
+        if (d.stride % 8 != 0) return FA_ERR_ALIGN;
+        span += (d.size - 1) * static_cast<size_t>(d.stride);
+    }
+    if (!aligned16(x->ptr)) return FA_ERR_ALIGN;
+    if (written && !rows_apart({{dims[0], dims[1], dims[2]}}, D)) return FA_ERR_ARG;
+    *range = range_of(x->ptr, span * 2);
+    *out = {x->ptr, x->b, x->h, x->t};
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int fa_cross_fwd(const fa_cross_shape* s, const fa_cross_tensor* q, const fa_cross_tensor* k, const fa_cross_tensor* v,
+                 const fa_cross_tensor* o, void* o_rest, float* lse, float scale, void* stream) {
+    if (!s || !lse) return FA_ERR_NULL;
+    int rc = check_cross(s, scale);
+    if (rc != FA_OK) return rc;
+    Range r[4];
+    fa::CrossTensor x[4];
+    if ((rc = check_cross_tensor(q, s->B, s->Hq, s->Tq, s->D, false, &r[0], &x[0])) != FA_OK ||
+        (rc = check_cross_tensor(k, s->B, s->Hkv, s->Tk, s->D, false, &r[1], &x[1])) != FA_OK ||
+        (rc = check_cross_tensor(v, s->B, s->Hkv, s->Tk, s->D, false, &r[2], &x[2])) != FA_OK ||
+        (rc = check_cross_tensor(o, s->B, s->Hq, s->Tq, s->D, true, &r[3], &x[3])) != FA_OK)
+        return rc;
+    if (!aligned16(lse) || !aligned16(o_rest)) return FA_ERR_ALIGN;
+    const size_t rows = static_cast<size_t>(s->B) * s->Hq * s->Tq;
+    const Range outs[3] = {r[3], range_of(lse, rows * 4), range_of(o_rest, o_rest ? rows * s->D * 2 : 0)};
+    r[3] = range_of(s->key_lengths, s->key_lengths ? s->B * static_cast<size_t>(4) : 0);
+    for (int i = 0; i < 3; ++i)
+        if (overlaps_any(outs[i], r, 4) || overlaps_any(outs[i], outs, i)) return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    const fa::CrossShape shape{s->B, s->Hq, s->Hkv, s->Tq, s->Tk, s->D, s->key_lengths};
+    return fa::launch_cross_fwd(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, static_cast<cudaStream_t>(stream), knobs(), sms);
+}
+
+long long fa_cross_bwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D) {
+    const fa_cross_shape s{B, Hq, Hkv, Tq, Tk, D, nullptr};
+    int rc = check_cross(&s, 1.f);
+    if (rc != FA_OK) return rc;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return static_cast<long long>(
+        fa::cross_bwd_workspace({B, Hq, Hkv, Tq, Tk, D, nullptr}, g_deterministic.load() != 0, sms));
+}
+
+int fa_cross_bwd(const fa_cross_shape* s, const fa_cross_tensor* q, const fa_cross_tensor* k, const fa_cross_tensor* v,
+                 const fa_cross_tensor* o, const void* o_rest, const fa_cross_tensor* dO, const float* lse,
+                 const fa_cross_tensor* dq, const fa_cross_tensor* dk, const fa_cross_tensor* dv, float scale, void* workspace,
+                 long long workspace_bytes, void* stream) {
+    if (!s || !lse) return FA_ERR_NULL;
+    int rc = check_cross(s, scale);
+    if (rc != FA_OK) return rc;
+    const fa_cross_tensor* given[8] = {q, k, v, o, dO, dq, dk, dv};
+    Range r[8];
+    fa::CrossTensor x[8];
+    for (int i = 0; i < 8; ++i) {
+        const bool keys = i == 1 || i == 2 || i == 6 || i == 7;
+        rc = check_cross_tensor(given[i], s->B, keys ? s->Hkv : s->Hq, keys ? s->Tk : s->Tq, s->D, i >= 5, &r[i], &x[i]);
+        if (rc != FA_OK) return rc;
+    }
+    if (!aligned16(lse) || !aligned16(o_rest)) return FA_ERR_ALIGN;
+    const size_t rows = static_cast<size_t>(s->B) * s->Hq * s->Tq;
+    const Range outs[3] = {r[5], r[6], r[7]};
+    r[5] = range_of(lse, rows * 4);
+    r[7] = range_of(o_rest, o_rest ? rows * s->D * 2 : 0);
+    r[6] = range_of(s->key_lengths, s->key_lengths ? s->B * static_cast<size_t>(4) : 0);
+    for (int i = 0; i < 3; ++i)
+        if (overlaps_any(outs[i], r, 8) || overlaps_any(outs[i], outs, i)) return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    const fa::DebugKnobs k_ = knobs();
+    const fa::CrossShape shape{s->B, s->Hq, s->Hkv, s->Tq, s->Tk, s->D, s->key_lengths};
+    const size_t need = fa::cross_bwd_workspace(shape, k_.deterministic != 0, sms);
+    if (workspace) {
+        const Range w = range_of(workspace, need);
+        if (overlaps_any(w, r, 8) || overlaps_any(w, outs, 3)) return FA_ERR_ARG;
+    }
+    Workspace ws;
+    rc = ws.take(workspace, static_cast<size_t>(workspace_bytes > 0 ? workspace_bytes : 0), need,
+                 static_cast<cudaStream_t>(stream), 256);
+    if (rc != FA_OK) return rc;
+    rc = fa::launch_cross_bwd(shape, x[0], x[1], x[2], x[3], o_rest, x[4], lse, x[5], x[6], x[7], scale, ws.ptr,
+                              static_cast<cudaStream_t>(stream), k_, sms);
+    return ws.release(rc);
+}
 
 int fa_rope(const fa_rope_tensor* tensors, int n_tensors, const void* positions, int positions_64, long long positions_b,
             const void* freq, int B, int T, int D, int rotary, int interleaved, float amplitude, int inverse, int dtype,
@@ -397,39 +539,6 @@ Range kv4_table_range(const fa_kv4_cache* c) {
     return range_of(c->block_table, static_cast<size_t>(c->B) * c->width * 4);
 }
 Range kv4_lengths_range(const fa_kv4_cache* c) { return range_of(c->lengths, static_cast<size_t>(c->B) * 4); }
-bool overlaps_any(Range a, const Range* r, int n) {
-    for (int i = 0; i < n; ++i)
-        if (overlap(a, r[i])) return true;
-    return false;
-}
-
-// The caller's workspace, or one taken stream-ordered for the call.
-struct Workspace {
-    void* ptr = nullptr;
-    bool mine = false;
-    cudaStream_t stream;
-    int take(void* given, size_t given_bytes, size_t need, cudaStream_t st) {
-        stream = st;
-        if (need == 0) return FA_OK;
-        if (given != nullptr) {
-            if (given_bytes < need) return FA_ERR_SCRATCH;
-            if (!aligned16(given)) return FA_ERR_ALIGN;
-            ptr = given;
-            return FA_OK;
-        }
-        if (cudaMallocAsync(&ptr, need, st) != cudaSuccess) {
-            cudaGetLastError();
-            return FA_ERR_NOMEM;
-        }
-        mine = true;
-        return FA_OK;
-    }
-    int release(int rc) {
-        if (mine && cudaFreeAsync(ptr, stream) != cudaSuccess && rc == FA_OK) return FA_ERR_CUDA;
-        return rc;
-    }
-};
-
 }  // namespace
 
 extern "C" {

@@ -181,7 +181,24 @@ struct BwdParams {
     // of the grids is h * n_seq + s (per-row vectors: bh * T_pad + t).
     const int* cu_seqlens;
     int n_seq, total;
+    // Cross attention (CROSS kernels): T above is the number of queries, Tk that of keys,
+    // key_lengths[b] (null: all) of them there; the tensor maps are {D, T, heads, B}.
+    int Tk;
+    const int* key_lengths;
+    CrossTensor dq_cross, dk_cross, dv_cross;
 };
+
+// Keys of sequence b in cross attention; a length that the tensor cannot hold is reported and counts as 0.
+__device__ __forceinline__ int keys_of(const int* key_lengths, int Tk, int b) {
+    if (key_lengths == nullptr) return Tk;
+    const int len = __ldg(key_lengths + b);
+    if (len >= 0 && len <= Tk) return len;
+    atomicCAS(&g_status_bwd, 0, kStatusBadSeqlen);
+    return 0;
+}
+__device__ __forceinline__ __nv_bfloat16* row_of(const CrossTensor& x, int b, int h, long long t) {
+    return static_cast<__nv_bfloat16*>(x.ptr) + b * x.b + h * x.h + t * x.t;
+}
 
 // Sequence of grid row bh: its length and first packed row (VARLEN), or the
 // dense T and row 0.  A sequence longer than T, or outside the packed rows,
@@ -256,14 +273,25 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, Ctl c) {
 // ---------------------------------------------------------------- preprocess
 // D_i = rowsum(dO o O) ("Lab 06", section 4) and LSE2 = LSE * log2(e), both
 // stored NEGATED (the main kernels add them with FMAs); rows t >= T of the
-// padded vectors are 0.  8 elements per thread.
-template <int D, bool VARLEN>
+// padded vectors are 0.  8 elements per thread.  CROSS: o and dO by their strides,
+// and dq (unless summed in place) of a sequence without keys is zeroed here.  D is wanted
+// more exactly than from a rounded O: an error of D goes into dQ times sum_j P_ij K_j, which
+// does not average out where keys have a mean (2 x 8192 x 8192, means of 0.3: dQ off by
+// 8.4e-3 of its norm with D from O alone, 2.4e-3 with the rest).
+struct PreCross {
+    CrossTensor o, dO, dq;
+    const __nv_bfloat16* rest;  // of O's rounding, contiguous (B, Hq, Tq, D), or null
+    const int* key_lengths;
+    int Tk;
+};
+template <int D, bool VARLEN, bool CROSS = false>
 __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o,
                                                          const __nv_bfloat16* __restrict__ dO,
                                                          const float* __restrict__ lse, float* __restrict__ dvec,
                                                          float* __restrict__ lse2, int BH, int T, int T_pad,
                                                          int* __restrict__ dq_next, const int* __restrict__ cu_seqlens,
-                                                         int n_seq, int H, int total, float* __restrict__ dqacc) {
+                                                         int n_seq, int H, int total, float* __restrict__ dqacc,
+                                                         PreCross x) {
     constexpr int TPR = D / 8;            // threads per row
     constexpr int RPW = 32 / TPR;         // rows per warp
     if (blockIdx.x == 0 && threadIdx.x == 0) *dq_next = 0;  // the dQ kernel's item counter
@@ -289,13 +317,29 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const __nv_bfloat16* __
         float acc = 0.f;
         if (in && t < len) {
             const size_t off = orow * D + sub * 8;
-            const uint4 a = *reinterpret_cast<const uint4*>(o + off);
-            const uint4 b = *reinterpret_cast<const uint4*>(dO + off);
+            const __nv_bfloat16 *oat = o + off, *dat = dO + off;
+            if constexpr (CROSS) {
+                const int sq = bh / H, h = bh % H;
+                oat = row_of(x.o, sq, h, t) + sub * 8;
+                dat = row_of(x.dO, sq, h, t) + sub * 8;
+                if (x.dq.ptr != nullptr && keys_of(x.key_lengths, x.Tk, sq) == 0)
+                    *reinterpret_cast<uint4*>(row_of(x.dq, sq, h, t) + sub * 8) = make_uint4(0, 0, 0, 0);
+            }
+            const uint4 a = *reinterpret_cast<const uint4*>(oat);
+            const uint4 b = *reinterpret_cast<const uint4*>(dat);
+            uint4 r4 = make_uint4(0, 0, 0, 0);
+            if (CROSS && x.rest != nullptr) r4 = *reinterpret_cast<const uint4*>(x.rest + off);
             const __nv_bfloat162* pa = reinterpret_cast<const __nv_bfloat162*>(&a);
             const __nv_bfloat162* pb = reinterpret_cast<const __nv_bfloat162*>(&b);
+            const __nv_bfloat162* pr = reinterpret_cast<const __nv_bfloat162*>(&r4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 fa2 = __bfloat1622float2(pa[e]);
+                float2 fa2 = __bfloat1622float2(pa[e]);
+                if constexpr (CROSS) {
+                    const float2 fr2 = __bfloat1622float2(pr[e]);
+                    fa2.x += fr2.x;
+                    fa2.y += fr2.y;
+                }
                 const float2 fb2 = __bfloat1622float2(pb[e]);
                 acc = fmaf(fa2.x, fb2.x, acc);
                 acc = fmaf(fa2.y, fb2.y, acc);
@@ -317,10 +361,10 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const __nv_bfloat16* __
 
 // dQ = bf16(dQacc * scale) for the rows t < T of the fused backward's fp32
 // accumulator (B*H, T_pad, D); 8 elements per thread.
-template <int D>
+template <int D, bool CROSS = false>
 __global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const float* __restrict__ acc,
                                                                 __nv_bfloat16* __restrict__ dq, int BH, int T,
-                                                                int T_pad, float scale) {
+                                                                int T_pad, float scale, int H, CrossTensor dq_cross) {
     constexpr int G = D / 8;
     const long long n = static_cast<long long>(BH) * T * G;
     for (long long g = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; g < n;
@@ -335,12 +379,26 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const float* __r
         o.y = pack_bf16x2(a.z * scale, a.w * scale);
         o.z = pack_bf16x2(b.x * scale, b.y * scale);
         o.w = pack_bf16x2(b.z * scale, b.w * scale);
-        reinterpret_cast<uint4*>(dq + row * D + c8 * 8)[0] = o;
+        __nv_bfloat16* to = dq + row * D;
+        if constexpr (CROSS) to = row_of(dq_cross, static_cast<int>(bh) / H, static_cast<int>(bh) % H, t);
+        reinterpret_cast<uint4*>(to + c8 * 8)[0] = o;
     }
 }
 
 // ---------------------------------------------------------------- dK / dV kernel
-template <int D, bool CAUSAL, bool VARLEN, bool FUSE = false>
+// A 128-row tile's 64 columns, by the layout's coordinates.
+template <bool CROSS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int y, int z,
+                                          int heads, uint64_t policy) {
+    if constexpr (CROSS)
+        tma_load_4d_hint(dst, map, bar, col, y, z % heads, z / heads, policy);
+    else
+        tma_load_3d_hint(dst, map, bar, col, y, z, policy);
+}
+
+// CROSS: queries and keys of different sequences.  Rows of K and V past a sequence's keys
+// are zeroed in shared memory (as 0 x NaN would reach the gradients) and their gradients are 0.
+template <int D, bool CAUSAL, bool VARLEN, bool FUSE = false, bool CROSS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -401,7 +459,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // the sequence of this row of the grid (packed batches: its own length and rows)
     const SeqSpan span = seq_span<VARLEN>(p, bh);
     const int T = span.T;
-    if (kt * kBN >= T) return;  // a shorter sequence has fewer key tiles: the whole CTA leaves
+    const int Tk = CROSS ? keys_of(p.key_lengths, p.Tk, bh / p.Hkv) : T;  // keys of this sequence
+    if constexpr (CROSS) {
+        if (kt * kBN >= Tk) {  // no keys in this tile: gradients of 0, up to the tensor's end
+            const int row = kt * kBN + (tid >> 1);
+            if (tid < 256 && row < p.Tk) {
+                const CrossTensor& x = tid & 1 ? p.dv_cross : p.dk_cross;
+                uint4* to = reinterpret_cast<uint4*>(row_of(x, bh / p.Hkv, bh % p.Hkv, row));
+                for (int c = 0; c < D / 8; ++c) to[c] = make_uint4(0, 0, 0, 0);
+            }
+            return;
+        }
+    }
+    if (kt * kBN >= Tk) return;  // a shorter sequence has fewer key tiles: the whole CTA leaves
     // TMA coordinates (y, z) of the 128-row tile starting at row r0 of grid row bhx
     auto tile_yz = [&](int r0, int bhx, int& y, int& z) {
         if constexpr (VARLEN) {
@@ -465,11 +535,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             int ky, kz;
             tile_yz(kt * kBN, bh, ky, kz);
             // the key tile starts inside its sequence and its head exists
-            const bool kv_ok = FA_CHECK(kt * kBN < T && bh >= 0 && bh < p.BH, &g_status_bwd, abort_flag);
+            const bool kv_ok = FA_CHECK(kt * kBN < Tk && bh >= 0 && bh < p.BH, &g_status_bwd, abort_flag);
             if (kv_ok) mbar_arrive_expect_tx(kv_full, 2 * C::kKVBytes);
             for (int a = 0; kv_ok && a < C::kAtomsD; ++a) {
-                tma_load_3d_hint(sK + a * 128 * 128, &tm_k, kv_full, 64 * a, ky, kz, pol_kv);
-                tma_load_3d_hint(sV + a * 128 * 128, &tm_v, kv_full, 64 * a, ky, kz, pol_kv);
+                load_tile<CROSS>(sK + a * 128 * 128, &tm_k, kv_full, 64 * a, ky, kz, p.Hkv, pol_kv);
+                load_tile<CROSS>(sV + a * 128 * 128, &tm_v, kv_full, 64 * a, ky, kz, p.Hkv, pol_kv);
             }
             for (int it = 0; it < n_it; ++it) {
                 const int qt = q_tile_of(it), bhq = q_head_of(it);
@@ -494,7 +564,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         int qy, qz;
                         tile_yz(qt * BM, bhq, qy, qz);
                         for (int a = 0; a < C::kAtomsD; ++a)
-                            tma_load_3d_hint(sQ(st) + a * BM * 128, &tm_q, fb, 64 * a, qy, qz, pol_q);
+                            load_tile<CROSS>(sQ(st) + a * BM * 128, &tm_q, fb, 64 * a, qy, qz, p.Hq, pol_q);
                         bulk_load_1d(sLse(st), p.lse2 + voff, BM * 4, fb);
                         bulk_load_1d(sDv(st), p.dvec + voff, BM * 4, fb);
                     }
@@ -511,7 +581,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     int qy, qz;
                     tile_yz(qt * BM, bhq, qy, qz);
                     for (int a = 0; a < C::kAtomsD; ++a)
-                        tma_load_3d_hint(sdO(st) + a * BM * 128, &tm_do, fb, 64 * a, qy, qz, pol_q);
+                        load_tile<CROSS>(sdO(st) + a * BM * 128, &tm_do, fb, 64 * a, qy, qz, p.Hq, pol_q);
                 }
             }
             // drain: copies still in flight must land before the CTA exits
@@ -563,6 +633,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // The compute warps turn dP^T(i) into dS^T(i) while dV(i) and S^T(i+1)
             // run, and S^T(i+1) into P^T(i+1) while dK(i) and dP^T(i+1) run.
             if (!wait_all(kv_full, 0, ctl)) goto mma_teardown;
+            if constexpr (CROSS) {
+                if ((kt + 1) * kBN > Tk && Tk < p.Tk) {
+                    zero_tail_rows(sK, C::kAtomsD, Tk - kt * kBN, lane);
+                    zero_tail_rows(sV, C::kAtomsD, Tk - kt * kBN, lane);
+                }
+            }
             if (!wait_all(q_full(0), 0, ctl)) goto mma_teardown;
             tc_fence_after();
             issue_s(0);
@@ -680,7 +756,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int it = 0; it < n_it; ++it) {
             const int st = it % NQS;
             const int qt = q_tile_of(it), q0 = qt * BM;
-            const bool masked = bwd_tile_class(T, CAUSAL, BM, qt, kt) == kMasked;
+            const bool masked = CROSS ? q0 + BM > T || (kt + 1) * kBN > Tk
+                                      : bwd_tile_class(T, CAUSAL, BM, qt, kt) == kMasked;
+            auto visible = [&](int q, int key) {
+                return CROSS ? q < T && key < Tk : bwd_elem_visible(T, CAUSAL, q, key);
+            };
             if (!warp_wait(q_full(st), (it / NQS) & 1, ctl) || !warp_wait<false>(s_full, it & 1, ctl)) {
                 ok = false;
                 break;
@@ -722,8 +802,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         const int e = 32 * (r >> 1) + 4 * k + 2 * (r & 1);
                         const int key = key_base + 16 * (r >> 1) + 8 * (r & 1);
                         const int q = q0 + 64 * h + 8 * k + 2 * t4;
-                        if (!bwd_elem_visible(T, CAUSAL, q, key)) pf[e] = 0.f;
-                        if (!bwd_elem_visible(T, CAUSAL, q + 1, key)) pf[e + 1] = 0.f;
+                        if (!visible(q, key)) pf[e] = 0.f;
+                        if (!visible(q + 1, key)) pf[e + 1] = 0.f;
                     }
             }
 #pragma unroll
@@ -850,6 +930,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t col = h ? C::kDV : C::kDK;
             const float mul = h ? 1.f : p.scale;
             const uint32_t stage = h ? sdO(0) : sQ(0);
+            const bool there = !CROSS || kt * kBN + static_cast<int>(row) < Tk;
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
                 uint32_t v[32];
@@ -862,8 +943,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     uint32_t w4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        w4[e] = pack_bf16x2(__uint_as_float(v[8 * g + 2 * e]) * mul,
-                                            __uint_as_float(v[8 * g + 2 * e + 1]) * mul);
+                        w4[e] = there ? pack_bf16x2(__uint_as_float(v[8 * g + 2 * e]) * mul,
+                                                    __uint_as_float(v[8 * g + 2 * e + 1]) * mul)
+                                      : 0u;
                     st_shared_v4(atom + sw128_off(row, (ch & 1) * 4 + g), w4[0], w4[1], w4[2], w4[3]);
                 }
             }
@@ -871,9 +953,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(epi_bar(h));
             if (wq == 0 && lane == 0 && wait_bar(epi_bar(h), 0, ctl) &&
-                FA_CHECK(kt * kBN < T && bh >= 0 && bh < p.BH, &g_status_bwd, abort_flag)) {
-                for (int a = 0; a < C::kAtomsD; ++a)
-                    tma_store_3d(h ? &tm_dv : &tm_dk, stage + a * (BM * 128), 64 * a, kt * kBN, bh);
+                FA_CHECK(kt * kBN < Tk && bh >= 0 && bh < p.BH, &g_status_bwd, abort_flag)) {
+                for (int a = 0; a < C::kAtomsD; ++a) {
+                    if constexpr (CROSS)
+                        tma_store_4d(h ? &tm_dv : &tm_dk, stage + a * (BM * 128), 64 * a, kt * kBN, bh % p.Hkv,
+                                     bh / p.Hkv);
+                    else
+                        tma_store_3d(h ? &tm_dv : &tm_dk, stage + a * (BM * 128), 64 * a, kt * kBN, bh);
+                }
                 bulk_commit();
                 bulk_wait0();
             }
@@ -913,7 +1000,7 @@ __device__ __forceinline__ void dq_item_at(int w, const BwdParams& p, int& bh, i
 }
 constexpr int kDqItemRing = 4;  // item numbers passed from the producer to the other roles
 
-template <int D, bool CAUSAL, bool VARLEN>
+template <int D, bool CAUSAL, bool VARLEN, bool CROSS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -958,6 +1045,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     struct Item {
         int bh, qt, bh_kv, n;
         int T, row0, head;  // its sequence: length, first packed row, head (VARLEN)
+        int Tk;             // its keys (T unless CROSS)
     };
     auto item = [&](int bh, int qt) {
         Item it;
@@ -968,7 +1056,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         it.T = span.T;
         it.row0 = span.row0;
         it.head = span.head;
-        it.n = it.qt * 128 < it.T ? fwd_num_kv_tiles(it.T, CAUSAL, it.qt) : 0;  // key tiles this query tile sees
+        it.Tk = CROSS ? keys_of(p.key_lengths, p.Tk, bh / p.Hq) : it.T;
+        // key tiles this query tile sees
+        it.n = it.qt * 128 < it.T ? (CROSS ? cdiv(it.Tk, kBN) : fwd_num_kv_tiles(it.T, CAUSAL, it.qt)) : 0;
         return it;
     };
     // TMA coordinates (y, z) of the 128-row tile starting at row r0 of grid row bhx of item it
@@ -1054,15 +1144,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 int qy, qz;
                 tile_yz(it, it.qt * 128, it.bh, qy, qz);
                 for (int a = 0; a < C::kAtomsD; ++a) {
-                    tma_load_3d_hint(sQ + a * 128 * 128, &tm_q, qdo_full, 64 * a, qy, qz, pol_q);
-                    tma_load_3d_hint(sdO + a * 128 * 128, &tm_do, qdo_full, 64 * a, qy, qz, pol_q);
+                    load_tile<CROSS>(sQ + a * 128 * 128, &tm_q, qdo_full, 64 * a, qy, qz, p.Hq, pol_q);
+                    load_tile<CROSS>(sdO + a * 128 * 128, &tm_do, qdo_full, 64 * a, qy, qz, p.Hq, pol_q);
                 }
                 bool fail = false;
                 for (int j = 0; j < it.n; ++j) {
                     {
                         const int st = kf % NKS;
                         if (!wait_bar(k_empty(st), ((kf / NKS) & 1) ^ 1, ctl) ||
-                            !FA_CHECK(j * kBN < it.T && st < NKS && C::kKOff + (st + 1) * C::kTileBytes <= C::kVOff,
+                            !FA_CHECK(j * kBN < it.Tk && st < NKS && C::kKOff + (st + 1) * C::kTileBytes <= C::kVOff,
                                       &g_status_bwd, abort_flag)) {
                             fail = true;
                             break;
@@ -1075,7 +1165,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                             int ky, kz;
                             tile_yz(it, j * kBN, it.bh_kv, ky, kz);
                             for (int a = 0; a < C::kAtomsD; ++a)
-                                tma_load_3d_hint(sK(st) + a * 128 * 128, &tm_k, k_full(st), 64 * a, ky, kz, pol_kv);
+                                load_tile<CROSS>(sK(st) + a * 128 * 128, &tm_k, k_full(st), 64 * a, ky, kz, p.Hkv,
+                                                 pol_kv);
                         }
                     }
                     {
@@ -1091,7 +1182,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         int vy, vz;
                         tile_yz(it, j * kBN, it.bh_kv, vy, vz);
                         for (int a = 0; a < C::kAtomsD; ++a)
-                            tma_load_3d_hint(sV(st) + a * 128 * 128, &tm_v, v_full(st), 64 * a, vy, vz, pol_kv);
+                            load_tile<CROSS>(sV(st) + a * 128 * 128, &tm_v, v_full(st), 64 * a, vy, vz, p.Hkv, pol_kv);
                     }
                 }
                 if (fail) break;
@@ -1115,10 +1206,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             constexpr uint32_t kTile16 = C::kTileBytes >> 4;
             uint32_t kc = 0, vc = 0, sc = 0, dsc = 0, qc = 0, item_no = 0;  // K, V, S, dS, Q/dO consumed so far
             // S number g = Q K_j^T into buffer g & 1: M = 128 queries, N = 128 keys, K = D (both K-major)
-            auto issue_s = [&](uint32_t kidx, uint32_t g) -> bool {
+            // `there`: the tile's keys; past them K and V are zeroed (past the tensor, TMA has done it)
+            auto issue_s = [&](uint32_t kidx, uint32_t g, int there) -> bool {
                 const int ks = kidx % NKS;
                 if (!wait_all(k_full(ks), (kidx / NKS) & 1, ctl)) return false;
                 tc_fence_after();
+                if (CROSS && there < kBN) zero_tail_rows(sK(ks), C::kAtomsD, there, lane);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
@@ -1128,10 +1221,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 return true;
             };
             // dP = dO V^T
-            auto issue_dp = [&](uint32_t vidx) -> bool {
+            auto issue_dp = [&](uint32_t vidx, int there) -> bool {
                 const int vs = vidx % NVS;
                 if (!wait_all(v_full(vs), (vidx / NVS) & 1, ctl)) return false;
                 tc_fence_after();
+                if (CROSS && there < kBN) zero_tail_rows(sV(vs), C::kAtomsD, there, lane);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
@@ -1161,14 +1255,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!wait_all(qdo_full, qc & 1, ctl)) goto mma_teardown;
                 ++qc;
                 tc_fence_after();
-                if (!issue_s(kc, sc)) goto mma_teardown;
-                if (!issue_dp(vc)) goto mma_teardown;
-                if (it.n > 1 && !issue_s(kc + 1, sc + 1)) goto mma_teardown;
+                auto keys_in = [&](int j) { return CROSS && it.Tk < p.Tk ? it.Tk - j * kBN : kBN; };
+                if (!issue_s(kc, sc, keys_in(0))) goto mma_teardown;
+                if (!issue_dp(vc, keys_in(0))) goto mma_teardown;
+                if (it.n > 1 && !issue_s(kc + 1, sc + 1, keys_in(1))) goto mma_teardown;
                 for (int j = 0; j < it.n; ++j) {
                     if (!wait_all(ds_full, dsc & 1, ctl)) goto mma_teardown;
                     ++dsc;
                     tc_fence_after();
-                    if (j + 1 < it.n && !issue_dp(vc + j + 1)) goto mma_teardown;
+                    if (j + 1 < it.n && !issue_dp(vc + j + 1, keys_in(j + 1))) goto mma_teardown;
                     if (j == it.n - 1 && leader) mma_commit(qdo_empty);  // every S and dP of the item is issued
                     if (j == 0) {
                         // the previous item's dQ must have left TMEM
@@ -1181,7 +1276,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         if (leader) mma_ts_d(tmem + C::kDQ, tmem + C::kS(b) + C::kDSCol + s * 8, dK_mn,
                                  ks * kTile16 + s * (2048 >> 4), C::kIdescDQ, (j > 0 || s > 0) ? 1u : 0u);
                     if (leader) mma_commit(k_empty(ks));
-                    if (j + 2 < it.n && !issue_s(kc + j + 2, sc + j + 2)) goto mma_teardown;
+                    if (j + 2 < it.n && !issue_s(kc + j + 2, sc + j + 2, keys_in(j + 2))) goto mma_teardown;
                 }
                 if (leader) mma_commit(dq_full);
                 kc += it.n;
@@ -1226,7 +1321,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint64_t nlse2 = f2(nlse, nlse), nd2 = f2(nd, nd);
             for (int j = 0; j < it.n; ++j) {
                 const uint32_t g = sc + j, b = g & 1;
-                const bool masked = bwd_tile_class(it.T, CAUSAL, 128, it.qt, j) == kMasked;
+                const bool masked = CROSS ? it.qt * 128 + 128 > it.T || (j + 1) * kBN > it.Tk
+                                          : bwd_tile_class(it.T, CAUSAL, 128, it.qt, j) == kMasked;
                 if (!warp_wait<false>(s_full(b), (g >> 1) & 1, ctl)) goto compute_done;
                 tc_fence_after();
                 uint32_t sr[64];
@@ -1252,7 +1348,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const int key0 = j * kBN + 64 * h;
 #pragma unroll
                     for (int e = 0; e < 64; ++e)
-                        if (!bwd_elem_visible(it.T, CAUSAL, q, key0 + e)) pf[e] = 0.f;
+                        if (CROSS ? q >= it.T || key0 + e >= it.Tk : !bwd_elem_visible(it.T, CAUSAL, q, key0 + e))
+                            pf[e] = 0.f;
                 }
                 if (!warp_wait<false>(dp_full, (vc + j) & 1, ctl)) goto compute_done;
                 tc_fence_after();
@@ -1299,7 +1396,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (q < it.T) {
                     const size_t drow = VARLEN ? static_cast<size_t>(it.row0 + q) * p.Hq + it.head
                                                : static_cast<size_t>(it.bh) * T + q;
-                    uint4* dst = reinterpret_cast<uint4*>(p.dq + drow * D + h * kCols);
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        (CROSS ? row_of(p.dq_cross, it.bh / p.Hq, it.bh % p.Hq, q) : p.dq + drow * D) + h * kCols);
 #pragma unroll
                     for (int g = 0; g < kCols / 8; ++g) {
                         uint4 o;
@@ -1327,27 +1425,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
 }
 
-template <typename K>
-bool set_smem_once(K kern, int bytes, bool& done) {
-    if (!done) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-            return false;
-        done = true;
-    }
-    return true;
-}
-
 // The fused backward (D = 64): one dK/dV grid that also adds every query
 // tile's dQ contribution into the fp32 accumulator (zeroed by the
 // preprocess kernel), then the conversion of the accumulator to bf16 dQ.
-template <bool CAUSAL>
+template <bool CAUSAL, bool CROSS = false>
 int launch_fused_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                    const CUtensorMap& tdk, const CUtensorMap& tdv, const CUtensorMap& tacc, BwdParams p, int BHq,
                    int BHkv, const float* acc, cudaStream_t st, const DebugKnobs& dbg, int num_sms) {
     constexpr int D = 64;
-    static bool attr = false;
-    auto ka = fa_bwd_dkdv_kernel<D, CAUSAL, false, true>;
-    if (!set_smem_once(ka, DkvCfg<D, true>::kSmemBytes, attr)) return -5;
+    static std::atomic<unsigned long long> allowed{0};
+    auto ka = fa_bwd_dkdv_kernel<D, CAUSAL, false, true, CROSS>;
+    if (!allow_shared_memory(ka, DkvCfg<D, true>::kSmemBytes, allowed)) return -5;
     if (dbg.ev[2]) cudaEventRecord(dbg.ev[2], st);
     p.BH = BHkv;
     p.kt_major = (p.n_kt * BHkv < 8 * num_sms) ? 1 : 0;
@@ -1357,20 +1445,21 @@ int launch_fused_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     const long long groups = static_cast<long long>(BHq) * p.T * (D / 8);
     const long long blocks = (groups + 255) / 256;
     const int grid = static_cast<int>(blocks < 8LL * num_sms ? blocks : 8LL * num_sms);
-    fa_bwd_dq_convert_kernel<D><<<grid, 256, 0, st>>>(acc, p.dq, BHq, p.T, p.T_pad, p.scale);
+    fa_bwd_dq_convert_kernel<D, CROSS><<<grid, 256, 0, st>>>(acc, p.dq, BHq, p.T, p.T_pad, p.scale, p.Hq, p.dq_cross);
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (dbg.ev[4]) cudaEventRecord(dbg.ev[4], st);
     return 0;
 }
 
-template <int D, bool CAUSAL, bool VARLEN>
+template <int D, bool CAUSAL, bool VARLEN, bool CROSS = false>
 int launch_main_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                   const CUtensorMap& tdk, const CUtensorMap& tdv, BwdParams p, int BHq, int BHkv, cudaStream_t st,
                   const DebugKnobs& dbg, int num_sms) {
-    static bool attr_a = false, attr_b = false;
-    auto ka = fa_bwd_dkdv_kernel<D, CAUSAL, VARLEN>;
-    auto kb = fa_bwd_dq_kernel<D, CAUSAL, VARLEN>;
-    if (!set_smem_once(ka, DkvCfg<D>::kSmemBytes, attr_a) || !set_smem_once(kb, DqCfg<D>::kSmemBytes, attr_b))
+    static std::atomic<unsigned long long> allowed_a{0}, allowed_b{0};
+    auto ka = fa_bwd_dkdv_kernel<D, CAUSAL, VARLEN, false, CROSS>;
+    auto kb = fa_bwd_dq_kernel<D, CAUSAL, VARLEN, CROSS>;
+    if (!allow_shared_memory(ka, DkvCfg<D>::kSmemBytes, allowed_a) ||
+        !allow_shared_memory(kb, DqCfg<D>::kSmemBytes, allowed_b))
         return -5;
     if (dbg.ev[2]) cudaEventRecord(dbg.ev[2], st);
     p.BH = BHkv;
@@ -1382,6 +1471,7 @@ int launch_main_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (dbg.ev[3]) cudaEventRecord(dbg.ev[3], st);
     p.BH = BHq;
+    if (CROSS) p.n_kt = cdiv(p.T, 128);  // query tiles
     p.n_items = p.n_kt * BHq;
     const int grid_b = p.n_items < num_sms ? p.n_items : num_sms;  // persistent: one CTA per SM
     {
@@ -1430,13 +1520,13 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const vo
     if (D == 64)
         fa_bwd_pre_kernel<64, false><<<pre_grid, 256, 0, stream>>>(
             static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, dvec, lse2, BH, T, T_pad,
-            dq_next, nullptr, 1, Hq, 0, dqacc);
+            dq_next, nullptr, 1, Hq, 0, dqacc, {});
     else
         fa_bwd_pre_kernel<128, false><<<pre_grid, 256, 0, stream>>>(
             static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, dvec, lse2, BH, T, T_pad,
-            dq_next, nullptr, 1, Hq, 0, nullptr);
+            dq_next, nullptr, 1, Hq, 0, nullptr, {});
     if (cudaGetLastError() != cudaSuccess) return -5;
-    BwdParams p;
+    BwdParams p{};
     p.lse2 = lse2;
     p.dvec = dvec;
     p.dq_next = dq_next;
@@ -1496,13 +1586,13 @@ int run_bwd_varlen(const void* q, const void* k, const void* v, const void* o, c
     if (D == 64)
         fa_bwd_pre_kernel<64, true><<<pre_grid, 256, 0, stream>>>(
             static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, dvec, lse2, BH,
-            max_seqlen, T_pad, dq_next, cu_seqlens, n_seq, H, total, nullptr);
+            max_seqlen, T_pad, dq_next, cu_seqlens, n_seq, H, total, nullptr, {});
     else
         fa_bwd_pre_kernel<128, true><<<pre_grid, 256, 0, stream>>>(
             static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), lse, dvec, lse2, BH,
-            max_seqlen, T_pad, dq_next, cu_seqlens, n_seq, H, total, nullptr);
+            max_seqlen, T_pad, dq_next, cu_seqlens, n_seq, H, total, nullptr, {});
     if (cudaGetLastError() != cudaSuccess) return -5;
-    BwdParams p;
+    BwdParams p{};
     p.lse2 = lse2;
     p.dvec = dvec;
     p.dq_next = dq_next;
@@ -1596,6 +1686,73 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* o, const
                      num_sms);
     if (cudaFreeAsync(ws, stream) != cudaSuccess && rc == 0) rc = -5;
     return rc;
+}
+
+// ---------------------------------------------------------------- cross attention
+size_t cross_bwd_workspace(const CrossShape& s, bool deterministic, int num_sms) {
+    DebugKnobs k{};
+    k.deterministic = deterministic ? 1 : 0;
+    return bwd_workspace_bytes(s.B, s.Hq, s.Tq, s.D, bwd_fuses(s.D, cdiv(s.Tk, kBN), s.B * s.Hkv, num_sms, k));
+}
+
+int launch_cross_bwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
+                     const CrossTensor& o, const void* o_rest, const CrossTensor& dO, const float* lse, const CrossTensor& dq,
+                     const CrossTensor& dk, const CrossTensor& dv, float scale, void* ws, cudaStream_t stream,
+                     const DebugKnobs& dbg, int num_sms) {
+    const int BH = s.B * s.Hq, BHkv = s.B * s.Hkv, D = s.D;
+    const bool fuse = bwd_fuses(D, cdiv(s.Tk, kBN), BHkv, num_sms, dbg);
+    const int T_pad = cdiv(s.Tq, 128) * 128;
+    const size_t bytes_vec = (static_cast<size_t>(BH) * T_pad * 4 + 255) / 256 * 256;
+    float* dvec = static_cast<float*>(ws);
+    float* lse2 = reinterpret_cast<float*>(static_cast<char*>(ws) + bytes_vec);
+    int* dq_next = reinterpret_cast<int*>(static_cast<char*>(ws) + 2 * bytes_vec);
+    float* dqacc = fuse ? reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * bytes_vec + 256) : nullptr;
+    CUtensorMap tq, tk, tv, tdo, tdk, tdv, tacc;
+    auto map = [&](CUtensorMap* m, const CrossTensor& x, int heads, int T) {
+        return make_tmap_strided(m, {x.ptr, x.b, x.h, x.t}, s.B, heads, T, D, 128);
+    };
+    if (!map(&tq, q, s.Hq, s.Tq) || !map(&tk, k, s.Hkv, s.Tk) || !map(&tv, v, s.Hkv, s.Tk) ||
+        !map(&tdo, dO, s.Hq, s.Tq) || !map(&tdk, dk, s.Hkv, s.Tk) || !map(&tdv, dv, s.Hkv, s.Tk))
+        return -5;
+    if (fuse && !make_tmap_f32_acc(&tacc, dqacc, BH, T_pad, D, 32)) return -5;
+    const long long blocks = (static_cast<long long>(BH) * T_pad * (D / 8) + 255) / 256;
+    const int pre_grid = static_cast<int>(blocks < 8LL * num_sms ? blocks : 8LL * num_sms);
+    PreCross x{o, dO, dq, static_cast<const __nv_bfloat16*>(o_rest), s.key_lengths, s.Tk};
+    if (fuse) x.dq.ptr = nullptr;  // the accumulator of a sequence without keys stays 0
+    auto pre = D == 64 ? fa_bwd_pre_kernel<64, false, true> : fa_bwd_pre_kernel<128, false, true>;
+    pre<<<pre_grid, 256, 0, stream>>>(nullptr, nullptr, lse, dvec, lse2, BH, s.Tq, T_pad, dq_next, nullptr, 1, s.Hq, 0,
+                                      dqacc, x);
+    if (cudaGetLastError() != cudaSuccess) return -5;
+    BwdParams p{};
+    p.lse2 = lse2;
+    p.dvec = dvec;
+    p.dq_next = dq_next;
+    p.T = s.Tq;
+    p.T_pad = T_pad;
+    p.Tk = s.Tk;
+    p.key_lengths = s.key_lengths;
+    p.dq_cross = dq;
+    p.dk_cross = dk;
+    p.dv_cross = dv;
+    p.n_kt = cdiv(s.Tk, kBN);
+    p.BH = BHkv;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.group = s.Hq / s.Hkv;
+    p.scale = scale;
+    p.sl2 = scale * kLog2e;
+    p.prescale = p.sl2 > 0.f ? 0 : 1;
+    p.sl2_eff = p.prescale ? 1.f : p.sl2;
+    p.timeout_ns = dbg.timeout_ns;
+    p.inject = dbg.inject;
+    p.n_seq = 1;
+    DebugKnobs quiet = dbg;  // the timing events belong to fa_bwd
+    for (cudaEvent_t& e : quiet.ev) e = nullptr;
+    if (fuse)
+        return launch_fused_t<false, true>(tq, tk, tv, tdo, tdk, tdv, tacc, p, BH, BHkv, dqacc, stream, quiet, num_sms);
+    return D == 64 ? launch_main_t<64, false, false, true>(tq, tk, tv, tdo, tdk, tdv, p, BH, BHkv, stream, quiet, num_sms)
+                   : launch_main_t<128, false, false, true>(tq, tk, tv, tdo, tdk, tdv, p, BH, BHkv, stream, quiet,
+                                                            num_sms);
 }
 
 // ---------------------------------------------------------------- fixed scratch

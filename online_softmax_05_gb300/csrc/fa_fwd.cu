@@ -79,6 +79,12 @@ struct FwdParams {
     const int* cu_seqlens;
     int n_seq, total;
     __nv_bfloat16* o_packed;  // O of the packed layout (stored row by row, not by TMA)
+    // Cross attention: Tk keys a sequence, key_lengths[b] (null: all) of them there; T above is
+    // the number of queries.  The tensor maps are {D, T, heads, B}.
+    int Tk;
+    const int* key_lengths;
+    CrossTensor o_cross;  // O by its strides (rows of sequences without keys are zeroed in place)
+    __nv_bfloat16* o_rest;  // what O's rounding took off, contiguous (B, Hq, Tq, D), or null
     int head_pairs;       // 1: the two query tiles of an item are two heads of one group at the same rows
     int n_tiles;          // query tiles per head
     int single_tiles;     // 1: an item is one query tile whose key tiles the two softmax warpgroups split
@@ -149,14 +155,15 @@ struct FwdItem {
     int bh[2];    // head coordinate of each half's Q / O rows in the tensor maps
     int bh_kv;    // head coordinate of the K/V rows
     int T;        // length of this item's sequence
+    int Tk;       // keys of this item's sequence (T unless cross attention)
     int row0;     // row coordinate of the sequence's first token (0 unless packed)
     bool valid0;  // the first half has rows < T (false: skip the item)
     bool valid1;  // the second half has rows < T
 };
-template <bool VARLEN>
+template <bool VARLEN, bool CROSS>
 __device__ __forceinline__ FwdItem fwd_item(int w, const FwdParams& p) {
     FwdItem it;
-    it.T = p.T;
+    it.T = it.Tk = p.T;
     it.row0 = 0;
     it.valid0 = true;
     if constexpr (VARLEN) {
@@ -177,6 +184,7 @@ __device__ __forceinline__ FwdItem fwd_item(int w, const FwdParams& p) {
             atomicCAS(&g_status_fwd, 0, kStatusBadSeqlen);
             it.T = 0;
         }
+        it.Tk = it.T;
         it.valid0 = it.tile[0] * kFwdBM < it.T;
         it.valid1 = it.tile[1] * kFwdBM < it.T;
         return it;
@@ -208,7 +216,30 @@ __device__ __forceinline__ FwdItem fwd_item(int w, const FwdParams& p) {
         it.bh_kv = (bh / p.Hq) * p.Hkv + (bh % p.Hq) / p.group;
         it.valid1 = it.tile[1] * kFwdBM < p.T;
     }
+    if constexpr (CROSS) {
+        it.Tk = p.key_lengths != nullptr ? __ldg(p.key_lengths + it.bh[0] / p.Hq) : p.Tk;
+        if (it.Tk < 0 || it.Tk > p.Tk) {
+            atomicCAS(&g_status_fwd, 0, kStatusBadSeqlen);
+            it.Tk = 0;
+        }
+        it.valid0 = it.Tk > 0;  // without keys there is nothing to load or multiply
+    }
     return it;
+}
+
+// Key tiles of one half of an item, and whether the last of them has keys to be masked.
+template <bool CAUSAL, bool CROSS>
+__device__ __forceinline__ int num_kv_tiles(const FwdItem& it, int half) {
+    return CROSS ? cdiv(it.Tk, kBN) : fwd_num_kv_tiles(it.T, CAUSAL, it.tile[half]);
+}
+// Copies 64 columns of a 128-row tile from its row and head, in the order of the layout's tensor map.
+template <bool VARLEN, bool CROSS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int row, int bh,
+                                          int heads, uint64_t policy) {
+    if constexpr (CROSS)
+        tma_load_4d_hint(dst, map, bar, col, row, bh % heads, bh / heads, policy);
+    else
+        tma_load_3d_hint(dst, map, bar, col, VARLEN ? bh : row, VARLEN ? row : bh, policy);
 }
 
 // Item k of this CTA in snake order over items sorted heaviest first
@@ -222,7 +253,9 @@ __device__ __forceinline__ int item_of(int k, int n_items) {
 // SPLIT: every item is one query tile whose key tiles the two softmax
 // warpgroups split (launched when the items are too few to fill the SMs);
 // compiled apart so the paired kernel carries none of it.
-template <int D, bool CAUSAL, bool VARLEN, bool SPLIT>
+// CROSS: queries and keys of different sequences; keys past a sequence's length are
+// masked, and their V rows zeroed in shared memory, as 0 x NaN would reach O.
+template <int D, bool CAUSAL, bool VARLEN, bool SPLIT, bool CROSS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, FwdParams p) {
@@ -295,11 +328,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int k = 0;; ++k) {
                 int w = item_of(k, p.n_items);
                 if (w < 0) break;
-                const FwdItem item = fwd_item<VARLEN>(w, p);
+                const FwdItem item = fwd_item<VARLEN, CROSS>(w, p);
                 if (!item.valid0) continue;
                 const bool valid1 = item.valid1;
-                const int n0 = fwd_num_kv_tiles(item.T, CAUSAL, item.tile[0]);
-                const int n1 = valid1 ? fwd_num_kv_tiles(item.T, CAUSAL, item.tile[1]) : 0;
+                const int n0 = num_kv_tiles<CAUSAL, CROSS>(item, 0);
+                const int n1 = valid1 ? num_kv_tiles<CAUSAL, CROSS>(item, 1) : 0;
                 const int nmax = n0 > n1 ? n0 : n1;
                 const int bh = item.bh_kv;
                 for (int t = 0; t < 2; ++t) {
@@ -315,8 +348,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mbar_arrive_expect_tx(q_full(t), C::kTileBytes);
                     ++q_armed[t];
                     for (int a = 0; a < C::kAtoms; ++a)
-                        tma_load_3d_hint(sQ[t] + a * C::kAtomBytes, &tm_q, q_full(t), 64 * a,
-                                         VARLEN ? item.bh[t] : qrow, VARLEN ? qrow : item.bh[t], pol_q);
+                        load_tile<VARLEN, CROSS>(sQ[t] + a * C::kAtomBytes, &tm_q, q_full(t), 64 * a, qrow,
+                                                 item.bh[t], p.Hq, pol_q);
                 }
                 // one K (kind 0) or V (kind 1) tile into the next ring stage
                 auto fill = [&](int kind, int jt) -> bool {
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int krow = item.row0 + jt * kBN;
                     // the key tile is one this query tile needs, inside the tensor, and its ring
                     // stage lies inside the shared-memory window
-                    if (!FA_CHECK(jt * kBN < item.T && bh >= 0 && bh < p.BH / p.group &&
+                    if (!FA_CHECK(jt * kBN < item.Tk && bh >= 0 && bh < p.BH / p.group &&
                                       C::kKVOff + (slot + 1) * C::kTileBytes <= C::kBarOff,
                                   &g_status_fwd, abort_flag)) {
                         --kv_cnt;  // nothing was armed: the drain must not wait for this fill
@@ -340,8 +373,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mbar_arrive_expect_tx(kv_full(slot), C::kTileBytes);
                     const CUtensorMap* tm = kind ? &tm_v : &tm_k;
                     for (int a = 0; a < C::kAtoms; ++a)
-                        tma_load_3d_hint(sKV + slot * C::kTileBytes + a * C::kAtomBytes, tm, kv_full(slot), 64 * a,
-                                         VARLEN ? bh : krow, VARLEN ? krow : bh, pol_kv);
+                        load_tile<VARLEN, CROSS>(sKV + slot * C::kTileBytes + a * C::kAtomBytes, tm, kv_full(slot),
+                                                 64 * a, krow, bh, p.Hkv, pol_kv);
                     return true;
                 };
                 if constexpr (SPLIT) {
@@ -409,14 +442,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (leader) mma_ts_d(tmem + C::kO(t), tmem + C::kS(t) + s * 8, dKV_mn, vo + s * (2048 >> 4), C::kIdescPV,
                              (acc || s > 0) ? 1u : 0u);
             };
+            // V tile jt of an item: what lies past its keys must not meet P = 0 as NaN or infinity
+            // (past the tensor TMA has filled zeros)
+            auto clean_v = [&](const FwdItem& item, int jt, uint32_t slot) {
+                if constexpr (CROSS) {
+                    const int left = item.Tk - jt * kBN;
+                    if (left < kBN && item.Tk < p.Tk) zero_tail_rows(sKV + slot * C::kTileBytes, C::kAtoms, left, lane);
+                }
+            };
             for (int k = 0;; ++k) {
                 int w = item_of(k, p.n_items);
                 if (w < 0) break;
-                const FwdItem item = fwd_item<VARLEN>(w, p);
+                const FwdItem item = fwd_item<VARLEN, CROSS>(w, p);
                 if (!item.valid0) continue;
                 const bool valid1 = item.valid1;
-                const int n0 = fwd_num_kv_tiles(item.T, CAUSAL, item.tile[0]);
-                const int n1 = valid1 ? fwd_num_kv_tiles(item.T, CAUSAL, item.tile[1]) : 0;
+                const int n0 = num_kv_tiles<CAUSAL, CROSS>(item, 0);
+                const int n1 = valid1 ? num_kv_tiles<CAUSAL, CROSS>(item, 1) : 0;
                 const int nmax = n0 > n1 ? n0 : n1;
                 if (!wait_all(q_full(0), q_cnt[0] & 1, ctl)) goto mma_done_label;
                 ++q_cnt[0];
@@ -451,6 +492,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             if (j >= cnt[t]) continue;
                             uint32_t vs;
                             if (!next_slot(vs)) goto mma_done_label;
+                            clean_v(item, t ? h + j : j, vs);
                             if (!wait_all(ph_full(t), p_cnt[t] & 1, ctl)) goto mma_done_label;
                             tc_fence_after();
                             issue_pv_half(t, vs, j > 0, 0);
@@ -492,6 +534,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (!wait_all(kv_full(vs), (kv_cnt / C::kStages) & 1, ctl)) goto mma_done_label;
                     ++kv_cnt;
                     tc_fence_after();
+                    clean_v(item, j, vs);
                     const bool has_next = j + 1 < nmax;
                     const uint32_t ks = kv_cnt % C::kStages;
                     bool k_ready = false;
@@ -553,11 +596,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int k = 0;; ++k) {
             int w = item_of(k, p.n_items);
             if (w < 0) break;
-            const FwdItem item = fwd_item<VARLEN>(w, p);
+            const FwdItem item = fwd_item<VARLEN, CROSS>(w, p);
             const int tile = item.tile[t], bh = item.bh[t], T = item.T;
             if (tile * kFwdBM >= T) continue;  // the second tile of an item may be empty (or the whole item)
             const int row = tile * kFwdBM + r_local;  // row within the sequence
-            const int n_all = fwd_num_kv_tiles(T, CAUSAL, tile);
+            const int n_all = num_kv_tiles<CAUSAL, CROSS>(item, t);
+            if constexpr (CROSS) {
+                if (n_all == 0) {  // no keys: outputs of 0, and the log of an empty sum
+                    if (row < T && (!SPLIT || t == 0)) {
+                        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o_cross.ptr) +
+                                                             bh / p.Hq * p.o_cross.b + bh % p.Hq * p.o_cross.h +
+                                                             row * p.o_cross.t);
+                        for (int c = 0; c < D / 8; ++c) to[c] = make_uint4(0, 0, 0, 0);
+                        if (p.o_rest != nullptr) {
+                            to = reinterpret_cast<uint4*>(p.o_rest + (static_cast<size_t>(bh) * T + row) * D);
+                            for (int c = 0; c < D / 8; ++c) to[c] = make_uint4(0, 0, 0, 0);
+                        }
+                        p.lse[static_cast<size_t>(bh) * T + row] = -INFINITY;
+                    }
+                    continue;
+                }
+            }
             // split item: this warpgroup's share of the key tiles (the first half, rounded up,
             // for warpgroup 0); otherwise all of them
             const int h_split = (n_all + 1) / 2;
@@ -584,11 +643,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         f2_split(v, s[2 * c], s[2 * c + 1]);
                     }
                 }
-                if (fwd_tile_class(T, CAUSAL, tile, j) == kMasked) {
+                if (CROSS ? (j + 1) * kBN > item.Tk : fwd_tile_class(T, CAUSAL, tile, j) == kMasked) {
                     const int key0 = j * kBN;
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
-                        if (!elem_visible(T, CAUSAL, row, key0 + c)) s[c] = -INFINITY;
+                        if (CROSS ? key0 + c >= item.Tk : !elem_visible(T, CAUSAL, row, key0 + c)) s[c] = -INFINITY;
                 }
                 // row max: 8 independent chains of 3-input max, then a small tree
                 float mx8[8];
@@ -771,6 +830,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             w4[e] = pack_bf16x2(__uint_as_float(orr[8 * q4 + 2 * e]) * inv,
                                                 __uint_as_float(orr[8 * q4 + 2 * e + 1]) * inv);
                         st_shared_v4(atom + sw128_off(r_local, chunk), w4[0], w4[1], w4[2], w4[3]);
+                        if constexpr (CROSS) {
+                            if (p.o_rest != nullptr && row < T) {
+                                uint32_t r4[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    r4[e] = pack_bf16x2(
+                                        fmaf(__uint_as_float(orr[8 * q4 + 2 * e]), inv, -__uint_as_float(w4[e] << 16)),
+                                        fmaf(__uint_as_float(orr[8 * q4 + 2 * e + 1]), inv,
+                                             -__uint_as_float(w4[e] & 0xffff0000u)));
+                                reinterpret_cast<uint4*>(p.o_rest + (static_cast<size_t>(bh) * T + row) * D + col0)[q4] =
+                                    make_uint4(r4[0], r4[1], r4[2], r4[3]);
+                            }
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -781,8 +853,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (wq == 0 && lane == 0) {
                     if (wait_bar(epi_bar(t), epi_cnt & 1, ctl) &&
                         FA_CHECK(tile * kFwdBM < T && bh >= 0 && bh < p.BH, &g_status_fwd, abort_flag)) {
-                        for (int a = 0; a < C::kAtoms; ++a)
-                            tma_store_3d(&tm_o, sQ[t] + a * C::kAtomBytes, 64 * a, tile * kFwdBM, bh);
+                        for (int a = 0; a < C::kAtoms; ++a) {
+                            if constexpr (CROSS)
+                                tma_store_4d(&tm_o, sQ[t] + a * C::kAtomBytes, 64 * a, tile * kFwdBM, bh % p.Hq,
+                                             bh / p.Hq);
+                            else
+                                tma_store_3d(&tm_o, sQ[t] + a * C::kAtomBytes, 64 * a, tile * kFwdBM, bh);
+                        }
                         bulk_commit();
                         bulk_wait_read0();
                     }
@@ -805,17 +882,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
 }
 
-template <int D, bool CAUSAL, bool VARLEN = false, bool SPLIT = false>
+template <int D, bool CAUSAL, bool VARLEN = false, bool SPLIT = false, bool CROSS = false>
 int launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                  const FwdParams& p, int grid, cudaStream_t st) {
-    static bool attr_set = false;
-    auto kern = fa_fwd_kernel<D, CAUSAL, VARLEN, SPLIT>;
-    if (!attr_set) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::kSmemBytes) !=
-            cudaSuccess)
-            return -5;
-        attr_set = true;
-    }
+    static std::atomic<unsigned long long> allowed{0};
+    auto kern = fa_fwd_kernel<D, CAUSAL, VARLEN, SPLIT, CROSS>;
+    if (!allow_shared_memory(kern, FwdCfg<D>::kSmemBytes, allowed)) return -5;
     kern<<<grid, kFwdThreads, FwdCfg<D>::kSmemBytes, st>>>(tq, tk, tv, to, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
@@ -914,6 +986,48 @@ int launch_fwd_varlen(const void* q, const void* k, const void* v, void* o, floa
                       : launch_fwd_t<64, false, true>(tq, tk, tv, tq, p, grid, stream);
     return causal ? launch_fwd_t<128, true, true>(tq, tk, tv, tq, p, grid, stream)
                   : launch_fwd_t<128, false, true>(tq, tk, tv, tq, p, grid, stream);
+}
+
+int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
+                     const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
+                     const DebugKnobs& dbg, int num_sms) {
+    CUtensorMap tq, tk, tv, to;
+    if (!make_tmap_strided(&tq, {q.ptr, q.b, q.h, q.t}, s.B, s.Hq, s.Tq, s.D, 128) ||
+        !make_tmap_strided(&tk, {k.ptr, k.b, k.h, k.t}, s.B, s.Hkv, s.Tk, s.D, 128) ||
+        !make_tmap_strided(&tv, {v.ptr, v.b, v.h, v.t}, s.B, s.Hkv, s.Tk, s.D, 128) ||
+        !make_tmap_strided(&to, {o.ptr, o.b, o.h, o.t}, s.B, s.Hq, s.Tq, s.D, 128))
+        return -5;
+    FwdParams p{};
+    p.lse = lse;
+    p.T = s.Tq;
+    p.Tk = s.Tk;
+    p.key_lengths = s.key_lengths;
+    p.o_cross = o;
+    p.o_rest = static_cast<__nv_bfloat16*>(o_rest);
+    p.BH = s.B * s.Hq;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.group = s.Hq / s.Hkv;
+    p.n_tiles = cdiv(s.Tq, kFwdBM);
+    p.n_pairs = cdiv(s.Tq, 2 * kFwdBM);
+    p.head_pairs = p.group % 2 == 0 ? 1 : 0;
+    p.n_items = p.head_pairs ? p.n_tiles * (p.BH / 2) : p.n_pairs * p.BH;
+    p.single_tiles = 2LL * p.n_items <= num_sms ? 1 : 0;  // as in launch_fwd
+    if (p.single_tiles) p.n_items = p.n_tiles * p.BH;
+    p.head_major = 1;
+    p.n_seq = s.B;
+    p.total = s.B * s.Tq;
+    p.sl2 = scale * kLog2e;
+    p.prescale = p.sl2 > 0.f ? 0 : 1;
+    p.sl2_eff = p.prescale ? 1.f : p.sl2;
+    p.timeout_ns = dbg.timeout_ns;
+    p.inject = dbg.inject;
+    const int grid = p.n_items < num_sms ? p.n_items : num_sms;
+    if (p.single_tiles)
+        return s.D == 64 ? launch_fwd_t<64, false, false, true, true>(tq, tk, tv, to, p, grid, stream)
+                         : launch_fwd_t<128, false, false, true, true>(tq, tk, tv, to, p, grid, stream);
+    return s.D == 64 ? launch_fwd_t<64, false, false, false, true>(tq, tk, tv, to, p, grid, stream)
+                     : launch_fwd_t<128, false, false, false, true>(tq, tk, tv, to, p, grid, stream);
 }
 
 int fwd_take_status() {

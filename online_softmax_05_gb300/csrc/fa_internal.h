@@ -44,6 +44,25 @@ int launch_bwd_varlen(const void* q, const void* k, const void* v, const void* o
 int launch_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Tq, int Tk,
                   int D, float scale, cudaStream_t stream, int num_sms);
 
+// Cross attention: Tq queries over Tk keys, key_lengths[b] (null: Tk) of them there, (B, heads, T, D)
+// tensors by their strides in elements.
+struct CrossShape {
+    int B, Hq, Hkv, Tq, Tk, D;
+    const int* key_lengths;
+};
+struct CrossTensor {
+    void* ptr;
+    long long b, h, t;
+};
+int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
+                     const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
+                     const DebugKnobs& dbg, int num_sms);
+size_t cross_bwd_workspace(const CrossShape& s, bool deterministic, int num_sms);
+int launch_cross_bwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
+                     const CrossTensor& o, const void* o_rest, const CrossTensor& dO, const float* lse, const CrossTensor& dq,
+                     const CrossTensor& dk, const CrossTensor& dv, float scale, void* workspace, cudaStream_t stream,
+                     const DebugKnobs& dbg, int num_sms);
+
 // Backward with the library's fixed device scratch buffer instead of an
 // allocation; returns -10 if the problem does not fit, without launching.
 size_t bwd_scratch_bytes(int B, int H, int T, int D);
