@@ -409,6 +409,56 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
                   long long workspace_bytes, void* stream);
 
 /*
+ * Attention of a tree of drafted tokens over the 4-bit cache.  The last N slots of each
+ * sequence (cache->lengths counts them) are the tree's places, written by
+ * fa_kv4_append as any tokens.  Place i sees the context before the tree, its
+ * ancestors and itself.
+ *   q       in: (B, Hq, N, D) bf16, 1 <= N <= FA_TREE_MAX_PLACES; query head h reads
+ *               key/value head h / (Hq / Hkv)
+ *   parents in: DEVICE int32 [B][N]: the place of i's parent, below i, or -1 behind the
+ *               context.  Any other value marks a place without a token: it, and what
+ *               hangs on it, sees nothing and is seen by no other.
+ *   o      out: (B, Hq, N, D) bf16;  lse out: (B, Hq, N) float32
+ * A place without a token, or a sequence of length 0, gives o = 0 and lse = -infinity.
+ * A length between 0 and N is recorded as FA_ERR_SEQLEN and counts as 0.  What a place does not
+ * see does not touch its result, whatever the cache holds there.  Scores, sums and the
+ * softmax are float32 and keys are exact; weights and values go into their product as
+ * bf16, each rounded once.  No workspace.
+ */
+#define FA_TREE_MAX_PLACES 64
+int fa_kv4_tree(const fa_kv4_cache* cache, const void* q, const int* parents, void* o, float* lse, int Hq, int N,
+                float scale, void* stream);
+
+/*
+ * Which of a tree's tokens stand: place i does if it and every place on its way from a root
+ * holds what the model picked behind the place before it (picks[b][parent], and for a root
+ * first[b], the pick behind the context; first NULL: every root stands).  Kept is the way
+ * to the deepest place that stands, to the lowest of equally deep ones.
+ *   parents         in: DEVICE int32 [B][N], as in fa_kv4_tree
+ *   tokens, picks   in: DEVICE int32 (int64 if tokens_64) [B][N]; first [B] or NULL
+ *   path           out: int32 [B][N], the places on the way from the root on, -1 behind them
+ *   counts         out: int32 [B], how many
+ *   next           out: int32 / int64 [B], the pick behind the last of them (first[b], or -1
+ *                       without first, where none stands)
+ */
+int fa_tree_accept(const int* parents, const void* tokens, const void* picks, const void* first, int tokens_64, int B,
+                   int N, int* path, int* counts, void* next, void* stream);
+
+/*
+ * Keeps a path of the tree's places in the cache: token path[b][i] of the last N slots moves
+ * to slot length - N + i, in every key/value head, and the rest is dropped.
+ *   path        in: DEVICE int32 [B][N], rising places, up to the first -1
+ *   lengths_out out: int32[B], length - N + the path's length; use it from then on
+ *                    (cache->lengths is not changed); 0 for a sequence of length 0
+ *   weights, slot_positions: float32 / int32 [B][Hkv][slots] or NULL: moved alike, in place
+ * A path that does not rise or leaves the N places, a length between 0 and N or one that the
+ * table or the accounts cannot hold is recorded as FA_ERR_SEQLEN: that sequence and its length stay as
+ * they are.  The pages of the last N slots must be the sequence's own.
+ */
+int fa_kv4_keep(const fa_kv4_cache* cache, const int* path, int N, int* lengths_out, float* weights, int* slot_positions,
+                long long slots, void* stream);
+
+/*
  * Evicts down to `budget` tokens per sequence, for each key/value head by
  * itself.  Kept are the `recent` newest tokens (positions above the newest
  * minus recent) and the ones with the largest weights, ties to the lowest slot;

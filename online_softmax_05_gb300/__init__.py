@@ -16,7 +16,7 @@ __all__ = ["fa_fwd", "fa_bwd", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_varlen", "att
            "attention_forward", "attention_backward", "FAError", "library_path", "load_library",
            "FlashAttention", "flash_attention", "rope", "rotary_frequencies", "rotary_amplitude", "kv4_pool", "kv4_append",
            "kv4_read", "attention_decode_kv4", "kv4_evict", "attention_forward_cross", "attention_backward_cross",
-           "cross_attention"]
+           "cross_attention", "attention_tree_kv4", "tree_accept", "kv4_keep"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -115,6 +115,12 @@ def load_library():
         lib.fa_cross_bwd_workspace.restype = ll
         lib.fa_cross_bwd.argtypes = [blob] * 5 + [vp, blob, vp] + [blob] * 3 + [f, vp, ll, vp]
         lib.fa_cross_bwd.restype = i
+        lib.fa_kv4_tree.argtypes = [blob, vp, vp, vp, vp, i, i, f, vp]
+        lib.fa_kv4_tree.restype = i
+        lib.fa_tree_accept.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, vp, vp]
+        lib.fa_tree_accept.restype = i
+        lib.fa_kv4_keep.argtypes = [blob, vp, i, vp, vp, vp, ll, vp]
+        lib.fa_kv4_keep.restype = i
         _lib = lib
         return lib
 
@@ -424,3 +430,4 @@ def flash_attention(q, k, v, causal: bool = False, scale: float | None = None, r
 from .rotary import rope, rotary_amplitude, rotary_frequencies  # noqa: E402
 from .kv4 import attention_decode_kv4, kv4_append, kv4_evict, kv4_pool, kv4_read  # noqa: E402
 from .cross import attention_backward_cross, attention_forward_cross, cross_attention  # noqa: E402
+from .tree import attention_tree_kv4, kv4_keep, tree_accept  # noqa: E402

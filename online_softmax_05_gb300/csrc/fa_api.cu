@@ -290,7 +290,8 @@ int fa_get_device_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
     int first = FA_OK;
     for (const auto take : {fa::fwd_take_status, fa::bwd_take_status, fa::kv4_cache_take_status,
-                            fa::kv4_decode_take_status}) {
+                            fa::kv4_decode_take_status, fa::cross_rows_take_status,
+                            fa::kv4_tree_take_status, fa::kv4_keep_take_status}) {
         const int status = take();
         if (status == FA_ERR_CUDA) return FA_ERR_CUDA;
         if (first == FA_OK) first = status;
@@ -406,7 +407,8 @@ int fa_cross_fwd(const fa_cross_shape* s, const fa_cross_tensor* q, const fa_cro
     rc = current_device(&dev, &sms);
     if (rc != FA_OK) return rc;
     const fa::CrossShape shape{s->B, s->Hq, s->Hkv, s->Tq, s->Tk, s->D, s->key_lengths};
-    return fa::launch_cross_fwd(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, static_cast<cudaStream_t>(stream), knobs(), sms);
+    const auto launch = fa::cross_rows_wanted(shape) ? fa::launch_cross_rows : fa::launch_cross_fwd;
+    return launch(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, static_cast<cudaStream_t>(stream), knobs(), sms);
 }
 
 long long fa_cross_bwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D) {
@@ -698,6 +700,77 @@ int fa_kv4_evict(const fa_kv4_cache* cache, const float* weights, const int* slo
                               slot_positions, slots, budget, recent, weights_out, positions_out, lengths_out, source,
                               ws.ptr, static_cast<cudaStream_t>(stream), sms);
     return ws.release(rc);
+}
+
+int fa_kv4_tree(const fa_kv4_cache* cache, const void* q, const int* parents, void* o, float* lse, int Hq, int N,
+                float scale, void* stream) {
+    int rc = check_kv4(cache);
+    if (rc != FA_OK) return rc;
+    if (!q || !parents || !o || !lse) return FA_ERR_NULL;
+    if (Hq < 1 || Hq % cache->Hkv != 0 || N < 1) return FA_ERR_SHAPE;
+    if (N > FA_TREE_MAX_PLACES) return FA_ERR_UNSUPPORTED;
+    const size_t rows = static_cast<size_t>(cache->B) * Hq * N;
+    if (static_cast<long long>(cache->B) * Hq > INT_MAX / N) return FA_ERR_SHAPE;
+    if (!std::isfinite(scale)) return FA_ERR_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(parents) & 3u))
+        return FA_ERR_ALIGN;
+    const Range ins[5] = {range_of(q, rows * cache->D * 2), kv4_pool_range(cache), kv4_table_range(cache),
+                          kv4_lengths_range(cache), range_of(parents, static_cast<size_t>(cache->B) * N * 4)};
+    const Range ro = range_of(o, rows * cache->D * 2), rl = range_of(lse, rows * 4);
+    if (overlaps_any(ro, ins, 5) || overlaps_any(rl, ins, 5) || overlap(ro, rl)) return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return fa::launch_kv4_tree(kv4_shape(cache), cache->pool, cache->block_table, cache->lengths, parents, q, o, lse, Hq, N,
+                               scale, static_cast<cudaStream_t>(stream), knobs(), sms);
+}
+
+int fa_tree_accept(const int* parents, const void* tokens, const void* picks, const void* first, int tokens_64, int B,
+                   int N, int* path, int* counts, void* next, void* stream) {
+    if (!parents || !tokens || !picks || !path || !counts || !next) return FA_ERR_NULL;
+    if (B < 1 || N < 1 || static_cast<long long>(B) * N > INT_MAX) return FA_ERR_SHAPE;
+    if (N > FA_TREE_MAX_PLACES) return FA_ERR_UNSUPPORTED;
+    if (tokens_64 != 0 && tokens_64 != 1) return FA_ERR_ARG;
+    const size_t n = static_cast<size_t>(B) * N, size = tokens_64 ? 8 : 4;
+    if (((reinterpret_cast<uintptr_t>(parents) | reinterpret_cast<uintptr_t>(path) | reinterpret_cast<uintptr_t>(counts)) & 3u) ||
+        ((reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(picks) | reinterpret_cast<uintptr_t>(first) |
+          reinterpret_cast<uintptr_t>(next)) & (size - 1)))
+        return FA_ERR_ALIGN;
+    const Range ins[4] = {range_of(parents, n * 4), range_of(tokens, n * size), range_of(picks, n * size),
+                          range_of(first, first ? B * size : 0)};
+    const Range outs[3] = {range_of(path, n * 4), range_of(counts, static_cast<size_t>(B) * 4), range_of(next, B * size)};
+    for (int i = 0; i < 3; ++i)
+        if (overlaps_any(outs[i], ins, 4) || overlaps_any(outs[i], outs, i)) return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    const int rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return fa::launch_tree_accept(parents, tokens, picks, first, tokens_64, B, N, path, counts, next,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+int fa_kv4_keep(const fa_kv4_cache* cache, const int* path, int N, int* lengths_out, float* weights, int* slot_positions,
+                long long slots, void* stream) {
+    int rc = check_kv4(cache);
+    if (rc != FA_OK) return rc;
+    if (!path || !lengths_out) return FA_ERR_NULL;
+    if (N < 1 || ((weights || slot_positions) && slots < 1)) return FA_ERR_SHAPE;
+    if (N > FA_TREE_MAX_PLACES) return FA_ERR_UNSUPPORTED;
+    const void* words[4] = {path, lengths_out, weights, slot_positions};
+    for (const void* w : words)
+        if (reinterpret_cast<uintptr_t>(w) & 3u) return FA_ERR_ALIGN;
+    const size_t account = static_cast<size_t>(cache->B) * cache->Hkv * (slots > 0 ? slots : 0) * 4;
+    const Range ins[3] = {kv4_table_range(cache), kv4_lengths_range(cache),
+                          range_of(path, static_cast<size_t>(cache->B) * N * 4)};
+    const Range outs[4] = {kv4_pool_range(cache), range_of(lengths_out, cache->B * static_cast<size_t>(4)),
+                           range_of(weights, weights ? account : 0),
+                           range_of(slot_positions, slot_positions ? account : 0)};
+    for (int i = 0; i < 4; ++i)
+        if (overlaps_any(outs[i], ins, 3) || overlaps_any(outs[i], outs, i)) return FA_ERR_ARG;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return fa::launch_kv4_keep(kv4_shape(cache), cache->pool, cache->block_table, cache->lengths, path, N, lengths_out,
+                               weights, slot_positions, slots, static_cast<cudaStream_t>(stream));
 }
 
 long long fa_kv4_block_offset(const int* block_table, int width, int Hkv, int D, int group, int page_size,

@@ -1,0 +1,427 @@
+// fa_cross_rows.cu -- cross attention of a few query rows over many keys on sm_103a.
+//
+// The rows of one key/value head, its group's heads times their Tq queries, are packed into
+// a tile of 128 (row = head in the group x Tq + query), so that K and V are read once
+// whatever the grouping, and the keys are split over a cluster of CTAs, whose states
+//   m = max S, l = sum 2^(S - m), acc = sum 2^(S - m) V      (scores in log2 units)
+// join by the online-softmax rule through distributed shared memory:
+//   M = max m_c,  L = sum l_c 2^(m_c - M),  O = sum acc_c 2^(m_c - M) / L.
+//
+// Per CTA: warps 0-3 softmax (a TMEM lane is a row), warp 4 loads (TMA, K and V tiles of 128
+// keys in one ring), warp 5 issues tcgen05.mma: S = Q K^T, then O += P V with P, in bf16, in the
+// S columns.  A CTA's chain per tile is serial (S, softmax, P V): two CTAs share an SM
+// and fill each other's gaps, and the ring keeps loads in flight meanwhile.  K's and V's bytes
+// bound it; the tensor cores' 128-row tiles are mostly padding then, which costs nothing
+// that is not idle.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "fa_check.cuh"
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+#include "fa_tmap.h"
+#include "fa_wait.cuh"
+
+namespace fa {
+
+static __device__ int g_status_cross_rows;
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 192;
+constexpr int kKeys = 128;   // of a tile
+constexpr int kMaxSplit = 8; // CTAs of a cluster
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int D>
+struct RowsCfg {
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kAtomBytes = 128 * 128;
+    static constexpr int kTileBytes = 128 * D * 2;
+    static constexpr int kStages = D == 128 ? 2 : 5;  // two CTAs an SM
+    static constexpr int kRingOff = kTileBytes;       // Q first
+    static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+    // kv_full[], kv_empty[], q_full, s_full, p_full, o_full, mma_done
+    static constexpr int kNumBars = 2 * kStages + 5;
+    static constexpr int kMlOff = kBarOff + kNumBars * 8 + 8;  // [2][128] row maxima and sums, for the cluster
+    static constexpr int kMiscOff = kMlOff + 2 * 128 * 4;
+    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;    // + tensor memory's address, abort flag; alignment
+    static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert(kBarOff >= 128 * D * 4, "a CTA's scaled rows go where Q and the ring were");
+    // 256 TMEM columns: S (P over its first half), O
+    static constexpr uint32_t kS = 0, kO = 128;
+    static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kKeys, false, false);
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
+};
+
+struct RowsParams {
+    CrossTensor q, o;
+    __nv_bfloat16* o_rest;
+    float* lse;
+    const int* key_lengths;
+    int Hq, Hkv, group, Tq, Tk, R, row_tiles;
+    float sl2, sl2_eff;
+    int prescale;
+    unsigned long long timeout_ns;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    fa_cross_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         RowsParams p) {
+    using C = RowsCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sQ = smem_u32(smem), ring = sQ + C::kRingOff, bars = sQ + C::kBarOff;
+    auto kv_full = [&](int s) { return bars + 8u * s; };
+    auto kv_empty = [&](int s) { return bars + 8u * (C::kStages + s); };
+    const uint32_t q_full = bars + 8u * (2 * C::kStages), s_full = q_full + 8, p_full = q_full + 16,
+                   o_full = q_full + 24, mma_done = q_full + 32;
+    float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    const WaitCtl ctl{abort_flag, &g_status_cross_rows, p.timeout_ns};
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x / splits;
+    const int tile = unit % p.row_tiles, bh = unit / p.row_tiles;
+    const int b = bh / p.Hkv, hk = bh % p.Hkv;
+    const int rows = min(128, p.R - tile * 128);  // of this tile
+    const int active = (rows + 31) / 32;          // softmax warps with rows
+
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(kv_full(s), 1);
+            mbar_init(kv_empty(s), 1);
+        }
+        mbar_init(q_full, 4);
+        mbar_init(s_full, 1);
+        mbar_init(p_full, active);
+        mbar_init(o_full, 1);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) {
+        tmem_alloc(smem_u32(tmem_slot), 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    wait_for_stream();
+
+    // this CTA's key tiles
+    int keys = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.Tk;
+    if (keys < 0 || keys > p.Tk) {
+        if (tid == 0) atomicCAS(&g_status_cross_rows, 0, kStatusBadSeqlen);
+        keys = 0;
+    }
+    const int all = (keys + kKeys - 1) / kKeys, share = (all + splits - 1) / splits;
+    const int j0 = min(all, rank * share), n = min(all - j0, share);
+
+    // a softmax thread's row: its state, and whether it is one
+    const int r = 32 * warp + lane;
+    const int row = tile * 128 + r, head = hk * p.group + row / p.Tq, tok = row % p.Tq;
+    float m = -INFINITY, l = 0.f;
+    const uint32_t lane_base = tmem + ((32u * (warp & 3)) << 16);
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            const uint64_t policy = l2_policy_evict_first();
+            int fills = 0;
+            for (int i = 0; i < 2 * n; ++i) {
+                const int slot = i % C::kStages;
+                const bool is_v = i & 1;
+                const int j = j0 + i / 2;
+                if (!wait_one(kv_empty(slot), ((i / C::kStages) & 1) ^ 1, ctl) ||
+                    !FA_CHECK(j >= 0 && j * kKeys < keys, &g_status_cross_rows, abort_flag))
+                    break;
+                mbar_arrive_expect_tx(kv_full(slot), C::kTileBytes);
+                ++fills;
+                for (int a = 0; a < C::kAtoms; ++a)
+                    tma_load_4d_hint(ring + slot * C::kTileBytes + a * C::kAtomBytes, is_v ? &tm_v : &tm_k, kv_full(slot),
+                                     64 * a, j * kKeys, hk, b, policy);
+            }
+            for (int f = max(0, fills - C::kStages); f < fills; ++f)
+                drain(kv_full(f % C::kStages), (f / C::kStages) & 1, ctl);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ matrix instructions
+        const bool leader = elect_one_sync();
+        const SDesc dQ = sdesc_make(sQ, 16, 1024), dK = sdesc_make(ring, 16, 1024),
+                    dV = sdesc_make(ring, C::kAtomBytes, 1024);
+        constexpr uint32_t kTile16 = C::kTileBytes >> 4;
+        int i = 0;  // ring fills used
+        if (n > 0 && wait_warp(q_full, 0, ctl)) {
+            tc_fence_after();
+            for (int j = 0; j < n; ++j) {
+                const int ks = i % C::kStages;
+                if (!wait_warp(kv_full(ks), (i / C::kStages) & 1, ctl)) break;
+                ++i;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = ((s >> 2) * C::kAtomBytes + (s & 3) * 32) >> 4;
+                    if (leader) mma_ss_d(tmem + C::kS, dQ, off, dK, ks * kTile16 + off, C::kIdescS, s > 0);
+                }
+                if (leader) {
+                    mma_commit(s_full);
+                    mma_commit(kv_empty(ks));
+                }
+                const int vs = i % C::kStages;
+                if (!wait_warp(kv_full(vs), (i / C::kStages) & 1, ctl)) break;
+                ++i;
+                // what lies past the keys must not meet P = 0 as NaN (past the tensor, TMA has filled zeros)
+                const int left = keys - (j0 + j) * kKeys;
+                if (left < kKeys && keys < p.Tk) zero_tail_rows(ring + vs * C::kTileBytes, C::kAtoms, left, lane);
+                if (!wait_warp(p_full, j & 1, ctl)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kKeys / 16; ++s)
+                    if (leader)
+                        mma_ts_d(tmem + C::kO, tmem + C::kS + s * 8, dV, vs * kTile16 + s * (2048 >> 4), C::kIdescPV,
+                                 (j > 0 || s > 0) ? 1u : 0u);
+                if (leader) mma_commit(kv_empty(vs));
+            }
+        }
+        if (leader) {
+            mma_commit(o_full);
+            mma_commit(mma_done);
+            drain(mma_done, 0, ctl);  // before tensor memory is given back
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        {
+            uint4 x[D / 8];
+            const bool there = r < rows;
+            const uint4* from = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q.ptr) + b * p.q.b +
+                                                               head * p.q.h + tok * p.q.t);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) x[c] = there ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                st_shared_v4(sQ + (c >> 3) * C::kAtomBytes + sw128_off(r, c & 7), x[c].x, x[c].y, x[c].z, x[c].w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        const uint32_t tS = lane_base + C::kS, tO = lane_base + C::kO;
+        const float eff = p.sl2_eff;
+        for (int j = 0; j < n && warp < active; ++j) {
+            if (!wait_warp(s_full, j & 1, ctl)) break;
+            tc_fence_after();
+            uint32_t sr[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, sr + 32 * c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) reg_fence32(sr + 32 * c);
+            float* s = reinterpret_cast<float*>(sr);
+            if (p.prescale) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] *= p.sl2;
+            }
+            const int left = keys - (j0 + j) * kKeys;
+            if (left < kKeys) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c >= left) s[c] = -INFINITY;
+            }
+            float mx8[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mx8[c] = fmaxf(s[c], s[c + 8]);
+#pragma unroll
+            for (int c = 16; c < 128; c += 16)
+#pragma unroll
+                for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], s[c + a], s[c + 8 + a]);
+            const float mx =
+                fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * eff;
+            // the reference is the running maximum itself: the dominant weight is then 1, exact in bf16
+            const bool grows = j > 0 && mx > m;
+            const float m_new = fmaxf(m, mx);
+            const float alpha = grows ? ex2_approx(m - m_new) : 1.f;
+            l *= alpha;
+            m = m_new;
+            const uint64_t eff2 = f2(eff, eff), neg2 = f2(-m, -m);
+            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+            auto weights = [&](int c0) {  // of 64 keys, packed into sr[c0 / 2 ..]
+#pragma unroll
+                for (int c = c0 / 2; c < c0 / 2 + 32; ++c) {
+                    float x0, x1;
+                    f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), eff2, neg2), x0, x1);
+                    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                    sum[c & 3] = add2(sum[c & 3], f2(p0, p1));
+                    sr[c] = pack_bf16x2(p0, p1);
+                }
+                tmem_st32(tS + c0 / 2, sr + c0 / 2);
+            };
+            weights(0);
+            if (__any_sync(0xffffffffu, grows)) {  // in the registers that half of the scores have left
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t* o = sr;
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_ld_wait();
+                    reg_fence32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tmem_st32(tO + 32 * c, o);
+                }
+            }
+            weights(64);
+            float s0, s1;
+            f2_split(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+            l += s0 + s1;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+        }
+        wait_warp(o_full, 0, ctl);
+        tc_fence_after();
+        ml[r] = m;
+        ml[128 + r] = l;
+    }
+
+    // ------------------------------------------------------------ join
+    // (o_full and the loads' drain are behind every thread: Q and the ring are free)
+    float factor = 0.f;
+    if (splits > 1) {
+        cluster.sync();
+        if (warp < active) {
+            float top = -INFINITY, sum = 0.f;
+            for (int c = 0; c < splits; ++c) top = fmaxf(top, cluster.map_shared_rank(ml, c)[r]);
+            for (int c = 0; c < splits; ++c) {
+                const float* x = cluster.map_shared_rank(ml, c);
+                const float lc = x[128 + r];
+                if (lc != 0.f) sum += lc * ex2_approx(x[r] - top);  // (a CTA without keys has l = 0)
+            }
+            if (l != 0.f) factor = ex2_approx(m - top) / sum;
+            m = top;
+            l = sum;
+        }
+    } else if (l != 0.f) {
+        factor = 1.f / l;
+    }
+    __syncthreads();
+    if (warp < active) {
+        // rows times their factors: fp32 into shared memory, 16-byte chunks turned by the row against conflicts
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            if (n > 0) {
+                tmem_ld32(lane_base + C::kO + 32 * c, o);
+                tmem_ld_wait();
+                reg_fence32(o);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = n > 0 ? __float_as_uint(__uint_as_float(o[e]) * factor) : 0u;
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+                st_shared_v4(sQ + r * (D * 4) + (((8 * c + g) ^ (r & (D / 4 - 1))) << 4), o[4 * g], o[4 * g + 1],
+                             o[4 * g + 2], o[4 * g + 3]);
+        }
+        if (rank == 0 && r < rows)
+            p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Tq + tok] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    }
+    if (splits > 1) cluster.sync();
+    else __syncthreads();
+    // each CTA adds up and stores its share of the rows
+    for (int i = rank * kThreads + tid; i < rows * (D / 8); i += splits * kThreads) {
+        const int rr = i / (D / 8), c = i % (D / 8);
+        float x[8] = {};
+        for (int k = 0; k < splits; ++k) {
+            const uint8_t* from = splits > 1 ? cluster.map_shared_rank(smem, k) : smem;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 y = *reinterpret_cast<const float4*>(from + rr * (D * 4) +
+                                                                  (((2 * c + h) ^ (rr & (D / 4 - 1))) << 4));
+                x[4 * h] += y.x;
+                x[4 * h + 1] += y.y;
+                x[4 * h + 2] += y.z;
+                x[4 * h + 3] += y.w;
+            }
+        }
+        const int at = tile * 128 + rr, hq = hk * p.group + at / p.Tq, t = at % p.Tq;
+        uint32_t w[4], e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+            e[k] = pack_bf16x2(x[2 * k] - __uint_as_float(w[k] << 16), x[2 * k + 1] - __uint_as_float(w[k] & 0xffff0000u));
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o.ptr) + b * p.o.b + hq * p.o.h + t * p.o.t + c * 8) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+        if (p.o_rest != nullptr)
+            *reinterpret_cast<uint4*>(p.o_rest + ((static_cast<size_t>(b) * p.Hq + hq) * p.Tq + t) * D + c * 8) =
+                make_uint4(e[0], e[1], e[2], e[3]);
+    }
+    if (splits > 1) cluster.sync();  // the others may still read this CTA's rows
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+template <int D>
+int launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const RowsParams& p, int units, int splits,
+             cudaStream_t stream) {
+    static std::atomic<unsigned long long> allowed{0};
+    auto kern = fa_cross_rows_kernel<D>;
+    if (!allow_shared_memory(kern, RowsCfg<D>::kSmemBytes, allowed)) return -5;
+    return launch_clusters(kern, units * splits, splits, kThreads, RowsCfg<D>::kSmemBytes, stream, tk, tv, p);
+}
+
+}  // namespace
+
+bool cross_rows_wanted(const CrossShape& s) { return static_cast<long long>(s.Hq / s.Hkv) * s.Tq <= 128; }
+
+int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
+                      const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
+                      const DebugKnobs& dbg, int num_sms) {
+    CUtensorMap tk, tv;
+    if (!make_tmap_strided(&tk, {k.ptr, k.b, k.h, k.t}, s.B, s.Hkv, s.Tk, s.D, kKeys) ||
+        !make_tmap_strided(&tv, {v.ptr, v.b, v.h, v.t}, s.B, s.Hkv, s.Tk, s.D, kKeys))
+        return -5;
+    RowsParams p{};
+    p.q = q;
+    p.o = o;
+    p.o_rest = static_cast<__nv_bfloat16*>(o_rest);
+    p.lse = lse;
+    p.key_lengths = s.key_lengths;
+    p.Hq = s.Hq;
+    p.Hkv = s.Hkv;
+    p.group = s.Hq / s.Hkv;
+    p.Tq = s.Tq;
+    p.Tk = s.Tk;
+    p.R = p.group * s.Tq;
+    p.row_tiles = (p.R + 127) / 128;
+    p.sl2 = scale * kLog2e;
+    p.prescale = p.sl2 > 0.f ? 0 : 1;
+    p.sl2_eff = p.prescale ? 1.f : p.sl2;
+    p.timeout_ns = dbg.timeout_ns;
+    const int units = s.B * s.Hkv * p.row_tiles, tiles = (s.Tk + kKeys - 1) / kKeys;
+    int splits = 1;
+    while (splits < kMaxSplit && 2 * splits <= tiles && 2LL * splits * units <= 2LL * num_sms) splits *= 2;
+    return s.D == 64 ? launch_t<64>(tk, tv, p, units, splits, stream) : launch_t<128>(tk, tv, p, units, splits, stream);
+}
+
+int cross_rows_take_status() {
+    int h = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&h, g_status_cross_rows, sizeof(int)) != cudaSuccess) return -5;
+    if (cudaMemcpyToSymbol(g_status_cross_rows, &z, sizeof(int)) != cudaSuccess) return -5;
+    return h;
+}
+
+}  // namespace fa

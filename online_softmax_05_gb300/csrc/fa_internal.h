@@ -57,6 +57,12 @@ struct CrossTensor {
 int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
                      const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
                      const DebugKnobs& dbg, int num_sms);
+// The same for few rows a key/value head (fa_cross_rows.cu): whether it is the one to take, and its launch.
+bool cross_rows_wanted(const CrossShape& s);
+int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
+                      const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
+                      const DebugKnobs& dbg, int num_sms);
+int cross_rows_take_status();
 size_t cross_bwd_workspace(const CrossShape& s, bool deterministic, int num_sms);
 int launch_cross_bwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
                      const CrossTensor& o, const void* o_rest, const CrossTensor& dO, const float* lse, const CrossTensor& dq,
@@ -102,6 +108,15 @@ bool kv4_decode_fits(const Kv4Shape& c, int Hq, int Tq);  // whether the kernel'
 int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const void* q,
                       void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
                       float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms);
+int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* parents,
+                    const void* q, void* o, float* lse, int Hq, int N, float scale, cudaStream_t stream,
+                    const DebugKnobs& dbg, int num_sms);
+int launch_tree_accept(const int* parents, const void* tokens, const void* picks, const void* first, int tokens64, int B,
+                       int N, int* path, int* counts, void* next, cudaStream_t stream);
+int launch_kv4_keep(const Kv4Shape& c, void* pool, const int* table, const int* lengths, const int* path, int N,
+                    int* lengths_out, float* weights, int* slot_positions, long long slots, cudaStream_t stream);
+int kv4_tree_take_status();
+int kv4_keep_take_status();
 int kv4_cache_take_status();
 int kv4_decode_take_status();
 
@@ -121,6 +136,25 @@ inline int launch_chained(void (*kernel)(Params...), dim3 grid, int threads, siz
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -5;
+}
+// The same in clusters of `cluster` CTAs of a one-dimensional grid.
+template <typename... Params, typename... Args>
+inline int launch_clusters(void (*kernel)(Params...), int grid, int cluster, int threads, size_t smem,
+                           cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -5;
 }
 #ifdef __CUDACC__

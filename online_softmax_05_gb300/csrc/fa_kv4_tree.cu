@@ -1,0 +1,662 @@
+// fa_kv4_tree.cu -- attention of a tree of drafted tokens over the 4-bit paged cache.
+//
+// The last N slots of a sequence are the tree's places; place i sees the context
+// before them, its ancestors and itself.  The rows of a key/value head (group x N) are
+// many enough for the tensor cores' 128-row tiles, which want whole operands in shared memory, so
+// the codes are unpacked there, once for up to 256 rows.  With k = s n + m and v = s n + m per
+// group of channels (fa_kv4.cuh):
+//   K   s = sa + sb, its upper and lower four bits of significand: sa n and sb n have
+//       eight bits and are exact in bf16.  S = q.(sa n) + q.(sb n) + sum_g m_g sum(q_g), the
+//       last as 16 more channels: m_g against three bf16 pieces (24 bits) of sum(q_g).
+//       Every operand is exact; S is what fp32 sums give.  (One bf16 number for k would put
+//       2^-9 into each product, 2e-3 into a score and so into the log-sum-exp.)
+//   V   s n + m rounded once to bf16, as P is: both average out over a row's tokens and
+//       are at most the output's own rounding where one token has all the weight.
+// One packed multiply-add makes two products: 128 + n is the bf16 number 0x4300 | n, and
+// sa (128 + n) - 128 sa is exact.  Channels stay in the order of the codes' words; Q is stored
+// in that order, and V's is undone when the outputs leave.
+//
+// Ranges.  Rows of q are scaled by a power of two to [1, 2), K by 2^-16 and V by 2^-24, undone in the
+// row's score factor and at the end: no product or sum overflows for any bf16 numbers in the cache.
+// A token that a row does not see adds nothing whatever it holds: S is replaced, and a tree's value
+// group that is NaN goes into the products as 0 and into the rows that see it at the end.
+//
+// Per CTA: warps 0-3 and 4-7 softmax (two tiles of 128 rows; with at most 128 rows the two take
+// every other tile of keys instead and are joined at the end), warps 8-11 fetch and unpack
+// 64 tokens at a time (a thread a token, 8 and 9 keys, 10 and 11 values, each copying the bytes that it
+// will use four tiles ahead), warp 12 issues tcgen05.mma.  The tokens are split over a cluster
+// of CTAs, joined as in fa_cross_rows.cu.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "fa_check.cuh"
+#include "fa_internal.h"
+#include "fa_kv4.cuh"
+#include "fa_ptx.cuh"
+#include "fa_tree.cuh"
+#include "fa_wait.cuh"
+
+namespace fa {
+
+static __device__ int g_status_kv4_tree;
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 416;
+constexpr int kTok = 64;       // of a tile
+constexpr int kRaw = 4;        // tiles of codes on their way
+constexpr int kMaxSplit = 8;   // CTAs of a cluster
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kKeyUnit = 0x1p-16f, kValueUnit = 0x1p-24f;
+
+template <int D_, int G_>
+struct TreeCfg : Kv4<D_, G_> {
+    using L = Kv4<D_, G_>;
+    static constexpr int kWords = D_ / 8;                  // 32-bit words of a row of codes
+    static constexpr int kTile = kTok * D_ * 2;            // an operand tile of keys or values
+    static constexpr int kAugTile = kTok * 32;             // 16 more channels a token
+    static constexpr int kStage = 3 * kTile + kAugTile;    // sa n, sb n, V, minima
+    static constexpr int kStages = D_ == 128 ? 2 : 4;
+    static constexpr int kQTile = 128 * D_ * 2, kQAug = 128 * 32;
+    static constexpr int kQOff = kStages * kStage;
+    static constexpr int kRawOff = kQOff + 2 * (kQTile + kQAug);
+    static constexpr int kRawTile = 128 * (L::kRow + L::kScaleRow);  // and then all threads' scales
+    static constexpr int kBarOff = kRawOff + kRaw * kRawTile;
+    // full[], empty[], s_full[2][2], p_full[2][2], pv_done[2], o_full, q_full, mma_done
+    static constexpr int kNumBars = 2 * kStages + 8 + 2 + 3;
+    static constexpr int kMlOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // [2][2][128] row maxima and sums
+    static constexpr int kTreeOff = kMlOff + 4 * 128 * 4;    // [64] ancestors
+    static constexpr int kPoisonOff = kTreeOff + 64 * 8;     // [groups] places whose value group is NaN
+    static constexpr int kMaskOff = kPoisonOff + 4 * 8;      // [stages] tokens that are there
+    static constexpr int kMiscOff = kMaskOff + kStages * 8;
+    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    static_assert(kRawOff >= 2 * 128 * D_ * 4, "two tiles of scaled rows go where the stages and Q were");
+    // TMEM: per half t two S tiles of 64 tokens (P over them) and O
+    __device__ static constexpr uint32_t kS(int t, int buf) { return 256u * t + 64u * buf; }
+    __device__ static constexpr uint32_t kO(int t) { return 256u * t + 128u; }
+    static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTok, false, false);
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D_, false, true);
+};
+
+struct TreeParams {
+    const __nv_bfloat16* q;
+    Kv4Pages pages;
+    const int* lengths;
+    const int* parents;
+    __nv_bfloat16* o;
+    float* lse;
+    int N, R, row_units;
+    float sl2;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
+// a x + b of bf16 pairs, rounded once.
+__device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t x, uint32_t b) {
+    return as_u32(__hfma2(as_bf2(a), as_bf2(x), as_bf2(b)));
+}
+__device__ __forceinline__ uint32_t twice(float x) { return pack_bf16x2(x, x); }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&x)[WORDS]) {
+    if constexpr (WORDS == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[0]) : "r"(addr));
+    if constexpr (WORDS == 2) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(addr));
+    if constexpr (WORDS == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(addr));
+}
+// 16-byte chunk of a row of 16 channels: rows of 32 bytes, 32-byte swizzle.
+__device__ __forceinline__ uint32_t sw32_off(uint32_t row, uint32_t chunk) {
+    return row * 32u + ((chunk ^ ((row >> 2) & 1u)) << 4);
+}
+// Descriptor of such a K-major tile: 8 rows are 256 bytes.
+__device__ __forceinline__ SDesc sdesc_sw32(uint32_t saddr) {
+    SDesc d = sdesc_make(saddr, 16, 256);
+    d.hi = (d.hi & 0x1fffffffu) | (6u << 29);
+    return d;
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) {
+    using C = TreeCfg<D, G>;
+    constexpr int ST = C::kStages, NG = C::kGroups, S32 = D / 32;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t base = smem_u32(smem), bars = base + C::kBarOff;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (ST + s); };
+    auto s_full = [&](int t, int b) { return bars + 8u * (2 * ST + 2 * t + b); };
+    auto p_full = [&](int t, int b) { return bars + 8u * (2 * ST + 4 + 2 * t + b); };
+    auto pv_done = [&](int t) { return bars + 8u * (2 * ST + 8 + t); };
+    const uint32_t o_full = bars + 8u * (2 * ST + 10), q_full = o_full + 8, mma_done = o_full + 16;
+    auto sQ = [&](int t) { return base + C::kQOff + t * (C::kQTile + C::kQAug); };
+    auto sQAug = [&](int t) { return sQ(t) + C::kQTile; };
+    auto sStage = [&](int s) { return base + s * C::kStage; };
+    float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
+    unsigned long long* tree = reinterpret_cast<unsigned long long*>(smem + C::kTreeOff);
+    unsigned long long* poison = reinterpret_cast<unsigned long long*>(smem + C::kPoisonOff);
+    volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::kMaskOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    const WaitCtl ctl{abort_flag, &g_status_kv4_tree, p.timeout_ns};
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = blockIdx.x / splits;
+    const int ru = unit % p.row_units, bh = unit / p.row_units;
+    const int b = bh / p.pages.heads, hk = bh % p.pages.heads;
+    const int row0 = ru * 256, rows = min(256, p.R - row0);
+    const bool paired = rows > 128;  // two tiles of rows; otherwise the halves take every other tile of keys
+
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full(s), 4);
+            mbar_init(empty(s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            for (int y = 0; y < 2; ++y) {
+                mbar_init(s_full(t, y), 1);
+                mbar_init(p_full(t, y), 4);
+            }
+            mbar_init(pv_done(t), 1);
+        }
+        mbar_init(o_full, 1);
+        mbar_init(q_full, paired ? 8 : 4);
+        mbar_init(mma_done, 1);
+        for (int g = 0; g < NG; ++g) poison[g] = 0;
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    wait_for_stream();
+
+    int len = __ldg(p.lengths + b);
+    if (len < 0 || len > p.pages.capacity() || (len > 0 && len < p.N)) {
+        if (tid == 0) atomicCAS(&g_status_kv4_tree, 0, kStatusBadSeqlen);
+        len = 0;
+    }
+    const int ctx = len - p.N;  // tokens before the tree
+    const int all = (len + kTok - 1) / kTok, share = (all + splits - 1) / splits;
+    const int j0 = min(all, rank * share), n = min(all - j0, share);  // this CTA's tiles
+
+    // a softmax thread's row, state and what it sees of the tree
+    const int t = warp >> 2, r = tid & 127;
+    const int row = row0 + (paired ? 128 * t : 0) + r;
+    float m = -INFINITY, l = 0.f;
+    unsigned long long sees = 0;
+    const uint32_t lane_base = tmem + ((32u * (warp & 3)) << 16);
+
+    if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------------------ fetch and unpack
+        const bool is_v = warp >= 10;
+        const int tok = tid & 63, th = tid - 256;
+        constexpr int CH = C::kRow / 16;  // 16-byte chunks of a row of codes
+        const uint32_t raw = base + C::kRawOff + th * C::kRow, raw_scales = base + C::kRawOff + 128 * C::kRow + th * C::kScaleRow;
+        const int turn = (tok / (8 / CH)) % CH;  // the chunks' order in shared memory, against bank conflicts
+        const int section = is_v ? C::kValueCodes : C::kKeyCodes, scales = is_v ? C::kValueScales : C::kKeyScales;
+        const int rowb = tok & 15;
+        uint32_t here = 0;  // bit i: this thread's token is there in raw tile i
+        auto fetch = [&](int i) {
+            if (i < n) {
+                const int at = (j0 + i) * kTok + tok;
+                const int slot = i % kRaw;
+                here &= ~(1u << slot);
+                if (at < len) {
+                    const long long off = p.pages.block_of(b, at >> 4);
+                    if (off >= 0) {
+                        here |= 1u << slot;
+                        const unsigned char* from = p.pages.pool + off + hk * p.pages.head_bytes();
+#pragma unroll
+                        for (int c = 0; c < CH; ++c)
+                            copy_async<16>(raw + slot * C::kRawTile + ((c ^ turn) << 4), from + section + rowb * C::kRow + c * 16);
+                        copy_async<C::kScaleRow>(raw_scales + slot * C::kRawTile, from + scales + rowb * C::kScaleRow);
+                    } else if (rowb == 0) {
+                        atomicCAS(&g_status_kv4_tree, 0, kStatusBadPage);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int i = 0; i < kRaw; ++i) fetch(i);
+        for (int i = 0; i < n; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
+            const int slot = i % kRaw, st = i % ST;
+            const bool there = here >> slot & 1;
+            uint32_t w[C::kWords], sc[NG];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                uint32_t x[4];
+                load_words(raw + slot * C::kRawTile + ((c ^ turn) << 4), x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[4 * c + e] = there ? x[e] : 0u;
+            }
+            load_words(raw_scales + slot * C::kRawTile, sc);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sc[g] = there ? sc[g] : 0u;
+            fetch(i + kRaw);
+            if (!wait_warp(empty(st), ((i / ST) & 1) ^ 1, ctl)) break;
+            const uint32_t stage = sStage(st);
+            if (!is_v) {
+                uint32_t sa[NG], sb[NG], ca[NG], cb[NG];  // pairs: the parts of s, and -128 of them
+                float mn[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float2 x = kv4_scale(sc[g]);
+                    const float hi = __uint_as_float(__float_as_uint(x.x) & 0xfff00000u), lo = x.x - hi;
+                    sa[g] = twice(hi * kKeyUnit);
+                    sb[g] = twice(lo * kKeyUnit);
+                    ca[g] = twice(hi * kKeyUnit * -128.f);
+                    cb[g] = twice(lo * kKeyUnit * -128.f);
+                    mn[g] = x.y * kKeyUnit;
+                }
+#pragma unroll
+                for (int c = 0; c < C::kWords; ++c) {
+                    const int g = c % S32 * 32 / G;
+                    uint32_t ya[4], yb[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x = ((w[c] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+                        ya[e] = fma_pair(sa[g], x, ca[g]);
+                        yb[e] = fma_pair(sb[g], x, cb[g]);
+                    }
+                    const uint32_t at = stage + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7);
+                    st_shared_v4(at, ya[0], ya[1], ya[2], ya[3]);
+                    st_shared_v4(at + C::kTile, yb[0], yb[1], yb[2], yb[3]);
+                }
+                // the minima, three times each: against the three pieces of sum(q_g)
+                float c[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) c[e] = e < 3 * NG ? mn[e < 3 * NG ? e / 3 : 0] : 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    st_shared_v4(stage + 3 * C::kTile + sw32_off(tok, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
+                                 pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
+                                 pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
+                const uint32_t mask = __ballot_sync(0xffffffffu, there);
+                if (lane == 0) masks[2 * st + (warp - 8)] = mask;
+            } else {
+                float vs[NG], vm[NG];
+                const int place = (j0 + i) * kTok + tok - ctx;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float2 x = kv4_scale(sc[g]);
+                    vs[g] = x.x * kValueUnit;
+                    vm[g] = x.y * kValueUnit;
+                    if (place >= 0 && !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY)) {
+                        // rows that do not see this token must not meet it as 0 x NaN
+                        if (there) atomicOr(poison + g, 1ull << place);
+                        vs[g] = vm[g] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < C::kWords; ++c) {
+                    const int g0 = 2 * c % S32 * 32 / G, g1 = (2 * c + 1) % S32 * 32 / G;
+                    const uint32_t s2 = pack_bf16x2(vs[g0], vs[g1]), m2 = pack_bf16x2(vm[g0], vm[g1]);
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x = ((w[c] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+                        y[e] = fma_pair(as_u32(__hsub2(as_bf2(x), as_bf2(0x43004300u))), s2, m2);
+                    }
+                    st_shared_v4(stage + 2 * C::kTile + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1], y[2],
+                                 y[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full(st));
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 12) {
+        // ------------------------------------------------------------ matrix instructions
+        const bool leader = elect_one_sync();
+        const SDesc dQ = sdesc_make(sQ(0), 16, 1024), dK = sdesc_make(sStage(0), 16, 1024),
+                    dV = sdesc_make(sStage(0) + 2 * C::kTile, kTok * 128, 1024),
+                    dQA = sdesc_sw32(sQAug(0)), dKA = sdesc_sw32(sStage(0) + 3 * C::kTile);
+        constexpr uint32_t kStage16 = C::kStage >> 4, kQ16 = (C::kQTile + C::kQAug) >> 4;
+        auto issue_s = [&](int h, int i, int st) {  // the i-th tile of half h
+            const uint32_t to = tmem + C::kS(h, i & 1), qo = paired ? h * kQ16 : 0u, ko = st * kStage16;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    if (leader)
+                        mma_ss_d(to, dQ, qo + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4), dK,
+                                 ko + ((part * C::kTile + (s >> 2) * (kTok * 128) + (s & 3) * 32) >> 4), C::kIdescS,
+                                 part > 0 || s > 0);
+            if (leader) {
+                mma_ss_d(to, dQA, qo, dKA, ko, C::kIdescS, 1);
+                mma_commit(s_full(h, i & 1));
+            }
+        };
+        if (n > 0 && wait_warp(q_full, 0, ctl) && wait_warp(full(0), 0, ctl)) {
+            tc_fence_after();
+            for (int h = 0; h < (paired ? 2 : 1); ++h) issue_s(h, 0, 0);
+            for (int j = 0; j < n; ++j) {
+                const int st = j % ST;
+                if (j + 1 < n) {
+                    const int s1 = (j + 1) % ST;
+                    if (!wait_warp(full(s1), ((j + 1) / ST) & 1, ctl)) break;
+                    tc_fence_after();
+                    for (int h = 0; h < 2; ++h)
+                        if (paired || h == ((j + 1) & 1)) issue_s(h, paired ? j + 1 : (j + 1) >> 1, s1);
+                }
+                bool ok = true;
+                for (int h = 0; h < 2 && ok; ++h) {
+                    if (!paired && h != (j & 1)) continue;
+                    const int i = paired ? j : j >> 1;
+                    ok = wait_warp(p_full(h, i & 1), (i >> 1) & 1, ctl);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < kTok / 16; ++s)
+                        if (leader)
+                            mma_ts_d(tmem + C::kO(h), tmem + C::kS(h, i & 1) + s * 8, dV, st * kStage16 + s * (2048 >> 4),
+                                     C::kIdescPV, (i > 0 || s > 0) ? 1u : 0u);
+                    if (leader) mma_commit(pv_done(h));
+                }
+                if (!ok) break;
+                if (leader) mma_commit(empty(st));
+            }
+        }
+        if (leader) {
+            mma_commit(o_full);
+            mma_commit(mma_done);
+            drain(mma_done, 0, ctl);  // before tensor memory is given back
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        float factor;
+        {
+            uint4 x[D / 8];
+            const bool there = row < row0 + rows;
+            const uint4* from = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(bh) * p.R + row) * D);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) x[c] = there ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = fmax3(top, fabsf(__uint_as_float(y[e] << 16)), fabsf(__uint_as_float(y[e] & 0xffff0000u)));
+            }
+            const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+            const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((127 - ex) << 23), p.sl2);
+            factor = p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * __int_as_float((127 + ex) << 23) * (1.f / kKeyUnit);
+            if (paired || t == 0) {
+                float sum[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+                const int half = paired ? t : 0;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {  // channels 8 c .. 8 c + 7 go where the codes' words have them
+                    const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[2 * e] = __uint_as_float(y[e] << 16) * up;
+                        f[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u) * up;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[c * 8 / G] += f[e];
+                    const int word = c % 4 * S32 + c / 4;
+                    st_shared_v4(sQ(half) + (word >> 3) * (128 * 128) + sw128_off(r, word & 7), pack_bf16x2(f[0], f[4]),
+                                 pack_bf16x2(f[1], f[5]), pack_bf16x2(f[2], f[6]), pack_bf16x2(f[3], f[7]));
+                }
+                float c[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) c[e] = 0.f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    c[3 * g] = __bfloat162float(__float2bfloat16_rn(sum[g]));
+                    c[3 * g + 1] = __bfloat162float(__float2bfloat16_rn(sum[g] - c[3 * g]));
+                    c[3 * g + 2] = sum[g] - c[3 * g] - c[3 * g + 1];
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    st_shared_v4(sQAug(half) + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
+                                 pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
+                                 pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            if (warp == 0) {
+                unsigned long long up[2];
+                tree_ancestors(p.parents + static_cast<size_t>(b) * p.N, p.N, lane, up);
+                tree[lane] = up[0];
+                tree[lane + 32] = up[1];
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (there && len > 0) sees = tree[row % p.N];
+        }
+        const int mine = paired ? n : (n + 1 - t) / 2;
+        for (int i = 0; i < mine; ++i) {
+            const int j = paired ? i : 2 * i + t, st = j % ST, buf = i & 1;
+            if (!wait_warp(s_full(t, buf), (i >> 1) & 1, ctl)) break;
+            if (!wait_warp(full(st), (j / ST) & 1, ctl)) break;  // has completed: what the unpacking warps wrote is seen
+            tc_fence_after();
+            const uint32_t tS = lane_base + C::kS(t, buf), tO = lane_base + C::kO(t);
+            uint32_t sr[64];
+            tmem_ld32(tS, sr);
+            tmem_ld32(tS + 32, sr + 32);
+            tmem_ld_wait();
+            reg_fence32(sr);
+            reg_fence32(sr + 32);
+            float* s = reinterpret_cast<float*>(sr);
+            const int t0 = (j0 + j) * kTok;
+            const uint32_t have0 = masks[2 * st], have1 = masks[2 * st + 1];
+            if (t0 + kTok > ctx || (have0 & have1) != 0xffffffffu) {
+                // bit c: the row sees token t0 + c
+                unsigned long long vis = t0 >= ctx ? sees >> (t0 - ctx)
+                                         : ctx - t0 >= kTok ? ~0ull
+                                                            : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
+                vis &= have0 | static_cast<unsigned long long>(have1) << 32;
+                const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (!((c < 32 ? v0 : v1) >> (c & 31) & 1)) s[c] = -INFINITY;
+            }
+            float mx8[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mx8[c] = fmaxf(s[c], s[c + 8]);
+#pragma unroll
+            for (int c = 16; c < 64; c += 16)
+#pragma unroll
+                for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], s[c + a], s[c + 8 + a]);
+            const float mx =
+                fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * factor;
+            const bool grows = i > 0 && mx > m;
+            const float m_new = fmaxf(m, mx);
+            if (__any_sync(0xffffffffu, grows)) {
+                if (!wait_warp(pv_done(t), (i - 1) & 1, ctl)) break;
+                tc_fence_after();
+                const float alpha = grows ? ex2_approx(m - m_new) : 1.f;
+                l *= alpha;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_ld_wait();
+                    reg_fence32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tmem_st32(tO + 32 * c, o);
+                }
+            }
+            m = m_new;
+            const float ref = m == -INFINITY ? 0.f : -m;  // nothing seen yet
+            const uint64_t f2x = f2(factor, factor), neg2 = f2(ref, ref);
+            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                float x0, x1;
+                f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), f2x, neg2), x0, x1);
+                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                sum[c & 3] = add2(sum[c & 3], f2(p0, p1));
+                sr[c] = pack_bf16x2(p0, p1);
+            }
+            float s0, s1;
+            f2_split(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+            l += s0 + s1;
+            tmem_st32(tS, sr);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(t, buf));
+        }
+        wait_warp(o_full, 0, ctl);
+        tc_fence_after();
+        ml[256 * t + r] = m;
+        ml[256 * t + 128 + r] = l;
+    }
+
+    // ------------------------------------------------------------ join
+    // a row's states: one a CTA, or two where the halves shared its keys
+    float factor = 0.f;
+    if (splits > 1) cluster.sync();
+    else __syncthreads();
+    if (warp < 8) {
+        const int first = paired ? t : 0, last = paired ? t : 1;
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < splits; ++c)
+            for (int h = first; h <= last; ++h) {
+                const float* x = (splits > 1 ? cluster.map_shared_rank(ml, c) : ml) + 256 * h + r;
+                if (x[128] != 0.f) top = fmaxf(top, x[0]);
+            }
+        for (int c = 0; c < splits; ++c)
+            for (int h = first; h <= last; ++h) {
+                const float* x = (splits > 1 ? cluster.map_shared_rank(ml, c) : ml) + 256 * h + r;
+                if (x[128] != 0.f) sum += x[128] * ex2_approx(x[0] - top);
+            }
+        const bool used = sees != 0 && l != 0.f;  // a place without a token gives 0
+        if (used) factor = ex2_approx(m - top) / sum * (1.f / kValueUnit);
+        const bool any = (paired || t == 0 ? n > 0 : n > 1);
+        // rows times their factors, fp32, channels in their order; 16-byte chunks turned by the row
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            if (any) {
+                tmem_ld32(lane_base + C::kO(t) + 32 * c, o);
+                tmem_ld_wait();
+                reg_fence32(o);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // half-word 2 (4 c + k) + h of the codes holds channels 32 g + 4 r' .. + 3
+                    const int hw = 2 * (4 * c + k) + h, g = hw % S32, chunk = 8 * g + hw / S32;
+                    const bool bad = (sees & poison[g * 32 / G]) != 0;
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = __uint_as_float(o[8 * k + 2 * e + h]) * factor;
+                        y[e] = used && any ? __float_as_uint(bad ? __int_as_float(0x7fffffff) : v) : 0u;
+                    }
+                    st_shared_v4(base + (t * 128 + r) * (D * 4) + ((chunk ^ (r & (D / 4 - 1))) << 4), y[0], y[1], y[2], y[3]);
+                }
+        }
+        if (rank == 0 && row < row0 + rows && (paired || t == 0))
+            p.lse[static_cast<size_t>(bh) * p.R + row] =
+                sees == 0 || sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+    }
+    if (splits > 1) cluster.sync();
+    else __syncthreads();
+    // each CTA adds up and stores its share of the rows
+    for (int i = rank * kThreads + tid; i < rows * (D / 8); i += splits * kThreads) {
+        const int rr = i / (D / 8), c = i % (D / 8);
+        float x[8] = {};
+        for (int k = 0; k < splits; ++k) {
+            const uint8_t* from = splits > 1 ? cluster.map_shared_rank(smem, k) : smem;
+            for (int h = 0; h < (paired ? 1 : 2); ++h) {
+                const int at = rr + 128 * h;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float4 z = *reinterpret_cast<const float4*>(from + at * (D * 4) +
+                                                                      (((2 * c + y) ^ (at & (D / 4 - 1))) << 4));
+                    x[4 * y] += z.x;
+                    x[4 * y + 1] += z.y;
+                    x[4 * y + 2] += z.z;
+                    x[4 * y + 3] += z.w;
+                }
+            }
+        }
+        *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(bh) * p.R + row0 + rr) * D + c * 8) =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    if (splits > 1) cluster.sync();  // the others may still read this CTA's rows
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int G>
+int launch_t(const TreeParams& p, int units, int splits, cudaStream_t stream) {
+    static std::atomic<unsigned long long> allowed{0};
+    auto kern = fa_kv4_tree_kernel<D, G>;
+    if (!allow_shared_memory(kern, TreeCfg<D, G>::kSmemBytes, allowed)) return -5;
+    return launch_clusters(kern, units * splits, splits, kThreads, TreeCfg<D, G>::kSmemBytes, stream, p);
+}
+
+}  // namespace
+
+int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* parents,
+                    const void* q, void* o, float* lse, int Hq, int N, float scale, cudaStream_t stream,
+                    const DebugKnobs& dbg, int num_sms) {
+    TreeParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.pages = kv4_pages(static_cast<unsigned char*>(const_cast<void*>(pool)), table, c.width, c.num_pages, c.Hkv,
+                        c.page_size, c.D, c.group);
+    p.lengths = lengths;
+    p.parents = parents;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.N = N;
+    p.R = Hq / c.Hkv * N;
+    p.row_units = (p.R + 255) / 256;
+    p.sl2 = scale * kLog2e;
+    p.timeout_ns = dbg.timeout_ns;
+    const long long units = static_cast<long long>(c.B) * c.Hkv * p.row_units;
+    const long long tiles = (static_cast<long long>(c.width) * c.page_size + kTok - 1) / kTok;
+    int splits = 1;
+    while (splits < kMaxSplit && 4 * splits <= tiles && splits * units <= 2LL * num_sms) splits *= 2;
+    const int n = static_cast<int>(units);
+    if (c.D == 64) return c.group == 32 ? launch_t<64, 32>(p, n, splits, stream) : launch_t<64, 64>(p, n, splits, stream);
+    return c.group == 32 ? launch_t<128, 32>(p, n, splits, stream) : launch_t<128, 64>(p, n, splits, stream);
+}
+
+int kv4_tree_take_status() {
+    int h = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&h, g_status_kv4_tree, sizeof(int)) != cudaSuccess) return -5;
+    if (cudaMemcpyToSymbol(g_status_kv4_tree, &z, sizeof(int)) != cudaSuccess) return -5;
+    return h;
+}
+
+}  // namespace fa
