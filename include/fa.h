@@ -423,11 +423,15 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
  * A length between 0 and N is recorded as FA_ERR_SEQLEN and counts as 0.  What a place does not
  * see does not touch its result, whatever the cache holds there.  Scores, sums and the
  * softmax are float32 and keys are exact; weights and values go into their product as
- * bf16, each rounded once.  No workspace.
+ * bf16, each rounded once.
+ *   workspace : fa_kv4_tree_workspace(B, Hq, Hkv, N, D, width * page_size) bytes, 16-byte
+ *               aligned, used until the call's work on `stream` is done; or NULL: taken with
+ *               cudaMallocAsync.  FA_ERR_SCRATCH if workspace_bytes is too small.
  */
 #define FA_TREE_MAX_PLACES 64
+long long fa_kv4_tree_workspace(int B, int Hq, int Hkv, int N, int D, int slots);
 int fa_kv4_tree(const fa_kv4_cache* cache, const void* q, const int* parents, void* o, float* lse, int Hq, int N,
-                float scale, void* stream);
+                float scale, void* workspace, long long workspace_bytes, void* stream);
 
 /*
  * Which of a tree's tokens stand: place i does if it and every place on its way from a root

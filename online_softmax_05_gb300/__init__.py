@@ -115,7 +115,9 @@ def load_library():
         lib.fa_cross_bwd_workspace.restype = ll
         lib.fa_cross_bwd.argtypes = [blob] * 5 + [vp, blob, vp] + [blob] * 3 + [f, vp, ll, vp]
         lib.fa_cross_bwd.restype = i
-        lib.fa_kv4_tree.argtypes = [blob, vp, vp, vp, vp, i, i, f, vp]
+        lib.fa_kv4_tree_workspace.argtypes = [i] * 6
+        lib.fa_kv4_tree_workspace.restype = ll
+        lib.fa_kv4_tree.argtypes = [blob, vp, vp, vp, vp, i, i, f, vp, ll, vp]
         lib.fa_kv4_tree.restype = i
         lib.fa_tree_accept.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, vp, vp]
         lib.fa_tree_accept.restype = i

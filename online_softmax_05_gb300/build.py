@@ -35,7 +35,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-
 
 PRODUCT_UNITS = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_rope.cu", "fa_kv4_cache.cu",
                  "fa_kv4_decode.cu", "fa_cross_rows.cu",
-                 "fa_kv4_tree.cu", "fa_kv4_keep.cu"]
+                 "fa_kv4_tree.cu", "fa_kv4_keep.cu", "fa_split_join.cu"]
 PROBE_UNITS = ["fa_probe.cu"]
 
 

@@ -702,8 +702,18 @@ int fa_kv4_evict(const fa_kv4_cache* cache, const float* weights, const int* slo
     return ws.release(rc);
 }
 
+long long fa_kv4_tree_workspace(int B, int Hq, int Hkv, int N, int D, int slots) {
+    if (B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || N < 1 || slots < 16 || slots % 16 != 0) return FA_ERR_SHAPE;
+    if (static_cast<long long>(B) * Hkv > 65535 || static_cast<long long>(B) * Hq > INT_MAX / N) return FA_ERR_SHAPE;
+    if ((D != 64 && D != 128) || N > FA_TREE_MAX_PLACES) return FA_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    const int rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return static_cast<long long>(fa::kv4_tree_workspace({B, Hkv, D, 64, 16, 1, slots / 16}, Hq, N, sms));
+}
+
 int fa_kv4_tree(const fa_kv4_cache* cache, const void* q, const int* parents, void* o, float* lse, int Hq, int N,
-                float scale, void* stream) {
+                float scale, void* workspace, long long workspace_bytes, void* stream) {
     int rc = check_kv4(cache);
     if (rc != FA_OK) return rc;
     if (!q || !parents || !o || !lse) return FA_ERR_NULL;
@@ -721,8 +731,18 @@ int fa_kv4_tree(const fa_kv4_cache* cache, const void* q, const int* parents, vo
     int dev = 0, sms = 0;
     rc = current_device(&dev, &sms);
     if (rc != FA_OK) return rc;
-    return fa::launch_kv4_tree(kv4_shape(cache), cache->pool, cache->block_table, cache->lengths, parents, q, o, lse, Hq, N,
-                               scale, static_cast<cudaStream_t>(stream), knobs(), sms);
+    const size_t need = fa::kv4_tree_workspace(kv4_shape(cache), Hq, N, sms);
+    if (workspace) {
+        const Range w = range_of(workspace, need);
+        if (overlaps_any(w, ins, 5) || overlap(w, ro) || overlap(w, rl)) return FA_ERR_ARG;
+    }
+    Workspace ws;
+    rc = ws.take(workspace, static_cast<size_t>(workspace_bytes > 0 ? workspace_bytes : 0), need,
+                 static_cast<cudaStream_t>(stream));
+    if (rc != FA_OK) return rc;
+    rc = fa::launch_kv4_tree(kv4_shape(cache), cache->pool, cache->block_table, cache->lengths, parents, q, o, lse, Hq, N,
+                             scale, ws.ptr, static_cast<cudaStream_t>(stream), knobs(), sms);
+    return ws.release(rc);
 }
 
 int fa_tree_accept(const int* parents, const void* tokens, const void* picks, const void* first, int tokens_64, int B,

@@ -109,8 +109,9 @@ int launch_kv4_decode(const Kv4Shape& c, const void* pool, const int* table, con
                       void* o, float* lse, int Hq, int Tq, float scale, bool causal, const float* weights,
                       float* weights_out, long long slots, void* workspace, cudaStream_t stream, int num_sms);
 int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* parents,
-                    const void* q, void* o, float* lse, int Hq, int N, float scale, cudaStream_t stream,
+                    const void* q, void* o, float* lse, int Hq, int N, float scale, void* workspace, cudaStream_t stream,
                     const DebugKnobs& dbg, int num_sms);
+size_t kv4_tree_workspace(const Kv4Shape& c, int Hq, int N, int num_sms);
 int launch_tree_accept(const int* parents, const void* tokens, const void* picks, const void* first, int tokens64, int B,
                        int N, int* path, int* counts, void* next, cudaStream_t stream);
 int launch_kv4_keep(const Kv4Shape& c, void* pool, const int* table, const int* lengths, const int* path, int N,

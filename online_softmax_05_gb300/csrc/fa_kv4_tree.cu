@@ -22,17 +22,18 @@
 // group that is NaN goes into the products as 0 and into the rows that see it at the end.
 //
 // Per CTA: warps 0-3 and 4-7 softmax (two tiles of 128 rows; with at most 128 rows the two take
-// every other tile of keys instead and are joined at the end), warps 8-11 fetch and unpack
-// 64 tokens at a time (a thread a token, 8 and 9 keys, 10 and 11 values, each copying the bytes that it
-// will use four tiles ahead), warp 12 issues tcgen05.mma.  The tokens are split over a cluster
-// of CTAs, joined as in fa_cross_rows.cu.
-#include <cooperative_groups.h>
+// every other tile of keys instead and are joined at the end), two teams of four warps fetch and unpack
+// tiles of 64 tokens in turn (a thread a token's keys or values, copying the bytes that it will use
+// four tiles ahead), the last warp issues tcgen05.mma.  Q is the products' operand in tensor memory: with both
+// operands in shared memory an instruction of 64 keys takes its 48 cycles of reads, not 32.
+// A ragged batch is cut over the CTAs by fa_split.cuh.
 #include <cuda_runtime.h>
 
 #include "fa_check.cuh"
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_ptx.cuh"
+#include "fa_split.cuh"
 #include "fa_tree.cuh"
 #include "fa_wait.cuh"
 
@@ -42,12 +43,14 @@ static __device__ int g_status_kv4_tree;
 
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kThreads = 416;
+constexpr int kTeams = 2;       // of four unpacking warps, a tile each in turn
+constexpr int kUnpackWarps = 4 * kTeams;
+constexpr int kThreads = (8 + kUnpackWarps + 1) * 32;
+constexpr int kMmaWarp = 8 + kUnpackWarps;
 constexpr int kTok = 64;       // of a tile
-constexpr int kRaw = 4;        // tiles of codes on their way
-constexpr int kMaxSplit = 8;   // CTAs of a cluster
+constexpr int kRaw = 2;        // tiles of codes on their way to a team
+constexpr int kUnitRows = 256;  // of a CTA
+constexpr int kLeast = 6;      // tiles that are not worth cutting
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kKeyUnit = 0x1p-16f, kValueUnit = 0x1p-24f;
@@ -55,29 +58,30 @@ constexpr float kKeyUnit = 0x1p-16f, kValueUnit = 0x1p-24f;
 template <int D_, int G_>
 struct TreeCfg : Kv4<D_, G_> {
     using L = Kv4<D_, G_>;
-    static constexpr int kWords = D_ / 8;                  // 32-bit words of a row of codes
     static constexpr int kTile = kTok * D_ * 2;            // an operand tile of keys or values
     static constexpr int kAugTile = kTok * 32;             // 16 more channels a token
     static constexpr int kStage = 3 * kTile + kAugTile;    // sa n, sb n, V, minima
-    static constexpr int kStages = D_ == 128 ? 2 : 4;
-    static constexpr int kQTile = 128 * D_ * 2, kQAug = 128 * 32;
+    static constexpr int kStages = D_ == 128 ? 3 : 4;
+    static constexpr int kQAug = 128 * 32;
     static constexpr int kQOff = kStages * kStage;
-    static constexpr int kRawOff = kQOff + 2 * (kQTile + kQAug);
-    static constexpr int kRawTile = 128 * (L::kRow + L::kScaleRow);  // and then all threads' scales
+    static constexpr int kRawOff = kQOff + 2 * kQAug;
+    static constexpr int kRawTile = kUnpackWarps * 32 * (L::kRow + L::kScaleRow);  // of all threads: a row's codes, scales
     static constexpr int kBarOff = kRawOff + kRaw * kRawTile;
-    // full[], empty[], s_full[2][2], p_full[2][2], pv_done[2], o_full, q_full, mma_done
-    static constexpr int kNumBars = 2 * kStages + 8 + 2 + 3;
+    // full[], empty[], s_full[2], p_full[2], o_full, q_full, mma_done
+    static constexpr int kNumBars = 2 * kStages + 4 + 3;
     static constexpr int kMlOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // [2][2][128] row maxima and sums
     static constexpr int kTreeOff = kMlOff + 4 * 128 * 4;    // [64] ancestors
     static constexpr int kPoisonOff = kTreeOff + 64 * 8;     // [groups] places whose value group is NaN
     static constexpr int kMaskOff = kPoisonOff + 4 * 8;      // [stages] tokens that are there
     static constexpr int kMiscOff = kMaskOff + kStages * 8;
-    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+    static constexpr int kSmemBytes = kMiscOff + 16 + sizeof(SplitItem) + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-    static_assert(kRawOff >= 2 * 128 * D_ * 4, "two tiles of scaled rows go where the stages and Q were");
-    // TMEM: per half t two S tiles of 64 tokens (P over them) and O
-    __device__ static constexpr uint32_t kS(int t, int buf) { return 256u * t + 64u * buf; }
-    __device__ static constexpr uint32_t kO(int t) { return 256u * t + 128u; }
+    static_assert(kSmemBytes > 114 * 1024, "one CTA an SM: it takes all of tensor memory");
+    static_assert(kRawOff + kRaw * kRawTile >= 2 * 128 * D_ * 4, "two tiles of scaled rows go where the stages were");
+    // TMEM: O of both halves, S of both (P over it), Q of both
+    __device__ static constexpr uint32_t kO(int t) { return 128u * t; }
+    __device__ static constexpr uint32_t kS(int t) { return 256u + 64u * t; }
+    __device__ static constexpr uint32_t kQ(int t) { return 384u + 64u * t; }
     static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTok, false, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D_, false, true);
 };
@@ -89,6 +93,8 @@ struct TreeParams {
     const int* parents;
     __nv_bfloat16* o;
     float* lse;
+    SplitPlan plan;
+    SplitParts parts;
     int N, R, row_units;
     float sl2;
     unsigned long long timeout_ns;
@@ -138,12 +144,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     const uint32_t base = smem_u32(smem), bars = base + C::kBarOff;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (ST + s); };
-    auto s_full = [&](int t, int b) { return bars + 8u * (2 * ST + 2 * t + b); };
-    auto p_full = [&](int t, int b) { return bars + 8u * (2 * ST + 4 + 2 * t + b); };
-    auto pv_done = [&](int t) { return bars + 8u * (2 * ST + 8 + t); };
-    const uint32_t o_full = bars + 8u * (2 * ST + 10), q_full = o_full + 8, mma_done = o_full + 16;
-    auto sQ = [&](int t) { return base + C::kQOff + t * (C::kQTile + C::kQAug); };
-    auto sQAug = [&](int t) { return sQ(t) + C::kQTile; };
+    auto s_full = [&](int t) { return bars + 8u * (2 * ST + t); };
+    auto p_full = [&](int t) { return bars + 8u * (2 * ST + 2 + t); };
+    const uint32_t o_full = bars + 8u * (2 * ST + 4), q_full = o_full + 8, mma_done = o_full + 16;
+    auto sQAug = [&](int t) { return base + C::kQOff + t * C::kQAug; };
     auto sStage = [&](int s) { return base + s * C::kStage; };
     float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
     unsigned long long* tree = reinterpret_cast<unsigned long long*>(smem + C::kTreeOff);
@@ -152,81 +156,103 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     const WaitCtl ctl{abort_flag, &g_status_kv4_tree, p.timeout_ns};
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-
+    SplitItem* s_item = reinterpret_cast<SplitItem*>(smem + C::kMiscOff + 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int unit = blockIdx.x / splits;
-    const int ru = unit % p.row_units, bh = unit / p.row_units;
-    const int b = bh / p.pages.heads, hk = bh % p.pages.heads;
-    const int row0 = ru * 256, rows = min(256, p.R - row0);
-    const bool paired = rows > 128;  // two tiles of rows; otherwise the halves take every other tile of keys
 
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    wait_for_stream();
+    auto length_of = [&](int b) {
+        const int len = __ldg(p.lengths + b);
+        if (len >= 0 && len <= p.pages.capacity() && (len == 0 || len >= p.N)) return len;
+        atomicCAS(&g_status_kv4_tree, 0, kStatusBadSeqlen);
+        return 0;
+    };
+    if (warp == 0) {
+        const SplitItem it =
+            split_item(p.plan, blockIdx.x, lane, [&](int b) { return (length_of(b) + kTok - 1) / kTok; });
+        if (lane == 0) *s_item = it;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const SplitItem item = *s_item;
+    if (item.unit < 0) {  // more CTAs than pieces
+        if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+        return;
+    }
+    const int b = item.b, ru = item.unit % p.row_units, hk = item.unit / p.row_units;
+    const int bh = b * p.pages.heads + hk;
+    const int row0 = ru * kUnitRows, rows = min(kUnitRows, p.R - row0);
+    const bool paired = rows > 128;  // two tiles of rows; otherwise the halves take every other tile of keys
+    const int len = length_of(b), ctx = len - p.N;  // tokens, and those before the tree
+    const int j0 = item.j0, n = item.n;             // this CTA's tiles
+
+    // softmax warps of a half that have rows
+    auto active = [&](int t) { return paired ? (t == 0 ? 4 : (rows - 97) / 32) : (rows + 31) / 32; };
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), 4);
             mbar_init(empty(s), 1);
         }
         for (int t = 0; t < 2; ++t) {
-            for (int y = 0; y < 2; ++y) {
-                mbar_init(s_full(t, y), 1);
-                mbar_init(p_full(t, y), 4);
-            }
-            mbar_init(pv_done(t), 1);
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), active(t));
         }
         mbar_init(o_full, 1);
-        mbar_init(q_full, paired ? 8 : 4);
+        mbar_init(q_full, 8);
         mbar_init(mma_done, 1);
         for (int g = 0; g < NG; ++g) poison[g] = 0;
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 12) {
-        tmem_alloc(smem_u32(tmem_slot), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-    wait_for_stream();
-
-    int len = __ldg(p.lengths + b);
-    if (len < 0 || len > p.pages.capacity() || (len > 0 && len < p.N)) {
-        if (tid == 0) atomicCAS(&g_status_kv4_tree, 0, kStatusBadSeqlen);
-        len = 0;
-    }
-    const int ctx = len - p.N;  // tokens before the tree
-    const int all = (len + kTok - 1) / kTok, share = (all + splits - 1) / splits;
-    const int j0 = min(all, rank * share), n = min(all - j0, share);  // this CTA's tiles
 
     // a softmax thread's row, state and what it sees of the tree
-    const int t = warp >> 2, r = tid & 127;
+    const int t = warp >> 2 & 1, r = tid & 127;
     const int row = row0 + (paired ? 128 * t : 0) + r;
     float m = -INFINITY, l = 0.f;
     unsigned long long sees = 0;
     const uint32_t lane_base = tmem + ((32u * (warp & 3)) << 16);
 
-    if (warp >= 8 && warp < 12) {
+    if (warp >= 8 && warp < kMmaWarp) {
         // ------------------------------------------------------------ fetch and unpack
-        const bool is_v = warp >= 10;
-        const int tok = tid & 63, th = tid - 256;
-        constexpr int CH = C::kRow / 16;  // 16-byte chunks of a row of codes
-        const uint32_t raw = base + C::kRawOff + th * C::kRow, raw_scales = base + C::kRawOff + 128 * C::kRow + th * C::kScaleRow;
+        constexpr int CH = C::kRow / 16, kWords = C::kRow / 4;  // 16-byte chunks and words of a row of codes
+        const int th = tid - 256, team = th >> 7, tok = th & 63;
+        const bool is_v = th >> 6 & 1;
+        const uint32_t raw = base + C::kRawOff + th * C::kRow,
+                       raw_scales = base + C::kRawOff + kUnpackWarps * 32 * C::kRow + th * C::kScaleRow;
         const int turn = (tok / (8 / CH)) % CH;  // the chunks' order in shared memory, against bank conflicts
         const int section = is_v ? C::kValueCodes : C::kKeyCodes, scales = is_v ? C::kValueScales : C::kKeyScales;
         const int rowb = tok & 15;
+        const int mine = (n + kTeams - 1 - team) / kTeams;  // this team's tiles: team, team + kTeams, ..
         uint32_t here = 0;  // bit i: this thread's token is there in raw tile i
+        // the table's entry for this thread's token of tile i, read a tile ahead of its use; and the block in that page
+        const int* entries = p.pages.table + static_cast<long long>(b) * p.pages.width;
+        int page = -1, inside = 0;
+        auto look_up = [&](int i) {
+            const int at = (j0 + team + kTeams * i) * kTok + tok, block = at >> 4;
+            if (i < mine && at < len) {
+                const int e = p.pages.shift >= 0 ? block >> p.pages.shift : block / p.pages.blocks_page;
+                inside = block - e * p.pages.blocks_page;
+                page = __ldg(entries + e);  // len is within the table
+            }
+        };
+        look_up(0);
         auto fetch = [&](int i) {
-            if (i < n) {
-                const int at = (j0 + i) * kTok + tok;
+            if (i < mine) {
+                const int at = (j0 + team + kTeams * i) * kTok + tok;
                 const int slot = i % kRaw;
                 here &= ~(1u << slot);
                 if (at < len) {
-                    const long long off = p.pages.block_of(b, at >> 4);
-                    if (off >= 0) {
+                    if (page >= 0 && page < p.pages.num_pages) {
                         here |= 1u << slot;
-                        const unsigned char* from = p.pages.pool + off + hk * p.pages.head_bytes();
+                        const unsigned char* from =
+                            p.pages.pool + (page * static_cast<long long>(p.pages.heads) + hk) * p.pages.head_bytes() +
+                            inside * C::kBlock;
 #pragma unroll
                         for (int c = 0; c < CH; ++c)
                             copy_async<16>(raw + slot * C::kRawTile + ((c ^ turn) << 4), from + section + rowb * C::kRow + c * 16);
@@ -237,13 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            look_up(i + 1);
         };
         for (int i = 0; i < kRaw; ++i) fetch(i);
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < mine; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-            const int slot = i % kRaw, st = i % ST;
+            const int j = team + kTeams * i, slot = i % kRaw, st = j % ST;
             const bool there = here >> slot & 1;
-            uint32_t w[C::kWords], sc[NG];
+            uint32_t w[kWords], sc[NG];
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 uint32_t x[4];
@@ -255,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
 #pragma unroll
             for (int g = 0; g < NG; ++g) sc[g] = there ? sc[g] : 0u;
             fetch(i + kRaw);
-            if (!wait_warp(empty(st), ((i / ST) & 1) ^ 1, ctl)) break;
+            if (!wait_warp(empty(st), ((j / ST) & 1) ^ 1, ctl)) break;
             const uint32_t stage = sStage(st);
             if (!is_v) {
                 uint32_t sa[NG], sb[NG], ca[NG], cb[NG];  // pairs: the parts of s, and -128 of them
@@ -271,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                     mn[g] = x.y * kKeyUnit;
                 }
 #pragma unroll
-                for (int c = 0; c < C::kWords; ++c) {
+                for (int c = 0; c < kWords; ++c) {
                     const int g = c % S32 * 32 / G;
                     uint32_t ya[4], yb[4];
 #pragma unroll
@@ -294,10 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                                  pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
                                  pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
                 const uint32_t mask = __ballot_sync(0xffffffffu, there);
-                if (lane == 0) masks[2 * st + (warp - 8)] = mask;
+                if (lane == 0) masks[2 * st + (tok >> 5)] = mask;
             } else {
                 float vs[NG], vm[NG];
-                const int place = (j0 + i) * kTok + tok - ctx;
+                const int place = (j0 + j) * kTok + tok - ctx;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const float2 x = kv4_scale(sc[g]);
@@ -310,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < C::kWords; ++c) {
+                for (int c = 0; c < kWords; ++c) {
                     const int g0 = 2 * c % S32 * 32 / G, g1 = (2 * c + 1) % S32 * 32 / G;
                     const uint32_t s2 = pack_bf16x2(vs[g0], vs[g1]), m2 = pack_bf16x2(vm[g0], vm[g1]);
                     uint32_t y[4];
@@ -319,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                         const uint32_t x = ((w[c] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
                         y[e] = fma_pair(as_u32(__hsub2(as_bf2(x), as_bf2(0x43004300u))), s2, m2);
                     }
-                    st_shared_v4(stage + 2 * C::kTile + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1], y[2],
-                                 y[3]);
+                    st_shared_v4(stage + 2 * C::kTile + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1],
+                                 y[2], y[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -328,56 +355,68 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             if (lane == 0) mbar_arrive(full(st));
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 12) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ matrix instructions
         const bool leader = elect_one_sync();
-        const SDesc dQ = sdesc_make(sQ(0), 16, 1024), dK = sdesc_make(sStage(0), 16, 1024),
-                    dV = sdesc_make(sStage(0) + 2 * C::kTile, kTok * 128, 1024),
+        const SDesc dK = sdesc_make(sStage(0), 16, 1024), dV = sdesc_make(sStage(0) + 2 * C::kTile, kTok * 128, 1024),
                     dQA = sdesc_sw32(sQAug(0)), dKA = sdesc_sw32(sStage(0) + 3 * C::kTile);
-        constexpr uint32_t kStage16 = C::kStage >> 4, kQ16 = (C::kQTile + C::kQAug) >> 4;
-        auto issue_s = [&](int h, int i, int st) {  // the i-th tile of half h
-            const uint32_t to = tmem + C::kS(h, i & 1), qo = paired ? h * kQ16 : 0u, ko = st * kStage16;
+        constexpr uint32_t kStage16 = C::kStage >> 4;
+        auto issue_s = [&](int h, int st) {
+            const uint32_t to = tmem + C::kS(h), q = paired ? h : 0, ko = st * kStage16;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
                     if (leader)
-                        mma_ss_d(to, dQ, qo + (((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4), dK,
+                        mma_ts_d(to, tmem + C::kQ(q) + 8 * s, dK,
                                  ko + ((part * C::kTile + (s >> 2) * (kTok * 128) + (s & 3) * 32) >> 4), C::kIdescS,
                                  part > 0 || s > 0);
             if (leader) {
-                mma_ss_d(to, dQA, qo, dKA, ko, C::kIdescS, 1);
-                mma_commit(s_full(h, i & 1));
+                mma_ss_d(to, dQA, q * (C::kQAug >> 4), dKA, ko, C::kIdescS, 1);
+                mma_commit(s_full(h));
             }
         };
-        if (n > 0 && wait_warp(q_full, 0, ctl) && wait_warp(full(0), 0, ctl)) {
+        auto ready = [&](int j) -> bool {
+            if (!wait_warp(full(j % ST), (j / ST) & 1, ctl)) return false;
             tc_fence_after();
-            for (int h = 0; h < (paired ? 2 : 1); ++h) issue_s(h, 0, 0);
+            return true;
+        };
+        auto issue_pv = [&](int h, int i, int st) -> bool {  // the i-th tile of half h
+            if (!wait_warp(p_full(h), i & 1, ctl)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < kTok / 16; ++s)
+                if (leader)
+                    mma_ts_d(tmem + C::kO(h), tmem + C::kS(h) + s * 8, dV, st * kStage16 + s * (2048 >> 4), C::kIdescPV,
+                             (i > 0 || s > 0) ? 1u : 0u);
+            return true;
+        };
+        // S of a half follows P V of it, whose P lies in the same columns; the halves alternate
+        if (n > 0 && wait_warp(q_full, 0, ctl) && ready(0)) {
+            issue_s(0, 0);
+            if (paired) issue_s(1, 0);
+            else if (n > 1 && ready(1)) issue_s(1, 1);
             for (int j = 0; j < n; ++j) {
                 const int st = j % ST;
-                if (j + 1 < n) {
-                    const int s1 = (j + 1) % ST;
-                    if (!wait_warp(full(s1), ((j + 1) / ST) & 1, ctl)) break;
-                    tc_fence_after();
-                    for (int h = 0; h < 2; ++h)
-                        if (paired || h == ((j + 1) & 1)) issue_s(h, paired ? j + 1 : (j + 1) >> 1, s1);
-                }
                 bool ok = true;
-                for (int h = 0; h < 2 && ok; ++h) {
-                    if (!paired && h != (j & 1)) continue;
-                    const int i = paired ? j : j >> 1;
-                    ok = wait_warp(p_full(h, i & 1), (i >> 1) & 1, ctl);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int s = 0; s < kTok / 16; ++s)
-                        if (leader)
-                            mma_ts_d(tmem + C::kO(h), tmem + C::kS(h, i & 1) + s * 8, dV, st * kStage16 + s * (2048 >> 4),
-                                     C::kIdescPV, (i > 0 || s > 0) ? 1u : 0u);
-                    if (leader) mma_commit(pv_done(h));
+                if (paired) {
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        ok = issue_pv(h, j, st);
+                        if (h == 1 && leader && ok) mma_commit(empty(st));
+                        if (ok && j + 1 < n) {
+                            ok = h == 1 || ready(j + 1);
+                            if (ok) issue_s(h, (j + 1) % ST);
+                        }
+                    }
+                } else {
+                    ok = issue_pv(j & 1, j >> 1, st);
+                    if (leader && ok) mma_commit(empty(st));
+                    if (ok && j + 2 < n) {
+                        ok = ready(j + 2);
+                        if (ok) issue_s(j & 1, (j + 2) % ST);
+                    }
                 }
                 if (!ok) break;
-                if (leader) mma_commit(empty(st));
             }
         }
         if (leader) {
@@ -390,18 +429,24 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         // ------------------------------------------------------------ softmax
         float factor;
         {
-            uint4 x[D / 8];
             const bool there = row < row0 + rows;
             const uint4* from = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(bh) * p.R + row) * D);
+            auto chunk = [&](int c, float (&f)[8], float up) {
+                const uint4 x = there ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) x[c] = there ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(y[e] << 16) * up;
+                    f[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u) * up;
+                }
+            };
             float top = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-                const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                float f[8];
+                chunk(c, f, 1.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    top = fmax3(top, fabsf(__uint_as_float(y[e] << 16)), fabsf(__uint_as_float(y[e] & 0xffff0000u)));
+                for (int e = 0; e < 8; e += 2) top = fmax3(top, fabsf(f[e]), fabsf(f[e + 1]));
             }
             const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
             const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((127 - ex) << 23), p.sl2);
@@ -410,21 +455,20 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 float sum[NG];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) sum[g] = 0.f;
-                const int half = paired ? t : 0;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {  // channels 8 c .. 8 c + 7 go where the codes' words have them
-                    const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-                    float f[8];
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    uint32_t x[32];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[2 * e] = __uint_as_float(y[e] << 16) * up;
-                        f[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u) * up;
+                    for (int k = 0; k < 8; ++k) {  // the channels of the codes' word 8 hf + k, in its pairs
+                        const int word = 8 * hf + k, c = word % S32 * 4 + word / S32;
+                        float f[8];
+                        chunk(c, f, up);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) sum[c * 8 / G] += f[e];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[4 * k + e] = pack_bf16x2(f[e], f[e + 4]);
                     }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[c * 8 / G] += f[e];
-                    const int word = c % 4 * S32 + c / 4;
-                    st_shared_v4(sQ(half) + (word >> 3) * (128 * 128) + sw128_off(r, word & 7), pack_bf16x2(f[0], f[4]),
-                                 pack_bf16x2(f[1], f[5]), pack_bf16x2(f[2], f[6]), pack_bf16x2(f[3], f[7]));
+                    tmem_st32(lane_base + C::kQ(t) + 32 * hf, x);
                 }
                 float c[16];
 #pragma unroll
@@ -437,13 +481,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    st_shared_v4(sQAug(half) + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
+                    st_shared_v4(sQAug(t) + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
                                  pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
                                  pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
+                tmem_st_wait();
+                tc_fence_before();
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
             if (warp == 0) {
                 unsigned long long up[2];
                 tree_ancestors(p.parents + static_cast<size_t>(b) * p.N, p.N, lane, up);
@@ -451,15 +497,27 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 tree[lane + 32] = up[1];
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (there && len > 0) sees = tree[row % p.N];
+            if (row < row0 + rows && len > 0) sees = tree[row % p.N];
         }
         const int mine = paired ? n : (n + 1 - t) / 2;
-        for (int i = 0; i < mine; ++i) {
-            const int j = paired ? i : 2 * i + t, st = j % ST, buf = i & 1;
-            if (!wait_warp(s_full(t, buf), (i >> 1) & 1, ctl)) break;
+        for (int i = 0; i < mine && (warp & 3) < active(t); ++i) {
+            const int j = paired ? i : 2 * i + t, st = j % ST;
+            if (!wait_warp(s_full(t), i & 1, ctl)) break;
             if (!wait_warp(full(st), (j / ST) & 1, ctl)) break;  // has completed: what the unpacking warps wrote is seen
             tc_fence_after();
-            const uint32_t tS = lane_base + C::kS(t, buf), tO = lane_base + C::kO(t);
+            const uint32_t tS = lane_base + C::kS(t), tO = lane_base + C::kO(t);
+            const int t0 = (j0 + j) * kTok;
+            const uint32_t have0 = masks[2 * st], have1 = masks[2 * st + 1];
+            uint32_t v[2] = {0xffffffffu, 0xffffffffu};  // bit c: the row sees token t0 + c
+            const bool hides = t0 + kTok > ctx || (have0 & have1) != 0xffffffffu;
+            if (hides) {
+                unsigned long long vis = t0 >= ctx ? sees >> (t0 - ctx)
+                                         : ctx - t0 >= kTok ? ~0ull
+                                                            : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
+                vis &= have0 | static_cast<unsigned long long>(have1) << 32;
+                v[0] = static_cast<uint32_t>(vis);
+                v[1] = static_cast<uint32_t>(vis >> 32);
+            }
             uint32_t sr[64];
             tmem_ld32(tS, sr);
             tmem_ld32(tS + 32, sr + 32);
@@ -467,66 +525,54 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             reg_fence32(sr);
             reg_fence32(sr + 32);
             float* s = reinterpret_cast<float*>(sr);
-            const int t0 = (j0 + j) * kTok;
-            const uint32_t have0 = masks[2 * st], have1 = masks[2 * st + 1];
-            if (t0 + kTok > ctx || (have0 & have1) != 0xffffffffu) {
-                // bit c: the row sees token t0 + c
-                unsigned long long vis = t0 >= ctx ? sees >> (t0 - ctx)
-                                         : ctx - t0 >= kTok ? ~0ull
-                                                            : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
-                vis &= have0 | static_cast<unsigned long long>(have1) << 32;
-                const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
+            if (hides) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
-                    if (!((c < 32 ? v0 : v1) >> (c & 31) & 1)) s[c] = -INFINITY;
+                    if (!(v[c >> 5] >> (c & 31) & 1)) s[c] = -INFINITY;
             }
-            float mx8[8];
+            float mx4[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) mx8[c] = fmaxf(s[c], s[c + 8]);
+            for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(s[c], s[c + 4]);
 #pragma unroll
-            for (int c = 16; c < 64; c += 16)
+            for (int c = 8; c < 64; c += 8)
 #pragma unroll
-                for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], s[c + a], s[c + 8 + a]);
-            const float mx =
-                fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * factor;
+                for (int a = 0; a < 4; ++a) mx4[a] = fmax3(mx4[a], s[c + a], s[c + 4 + a]);
+            const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * factor;
             const bool grows = i > 0 && mx > m;
-            const float m_new = fmaxf(m, mx);
-            if (__any_sync(0xffffffffu, grows)) {
-                if (!wait_warp(pv_done(t), (i - 1) & 1, ctl)) break;
-                tc_fence_after();
-                const float alpha = grows ? ex2_approx(m - m_new) : 1.f;
-                l *= alpha;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * c, o);
-                    tmem_ld_wait();
-                    reg_fence32(o);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tmem_st32(tO + 32 * c, o);
-                }
-            }
+            const float m_new = fmaxf(m, mx), alpha = grows ? ex2_approx(m - m_new) : 1.f;
+            l *= alpha;
             m = m_new;
             const float ref = m == -INFINITY ? 0.f : -m;  // nothing seen yet
             const uint64_t f2x = f2(factor, factor), neg2 = f2(ref, ref);
-            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
                 float x0, x1;
                 f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), f2x, neg2), x0, x1);
                 const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                sum[c & 3] = add2(sum[c & 3], f2(p0, p1));
+                sum[c & 1] = add2(sum[c & 1], f2(p0, p1));
                 sr[c] = pack_bf16x2(p0, p1);
             }
             float s0, s1;
-            f2_split(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+            f2_split(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
             tmem_st32(tS, sr);
+            // (S was issued behind P V of the tile before it: O is complete)
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    tmem_ld32(tO + 32 * c, sr);
+                    tmem_ld_wait();
+                    reg_fence32(sr);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * alpha);
+                    tmem_st32(tO + 32 * c, sr);
+                }
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(t, buf));
+            if (lane == 0) mbar_arrive(p_full(t));
         }
         wait_warp(o_full, 0, ctl);
         tc_fence_after();
@@ -535,26 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     }
 
     // ------------------------------------------------------------ join
-    // a row's states: one a CTA, or two where the halves shared its keys
-    float factor = 0.f;
-    if (splits > 1) cluster.sync();
-    else __syncthreads();
+    // a row's states: one, or two where the halves shared its keys
+    __syncthreads();
+    const bool whole = item.pieces == 1;
     if (warp < 8) {
-        const int first = paired ? t : 0, last = paired ? t : 1;
-        float top = -INFINITY, sum = 0.f;
-        for (int c = 0; c < splits; ++c)
-            for (int h = first; h <= last; ++h) {
-                const float* x = (splits > 1 ? cluster.map_shared_rank(ml, c) : ml) + 256 * h + r;
-                if (x[128] != 0.f) top = fmaxf(top, x[0]);
-            }
-        for (int c = 0; c < splits; ++c)
-            for (int h = first; h <= last; ++h) {
-                const float* x = (splits > 1 ? cluster.map_shared_rank(ml, c) : ml) + 256 * h + r;
-                if (x[128] != 0.f) sum += x[128] * ex2_approx(x[0] - top);
-            }
+        float top = m, sum = l;
+        if (!paired) {
+            const float ma = ml[r], la = ml[128 + r], mb = ml[256 + r], lb = ml[384 + r];
+            top = fmaxf(la != 0.f ? ma : -INFINITY, lb != 0.f ? mb : -INFINITY);
+            sum = (la != 0.f ? la * ex2_approx(ma - top) : 0.f) + (lb != 0.f ? lb * ex2_approx(mb - top) : 0.f);
+        }
         const bool used = sees != 0 && l != 0.f;  // a place without a token gives 0
-        if (used) factor = ex2_approx(m - top) / sum * (1.f / kValueUnit);
-        const bool any = (paired || t == 0 ? n > 0 : n > 1);
+        const float factor = used ? ex2_approx(m - top) / sum * (1.f / kValueUnit) : 0.f;
+        const bool any = paired || t == 0 ? n > 0 : n > 1;
         // rows times their factors, fp32, channels in their order; 16-byte chunks turned by the row
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -574,62 +613,94 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                     uint32_t y[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float v = __uint_as_float(o[8 * k + 2 * e + h]) * factor;
-                        y[e] = used && any ? __float_as_uint(bad ? __int_as_float(0x7fffffff) : v) : 0u;
+                        const float x = __uint_as_float(o[8 * k + 2 * e + h]) * factor;
+                        y[e] = used && any ? __float_as_uint(bad ? __int_as_float(0x7fffffff) : x) : 0u;
                     }
                     st_shared_v4(base + (t * 128 + r) * (D * 4) + ((chunk ^ (r & (D / 4 - 1))) << 4), y[0], y[1], y[2], y[3]);
                 }
         }
-        if (rank == 0 && row < row0 + rows && (paired || t == 0))
-            p.lse[static_cast<size_t>(bh) * p.R + row] =
-                sees == 0 || sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
-    }
-    if (splits > 1) cluster.sync();
-    else __syncthreads();
-    // each CTA adds up and stores its share of the rows
-    for (int i = rank * kThreads + tid; i < rows * (D / 8); i += splits * kThreads) {
-        const int rr = i / (D / 8), c = i % (D / 8);
-        float x[8] = {};
-        for (int k = 0; k < splits; ++k) {
-            const uint8_t* from = splits > 1 ? cluster.map_shared_rank(smem, k) : smem;
-            for (int h = 0; h < (paired ? 1 : 2); ++h) {
-                const int at = rr + 128 * h;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float4 z = *reinterpret_cast<const float4*>(from + at * (D * 4) +
-                                                                      (((2 * c + y) ^ (at & (D / 4 - 1))) << 4));
-                    x[4 * y] += z.x;
-                    x[4 * y + 1] += z.y;
-                    x[4 * y + 2] += z.z;
-                    x[4 * y + 3] += z.w;
-                }
-            }
+        if (row < row0 + rows && (paired || t == 0)) {
+            const bool none = sees == 0 || sum == 0.f;
+            const float lse2 = none ? -INFINITY : top + __log2f(sum);
+            if (whole) p.lse[static_cast<size_t>(bh) * p.R + row] = lse2 * kLn2;
+            else p.parts.lse[static_cast<size_t>(blockIdx.x) * p.parts.rows + row - row0] = lse2;
         }
-        *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(bh) * p.R + row0 + rr) * D + c * 8) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
-    if (splits > 1) cluster.sync();  // the others may still read this CTA's rows
+    if (tid == 0 && blockIdx.x == item.first)
+        p.parts.units[bh * p.row_units + ru] = make_int2(item.first, item.pieces);
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 8); i += kThreads) {
+        const int rr = i / (D / 8), c = i % (D / 8);
+        float x[8];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            auto part = [&](int at) {
+                return *reinterpret_cast<const float4*>(smem + at * (D * 4) + (((2 * c + y) ^ (at & (D / 4 - 1))) << 4));
+            };
+            float4 z = part(rr);
+            if (!paired) {
+                const float4 w = part(rr + 128);
+                z = make_float4(z.x + w.x, z.y + w.y, z.z + w.z, z.w + w.w);
+            }
+            x[4 * y] = z.x;
+            x[4 * y + 1] = z.y;
+            x[4 * y + 2] = z.z;
+            x[4 * y + 3] = z.w;
+        }
+        if (whole) {
+            *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(bh) * p.R + row0 + rr) * D + c * 8) = make_uint4(
+                pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        } else {
+            float4* to = reinterpret_cast<float4*>(p.parts.o +
+                                                   (static_cast<size_t>(blockIdx.x) * p.parts.rows + rr) * D + c * 8);
+            to[0] = make_float4(x[0], x[1], x[2], x[3]);
+            to[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
 template <int D, int G>
-int launch_t(const TreeParams& p, int units, int splits, cudaStream_t stream) {
+int launch_t(const TreeParams& p, cudaStream_t stream) {
     static std::atomic<unsigned long long> allowed{0};
     auto kern = fa_kv4_tree_kernel<D, G>;
     if (!allow_shared_memory(kern, TreeCfg<D, G>::kSmemBytes, allowed)) return -5;
-    return launch_clusters(kern, units * splits, splits, kThreads, TreeCfg<D, G>::kSmemBytes, stream, p);
+    return launch_chained(kern, dim3(p.plan.items), kThreads, TreeCfg<D, G>::kSmemBytes, stream, p);
+}
+
+struct TreeUnits {
+    int row_units, rows;  // of a head; most rows of a unit
+    long long units;
+    int items;
+};
+TreeUnits units_of(const Kv4Shape& c, int Hq, int N, int num_sms) {
+    TreeUnits u;
+    const int R = Hq / c.Hkv * N;
+    u.row_units = (R + kUnitRows - 1) / kUnitRows;
+    u.rows = R < kUnitRows ? R : kUnitRows;
+    u.units = static_cast<long long>(c.B) * c.Hkv * u.row_units;
+    // no sequence of the table has tiles enough to be cut: an item a unit
+    const bool small = static_cast<long long>(c.width) * c.page_size <= kLeast * kTok;
+    u.items = small ? static_cast<int>(u.units) : split_items(u.units, num_sms);
+    return u;
 }
 
 }  // namespace
 
+size_t kv4_tree_workspace(const Kv4Shape& c, int Hq, int N, int num_sms) {
+    const TreeUnits u = units_of(c, Hq, N, num_sms);
+    return split_workspace(u.items, u.units, u.rows, c.D);
+}
+
 int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* parents,
-                    const void* q, void* o, float* lse, int Hq, int N, float scale, cudaStream_t stream,
+                    const void* q, void* o, float* lse, int Hq, int N, float scale, void* workspace, cudaStream_t stream,
                     const DebugKnobs& dbg, int num_sms) {
+    const TreeUnits u = units_of(c, Hq, N, num_sms);
     TreeParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.pages = kv4_pages(static_cast<unsigned char*>(const_cast<void*>(pool)), table, c.width, c.num_pages, c.Hkv,
@@ -640,16 +711,24 @@ int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const
     p.lse = lse;
     p.N = N;
     p.R = Hq / c.Hkv * N;
-    p.row_units = (p.R + 255) / 256;
+    p.row_units = u.row_units;
+    p.plan = {c.B, c.Hkv * u.row_units, u.items, kLeast};
+    p.parts = split_parts(workspace, u.items, u.rows, c.D);
     p.sl2 = scale * kLog2e;
     p.timeout_ns = dbg.timeout_ns;
-    const long long units = static_cast<long long>(c.B) * c.Hkv * p.row_units;
-    const long long tiles = (static_cast<long long>(c.width) * c.page_size + kTok - 1) / kTok;
-    int splits = 1;
-    while (splits < kMaxSplit && 4 * splits <= tiles && splits * units <= 2LL * num_sms) splits *= 2;
-    const int n = static_cast<int>(units);
-    if (c.D == 64) return c.group == 32 ? launch_t<64, 32>(p, n, splits, stream) : launch_t<64, 64>(p, n, splits, stream);
-    return c.group == 32 ? launch_t<128, 32>(p, n, splits, stream) : launch_t<128, 64>(p, n, splits, stream);
+    const int rc = c.D == 64 ? (c.group == 32 ? launch_t<64, 32>(p, stream) : launch_t<64, 64>(p, stream))
+                             : (c.group == 32 ? launch_t<128, 32>(p, stream) : launch_t<128, 64>(p, stream));
+    if (rc != 0 || u.items == u.units) return rc;
+    SplitOut out{};
+    out.o = {o, static_cast<long long>(Hq) * N * c.D, static_cast<long long>(N) * c.D, c.D};
+    out.lse = lse;
+    out.Hkv = c.Hkv;
+    out.group = Hq / c.Hkv;
+    out.T = N;
+    out.R = p.R;
+    out.row_units = u.row_units;
+    out.unit_rows = kUnitRows;
+    return launch_split_join(p.parts, out, c.B, c.D, u.items, stream);
 }
 
 int kv4_tree_take_status() {

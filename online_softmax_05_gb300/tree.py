@@ -14,6 +14,9 @@ from .kv4 import _account, _cache
 __all__ = ["attention_tree_kv4", "tree_accept", "kv4_keep"]
 
 
+_workspace_bytes: dict = {}
+
+
 def _check_parents(parents, B, N, dev):
     import torch
     if not (parents.dtype is torch.int32 and parents.shape == (B, N) and parents.is_contiguous()
@@ -23,7 +26,7 @@ def _check_parents(parents, B, N, dev):
 
 def _attention(q, pool, block_table, lengths, parents, scale, out, lse):
     import torch
-    packed, B, _, D, _, dev = _cache(pool, block_table, lengths)
+    packed, B, heads, D, slots, dev = _cache(pool, block_table, lengths)
     shape = q.shape
     if not (q.dtype is torch.bfloat16 and len(shape) == 4 and q.is_contiguous() and q.get_device() == dev
             and shape[0] == B and shape[3] == D):
@@ -39,8 +42,19 @@ def _attention(q, pool, block_table, lengths, parents, scale, out, lse):
     elif not (lse.dtype is torch.float32 and lse.shape == (B, Hq, N) and lse.is_contiguous()
               and lse.get_device() == dev):
         raise ValueError("lse must be a contiguous float32 (B, H, N) tensor on the pool's device")
-    rc = load_library().fa_kv4_tree(packed, q.data_ptr(), parents.data_ptr(), out.data_ptr(), lse.data_ptr(), Hq, N,
-                                    1.0 / math.sqrt(D) if scale is None else scale, _raw_stream(dev))
+    lib = load_library()
+    key = B, Hq, heads, N, D, slots, dev
+    need = _workspace_bytes.get(key)
+    if need is None:
+        need = lib.fa_kv4_tree_workspace(B, Hq, heads, N, D, slots)
+        if need < 0:
+            raise FAError(need, "fa_kv4_tree_workspace")
+        if len(_workspace_bytes) > 4096:
+            _workspace_bytes.clear()
+        _workspace_bytes[key] = need
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    rc = lib.fa_kv4_tree(packed, q.data_ptr(), parents.data_ptr(), out.data_ptr(), lse.data_ptr(), Hq, N,
+                         1.0 / math.sqrt(D) if scale is None else scale, workspace.data_ptr(), need, _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv4_tree")
     return out, lse

@@ -293,8 +293,10 @@ def cache(pool=1 << 20, table=1 << 24, lengths=1 << 25, B=2, heads=2, D=64, grou
     return struct.pack("QQQ7i4x", pool, table, lengths, B, heads, D, group, page, pages, width)
 
 
-def call(c=None, q=1 << 26, parents=1 << 27, o=1 << 28, lse=1 << 29, Hq=4, N=5, scale=0.1):
-    return fa.load_library().fa_kv4_tree(c or cache(), q, parents, o, lse, Hq, N, ctypes.c_float(scale), None)
+def call(c=None, q=1 << 26, parents=1 << 27, o=1 << 28, lse=1 << 29, Hq=4, N=5, scale=0.1,
+         workspace=None, size=0):
+    return fa.load_library().fa_kv4_tree(c or cache(), q, parents, o, lse, Hq, N, ctypes.c_float(scale), workspace, size,
+                                         None)
 
 
 def test_refusals_of_the_c_abi():
@@ -313,6 +315,9 @@ def test_refusals_of_the_c_abi():
     assert call(scale=float("nan")) == -8
     assert call(o=1 << 26) == -8 and call(lse=1 << 28) == -8 and call(o=1 << 20) == -8 and call(lse=1 << 27) == -8
     assert call(o=1 << 25) == -8
+    query = fa.load_library().fa_kv4_tree_workspace
+    assert query(0, 4, 2, 5, 64, 64) == -2 and query(2, 3, 2, 5, 64, 64) == -2 and query(2, 4, 2, 0, 64, 64) == -2
+    assert query(2, 4, 2, 5, 64, 60) == -2 and query(2, 4, 2, 65, 64, 64) == -3 and query(2, 4, 2, 5, 96, 64) == -3
 
 
 @pytest.mark.gpu
