@@ -3,8 +3,8 @@
 // The last N slots of a sequence are the tree's places; place i sees the context
 // before them, its ancestors and itself.  The rows of a key/value head (group x N) are
 // many enough for the tensor cores' 128-row tiles, which want whole operands in shared memory, so
-// the codes are unpacked there, once for up to 256 rows.  With k = s n + m and v = s n + m per
-// group of channels (fa_kv4.cuh):
+// the codes are unpacked there.  With k = s n + m and v = s n + m per group of channels
+// (fa_kv4.cuh):
 //   K   s = sa + sb, its upper and lower four bits of significand: sa n and sb n have
 //       eight bits and are exact in bf16.  S = q.(sa n) + q.(sb n) + sum_g m_g sum(q_g), the
 //       last as 16 more channels: m_g against three bf16 pieces (24 bits) of sum(q_g).
@@ -21,11 +21,12 @@
 // A token that a row does not see adds nothing whatever it holds: S is replaced, and a tree's value
 // group that is NaN goes into the products as 0 and into the rows that see it at the end.
 //
-// Per CTA: warps 0-3 and 4-7 softmax (two tiles of 128 rows; with at most 128 rows the two take
-// every other tile of keys instead and are joined at the end), two teams of four warps fetch and unpack
-// tiles of 64 tokens in turn (a thread a token's keys or values, copying the bytes that it will use
-// four tiles ahead), the last warp issues tcgen05.mma.  Q is the products' operand in tensor memory: with both
-// operands in shared memory an instruction of 64 keys takes its 48 cycles of reads, not 32.
+// Per CTA, 128 rows: warps 0-3 softmax of a tile's first 32 tokens, 4-7 of its last, the rows' maxima
+// exchanged through shared memory; two teams of four warps fetch and unpack tiles of 64 tokens
+// in turn (a thread a token's keys or values, copying the bytes that it will use four tiles ahead);
+// the last warp issues tcgen05.mma.  sa n and sb n lie side by side as 128 columns of one
+// product, added by the softmax warps: an instruction of 64 columns takes as long as one of 128.  Q
+// is in tensor memory: from shared memory it would take half of that memory's cycles.
 // A ragged batch is cut over the CTAs by fa_split.cuh.
 #include <cuda_runtime.h>
 
@@ -49,7 +50,7 @@ constexpr int kThreads = (8 + kUnpackWarps + 1) * 32;
 constexpr int kMmaWarp = 8 + kUnpackWarps;
 constexpr int kTok = 64;       // of a tile
 constexpr int kRaw = 2;        // tiles of codes on their way to a team
-constexpr int kUnitRows = 256;  // of a CTA
+constexpr int kUnitRows = 128;  // of a CTA
 constexpr int kLeast = 6;      // tiles that are not worth cutting
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -64,12 +65,12 @@ struct TreeCfg : Kv4<D_, G_> {
     static constexpr int kStages = D_ == 128 ? 3 : 4;
     static constexpr int kQAug = 128 * 32;
     static constexpr int kQOff = kStages * kStage;
-    static constexpr int kRawOff = kQOff + 2 * kQAug;
+    static constexpr int kRawOff = kQOff + kQAug;
     static constexpr int kRawTile = kUnpackWarps * 32 * (L::kRow + L::kScaleRow);  // of all threads: a row's codes, scales
     static constexpr int kBarOff = kRawOff + kRaw * kRawTile;
-    // full[], empty[], s_full[2], p_full[2], o_full, q_full, mma_done
-    static constexpr int kNumBars = 2 * kStages + 4 + 3;
-    static constexpr int kMlOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // [2][2][128] row maxima and sums
+    // full[], empty[], s_full[2], p_full[2], pv_done, o_full, q_full, mma_done
+    static constexpr int kNumBars = 2 * kStages + 4 + 4;
+    static constexpr int kMlOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // [2][2][128] row maxima of a tile's halves, by its parity
     static constexpr int kTreeOff = kMlOff + 4 * 128 * 4;    // [64] ancestors
     static constexpr int kPoisonOff = kTreeOff + 64 * 8;     // [groups] places whose value group is NaN
     static constexpr int kMaskOff = kPoisonOff + 4 * 8;      // [stages] tokens that are there
@@ -77,12 +78,12 @@ struct TreeCfg : Kv4<D_, G_> {
     static constexpr int kSmemBytes = kMiscOff + 16 + sizeof(SplitItem) + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kSmemBytes > 114 * 1024, "one CTA an SM: it takes all of tensor memory");
-    static_assert(kRawOff + kRaw * kRawTile >= 2 * 128 * D_ * 4, "two tiles of scaled rows go where the stages were");
-    // TMEM: O of both halves, S of both (P over it), Q of both
-    __device__ static constexpr uint32_t kO(int t) { return 128u * t; }
-    __device__ static constexpr uint32_t kS(int t) { return 256u + 64u * t; }
-    __device__ static constexpr uint32_t kQ(int t) { return 384u + 64u * t; }
-    static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTok, false, false);
+    static_assert(kQOff >= 128 * D_ * 4, "the scaled rows go where the stages were");
+    // TMEM: O, two tiles of S (sa n, sb n; P over the first 32 columns), Q
+    static constexpr uint32_t kO = 0, kQ = 384;
+    __device__ static constexpr uint32_t kS(int buf) { return 128u + 128u * buf; }
+    static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 2 * kTok, false, false);
+    static constexpr uint32_t kIdescAug = idesc_bf16_f32(128, kTok, false, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D_, false, true);
 };
 
@@ -135,6 +136,20 @@ __device__ __forceinline__ SDesc sdesc_sw32(uint32_t saddr) {
     return d;
 }
 
+// Barrier of two warps; whether a predicate holds in any of their threads.
+__device__ __forceinline__ bool any_of_pair(int barrier, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(x ? 1u : 0u), "r"(barrier)
+        : "memory");
+    return any != 0;
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) {
     using C = TreeCfg<D, G>;
@@ -144,10 +159,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     const uint32_t base = smem_u32(smem), bars = base + C::kBarOff;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (ST + s); };
-    auto s_full = [&](int t) { return bars + 8u * (2 * ST + t); };
-    auto p_full = [&](int t) { return bars + 8u * (2 * ST + 2 + t); };
-    const uint32_t o_full = bars + 8u * (2 * ST + 4), q_full = o_full + 8, mma_done = o_full + 16;
-    auto sQAug = [&](int t) { return base + C::kQOff + t * C::kQAug; };
+    auto s_full = [&](int buf) { return bars + 8u * (2 * ST + buf); };
+    auto p_full = [&](int buf) { return bars + 8u * (2 * ST + 2 + buf); };
+    const uint32_t pv_done = bars + 8u * (2 * ST + 4), o_full = pv_done + 8, q_full = pv_done + 16, mma_done = pv_done + 24;
+    const uint32_t sQAug = base + C::kQOff;
     auto sStage = [&](int s) { return base + s * C::kStage; };
     float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
     unsigned long long* tree = reinterpret_cast<unsigned long long*>(smem + C::kTreeOff);
@@ -187,12 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     const int b = item.b, ru = item.unit % p.row_units, hk = item.unit / p.row_units;
     const int bh = b * p.pages.heads + hk;
     const int row0 = ru * kUnitRows, rows = min(kUnitRows, p.R - row0);
-    const bool paired = rows > 128;  // two tiles of rows; otherwise the halves take every other tile of keys
     const int len = length_of(b), ctx = len - p.N;  // tokens, and those before the tree
     const int j0 = item.j0, n = item.n;             // this CTA's tiles
 
-    // softmax warps of a half that have rows
-    auto active = [&](int t) { return paired ? (t == 0 ? 4 : (rows - 97) / 32) : (rows + 31) / 32; };
+    const int active = (rows + 31) / 32;  // quarters of the tile that have rows
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), 4);
@@ -200,10 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), active(t));
+            mbar_init(p_full(t), 2 * active);
         }
+        mbar_init(pv_done, 1);
         mbar_init(o_full, 1);
-        mbar_init(q_full, 8);
+        mbar_init(q_full, 4);
         mbar_init(mma_done, 1);
         for (int g = 0; g < NG; ++g) poison[g] = 0;
         *abort_flag = 0;
@@ -212,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     __syncthreads();
 
     // a softmax thread's row, state and what it sees of the tree
-    const int t = warp >> 2 & 1, r = tid & 127;
-    const int row = row0 + (paired ? 128 * t : 0) + r;
+    const int half = warp >> 2 & 1, r = tid & 127;
+    const int row = row0 + r;
     float m = -INFINITY, l = 0.f;
     unsigned long long sees = 0;
     const uint32_t lane_base = tmem + ((32u * (warp & 3)) << 16);
@@ -307,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                         ya[e] = fma_pair(sa[g], x, ca[g]);
                         yb[e] = fma_pair(sb[g], x, cb[g]);
                     }
-                    const uint32_t at = stage + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7);
+                    const uint32_t at = stage + (c >> 3) * (2 * kTok * 128) + sw128_off(tok, c & 7);
                     st_shared_v4(at, ya[0], ya[1], ya[2], ya[3]);
-                    st_shared_v4(at + C::kTile, yb[0], yb[1], yb[2], yb[3]);
+                    st_shared_v4(at + kTok * 128, yb[0], yb[1], yb[2], yb[3]);
                 }
                 // the minima, three times each: against the three pieces of sum(q_g)
                 float c[16];
@@ -359,64 +373,40 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         // ------------------------------------------------------------ matrix instructions
         const bool leader = elect_one_sync();
         const SDesc dK = sdesc_make(sStage(0), 16, 1024), dV = sdesc_make(sStage(0) + 2 * C::kTile, kTok * 128, 1024),
-                    dQA = sdesc_sw32(sQAug(0)), dKA = sdesc_sw32(sStage(0) + 3 * C::kTile);
+                    dQA = sdesc_sw32(sQAug), dKA = sdesc_sw32(sStage(0) + 3 * C::kTile);
         constexpr uint32_t kStage16 = C::kStage >> 4;
-        auto issue_s = [&](int h, int st) {
-            const uint32_t to = tmem + C::kS(h), q = paired ? h : 0, ko = st * kStage16;
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    if (leader)
-                        mma_ts_d(to, tmem + C::kQ(q) + 8 * s, dK,
-                                 ko + ((part * C::kTile + (s >> 2) * (kTok * 128) + (s & 3) * 32) >> 4), C::kIdescS,
-                                 part > 0 || s > 0);
-            if (leader) {
-                mma_ss_d(to, dQA, q * (C::kQAug >> 4), dKA, ko, C::kIdescS, 1);
-                mma_commit(s_full(h));
-            }
-        };
-        auto ready = [&](int j) -> bool {
-            if (!wait_warp(full(j % ST), (j / ST) & 1, ctl)) return false;
+        auto issue_s = [&](int j) -> bool {
+            const int st = j % ST, buf = j & 1;
+            if (!wait_warp(full(st), (j / ST) & 1, ctl)) return false;
             tc_fence_after();
-            return true;
-        };
-        auto issue_pv = [&](int h, int i, int st) -> bool {  // the i-th tile of half h
-            if (!wait_warp(p_full(h), i & 1, ctl)) return false;
-            tc_fence_after();
+            const uint32_t to = tmem + C::kS(buf), ko = st * kStage16;
 #pragma unroll
-            for (int s = 0; s < kTok / 16; ++s)
+            for (int s = 0; s < D / 16; ++s)
                 if (leader)
-                    mma_ts_d(tmem + C::kO(h), tmem + C::kS(h) + s * 8, dV, st * kStage16 + s * (2048 >> 4), C::kIdescPV,
-                             (i > 0 || s > 0) ? 1u : 0u);
+                    mma_ts_d(to, tmem + C::kQ + 8 * s, dK, ko + (((s >> 2) * (2 * kTok * 128) + (s & 3) * 32) >> 4),
+                             C::kIdescS, s > 0);
+            if (leader) {
+                mma_ss_d(to, dQA, 0, dKA, ko, C::kIdescAug, 1);
+                mma_commit(s_full(buf));
+            }
             return true;
         };
-        // S of a half follows P V of it, whose P lies in the same columns; the halves alternate
-        if (n > 0 && wait_warp(q_full, 0, ctl) && ready(0)) {
-            issue_s(0, 0);
-            if (paired) issue_s(1, 0);
-            else if (n > 1 && ready(1)) issue_s(1, 1);
+        // S(j + 1) is computed beside the softmax of tile j; its buffer's P, of tile j - 1, has been multiplied
+        if (n > 0 && wait_warp(q_full, 0, ctl) && issue_s(0)) {
             for (int j = 0; j < n; ++j) {
-                const int st = j % ST;
-                bool ok = true;
-                if (paired) {
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        ok = issue_pv(h, j, st);
-                        if (h == 1 && leader && ok) mma_commit(empty(st));
-                        if (ok && j + 1 < n) {
-                            ok = h == 1 || ready(j + 1);
-                            if (ok) issue_s(h, (j + 1) % ST);
-                        }
-                    }
-                } else {
-                    ok = issue_pv(j & 1, j >> 1, st);
-                    if (leader && ok) mma_commit(empty(st));
-                    if (ok && j + 2 < n) {
-                        ok = ready(j + 2);
-                        if (ok) issue_s(j & 1, (j + 2) % ST);
-                    }
+                const int st = j % ST, buf = j & 1;
+                if (j + 1 < n && !issue_s(j + 1)) break;
+                if (!wait_warp(p_full(buf), (j >> 1) & 1, ctl)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kTok / 16; ++s)
+                    if (leader)
+                        mma_ts_d(tmem + C::kO, tmem + C::kS(buf) + s * 8, dV, st * kStage16 + s * (2048 >> 4), C::kIdescPV,
+                                 (j > 0 || s > 0) ? 1u : 0u);
+                if (leader) {
+                    mma_commit(pv_done);
+                    mma_commit(empty(st));
                 }
-                if (!ok) break;
             }
         }
         if (leader) {
@@ -451,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
             const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((127 - ex) << 23), p.sl2);
             factor = p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * __int_as_float((127 + ex) << 23) * (1.f / kKeyUnit);
-            if (paired || t == 0) {
+            if (half == 0) {
                 float sum[NG];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) sum[g] = 0.f;
@@ -468,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[4 * k + e] = pack_bf16x2(f[e], f[e + 4]);
                     }
-                    tmem_st32(lane_base + C::kQ(t) + 32 * hf, x);
+                    tmem_st32(lane_base + C::kQ + 32 * hf, x);
                 }
                 float c[16];
 #pragma unroll
@@ -481,15 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    st_shared_v4(sQAug(t) + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
+                    st_shared_v4(sQAug + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
                                  pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
                                  pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
                 fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
             if (warp == 0) {
                 unsigned long long up[2];
                 tree_ancestors(p.parents + static_cast<size_t>(b) * p.N, p.N, lane, up);
@@ -499,46 +489,49 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (row < row0 + rows && len > 0) sees = tree[row % p.N];
         }
-        const int mine = paired ? n : (n + 1 - t) / 2;
-        for (int i = 0; i < mine && (warp & 3) < active(t); ++i) {
-            const int j = paired ? i : 2 * i + t, st = j % ST;
-            if (!wait_warp(s_full(t), i & 1, ctl)) break;
-            if (!wait_warp(full(st), (j / ST) & 1, ctl)) break;  // has completed: what the unpacking warps wrote is seen
+        const uint32_t tO = lane_base + C::kO + half * (D / 2);
+        bool ok = true;  // a wait that ran out ends the loop of both halves at their next barrier
+        for (int j = 0; j < n && (warp & 3) < active; ++j) {
+            const int st = j % ST, buf = j & 1;
+            // (full has completed: what the unpacking warps wrote is seen)
+            ok = ok && wait_warp(s_full(buf), (j >> 1) & 1, ctl) && wait_warp(full(st), (j / ST) & 1, ctl);
             tc_fence_after();
-            const uint32_t tS = lane_base + C::kS(t), tO = lane_base + C::kO(t);
-            const int t0 = (j0 + j) * kTok;
-            const uint32_t have0 = masks[2 * st], have1 = masks[2 * st + 1];
-            uint32_t v[2] = {0xffffffffu, 0xffffffffu};  // bit c: the row sees token t0 + c
-            const bool hides = t0 + kTok > ctx || (have0 & have1) != 0xffffffffu;
-            if (hides) {
-                unsigned long long vis = t0 >= ctx ? sees >> (t0 - ctx)
-                                         : ctx - t0 >= kTok ? ~0ull
-                                                            : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
-                vis &= have0 | static_cast<unsigned long long>(have1) << 32;
-                v[0] = static_cast<uint32_t>(vis);
-                v[1] = static_cast<uint32_t>(vis >> 32);
-            }
-            uint32_t sr[64];
-            tmem_ld32(tS, sr);
-            tmem_ld32(tS + 32, sr + 32);
+            const uint32_t tS = lane_base + C::kS(buf);
+            uint32_t sr[32], sb[32];
+            tmem_ld32(tS + 32 * half, sr);
+            tmem_ld32(tS + kTok + 32 * half, sb);
+            const int t0 = (j0 + j) * kTok + 32 * half;
+            const uint32_t have = masks[2 * st + half];
             tmem_ld_wait();
             reg_fence32(sr);
-            reg_fence32(sr + 32);
+            reg_fence32(sb);
             float* s = reinterpret_cast<float*>(sr);
-            if (hides) {
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (!(v[c >> 5] >> (c & 31) & 1)) s[c] = -INFINITY;
+            for (int c = 0; c < 32; c += 2)
+                f2_split(add2(f2(s[c], s[c + 1]), f2(__uint_as_float(sb[c]), __uint_as_float(sb[c + 1]))), s[c], s[c + 1]);
+            if (t0 + 32 > ctx || have != 0xffffffffu) {
+                // bit c: the row sees token t0 + c
+                const unsigned long long vis = t0 >= ctx ? sees >> min(t0 - ctx, 63)
+                                               : ctx - t0 >= 32 ? ~0ull
+                                                                : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
+                const uint32_t v = t0 - ctx > 63 ? 0u : static_cast<uint32_t>(vis) & have;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (!(v >> c & 1)) s[c] = -INFINITY;
             }
             float mx4[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(s[c], s[c + 4]);
 #pragma unroll
-            for (int c = 8; c < 64; c += 8)
+            for (int c = 8; c < 32; c += 8)
 #pragma unroll
                 for (int a = 0; a < 4; ++a) mx4[a] = fmax3(mx4[a], s[c + a], s[c + 4 + a]);
-            const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * factor;
-            const bool grows = i > 0 && mx > m;
+            float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * factor;
+            // with the other half's maximum; behind the barrier both have read S, and P may go over it
+            ml[256 * buf + 128 * half + r] = mx;
+            if (any_of_pair(2 + (warp & 3), !ok)) break;
+            mx = fmaxf(mx, ml[256 * buf + 128 * (half ^ 1) + r]);
+            const bool grows = j > 0 && mx > m;
             const float m_new = fmaxf(m, mx), alpha = grows ? ex2_approx(m - m_new) : 1.f;
             l *= alpha;
             m = m_new;
@@ -546,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             const uint64_t f2x = f2(factor, factor), neg2 = f2(ref, ref);
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
+            for (int c = 0; c < 16; ++c) {
                 float x0, x1;
                 f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), f2x, neg2), x0, x1);
                 const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -556,50 +549,45 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             float s0, s1;
             f2_split(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
-            tmem_st32(tS, sr);
-            // (S was issued behind P V of the tile before it: O is complete)
+            tmem_st16(tS + 16 * half, sr);
             if (__any_sync(0xffffffffu, grows)) {
+                ok = wait_warp(pv_done, (j - 1) & 1, ctl);  // O holds the tiles before
+                tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    tmem_ld32(tO + 32 * c, sr);
+                for (int c = 0; c < D / 64; ++c) {
+                    tmem_ld32(tO + 32 * c, sb);
                     tmem_ld_wait();
-                    reg_fence32(sr);
+                    reg_fence32(sb);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * alpha);
-                    tmem_st32(tO + 32 * c, sr);
+                    for (int e = 0; e < 32; ++e) sb[e] = __float_as_uint(__uint_as_float(sb[e]) * alpha);
+                    tmem_st32(tO + 32 * c, sb);
                 }
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(t));
+            if (lane == 0) mbar_arrive(p_full(buf));
         }
         wait_warp(o_full, 0, ctl);
         tc_fence_after();
-        ml[256 * t + r] = m;
-        ml[256 * t + 128 + r] = l;
     }
 
     // ------------------------------------------------------------ join
-    // a row's states: one, or two where the halves shared its keys
     __syncthreads();
     const bool whole = item.pieces == 1;
+    if (warp < 8) ml[128 * half + r] = l;
+    __syncthreads();
     if (warp < 8) {
-        float top = m, sum = l;
-        if (!paired) {
-            const float ma = ml[r], la = ml[128 + r], mb = ml[256 + r], lb = ml[384 + r];
-            top = fmaxf(la != 0.f ? ma : -INFINITY, lb != 0.f ? mb : -INFINITY);
-            sum = (la != 0.f ? la * ex2_approx(ma - top) : 0.f) + (lb != 0.f ? lb * ex2_approx(mb - top) : 0.f);
-        }
-        const bool used = sees != 0 && l != 0.f;  // a place without a token gives 0
-        const float factor = used ? ex2_approx(m - top) / sum * (1.f / kValueUnit) : 0.f;
-        const bool any = paired || t == 0 ? n > 0 : n > 1;
+        const float sum = ml[r] + ml[128 + r];
+        const bool used = sees != 0 && sum != 0.f;  // a place without a token gives 0
+        const float factor = used ? 1.f / sum * (1.f / kValueUnit) : 0.f;
         // rows times their factors, fp32, channels in their order; 16-byte chunks turned by the row
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
+            const int at = half * (D / 64) + c;  // 32 columns
             uint32_t o[32];
-            if (any) {
-                tmem_ld32(lane_base + C::kO(t) + 32 * c, o);
+            if (n > 0) {
+                tmem_ld32(lane_base + C::kO + 32 * at, o);
                 tmem_ld_wait();
                 reg_fence32(o);
             }
@@ -607,21 +595,20 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // half-word 2 (4 c + k) + h of the codes holds channels 32 g + 4 r' .. + 3
-                    const int hw = 2 * (4 * c + k) + h, g = hw % S32, chunk = 8 * g + hw / S32;
+                    // half-word 2 (4 at + k) + h of the codes holds channels 32 g + 4 r' .. + 3
+                    const int hw = 2 * (4 * at + k) + h, g = hw % S32, chunk = 8 * g + hw / S32;
                     const bool bad = (sees & poison[g * 32 / G]) != 0;
                     uint32_t y[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float x = __uint_as_float(o[8 * k + 2 * e + h]) * factor;
-                        y[e] = used && any ? __float_as_uint(bad ? __int_as_float(0x7fffffff) : x) : 0u;
+                        y[e] = used && n > 0 ? __float_as_uint(bad ? __int_as_float(0x7fffffff) : x) : 0u;
                     }
-                    st_shared_v4(base + (t * 128 + r) * (D * 4) + ((chunk ^ (r & (D / 4 - 1))) << 4), y[0], y[1], y[2], y[3]);
+                    st_shared_v4(base + r * (D * 4) + ((chunk ^ (r & (D / 4 - 1))) << 4), y[0], y[1], y[2], y[3]);
                 }
         }
-        if (row < row0 + rows && (paired || t == 0)) {
-            const bool none = sees == 0 || sum == 0.f;
-            const float lse2 = none ? -INFINITY : top + __log2f(sum);
+        if (row < row0 + rows && half == 0) {
+            const float lse2 = used ? m + __log2f(sum) : -INFINITY;
             if (whole) p.lse[static_cast<size_t>(bh) * p.R + row] = lse2 * kLn2;
             else p.parts.lse[static_cast<size_t>(blockIdx.x) * p.parts.rows + row - row0] = lse2;
         }
@@ -634,14 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         float x[8];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            auto part = [&](int at) {
-                return *reinterpret_cast<const float4*>(smem + at * (D * 4) + (((2 * c + y) ^ (at & (D / 4 - 1))) << 4));
-            };
-            float4 z = part(rr);
-            if (!paired) {
-                const float4 w = part(rr + 128);
-                z = make_float4(z.x + w.x, z.y + w.y, z.z + w.z, z.w + w.w);
-            }
+            const float4 z =
+                *reinterpret_cast<const float4*>(smem + rr * (D * 4) + (((2 * c + y) ^ (rr & (D / 4 - 1))) << 4));
             x[4 * y] = z.x;
             x[4 * y + 1] = z.y;
             x[4 * y + 2] = z.z;
