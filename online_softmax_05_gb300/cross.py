@@ -18,8 +18,14 @@ _autograd_cls = None
 
 def _fits(t) -> bool:
     """Whether the kernels take the tensor by its strides."""
-    return (t.stride(3) == 1 and t.data_ptr() % 16 == 0
-            and all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])))
+    b, h, s, c = t.stride()
+    if c != 1 or t.data_ptr() & 15:
+        return False
+    if b > 0 and h > 0 and s > 0 and not (b | h | s) & 7:
+        return True
+    B, H, T, _ = t.shape  # a dimension of one may have any stride
+    return ((B == 1 or (b > 0 and not b & 7)) and (H == 1 or (h > 0 and not h & 7))
+            and (T == 1 or (s > 0 and not s & 7)))
 
 
 def _tensor(t, name, shape, dev) -> bytes:
@@ -29,7 +35,12 @@ def _tensor(t, name, shape, dev) -> bytes:
     if not _fits(t):
         raise ValueError(f"{name} must have contiguous channels, 16-byte alignment and strides that are positive "
                          "multiples of 8")
-    return _pack_tensor(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    return _packed(t)
+
+
+def _packed(t) -> bytes:
+    b, h, s, _ = t.stride()
+    return _pack_tensor(t.data_ptr(), b, h, s)
 
 
 def _shape(q, k, key_lengths):
@@ -45,9 +56,8 @@ def _shape(q, k, key_lengths):
     if key_lengths is not None and not (key_lengths.dtype is torch.int32 and key_lengths.shape == (B,)
                                         and key_lengths.is_contiguous() and key_lengths.get_device() == dev):
         raise ValueError("key_lengths must be a contiguous int32 (B,) tensor on the device of q")
-    for n in (B, Hq, Hkv, Tq, Tk):
-        if n >= 1 << 31:
-            raise ValueError("a dimension is out of range")
+    if max(B, Hq, Hkv, Tq, Tk) >= 1 << 31:
+        raise ValueError("a dimension is out of range")
     packed = _pack_shape(B, Hq, Hkv, Tq, Tk, D, 0 if key_lengths is None else key_lengths.data_ptr())
     return packed, (B, Hq, Tq, D), (B, Hkv, Tk, D), dev
 
@@ -70,15 +80,17 @@ def _rest(rest, shape, dev):
 def _forward(q, k, v, key_lengths, scale, out, lse, rest):
     import torch
     packed, rows, keys, dev = _shape(q, k, key_lengths)
-    tensors = [_tensor(q, "q", rows, dev), _tensor(k, "k", keys, dev), _tensor(v, "v", keys, dev)]
+    qp, kp, vp = _tensor(q, "q", rows, dev), _tensor(k, "k", keys, dev), _tensor(v, "v", keys, dev)
     if out is None:
         out = torch.empty_like(q)
-    tensors.append(_tensor(out, "out", rows, dev))
+        op = _packed(out)
+    else:
+        op = _tensor(out, "out", rows, dev)
     if lse is None:
         lse = torch.empty(rows[:3], device=q.device, dtype=torch.float32)
     else:
         _check_lse(lse, rows[:3], dev)
-    rc = load_library().fa_cross_fwd(packed, *tensors, _rest(rest, rows, dev), lse.data_ptr(),
+    rc = load_library().fa_cross_fwd(packed, qp, kp, vp, op, _rest(rest, rows, dev), lse.data_ptr(),
                                      1.0 / math.sqrt(rows[3]) if scale is None else scale, _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_cross_fwd")

@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             else p.parts.lse[static_cast<size_t>(blockIdx.x) * p.parts.rows + row - row0] = lse2;
         }
     }
-    if (tid == 0 && blockIdx.x == item.first)
+    if (p.parts.units != nullptr && tid == 0 && blockIdx.x == item.first)
         p.parts.units[bh * p.row_units + ru] = make_int2(item.first, item.pieces);
     __syncthreads();
     for (int i = tid; i < rows * (D / 8); i += kThreads) {
@@ -675,7 +675,7 @@ TreeUnits units_of(const Kv4Shape& c, int Hq, int N, int num_sms) {
 
 size_t kv4_tree_workspace(const Kv4Shape& c, int Hq, int N, int num_sms) {
     const TreeUnits u = units_of(c, Hq, N, num_sms);
-    return split_workspace(u.items, u.units, u.rows, c.D);
+    return u.items == u.units ? 0 : split_workspace(u.items, u.units, u.rows, c.D);
 }
 
 int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* parents,
@@ -694,7 +694,7 @@ int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const
     p.R = Hq / c.Hkv * N;
     p.row_units = u.row_units;
     p.plan = {c.B, c.Hkv * u.row_units, u.items, kLeast};
-    p.parts = split_parts(workspace, u.items, u.rows, c.D);
+    if (u.items != u.units) p.parts = split_parts(workspace, u.items, u.rows, c.D);
     p.sl2 = scale * kLog2e;
     p.timeout_ns = dbg.timeout_ns;
     const int rc = c.D == 64 ? (c.group == 32 ? launch_t<64, 32>(p, stream) : launch_t<64, 64>(p, stream))

@@ -52,9 +52,10 @@ def _attention(q, pool, block_table, lengths, parents, scale, out, lse):
         if len(_workspace_bytes) > 4096:
             _workspace_bytes.clear()
         _workspace_bytes[key] = need
-    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     rc = lib.fa_kv4_tree(packed, q.data_ptr(), parents.data_ptr(), out.data_ptr(), lse.data_ptr(), Hq, N,
-                         1.0 / math.sqrt(D) if scale is None else scale, workspace.data_ptr(), need, _raw_stream(dev))
+                         1.0 / math.sqrt(D) if scale is None else scale, workspace.data_ptr() if need else None, need,
+                         _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv4_tree")
     return out, lse
@@ -77,18 +78,22 @@ def _accept(parents, tokens, picks, first):
     B, N = parents.shape
     dev = parents.get_device()
     _check_parents(parents, B, N, dev)
-    if tokens.dtype not in (torch.int32, torch.int64):
+    kind, shape, device = tokens.dtype, parents.shape, parents.device
+    if kind is not torch.int64 and kind is not torch.int32:
         raise ValueError("tokens must be int32 or int64")
-    for t, name, shape in ((tokens, "tokens", (B, N)), (picks, "picks", (B, N)), (first, "first", (B,))):
-        if t is not None and not (t.dtype is tokens.dtype and t.shape == shape and t.is_contiguous()
-                                  and t.get_device() == dev):
-            raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of the tokens' type on the same device")
+    if not (tokens.shape == shape and tokens.is_contiguous() and tokens.get_device() == dev):
+        raise ValueError("tokens must be a contiguous (B, N) tensor on the same device")
+    if not (picks.dtype is kind and picks.shape == shape and picks.is_contiguous() and picks.get_device() == dev):
+        raise ValueError("picks must be a contiguous (B, N) tensor of the tokens' type on the same device")
+    if first is not None and not (first.dtype is kind and first.shape == (B,) and first.is_contiguous()
+                                  and first.get_device() == dev):
+        raise ValueError("first must be a contiguous (B,) tensor of the tokens' type on the same device")
     path = torch.empty_like(parents)
-    counts = torch.empty(B, dtype=torch.int32, device=parents.device)
-    follow = torch.empty(B, dtype=tokens.dtype, device=parents.device)
+    counts = torch.empty(B, dtype=torch.int32, device=device)
+    follow = torch.empty(B, dtype=kind, device=device)
     rc = load_library().fa_tree_accept(parents.data_ptr(), tokens.data_ptr(), picks.data_ptr(),
-                                       None if first is None else first.data_ptr(), int(tokens.dtype is torch.int64), B,
-                                       N, path.data_ptr(), counts.data_ptr(), follow.data_ptr(), _raw_stream(dev))
+                                       None if first is None else first.data_ptr(), kind is torch.int64, B, N,
+                                       path.data_ptr(), counts.data_ptr(), follow.data_ptr(), _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_tree_accept")
     return path, counts, follow
