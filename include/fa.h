@@ -243,10 +243,11 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
  *                     bf16 took off, written by the forward for the backward, whose
  *                     rowsum(dO o O) is then of O to 16 bits.  Without it dq is less exact where
  *                     keys have a mean.
- *   workspace       : fa_cross_bwd: fa_cross_bwd_workspace(B, Hq, Hkv, Tq, Tk, D)
- *                     bytes, 256-byte aligned, used until the call's work on `stream` is
- *                     done; or NULL: taken with cudaMallocAsync.  FA_ERR_SCRATCH if
- *                     workspace_bytes is too small.  The forward takes none.
+ *   workspace       : fa_cross_fwd_workspace / fa_cross_bwd_workspace(B, Hq, Hkv, Tq,
+ *                     Tk, D) bytes (0 for a forward that cuts no keys), 16-byte and
+ *                     256-byte aligned, used until the call's work on `stream` is done; or
+ *                     NULL: taken with cudaMallocAsync.  FA_ERR_SCRATCH if
+ *                     workspace_bytes is too small.
  * B * Hq * Tq and B * Hkv * Tk within int32.  FA_ERR_ALIGN for a base that is not
  * 16-byte aligned or a stride that is no multiple of 8; FA_ERR_ARG for a stride
  * below 1, an output whose rows may share elements, or one whose range of addresses
@@ -263,7 +264,8 @@ typedef struct fa_cross_tensor {
 } fa_cross_tensor;
 int fa_cross_fwd(const fa_cross_shape* shape, const fa_cross_tensor* q, const fa_cross_tensor* k,
                  const fa_cross_tensor* v, const fa_cross_tensor* o, void* o_rest, float* lse, float scale,
-                 void* stream);
+                 void* workspace, long long workspace_bytes, void* stream);
+long long fa_cross_fwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D);
 long long fa_cross_bwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D);
 int fa_cross_bwd(const fa_cross_shape* shape, const fa_cross_tensor* q, const fa_cross_tensor* k,
                  const fa_cross_tensor* v, const fa_cross_tensor* o, const void* o_rest,

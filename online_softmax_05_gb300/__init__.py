@@ -109,8 +109,10 @@ def load_library():
         lib.fa_kv4_evict_workspace.restype = ll
         lib.fa_kv4_evict.argtypes = [blob, vp, vp, ll, i, i, vp, vp, vp, vp, vp, ll, vp]
         lib.fa_kv4_evict.restype = i
-        lib.fa_cross_fwd.argtypes = [blob] * 5 + [vp, vp, f, vp]
+        lib.fa_cross_fwd.argtypes = [blob] * 5 + [vp, vp, f, vp, ll, vp]
         lib.fa_cross_fwd.restype = i
+        lib.fa_cross_fwd_workspace.argtypes = [i] * 6
+        lib.fa_cross_fwd_workspace.restype = ll
         lib.fa_cross_bwd_workspace.argtypes = [i] * 6
         lib.fa_cross_bwd_workspace.restype = ll
         lib.fa_cross_bwd.argtypes = [blob] * 5 + [vp, blob, vp] + [blob] * 3 + [f, vp, ll, vp]

@@ -14,6 +14,7 @@ _pack_shape = struct.Struct("6iQ").pack
 _pack_tensor = struct.Struct("Q3q").pack
 _lock = threading.Lock()
 _autograd_cls = None
+_forward_bytes: dict = {}
 
 
 def _fits(t) -> bool:
@@ -90,8 +91,20 @@ def _forward(q, k, v, key_lengths, scale, out, lse, rest):
         lse = torch.empty(rows[:3], device=q.device, dtype=torch.float32)
     else:
         _check_lse(lse, rows[:3], dev)
-    rc = load_library().fa_cross_fwd(packed, qp, kp, vp, op, _rest(rest, rows, dev), lse.data_ptr(),
-                                     1.0 / math.sqrt(rows[3]) if scale is None else scale, _raw_stream(dev))
+    lib = load_library()
+    key = rows, keys, dev
+    need = _forward_bytes.get(key)
+    if need is None:
+        need = lib.fa_cross_fwd_workspace(rows[0], rows[1], keys[1], rows[2], keys[2], rows[3])
+        if need < 0:
+            raise FAError(need, "fa_cross_fwd_workspace")
+        if len(_forward_bytes) > 4096:
+            _forward_bytes.clear()
+        _forward_bytes[key] = need
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    rc = lib.fa_cross_fwd(packed, qp, kp, vp, op, _rest(rest, rows, dev), lse.data_ptr(),
+                          1.0 / math.sqrt(rows[3]) if scale is None else scale,
+                          workspace.data_ptr() if need else None, need, _raw_stream(dev))
     if rc != FA_OK:
         raise FAError(rc, "fa_cross_fwd")
     return out, lse

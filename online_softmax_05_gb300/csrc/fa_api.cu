@@ -386,7 +386,8 @@ int check_cross_tensor(const fa_cross_tensor* x, int B, int heads, int T, int D,
 extern "C" {
 
 int fa_cross_fwd(const fa_cross_shape* s, const fa_cross_tensor* q, const fa_cross_tensor* k, const fa_cross_tensor* v,
-                 const fa_cross_tensor* o, void* o_rest, float* lse, float scale, void* stream) {
+                 const fa_cross_tensor* o, void* o_rest, float* lse, float scale, void* workspace,
+                 long long workspace_bytes, void* stream) {
     if (!s || !lse) return FA_ERR_NULL;
     int rc = check_cross(s, scale);
     if (rc != FA_OK) return rc;
@@ -407,8 +408,28 @@ int fa_cross_fwd(const fa_cross_shape* s, const fa_cross_tensor* q, const fa_cro
     rc = current_device(&dev, &sms);
     if (rc != FA_OK) return rc;
     const fa::CrossShape shape{s->B, s->Hq, s->Hkv, s->Tq, s->Tk, s->D, s->key_lengths};
-    const auto launch = fa::cross_rows_wanted(shape) ? fa::launch_cross_rows : fa::launch_cross_fwd;
-    return launch(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, static_cast<cudaStream_t>(stream), knobs(), sms);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!fa::cross_rows_wanted(shape))
+        return fa::launch_cross_fwd(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, st, knobs(), sms);
+    const size_t need = fa::cross_rows_workspace(shape, sms);
+    if (workspace) {
+        const Range w = range_of(workspace, need);
+        if (overlaps_any(w, r, 4) || overlaps_any(w, outs, 3)) return FA_ERR_ARG;
+    }
+    Workspace ws;
+    rc = ws.take(workspace, static_cast<size_t>(workspace_bytes > 0 ? workspace_bytes : 0), need, st);
+    if (rc != FA_OK) return rc;
+    return ws.release(fa::launch_cross_rows(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, ws.ptr, st, knobs(), sms));
+}
+
+long long fa_cross_fwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D) {
+    const fa_cross_shape s{B, Hq, Hkv, Tq, Tk, D, nullptr};
+    int rc = check_cross(&s, 1.f);
+    if (rc != FA_OK) return rc;
+    int dev = 0, sms = 0;
+    rc = current_device(&dev, &sms);
+    if (rc != FA_OK) return rc;
+    return static_cast<long long>(fa::cross_rows_workspace({B, Hq, Hkv, Tq, Tk, D, nullptr}, sms));
 }
 
 long long fa_cross_bwd_workspace(int B, int Hq, int Hkv, int Tq, int Tk, int D) {

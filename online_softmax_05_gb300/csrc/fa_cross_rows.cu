@@ -1,11 +1,9 @@
 // fa_cross_rows.cu -- cross attention of a few query rows over many keys on sm_103a.
 //
 // The rows of one key/value head, its group's heads times their Tq queries, are packed into
-// a tile of 128 (row = head in the group x Tq + query), so that K and V are read once
-// whatever the grouping, and the keys are split over a cluster of CTAs, whose states
-//   m = max S, l = sum 2^(S - m), acc = sum 2^(S - m) V      (scores in log2 units)
-// join by the online-softmax rule through distributed shared memory:
-//   M = max m_c,  L = sum l_c 2^(m_c - M),  O = sum acc_c 2^(m_c - M) / L.
+// tiles of 128 (row = head in the group x Tq + query), so that K and V are read once
+// whatever the grouping, and the keys of a ragged batch are cut over the CTAs by fa_split.cuh,
+// their pieces joined by a second kernel.
 //
 // Per CTA: warps 0-3 softmax (a TMEM lane is a row), warp 4 loads (TMA, K and V tiles of 128
 // keys in one ring), warp 5 issues tcgen05.mma: S = Q K^T, then O += P V with P, in bf16, in the
@@ -13,12 +11,12 @@
 // and fill each other's gaps, and the ring keeps loads in flight meanwhile.  K's and V's bytes
 // bound it; the tensor cores' 128-row tiles are mostly padding then, which costs nothing
 // that is not idle.
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "fa_check.cuh"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
+#include "fa_split.cuh"
 #include "fa_tmap.h"
 #include "fa_wait.cuh"
 
@@ -28,11 +26,10 @@ static __device__ int g_status_cross_rows;
 
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kThreads = 192;
 constexpr int kKeys = 128;   // of a tile
-constexpr int kMaxSplit = 8; // CTAs of a cluster
+constexpr int kRows = 128;   // of a unit
+constexpr int kLeast = 1;    // tiles that are not worth cutting (12 tiles in pieces of 1, 2, 4: 9.6, 10.3, 12.4 us)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -46,9 +43,8 @@ struct RowsCfg {
     static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
     // kv_full[], kv_empty[], q_full, s_full, p_full, o_full, mma_done
     static constexpr int kNumBars = 2 * kStages + 5;
-    static constexpr int kMlOff = kBarOff + kNumBars * 8 + 8;  // [2][128] row maxima and sums, for the cluster
-    static constexpr int kMiscOff = kMlOff + 2 * 128 * 4;
-    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;    // + tensor memory's address, abort flag; alignment
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8 + 8;
+    static constexpr int kSmemBytes = kMiscOff + 16 + sizeof(SplitItem) + 1024;  // + tensor memory's address, abort flag; alignment
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
     static_assert(kBarOff >= 128 * D * 4, "a CTA's scaled rows go where Q and the ring were");
     // 256 TMEM columns: S (P over its first half), O
@@ -62,6 +58,8 @@ struct RowsParams {
     __nv_bfloat16* o_rest;
     float* lse;
     const int* key_lengths;
+    SplitPlan plan;
+    SplitParts parts;
     int Hq, Hkv, group, Tq, Tk, R, row_tiles;
     float sl2, sl2_eff;
     int prescale;
@@ -80,20 +78,41 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto kv_empty = [&](int s) { return bars + 8u * (C::kStages + s); };
     const uint32_t q_full = bars + 8u * (2 * C::kStages), s_full = q_full + 8, p_full = q_full + 16,
                    o_full = q_full + 24, mma_done = q_full + 32;
-    float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     const WaitCtl ctl{abort_flag, &g_status_cross_rows, p.timeout_ns};
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int splits = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    SplitItem* s_item = reinterpret_cast<SplitItem*>(smem + C::kMiscOff + 16);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int unit = blockIdx.x / splits;
-    const int tile = unit % p.row_tiles, bh = unit / p.row_tiles;
-    const int b = bh / p.Hkv, hk = bh % p.Hkv;
-    const int rows = min(128, p.R - tile * 128);  // of this tile
-    const int active = (rows + 31) / 32;          // softmax warps with rows
-
+    if (warp == 5) {
+        tmem_alloc(smem_u32(tmem_slot), 256);
+        tmem_relinquish();
+    }
+    wait_for_stream();
+    auto keys_of = [&](int b) {
+        const int keys = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.Tk;
+        if (keys >= 0 && keys <= p.Tk) return keys;
+        atomicCAS(&g_status_cross_rows, 0, kStatusBadSeqlen);
+        return 0;
+    };
+    if (warp == 0) {
+        const SplitItem it =
+            split_item(p.plan, blockIdx.x, lane, [&](int b) { return (keys_of(b) + kKeys - 1) / kKeys; });
+        if (lane == 0) *s_item = it;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    const SplitItem item = *s_item;
+    if (item.unit < 0) {  // more CTAs than pieces
+        if (warp == 5) tmem_dealloc(tmem, 256);
+        return;
+    }
+    const int b = item.b, tile = item.unit % p.row_tiles, hk = item.unit / p.row_tiles, bh = b * p.Hkv + hk;
+    const int rows = min(kRows, p.R - tile * kRows);  // of this tile
+    const int active = (rows + 31) / 32;              // softmax warps with rows
+    const int keys = keys_of(b), j0 = item.j0, n = item.n;  // this CTA's key tiles
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(kv_full(s), 1);
@@ -107,24 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 5) {
-        tmem_alloc(smem_u32(tmem_slot), 256);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-    wait_for_stream();
-
-    // this CTA's key tiles
-    int keys = p.key_lengths != nullptr ? __ldg(p.key_lengths + b) : p.Tk;
-    if (keys < 0 || keys > p.Tk) {
-        if (tid == 0) atomicCAS(&g_status_cross_rows, 0, kStatusBadSeqlen);
-        keys = 0;
-    }
-    const int all = (keys + kKeys - 1) / kKeys, share = (all + splits - 1) / splits;
-    const int j0 = min(all, rank * share), n = min(all - j0, share);
 
     // a softmax thread's row: its state, and whether it is one
     const int r = 32 * warp + lane;
@@ -289,33 +291,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         wait_warp(o_full, 0, ctl);
         tc_fence_after();
-        ml[r] = m;
-        ml[128 + r] = l;
     }
 
-    // ------------------------------------------------------------ join
+    // ------------------------------------------------------------ outputs
     // (o_full and the loads' drain are behind every thread: Q and the ring are free)
-    float factor = 0.f;
-    if (splits > 1) {
-        cluster.sync();
-        if (warp < active) {
-            float top = -INFINITY, sum = 0.f;
-            for (int c = 0; c < splits; ++c) top = fmaxf(top, cluster.map_shared_rank(ml, c)[r]);
-            for (int c = 0; c < splits; ++c) {
-                const float* x = cluster.map_shared_rank(ml, c);
-                const float lc = x[128 + r];
-                if (lc != 0.f) sum += lc * ex2_approx(x[r] - top);  // (a CTA without keys has l = 0)
-            }
-            if (l != 0.f) factor = ex2_approx(m - top) / sum;
-            m = top;
-            l = sum;
-        }
-    } else if (l != 0.f) {
-        factor = 1.f / l;
-    }
+    const bool whole = item.pieces == 1;
     __syncthreads();
     if (warp < active) {
         // rows times their factors: fp32 into shared memory, 16-byte chunks turned by the row against conflicts
+        const float factor = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -331,26 +315,32 @@ __global__ void __launch_bounds__(kThreads, 2)
                 st_shared_v4(sQ + r * (D * 4) + (((8 * c + g) ^ (r & (D / 4 - 1))) << 4), o[4 * g], o[4 * g + 1],
                              o[4 * g + 2], o[4 * g + 3]);
         }
-        if (rank == 0 && r < rows)
-            p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Tq + tok] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        if (r < rows) {
+            const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
+            if (whole) p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Tq + tok] = lse2 * kLn2;
+            else p.parts.lse[static_cast<size_t>(blockIdx.x) * p.parts.rows + r] = lse2;
+        }
     }
-    if (splits > 1) cluster.sync();
-    else __syncthreads();
-    // each CTA adds up and stores its share of the rows
-    for (int i = rank * kThreads + tid; i < rows * (D / 8); i += splits * kThreads) {
+    if (p.parts.units != nullptr && tid == 0 && blockIdx.x == item.first)
+        p.parts.units[bh * p.row_tiles + tile] = make_int2(item.first, item.pieces);
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 8); i += kThreads) {
         const int rr = i / (D / 8), c = i % (D / 8);
-        float x[8] = {};
-        for (int k = 0; k < splits; ++k) {
-            const uint8_t* from = splits > 1 ? cluster.map_shared_rank(smem, k) : smem;
+        float x[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 y = *reinterpret_cast<const float4*>(from + rr * (D * 4) +
-                                                                  (((2 * c + h) ^ (rr & (D / 4 - 1))) << 4));
-                x[4 * h] += y.x;
-                x[4 * h + 1] += y.y;
-                x[4 * h + 2] += y.z;
-                x[4 * h + 3] += y.w;
-            }
+        for (int h = 0; h < 2; ++h) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(smem + rr * (D * 4) + (((2 * c + h) ^ (rr & (D / 4 - 1))) << 4));
+            x[4 * h] = y.x;
+            x[4 * h + 1] = y.y;
+            x[4 * h + 2] = y.z;
+            x[4 * h + 3] = y.w;
+        }
+        if (!whole) {
+            float4* to = reinterpret_cast<float4*>(p.parts.o + (static_cast<size_t>(blockIdx.x) * p.parts.rows + rr) * D + c * 8);
+            to[0] = make_float4(x[0], x[1], x[2], x[3]);
+            to[1] = make_float4(x[4], x[5], x[6], x[7]);
+            continue;
         }
         const int at = tile * 128 + rr, hq = hk * p.group + at / p.Tq, t = at % p.Tq;
         uint32_t w[4], e[4];
@@ -365,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<uint4*>(p.o_rest + ((static_cast<size_t>(b) * p.Hq + hq) * p.Tq + t) * D + c * 8) =
                 make_uint4(e[0], e[1], e[2], e[3]);
     }
-    if (splits > 1) cluster.sync();  // the others may still read this CTA's rows
     tc_fence_before();
     __syncthreads();
     if (warp == 5) {
@@ -375,25 +364,46 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int D>
-int launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const RowsParams& p, int units, int splits,
-             cudaStream_t stream) {
+int launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const RowsParams& p, cudaStream_t stream) {
     static std::atomic<unsigned long long> allowed{0};
     auto kern = fa_cross_rows_kernel<D>;
     if (!allow_shared_memory(kern, RowsCfg<D>::kSmemBytes, allowed)) return -5;
-    return launch_clusters(kern, units * splits, splits, kThreads, RowsCfg<D>::kSmemBytes, stream, tk, tv, p);
+    return launch_chained(kern, dim3(p.plan.items), kThreads, RowsCfg<D>::kSmemBytes, stream, tk, tv, p);
+}
+
+struct RowUnits {
+    int R, row_tiles, rows;  // of a head; most rows of a unit
+    long long units;
+    int items;
+};
+RowUnits units_of(const CrossShape& s, int num_sms) {
+    RowUnits u;
+    u.R = s.Hq / s.Hkv * s.Tq;
+    u.row_tiles = (u.R + kRows - 1) / kRows;
+    u.rows = u.R < kRows ? u.R : kRows;
+    u.units = static_cast<long long>(s.B) * s.Hkv * u.row_tiles;
+    u.items = s.Tk <= kLeast * kKeys ? static_cast<int>(u.units) : split_items(u.units, 2 * num_sms);
+    return u;
 }
 
 }  // namespace
 
-bool cross_rows_wanted(const CrossShape& s) { return static_cast<long long>(s.Hq / s.Hkv) * s.Tq <= 128; }
+bool cross_rows_wanted(const CrossShape& s) { return static_cast<long long>(s.Hq / s.Hkv) * s.Tq <= kRows; }
+
+size_t cross_rows_workspace(const CrossShape& s, int num_sms) {
+    if (!cross_rows_wanted(s)) return 0;
+    const RowUnits u = units_of(s, num_sms);
+    return u.items == u.units ? 0 : split_workspace(u.items, u.units, u.rows, s.D);
+}
 
 int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
-                      const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
+                      const CrossTensor& o, void* o_rest, float* lse, float scale, void* workspace, cudaStream_t stream,
                       const DebugKnobs& dbg, int num_sms) {
     CUtensorMap tk, tv;
     if (!make_tmap_strided(&tk, {k.ptr, k.b, k.h, k.t}, s.B, s.Hkv, s.Tk, s.D, kKeys) ||
         !make_tmap_strided(&tv, {v.ptr, v.b, v.h, v.t}, s.B, s.Hkv, s.Tk, s.D, kKeys))
         return -5;
+    const RowUnits u = units_of(s, num_sms);
     RowsParams p{};
     p.q = q;
     p.o = o;
@@ -405,16 +415,29 @@ int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTens
     p.group = s.Hq / s.Hkv;
     p.Tq = s.Tq;
     p.Tk = s.Tk;
-    p.R = p.group * s.Tq;
-    p.row_tiles = (p.R + 127) / 128;
+    p.R = u.R;
+    p.row_tiles = u.row_tiles;
+    // Many units of one length keep the memory busy by themselves, and pieces of them only cost their join (256
+    // units of 24 tiles: 64 us whole, 71 in halves; of 0 to 24: 48 and 45); few are cut as far as the CTAs go.
+    p.plan = {s.B, s.Hkv * u.row_tiles, u.items, kLeast, u.units > num_sms};
+    if (u.items != u.units) p.parts = split_parts(workspace, u.items, u.rows, s.D);
     p.sl2 = scale * kLog2e;
     p.prescale = p.sl2 > 0.f ? 0 : 1;
     p.sl2_eff = p.prescale ? 1.f : p.sl2;
     p.timeout_ns = dbg.timeout_ns;
-    const int units = s.B * s.Hkv * p.row_tiles, tiles = (s.Tk + kKeys - 1) / kKeys;
-    int splits = 1;
-    while (splits < kMaxSplit && 2 * splits <= tiles && 2LL * splits * units <= 2LL * num_sms) splits *= 2;
-    return s.D == 64 ? launch_t<64>(tk, tv, p, units, splits, stream) : launch_t<128>(tk, tv, p, units, splits, stream);
+    const int rc = s.D == 64 ? launch_t<64>(tk, tv, p, stream) : launch_t<128>(tk, tv, p, stream);
+    if (rc != 0 || u.items == u.units) return rc;
+    SplitOut out{};
+    out.o = o;
+    out.rest = p.o_rest;
+    out.lse = lse;
+    out.Hkv = s.Hkv;
+    out.group = p.group;
+    out.T = s.Tq;
+    out.R = u.R;
+    out.row_units = u.row_tiles;
+    out.unit_rows = kRows;
+    return launch_split_join(p.parts, out, s.B, s.D, u.items, stream);
 }
 
 int cross_rows_take_status() {

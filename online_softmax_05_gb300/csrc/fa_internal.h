@@ -60,8 +60,9 @@ int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTenso
 // The same for few rows a key/value head (fa_cross_rows.cu): whether it is the one to take, and its launch.
 bool cross_rows_wanted(const CrossShape& s);
 int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
-                      const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
-                      const DebugKnobs& dbg, int num_sms);
+                      const CrossTensor& o, void* o_rest, float* lse, float scale, void* workspace,
+                      cudaStream_t stream, const DebugKnobs& dbg, int num_sms);
+size_t cross_rows_workspace(const CrossShape& s, int num_sms);  // 0 where they are not wanted
 int cross_rows_take_status();
 size_t cross_bwd_workspace(const CrossShape& s, bool deterministic, int num_sms);
 int launch_cross_bwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
@@ -137,25 +138,6 @@ inline int launch_chained(void (*kernel)(Params...), dim3 grid, int threads, siz
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -5;
-}
-// The same in clusters of `cluster` CTAs of a one-dimensional grid.
-template <typename... Params, typename... Args>
-inline int launch_clusters(void (*kernel)(Params...), int grid, int cluster, int threads, size_t smem,
-                           cudaStream_t stream, Args... args) {
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -5;
 }
 #ifdef __CUDACC__

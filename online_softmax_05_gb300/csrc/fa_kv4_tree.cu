@@ -693,7 +693,7 @@ int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const
     p.N = N;
     p.R = Hq / c.Hkv * N;
     p.row_units = u.row_units;
-    p.plan = {c.B, c.Hkv * u.row_units, u.items, kLeast};
+    p.plan = {c.B, c.Hkv * u.row_units, u.items, kLeast, 0};
     if (u.items != u.units) p.parts = split_parts(workspace, u.items, u.rows, c.D);
     p.sl2 = scale * kLog2e;
     p.timeout_ns = dbg.timeout_ns;

@@ -22,6 +22,7 @@ struct SplitPlan {
     int B, per_seq;    // sequences, units of each
     int items;         // CTAs, at least B * per_seq
     int least;         // tiles that are not worth cutting
+    int whole;         // 1: sequences of about one length (none 3/2 of the mean) are not cut
 };
 struct SplitItem {
     int b, unit;       // sequence; unit within it; -1: no item of this number
@@ -91,12 +92,24 @@ __device__ __forceinline__ SplitItem split_item(const SplitPlan& p, int number, 
         }
         chunk = lo;
     } else {
-        for (int b = 32 * kHeld + lane; b < p.B; b += 32) total += tiles_of(b);
+        for (int b = 32 * kHeld + lane; b < p.B; b += 32) {
+            const int tiles = tiles_of(b);
+            total += tiles;
+            most = max(most, tiles);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         // ceil(t / c) <= t / c + 1; the host gives more items than units here
         const long long room = p.items - static_cast<long long>(p.B) * p.per_seq;
         chunk = static_cast<int>(max(static_cast<long long>(max(1, p.least)), (total * p.per_seq + room - 1) / room));
+    }
+    if (p.whole) {
+        if (p.B <= 32 * kHeld) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (2LL * most * p.B <= 3 * total) chunk = max(chunk, most);
     }
     SplitItem it{0, -1, 0, 0, 0, 0, 0};
     int base = 0;

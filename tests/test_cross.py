@@ -364,7 +364,7 @@ BASE = 1 << 20
 def forward(shape=None, q=None, k=None, v=None, o=None, lse=BASE * 9, scale=0.1, rest=None):
     lib = fa.load_library()
     return lib.fa_cross_fwd(shape or shape_of(), q or view(BASE), k or view(2 * BASE), v or view(3 * BASE),
-                            o or view(4 * BASE), rest, lse, scale, None)
+                            o or view(4 * BASE), rest, lse, scale, None, 0, None)
 
 
 def backward(shape=None, scale=0.1, lse=BASE * 9, workspace=None, size=0, rest=None, **x):
@@ -417,9 +417,10 @@ def test_refusals_of_the_c_abi():
 
 def test_workspace_query_refuses():
     lib = fa.load_library()
-    assert lib.fa_cross_bwd_workspace(0, 1, 1, 1, 1, 64) == -2
-    assert lib.fa_cross_bwd_workspace(1, 3, 2, 1, 1, 64) == -2
-    assert lib.fa_cross_bwd_workspace(1, 2, 2, 1, 1, 32) == -3
+    for query in (lib.fa_cross_fwd_workspace, lib.fa_cross_bwd_workspace):
+        assert query(0, 1, 1, 1, 1, 64) == -2
+        assert query(1, 3, 2, 1, 1, 64) == -2
+        assert query(1, 2, 2, 1, 1, 32) == -3
 
 
 def test_cpu_tensors_are_refused():
