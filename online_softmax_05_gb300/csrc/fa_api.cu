@@ -409,7 +409,7 @@ int fa_cross_fwd(const fa_cross_shape* s, const fa_cross_tensor* q, const fa_cro
     if (rc != FA_OK) return rc;
     const fa::CrossShape shape{s->B, s->Hq, s->Hkv, s->Tq, s->Tk, s->D, s->key_lengths};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!fa::cross_rows_wanted(shape))
+    if (!fa::cross_rows_wanted(shape, sms))
         return fa::launch_cross_fwd(shape, x[0], x[1], x[2], x[3], o_rest, lse, scale, st, knobs(), sms);
     const size_t need = fa::cross_rows_workspace(shape, sms);
     if (workspace) {

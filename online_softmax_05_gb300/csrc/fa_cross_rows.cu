@@ -318,11 +318,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (r < rows) {
             const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
             if (whole) p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Tq + tok] = lse2 * kLn2;
-            else p.parts.lse[static_cast<size_t>(blockIdx.x) * p.parts.rows + r] = lse2;
+            else p.parts.lse[static_cast<size_t>(item.part + item.k) * p.parts.rows + r] = lse2;
         }
     }
-    if (p.parts.units != nullptr && tid == 0 && blockIdx.x == item.first)
-        p.parts.units[bh * p.row_tiles + tile] = make_int2(item.first, item.pieces);
+    if (p.parts.units != nullptr && tid == 0 && item.k == 0)
+        p.parts.units[bh * p.row_tiles + tile] = make_int2(item.part, item.pieces);
     __syncthreads();
     for (int i = tid; i < rows * (D / 8); i += kThreads) {
         const int rr = i / (D / 8), c = i % (D / 8);
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             x[4 * h + 3] = y.w;
         }
         if (!whole) {
-            float4* to = reinterpret_cast<float4*>(p.parts.o + (static_cast<size_t>(blockIdx.x) * p.parts.rows + rr) * D + c * 8);
+            float4* to = reinterpret_cast<float4*>(p.parts.o + (static_cast<size_t>(item.part + item.k) * p.parts.rows + rr) * D + c * 8);
             to[0] = make_float4(x[0], x[1], x[2], x[3]);
             to[1] = make_float4(x[4], x[5], x[6], x[7]);
             continue;
@@ -374,7 +374,7 @@ int launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const RowsParams& p, 
 struct RowUnits {
     int R, row_tiles, rows;  // of a head; most rows of a unit
     long long units;
-    int items;
+    SplitPlan plan;          // items == units: nothing is cut
 };
 RowUnits units_of(const CrossShape& s, int num_sms) {
     RowUnits u;
@@ -382,18 +382,30 @@ RowUnits units_of(const CrossShape& s, int num_sms) {
     u.row_tiles = (u.R + kRows - 1) / kRows;
     u.rows = u.R < kRows ? u.R : kRows;
     u.units = static_cast<long long>(s.B) * s.Hkv * u.row_tiles;
-    u.items = s.Tk <= kLeast * kKeys ? static_cast<int>(u.units) : split_items(u.units, 2 * num_sms);
+    // Many units keep the memory busy by themselves, and pieces of them only cost their join (256 units of 0 to 24
+    // tiles with 4, 64 and 128 rows: 47, 53 and 58 us whole, 48, 57 and 66 in halves); few are better cut (64
+    // units: 18 us, whole 40).
+    u.plan = split_plan(s.B, u.units, 2 * num_sms, kLeast, 10);
+    if (s.Tk <= kLeast * kKeys) u.plan.items = static_cast<int>(u.units);
     return u;
 }
 
 }  // namespace
 
-bool cross_rows_wanted(const CrossShape& s) { return static_cast<long long>(s.Hq / s.Hkv) * s.Tq <= kRows; }
+// One tile of rows a head, or too few pairs of query tiles for the kernel of whole tiles to have one on half
+// the SMs (8 heads of 1024 rows over 8192 keys: 44 us here, 57 there; 16 of 512 over 4096, D = 64: 25 and 28).
+// With more, that kernel shares each key tile between two of rows (64 heads of 2048 rows over 0 to 3000 keys,
+// D = 64: 59 us there, 117 here).
+bool cross_rows_wanted(const CrossShape& s, int num_sms) {
+    const long long group = s.Hq / s.Hkv, heads = static_cast<long long>(s.B) * s.Hq;
+    const long long pairs = group % 2 == 0 ? heads / 2 * ((s.Tq + 127) / 128) : heads * ((s.Tq + 255) / 256);
+    return group * s.Tq <= kRows || 2 * pairs <= num_sms;
+}
 
 size_t cross_rows_workspace(const CrossShape& s, int num_sms) {
-    if (!cross_rows_wanted(s)) return 0;
+    if (!cross_rows_wanted(s, num_sms)) return 0;
     const RowUnits u = units_of(s, num_sms);
-    return u.items == u.units ? 0 : split_workspace(u.items, u.units, u.rows, s.D);
+    return split_workspace(u.plan, u.rows, s.D);
 }
 
 int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
@@ -417,16 +429,14 @@ int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTens
     p.Tk = s.Tk;
     p.R = u.R;
     p.row_tiles = u.row_tiles;
-    // Many units of one length keep the memory busy by themselves, and pieces of them only cost their join (256
-    // units of 24 tiles: 64 us whole, 71 in halves; of 0 to 24: 48 and 45); few are cut as far as the CTAs go.
-    p.plan = {s.B, s.Hkv * u.row_tiles, u.items, kLeast, u.units > num_sms};
-    if (u.items != u.units) p.parts = split_parts(workspace, u.items, u.rows, s.D);
+    p.plan = u.plan;
+    p.parts = split_parts(workspace, u.plan, u.rows, s.D);
     p.sl2 = scale * kLog2e;
     p.prescale = p.sl2 > 0.f ? 0 : 1;
     p.sl2_eff = p.prescale ? 1.f : p.sl2;
     p.timeout_ns = dbg.timeout_ns;
     const int rc = s.D == 64 ? launch_t<64>(tk, tv, p, stream) : launch_t<128>(tk, tv, p, stream);
-    if (rc != 0 || u.items == u.units) return rc;
+    if (rc != 0 || u.plan.items == u.units) return rc;
     SplitOut out{};
     out.o = o;
     out.rest = p.o_rest;
@@ -437,7 +447,7 @@ int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTens
     out.R = u.R;
     out.row_units = u.row_tiles;
     out.unit_rows = kRows;
-    return launch_split_join(p.parts, out, s.B, s.D, u.items, stream);
+    return launch_split_join(p.parts, out, s.B, s.D, u.plan.items, stream);
 }
 
 int cross_rows_take_status() {

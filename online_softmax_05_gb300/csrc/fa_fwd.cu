@@ -1042,8 +1042,6 @@ int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTenso
     p.n_pairs = cdiv(s.Tq, 2 * kFwdBM);
     p.head_pairs = p.group % 2 == 0 ? 1 : 0;
     p.n_items = p.head_pairs ? p.n_tiles * (p.BH / 2) : p.n_pairs * p.BH;
-    p.single_tiles = 2LL * p.n_items <= num_sms ? 1 : 0;  // as in launch_fwd
-    if (p.single_tiles) p.n_items = p.n_tiles * p.BH;
     p.head_major = 1;
     p.sorted = s.key_lengths != nullptr && s.B > 1 && s.B <= kSortedMost ? 1 : 0;
     p.n_seq = s.B;
@@ -1054,9 +1052,6 @@ int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTenso
     p.timeout_ns = dbg.timeout_ns;
     p.inject = dbg.inject;
     const int grid = p.n_items < num_sms ? p.n_items : num_sms;
-    if (p.single_tiles)
-        return s.D == 64 ? launch_fwd_t<64, false, false, true, true>(tq, tk, tv, to, p, grid, stream)
-                         : launch_fwd_t<128, false, false, true, true>(tq, tk, tv, to, p, grid, stream);
     return s.D == 64 ? launch_fwd_t<64, false, false, false, true>(tq, tk, tv, to, p, grid, stream)
                      : launch_fwd_t<128, false, false, false, true>(tq, tk, tv, to, p, grid, stream);
 }

@@ -58,7 +58,7 @@ int launch_cross_fwd(const CrossShape& s, const CrossTensor& q, const CrossTenso
                      const CrossTensor& o, void* o_rest, float* lse, float scale, cudaStream_t stream,
                      const DebugKnobs& dbg, int num_sms);
 // The same for few rows a key/value head (fa_cross_rows.cu): whether it is the one to take, and its launch.
-bool cross_rows_wanted(const CrossShape& s);
+bool cross_rows_wanted(const CrossShape& s, int num_sms);
 int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
                       const CrossTensor& o, void* o_rest, float* lse, float scale, void* workspace,
                       cudaStream_t stream, const DebugKnobs& dbg, int num_sms);

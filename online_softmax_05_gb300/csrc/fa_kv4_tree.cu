@@ -610,11 +610,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         if (row < row0 + rows && half == 0) {
             const float lse2 = used ? m + __log2f(sum) : -INFINITY;
             if (whole) p.lse[static_cast<size_t>(bh) * p.R + row] = lse2 * kLn2;
-            else p.parts.lse[static_cast<size_t>(blockIdx.x) * p.parts.rows + row - row0] = lse2;
+            else p.parts.lse[static_cast<size_t>(item.part + item.k) * p.parts.rows + row - row0] = lse2;
         }
     }
-    if (p.parts.units != nullptr && tid == 0 && blockIdx.x == item.first)
-        p.parts.units[bh * p.row_units + ru] = make_int2(item.first, item.pieces);
+    if (p.parts.units != nullptr && tid == 0 && item.k == 0)
+        p.parts.units[bh * p.row_units + ru] = make_int2(item.part, item.pieces);
     __syncthreads();
     for (int i = tid; i < rows * (D / 8); i += kThreads) {
         const int rr = i / (D / 8), c = i % (D / 8);
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
         } else {
             float4* to = reinterpret_cast<float4*>(p.parts.o +
-                                                   (static_cast<size_t>(blockIdx.x) * p.parts.rows + rr) * D + c * 8);
+                                                   (static_cast<size_t>(item.part + item.k) * p.parts.rows + rr) * D + c * 8);
             to[0] = make_float4(x[0], x[1], x[2], x[3]);
             to[1] = make_float4(x[4], x[5], x[6], x[7]);
         }
@@ -657,7 +657,7 @@ int launch_t(const TreeParams& p, cudaStream_t stream) {
 struct TreeUnits {
     int row_units, rows;  // of a head; most rows of a unit
     long long units;
-    int items;
+    SplitPlan plan;       // items == units: nothing is cut
 };
 TreeUnits units_of(const Kv4Shape& c, int Hq, int N, int num_sms) {
     TreeUnits u;
@@ -665,9 +665,9 @@ TreeUnits units_of(const Kv4Shape& c, int Hq, int N, int num_sms) {
     u.row_units = (R + kUnitRows - 1) / kUnitRows;
     u.rows = R < kUnitRows ? R : kUnitRows;
     u.units = static_cast<long long>(c.B) * c.Hkv * u.row_units;
+    u.plan = split_plan(c.B, u.units, num_sms, kLeast, 4);
     // no sequence of the table has tiles enough to be cut: an item a unit
-    const bool small = static_cast<long long>(c.width) * c.page_size <= kLeast * kTok;
-    u.items = small ? static_cast<int>(u.units) : split_items(u.units, num_sms);
+    if (static_cast<long long>(c.width) * c.page_size <= kLeast * kTok) u.plan.items = static_cast<int>(u.units);
     return u;
 }
 
@@ -675,7 +675,7 @@ TreeUnits units_of(const Kv4Shape& c, int Hq, int N, int num_sms) {
 
 size_t kv4_tree_workspace(const Kv4Shape& c, int Hq, int N, int num_sms) {
     const TreeUnits u = units_of(c, Hq, N, num_sms);
-    return u.items == u.units ? 0 : split_workspace(u.items, u.units, u.rows, c.D);
+    return split_workspace(u.plan, u.rows, c.D);
 }
 
 int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const int* lengths, const int* parents,
@@ -693,13 +693,13 @@ int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const
     p.N = N;
     p.R = Hq / c.Hkv * N;
     p.row_units = u.row_units;
-    p.plan = {c.B, c.Hkv * u.row_units, u.items, kLeast, 0};
-    if (u.items != u.units) p.parts = split_parts(workspace, u.items, u.rows, c.D);
+    p.plan = u.plan;
+    p.parts = split_parts(workspace, u.plan, u.rows, c.D);
     p.sl2 = scale * kLog2e;
     p.timeout_ns = dbg.timeout_ns;
     const int rc = c.D == 64 ? (c.group == 32 ? launch_t<64, 32>(p, stream) : launch_t<64, 64>(p, stream))
                              : (c.group == 32 ? launch_t<128, 32>(p, stream) : launch_t<128, 64>(p, stream));
-    if (rc != 0 || u.items == u.units) return rc;
+    if (rc != 0 || u.plan.items == u.units) return rc;
     SplitOut out{};
     out.o = {o, static_cast<long long>(Hq) * N * c.D, static_cast<long long>(N) * c.D, c.D};
     out.lse = lse;
@@ -709,7 +709,7 @@ int launch_kv4_tree(const Kv4Shape& c, const void* pool, const int* table, const
     out.R = p.R;
     out.row_units = u.row_units;
     out.unit_rows = kUnitRows;
-    return launch_split_join(p.parts, out, c.B, c.D, u.items, stream);
+    return launch_split_join(p.parts, out, c.B, c.D, u.plan.items, stream);
 }
 
 int kv4_tree_take_status() {

@@ -22,18 +22,20 @@ struct SplitPlan {
     int B, per_seq;    // sequences, units of each
     int items;         // CTAs, at least B * per_seq
     int least;         // tiles that are not worth cutting
-    int whole;         // 1: sequences of about one length (none 3/2 of the mean) are not cut
+    int slots;         // CTAs that run at a time
+    int share;         // pieces are no shorter than share / 4 of a slot's part of all tiles (0: as short as the items allow)
 };
 struct SplitItem {
     int b, unit;       // sequence; unit within it; -1: no item of this number
     int j0, n;         // its tiles
     int tiles;         // of the whole unit
-    int first, pieces; // the unit's items
+    int pieces;        // of the unit
+    int part, k;       // where they are left: part + k is this item's; k = 0: its first
 };
 // What the second kernel reads: [unit] (first piece, pieces), pieces of `rows` rows.
 struct SplitParts {
-    float* o;          // [item][rows][D], normalised
-    float* lse;        // [item][rows], log2 units, -inf where a row saw nothing
+    float* o;          // [part][rows][D], normalised
+    float* lse;        // [part][rows], log2 units, -inf where a row saw nothing
     int2* units;
     int rows;
 };
@@ -49,14 +51,15 @@ struct SplitOut {
 int launch_split_join(const SplitParts& parts, const SplitOut& out, int B, int D, int items, cudaStream_t stream);
 
 // Bytes of the pieces' workspace, and its parts.
-inline size_t split_workspace(int items, long long units, int rows, int D) {
-    return (static_cast<size_t>(items) * rows * D + (static_cast<size_t>(items) * rows + 1) / 2 * 2) * 4 +
-           static_cast<size_t>(units) * 8;
+inline size_t split_workspace(const SplitPlan& p, int rows, int D) {
+    const size_t units = static_cast<size_t>(p.B) * p.per_seq, n = 2 * (p.items - units) * rows;
+    return n == 0 ? 0 : n * (D + 1) * 4 + units * 8;
 }
-inline SplitParts split_parts(void* ws, int items, int rows, int D) {
+inline SplitParts split_parts(void* ws, const SplitPlan& p, int rows, int D) {
+    const size_t n = 2 * (p.items - static_cast<size_t>(p.B) * p.per_seq) * rows;
+    if (n == 0) return {};
     float* o = static_cast<float*>(ws);
-    float* lse = o + static_cast<size_t>(items) * rows * D;
-    return {o, lse, reinterpret_cast<int2*>(lse + (static_cast<size_t>(items) * rows + 1) / 2 * 2), rows};
+    return {o, o + n * D, reinterpret_cast<int2*>(o + n * (D + 1)), rows};
 }
 
 __device__ __forceinline__ int split_sum(int x) {
@@ -92,29 +95,36 @@ __device__ __forceinline__ SplitItem split_item(const SplitPlan& p, int number, 
         }
         chunk = lo;
     } else {
-        for (int b = 32 * kHeld + lane; b < p.B; b += 32) {
-            const int tiles = tiles_of(b);
-            total += tiles;
-            most = max(most, tiles);
-        }
+        for (int b = 32 * kHeld + lane; b < p.B; b += 32) total += tiles_of(b);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         // ceil(t / c) <= t / c + 1; the host gives more items than units here
         const long long room = p.items - static_cast<long long>(p.B) * p.per_seq;
         chunk = static_cast<int>(max(static_cast<long long>(max(1, p.least)), (total * p.per_seq + room - 1) / room));
     }
-    if (p.whole) {
+    if (p.share > 0) {
         if (p.B <= 32 * kHeld) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (2LL * most * p.B <= 3 * total) chunk = max(chunk, most);
+        chunk = static_cast<int>(max(static_cast<long long>(chunk), total * p.per_seq * p.share / (4LL * p.slots)));
     }
-    SplitItem it{0, -1, 0, 0, 0, 0, 0};
+    // up to 32 sequences: those with longer pieces first, as CTAs start in the order of their numbers
+    int mine = lane;
+    if (p.B <= 32) {
+        const int size = held[0] >= 0 ? held[0] / split_pieces(held[0], chunk) : -1;
+        int rank = 0;
+        for (int i = 0; i < p.B; ++i) {
+            const int other = __shfl_sync(0xffffffffu, size, i);
+            rank += other > size || (other == size && i < lane);
+        }
+        for (int i = 0; i < p.B; ++i)
+            if (__shfl_sync(0xffffffffu, rank, i) == lane) mine = i;
+    }
+    SplitItem it{0, -1, 0, 0, 0, 0, 0, 0};
     int base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane, tiles = b < p.B ? tiles_of(b) : 0;
+        const int b = b0 + mine, tiles = b < p.B ? tiles_of(b) : 0;
         const int n = b < p.B ? split_pieces(tiles, chunk) : 0;
         int sum = n * p.per_seq;
 #pragma unroll
@@ -125,15 +135,16 @@ __device__ __forceinline__ SplitItem split_item(const SplitPlan& p, int number, 
         const unsigned hit = __ballot_sync(0xffffffffu, base + sum > number);
         if (hit != 0) {
             const int src = __ffs(hit) - 1;
-            it.b = b0 + src;
+            it.b = b0 + __shfl_sync(0xffffffffu, mine, src);
             it.pieces = __shfl_sync(0xffffffffu, n, src);
             it.tiles = __shfl_sync(0xffffffffu, tiles, src);
             const int rem = number - (base + __shfl_sync(0xffffffffu, sum, src) - it.pieces * p.per_seq);
             it.unit = rem / it.pieces;
-            const int k = rem - it.unit * it.pieces;
-            it.first = number - k;
-            it.j0 = static_cast<int>(static_cast<long long>(it.tiles) * k / it.pieces);
-            it.n = static_cast<int>(static_cast<long long>(it.tiles) * (k + 1) / it.pieces) - it.j0;
+            it.k = rem - it.unit * it.pieces;
+            // items before that are a further piece of their unit; a cut unit's pieces are at most twice its further ones
+            it.part = 2 * (number - it.k - ((b0 + src) * p.per_seq + it.unit));
+            it.j0 = static_cast<int>(static_cast<long long>(it.tiles) * it.k / it.pieces);
+            it.n = static_cast<int>(static_cast<long long>(it.tiles) * (it.k + 1) / it.pieces) - it.j0;
             break;
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
@@ -141,12 +152,13 @@ __device__ __forceinline__ SplitItem split_item(const SplitPlan& p, int number, 
     return it;
 }
 
-// Host: how many items for `units` units where `slots` CTAs run at a time.  With few units one
-// wave; with more, waves of about half a unit each, which even out over the SMs; from four waves
-// of whole units on nothing is cut.
-inline int split_items(long long units, int slots) {
-    if (units >= 4LL * slots) return static_cast<int>(units);
-    return static_cast<int>(2 * units <= slots ? slots : (2 * units + slots - 1) / slots * slots);
+// Host: the plan for `units` units, per_seq of each sequence, where `slots` CTAs run at a time.  Few units
+// are cut as far as the CTAs go, in one wave.  Many go out whole, longest first, but for what is longer
+// than share / 4 of a CTA's part, at most 4 slots / share further pieces.
+inline SplitPlan split_plan(int B, long long units, int slots, int least, int share) {
+    const bool few = 2 * units <= slots;
+    const long long items = few ? slots : units + (4LL * slots + share - 1) / share;
+    return {B, static_cast<int>(units / B), static_cast<int>(items), least, slots, few ? 0 : share};
 }
 
 }  // namespace fa
