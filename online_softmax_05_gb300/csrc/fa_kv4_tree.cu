@@ -5,30 +5,37 @@
 // many enough for the tensor cores' 128-row tiles, which want whole operands in shared memory, so
 // the codes are unpacked there.  With k = s n + m and v = s n + m per group of channels
 // (fa_kv4.cuh):
-//   K   s = sa + sb, its upper and lower four bits of significand: sa n and sb n have
-//       eight bits and are exact in bf16.  S = q.(sa n) + q.(sb n) + sum_g m_g sum(q_g), the
-//       last as 16 more channels: m_g against three bf16 pieces (24 bits) of sum(q_g).
-//       Every operand is exact; S is what fp32 sums give.  (One bf16 number for k would put
-//       2^-9 into each product, 2e-3 into a score and so into the log-sum-exp.)
+//   K   s (n - 8) has eleven bits, as many as fp16: with q in fp16 too (a row scaled by a power of
+//       two to [2^8, 2^9): exact down to 2^-25 of its largest), S is what fp32 sums give,
+//         S = q.(s (n - 8)) + sum_g (m_g + 8 s_g) sum(q_g),
+//       the last as 16 more channels: m_g and 8 s_g against two fp16 pieces (22 bits) of
+//       sum(q_g).  (One bf16 number for k would put 2^-9 into each product, 2e-3 into a score and so
+//       into the log-sum-exp.)  One multiply-add makes a pair of products: 16 + n is the fp16
+//       number 0x4c00 | n << 6, and s (16 + n) - 24 s is exact.
+//       A tile that has a scale or minimum outside [2^-17, 2^11] goes as bf16 instead, in
+//       two parts, s = sa + sb its upper and lower four bits: sa n and sb n have eight bits,
+//       and the minima meet three bf16 pieces of sum(q_g).
 //   V   s n + m rounded once to bf16, as P is: both average out over a row's tokens and
 //       are at most the output's own rounding where one token has all the weight.
-// One packed multiply-add makes two products: 128 + n is the bf16 number 0x4300 | n, and
-// sa (128 + n) - 128 sa is exact.  Channels stay in the order of the codes' words; Q is stored
-// in that order, and V's is undone when the outputs leave.
+// Channels stay in the order of the codes' words; Q is stored in that order, and V's is
+// undone when the outputs leave.
 //
-// Ranges.  Rows of q are scaled by a power of two to [1, 2), K by 2^-16 and V by 2^-24, undone in the
-// row's score factor and at the end: no product or sum overflows for any bf16 numbers in the cache.
-// A token that a row does not see adds nothing whatever it holds: S is replaced, and a tree's value
-// group that is NaN goes into the products as 0 and into the rows that see it at the end.
+// Ranges.  In bf16 K is scaled by 2^-16, V always by 2^-24, undone in the scores' factor and at the
+// end: no product or sum overflows for any bf16 numbers in the cache.  A token that a row does
+// not see adds nothing whatever it holds: S is replaced, and a tree's value group that is NaN
+// goes into the products as 0 and into the rows that see it at the end.
 //
-// Per CTA, 128 rows: warps 0-3 softmax of a tile's first 32 tokens, 4-7 of its last, the rows' maxima
-// exchanged through shared memory; two teams of four warps fetch and unpack tiles of 64 tokens
-// in turn (a thread a token's keys or values, copying the bytes that it will use four tiles ahead);
-// the last warp issues tcgen05.mma.  sa n and sb n lie side by side as 128 columns of one
-// product, added by the softmax warps: an instruction of 64 columns takes as long as one of 128.  Q
-// is in tensor memory: from shared memory it would take half of that memory's cycles.
+// Per CTA, 128 rows and tiles of 128 tokens: warps 0-3 softmax of a tile's first 64 tokens, 4-7 of
+// its last, the rows' maxima exchanged through shared memory (in clocks a tile of 64 that way took
+// 1950, three quarters of it waits and latencies: so 128); four warps fetch and unpack keys, four
+// values (a thread a token, copying the bytes that it will use two tiles ahead); the last warp
+// issues tcgen05.mma, S of the next tile beside the softmax of this.  Q is in tensor memory: from
+// shared memory it would take half of that memory's cycles.
 // A ragged batch is cut over the CTAs by fa_split.cuh.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "fa_check.cuh"
 #include "fa_internal.h"
@@ -44,14 +51,14 @@ static __device__ int g_status_kv4_tree;
 
 namespace {
 
-constexpr int kTeams = 2;       // of four unpacking warps, a tile each in turn
-constexpr int kUnpackWarps = 4 * kTeams;
+constexpr int kUnpackWarps = 8;  // half of them keys, half values
 constexpr int kThreads = (8 + kUnpackWarps + 1) * 32;
 constexpr int kMmaWarp = 8 + kUnpackWarps;
-constexpr int kTok = 64;       // of a tile
-constexpr int kRaw = 2;        // tiles of codes on their way to a team
+constexpr int kTok = 128;      // of a tile
+constexpr int kRaw = 2;        // tiles of codes on their way
+constexpr int kInfo = 8;       // tiles whose masks are held: more than can be between their unpacking and their softmax
 constexpr int kUnitRows = 128;  // of a CTA
-constexpr int kLeast = 6;      // tiles that are not worth cutting
+constexpr int kLeast = 3;      // tiles that are not worth cutting
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kKeyUnit = 0x1p-16f, kValueUnit = 0x1p-24f;
@@ -60,30 +67,31 @@ template <int D_, int G_>
 struct TreeCfg : Kv4<D_, G_> {
     using L = Kv4<D_, G_>;
     static constexpr int kTile = kTok * D_ * 2;            // an operand tile of keys or values
-    static constexpr int kAugTile = kTok * 32;             // 16 more channels a token
-    static constexpr int kStage = 3 * kTile + kAugTile;    // sa n, sb n, V, minima
-    static constexpr int kStages = D_ == 128 ? 3 : 4;
-    static constexpr int kQAug = 128 * 32;
-    static constexpr int kQOff = kStages * kStage;
-    static constexpr int kRawOff = kQOff + kQAug;
+    static constexpr int kKStage = kTile + kTok * 32;      // and 16 more channels a token of keys
+    static constexpr int kKStages = D_ == 128 ? 3 : 4, kVStages = D_ == 128 ? 2 : 3;
+    static constexpr int kVOff = kKStages * kKStage;
+    static constexpr int kQOff = kVOff + kVStages * kTile;
+    static constexpr int kQAug = 128 * 32;                 // of fp16, then of bf16
+    static constexpr int kRawOff = kQOff + 2 * kQAug;
     static constexpr int kRawTile = kUnpackWarps * 32 * (L::kRow + L::kScaleRow);  // of all threads: a row's codes, scales
     static constexpr int kBarOff = kRawOff + kRaw * kRawTile;
-    // full[], empty[], s_full[2], p_full[2], pv_done, o_full, q_full, mma_done
-    static constexpr int kNumBars = 2 * kStages + 4 + 4;
+    // k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], pv_done, o_full, q_full, mma_done
+    static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 4;
     static constexpr int kMlOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // [2][2][128] row maxima of a tile's halves, by its parity
     static constexpr int kTreeOff = kMlOff + 4 * 128 * 4;    // [64] ancestors
     static constexpr int kPoisonOff = kTreeOff + 64 * 8;     // [groups] places whose value group is NaN
-    static constexpr int kMaskOff = kPoisonOff + 4 * 8;      // [stages] tokens that are there
-    static constexpr int kMiscOff = kMaskOff + kStages * 8;
+    static constexpr int kMaskOff = kPoisonOff + 4 * 8;      // [tiles] tokens that are there
+    static constexpr int kWideOff = kMaskOff + kInfo * 16;   // [tiles] whether it is in bf16
+    static constexpr int kMiscOff = kWideOff + kInfo * 4;
     static constexpr int kSmemBytes = kMiscOff + 16 + sizeof(SplitItem) + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kSmemBytes > 114 * 1024, "one CTA an SM: it takes all of tensor memory");
     static_assert(kQOff >= 128 * D_ * 4, "the scaled rows go where the stages were");
-    // TMEM: O, two tiles of S (sa n, sb n; P over the first 32 columns), Q
-    static constexpr uint32_t kO = 0, kQ = 384;
+    // TMEM: O, two tiles of S (P over their first half), Q in fp16 and in bf16
+    static constexpr uint32_t kO = 0, kQ = 384, kQWide = 448;
     __device__ static constexpr uint32_t kS(int buf) { return 128u + 128u * buf; }
-    static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 2 * kTok, false, false);
-    static constexpr uint32_t kIdescAug = idesc_bf16_f32(128, kTok, false, false);
+    static constexpr uint32_t kIdescWide = idesc_bf16_f32(128, kTok, false, false);
+    static constexpr uint32_t kIdescS = kIdescWide & ~((7u << 7) | (7u << 10));  // operand formats 0: fp16
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D_, false, true);
 };
 
@@ -108,6 +116,15 @@ __device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t x, uint32_t b)
     return as_u32(__hfma2(as_bf2(a), as_bf2(x), as_bf2(b)));
 }
 __device__ __forceinline__ uint32_t twice(float x) { return pack_bf16x2(x, x); }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t x, uint32_t b) {
+    const __half2 h = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ bool in_range(float x) { return x == 0.f || (fabsf(x) >= 0x1p-17f && fabsf(x) <= 0x1p11f); }
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
@@ -136,16 +153,16 @@ __device__ __forceinline__ SDesc sdesc_sw32(uint32_t saddr) {
     return d;
 }
 
-// Barrier of two warps; whether a predicate holds in any of their threads.
-__device__ __forceinline__ bool any_of_pair(int barrier, bool x) {
+// Barrier of `threads` threads; whether a predicate holds in any of them.
+__device__ __forceinline__ bool any_of(int barrier, int threads, bool x) {
     uint32_t any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"(x ? 1u : 0u), "r"(barrier)
+        : "r"(x ? 1u : 0u), "r"(barrier), "r"(threads)
         : "memory");
     return any != 0;
 }
@@ -153,21 +170,26 @@ __device__ __forceinline__ bool any_of_pair(int barrier, bool x) {
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) {
     using C = TreeCfg<D, G>;
-    constexpr int ST = C::kStages, NG = C::kGroups, S32 = D / 32;
+    constexpr int KST = C::kKStages, VST = C::kVStages, NG = C::kGroups, S32 = D / 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_u32(smem), bars = base + C::kBarOff;
-    auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (ST + s); };
-    auto s_full = [&](int buf) { return bars + 8u * (2 * ST + buf); };
-    auto p_full = [&](int buf) { return bars + 8u * (2 * ST + 2 + buf); };
-    const uint32_t pv_done = bars + 8u * (2 * ST + 4), o_full = pv_done + 8, q_full = pv_done + 16, mma_done = pv_done + 24;
-    const uint32_t sQAug = base + C::kQOff;
-    auto sStage = [&](int s) { return base + s * C::kStage; };
+    auto k_full = [&](int s) { return bars + 8u * s; };
+    auto k_empty = [&](int s) { return bars + 8u * (KST + s); };
+    auto v_full = [&](int s) { return bars + 8u * (2 * KST + s); };
+    auto v_empty = [&](int s) { return bars + 8u * (2 * KST + VST + s); };
+    constexpr int kFirst = 2 * KST + 2 * VST;
+    auto s_full = [&](int buf) { return bars + 8u * (kFirst + buf); };
+    auto p_full = [&](int buf) { return bars + 8u * (kFirst + 2 + buf); };
+    const uint32_t pv_done = bars + 8u * (kFirst + 4), o_full = pv_done + 8, q_full = pv_done + 16, mma_done = pv_done + 24;
+    const uint32_t sQAug = base + C::kQOff, sQWide = sQAug + C::kQAug;
+    auto sK = [&](int s) { return base + s * C::kKStage; };
+    auto sV = [&](int s) { return base + C::kVOff + s * C::kTile; };
     float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
     unsigned long long* tree = reinterpret_cast<unsigned long long*>(smem + C::kTreeOff);
     unsigned long long* poison = reinterpret_cast<unsigned long long*>(smem + C::kPoisonOff);
     volatile uint32_t* masks = reinterpret_cast<volatile uint32_t*>(smem + C::kMaskOff);
+    volatile uint32_t* wides = reinterpret_cast<volatile uint32_t*>(smem + C::kWideOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     const WaitCtl ctl{abort_flag, &g_status_kv4_tree, p.timeout_ns};
@@ -207,12 +229,16 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
 
     const int active = (rows + 31) / 32;  // quarters of the tile that have rows
     if (tid == 0) {
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(full(s), 4);
-            mbar_init(empty(s), 1);
+        for (int s = 0; s < KST; ++s) {
+            mbar_init(k_full(s), kUnpackWarps / 2);
+            mbar_init(k_empty(s), 1);
+        }
+        for (int s = 0; s < VST; ++s) {
+            mbar_init(v_full(s), kUnpackWarps / 2);
+            mbar_init(v_empty(s), 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1);
+            mbar_init(s_full(t), 2);  // the products, and the word of the warp that has seen the masks
             mbar_init(p_full(t), 2 * active);
         }
         mbar_init(pv_done, 1);
@@ -234,22 +260,22 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
 
     if (warp >= 8 && warp < kMmaWarp) {
         // ------------------------------------------------------------ fetch and unpack
-        constexpr int CH = C::kRow / 16, kWords = C::kRow / 4;  // 16-byte chunks and words of a row of codes
-        const int th = tid - 256, team = th >> 7, tok = th & 63;
-        const bool is_v = th >> 6 & 1;
+        constexpr int CH = C::kRow / 16;  // 16-byte chunks of a row of codes
+        const int th = tid - 256, tok = th & (kTok - 1);
+        auto unpack = [&](auto of_values) {
+        constexpr bool is_v = decltype(of_values)::value;
         const uint32_t raw = base + C::kRawOff + th * C::kRow,
                        raw_scales = base + C::kRawOff + kUnpackWarps * 32 * C::kRow + th * C::kScaleRow;
         const int turn = (tok / (8 / CH)) % CH;  // the chunks' order in shared memory, against bank conflicts
-        const int section = is_v ? C::kValueCodes : C::kKeyCodes, scales = is_v ? C::kValueScales : C::kKeyScales;
+        constexpr int section = is_v ? C::kValueCodes : C::kKeyCodes, scales = is_v ? C::kValueScales : C::kKeyScales;
         const int rowb = tok & 15;
-        const int mine = (n + kTeams - 1 - team) / kTeams;  // this team's tiles: team, team + kTeams, ..
         uint32_t here = 0;  // bit i: this thread's token is there in raw tile i
         // the table's entry for this thread's token of tile i, read a tile ahead of its use; and the block in that page
         const int* entries = p.pages.table + static_cast<long long>(b) * p.pages.width;
         int page = -1, inside = 0;
         auto look_up = [&](int i) {
-            const int at = (j0 + team + kTeams * i) * kTok + tok, block = at >> 4;
-            if (i < mine && at < len) {
+            const int at = (j0 + i) * kTok + tok, block = at >> 4;
+            if (i < n && at < len) {
                 const int e = p.pages.shift >= 0 ? block >> p.pages.shift : block / p.pages.blocks_page;
                 inside = block - e * p.pages.blocks_page;
                 page = __ldg(entries + e);  // len is within the table
@@ -257,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         };
         look_up(0);
         auto fetch = [&](int i) {
-            if (i < mine) {
-                const int at = (j0 + team + kTeams * i) * kTok + tok;
+            if (i < n) {
+                const int at = (j0 + i) * kTok + tok;
                 const int slot = i % kRaw;
                 here &= ~(1u << slot);
                 if (at < len) {
@@ -280,63 +306,116 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             look_up(i + 1);
         };
         for (int i = 0; i < kRaw; ++i) fetch(i);
-        for (int i = 0; i < mine; ++i) {
+        int entry = 0;   // of the keys' ring: a tile in bf16 takes two
+        bool ok = true;  // a wait that ran out: the keys' warps still meet at their barrier
+        for (int j = 0; j < n; ++j) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-            const int j = team + kTeams * i, slot = i % kRaw, st = j % ST;
+            const int slot = j % kRaw;
             const bool there = here >> slot & 1;
-            uint32_t w[kWords], sc[NG];
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                uint32_t x[4];
-                load_words(raw + slot * C::kRawTile + ((c ^ turn) << 4), x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[4 * c + e] = there ? x[e] : 0u;
-            }
+            uint32_t sc[NG];  // of a token that is not there 0: its codes, whatever they are, count for nothing
             load_words(raw_scales + slot * C::kRawTile, sc);
 #pragma unroll
             for (int g = 0; g < NG; ++g) sc[g] = there ? sc[g] : 0u;
-            fetch(i + kRaw);
-            if (!wait_warp(empty(st), ((j / ST) & 1) ^ 1, ctl)) break;
-            const uint32_t stage = sStage(st);
-            if (!is_v) {
-                uint32_t sa[NG], sb[NG], ca[NG], cb[NG];  // pairs: the parts of s, and -128 of them
-                float mn[NG];
+            // four words of codes at a time
+            auto codes = [&](int chunk, uint32_t (&w)[4]) { load_words(raw + slot * C::kRawTile + ((chunk ^ turn) << 4), w); };
+            if constexpr (!is_v) {
+                bool fits = true;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const float2 x = kv4_scale(sc[g]);
-                    const float hi = __uint_as_float(__float_as_uint(x.x) & 0xfff00000u), lo = x.x - hi;
-                    sa[g] = twice(hi * kKeyUnit);
-                    sb[g] = twice(lo * kKeyUnit);
-                    ca[g] = twice(hi * kKeyUnit * -128.f);
-                    cb[g] = twice(lo * kKeyUnit * -128.f);
-                    mn[g] = x.y * kKeyUnit;
+                    fits = fits && in_range(x.x) && in_range(x.y);
                 }
+                const bool wide = any_of(8, kTok, !fits);
+                const uint32_t mask = __ballot_sync(0xffffffffu, there);
+                if (lane == 0) masks[4 * (j % kInfo) + (tok >> 5)] = mask;
+                if (tok == 0) wides[j % kInfo] = wide;
+                auto leave = [&]() {  // the entry is written
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(k_full(entry % KST));
+                    ++entry;
+                };
+                ok = ok && wait_warp(k_empty(entry % KST), ((entry / KST) & 1) ^ 1, ctl);
+                if (!ok) continue;  // nothing more is fetched
+                uint32_t stage = sK(entry % KST);
+                uint32_t extra[8];  // the 16 more channels
+                if (!wide) {
+                    uint32_t s2[NG], c2[NG];
 #pragma unroll
-                for (int c = 0; c < kWords; ++c) {
-                    const int g = c % S32 * 32 / G;
-                    uint32_t ya[4], yb[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t x = ((w[c] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
-                        ya[e] = fma_pair(sa[g], x, ca[g]);
-                        yb[e] = fma_pair(sb[g], x, cb[g]);
+                    for (int g = 0; g < NG; ++g) {
+                        const float2 x = kv4_scale(sc[g]);
+                        s2[g] = pack_f16(x.x, x.x);
+                        c2[g] = pack_f16(-24.f * x.x, -24.f * x.x);
                     }
-                    const uint32_t at = stage + (c >> 3) * (2 * kTok * 128) + sw128_off(tok, c & 7);
-                    st_shared_v4(at, ya[0], ya[1], ya[2], ya[3]);
-                    st_shared_v4(at + kTok * 128, yb[0], yb[1], yb[2], yb[3]);
-                }
-                // the minima, three times each: against the three pieces of sum(q_g)
-                float c[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) c[e] = e < 3 * NG ? mn[e < 3 * NG ? e / 3 : 0] : 0.f;
+                    for (int chunk = 0; chunk < CH; ++chunk) {
+                        uint32_t w[4];
+                        codes(chunk, w);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = 4 * chunk + k, g = c % S32 * 32 / G;
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t x = e < 2 ? w[k] << (6 - 4 * e) : w[k] >> (4 * e - 6);
+                                y[e] = fma_f16(s2[g], (x & 0x03c003c0u) | 0x4c004c00u, c2[g]);
+                            }
+                            st_shared_v4(stage + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1], y[2], y[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float2 x = g < NG ? kv4_scale(sc[g < NG ? g : 0]) : make_float2(0.f, 0.f);
+                        extra[2 * g] = pack_f16(x.y, x.y);
+                        extra[2 * g + 1] = pack_f16(8.f * x.x, 8.f * x.x);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t s2[NG], c2[NG];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const float s = kv4_scale(sc[g]).x, hi = __uint_as_float(__float_as_uint(s) & 0xfff00000u);
+                            const float x = (part == 0 ? hi : s - hi) * kKeyUnit;
+                            s2[g] = twice(x);
+                            c2[g] = twice(x * -128.f);
+                        }
+#pragma unroll 1
+                        for (int chunk = 0; chunk < CH; ++chunk) {
+                            uint32_t w[4];
+                            codes(chunk, w);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int c = 4 * chunk + k, g = (S32 == 4 ? k : k % 2) * 32 / G;
+                                uint32_t y[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    y[e] = fma_pair(s2[g], ((w[k] >> (4 * e)) & 0x000f000fu) | 0x43004300u, c2[g]);
+                                st_shared_v4(stage + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1], y[2], y[3]);
+                            }
+                        }
+                        if (part == 0) {
+                            leave();
+                            ok = wait_warp(k_empty(entry % KST), ((entry / KST) & 1) ^ 1, ctl);
+                            if (!ok) break;
+                            stage = sK(entry % KST);
+                        }
+                    }
+                    if (!ok) continue;
+                    float c[16];  // the minima, three times each: they go with the second part
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) c[e] = e < 3 * NG ? kv4_scale(sc[e < 3 * NG ? e / 3 : 0]).y * kKeyUnit : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) extra[e] = pack_bf16x2(c[2 * e], c[2 * e + 1]);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    st_shared_v4(stage + 3 * C::kTile + sw32_off(tok, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
-                                 pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
-                                 pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
-                const uint32_t mask = __ballot_sync(0xffffffffu, there);
-                if (lane == 0) masks[2 * st + (tok >> 5)] = mask;
+                    st_shared_v4(stage + C::kTile + sw32_off(tok, h), extra[4 * h], extra[4 * h + 1], extra[4 * h + 2],
+                                 extra[4 * h + 3]);
+                leave();
             } else {
+                if (!wait_warp(v_empty(j % VST), ((j / VST) & 1) ^ 1, ctl)) break;
+                const uint32_t stage = sV(j % VST);
                 float vs[NG], vm[NG];
                 const int place = (j0 + j) * kTok + tok - ctx;
 #pragma unroll
@@ -351,61 +430,89 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < kWords; ++c) {
-                    const int g0 = 2 * c % S32 * 32 / G, g1 = (2 * c + 1) % S32 * 32 / G;
-                    const uint32_t s2 = pack_bf16x2(vs[g0], vs[g1]), m2 = pack_bf16x2(vm[g0], vm[g1]);
-                    uint32_t y[4];
+                for (int chunk = 0; chunk < CH; ++chunk) {
+                    uint32_t w[4];
+                    codes(chunk, w);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t x = ((w[c] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
-                        y[e] = fma_pair(as_u32(__hsub2(as_bf2(x), as_bf2(0x43004300u))), s2, m2);
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 4 * chunk + k, g0 = 2 * c % S32 * 32 / G, g1 = (2 * c + 1) % S32 * 32 / G;
+                        const uint32_t s2 = pack_bf16x2(vs[g0], vs[g1]), m2 = pack_bf16x2(vm[g0], vm[g1]);
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t x = ((w[k] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
+                            y[e] = fma_pair(as_u32(__hsub2(as_bf2(x), as_bf2(0x43004300u))), s2, m2);
+                        }
+                        st_shared_v4(stage + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1], y[2], y[3]);
                     }
-                    st_shared_v4(stage + 2 * C::kTile + (c >> 3) * (kTok * 128) + sw128_off(tok, c & 7), y[0], y[1],
-                                 y[2], y[3]);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_full(j % VST));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full(st));
+            fetch(j + kRaw);  // over the codes just used
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        };
+        if (th < kTok) unpack(std::false_type{});
+        else unpack(std::true_type{});
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ matrix instructions
         const bool leader = elect_one_sync();
-        const SDesc dK = sdesc_make(sStage(0), 16, 1024), dV = sdesc_make(sStage(0) + 2 * C::kTile, kTok * 128, 1024),
-                    dQA = sdesc_sw32(sQAug), dKA = sdesc_sw32(sStage(0) + 3 * C::kTile);
-        constexpr uint32_t kStage16 = C::kStage >> 4;
-        auto issue_s = [&](int j) -> bool {
-            const int st = j % ST, buf = j & 1;
-            if (!wait_warp(full(st), (j / ST) & 1, ctl)) return false;
-            tc_fence_after();
-            const uint32_t to = tmem + C::kS(buf), ko = st * kStage16;
+        const SDesc dK = sdesc_make(sK(0), 16, 1024), dV = sdesc_make(sV(0), kTok * 128, 1024),
+                    dQA = sdesc_sw32(sQAug), dKA = sdesc_sw32(sK(0) + C::kTile);
+        int entry = 0;  // of the keys' ring
+        // S (+)= Q K^T of the next entry
+        auto products = [&](uint32_t to, uint32_t q, uint32_t idesc, bool add, bool extra, uint32_t aug) {
+            const uint32_t ko = entry % KST * (C::kKStage >> 4);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
                 if (leader)
-                    mma_ts_d(to, tmem + C::kQ + 8 * s, dK, ko + (((s >> 2) * (2 * kTok * 128) + (s & 3) * 32) >> 4),
-                             C::kIdescS, s > 0);
+                    mma_ts_d(to, tmem + q + 8 * s, dK, ko + (((s >> 2) * (kTok * 128) + (s & 3) * 32) >> 4), idesc,
+                             add || s > 0);
             if (leader) {
-                mma_ss_d(to, dQA, 0, dKA, ko, C::kIdescAug, 1);
-                mma_commit(s_full(buf));
+                if (extra) mma_ss_d(to, dQA, aug, dKA, ko, idesc, 1);
+                mma_commit(k_empty(entry % KST));
+            }
+            ++entry;
+        };
+        auto ready = [&]() -> bool {
+            if (!wait_warp(k_full(entry % KST), (entry / KST) & 1, ctl)) return false;
+            tc_fence_after();
+            return true;
+        };
+        auto issue_s = [&](int j) -> bool {
+            if (!ready()) return false;
+            const uint32_t to = tmem + C::kS(j & 1);
+            if (wides[j % kInfo]) {
+                products(to, C::kQWide, C::kIdescWide, false, false, 0);
+                if (!ready()) return false;
+                products(to, C::kQWide, C::kIdescWide, true, true, C::kQAug >> 4);
+            } else {
+                products(to, C::kQ, C::kIdescS, false, true, 0);
+            }
+            if (leader) {
+                mma_commit(s_full(j & 1));
+                mbar_arrive(s_full(j & 1));
             }
             return true;
         };
         // S(j + 1) is computed beside the softmax of tile j; its buffer's P, of tile j - 1, has been multiplied
         if (n > 0 && wait_warp(q_full, 0, ctl) && issue_s(0)) {
             for (int j = 0; j < n; ++j) {
-                const int st = j % ST, buf = j & 1;
+                const int st = j % VST, buf = j & 1;
                 if (j + 1 < n && !issue_s(j + 1)) break;
+                if (!wait_warp(v_full(st), (j / VST) & 1, ctl)) break;
                 if (!wait_warp(p_full(buf), (j >> 1) & 1, ctl)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < kTok / 16; ++s)
                     if (leader)
-                        mma_ts_d(tmem + C::kO, tmem + C::kS(buf) + s * 8, dV, st * kStage16 + s * (2048 >> 4), C::kIdescPV,
-                                 (j > 0 || s > 0) ? 1u : 0u);
+                        mma_ts_d(tmem + C::kO, tmem + C::kS(buf) + s * 8, dV, st * (C::kTile >> 4) + s * (2048 >> 4),
+                                 C::kIdescPV, (j > 0 || s > 0) ? 1u : 0u);
                 if (leader) {
                     mma_commit(pv_done);
-                    mma_commit(empty(st));
+                    mma_commit(v_empty(st));
                 }
             }
         }
@@ -439,26 +546,31 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 for (int e = 0; e < 8; e += 2) top = fmax3(top, fabsf(f[e]), fabsf(f[e + 1]));
             }
             const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
-            const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((127 - ex) << 23), p.sl2);
-            factor = p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * __int_as_float((127 + ex) << 23) * (1.f / kKeyUnit);
+            const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((127 + 8 - ex) << 23), p.sl2);
+            factor = p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * __int_as_float((127 - 8 + ex) << 23);
             if (half == 0) {
                 float sum[NG];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) sum[g] = 0.f;
 #pragma unroll
                 for (int hf = 0; hf < D / 64; ++hf) {
-                    uint32_t x[32];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {  // the channels of the codes' word 8 hf + k, in its pairs
-                        const int word = 8 * hf + k, c = word % S32 * 4 + word / S32;
-                        float f[8];
-                        chunk(c, f, up);
+                    for (int wide = 0; wide < 2; ++wide) {
+                        uint32_t x[32];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) sum[c * 8 / G] += f[e];
+                        for (int k = 0; k < 8; ++k) {  // the channels of the codes' word 8 hf + k, in its pairs
+                            const int word = 8 * hf + k, c = word % S32 * 4 + word / S32;
+                            float f[8];
+                            chunk(c, f, up);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[4 * k + e] = pack_bf16x2(f[e], f[e + 4]);
+                            for (int e = 0; e < 8; ++e)
+                                if (wide == 0) sum[c * 8 / G] += f[e];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[4 * k + e] = wide ? pack_bf16x2(f[e], f[e + 4]) : pack_f16(f[e], f[e + 4]);
+                        }
+                        tmem_st32(lane_base + (wide ? C::kQWide : C::kQ) + 32 * hf, x);
                     }
-                    tmem_st32(lane_base + C::kQ + 32 * hf, x);
                 }
                 float c[16];
 #pragma unroll
@@ -469,11 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                     c[3 * g + 1] = __bfloat162float(__float2bfloat16_rn(sum[g] - c[3 * g]));
                     c[3 * g + 2] = sum[g] - c[3 * g] - c[3 * g + 1];
                 }
+                uint32_t a[8];  // fp16: two pieces against the minima, two against the steps
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    st_shared_v4(sQAug + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
+                for (int g = 0; g < 4; ++g) {
+                    const float x = g < NG ? sum[g < NG ? g : 0] : 0.f, hi = __half2float(__float2half_rn(x));
+                    a[2 * g] = a[2 * g + 1] = pack_f16(hi, x - hi);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    st_shared_v4(sQAug + sw32_off(r, h), a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]);
+                    st_shared_v4(sQWide + sw32_off(r, h), pack_bf16x2(c[8 * h], c[8 * h + 1]),
                                  pack_bf16x2(c[8 * h + 2], c[8 * h + 3]), pack_bf16x2(c[8 * h + 4], c[8 * h + 5]),
                                  pack_bf16x2(c[8 * h + 6], c[8 * h + 7]));
+                }
                 fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
@@ -492,54 +612,53 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         const uint32_t tO = lane_base + C::kO + half * (D / 2);
         bool ok = true;  // a wait that ran out ends the loop of both halves at their next barrier
         for (int j = 0; j < n && (warp & 3) < active; ++j) {
-            const int st = j % ST, buf = j & 1;
-            // (full has completed: what the unpacking warps wrote is seen)
-            ok = ok && wait_warp(s_full(buf), (j >> 1) & 1, ctl) && wait_warp(full(st), (j / ST) & 1, ctl);
+            const int buf = j & 1;
+            ok = ok && wait_warp(s_full(buf), (j >> 1) & 1, ctl);
             tc_fence_after();
             const uint32_t tS = lane_base + C::kS(buf);
-            uint32_t sr[32], sb[32];
-            tmem_ld32(tS + 32 * half, sr);
-            tmem_ld32(tS + kTok + 32 * half, sb);
-            const int t0 = (j0 + j) * kTok + 32 * half;
-            const uint32_t have = masks[2 * st + half];
+            uint32_t sr[64];
+            tmem_ld32(tS + 64 * half, sr);
+            tmem_ld32(tS + 64 * half + 32, sr + 32);
+            const int t0 = (j0 + j) * kTok + 64 * half;
+            const uint32_t have0 = masks[4 * (j % kInfo) + 2 * half], have1 = masks[4 * (j % kInfo) + 2 * half + 1];
+            const float scale = wides[j % kInfo] ? factor * (1.f / kKeyUnit) : factor;
             tmem_ld_wait();
             reg_fence32(sr);
-            reg_fence32(sb);
+            reg_fence32(sr + 32);
             float* s = reinterpret_cast<float*>(sr);
-#pragma unroll
-            for (int c = 0; c < 32; c += 2)
-                f2_split(add2(f2(s[c], s[c + 1]), f2(__uint_as_float(sb[c]), __uint_as_float(sb[c + 1]))), s[c], s[c + 1]);
-            if (t0 + 32 > ctx || have != 0xffffffffu) {
+            if (t0 + 64 > ctx || (have0 & have1) != 0xffffffffu) {
                 // bit c: the row sees token t0 + c
-                const unsigned long long vis = t0 >= ctx ? sees >> min(t0 - ctx, 63)
-                                               : ctx - t0 >= 32 ? ~0ull
-                                                                : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
-                const uint32_t v = t0 - ctx > 63 ? 0u : static_cast<uint32_t>(vis) & have;
+                unsigned long long vis = t0 - ctx > 63 ? 0ull
+                                         : t0 >= ctx   ? sees >> (t0 - ctx)
+                                         : ctx - t0 >= 64 ? ~0ull
+                                                          : (sees << (ctx - t0)) | ((1ull << (ctx - t0)) - 1);
+                vis &= have0 | static_cast<unsigned long long>(have1) << 32;
+                const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (!(v >> c & 1)) s[c] = -INFINITY;
+                for (int c = 0; c < 64; ++c)
+                    if (!((c < 32 ? v0 : v1) >> (c & 31) & 1)) s[c] = -INFINITY;
             }
             float mx4[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(s[c], s[c + 4]);
 #pragma unroll
-            for (int c = 8; c < 32; c += 8)
+            for (int c = 8; c < 64; c += 8)
 #pragma unroll
                 for (int a = 0; a < 4; ++a) mx4[a] = fmax3(mx4[a], s[c + a], s[c + 4 + a]);
-            float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * factor;
+            float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale;
             // with the other half's maximum; behind the barrier both have read S, and P may go over it
             ml[256 * buf + 128 * half + r] = mx;
-            if (any_of_pair(2 + (warp & 3), !ok)) break;
+            if (any_of(2 + (warp & 3), 64, !ok)) break;
             mx = fmaxf(mx, ml[256 * buf + 128 * (half ^ 1) + r]);
             const bool grows = j > 0 && mx > m;
             const float m_new = fmaxf(m, mx), alpha = grows ? ex2_approx(m - m_new) : 1.f;
             l *= alpha;
             m = m_new;
             const float ref = m == -INFINITY ? 0.f : -m;  // nothing seen yet
-            const uint64_t f2x = f2(factor, factor), neg2 = f2(ref, ref);
+            const uint64_t f2x = f2(scale, scale), neg2 = f2(ref, ref);
             uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 32; ++c) {
                 float x0, x1;
                 f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), f2x, neg2), x0, x1);
                 const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -549,18 +668,18 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             float s0, s1;
             f2_split(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
-            tmem_st16(tS + 16 * half, sr);
+            tmem_st32(tS + 32 * half, sr);
             if (__any_sync(0xffffffffu, grows)) {
                 ok = wait_warp(pv_done, (j - 1) & 1, ctl);  // O holds the tiles before
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    tmem_ld32(tO + 32 * c, sb);
+                    tmem_ld32(tO + 32 * c, sr);
                     tmem_ld_wait();
-                    reg_fence32(sb);
+                    reg_fence32(sr);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) sb[e] = __float_as_uint(__uint_as_float(sb[e]) * alpha);
-                    tmem_st32(tO + 32 * c, sb);
+                    for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(__uint_as_float(sr[e]) * alpha);
+                    tmem_st32(tO + 32 * c, sr);
                 }
             }
             tmem_st_wait();
