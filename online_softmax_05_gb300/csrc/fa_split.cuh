@@ -72,6 +72,10 @@ __device__ __forceinline__ int split_pieces(int tiles, int chunk) { return max(1
 // By one warp; tiles_of(b): key tiles of a sequence.
 template <typename F>
 __device__ __forceinline__ SplitItem split_item(const SplitPlan& p, int number, int lane, F tiles_of) {
+    if (p.items == p.B * p.per_seq) {  // nothing is cut
+        const int b = number / p.per_seq, tiles = tiles_of(b);
+        return {b, number - b * p.per_seq, 0, tiles, tiles, 1, 0, 0};
+    }
     constexpr int kHeld = 4;  // up to 128 sequences the chunk is searched for, beyond it is an upper bound
     int held[kHeld], most = 0;
     long long total = 0;
@@ -154,10 +158,13 @@ __device__ __forceinline__ SplitItem split_item(const SplitPlan& p, int number, 
 
 // Host: the plan for `units` units, per_seq of each sequence, where `slots` CTAs run at a time.  Few units
 // are cut as far as the CTAs go, in one wave.  Many go out whole, longest first, but for what is longer
-// than share / 4 of a CTA's part, at most 4 slots / share further pieces.
+// than share / 4 of a CTA's part, at most 4 slots / share further pieces.  Of more than 512 sequences
+// none is cut, as every CTA looks through all of them: one row of 2 heads of 64 channels over 64 keys
+// each, all 64 but one of 8192, and 1 to 1000, us cut / whole: 512 sequences 46 / 23, 55 / 86, 62 / 41;
+// 1024: 111 / 37, 117 / 100, 138 / 72; 2048 (the long one 4096): 305 / 69, 330 / 100, 365 / 131.
 inline SplitPlan split_plan(int B, long long units, int slots, int least, int share) {
     const bool few = 2 * units <= slots;
-    const long long items = few ? slots : units + (4LL * slots + share - 1) / share;
+    const long long items = B > 512 ? units : few ? slots : units + (4LL * slots + share - 1) / share;
     return {B, static_cast<int>(units / B), static_cast<int>(items), least, slots, few ? 0 : share};
 }
 

@@ -36,6 +36,7 @@ def cross(lengths, heads, rows, Tk, seed, dim=64):
     [0] * 31 + [4000], [1] * 32, list(range(0, 4000, 130)),      # up to 32 sequences: sorted
     [1] * 32 + [4000], [0] * 40, list(range(3000, 3000 + 33)),   # more
     [5] * 127 + [3999], [5] * 128 + [3999], [0] * 200,           # the chunk is searched for up to 128
+    [3] * 511 + [900], [3] * 512 + [900],                        # cut up to 512
 ])
 def test_lengths(lengths, heads, rows):
     cross(lengths, heads, rows, 4000, seed=len(lengths) + heads)
