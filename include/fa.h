@@ -424,8 +424,10 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
  * A place without a token, or a sequence of length 0, gives o = 0 and lse = -infinity.
  * A length between 0 and N is recorded as FA_ERR_SEQLEN and counts as 0.  What a place does not
  * see does not touch its result, whatever the cache holds there.  Scores, sums and the
- * softmax are float32 and keys are exact; weights and values go into their product as
- * bf16, each rounded once.
+ * softmax are float32.  Keys are exact, and a query's elements down to 2^-25 of their row's
+ * largest; what is smaller loses bits.  (Whole queries stay exact over tiles of 128
+ * tokens with a key group whose s or m lies outside 2^-17 to 2^11.)  Weights and values go into
+ * their product as bf16, each rounded once.
  *   workspace : fa_kv4_tree_workspace(B, Hq, Hkv, N, D, width * page_size) bytes, 16-byte
  *               aligned, used until the call's work on `stream` is done; or NULL: taken with
  *               cudaMallocAsync.  FA_ERR_SCRATCH if workspace_bytes is too small.

@@ -20,8 +20,9 @@
 // Channels stay in the order of the codes' words; Q is stored in that order, and V's is
 // undone when the outputs leave.
 //
-// Ranges.  In bf16 K is scaled by 2^-16, V always by 2^-24, undone in the scores' factor and at the
-// end: no product or sum overflows for any bf16 numbers in the cache.  A token that a row does
+// Ranges.  In bf16 K is scaled by 2^-20, V always by 2^-24, undone in the scores' factor and at the
+// end: no product or sum overflows for any bf16 numbers in the cache (128 products of 2^9 and 2^109).  A
+// row of queries above 2^101 goes into bf16 less its power beyond, which the factor has no room for.  A token that a row does
 // not see adds nothing whatever it holds: S is replaced, and a tree's value group that is NaN
 // goes into the products as 0 and into the rows that see it at the end.
 //
@@ -61,7 +62,7 @@ constexpr int kUnitRows = 128;  // of a CTA
 constexpr int kLeast = 3;      // tiles that are not worth cutting
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kKeyUnit = 0x1p-16f, kValueUnit = 0x1p-24f;
+constexpr float kKeyUnit = 0x1p-20f, kValueUnit = 0x1p-24f;
 
 template <int D_, int G_>
 struct TreeCfg : Kv4<D_, G_> {
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        float factor;
+        float factor, wide_factor;  // of the scores' sums, in fp16 and in bf16
         {
             const bool there = row < row0 + rows;
             const uint4* from = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(bh) * p.R + row) * D);
@@ -545,9 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) top = fmax3(top, fabsf(f[e]), fabsf(f[e + 1]));
             }
-            const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+            const int ex = max(-100, min(127, static_cast<int>(__float_as_uint(top) >> 23) - 127));
             const float up = p.sl2 == 0.f ? 0.f : copysignf(__int_as_float((127 + 8 - ex) << 23), p.sl2);
             factor = p.sl2 == 0.f ? 1.f : fabsf(p.sl2) * __int_as_float((127 - 8 + ex) << 23);
+            const float more = __int_as_float((127 + max(0, ex - 100)) << 23);  // of q in bf16
+            wide_factor = factor * (1.f / kKeyUnit / more);
             if (half == 0) {
                 float sum[NG];
 #pragma unroll
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                         for (int k = 0; k < 8; ++k) {  // the channels of the codes' word 8 hf + k, in its pairs
                             const int word = 8 * hf + k, c = word % S32 * 4 + word / S32;
                             float f[8];
-                            chunk(c, f, up);
+                            chunk(c, f, wide ? up * more : up);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 if (wide == 0) sum[c * 8 / G] += f[e];
@@ -577,9 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
                 for (int e = 0; e < 16; ++e) c[e] = 0.f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    c[3 * g] = __bfloat162float(__float2bfloat16_rn(sum[g]));
-                    c[3 * g + 1] = __bfloat162float(__float2bfloat16_rn(sum[g] - c[3 * g]));
-                    c[3 * g + 2] = sum[g] - c[3 * g] - c[3 * g + 1];
+                    const float x = sum[g] * more;
+                    c[3 * g] = __bfloat162float(__float2bfloat16_rn(x));
+                    c[3 * g + 1] = __bfloat162float(__float2bfloat16_rn(x - c[3 * g]));
+                    c[3 * g + 2] = x - c[3 * g] - c[3 * g + 1];
                 }
                 uint32_t a[8];  // fp16: two pieces against the minima, two against the steps
 #pragma unroll
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             tmem_ld32(tS + 64 * half + 32, sr + 32);
             const int t0 = (j0 + j) * kTok + 64 * half;
             const uint32_t have0 = masks[4 * (j % kInfo) + 2 * half], have1 = masks[4 * (j % kInfo) + 2 * half + 1];
-            const float scale = wides[j % kInfo] ? factor * (1.f / kKeyUnit) : factor;
+            const float scale = wides[j % kInfo] ? wide_factor : factor;
             tmem_ld_wait();
             reg_fence32(sr);
             reg_fence32(sr + 32);

@@ -194,12 +194,96 @@ def test_values_up_to_the_largest():
     assert torch.isfinite(o).all() and o.abs().max() > 1e37
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("gain,std,scale", [(1.0, 2.0 ** 110, 2.0 ** -113), (2.0 ** -95, 2.0 ** 110, 2.0 ** -18),
+                                            (1.0, 2.0 ** 124, 2.0 ** -125), (2.0 ** 30, 2.0 ** 90, 2.0 ** -120)])
+def test_queries_up_to_the_largest(gain, std, scale):
+    c = ref.Batch([700, 77], 2, 128, 64, 32, seed=16, gain=gain)
+    _, o, lse = run(c, 8, trees(2, 21, seed=16, empty=0), scale=scale, std=std)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.gpu
+def test_keys_of_the_largest_in_every_channel():
+    """Scores of 2^7: each of 128 channels near bf16's largest in the cache, the query small."""
+    c = ref.Batch([300], 1, 128, 64, 16, seed=17)
+    at, size = ref.sections(128, 64)[1]
+    pairs = torch.from_numpy(c.pool[..., at:at + 16 * size].copy()).view(torch.bfloat16).view(-1, 2)
+    pairs[~pairs[:, 0].isnan()] = torch.tensor([0.0, 2.0 ** 127 * 1.9921875]).to(torch.bfloat16)
+    c.pool[..., at:at + 16 * size] = pairs.view(torch.uint8).numpy().reshape(c.pool[..., at:at + 16 * size].shape)
+    q = torch.full((1, 2, 9, 128), 2.0 ** -121 * 1.9921875, dtype=torch.bfloat16)
+    parents = trees(1, 9, seed=17, empty=0)
+    o, lse = fa.attention_tree_kv4(q.cuda(), *c.on(), torch.from_numpy(parents).cuda(), scale=2.0 ** -8)
+    assert fa.fa_get_device_status() == 0 and torch.isfinite(o).all()
+    check(c, q, parents, o, lse, 2.0 ** -8)
+
+
 def rescale(c, b, slot, section, group, value):
     """Sets the scales (s, m) of one group of one token, all heads."""
     at, size = ref.sections(c.dim, c.group)[section]
     page, block, r = c.table[b][slot // c.page], slot % c.page // 16, slot % 16
     pair = torch.tensor([value, value]).to(torch.bfloat16).view(torch.uint8).numpy()
     c.pool[page, :, block, at + r * size + 4 * group:at + r * size + 4 * group + 4] = pair
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", FORMATS)
+@pytest.mark.parametrize("slots", [[0], [130], [127, 128], [5, 300, 301, 640], [899], list(range(0, 900, 128)),
+                                   list(range(128, 900, 256))])
+@pytest.mark.parametrize("value", [2.0 ** -18, 2.0 ** -60, 2.0 ** 12, 2.0 ** -17, 2.0 ** 11, -2.0 ** -20])
+def test_keys_of_other_scales_among_ordinary_ones(dim, group, slots, value):
+    """Tiles whose keys go as fp16 beside those that cannot, in every order; and the ends of fp16's range."""
+    c = ref.Batch([900], 1, dim, group, 16, seed=18)
+    for i, slot in enumerate(slots):
+        rescale(c, 0, slot, 1, i % (dim // group), value)
+    run(c, 4, trees(1, 11, seed=18, empty=0), std=2.0 ** -12 if value > 1 else 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,group", [(128, 64), (128, 32), (64, 32)])
+@pytest.mark.parametrize("small", [2.0 ** -12, 2.0 ** -18, 2.0 ** -24])
+def test_small_queries_beside_large_ones(dim, group, small):
+    """The large channels of a row meet keys of 0, so that only the small ones make its scores.  fp16 holds a
+    row to half of 2^-24 where its largest is at least 2^8: 2^-33 of it for a channel, times s (n - 8),
+    no more than the group's largest s n (a group's codes reach 15)."""
+    c = ref.Batch([60], 1, dim, group, 16, seed=19)
+    for slot in range(60):
+        rescale(c, 0, slot, 1, 0, 0.0)
+    q = c.queries(2, 9, 1.0)
+    q[..., group:] *= small
+    parents = trees(1, 9, seed=19, empty=0)
+    scale = 1 / small
+    o, lse = fa.attention_tree_kv4(q.cuda(), *c.on(), torch.from_numpy(parents).cuda(), scale=scale)
+    assert fa.fa_get_device_status() == 0
+    x = q[0].double().numpy()
+    wo, wl, most, weighed = attend(x, c.loaded(0), scale, parents[0])
+    most_key = np.abs(c.loaded(0)[0]).max()
+    extra = scale * np.abs(x).max(-1) * 2.0 ** -33 * dim * most_key
+    assert (np.abs(lse[0].cpu().double().numpy() - wl) <= lse_tol(wl, most) + extra).all()
+    assert (np.abs(o[0].cpu().double().numpy() - wo) <= o_tol(wo, most, weighed) + 2 * (extra[..., None] * weighed)).all()
+
+
+@pytest.mark.gpu
+def test_a_workspace_of_exactly_the_size_asked_for():
+    c = ref.Batch([5000, 0, 700], 2, 128, 64, 16, seed=20)
+    parents = torch.from_numpy(trees(3, 40, seed=20)).cuda()
+    q = c.queries(8, 40).cuda()
+    pool, table, lengths = c.on()
+    want, want_lse = fa.attention_tree_kv4(q, pool, table, lengths, parents)
+    need = fa.load_library().fa_kv4_tree_workspace(3, 8, 2, 40, 128, table.shape[1] * 16)
+    assert need > 0
+    around = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty_like(want_lse)
+    held = struct.pack("QQQ7i4x", pool.data_ptr(), table.data_ptr(), lengths.data_ptr(), 3, 2, 128, 64, 16, pool.shape[0],
+                       table.shape[1])
+    stream = torch.cuda.current_stream().cuda_stream
+    for size, rc in ((need, 0), (need - 1, None)):
+        got = fa.load_library().fa_kv4_tree(held, q.data_ptr(), parents.data_ptr(), o.data_ptr(), lse.data_ptr(), 8, 40,
+                                            ctypes.c_float(128 ** -0.5), around.data_ptr() + 256, size, stream)
+        assert got == rc if rc is not None else got < 0
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert (around[:256] == 77).all() and (around[256 + need:] == 77).all()
 
 
 @pytest.mark.gpu
