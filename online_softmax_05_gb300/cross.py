@@ -194,7 +194,9 @@ def cross_attention(q, k, v, key_lengths=None, scale: float | None = None):
 
     q (B, Hq, Tq, D) and k, v (B, Hkv, Tk, D), or (B, T, D) as one head; Hq a multiple of Hkv.
     ``key_lengths`` (int32 CUDA tensor (B,)) are the keys there; scale defaults to 1/sqrt(D).
-    See attention_forward_cross; strides that the kernels cannot take (a broadcast, say) are copied."""
+    See attention_forward_cross; strides that the kernels cannot take (a broadcast, say) are copied.
+    A pass captured into a CUDA graph wants leaves that no eager autograd graph still holds: torch would
+    join that graph's stream to the capture, and fails."""
     global _autograd_cls
     if _autograd_cls is None:
         with _lock:

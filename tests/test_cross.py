@@ -309,6 +309,38 @@ def test_streams_and_graphs(rows, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,heads", [(2, 4), (300, 20)])
+def test_a_captured_training_pass(rows, heads):
+    """Forward and backward under autograd in one graph; the graphs of the passes before are gone by then."""
+    q, k, v, do = tensors((2, heads, heads, rows, 260, 128), seed=18)
+    n = ints([260, 100])
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+
+    def step():
+        o = fa.cross_attention(*leaves, n)
+        return (o.detach(),) + torch.autograd.grad(o, leaves, do)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for lengths, gain in (([260, 100], 1.0), ([0, 259], 0.5)):
+        n.copy_(ints(lengths))
+        with torch.no_grad():
+            leaves[0].copy_(q * gain)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in held]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows", [1, 200])
 def test_calls_from_a_thread_that_has_used_no_gpu(rows):
     """Tensor maps are made in a thread whose first call this is."""
