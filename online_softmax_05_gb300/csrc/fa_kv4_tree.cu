@@ -35,7 +35,7 @@
 // A ragged batch is cut over the CTAs by fa_split.cuh.
 //
 // Measured: 8 trees of 32 places, 32 heads on 8, over 1 to 12345 tokens 52 to 54 us; 4 of 64 places, 32 heads on 4,
-// over up to 8111 40 us; 8 places over 117 tokens 7.5.  Neither memory (16 % of the copy's rate)
+// over up to 8111 40 us; 8 places over 117 tokens 7.5.  Neither memory (14 % of the copy's rate)
 // nor the tensor cores (20 % busy) bound it but the chain of a tile: wait for S, maximum, exchange, exponentials,
 // P's store, O's rescaling.  Keys as two bf16 products of tiles of 64 tokens took 60 and 45 us.
 #include <cuda_fp16.h>

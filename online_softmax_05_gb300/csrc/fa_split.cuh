@@ -6,7 +6,7 @@
 //   sum over units of max(1, ceil(tiles / c)) <= CTAs,
 // so that one wave of CTAs, cut as evenly as whole tiles allow, does it all, and takes the
 // item of its number: a unit's n-th piece.  Units of one piece are finished by their CTA; the others
-// leave (O, log-sum-exp) pieces that a second kernel joins (fa_split_join.cu, 3 to 5 us of a pass).  (A cluster
+// leave (O, log-sum-exp) pieces that a second kernel joins (fa_split_join.cu: 5 to 8 us from cold caches).  (A cluster
 // per unit, joined through distributed shared memory, keeps to 8 CTAs a unit whatever the lengths:
 // 8 trees over 1 to 12345 tokens took 134 us at best, with one sequence of them 8 of 152 SMs a head.)
 #pragma once
