@@ -309,6 +309,39 @@ def test_streams_and_graphs(rows, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,heads,dim", [(3, 2, 128), (300, 20, 64), (300, 20, 128)])
+def test_strides_beyond_32_bits(rows, heads, dim, deterministic_backward):
+    """Sequences 2^31 + 64 elements apart, inputs and outputs; the results are those of tensors side by side."""
+    q, k, v, do = tensors((2, heads, heads, rows, 260, dim), seed=19)
+    n = ints([260, 131])
+    far = (1 << 31) + 64
+
+    def apart(*given):
+        """Copies of tensors, in one buffer one behind the other, their sequences far apart."""
+        sizes = [x[0].numel() for x in given]
+        assert sum(sizes) <= 1 << 22
+        buffer = torch.empty(far + (1 << 22), dtype=torch.bfloat16, device="cuda")
+        out, at = [], 0
+        for x, size in zip(given, sizes):
+            _, h, t, d = x.shape
+            out.append(torch.as_strided(buffer, x.shape, (far, t * d, d, 1), at))
+            out[-1].copy_(x)
+            at += size
+        return out
+
+    o, lse = fa.attention_forward_cross(q, k, v, n)
+    grads = fa.attention_backward_cross(q, k, v, o, lse, do, n)
+    q2, k2, v2, do2 = apart(q, k, v, do)
+    o2, lse2 = fa.attention_forward_cross(q2, k2, v2, n, out=apart(torch.zeros_like(q))[0])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    outs = [apart(torch.zeros_like(x))[0] for x in (q, k, v)]
+    fa.attention_backward_cross(q2, k2, v2, o2, lse2, do2, n, dq=outs[0], dk=outs[1], dv=outs[2])
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(grads, outs))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,heads", [(2, 4), (300, 20)])
 def test_a_captured_training_pass(rows, heads):
     """Forward and backward under autograd in one graph; the graphs of the passes before are gone by then."""

@@ -264,6 +264,28 @@ def test_small_queries_beside_large_ones(dim, group, small):
 
 
 @pytest.mark.gpu
+def test_pools_beyond_32_bits():
+    """The same pages behind 2^32 bytes of a pool: attention and keeping."""
+    c = ref.Batch([900, 70], 2, 128, 64, 16, seed=21)
+    parents = torch.from_numpy(trees(2, 12, seed=21, empty=0)).cuda()
+    q = c.queries(8, 12).cuda()
+    pool, table, lengths = c.on()
+    path = torch.full((2, 12), -1, dtype=torch.int32, device="cuda")
+    path[:, :3] = torch.tensor([1, 4, 11], dtype=torch.int32)
+    count, page_bytes = pool.shape[0], pool[0].numel()
+    before = (1 << 32) // page_bytes + 1
+    far = torch.empty(before + count, *pool.shape[1:], dtype=torch.uint8, device="cuda")
+    far[before:] = pool
+    far_table = torch.where(table >= 0, table + before, table)
+    o, lse = fa.attention_tree_kv4(q, pool, table, lengths, parents)
+    o2, lse2 = fa.attention_tree_kv4(q, far, far_table, lengths, parents)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    a, b = fa.kv4_keep(pool, table, lengths, path), fa.kv4_keep(far, far_table, lengths, path)
+    assert fa.fa_get_device_status() == 0
+    assert torch.equal(a, b) and torch.equal(far[before:], pool)
+
+
+@pytest.mark.gpu
 def test_a_workspace_of_exactly_the_size_asked_for():
     c = ref.Batch([5000, 0, 700], 2, 128, 64, 16, seed=20)
     parents = torch.from_numpy(trees(3, 40, seed=20)).cuda()
