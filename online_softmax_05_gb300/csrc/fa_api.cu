@@ -291,7 +291,7 @@ int fa_get_device_status(void* stream) {
     int first = FA_OK;
     for (const auto take : {fa::fwd_take_status, fa::bwd_take_status, fa::kv4_cache_take_status,
                             fa::kv4_decode_take_status, fa::cross_rows_take_status,
-                            fa::kv4_tree_take_status, fa::kv4_keep_take_status}) {
+                            fa::kv4_tree_take_status, fa::kv4_keep_take_status, fa::split_join_take_status}) {
         const int status = take();
         if (status == FA_ERR_CUDA) return FA_ERR_CUDA;
         if (first == FA_OK) first = status;

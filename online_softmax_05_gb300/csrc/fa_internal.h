@@ -64,6 +64,7 @@ int launch_cross_rows(const CrossShape& s, const CrossTensor& q, const CrossTens
                       cudaStream_t stream, const DebugKnobs& dbg, int num_sms);
 size_t cross_rows_workspace(const CrossShape& s, int num_sms);  // 0 where they are not wanted
 int cross_rows_take_status();
+int split_join_take_status();  // of the debug build's checks
 size_t cross_bwd_workspace(const CrossShape& s, bool deterministic, int num_sms);
 int launch_cross_bwd(const CrossShape& s, const CrossTensor& q, const CrossTensor& k, const CrossTensor& v,
                      const CrossTensor& o, const void* o_rest, const CrossTensor& dO, const float* lse, const CrossTensor& dq,

@@ -32,12 +32,14 @@ struct SplitItem {
     int pieces;        // of the unit
     int part, k;       // where they are left: part + k is this item's; k = 0: its first
 };
-// What the second kernel reads: [unit] (first piece, pieces), pieces of `rows` rows.
+// What the second kernel reads: [unit] (first piece, pieces), pieces of `rows` rows.  A unit of
+// one piece leaves none, and its first piece may be `count`.
 struct SplitParts {
     float* o;          // [part][rows][D], normalised
     float* lse;        // [part][rows], log2 units, -inf where a row saw nothing
     int2* units;
     int rows;
+    int count;         // pieces that there is room for
 };
 
 // Where a row of a unit goes: row r of a key/value head is query r % T of its group's head r / T.
@@ -59,7 +61,7 @@ inline SplitParts split_parts(void* ws, const SplitPlan& p, int rows, int D) {
     const size_t n = 2 * (p.items - static_cast<size_t>(p.B) * p.per_seq) * rows;
     if (n == 0) return {};
     float* o = static_cast<float*>(ws);
-    return {o, o + n * D, reinterpret_cast<int2*>(o + n * (D + 1)), rows};
+    return {o, o + n * D, reinterpret_cast<int2*>(o + n * (D + 1)), rows, static_cast<int>(n / rows)};
 }
 
 __device__ __forceinline__ int split_sum(int x) {

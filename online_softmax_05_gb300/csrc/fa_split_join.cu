@@ -5,11 +5,17 @@
 // kernel's end, then the unit's entry and the pieces, eight of a warp in flight at once.
 #include <cuda_runtime.h>
 
+#include "fa_check.cuh"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_split.cuh"
 
 namespace fa {
+
+#ifdef FA_DEBUG
+static __device__ int g_status_split_join;  // only checks record anything here
+#endif
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -21,6 +27,7 @@ __global__ void __launch_bounds__(kThreads) fa_split_join_kernel(SplitParts part
     constexpr int kLanes = D / 4, kRows = 32 / kLanes, kTeams = kThreads / 32 / WARPS;
     __shared__ float s_state[2][WARPS][kRows];   // of a row's warps: maxima, sums
     __shared__ float4 s_acc[WARPS][32];
+    [[maybe_unused]] __shared__ int s_failed;  // a check's flag: nothing is in flight that would be given up
     wait_for_stream();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % kLanes, mine = warp % WARPS;
     const long long at = (static_cast<long long>(blockIdx.x) * kTeams + warp / WARPS) * kRows + lane / kLanes;
@@ -30,8 +37,12 @@ __global__ void __launch_bounds__(kThreads) fa_split_join_kernel(SplitParts part
     const int bh = static_cast<int>(bhl), r = static_cast<int>(row_there ? at - bhl * out.R : 0);
     const int unit = bh * out.row_units + r / out.unit_rows, local = r % out.unit_rows;
     int2 pieces = __ldcg(parts.units + unit);
-    if (!row_there) pieces.y = 0;
-    if (WARPS == 1 && pieces.y <= 1) return;
+    // A unit of one piece was finished by its CTA: its entry names no piece that was written, behind the last
+    // cut unit not even one that the workspace holds.  (Its warps stay for the barriers.)
+    if (!row_there || pieces.y <= 1) pieces.y = 0;
+    if (WARPS == 1 && pieces.y == 0) return;
+    if (pieces.y > 0 && !FA_CHECK(pieces.x >= 0 && pieces.x + pieces.y <= parts.count, &g_status_split_join, &s_failed))
+        pieces.y = 0;
     const float* lse = parts.lse + static_cast<size_t>(pieces.x) * parts.rows + local;
     const float* o = parts.o + (static_cast<size_t>(pieces.x) * parts.rows + local) * D + 4 * sub;
     const size_t step = static_cast<size_t>(parts.rows);
@@ -101,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) fa_split_join_kernel(SplitParts part
     if constexpr (WARPS > 1) {
         s_acc[mine][lane] = make_float4(y[0], y[1], y[2], y[3]);
         __syncthreads();
-        if (mine != 0 || pieces.y <= 1) return;
+        if (mine != 0 || pieces.y == 0) return;
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) {
             const float4 z = s_acc[w][lane];
@@ -138,6 +149,16 @@ int launch_split_join(const SplitParts& parts, const SplitOut& out, int B, int D
     const bool wide = items >= 2 * kAtOnce * units;  // pieces of a unit, if its share is fair
     if (D == 64) return wide ? launch_t<64, 8>(parts, out, n, stream) : launch_t<64, 1>(parts, out, n, stream);
     return wide ? launch_t<128, 8>(parts, out, n, stream) : launch_t<128, 1>(parts, out, n, stream);
+}
+
+int split_join_take_status() {
+    int h = 0;
+#ifdef FA_DEBUG
+    const int z = 0;
+    if (cudaMemcpyFromSymbol(&h, g_status_split_join, sizeof(int)) != cudaSuccess) return -5;
+    if (cudaMemcpyToSymbol(g_status_split_join, &z, sizeof(int)) != cudaSuccess) return -5;
+#endif
+    return h;
 }
 
 }  // namespace fa
