@@ -461,7 +461,9 @@ int fa_tree_accept(const int* parents, const void* tokens, const void* picks, co
  *   weights, slot_positions: float32 / int32 [B][Hkv][slots] or NULL: moved alike, in place
  * A path that does not rise or leaves the N places, a length between 0 and N or one that the
  * table or the accounts cannot hold is recorded as FA_ERR_SEQLEN: that sequence and its length stay as
- * they are.  The pages of the last N slots must be the sequence's own.
+ * they are.  Where the table names no page of the pool for a place on the path, or for the slot that it
+ * goes to, FA_ERR_PAGE is recorded and that place is left out, its codes and its accounts: the length counts
+ * it, its slot holds what it held.  The pages of the last N slots must be the sequence's own.
  */
 int fa_kv4_keep(const fa_kv4_cache* cache, const int* path, int N, int* lengths_out, float* weights, int* slot_positions,
                 long long slots, void* stream);

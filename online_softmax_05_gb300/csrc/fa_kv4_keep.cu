@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kKeepThreads)
     uint32_t held[kMost];
     float weight = 0.f;
     int position = 0;
-    const bool account = tid < n && s_path[tid] != tid;
+    const bool account = tid < n && s_from[tid] >= 0;  // as the codes: one whose page is bad is left out of both
     const long long at = (static_cast<long long>(b) * pages.heads + h) * slots + ctx;
 #pragma unroll
     for (int k = 0; k < kMost; ++k) {
