@@ -157,12 +157,16 @@ def attention_backward_cross(q, k, v, o, lse, do, key_lengths=None, scale: float
 
 
 def _laid_out(t, name):
-    """(B, H, T, D) of a (B, H, T, D) or (B, T, D) tensor, copied if the kernels cannot take its strides."""
+    """(B, H, T, D) of a (B, H, T, D) or (B, T, D) tensor, copied if the kernels cannot take its strides or address."""
+    import torch
     if t.dim() == 3:
         t = t.unsqueeze(1)
     elif t.dim() != 4:
         raise ValueError(f"{name} must be (B, H, T, D) or (B, T, D)")
-    return t if _fits(t) else t.contiguous()
+    if _fits(t):
+        return t
+    # contiguous() returns a tensor that is already contiguous, whatever its address
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 def _make_autograd_class():
@@ -194,7 +198,7 @@ def cross_attention(q, k, v, key_lengths=None, scale: float | None = None):
 
     q (B, Hq, Tq, D) and k, v (B, Hkv, Tk, D), or (B, T, D) as one head; Hq a multiple of Hkv.
     ``key_lengths`` (int32 CUDA tensor (B,)) are the keys there; scale defaults to 1/sqrt(D).
-    See attention_forward_cross; strides that the kernels cannot take (a broadcast, say) are copied.
+    See attention_forward_cross; what the kernels cannot take (a broadcast, a view off 16-byte alignment) is copied.
     A pass captured into a CUDA graph wants leaves that no eager autograd graph still holds: torch would
     join that graph's stream to the capture, and fails."""
     global _autograd_cls
