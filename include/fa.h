@@ -542,7 +542,9 @@ int fa_sched_tile_rows(int D, int* bm_fwd, int* bn, int* bm_bwd);
  * fa_debug_inject: 0 = off; 1 = the forward's load warp skips its first
  *   K/V tile copy; 2 = the load warp of the backward's first dK/dV CTA skips
  *   its third Q tile copy (its first when it has fewer); 3 = the load warp of
- *   the backward's first dQ CTA skips its first K tile copy.  The waits that depend on the missing copy
+ *   the backward's first dQ CTA skips its first K tile copy; 4 = the load warp of the first CTA of cross
+ *   attention's few-rows kernel skips its first K tile copy; 5 = the first CTA of fa_kv4_tree keeps its
+ *   first tile of keys to itself.  The waits that depend on the missing copy
  *   run out, the CTA gives up (it waits, bounded, for its copies and MMAs in
  *   flight, frees its tensor memory and exits) and FA_ERR_DEVICE_TIMEOUT is
  *   reported instead of a hang; the outputs of that call are not valid.

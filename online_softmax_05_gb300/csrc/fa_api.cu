@@ -896,7 +896,7 @@ int fa_debug_checks_enabled(void) {
 }
 
 int fa_debug_inject(int mode) {
-    if (mode < 0 || mode > 3) return FA_ERR_ARG;
+    if (mode < 0 || mode > 5) return FA_ERR_ARG;
     g_inject.store(mode);
     return FA_OK;
 }
