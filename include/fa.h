@@ -577,9 +577,10 @@ int fa_bwd_sums_dq_in_place(int B, int Hkv, int T, int D);
 
 /*
  * 1 in the debug build of the library (compiled with FA_DEBUG), 0 in the
- * product build.  In the debug build every kernel checks the tile
+ * product build.  In the debug build the attention kernels check the tile
  * coordinates, ring stages, per-row vector offsets and tensor-memory columns
- * it computes at run time before it uses them; a failed check skips the
+ * that they compute at run time before they use them (fa_decode, fa_rope and the other
+ * fa_kv4_ calls but fa_kv4_tree and fa_kv4_keep have no such checks); a failed check skips the
  * access, makes the CTA give up through its bounded-wait exit path, and is
  * reported by fa_get_device_status as FA_ERR_DEBUG_CHECK.  Nothing traps.
  */

@@ -1,9 +1,9 @@
 """Build the CUDA libraries in-tree with nvcc for sm_103a.
 
   libfa.so        the product: C-ABI entry points of include/fa.h
-  libfa_debug.so  the same sources built with -DFA_DEBUG: every kernel checks
-                  its run-time tile, ring-stage, vector and tensor-memory
-                  indices before use and reports FA_ERR_DEBUG_CHECK instead of
+  libfa_debug.so  the same sources built with -DFA_DEBUG: the attention
+                  kernels check their run-time tile, ring-stage, vector and tensor-memory
+                  indices before use and report FA_ERR_DEBUG_CHECK instead of
                   touching memory out of bounds (tests only; slower)
   libfa_probe.so  test-only bring-up kernels (descriptor / TMA / TMEM layout checks)
 

@@ -301,6 +301,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ outputs
     // (o_full and the loads' drain are behind every thread: Q and the ring are free)
     const bool whole = item.pieces == 1;
+    // this item's piece, and its unit's entry, lie inside the workspace
+    const bool room = (whole || FA_CHECK(item.part >= 0 && item.part + item.k < p.parts.count, &g_status_cross_rows,
+                                         abort_flag)) &&
+                      FA_CHECK(bh * p.row_tiles + tile < p.plan.B * p.plan.per_seq, &g_status_cross_rows, abort_flag);
     __syncthreads();
     if (warp < active) {
         // rows times their factors: fp32 into shared memory, 16-byte chunks turned by the row against conflicts
@@ -323,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (r < rows) {
             const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
             if (whole) p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Tq + tok] = lse2 * kLn2;
-            else p.parts.lse[static_cast<size_t>(item.part + item.k) * p.parts.rows + r] = lse2;
+            else if (room) p.parts.lse[static_cast<size_t>(item.part + item.k) * p.parts.rows + r] = lse2;
         }
     }
-    if (p.parts.units != nullptr && tid == 0 && item.k == 0)
+    if (p.parts.units != nullptr && tid == 0 && item.k == 0 && room)
         p.parts.units[bh * p.row_tiles + tile] = make_int2(item.part, item.pieces);
     __syncthreads();
     for (int i = tid; i < rows * (D / 8); i += kThreads) {
@@ -342,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             x[4 * h + 3] = y.w;
         }
         if (!whole) {
+            if (!room) break;
             float4* to = reinterpret_cast<float4*>(p.parts.o + (static_cast<size_t>(item.part + item.k) * p.parts.rows + rr) * D + c * 8);
             to[0] = make_float4(x[0], x[1], x[2], x[3]);
             to[1] = make_float4(x[4], x[5], x[6], x[7]);

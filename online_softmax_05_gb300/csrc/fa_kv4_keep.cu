@@ -12,6 +12,7 @@
 // and a read back 11 us in a row.
 #include <cuda_runtime.h>
 
+#include "fa_check.cuh"
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_tree.cuh"
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kKeepThreads)
     constexpr int kMost = (kTreePlaces * 2 * kHalf + kKeepThreads - 1) / kKeepThreads;
     __shared__ long long s_from[kTreePlaces], s_to[kTreePlaces];  // byte offsets of a token's row in its block, or -1
     __shared__ int s_path[kTreePlaces];
+    [[maybe_unused]] __shared__ int s_failed;  // a check's flag: nothing is in flight that would be given up
     wait_for_stream();
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int len = __ldg(lengths + b);
@@ -125,7 +127,9 @@ __global__ void __launch_bounds__(kKeepThreads)
         const int from = ctx + s_path[tid], to = ctx + tid;
         const long long f = pages.block_of(b, from >> 4), t = pages.block_of(b, to >> 4);
         if (f < 0 || t < 0) atomicCAS(&g_status_kv4_keep, 0, kStatusBadPage);
-        const bool moves = f >= 0 && t >= 0 && from != to;
+        const long long bytes = static_cast<long long>(pages.num_pages) * pages.heads * pages.head_bytes();
+        const bool moves = f >= 0 && t >= 0 && from != to &&
+                           FA_CHECK(max(f, t) + h * pages.head_bytes() + L::kBlock <= bytes, &g_status_kv4_keep, &s_failed);
         s_from[tid] = moves ? f : -1;
         s_to[tid] = t;
     }

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
             if (i < n && at < len) {
                 const int e = p.pages.shift >= 0 ? block >> p.pages.shift : block / p.pages.blocks_page;
                 inside = block - e * p.pages.blocks_page;
-                page = __ldg(entries + e);  // len is within the table
+                // (len is within the table)
+                page = FA_CHECK(e >= 0 && e < p.pages.width, &g_status_kv4_tree, abort_flag) ? __ldg(entries + e) : -1;
             }
         };
         look_up(0);
@@ -705,6 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
     // ------------------------------------------------------------ join
     __syncthreads();
     const bool whole = item.pieces == 1;
+    // this item's piece, and its unit's entry, lie inside the workspace
+    const bool room = (whole || FA_CHECK(item.part >= 0 && item.part + item.k < p.parts.count, &g_status_kv4_tree,
+                                         abort_flag)) &&
+                      FA_CHECK(bh * p.row_units + ru < p.plan.B * p.plan.per_seq, &g_status_kv4_tree, abort_flag);
     if (warp < 8) ml[128 * half + r] = l;
     __syncthreads();
     if (warp < 8) {
@@ -740,10 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         if (row < row0 + rows && half == 0) {
             const float lse2 = used ? m + __log2f(sum) : -INFINITY;
             if (whole) p.lse[static_cast<size_t>(bh) * p.R + row] = lse2 * kLn2;
-            else p.parts.lse[static_cast<size_t>(item.part + item.k) * p.parts.rows + row - row0] = lse2;
+            else if (room) p.parts.lse[static_cast<size_t>(item.part + item.k) * p.parts.rows + row - row0] = lse2;
         }
     }
-    if (p.parts.units != nullptr && tid == 0 && item.k == 0)
+    if (p.parts.units != nullptr && tid == 0 && item.k == 0 && room)
         p.parts.units[bh * p.row_units + ru] = make_int2(item.part, item.pieces);
     __syncthreads();
     for (int i = tid; i < rows * (D / 8); i += kThreads) {
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_tree_kernel(TreeParams p) 
         if (whole) {
             *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(bh) * p.R + row0 + rr) * D + c * 8) = make_uint4(
                 pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        } else {
+        } else if (room) {
             float4* to = reinterpret_cast<float4*>(p.parts.o +
                                                    (static_cast<size_t>(item.part + item.k) * p.parts.rows + rr) * D + c * 8);
             to[0] = make_float4(x[0], x[1], x[2], x[3]);
