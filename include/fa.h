@@ -61,7 +61,7 @@ typedef enum fa_status {
     FA_ERR_DEVICE_TIMEOUT = -7,  /* a kernel's bounded wait ran out (pipeline stall); outputs invalid */
     FA_ERR_ARG = -8,             /* causal not 0/1, or scale not finite */
     FA_ERR_ARCH = -9,            /* current device is not compute capability 10.3 (sm_103a) */
-    FA_ERR_SCRATCH = -10,        /* fa_bwd_noalloc: problem needs more than its fixed scratch buffer */
+    FA_ERR_SCRATCH = -10,        /* fa_bwd_noalloc: problem needs more than its fixed scratch buffer; or a given workspace is too small */
     FA_ERR_SEQLEN = -11,         /* recorded by a kernel: a cu_seqlens length is negative or above max_seqlen,
                                     a key length is outside its tensor, or a cache's length, slot or position is outside its block table or accounts */
     FA_ERR_DEBUG_CHECK = -12,    /* debug library only: a kernel's run-time index failed its bounds check */
@@ -427,7 +427,10 @@ int fa_kv4_decode(const fa_kv4_cache* cache, const void* q, void* o, float* lse,
  * softmax are float32.  Keys are exact, and a query's elements down to 2^-25 of their row's
  * largest; what is smaller loses bits.  (Whole queries stay exact over tiles of 128
  * tokens with a key group whose s or m lies outside 2^-17 to 2^11.)  Weights and values go into
- * their product as bf16, each rounded once.
+ * their product as bf16, each rounded once: a chain of drafted tokens is less exact than the same
+ * tokens through fa_kv4_decode, which keeps the values' codes whole and rounds a weight times s to 11 bits.
+ * No weights are accumulated for fa_kv4_evict, as fa_kv4_decode can: steps with drafts leave the accounts
+ * as they are.
  *   workspace : fa_kv4_tree_workspace(B, Hq, Hkv, N, D, width * page_size) bytes, 16-byte
  *               aligned, used until the call's work on `stream` is done; or NULL: taken with
  *               cudaMallocAsync.  FA_ERR_SCRATCH if workspace_bytes is too small.

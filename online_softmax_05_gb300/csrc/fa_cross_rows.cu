@@ -14,6 +14,7 @@
 // Measured: 256 heads' 5 rows over 32768 keys of 128 channels 581 us, 7.4 TB/s (reads alone are faster than
 // the copy's 6.8); a token of 32 sequences of 0 to 3000 keys 45 us, 4.3 TB/s, as units end unevenly (all
 // of 3000: 66 us, 5.9 TB/s); a lone token's 8 heads over 1500 keys 9.6 us, all of it latency.
+// 168 registers a thread, spilled bytes (stores, loads): 68 and 116 at 128 channels, 16 and 20 at 64.
 #include <cuda_runtime.h>
 
 #include "fa_check.cuh"

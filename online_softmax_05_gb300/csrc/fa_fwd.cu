@@ -266,8 +266,9 @@ __device__ __forceinline__ int item_of(int k, int n_items) {
 // CROSS: queries and keys of different sequences; keys past a sequence's length are
 // masked, and their V rows zeroed in shared memory, as 0 x NaN would reach O.  The last item of
 // a head with an odd number of query tiles is split as well (a lone tile's S, softmax and P V
-// would wait for one another), and items go out by falling weight, in snake order (8 x 32 heads of
-// 333 queries over 0 to 3000 keys: 114 to 90 us).
+// would wait for one another), and the items of sequences with more keys go out first, in snake
+// order (8 x 32 heads of 333 queries over 0 to 3000 keys: 114 to 90 us).  Within a sequence items
+// keep their order, though a lone tile weighs half of a pair.
 template <int D, bool CAUSAL, bool VARLEN, bool SPLIT, bool CROSS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

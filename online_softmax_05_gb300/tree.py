@@ -67,7 +67,8 @@ def attention_tree_kv4(q, pool, block_table, lengths, parents, scale: float | No
 
     ``lengths`` counts the tree's N places, the sequence's last slots (kv4_append writes them).  Each
     place sees the context, its ancestors and itself; one without a token gives 0 and -infinity.
-    H is a multiple of the pool's kv heads.  A chain (parents -1, 0, 1, ...) is causal decoding."""
+    H is a multiple of the pool's kv heads.  A chain (parents -1, 0, 1, ...) is causal decoding, with
+    weights and values rounded to bf16.  No attention weights are accumulated for kv4_evict."""
     return _launch_on(pool, stream, _attention, q, pool, block_table, lengths, parents, scale, out, lse)
 
 
@@ -134,6 +135,6 @@ def kv4_keep(pool, block_table, lengths, path, weights=None, slot_positions=None
 
     path: int32 (B, N), rising places of the last N slots up to the first -1 (tree_accept's, say).  Their
     keys and values move to the first of those slots, and so do ``weights`` and ``slot_positions``
-    (float32 / int32 (B, kv heads, slots), kept for kv4_evict) in place.  The pages of the last N slots
-    must be the sequence's own."""
+    (float32 / int32 (B, kv heads, slots), kept for kv4_evict) in place.  A place whose page the table does not
+    name is left out (recorded).  The pages of the last N slots must be the sequence's own."""
     return _launch_on(pool, stream, _keep, pool, block_table, lengths, path, weights, slot_positions)
