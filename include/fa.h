@@ -248,7 +248,7 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
  *                     256-byte aligned, used until the call's work on `stream` is done; or
  *                     NULL: taken with cudaMallocAsync.  FA_ERR_SCRATCH if
  *                     workspace_bytes is too small.
- * B * Hq * Tq within int32, B * Hkv * Tk at most 2^31 - 128.  FA_ERR_ALIGN for a base that is not
+ * B * Hq * Tq and B * Hkv * Tk within int32, Tk at most 2^31 - 128.  FA_ERR_ALIGN for a base that is not
  * 16-byte aligned or a stride that is no multiple of 8; FA_ERR_ARG for a stride
  * below 1, an output whose rows may share elements, or one whose range of addresses
  * meets another tensor's.  fa_set_deterministic holds as for fa_bwd: at D = 64, with

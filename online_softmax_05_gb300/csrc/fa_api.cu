@@ -355,8 +355,8 @@ bool overlaps_any(Range a, const Range* r, int n) {
 int check_cross(const fa_cross_shape* s, float scale) {
     if (s->B < 1 || s->Hq < 1 || s->Hkv < 1 || s->Tq < 1 || s->Tk < 1 || s->Hq % s->Hkv != 0) return FA_ERR_SHAPE;
     const long long heads_q = static_cast<long long>(s->B) * s->Hq, heads_k = static_cast<long long>(s->B) * s->Hkv;
-    // the kernels round a number of keys up to tiles of 128
-    if (heads_q > (1 << 30) || heads_q * s->Tq > INT_MAX || heads_k * s->Tk > INT_MAX - 127) return FA_ERR_SHAPE;
+    if (heads_q > (1 << 30) || heads_q * s->Tq > INT_MAX || heads_k * s->Tk > INT_MAX) return FA_ERR_SHAPE;
+    if (s->Tk > INT_MAX - 127) return FA_ERR_SHAPE;  // the kernels round it up to tiles of 128
     if (s->D != 64 && s->D != 128) return FA_ERR_UNSUPPORTED;
     if (!std::isfinite(scale)) return FA_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(s->key_lengths) & 3u) return FA_ERR_ALIGN;
